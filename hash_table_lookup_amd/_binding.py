@@ -87,11 +87,27 @@ _SIGNATURES = {
     "emb_rowwise_adam": [_P, _P, _P, _I64, _P, _F, _F, _F, _F, _I64, _P],
     "segsum_adam_workspace_bytes": [_I64, _I64, _I32],
     "emb_grad_segment_sum_adam": [_P, _P, _P, _P, _I64, _P, _I64, _F, _F, _F, _F, _I64, _P, _SZ, _P],
+    "row_groups_workspace_bytes": [_I64, _I32],
+    "row_groups": [_P, _I64, _I32, _P, _P, _P, _SZ, _P],
+    "rows8_save": [_P, _I32, _I64, _I64, _I32, _I32, _P, _P, _P],
+    "rows8_load": [_P, _P, _I32, _I64, _I32, _P, _I32, _P],
+    "norm_rows": [_P, _I32, _I64, _P, _I32, _I64, _I32, _P, _P, _P, _I32, _I32, _F, _P, _I32, _P, _P, _I32, _P],
+    "norm_back_workspace_bytes": [_I64, _I32, _I32],
+    "norm_rows_backward": [_P, _I32, _I64, _P, _I32, _I64, _P, _I32, _P, _I64, _I64, _I32, _P, _P, _P, _I32, _I32, _F,
+                           _P, _P, _P, _P, _SZ, _P],
+    "norm_gate": [_P, _I32, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _P, _P, _P, _I32, _I32, _F, _I32, _F, _P, _P,
+                  _P, _P, _P, _I32, _P],
+    "norm_gate_backward": [_P, _I32, _I64, _P, _I64, _P, _P, _I64, _P, _I32, _I32, _I64, _I32, _P, _P, _P, _P, _I32,
+                           _I32, _F, _I32, _F, _P, _P, _P, _P, _P, _SZ, _P],
+    "grouped_mm": [_P, _I64, _P, _I32, _I64, _I32, _I32, _P, _P, _I32, _P, _I32, _P],
+    "grouped_mm_backward_workspace_bytes": [_I64, _I32, _I32, _I32],
+    "grouped_mm_backward": [_P, _I64, _P, _I64, _P, _I32, _I64, _I32, _I32, _P, _P, _I32, _P, _I32, _P, _P, _SZ, _P],
     "htl_copy_probe": [_P, _P, _I64, _P],
     "htl_last_error": [],
 }
 _SIZE_FUNCS = {"lru_workspace_bytes", "dedup_workspace_bytes", "segsum_workspace_bytes",
-               "segsum_adam_workspace_bytes", "emb_lookup_workspace_bytes"}
+               "segsum_adam_workspace_bytes", "emb_lookup_workspace_bytes", "row_groups_workspace_bytes",
+               "norm_back_workspace_bytes", "grouped_mm_backward_workspace_bytes"}
 EXPORTED = tuple(_SIGNATURES)
 
 _lib = None

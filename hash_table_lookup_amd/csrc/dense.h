@@ -1,0 +1,447 @@
+// Shared by the dense operators beside the lookup (rows8.hip, norm.hip,
+// gate.hip, product.hip): rows read and written eight elements per lane, the
+// 8-bit row format, and the map from workgroups to the rows of a group.
+#pragma once
+
+#include "htl_common.h"
+
+namespace htl {
+
+constexpr int kMaxGroups = HTL_MAX_GROUPS;
+constexpr int kMaxNormDim = HTL_MAX_NORM_DIM;
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 4096;   // row positions are int32
+
+// Where a row's elements come from: fp32, bf16, or 8-bit codes with scales.
+enum { kSrcF32 = 0, kSrcBf16 = 1, kSrcRows8 = 2 };
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// Rows in device memory.  vec: every row starts 16-byte aligned (8-byte for
+// codes) and holds whole groups of eight elements, so a lane moves its eight
+// at once; otherwise they move one at a time.
+struct RowsIn {
+    const void* p;
+    const uint8_t* scales;   // 8-bit rows only: [rows][ceil(dim / 32)]
+    int64_t ld;              // elements from row to row
+    int fmt;                 // 8-bit rows only: HTL_ROWS8_*
+    int vec;
+};
+struct RowsOut {
+    void* p;
+    int64_t ld;
+    int vec;
+};
+
+template <int SRC> struct Raw8;
+template <> struct Raw8<kSrcF32> { u32x4 lo, hi; };
+template <> struct Raw8<kSrcBf16> { u32x4 w; };
+template <> struct Raw8<kSrcRows8> { u32x2 c; uint32_t scale; };
+
+__device__ __forceinline__ u32x4 zeros4() {
+    u32x4 z = {0u, 0u, 0u, 0u};
+    return z;
+}
+
+// Eight elements of a row from `col` on, as they lie in memory; zeros from
+// dim on.  Loads only: nothing waits for them here.
+__device__ __forceinline__ void load8(const RowsIn& r, int64_t row, int col, int dim, Raw8<kSrcF32>& o) {
+    const float* p = (const float*)r.p + row * r.ld + col;
+    o.lo = o.hi = zeros4();
+    if (r.vec) {
+        if (col < dim) {
+            o.lo = *(const u32x4*)p;
+            o.hi = *(const u32x4*)(p + 4);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (col + j < dim) o.lo[j] = __float_as_uint(p[j]);
+            if (col + 4 + j < dim) o.hi[j] = __float_as_uint(p[4 + j]);
+        }
+    }
+}
+__device__ __forceinline__ void load8(const RowsIn& r, int64_t row, int col, int dim, Raw8<kSrcBf16>& o) {
+    const uint16_t* p = (const uint16_t*)r.p + row * r.ld + col;
+    o.w = zeros4();
+    if (r.vec) {
+        if (col < dim) o.w = *(const u32x4*)p;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (col + j < dim) o.w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+    }
+}
+__device__ __forceinline__ void load8(const RowsIn& r, int64_t row, int col, int dim, Raw8<kSrcRows8>& o) {
+    const uint8_t* p = (const uint8_t*)r.p + row * r.ld + col;
+    o.c = {0u, 0u};
+    o.scale = 0;
+    if (col < dim) o.scale = r.scales[row * ((dim + 31) >> 5) + (col >> 5)];
+    if (r.vec) {
+        if (col < dim) o.c = *(const u32x2*)p;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (col + j < dim) o.c[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+    }
+}
+
+__device__ __forceinline__ void unpack8(const RowsIn&, const Raw8<kSrcF32>& r, float* v) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[j] = __uint_as_float(r.lo[j]);
+        v[4 + j] = __uint_as_float(r.hi[j]);
+    }
+}
+__device__ __forceinline__ void unpack8(const RowsIn&, const Raw8<kSrcBf16>& r, float* v) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = bf16_lo(r.w[j]);
+        v[2 * j + 1] = bf16_hi(r.w[j]);
+    }
+}
+
+// The 8-bit row format.  A block of 32 elements of one row shares the scale
+// 2^e, with e >= -126 the least that brings the block's largest magnitude to
+// at most 127 (HTL_ROWS8_I8) or 448 (HTL_ROWS8_E4M3); an element x is kept as
+// the nearest integer, or the nearest e4m3 number, to x / 2^e, ties to even.
+// The scale byte is e + 127 (1..248), or 255 for a block that holds an
+// infinity or a NaN, which reads back as NaN throughout.  A power of two
+// costs up to one bit of the code's range against a free scale, and in
+// return multiplying by it is exact: codes times scales have at most 8
+// significant bits, so they are exact in bf16, and every reader sees the same
+// values whatever type it reads them in.
+__device__ __forceinline__ float rows8_scale(uint32_t byte) {
+    return __uint_as_float(byte == 255u ? 0x7FC00000u : byte << 23);
+}
+__device__ __forceinline__ void unpack8(const RowsIn& r, const Raw8<kSrcRows8>& q, float* v) {
+    const float s = rows8_scale(q.scale);
+    if (r.fmt == HTL_ROWS8_I8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)(q.c[j >> 2] >> (8 * (j & 3))) * s;
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            v[4 * h] = __builtin_amdgcn_cvt_f32_fp8((int)q.c[h], 0) * s;
+            v[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8((int)q.c[h], 1) * s;
+            v[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8((int)q.c[h], 2) * s;
+            v[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8((int)q.c[h], 3) * s;
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
+}
+
+template <int DST>
+__device__ __forceinline__ void store8(const RowsOut& r, int64_t row, int col, int dim, const float* v) {
+    if (DST == kSrcF32) {
+        float* p = (float*)r.p + row * r.ld + col;
+        if (r.vec) {
+            if (col < dim) {
+                u32x4 a, b;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    a[j] = __float_as_uint(v[j]);
+                    b[j] = __float_as_uint(v[4 + j]);
+                }
+                *(u32x4*)p = a;
+                *(u32x4*)(p + 4) = b;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (col + j < dim) p[j] = v[j];
+        }
+    } else {
+        uint16_t* p = (uint16_t*)r.p + row * r.ld + col;
+        if (r.vec) {
+            if (col < dim) {
+                u32x4 a;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+                *(u32x4*)p = a;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (col + j < dim) p[j] = (uint16_t)f32_to_bf16_bits(v[j]);
+        }
+    }
+}
+
+// 8-bit rows to be written beside another result (codes null: none).
+struct Rows8Out {
+    uint8_t* codes;
+    uint8_t* scales;
+    int fmt;
+    int vec;
+};
+// Four neighbouring lanes (col = 8 * lane) hold a block of 32 and call this
+// together; columns from dim on hold zeros.
+__device__ __forceinline__ void save8(const Rows8Out& r, int64_t row, int col, int dim, const float* v) {
+    uint32_t top = 0;                    // magnitudes compare as their bits; a NaN is above all
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+        top = a > top ? a : top;
+    }
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)top, off);
+        top = o > top ? o : top;
+    }
+    const bool i8 = r.fmt == HTL_ROWS8_I8;
+    // top = f * 2^k with f in [1, 2): e = k - 6 while f <= 127/64 (0x7E0000
+    // is 127/64's fraction), or k - 8 while f <= 448/256 (0x600000), else one
+    // more.  A subnormal top has e = -126.
+    int e = (int)(top >> 23) - 127 - (i8 ? 6 : 8) + ((top & 0x7FFFFFu) > (i8 ? 0x7E0000u : 0x600000u) ? 1 : 0);
+    e = e < -126 ? -126 : e;
+    const bool finite = top < 0x7F800000u;
+    const float inv = finite ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.0f;
+    u32x2 c = {0u, 0u};
+    if (finite) {
+        if (i8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) c[j >> 2] |= ((uint32_t)(int)rintf(v[j] * inv) & 0xFFu) << (8 * (j & 3));
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h] * inv, v[4 * h + 1] * inv, 0, false);
+                w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2] * inv, v[4 * h + 3] * inv, w, true);
+                c[h] = (uint32_t)w;
+            }
+        }
+    }
+    if (col < dim) {
+        if ((col & 31) == 0)
+            r.scales[row * ((dim + 31) >> 5) + (col >> 5)] = finite ? (uint8_t)(e + 127) : (uint8_t)255;
+        uint8_t* p = r.codes + row * (int64_t)dim + col;
+        if (r.vec) {
+            *(u32x2*)p = c;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (col + j < dim) p[j] = (uint8_t)(c[j >> 2] >> (8 * (j & 3)));
+        }
+    }
+}
+
+// Eight floats of a parameter row (fp32 [groups][dim]), zeros from dim on.
+__device__ __forceinline__ void load_param(const float* p, bool vec, int g, int col, int dim, float* v) {
+    const float* q = p + (int64_t)g * dim + col;
+    if (vec) {
+        u32x4 a = zeros4(), b = zeros4();
+        if (col < dim) {
+            a = *(const u32x4*)q;
+            b = *(const u32x4*)(q + 4);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = __uint_as_float(a[j]);
+            v[4 + j] = __uint_as_float(b[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = col + j < dim ? q[j] : 0.0f;
+    }
+}
+
+// ---------------------------------------------------- teams of lanes ----
+// Sum over a team of L lanes (L <= 64: aligned lanes of one wave; larger: the
+// whole workgroup of L threads, through LDS), the same in every lane.
+template <int L>
+__device__ __forceinline__ float team_sum(float v, float* s_red) {
+#pragma unroll
+    for (int off = 1; off < (L < 64 ? L : 64); off <<= 1) v += __shfl_xor(v, off);
+    if (L > 64) {
+        __syncthreads();                 // the previous sum's readers are done
+        if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < L / 64; ++w) v += s_red[w];
+    }
+    return v;
+}
+
+// How a row is held: L lanes with I groups of eight elements each, so a row of
+// up to 8 * L * I elements stays in registers between the statistics and the
+// result, and is read once.  Up to 64 lanes a workgroup holds several rows.
+template <int L_, int I_> struct Hold {
+    static constexpr int L = L_, I = I_;
+    static constexpr int kThreads = L_ > 64 ? L_ : 256;
+    static constexpr int kTeams = kThreads / L_;
+};
+// Calls f with the smallest Hold for a row of dim elements (<= kMaxNormDim).
+template <class F> void with_hold(int dim, F&& f) {
+    if (dim <= 64) f(Hold<8, 1>());
+    else if (dim <= 128) f(Hold<16, 1>());
+    else if (dim <= 256) f(Hold<32, 1>());
+    else if (dim <= 512) f(Hold<64, 1>());
+    else if (dim <= 1024) f(Hold<64, 2>());
+    else if (dim <= 2048) f(Hold<64, 4>());
+    else if (dim <= 4096) f(Hold<256, 2>());
+    else if (dim <= 8192) f(Hold<256, 4>());
+    else f(Hold<512, 4>());
+}
+
+// 1 / deviation and, in v, the centred and scaled row: v <- (v - [mean]) * r.
+// The mean is taken out before the squares are summed, both in fp32: a row
+// far from zero keeps its deviation.
+template <class H>
+__device__ __forceinline__ float normalize(float v[][8], bool center, int tl, int dim, float eps, float* s_red) {
+    if (center) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < H::I; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += v[i][j];
+        const float mean = team_sum<H::L>(s, s_red) / (float)dim;   // divided: exact for a constant row
+#pragma unroll
+        for (int i = 0; i < H::I; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = (i * H::L + tl) * 8 + j < dim ? v[i][j] - mean : 0.0f;
+    }
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < H::I; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q += v[i][j] * v[i][j];
+    const float r = 1.0f / sqrtf(team_sum<H::L>(q, s_red) / (float)dim + eps);
+#pragma unroll
+    for (int i = 0; i < H::I; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= r;
+    return r;
+}
+
+// Column sums of a workgroup's teams, written to dst[dim] (the partial row of
+// a chunk, or the group's result): lanes of a wave that hold the same columns
+// first, then the waves through s_col (kThreads / 64 rows of 8 * L * I
+// floats; none needed when one team fills the workgroup).
+template <class H>
+__device__ __forceinline__ void write_columns(float acc[][8], int tl, int dim, bool vec, float* s_col, float* dst) {
+    constexpr int kWaves = H::kThreads / 64;
+    if (H::L <= 64) {
+#pragma unroll
+        for (int i = 0; i < H::I; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int off = H::L; off < 64; off <<= 1) acc[i][j] += __shfl_xor(acc[i][j], off);
+        const int w = threadIdx.x >> 6;
+        __syncthreads();                 // s_col may still be read from the call before
+        if ((threadIdx.x & 63) < H::L)
+#pragma unroll
+            for (int i = 0; i < H::I; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s_col[(w * H::I * H::L + i * H::L + tl) * 8 + j] = acc[i][j];
+        __syncthreads();
+        for (int d = threadIdx.x; d < dim; d += H::kThreads) {
+            float s = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kWaves; ++q) s += s_col[q * H::I * H::L * 8 + d];
+            dst[d] = s;
+        }
+    } else {
+        const RowsOut o = {dst, 0, vec};
+#pragma unroll
+        for (int i = 0; i < H::I; ++i) store8<kSrcF32>(o, 0, (i * H::L + tl) * 8, dim, acc[i]);
+    }
+}
+
+// ------------------------------------------------- rows of a group ----
+// Position range [beg, end) of group g: offsets clamped into [0, m] and to a
+// non-negative length, so offsets that break the CSR rules read no row
+// outside the m given.
+__device__ __forceinline__ void group_range(const int32_t* offsets, int n_groups, int64_t m, int g, int64_t& beg,
+                                            int64_t& end) {
+    if (!offsets) {
+        beg = 0;
+        end = m;
+        return;
+    }
+    const int64_t a = offsets[g], b = g < n_groups ? (int64_t)offsets[g + 1] : m;
+    beg = a < 0 ? 0 : (a > m ? m : a);
+    end = b < beg ? beg : (b > m ? m : b);
+}
+
+// Work item `item` of the chunks of at most R positions that the groups are
+// cut into, group by group, each group with at least min_chunks (0 or 1);
+// the rows of no group follow as group n_groups.  count: chunks of the group.
+// All lanes of a wave call it together with the same arguments.  Returns
+// false past the last chunk.
+struct Chunk {
+    int g;
+    int64_t beg, end;
+    int index, count;       // which of the group's chunks
+};
+__device__ __forceinline__ bool find_chunk(const int32_t* offsets, int n_groups, int64_t m, uint32_t R, int min_chunks,
+                                           int64_t item, Chunk& c) {
+    const int lane = __lane_id();
+    int64_t run = 0;
+    for (int g0 = 0; g0 <= n_groups; g0 += 64) {
+        const int g = g0 + lane;
+        int64_t beg = 0, end = 0;
+        int cnt = 0;
+        if (g < n_groups || (g == n_groups && offsets)) {
+            group_range(offsets, n_groups, m, g, beg, end);
+            cnt = (int)(((uint32_t)(end - beg) + R - 1u) / R);
+            if (g < n_groups && cnt < min_chunks) cnt = min_chunks;
+        }
+        int incl = cnt;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int y = __shfl_up(incl, off);
+            if (lane >= off) incl += y;
+        }
+        const uint64_t past = __ballot(run + incl > item);
+        if (past) {
+            const int l = __ffsll((unsigned long long)past) - 1;
+            c.g = g0 + l;
+            c.count = __shfl(cnt, l);
+            c.index = (int)(item - run) - (__shfl(incl, l) - c.count);
+            const int64_t b = (int64_t)__shfl((int)beg, l), e = (int64_t)__shfl((int)end, l);
+            c.beg = b + (int64_t)c.index * R;
+            c.end = c.beg + R < e ? c.beg + R : e;
+            return true;
+        }
+        run += __shfl(incl, 63);
+    }
+    return false;
+}
+
+// The first work item of group g and how many it has, as find_chunk numbers them.
+__device__ __forceinline__ void chunks_of_group(const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
+                                                int min_chunks, int g, int64_t& first, int& count) {
+    const int lane = __lane_id();
+    int64_t sum = 0;
+    for (int q = lane; q < g; q += 64) {
+        int64_t beg, end;
+        group_range(offsets, n_groups, m, q, beg, end);
+        const int c = (int)(((uint32_t)(end - beg) + R - 1u) / R);
+        sum += c < min_chunks ? min_chunks : c;
+    }
+    int s = (int)sum;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) s += __shfl_xor(s, off);
+    first = s;
+    int64_t beg, end;
+    group_range(offsets, n_groups, m, g, beg, end);
+    count = (int)(((uint32_t)(end - beg) + R - 1u) / R);
+    if (count < min_chunks) count = min_chunks;
+}
+
+inline bool vec_ok(const void* p, int64_t ld, int dim, int elem) {
+    return dim % 8 == 0 && (ld * elem) % 16 == 0 && aligned(p, 16);
+}
+
+// Sums of a group's partial rows: out[g][d] = sum over its chunks of
+// partial[item][d], for the groups with more than one chunk (a lone chunk
+// writes its sums itself).  Chunks are added in order, so the result does
+// not depend on which workgroup ended first.
+htl_status sum_chunks(const float* partial, float* out, const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
+                      int64_t width, hipStream_t stream);
+
+}  // namespace htl

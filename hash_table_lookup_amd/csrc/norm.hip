@@ -1,0 +1,353 @@
+// A norm per row with its group's parameters, before a block ([MTGR] section
+// 4 describes a layer norm per token group; RMS is the other kind), and its
+// backward pass, from the input or from its 8-bit copy.
+//
+//   n = (x - [mean x]) * r,  r = 1 / sqrt(mean (x - [mean x])^2 + eps)
+//   y = n w_g + b_g;                        rows of no group: y = 0
+//   d = dy w_g;  dx = dres + r (d - [mean d] - n mean(d n))
+//   dw_g = sum dy n,  db_g = sum dy;        rows of no group: dx = dres
+//
+// Bound: bytes.  A row is read once into registers (see Hold in dense.h) and
+// its statistics are recomputed in the backward pass rather than kept.
+#include "dense.h"
+
+namespace htl {
+namespace {
+
+struct NormArgs {
+    RowsIn x;
+    RowsOut y;
+    Rows8Out save;
+    const float* weight;
+    const float* bias;       // nullable
+    const int32_t* ids;      // nullable: one group
+    int64_t m;
+    int dim, n_groups, pvec;
+    float eps;
+    bool center;
+};
+
+template <class H, int TX, int TY>
+__global__ __launch_bounds__(H::kThreads) void k_norm(NormArgs a) {
+    __shared__ float s_red[8];
+    const int tl = threadIdx.x % H::L;
+    const int64_t teams = (int64_t)gridDim.x * H::kTeams;
+    for (int64_t row0 = (int64_t)blockIdx.x * H::kTeams; row0 < a.m; row0 += teams) {
+        const int64_t row = row0 + threadIdx.x / H::L;
+        const bool in = row < a.m;       // lanes of a wave stay together for the sums
+        const int64_t r = in ? row : a.m - 1;
+        const int g = a.ids ? a.ids[r] : 0;
+        const bool grouped = (uint32_t)g < (uint32_t)a.n_groups;
+        Raw8<TX> raw[H::I];
+        float v[H::I][8];
+#pragma unroll
+        for (int i = 0; i < H::I; ++i) load8(a.x, r, (i * H::L + tl) * 8, a.dim, raw[i]);
+#pragma unroll
+        for (int i = 0; i < H::I; ++i) unpack8(a.x, raw[i], v[i]);
+        if (a.save.codes) {
+#pragma unroll
+            for (int i = 0; i < H::I; ++i) save8(a.save, r, in ? (i * H::L + tl) * 8 : a.dim, a.dim, v[i]);
+        }
+        normalize<H>(v, a.center, tl, a.dim, a.eps, s_red);
+#pragma unroll
+        for (int i = 0; i < H::I; ++i) {
+            const int col = (i * H::L + tl) * 8;
+            float w[8], b[8];
+            load_param(a.weight, a.pvec, grouped ? g : 0, col, a.dim, w);
+            if (a.bias) load_param(a.bias, a.pvec, grouped ? g : 0, col, a.dim, b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float y = v[i][j] * w[j];
+                if (a.bias) y += b[j];
+                v[i][j] = grouped ? y : 0.0f;
+            }
+            if (in) store8<TY>(a.y, row, col, a.dim, v[i]);
+        }
+    }
+}
+
+struct NormBackArgs {
+    RowsIn dy, x, dres;      // dres.p nullable
+    RowsOut dx;
+    const float* weight;
+    const int32_t* order;    // nullable: rows lie in group order
+    const int32_t* offsets;  // nullable: one group
+    float* dweight;          // [n_groups][dim]
+    float* dbias;            // nullable
+    float* partial;          // [chunks][dim], dbias's after dweight's
+    int64_t chunks;
+    int64_t m;
+    int dim, n_groups, pvec, gvec;
+    uint32_t rows;           // positions per chunk
+    float eps;
+    bool center;
+};
+
+// One workgroup per chunk of a group's rows, so the group's weights and the
+// column sums stay in registers over the chunk.
+template <class H, int TD, int TX, int TR>
+__global__ __launch_bounds__(H::kThreads) void k_norm_back(NormBackArgs a) {
+    __shared__ float s_red[8];
+    __shared__ float s_col[H::L <= 64 ? (H::kThreads / 64) * H::I * H::L * 8 : 1];
+    const int tl = threadIdx.x % H::L;
+    const float inv_dim = 1.0f / (float)a.dim;
+    Chunk c;
+    if (!find_chunk(a.offsets, a.n_groups, a.m, a.rows, 1, blockIdx.x, c)) return;
+    const bool grouped = c.g < a.n_groups;
+    float w[H::I][8], sw[H::I][8], sb[H::I][8];
+#pragma unroll
+    for (int i = 0; i < H::I; ++i) {
+        load_param(a.weight, a.pvec, grouped ? c.g : 0, (i * H::L + tl) * 8, a.dim, w[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sw[i][j] = sb[i][j] = 0.0f;
+    }
+    for (int64_t p0 = c.beg; p0 < c.end; p0 += H::kTeams) {
+        const int64_t p = p0 + threadIdx.x / H::L;
+        int64_t row = p < c.end ? (a.order ? a.order[p] : p) : -1;
+        const bool in = row >= 0 && row < a.m;
+        if (!in) row = 0;
+        Raw8<TX> rx[H::I];
+        Raw8<TD> rd[H::I];
+        Raw8<TR> rr[H::I];
+        float v[H::I][8], d[H::I][8];
+#pragma unroll
+        for (int i = 0; i < H::I; ++i) {
+            const int col = in ? (i * H::L + tl) * 8 : a.dim;
+            load8(a.x, row, col, a.dim, rx[i]);
+            load8(a.dy, row, col, a.dim, rd[i]);
+            if (a.dres.p) load8(a.dres, row, col, a.dim, rr[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < H::I; ++i) {
+            unpack8(a.x, rx[i], v[i]);
+            unpack8(a.dy, rd[i], d[i]);
+        }
+        const float r = normalize<H>(v, a.center, tl, a.dim, a.eps, s_red);
+        float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < H::I; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (in) {                // a row left out must not bring a NaN
+                    sw[i][j] += d[i][j] * v[i][j];
+                    sb[i][j] += d[i][j];
+                }
+                d[i][j] *= w[i][j];
+                c1 += d[i][j];
+                c2 += d[i][j] * v[i][j];
+            }
+        c1 = a.center ? team_sum<H::L>(c1, s_red) * inv_dim : 0.0f;
+        c2 = team_sum<H::L>(c2, s_red) * inv_dim;
+#pragma unroll
+        for (int i = 0; i < H::I; ++i) {
+            float res[8];
+            if (a.dres.p) unpack8(a.dres, rr[i], res);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float g = grouped ? r * (d[i][j] - c1 - v[i][j] * c2) : 0.0f;
+                d[i][j] = a.dres.p ? res[j] + g : g;
+            }
+            if (in) store8<TR>(a.dx, row, (i * H::L + tl) * 8, a.dim, d[i]);
+        }
+    }
+    if (!grouped) return;
+    const bool alone = c.count == 1;
+    const int64_t first = (int64_t)blockIdx.x * a.dim, whole = (int64_t)c.g * a.dim;
+    write_columns<H>(sw, tl, a.dim, a.gvec, s_col, alone ? a.dweight + whole : a.partial + first);
+    if (a.dbias)
+        write_columns<H>(sb, tl, a.dim, a.gvec, s_col, alone ? a.dbias + whole : a.partial + a.chunks * a.dim + first);
+}
+
+// 64 columns per workgroup; its 16 waves take every 16th chunk of the group.
+__global__ __launch_bounds__(1024) void k_sum_chunks(const float* __restrict__ partial, float* __restrict__ out,
+                                                    const int32_t* __restrict__ offsets, int n_groups, int64_t m,
+                                                    uint32_t R, int64_t width) {
+    __shared__ float s[16][64];
+    const int g = blockIdx.y, w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    int64_t first;
+    int count;
+    chunks_of_group(offsets, n_groups, m, R, 1, g, first, count);
+    if (count == 1) return;
+    for (int64_t d0 = blockIdx.x * 64ll; d0 < width; d0 += gridDim.x * 64ll) {
+        const int64_t d = d0 + lane;
+        float v = 0.0f;
+        if (d < width) {
+#pragma unroll 8
+            for (int c = w; c < count; c += 16) v += partial[(first + c) * width + d];
+        }
+        s[w][lane] = v;
+        __syncthreads();
+        if (w == 0 && d < width) {
+            for (int q = 1; q < 16; ++q) v += s[q][lane];
+            out[g * width + d] = v;
+        }
+        __syncthreads();
+    }
+}
+
+// Positions per chunk: about kChunks chunks in all, at least four rows for
+// each team.
+constexpr int64_t kChunks = 2048;
+uint32_t norm_chunk_rows(int64_t m, int dim) {
+    int teams = 1;
+    with_hold(dim, [&](auto h) { teams = decltype(h)::kTeams; });
+    int64_t r = ceil_div(m, teams > 1 ? kChunks : kChunks / 2);
+    return (uint32_t)(r < teams * 4 ? teams * 4 : r);
+}
+
+}  // namespace
+
+int64_t norm_chunks(int64_t m, int n_groups, int dim) { return m / norm_chunk_rows(m, dim) + n_groups + 1; }
+uint32_t norm_rows_per_chunk(int64_t m, int dim) { return norm_chunk_rows(m, dim); }
+
+htl_status sum_chunks(const float* partial, float* out, const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
+                      int64_t width, hipStream_t stream) {
+    if (m <= (int64_t)R) return HTL_OK;      // every group is one chunk
+    const int64_t cols = ceil_div(width, 64);
+    hipLaunchKernelGGL(k_sum_chunks, dim3((unsigned)(cols < 4096 ? cols : 4096), (unsigned)n_groups), dim3(1024), 0,
+                       stream, partial, out, offsets, n_groups, m, R, width);
+    return check_launch("partial sums");
+}
+
+}  // namespace htl
+
+using namespace htl;
+
+namespace {
+
+int elem(htl_dtype t) { return t == HTL_F32 ? 4 : 2; }
+bool known(htl_dtype t) { return t == HTL_F32 || t == HTL_BF16; }
+
+template <class H> void launch_norm(const NormArgs& a, int tx, int ty, hipStream_t s) {
+    const dim3 grid(grid_for(a.m, H::kTeams, 1 << 16)), block(H::kThreads);
+#define NORM_CASE(TX, TY) hipLaunchKernelGGL((k_norm<H, TX, TY>), grid, block, 0, s, a)
+    if (tx == kSrcF32 && ty == kSrcF32) NORM_CASE(kSrcF32, kSrcF32);
+    else if (tx == kSrcF32) NORM_CASE(kSrcF32, kSrcBf16);
+    else if (tx == kSrcBf16 && ty == kSrcF32) NORM_CASE(kSrcBf16, kSrcF32);
+    else if (tx == kSrcBf16) NORM_CASE(kSrcBf16, kSrcBf16);
+    else if (ty == kSrcF32) NORM_CASE(kSrcRows8, kSrcF32);
+    else NORM_CASE(kSrcRows8, kSrcBf16);
+#undef NORM_CASE
+}
+
+template <class H, int TD, int TX, int TR>
+void launch_norm_back(const NormBackArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)a.chunks), block(H::kThreads);
+    hipLaunchKernelGGL((k_norm_back<H, TD, TX, TR>), grid, block, 0, s, a);
+}
+
+}  // namespace
+
+extern "C" htl_status norm_rows(const void* x, htl_dtype x_dtype, int64_t ldx, const uint8_t* x_scales,
+                                htl_rows8_fmt x_fmt, int64_t m, int dim, const float* weight, const float* bias,
+                                const int32_t* ids, int n_groups, htl_norm_kind kind, float eps, void* y,
+                                htl_dtype y_dtype, uint8_t* codes, uint8_t* scales, htl_rows8_fmt fmt,
+                                hipStream_t stream) {
+    clear_error();
+    HTL_REQUIRE(m >= 0 && m <= kMaxRows, "norm_rows: row count out of range");
+    HTL_REQUIRE(dim >= 1 && dim <= kMaxNormDim, "norm_rows: dim out of range");
+    HTL_REQUIRE(n_groups >= 1 && n_groups <= kMaxGroups, "norm_rows: group count out of range");
+    HTL_REQUIRE(kind == HTL_NORM_RMS || kind == HTL_NORM_LAYER, "norm_rows: unknown kind");
+    HTL_REQUIRE(known(x_dtype) && known(y_dtype), "norm_rows: dtypes must be HTL_F32 or HTL_BF16");
+    HTL_REQUIRE(eps >= 0.0f, "norm_rows: eps must not be negative");
+    HTL_REQUIRE(ids || n_groups == 1, "norm_rows: several groups need ids");
+    HTL_REQUIRE(!codes == !scales, "norm_rows: codes and scales come together");
+    HTL_REQUIRE((fmt == HTL_ROWS8_I8 || fmt == HTL_ROWS8_E4M3) && (x_fmt == HTL_ROWS8_I8 || x_fmt == HTL_ROWS8_E4M3),
+                "norm_rows: unknown 8-bit format");
+    HTL_REQUIRE(!(codes && x_scales), "norm_rows: x is in 8 bits already");
+    HTL_REQUIRE(ldx >= dim, "norm_rows: row stride below dim");
+    if (m == 0) return HTL_OK;
+    const int xe = x_scales ? 1 : elem(x_dtype), ye = elem(y_dtype);
+    HTL_REQUIRE(x && weight && y, "norm_rows: null pointer");
+    HTL_REQUIRE(aligned(x, xe) && aligned(y, ye) && aligned(weight, 4) && aligned(bias, 4) && aligned(ids, 4),
+                "norm_rows: misaligned pointer");
+    NormArgs a;
+    a.x = {x, x_scales, ldx, (int)x_fmt,
+           x_scales ? (dim % 8 == 0 && ldx % 8 == 0 && aligned(x, 8)) : vec_ok(x, ldx, dim, xe)};
+    a.y = {y, dim, vec_ok(y, dim, dim, ye)};
+    a.save = {codes, scales, (int)fmt, dim % 8 == 0 && aligned(codes, 8)};
+    a.weight = weight;
+    a.bias = bias;
+    a.ids = ids;
+    a.m = m;
+    a.dim = dim;
+    a.n_groups = n_groups;
+    a.pvec = vec_ok(weight, dim, dim, 4) && aligned(bias, 16);
+    a.eps = eps;
+    a.center = kind == HTL_NORM_LAYER;
+    const int tx = x_scales ? kSrcRows8 : (int)x_dtype;
+    with_hold(dim, [&](auto h) { launch_norm<decltype(h)>(a, tx, (int)y_dtype, stream); });
+    return check_launch("norm_rows");
+}
+
+extern "C" size_t norm_back_workspace_bytes(int64_t m, int n_groups, int dim) {
+    if (m < 0 || m > kMaxRows || n_groups < 1 || n_groups > kMaxGroups || dim < 1 || dim > kMaxNormDim) return 0;
+    // partial sums of the weight's and the bias's gradients, a row per chunk each
+    return align_up((size_t)(2 * norm_chunks(m, n_groups, dim) * dim) * 4, 256);
+}
+
+extern "C" htl_status norm_rows_backward(const void* dy, htl_dtype dy_dtype, int64_t ld_dy, const void* x,
+                                         htl_dtype x_dtype, int64_t ldx, const uint8_t* x_scales, htl_rows8_fmt x_fmt,
+                                         const void* dres, int64_t ld_dres, int64_t m, int dim, const float* weight,
+                                         const int32_t* order, const int32_t* offsets, int n_groups,
+                                         htl_norm_kind kind, float eps, void* dx, float* dweight, float* dbias,
+                                         void* ws, size_t ws_bytes, hipStream_t stream) {
+    clear_error();
+    HTL_REQUIRE(m >= 0 && m <= kMaxRows, "norm_rows_backward: row count out of range");
+    HTL_REQUIRE(dim >= 1 && dim <= kMaxNormDim, "norm_rows_backward: dim out of range");
+    HTL_REQUIRE(n_groups >= 1 && n_groups <= kMaxGroups, "norm_rows_backward: group count out of range");
+    HTL_REQUIRE(kind == HTL_NORM_RMS || kind == HTL_NORM_LAYER, "norm_rows_backward: unknown kind");
+    HTL_REQUIRE(known(x_dtype) && known(dy_dtype), "norm_rows_backward: dtypes must be HTL_F32 or HTL_BF16");
+    HTL_REQUIRE(x_fmt == HTL_ROWS8_I8 || x_fmt == HTL_ROWS8_E4M3, "norm_rows_backward: unknown 8-bit format");
+    HTL_REQUIRE(eps >= 0.0f, "norm_rows_backward: eps must not be negative");
+    HTL_REQUIRE(offsets || (n_groups == 1 && !order), "norm_rows_backward: several groups need offsets");
+    HTL_REQUIRE(ldx >= dim && ld_dy >= dim && (!dres || ld_dres >= dim), "norm_rows_backward: row stride below dim");
+    const int xe = x_scales ? 1 : elem(x_dtype), de = elem(dy_dtype), re = elem(x_dtype);
+    HTL_REQUIRE(weight && dweight && (m == 0 || (dy && x && dx)), "norm_rows_backward: null pointer");
+    HTL_REQUIRE(aligned(x, xe) && aligned(dy, de) && aligned(dres, re) && aligned(dx, re) && aligned(weight, 4) &&
+                    aligned(dweight, 4) && aligned(dbias, 4) && aligned(order, 4) && aligned(offsets, 4),
+                "norm_rows_backward: misaligned pointer");
+    HTL_REQUIRE(ws && aligned(ws, 256) && ws_bytes >= norm_back_workspace_bytes(m, n_groups, dim),
+                "norm_rows_backward: workspace too small or misaligned");
+    NormBackArgs a;
+    a.dy = {dy, nullptr, ld_dy, 0, vec_ok(dy, ld_dy, dim, de)};
+    a.x = {x, x_scales, ldx, (int)x_fmt,
+           x_scales ? (dim % 8 == 0 && ldx % 8 == 0 && aligned(x, 8)) : vec_ok(x, ldx, dim, xe)};
+    a.dres = {dres, nullptr, ld_dres, 0, dres ? vec_ok(dres, ld_dres, dim, re) : 0};
+    a.dx = {dx, dim, vec_ok(dx, dim, dim, re)};
+    a.weight = weight;
+    a.order = order;
+    a.offsets = offsets;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    a.partial = (float*)ws;
+    a.rows = norm_rows_per_chunk(m, dim);
+    a.chunks = norm_chunks(m, n_groups, dim);
+    a.m = m;
+    a.dim = dim;
+    a.n_groups = n_groups;
+    a.pvec = vec_ok(weight, dim, dim, 4);
+    a.gvec = vec_ok(dweight, dim, dim, 4) && aligned(dbias, 16);
+    a.eps = eps;
+    a.center = kind == HTL_NORM_LAYER;
+    const bool d32 = dy_dtype == HTL_F32, x32 = x_dtype == HTL_F32;
+    with_hold(dim, [&](auto h) {
+        using H = decltype(h);
+        if (x_scales) {
+            if (d32 && x32) launch_norm_back<H, kSrcF32, kSrcRows8, kSrcF32>(a, stream);
+            else if (d32) launch_norm_back<H, kSrcF32, kSrcRows8, kSrcBf16>(a, stream);
+            else if (x32) launch_norm_back<H, kSrcBf16, kSrcRows8, kSrcF32>(a, stream);
+            else launch_norm_back<H, kSrcBf16, kSrcRows8, kSrcBf16>(a, stream);
+        } else {
+            if (d32 && x32) launch_norm_back<H, kSrcF32, kSrcF32, kSrcF32>(a, stream);
+            else if (d32) launch_norm_back<H, kSrcF32, kSrcBf16, kSrcBf16>(a, stream);
+            else if (x32) launch_norm_back<H, kSrcBf16, kSrcF32, kSrcF32>(a, stream);
+            else launch_norm_back<H, kSrcBf16, kSrcBf16, kSrcBf16>(a, stream);
+        }
+    });
+    const htl_status st = check_launch("norm_rows_backward");
+    if (st != HTL_OK) return st;
+    const htl_status s1 = sum_chunks(a.partial, dweight, offsets, n_groups, m, a.rows, dim, stream);
+    if (s1 != HTL_OK || !dbias) return s1;
+    return sum_chunks(a.partial + a.chunks * dim, dbias, offsets, n_groups, m, a.rows, dim, stream);
+}

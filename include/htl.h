@@ -557,6 +557,132 @@ htl_status emb_grad_segment_sum_adam(htl_table* t, const int32_t* slots, const f
                                      int64_t u_max, float lr, float b1, float b2, float eps,
                                      int64_t step, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---------------------------------------------- dense operators on rows --
+ * What follows the lookup: rows that belong to groups (the feature table of
+ * each row, or the expert that a router chose for it) pass through per-group
+ * norms and matrices.  [MTGR] section 4 describes the dense side of the
+ * model: a layer norm with its own parameters for each group of tokens, and
+ * blocks whose normed output is gated and added to their input.  The calls
+ * below are this library's reading of it, each with its backward pass.
+ *
+ * Shared by all of them:
+ *   - Rows are row-major with a row stride in elements (ld >= row length);
+ *     outputs are dense.  Any row length and alignment of at least the
+ *     element size is right; row lengths in multiples of 8 with 16-byte aligned rows are fast.
+ *   - Statistics, sums and products accumulate in fp32; a bf16 result is
+ *     rounded once, to nearest even.  Results depend on the inputs alone,
+ *     not on the order in which workgroups run.
+ *   - ids int32[m] is the group of each row; any value outside
+ *     [0, n_groups) means no group.  order, offsets are the plan that
+ *     row_groups writes for them.  Without a plan (null) all rows are of one
+ *     group; offsets without order mean rows that already lie group by group.
+ *     Offsets that break the rules of row_groups, and order entries outside
+ *     [0, m), read and write nothing outside the rows given. */
+#define HTL_MAX_GROUPS 4095
+#define HTL_MAX_NORM_DIM 16384
+#define HTL_MAX_PRODUCT_DIM 65536
+typedef enum { HTL_ROWS8_I8 = 0, HTL_ROWS8_E4M3 = 1, HTL_ROWS8_RANGE_ = 0x7FFFFFFF } htl_rows8_fmt;
+typedef enum { HTL_NORM_RMS = 0, HTL_NORM_LAYER = 1, HTL_NORM_RANGE_ = 0x7FFFFFFF } htl_norm_kind;
+typedef enum { HTL_ACT_NONE = 0, HTL_ACT_SIGMOID = 1, HTL_ACT_SILU = 2, HTL_ACT_RANGE_ = 0x7FFFFFFF } htl_act;
+
+/* row_groups -- which rows belong to which group.
+ *   ids      int32[m], 0 <= m < 2^31 - 4096; 1 <= n_groups <= HTL_MAX_GROUPS.
+ *   order    int32[m] out: the rows of group 0, of group 1, ..., each
+ *            group's rows in ascending order, then the rows of no group.
+ *   offsets  int32[n_groups + 1] out: order[offsets[g] .. offsets[g+1]) are
+ *            the rows of group g.
+ *   ws       at least row_groups_workspace_bytes(m, n_groups) bytes,
+ *            256-byte aligned (0 for arguments out of range). */
+size_t row_groups_workspace_bytes(int64_t m, int n_groups);
+htl_status row_groups(const int32_t* ids, int64_t m, int n_groups, int32_t* order, int32_t* offsets, void* ws,
+                      size_t ws_bytes, hipStream_t stream);
+
+/* rows8_save, rows8_load -- rows kept in 8 bits, and read back.  Each block
+ * of 32 elements of a row (the last may be shorter) shares the scale 2^e, e
+ * >= -126 the least with which its largest magnitude is at most 127 * 2^e
+ * (HTL_ROWS8_I8) or 448 * 2^e (HTL_ROWS8_E4M3); an element is kept as the
+ * nearest integer, or e4m3 number, to x / 2^e (ties to even).
+ *   x, y     dtype[m][dim], 1 <= dim <= 65536; ldx the row stride of x.
+ *   codes    uint8[m][dim]; scales uint8[m][ceil(dim / 32)]: e + 127, or 255
+ *            for a block with an infinity or NaN, which reads back as NaN.
+ * Codes times scales are exact in bf16 (but for subnormal results). */
+htl_status rows8_save(const void* x, htl_dtype dtype, int64_t ldx, int64_t m, int dim, htl_rows8_fmt fmt,
+                      uint8_t* codes, uint8_t* scales, hipStream_t stream);
+htl_status rows8_load(const uint8_t* codes, const uint8_t* scales, htl_rows8_fmt fmt, int64_t m, int dim, void* y,
+                      htl_dtype dtype, hipStream_t stream);
+
+/* norm_rows -- y = n w_g + b_g with n = (x - mean) / sqrt(var + eps)
+ * (HTL_NORM_LAYER) or x / sqrt(mean(x^2) + eps) (HTL_NORM_RMS); a row of no
+ * group gives zeros.
+ *   x          x_dtype[m][dim], 1 <= dim <= HTL_MAX_NORM_DIM; with x_scales,
+ *              x holds 8-bit codes of format x_fmt (a norm recomputed from
+ *              what was kept).
+ *   weight     float[n_groups][dim]; bias nullable, the same shape.
+ *   ids        nullable if n_groups is 1: then every row is of group 0.
+ *   codes, scales  nullable: x's 8-bit copy, as rows8_save writes it. */
+htl_status norm_rows(const void* x, htl_dtype x_dtype, int64_t ldx, const uint8_t* x_scales, htl_rows8_fmt x_fmt,
+                     int64_t m, int dim, const float* weight, const float* bias, const int32_t* ids, int n_groups,
+                     htl_norm_kind kind, float eps, void* y, htl_dtype y_dtype, uint8_t* codes, uint8_t* scales,
+                     htl_rows8_fmt fmt, hipStream_t stream);
+
+/* norm_rows_backward -- gradients of norm_rows at x (or at what x's 8-bit
+ * copy holds): dx[m][dim] in x_dtype, dweight and dbias (nullable) summed
+ * over each group's rows (zeros for a group of none).
+ *   dres       nullable x_dtype[m][dim]: added to dx (the gradient that
+ *              reaches x beside the norm); a row of no group has dx = dres, or 0.
+ *   ws         at least norm_back_workspace_bytes(m, n_groups, dim) bytes,
+ *              256-byte aligned. */
+size_t norm_back_workspace_bytes(int64_t m, int n_groups, int dim);
+htl_status norm_rows_backward(const void* dy, htl_dtype dy_dtype, int64_t ld_dy, const void* x, htl_dtype x_dtype,
+                              int64_t ldx, const uint8_t* x_scales, htl_rows8_fmt x_fmt, const void* dres,
+                              int64_t ld_dres, int64_t m, int dim, const float* weight, const int32_t* order,
+                              const int32_t* offsets, int n_groups, htl_norm_kind kind, float eps, void* dx,
+                              float* dweight, float* dbias, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* norm_gate -- the end of a block: out = x + scale * act(u) * (n w_g + b_g),
+ * n the norm of z as in norm_rows; a row of no group gives out = x.
+ *   x, out     x_dtype[m][dim]; z, u z_dtype[m][dim].
+ *   act        u itself, 1 / (1 + exp(-u)), or u / (1 + exp(-u)).
+ *   z_codes, z_scales, u_codes, u_scales  all null, or the 8-bit copies of z
+ *              and u, as rows8_save writes them. */
+htl_status norm_gate(const void* x, htl_dtype x_dtype, int64_t ldx, const void* z, int64_t ldz, const void* u,
+                     int64_t ldu, htl_dtype z_dtype, int64_t m, int dim, const float* weight, const float* bias,
+                     const int32_t* ids, int n_groups, htl_norm_kind kind, float eps, htl_act act, float scale,
+                     void* out, uint8_t* z_codes, uint8_t* z_scales, uint8_t* u_codes, uint8_t* u_scales,
+                     htl_rows8_fmt fmt, hipStream_t stream);
+
+/* norm_gate_backward -- gradients of norm_gate at z and u (or at what their
+ * 8-bit copies hold, with z_scales and u_scales): dz, du in z_dtype (zeros
+ * for a row of no group), dweight, dbias (nullable) as in
+ * norm_rows_backward.  The gradient of x is dout itself.  ws as
+ * norm_rows_backward. */
+htl_status norm_gate_backward(const void* dout, htl_dtype dout_dtype, int64_t ld_dout, const void* z, int64_t ldz,
+                              const uint8_t* z_scales, const void* u, int64_t ldu, const uint8_t* u_scales,
+                              htl_dtype z_dtype, htl_rows8_fmt fmt, int64_t m, int dim, const float* weight,
+                              const float* bias, const int32_t* order, const int32_t* offsets, int n_groups,
+                              htl_norm_kind kind, float eps, htl_act act, float scale, void* dz, void* du,
+                              float* dweight, float* dbias, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* grouped_mm -- y[i] = w[g] x[i], g the group of row i; zeros for a row of no
+ * group.  Rows stay where they are: the plan says which matrix each meets.
+ *   x          dtype[m][k]; w dtype[n_groups][n][k] dense; y y_dtype[m][n];
+ *              1 <= n, k <= HTL_MAX_PRODUCT_DIM. */
+htl_status grouped_mm(const void* x, int64_t ldx, const void* w, htl_dtype dtype, int64_t m, int n, int k,
+                      const int32_t* order, const int32_t* offsets, int n_groups, void* y, htl_dtype y_dtype,
+                      hipStream_t stream);
+
+/* grouped_mm_backward -- dx[i] = w[g]^T dy[i] (dx nullable: not wanted), and
+ * dw[g] = sum over the group's rows of dy[i] x[i]^T in fp32 (dw nullable;
+ * zeros for a group of no rows).
+ *   dy         dtype[m][n]; dx dx_dtype[m][k]; dw float[n_groups][n][k].
+ *   ws         at least grouped_mm_backward_workspace_bytes(m, n_groups, n,
+ *              k) bytes, 256-byte aligned (not needed without dw). */
+size_t grouped_mm_backward_workspace_bytes(int64_t m, int n_groups, int n, int k);
+htl_status grouped_mm_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, const void* w,
+                               htl_dtype dtype, int64_t m, int n, int k, const int32_t* order,
+                               const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype, float* dw,
+                               void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* htl_copy_probe -- a plain streaming device-to-device copy (one 16-byte
  * vector per thread, full grid), the achievable-bandwidth reference against
  * which the lookup kernels' HBM rates are read.  A measurement aid, not a

@@ -1,0 +1,553 @@
+"""Dense operators on rows against plain 64-bit forms.
+
+Tolerances are derived, not fitted: with u = 2^-24 the half step of fp32, a
+sum of n terms in fp32 is off by at most n u times the sum of magnitudes in
+any order, each further operation by u, and a bf16 result by half a step,
+2^-8 of its value.  The bounds below add these up per element.
+"""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = {torch.float32: U, torch.bfloat16: 2.0 ** -8}
+EPS = 1e-6
+
+
+def _ids(rng, m, g, kind):
+    if kind == "tables":
+        ids = np.arange(m) % g
+    elif kind == "none":
+        ids = np.full(m, -1)
+    elif kind == "one":                       # every row in one group, the others empty
+        ids = np.full(m, g // 2)
+    else:
+        ids = np.minimum((rng.random(m) ** 2 * g).astype(np.int64), g - 1)
+        if kind == "dropped" and m:
+            ids[rng.random(m) < 0.2] = -1
+            ids[rng.random(m) < 0.1] = g + 5
+        if kind == "sorted":
+            ids = np.sort(ids)
+    return ids.astype(np.int32)
+
+
+def _plan(htl, ids, g):
+    return htl.group_rows(torch.from_numpy(ids).cuda(), g)
+
+
+def _members(ids, g):
+    return [np.flatnonzero(ids == i) for i in range(g)]
+
+
+def _close(got, want, tol, what):
+    got = got.detach().cpu().double()
+    bad = ~((got - want).abs() <= tol)
+    bad &= ~(torch.isnan(got) & torch.isnan(want))
+    assert not bad.any(), (what, int(bad.sum()), float((got - want).abs()[bad].max()), float(tol[bad].min()))
+
+
+# ---------------------------------------------------------------- groups --
+@pytest.mark.parametrize("m", [0, 1, 2, 63, 64, 65, 1000, 16384, 16385, 70001, 1 << 20])
+@pytest.mark.parametrize("g,kind", [(1, "one"), (26, "tables"), (26, "dropped"), (70, "sorted"), (300, "none"),
+                                    (1023, "dropped"), (1024, "dropped"), (4095, "dropped")])
+def test_group_rows(htl, m, g, kind):
+    rng = np.random.default_rng(m + g)
+    ids = _ids(rng, m, g, kind)
+    plan = _plan(htl, ids, g)
+    key = np.where((ids < 0) | (ids >= g), g, ids)
+    assert np.array_equal(plan.order.cpu().numpy(), np.argsort(key, kind="stable"))
+    want = np.concatenate([[0], np.cumsum(np.bincount(key, minlength=g + 1)[:g])])
+    assert np.array_equal(plan.offsets.cpu().numpy(), want)
+
+
+# ----------------------------------------------------------------- rows8 --
+def _rows8(x, fmt):
+    """Values, scale bytes of 8-bit rows by their definition, in fp64."""
+    x = x.double()
+    m, dim = x.shape
+    nb = (dim + 31) // 32
+    most = 127.0 if fmt == "i8" else 448.0
+    out, scales = torch.empty_like(x), torch.empty(m, nb, dtype=torch.uint8)
+    for b in range(nb):
+        v = x[:, 32 * b:32 * b + 32]
+        top = v.abs().amax(1, keepdim=True)
+        e = torch.full_like(top, -126.0)
+        for k in range(-126, 122):
+            e = torch.where(torch.ldexp(torch.tensor(most).double(), torch.tensor(k)) < top, float(k + 1), e)
+        unit = torch.exp2(e)
+        q = v / unit
+        if fmt == "e4m3":
+            k = (torch.frexp(q.abs()).exponent - 1).clamp(min=-6).double()
+            step = torch.exp2(torch.where(q == 0, -6.0, k) - 3)
+            q = torch.round(q / step) * step
+        else:
+            q = torch.round(q)
+        fin = torch.isfinite(v).all(1, keepdim=True)
+        out[:, 32 * b:32 * b + 32] = torch.where(fin, q * unit, float("nan"))
+        scales[:, b] = torch.where(fin, e + 127, 255.0)[:, 0].to(torch.uint8)
+    return out, scales
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,dim", [(0, 8), (1, 1), (3, 7), (5, 31), (4, 32), (9, 33), (17, 64), (33, 77), (300, 128),
+                                   (2, 1000), (1, 65536)])
+def test_rows8(htl, fmt, dtype, m, dim):
+    gen = torch.Generator().manual_seed(m + dim)
+    x = (torch.randn(m, dim, generator=gen) * torch.exp2(torch.randint(-20, 20, (m, 1), generator=gen).float())).to(dtype)
+    if m > 2:
+        x[0] = 0.0
+        x[1, dim // 2] = float("inf") if fmt == "i8" else float("nan")
+        x[2] = torch.tensor(3.0e38).to(dtype) * torch.sign(x[2].float()).to(dtype)
+        x[-1] *= 2.0 ** -110                   # scales at their floor
+    want, scales = _rows8(x, fmt)
+    kept = htl.save_rows8(x.cuda(), fmt)
+    assert torch.equal(kept.scales.cpu(), scales)
+    for out in (torch.float32, torch.bfloat16):
+        got = htl.load_rows8(kept, out).cpu()
+        assert torch.equal(torch.nan_to_num(got.double(), nan=7.25), torch.nan_to_num(want.to(out).double(), nan=7.25))
+
+
+def test_rows8_ties_and_edges(htl):
+    # values half-way between codes, at the largest code, and just beyond it
+    x = torch.zeros(4, 32)
+    x[0, :4] = torch.tensor([127.0, 0.5, 1.5, -2.5])
+    x[1, :4] = torch.tensor([127.0 + 2.0 ** -10, 1.0, 3.0, -1.0])    # the scale doubles
+    x[2, :4] = torch.tensor([448.0, 17.0, 19.0, -2.0 ** -10])
+    x[3, :4] = torch.tensor([449.0, 34.0, 38.0, 2.0 ** -8])
+    for fmt in ("i8", "e4m3"):
+        want, scales = _rows8(x, fmt)
+        kept = htl.save_rows8(x.cuda(), fmt)
+        assert torch.equal(kept.scales.cpu(), scales)
+        assert torch.equal(htl.load_rows8(kept).cpu().double(), want)
+
+
+# ----------------------------------------------------------------- norms --
+class Norm:
+    """n and r of rows in fp64, and how far fp32 statistics may put n off, per element (e_n)."""
+
+    def __init__(self, x, kind):
+        x = x.double()
+        d = x.shape[1]
+        mean = x.mean(1, keepdim=True) if kind == "layer" else torch.zeros_like(x[:, :1])
+        c = x - mean
+        self.r = 1.0 / torch.sqrt((c * c).mean(1, keepdim=True) + EPS)
+        self.n = c * self.r
+        shift = (d + 4) * U * x.abs().mean(1, keepdim=True) if kind == "layer" else 0.0
+        self.e_n = self.r * shift * (1 + self.n.abs()) + (d + 16) * U * self.n.abs()
+        self.kind, self.dim = kind, d
+
+    def back(self, dn, e_dn):
+        """Gradient from that of n (off by e_dn), and its bound before rounding."""
+        d, n, r = self.dim, self.n, self.r
+        c1 = dn.mean(1, keepdim=True) if self.kind == "layer" else torch.zeros_like(r)
+        c2 = (dn * n).mean(1, keepdim=True)
+        e1 = e_dn.mean(1, keepdim=True) + (d + 4) * U * dn.abs().mean(1, keepdim=True) if self.kind == "layer" else 0.0
+        e2 = ((e_dn * n.abs() + dn.abs() * self.e_n).mean(1, keepdim=True)
+              + (d + 8) * U * (dn * n).abs().mean(1, keepdim=True))
+        mag = dn.abs() + c1.abs() + (n * c2).abs()
+        err = e_dn + e1 + n.abs() * e2 + self.e_n * c2.abs() + 8 * U * mag
+        return r * (dn - c1 - n * c2), r * (err + (d + 16) * U * mag)
+
+
+def _param_of(p, ids, g):
+    on = (ids >= 0) & (ids < g)
+    out = p.double()[torch.from_numpy(np.where(on, ids, 0)).long()]
+    return out, torch.from_numpy(on).unsqueeze(1)
+
+
+def _sum_of(t, tol, ids, g):
+    """Per-group sums of t's rows and their bound: each row's own, and the sum's."""
+    s = torch.zeros(g, t.shape[1], dtype=torch.float64)
+    e = torch.zeros_like(s)
+    for i, rows in enumerate(_members(ids, g)):
+        s[i] = t[rows].sum(0)
+        e[i] = tol[rows].sum(0) + (len(rows) + 8) * U * t[rows].abs().sum(0)
+    return s, e + 1e-30
+
+
+SHAPES = [(1, 1), (2, 7), (70, 8), (33, 33), (65, 64), (129, 100), (1000, 128), (7, 200), (40, 256), (19, 512),
+          (6, 1000), (9, 1024), (5, 2048), (3, 3000), (4, 4096), (3, 5001), (2, 8192), (3, 16384)]
+
+
+def _inputs(m, dim, g, seed, kinds=("tables", "dropped", "sorted", "one", "none")):
+    rng = np.random.default_rng(seed)
+    gen = torch.Generator().manual_seed(seed)
+    ids = _ids(rng, m, g, kinds[seed % len(kinds)])
+    return gen, ids
+
+
+@pytest.mark.parametrize("m,dim", SHAPES)
+@pytest.mark.parametrize("xd,yd,kind,save,bias,g", [
+    (torch.bfloat16, torch.bfloat16, "layer", "i8", True, 26), (torch.float32, torch.bfloat16, "rms", "e4m3", False, 3),
+    (torch.float32, torch.float32, "layer", None, True, 70), (torch.bfloat16, torch.float32, "rms", None, True, 1)])
+def test_norm_rows(htl, m, dim, xd, yd, kind, save, bias, g):
+    gen, ids = _inputs(m, dim, g, m + dim + g)
+    x = (torch.randn(m, dim, generator=gen) + 0.5).to(xd)
+    weight = 1 + 0.1 * torch.randn(g, dim, generator=gen)
+    b = 0.1 * torch.randn(g, dim, generator=gen) if bias else None
+    plan = _plan(htl, ids, g)
+    bc = None if b is None else b.cuda()
+    kw = dict(groups=plan, kind=kind, eps=EPS)
+    y, kept = htl.norm_rows(x.cuda(), weight.cuda(), bc, out_dtype=yd, save=save, **kw)
+    w, on = _param_of(weight, ids, g)
+    bw = _param_of(b, ids, g)[0] if bias else torch.zeros_like(w)
+
+    def check_y(y, src):
+        N = Norm(src, kind)
+        want = torch.where(on, N.n * w + bw, 0.0)
+        _close(y, want, w.abs() * N.e_n + 2 * U * ((N.n * w).abs() + bw.abs()) + HALF[yd] * want.abs() + 1e-37, "y")
+
+    check_y(y, x)
+    if save is None:
+        src = x
+    else:
+        src = _rows8(x, save)[0]
+        assert torch.equal(htl.load_rows8(kept, torch.float32).cpu().double(), src)
+        again, _ = htl.norm_rows(kept, weight.cuda(), bc, out_dtype=yd, **kw)     # recomputed from the copy
+        check_y(again, src)
+    N = Norm(src, kind)
+    dy = torch.randn(m, dim, generator=gen).to(yd)
+    dres = torch.randn(m, dim, generator=gen).to(xd)
+    for res in (dres, None):
+        dx, dw, db = htl.norm_rows_backward(dy.cuda(), kept, weight.cuda(), bias=bias,
+                                            dresidual=None if res is None else res.cuda(), **kw)
+        dyd = torch.where(on, dy.double(), 0.0)
+        gx, e = N.back(dyd * w, U * (dyd * w).abs())
+        gx = torch.where(on, gx, 0.0)
+        want = gx + (0.0 if res is None else res.double())
+        _close(dx, want, e + U * want.abs() + HALF[xd] * want.abs() * 1.01 + 1e-37, "dx")
+        s, t = _sum_of(dyd * N.n, dyd.abs() * N.e_n, ids, g)
+        _close(dw, s, t, "dweight")
+        if bias:
+            s, t = _sum_of(dyd, torch.zeros_like(dyd), ids, g)
+            _close(db, s, t, "dbias")
+        else:
+            assert db is None
+
+
+def _act(u, act):
+    s = torch.sigmoid(u)
+    if act == "none":
+        return u, torch.ones_like(u)
+    return (s, s * (1 - s)) if act == "sigmoid" else (u * s, s * (1 + u * (1 - s)))
+
+
+@pytest.mark.parametrize("m,dim", SHAPES)
+@pytest.mark.parametrize("xd,zd,kind,act,save,bias,g", [
+    (torch.float32, torch.bfloat16, "layer", "sigmoid", "e4m3", True, 26),
+    (torch.bfloat16, torch.bfloat16, "rms", "silu", None, False, 1),
+    (torch.bfloat16, torch.float32, "rms", "none", "i8", True, 3),
+    (torch.float32, torch.float32, "layer", "silu", None, True, 70)])
+def test_norm_gate(htl, m, dim, xd, zd, kind, act, save, bias, g):
+    gen, ids = _inputs(m, dim, g, m + dim + g + 1)
+    x = torch.randn(m, dim, generator=gen).to(xd)
+    z = (2 * torch.randn(m, dim, generator=gen) - 0.3).to(zd)
+    u = (2 * torch.randn(m, dim, generator=gen)).to(zd)
+    weight = 1 + 0.1 * torch.randn(g, dim, generator=gen)
+    b = 0.1 * torch.randn(g, dim, generator=gen) if bias else None
+    bc = None if b is None else b.cuda()
+    plan = _plan(htl, ids, g)
+    kw = dict(groups=plan, kind=kind, eps=EPS, act=act, scale=0.75)
+    out, kz, ku = htl.norm_gate(x.cuda(), z.cuda(), u.cuda(), weight.cuda(), bc, save=save, **kw)
+    w, on = _param_of(weight, ids, g)
+    bw = _param_of(b, ids, g)[0] if bias else torch.zeros_like(w)
+    N = Norm(z, kind)
+    v = N.n * w + bw
+    e_v = w.abs() * N.e_n + 2 * U * ((N.n * w).abs() + bw.abs())
+    a, _ = _act(u.double(), act)
+    add = torch.where(on, 0.75 * a * v, 0.0)
+    want = x.double() + add
+    # the activation is a few operations and one exponential: 16 u
+    _close(out, want, 0.75 * a.abs() * e_v + 20 * U * add.abs() + (U + HALF[xd]) * want.abs() + 1e-37, "out")
+    zs, us = z, u
+    if save is not None:
+        zs, us = _rows8(z, save)[0], _rows8(u, save)[0]
+        assert torch.equal(htl.load_rows8(kz, torch.float32).cpu().double(), zs)
+        assert torch.equal(htl.load_rows8(ku, torch.float32).cpu().double(), us)
+    dout = torch.randn(m, dim, generator=gen).to(xd)
+    dz, du, dw, db = htl.norm_gate_backward(dout.cuda(), kz, ku, weight.cuda(), bc, **kw)
+    N = Norm(zs, kind)
+    v = N.n * w + bw
+    e_v = w.abs() * N.e_n + 2 * U * ((N.n * w).abs() + bw.abs())
+    uu = us.double()
+    a, slope = _act(uu, act)
+    D = torch.where(on, 0.75 * dout.double(), 0.0)
+    s = torch.sigmoid(uu)
+    mag = s * (1 + uu.abs() * (1 + s)) if act == "silu" else (s if act == "sigmoid" else torch.ones_like(uu))
+    want = D * slope * v
+    _close(du, want, D.abs() * (16 * U * mag * v.abs() + (slope.abs() + 16 * U * mag) * e_v)
+           + (4 * U + HALF[zd]) * want.abs() + 1e-37, "dgate")
+    e = D * a
+    gz, err = N.back(e * w, 20 * U * (e * w).abs())
+    gz = torch.where(on, gz, 0.0)
+    _close(dz, gz, err + HALF[zd] * gz.abs() * 1.01 + 1e-37, "dz")
+    sums, t = _sum_of(e * N.n, e.abs() * N.e_n + 20 * U * (e * N.n).abs(), ids, g)
+    _close(dw, sums, t, "dweight")
+    if bias:
+        sums, t = _sum_of(e, 20 * U * e.abs(), ids, g)
+        _close(db, sums, t, "dbias")
+
+
+def test_norm_gradients_against_differences(htl):
+    """The backward calls against central differences of the forward calls (fp32).
+
+    f = sum(c * output) is differenced in single elements with h = 2^-6: the
+    truncation is f''' h^2 / 6 (bounded here by 1 with unit-scale inputs,
+    so 1e-4 of the scale of the derivative), and fp32 outputs off by u of
+    their value give 2 u sum|c y| / (2 h)."""
+    gen = torch.Generator().manual_seed(3)
+    m, dim, g, h = 6, 40, 2, 2.0 ** -6
+    ids = np.array([0, 1, 1, 0, -1, 1], np.int32)
+    plan = _plan(htl, ids, g)
+    x, z, u, c = (torch.randn(m, dim, generator=gen) for _ in range(4))
+    w, b = 1 + 0.1 * torch.randn(g, dim, generator=gen), 0.1 * torch.randn(g, dim, generator=gen)
+    kw = dict(groups=plan, kind="layer", eps=EPS)
+
+    def f_norm(x, w, b):
+        return htl.norm_rows(x.cuda(), w.cuda(), b.cuda(), **kw)[0].cpu().double().mul(c).sum()
+
+    def f_gate(z, u, w, b):
+        return htl.norm_gate(x.cuda(), z.cuda(), u.cuda(), w.cuda(), b.cuda(), scale=0.5, **kw)[0].cpu().double().mul(c).sum()
+
+    got = htl.norm_rows_backward(c.cuda(), x.cuda(), w.cuda(), bias=True, **kw)
+    dz, du, dw, db = htl.norm_gate_backward(c.cuda(), z.cuda(), u.cuda(), w.cuda(), b.cuda(), scale=0.5, **kw)
+    tol = 20 * h * h + 2 * U * float(c.abs().sum()) * 4 / (2 * h)
+    for f, args, grads in ((f_norm, [x, w, b], got), (f_gate, [z, u, w, b], (dz, du, dw, db))):
+        for k, grad in enumerate(grads):
+            for i, j in ((0, 0), (1, 17), (args[k].shape[0] - 1, dim - 1)):
+                up, dn = [t.clone() for t in args], [t.clone() for t in args]
+                up[k][i, j] += h
+                dn[k][i, j] -= h
+                want = float((f(*up) - f(*dn)) / (2 * h))
+                assert abs(float(grad[i, j]) - want) <= tol, (f.__name__, k, i, j, float(grad[i, j]), want)
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_norm_leaves_other_rows_alone(htl, kind):
+    """A row with a NaN, one of infinities, a constant row and a zero row: their neighbours, and rows of no
+    group whatever they hold, come out as without them."""
+    gen = torch.Generator().manual_seed(5)
+    m, dim, g = 40, 96, 3
+    ids = (np.arange(m) % (g + 1)).astype(np.int32)          # id 3: no group
+    x = torch.randn(m, dim, generator=gen)
+    w = torch.ones(g, dim)
+    plan = _plan(htl, ids, g)
+    kw = dict(groups=plan, kind=kind, eps=EPS)
+    dy = torch.randn(m, dim, generator=gen)
+    clean = htl.norm_rows(x.cuda(), w.cuda(), **kw)[0].cpu()
+    clean_dx, clean_dw, _ = htl.norm_rows_backward(dy.cuda(), x.cuda(), w.cuda(), **kw)
+    bad = x.clone()
+    bad[3, 5], bad[7] = float("nan"), float("inf")            # both of no group
+    got = htl.norm_rows(bad.cuda(), w.cuda(), **kw)[0].cpu()
+    assert torch.equal(got, clean)
+    dx, dw, _ = htl.norm_rows_backward(dy.cuda(), bad.cuda(), w.cuda(), **kw)
+    assert torch.equal(dx, clean_dx) and torch.equal(dw, clean_dw)
+    bad[0, 1], bad[4], bad[8], bad[12] = float("nan"), float("inf"), 0.0, 3.0
+    got = htl.norm_rows(bad.cuda(), w.cuda(), **kw)[0].cpu()
+    keep = [i for i in range(m) if i not in (0, 4, 8, 12)]
+    assert torch.equal(got[keep], clean[keep])
+    assert torch.isnan(got[0]).all() and not torch.isfinite(got[4]).any()
+    assert torch.equal(got[8], torch.zeros(dim))
+    if kind == "layer":
+        assert torch.equal(got[12], torch.zeros(dim))         # no deviation: eps alone under the root
+
+
+def test_norm_without_groups_and_strided_rows(htl):
+    gen = torch.Generator().manual_seed(6)
+    wide = torch.randn(50, 3 * 136, generator=gen).cuda()
+    w = (1 + 0.1 * torch.randn(128, generator=gen)).cuda()
+    for off in (0, 8, 1, 3):                                  # aligned and unaligned rows inside wider ones
+        x, z, u = wide[:, off:off + 128], wide[:, 136 + off:264 + off], wide[:, 272 + off:400 + off]
+        y, kept = htl.norm_rows(x, w)
+        yc, _ = htl.norm_rows(x.contiguous(), w)
+        assert torch.equal(y, yc)
+        assert kept.data_ptr() == x.data_ptr()
+        a = htl.norm_rows_backward(u, x, w, dresidual=z)
+        b = htl.norm_rows_backward(u.contiguous(), x.contiguous(), w, dresidual=z.contiguous())
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and a[2] is None and a[1].shape == (1, 128)
+        a = htl.norm_gate(x, z, u, w)[0]
+        b = htl.norm_gate(x.contiguous(), z.contiguous(), u.contiguous(), w)[0]
+        assert torch.equal(a, b)
+        a = htl.norm_gate_backward(x, z, u, w)
+        b = htl.norm_gate_backward(x.contiguous(), z.contiguous(), u.contiguous(), w)
+        assert all(torch.equal(p, q) for p, q in zip(a[:3], b[:3]))
+    # a broadcast row, and transposed storage
+    y, _ = htl.norm_rows(wide[:1, :128].expand(50, 128), w)
+    assert torch.equal(y, y[:1].expand(50, 128))
+    t = wide[:, :128].t().contiguous().t()
+    assert torch.equal(htl.norm_rows(t, w)[0], htl.norm_rows(wide[:, :128], w)[0])
+
+
+# -------------------------------------------------------------- products --
+PRODUCTS = [(1, 1, 1, 1), (3, 2, 7, 5), (26, 26, 128, 256), (64, 16, 64, 64), (200, 3, 72, 40), (300, 5, 128, 128),
+            (1000, 26, 64, 100), (999, 1, 33, 65), (70, 70, 136, 24), (513, 4, 256, 520), (2000, 3, 8, 8),
+            (16, 2, 1032, 264), (5, 3, 2048, 16), (700, 2, 1, 9), (4100, 2, 64, 72), (1500, 2, 264, 520)]
+
+
+def _product_check(htl, m, g, k, n, dtype, ids, seed, out=None):
+    gen = torch.Generator().manual_seed(seed)
+    out = out or dtype
+    x = torch.randn(m, k, generator=gen).to(dtype)
+    w = (torch.randn(g, n, k, generator=gen) / k ** 0.5).to(dtype)
+    dy = torch.randn(m, n, generator=gen).to(dtype)
+    plan = _plan(htl, ids, g)
+    y = htl.grouped_mm(x.cuda(), w.cuda(), plan, out_dtype=out)
+    dx, dw = htl.grouped_mm_backward(dy.cuda(), x.cuda(), w.cuda(), plan, dx_dtype=out)
+    ry, ty = torch.zeros(m, n, dtype=torch.float64), torch.zeros(m, n, dtype=torch.float64)
+    rx, tx = torch.zeros(m, k, dtype=torch.float64), torch.zeros(m, k, dtype=torch.float64)
+    for i, rows in enumerate(_members(ids, g)):
+        a, b, d = x[rows].double(), w[i].double(), dy[rows].double()
+        ry[rows], ty[rows] = a @ b.t(), (k + 2) * U * (a.abs() @ b.abs().t())
+        rx[rows], tx[rows] = d @ b, (n + 2) * U * (d.abs() @ b.abs())
+        _close(dw[i], d.t() @ a, (len(rows) + 2) * U * (d.abs().t() @ a.abs()) + 1e-37, ("dw", i))
+    _close(y, ry, ty + HALF[out] * (ry.abs() + ty) + 1e-37, "y")
+    _close(dx, rx, tx + HALF[out] * (rx.abs() + tx) + 1e-37, "dx")
+    return x, w, dy, plan, y, dx, dw
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,g,k,n", PRODUCTS)
+def test_grouped_mm(htl, m, g, k, n, dtype):
+    rng = np.random.default_rng(m + k)
+    kinds = ("dropped", "tables", "sorted", "one")
+    ids = _ids(rng, m, g, kinds[(m + g) % 4])
+    out = torch.float32 if (m + n) % 3 == 0 else dtype
+    x, w, dy, plan, y, dx, dw = _product_check(htl, m, g, k, n, dtype, ids, m + n, out)
+    # one gradient at a time
+    only_x = htl.grouped_mm_backward(dy.cuda(), x.cuda(), w.cuda(), plan, dx_dtype=out, need_dw=False)
+    only_w = htl.grouped_mm_backward(dy.cuda(), x.cuda(), w.cuda(), plan, need_dx=False)
+    assert only_x[1] is None and torch.equal(only_x[0], dx)
+    assert only_w[0] is None and torch.equal(only_w[1], dw)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_grouped_mm_no_rows_in_any_group(htl, dtype):
+    for m in (0, 5, 300):
+        _product_check(htl, m, 4, 64, 72, dtype, np.full(m, -1, np.int32), m)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_grouped_mm_keeps_nan_in_its_row(htl, dtype):
+    """A NaN or an infinity in a row of no group reaches nothing; in a row of a
+    group it reaches that row's products and that group's weight gradient."""
+    m, g, k, n = 333, 3, 72, 136
+    ids = (np.arange(m) % (g + 1)).astype(np.int32)
+    x, w, dy, plan, y, dx, dw = _product_check(htl, m, g, k, n, dtype, ids, 1)
+    bad, bdy = x.clone(), dy.clone()
+    bad[3], bad[7, 2], bdy[11, 3], bdy[15] = float("inf"), float("nan"), float("nan"), float("inf")
+    assert torch.equal(htl.grouped_mm(bad.cuda(), w.cuda(), plan), y)
+    b_dx, b_dw = htl.grouped_mm_backward(bdy.cuda(), bad.cuda(), w.cuda(), plan)
+    assert torch.equal(b_dx, dx) and torch.equal(b_dw, dw)
+    bad[5, 1] = float("nan")                                   # row 5: group 1
+    got = htl.grouped_mm(bad.cuda(), w.cuda(), plan)
+    keep = [i for i in range(m) if i != 5]
+    assert torch.equal(got[keep], y[keep]) and torch.isnan(got[5]).all()
+    _, b_dw = htl.grouped_mm_backward(dy.cuda(), bad.cuda(), w.cuda(), plan)
+    assert torch.equal(b_dw[0], dw[0]) and torch.equal(b_dw[2], dw[2]) and torch.isnan(b_dw[1][:, 1]).all()
+
+
+def test_grouped_mm_strided_rows_and_no_plan(htl):
+    gen = torch.Generator().manual_seed(8)
+    wide = torch.randn(90, 400, generator=gen).bfloat16().cuda()
+    w = torch.randn(136, 128, generator=gen).bfloat16().cuda()
+    for off in (0, 8, 3):
+        x, dy = wide[:, off:off + 128], wide[:, 200 + off:336 + off]
+        assert torch.equal(htl.grouped_mm(x, w), htl.grouped_mm(x.contiguous(), w))
+        a, b = htl.grouped_mm_backward(dy, x, w), htl.grouped_mm_backward(dy.contiguous(), x.contiguous(), w)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and a[1].shape == (1, 136, 128)
+    # rows that lie group by group: offsets alone are the plan
+    ids = np.sort(_ids(np.random.default_rng(1), 90, 4, "dropped") % 4).astype(np.int32)
+    plan = _plan(htl, ids, 4)
+    w4 = torch.randn(4, 136, 128, generator=gen).bfloat16().cuda()
+    x = wide[:, :128]
+    assert torch.equal(htl.grouped_mm(x, w4, plan), htl.grouped_mm(x, w4, plan._replace(order=None)))
+
+
+@pytest.mark.parametrize("seed", range(3))
+def test_broken_plans_stay_in_bounds(htl, seed):
+    """Offsets out of range or decreasing, and order entries outside the rows, are clamped or skipped: rows
+    around the tensors keep their bits."""
+    rng = np.random.default_rng(seed)
+    m, g, k, n = 500, 5, 64, 72
+    off = rng.integers(-100, 700, g + 1).astype(np.int32)
+    order = rng.integers(-300, 800, m).astype(np.int32)
+    ids = torch.from_numpy(rng.integers(-2, 8, m).astype(np.int32)).cuda()
+    plan = htl.RowGroups(ids, torch.from_numpy(order).cuda(), torch.from_numpy(off).cuda(), g)
+    x = torch.randn(m, k, device="cuda").bfloat16()
+    dy = torch.randn(m, n, device="cuda").bfloat16()
+    w = torch.randn(g, n, k, device="cuda").bfloat16()
+    p = torch.ones(g, k, device="cuda")
+    y = htl.grouped_mm(x, w, plan)
+    dx, dw = htl.grouped_mm_backward(dy, x, w, plan)
+    a = htl.norm_rows(x, p, groups=plan)
+    b = htl.norm_rows_backward(x, x, p, groups=plan)
+    c = htl.norm_gate_backward(x, x, x, p, groups=plan)
+    torch.cuda.synchronize()
+    assert y.shape == (m, n) and dx.shape == (m, k) and dw.shape == (g, n, k) and a[0].shape == b[0].shape == c[0].shape
+
+
+def test_calls_on_another_stream_and_in_a_graph(htl):
+    gen = torch.Generator().manual_seed(9)
+    m, g, k = 4000, 7, 64
+    ids = torch.from_numpy(_ids(np.random.default_rng(2), m, g, "dropped")).cuda()
+    x = torch.randn(m, k, generator=gen).cuda()
+    w = torch.randn(g, k, k, generator=gen).bfloat16().cuda()
+    p = torch.ones(g, k, device="cuda")
+
+    def step():
+        plan = htl.group_rows(ids, g)
+        h, kept = htl.norm_rows(x, p, groups=plan, out_dtype="bf16", save="i8")
+        z = htl.grouped_mm(h, w, plan)
+        out, kz, ku = htl.norm_gate(x, z, h, p, groups=plan, save="e4m3")
+        dz, du, dp2, _ = htl.norm_gate_backward(out, kz, ku, p, groups=plan)
+        dh, dw = htl.grouped_mm_backward(dz, h, w, plan)
+        dx, dp, _ = htl.norm_rows_backward(dh, kept, p, groups=plan, dresidual=out)
+        return out, dx, dw, dp, dp2, du
+
+    want = [t.clone() for t in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step()
+        step()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = step()
+    for i in range(4):
+        x.add_(0.25 * i)
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+
+
+def test_rows_past_32_bits(htl):
+    """More than 2^32 elements in a tensor: the last rows against the same rows alone."""
+    m, dim = (1 << 25) + 65, 136
+    x = torch.empty(m, dim, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, m, 1 << 23):
+        x[a:a + (1 << 23)].normal_()
+    w = (1 + 0.1 * torch.randn(dim)).cuda()
+    mat = torch.randn(dim, dim, device="cuda").bfloat16()
+    tail = x[-1000:].clone()
+    y, kept = htl.norm_rows(x, w, save="i8")
+    ty, tkept = htl.norm_rows(tail, w, save="i8")
+    assert torch.equal(y[-1000:], ty)
+    assert torch.equal(kept.codes[-1000:], tkept.codes) and torch.equal(kept.scales[-1000:], tkept.scales)
+    assert torch.equal(htl.load_rows8(kept)[-1000:], htl.load_rows8(tkept))
+    dx, _, _ = htl.norm_rows_backward(y, kept, w)
+    assert torch.equal(dx[-1000:], htl.norm_rows_backward(ty, tkept, w)[0])
+    del dx, kept
+    out = htl.grouped_mm(x, mat)
+    assert torch.equal(out[-1000:], htl.grouped_mm(tail, mat))
+    dx, dw = htl.grouped_mm_backward(x, y, mat)
+    assert torch.equal(dx[-1000:], htl.grouped_mm_backward(tail, ty, mat)[0])
+    assert torch.isfinite(dw).all()
