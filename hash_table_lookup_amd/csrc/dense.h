@@ -440,8 +440,8 @@ inline bool vec_ok(const void* p, int64_t ld, int dim, int elem) {
 // Sums of a group's partial rows: out[g][d] = sum over its chunks of
 // partial[item][d], for the groups with more than one chunk (a lone chunk
 // writes its sums itself).  Chunks are added in order, so the result does
-// not depend on which workgroup ended first.
-htl_status sum_chunks(const float* partial, float* out, const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
+// not depend on which workgroup ended first.  limit: rows that partial holds.
+htl_status sum_chunks(const float* partial, int64_t limit, float* out, const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
                       int64_t width, hipStream_t stream);
 
 }  // namespace htl

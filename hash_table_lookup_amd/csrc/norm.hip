@@ -159,7 +159,8 @@ __global__ __launch_bounds__(H::kThreads) void k_norm_back(NormBackArgs a) {
 }
 
 // 64 columns per workgroup; its 16 waves take every 16th chunk of the group.
-__global__ __launch_bounds__(1024) void k_sum_chunks(const float* __restrict__ partial, float* __restrict__ out,
+__global__ __launch_bounds__(1024) void k_sum_chunks(const float* __restrict__ partial, int64_t limit,
+                                                    float* __restrict__ out,
                                                     const int32_t* __restrict__ offsets, int n_groups, int64_t m,
                                                     uint32_t R, int64_t width) {
     __shared__ float s[16][64];
@@ -168,6 +169,7 @@ __global__ __launch_bounds__(1024) void k_sum_chunks(const float* __restrict__ p
     int count;
     chunks_of_group(offsets, n_groups, m, R, 1, g, first, count);
     if (count == 1) return;
+    if (first + count > limit) count = first < limit ? (int)(limit - first) : 0;   // offsets that overlap
     for (int64_t d0 = blockIdx.x * 64ll; d0 < width; d0 += gridDim.x * 64ll) {
         const int64_t d = d0 + lane;
         float v = 0.0f;
@@ -200,12 +202,12 @@ uint32_t norm_chunk_rows(int64_t m, int dim) {
 int64_t norm_chunks(int64_t m, int n_groups, int dim) { return m / norm_chunk_rows(m, dim) + n_groups + 1; }
 uint32_t norm_rows_per_chunk(int64_t m, int dim) { return norm_chunk_rows(m, dim); }
 
-htl_status sum_chunks(const float* partial, float* out, const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
+htl_status sum_chunks(const float* partial, int64_t limit, float* out, const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
                       int64_t width, hipStream_t stream) {
     if (m <= (int64_t)R) return HTL_OK;      // every group is one chunk
     const int64_t cols = ceil_div(width, 64);
     hipLaunchKernelGGL(k_sum_chunks, dim3((unsigned)(cols < 4096 ? cols : 4096), (unsigned)n_groups), dim3(1024), 0,
-                       stream, partial, out, offsets, n_groups, m, R, width);
+                       stream, partial, limit, out, offsets, n_groups, m, R, width);
     return check_launch("partial sums");
 }
 
@@ -347,7 +349,7 @@ extern "C" htl_status norm_rows_backward(const void* dy, htl_dtype dy_dtype, int
     });
     const htl_status st = check_launch("norm_rows_backward");
     if (st != HTL_OK) return st;
-    const htl_status s1 = sum_chunks(a.partial, dweight, offsets, n_groups, m, a.rows, dim, stream);
+    const htl_status s1 = sum_chunks(a.partial, a.chunks, dweight, offsets, n_groups, m, a.rows, dim, stream);
     if (s1 != HTL_OK || !dbias) return s1;
-    return sum_chunks(a.partial + a.chunks * dim, dbias, offsets, n_groups, m, a.rows, dim, stream);
+    return sum_chunks(a.partial + a.chunks * dim, a.chunks, dbias, offsets, n_groups, m, a.rows, dim, stream);
 }

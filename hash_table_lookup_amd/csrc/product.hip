@@ -12,6 +12,8 @@ namespace htl {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 struct ProdArgs {
     const void* a;           // x (forward), dy (dx and dw)
@@ -21,111 +23,451 @@ struct ProdArgs {
     const int32_t* offsets;  // nullable: one group
     int64_t m, lda, ldb;     // ldb: row stride of x in dw
     int n, k, n_groups;
-    uint32_t rows;           // dw: rows per chunk
-    int64_t chunks;          // of rows, over all groups (an upper bound)
+    uint32_t rows;           // positions per chunk
     float* partial;          // dw: [chunks][n][k]
     int out_f32;
+    int out_vec;             // four outputs of a lane are stored at once
+    int64_t limit;           // dw: chunks that `partial` has room for
 };
 
 enum { kFwd = 0, kDx = 1, kDw = 2 };
 
-template <int T> __device__ __forceinline__ float elem_at(const void* p, int64_t i) {
-    return T == kSrcF32 ? ((const float*)p)[i] : __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
+// The output is cut into tiles of BR x BC: rows are x's (dy's) rows of one
+// group and columns n (k), or n and k for dw.  A tile is reduced 128 bytes of
+// each operand row at a time (kStep elements), in LDS twice over so that the
+// next step's loads run under this step's products.
+//
+// An operand whose reduction runs along its rows in memory ("along") is kept
+// as [tile row][128 bytes]; one whose reduction runs across them ("across":
+// w in dx, both operands in dw) as [kStep][tile row], and is transposed on
+// the way to the registers.  In both, 16-byte pieces of a row are permuted by
+// an exclusive or with row bits, so that the lanes that a read serves
+// together hit different banks.
+template <int BR_, int BC_, int WR_, int WC_> struct Tile {
+    static constexpr int BR = BR_, BC = BC_, WR = WR_, WC = WC_;
+    static constexpr int kThreads = 64 * WR_ * WC_;
+    static constexpr int TR = BR_ / WR_ / 16, TC = BC_ / WC_ / 16;   // 16 x 16 outputs per wave
+};
+
+__device__ u32x4 g_zeros;    // what a piece outside an operand is loaded from
+
+// A 16-byte piece from global memory straight into LDS: lane l of the wave
+// writes lds + 16 l.
+__device__ __forceinline__ void load_piece(const char* src, char* lds) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                     (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+// `left` elements of a piece at any alignment of the element, zeros beyond.
+template <int ES> __device__ __forceinline__ u32x4 held_piece(const char* src, int64_t left) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (left >= 16 / ES) {
+        __builtin_memcpy(&v, __builtin_assume_aligned(src, ES), 16);
+    } else if (ES == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < left) v[j] = ((const uint32_t*)src)[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < left) v[j >> 1] |= (uint32_t)((const uint16_t*)src)[j] << (16 * (j & 1));
+    }
+    return v;
 }
 
-// Any widths, strides and types: 64 x 64 tiles of the output, operands
-// widened to fp32 in LDS element by element, 16x16x4 fp32 matrix
-// instructions.  out[r][c] = sum over e of A(r, e) B(c, e).
-constexpr int kT = 64, kE = 32;
+template <int ES> __device__ __forceinline__ int swap_along(int r) { return (r >> 1) & 7; }
+// Rows of at least 16 pieces.  bf16: 32 lanes read 32 bytes of rows 0..3 and
+// 8..11 (and the next 32 of rows 16 on); fp32: 64 lanes read 64 bytes of each
+// of four rows 4 apart.
+template <int ES> __device__ __forceinline__ int swap_across(int e) {
+    return ES == 4 ? ((e >> 2) & 3) << 2 : ((e & 3) | ((e >> 3) & 1) << 2) << 1;
+}
 
-template <int T, int MODE>
-__global__ __launch_bounds__(256) void k_product_any(ProdArgs p) {
-    __shared__ float sa[kT][kE + 1], sb[kT][kE + 1];
-    __shared__ int32_t s_row[kT];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+// One operand's share of a step, kN pieces per thread.
+template <int ES, int B, int NT, bool ASYNC> struct Along {
+    static constexpr int kN = B * 8 / NT, VE = 16 / ES;
+    static_assert(kN * NT == B * 8, "whole passes");
+    const char* src[kN];
+    int slot;
+    u32x4 held[ASYNC ? 1 : kN];
+    template <class F> __device__ __forceinline__ void begin(F row_start) {
+        slot = (threadIdx.x & 7) ^ swap_along<ES>(threadIdx.x >> 3);   // passes are 16 rows or more apart
+#pragma unroll
+        for (int i = 0; i < kN; ++i) src[i] = row_start((int)(i * (NT / 8) + (threadIdx.x >> 3))) + slot * 16;
+    }
+    __device__ __forceinline__ void load(char* lds, int64_t e0, int64_t len) {
+        const int64_t left = len - e0 - slot * VE;
+        char* at = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const char* s = src[i] + e0 * ES;
+            if (ASYNC) load_piece(left > 0 ? s : (const char*)&g_zeros, at + i * NT * 16);
+            else held[i] = held_piece<ES>(s, left);
+        }
+    }
+    __device__ __forceinline__ void store(char* lds) {
+        if (ASYNC) return;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) *(u32x4*)(lds + (i * NT + threadIdx.x) * 16) = held[i];
+    }
+};
+
+// ROWS: reduction element e is a row of the matrix at e rows from `base`
+// (w), else the row of position e of the chunk, through order.
+template <int ES, int B, int NT, bool ASYNC, bool GATHER> struct Across {
+    static constexpr int kN = B * 8 / NT, VE = 16 / ES, S = B * ES / 16, kRows = NT / S;
+    static_assert(kN * NT == B * 8 && S >= 16, "whole passes");
+    const char* base;
+    int64_t ld;              // bytes
+    int cols;                // elements of a row from this tile's first on
+    const int32_t* order;
+    int64_t pos, m;
+    int32_t row[GATHER ? kN : 1];
+    u32x4 held[ASYNC ? 1 : kN];
+    __device__ __forceinline__ int first() const { return threadIdx.x / S; }
+    __device__ __forceinline__ void begin(const char* p, int64_t ld_bytes, int cols_left, const int32_t* ord,
+                                          int64_t beg, int64_t rows, int64_t len) {
+        base = p;
+        ld = ld_bytes;
+        cols = cols_left;
+        order = ord;
+        pos = beg;
+        m = rows;
+        next_rows(0, len);
+    }
+    __device__ __forceinline__ void next_rows(int64_t e0, int64_t len) {
+        if (!GATHER) return;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int64_t e = e0 + first() + i * kRows;
+            row[i] = e < len ? (order ? order[pos + e] : (int32_t)(pos + e)) : -1;
+        }
+    }
+    __device__ __forceinline__ void load(char* lds, int64_t e0, int64_t len) {
+        char* at = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int e = first() + i * kRows, col = ((int)(threadIdx.x % S) ^ swap_across<ES>(e)) * VE;
+            const int64_t r = GATHER ? (int64_t)row[i] : e0 + e;
+            const int64_t left = (GATHER ? r >= 0 && r < m : r < len) ? cols - col : 0;
+            const char* s = base + r * ld + col * ES;
+            if (ASYNC) load_piece(left > 0 ? s : (const char*)&g_zeros, at + i * NT * 16);
+            else held[i] = held_piece<ES>(s, left);
+        }
+        next_rows(e0 + 128 / ES, len);
+    }
+    __device__ __forceinline__ void store(char* lds) {
+        if (ASYNC) return;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) *(u32x4*)(lds + (i * NT + threadIdx.x) * 16) = held[i];
+    }
+};
+
+template <int T> struct Frag;
+template <> struct Frag<kSrcBf16> { bf16x8 v; };
+template <> struct Frag<kSrcF32> { f32x4 v; };
+
+// What a lane gives a matrix instruction of 16 tile rows from r0 on: row
+// r0 + l % 16, elements (l / 16) * 8 .. + 8 of the half step's 32 in bf16,
+// (l / 16) * 4 .. + 4 of 16 in fp32.
+template <int T> __device__ __forceinline__ void frag_along(const char* lds, int r0, int half, Frag<T>& f) {
+    const int lane = __lane_id(), r = r0 + (lane & 15);
+    f.v = *(const decltype(f.v)*)(lds + r * 128 + ((half * 4 + (lane >> 4)) ^ swap_along<1>(lane & 15)) * 16);
+}
+template <int B> __device__ __forceinline__ void frag_across(const char* lds, int r0, int half, Frag<kSrcBf16>& f) {
+    // 16 lanes read four rows of 16 elements and each gets one column
+    const int lane = __lane_id(), q = lane >> 4, e = q * 8 + ((lane & 15) >> 2);
+    const char* at = lds + (half * 32 + e) * (B * 2) + (((r0 >> 3) + ((lane & 3) >> 1)) ^ swap_across<2>(e)) * 16 + (lane & 1) * 8;
+    typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+    union { i16x4 h[2]; bf16x8 v; } u;
+    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)at);
+    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(at + 4 * B * 2));
+    f.v = u.v;
+}
+template <int B> __device__ __forceinline__ void frag_across(const char* lds, int r0, int half, Frag<kSrcF32>& f) {
+    const int lane = __lane_id(), q = lane >> 4;
+    const char* at = lds + (half * 16 + q * 4) * (B * 4) + (((r0 >> 2) + ((lane & 15) >> 2)) ^ swap_across<4>(q * 4)) * 16 +
+                     (lane & 3) * 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f.v[j] = *(const float*)(at + j * B * 4);
+}
+
+__device__ __forceinline__ void multiply(const Frag<kSrcBf16>& c, const Frag<kSrcBf16>& r, f32x4& acc) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c.v, r.v, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void multiply(const Frag<kSrcF32>& c, const Frag<kSrcF32>& r, f32x4& acc) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(c.v[j], r.v[j], acc, 0, 0, 0);
+}
+
+// The tile that workgroup number b of the launch takes: consecutive tiles go
+// to one XCD (workgroups go round the eight of them), so that its L2 serves
+// what neighbours share.  Tiles run group by group, within a group over blocks
+// of kBlock chunks, in a block column by column: what is at work at one time
+// shares a few chunks' rows and a few columns of the group's matrix.
+struct TileAt {
+    int g;
+    int64_t beg, end;       // positions
+    int64_t chunk;          // among all groups' chunks
+    int count;              // chunks of the group
+    int col;                // which of the `cols` tiles beside each other
+};
+constexpr int kBlock = 8, kXcds = 8;
+// 1: found; 0: nothing at this b; -1: nothing at this or any later b.
+__device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, int64_t m, uint32_t R, int min_chunks,
+                                         int64_t cols, int64_t b, TileAt& t) {
+    const int lane = __lane_id();
+    auto chunks_at = [&](int g, int64_t& beg, int64_t& end) {
+        beg = end = 0;
+        int cnt = 0;
+        if (g < n_groups || (g == n_groups && offsets)) {
+            group_range(offsets, n_groups, m, g, beg, end);
+            cnt = (int)(((uint32_t)(end - beg) + R - 1u) / R);
+            if (g < n_groups && cnt < min_chunks) cnt = min_chunks;
+            if (g == n_groups && min_chunks) cnt = 0;        // sums leave out the rows of no group
+        }
+        return cnt;
+    };
+    int64_t total = 0, beg, end;
+    for (int g0 = 0; g0 <= n_groups; g0 += 64) {
+        int s = chunks_at(g0 + lane, beg, end);
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) s += __shfl_xor(s, off);
+        total += s;
+    }
+    total *= cols;
+    const int64_t each = total / kXcds, extra = total % kXcds, x = b % kXcds, i = b / kXcds;
+    if (i >= each + (x < extra)) return i > each ? -1 : 0;
+    const int64_t item = x * each + (x < extra ? x : extra) + i;
+    int64_t run = 0;
+    for (int g0 = 0; g0 <= n_groups; g0 += 64) {
+        const int cnt = chunks_at(g0 + lane, beg, end);
+        int incl = cnt;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int y = __shfl_up(incl, off);
+            if (lane >= off) incl += y;
+        }
+        const uint64_t past = __ballot((run + incl) * cols > item);
+        if (past) {
+            const int l = __ffsll((unsigned long long)past) - 1;
+            t.g = __builtin_amdgcn_readfirstlane(g0 + l);
+            t.count = __builtin_amdgcn_readfirstlane(__shfl(cnt, l));
+            const int64_t before = run + __shfl(incl, l) - t.count;
+            const int64_t local = item - before * cols;
+            const int64_t block = local / (cols * kBlock), in = local - block * cols * kBlock;
+            const int64_t left = t.count - block * kBlock, width = left < kBlock ? left : kBlock;
+            t.col = (int)(in / width);
+            const int64_t index = block * kBlock + (in - t.col * width);
+            t.chunk = before + index;
+            const int64_t gb = (int64_t)__shfl((int)beg, l), ge = (int64_t)__shfl((int)end, l);
+            t.beg = gb + index * R;
+            t.end = t.beg + R < ge ? t.beg + R : ge;
+            return 1;
+        }
+        run += __shfl(incl, 63);
+    }
+    return -1;
+}
+
+template <int T, int MODE, class C, bool ASYNC>
+__global__ __launch_bounds__(C::kThreads) void k_product(ProdArgs p) {
+    constexpr int ES = T == kSrcF32 ? 4 : 2, NT = C::kThreads, kStep = 128 / ES;
+    __shared__ __attribute__((aligned(128))) char lds0[(C::BR + C::BC) * 128];
+    __shared__ __attribute__((aligned(128))) char lds1[(C::BR + C::BC) * 128];
+    __shared__ int32_t s_row[MODE == kDw ? 1 : C::BR];
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wr = wv / C::WC * (C::TR * 16), wc = wv % C::WC * (C::TC * 16);
     const int cols = MODE == kFwd ? p.n : p.k;
-    const int col_tiles = (cols + kT - 1) / kT;
-    const int64_t tiles = MODE == kDw ? (int64_t)col_tiles * ((p.n + kT - 1) / kT) : col_tiles;
-    for (int64_t item = blockIdx.x; item < p.chunks * tiles; item += gridDim.x) {
-        const int64_t chunk = item / tiles;
-        const int tile = (int)(item - chunk * tiles);
-        Chunk c;
-        if (!find_chunk(p.offsets, p.n_groups, p.m, p.rows, MODE == kDw ? 1 : 0, chunk, c))
-            return;
-        const bool grouped = c.g < p.n_groups;
-        const int r0 = MODE == kDw ? tile / col_tiles * kT : 0;
-        const int c0 = tile % col_tiles * kT;
-        __syncthreads();                     // the tile before is written
-        if (MODE == kDw) {
-            if (!grouped) return;
-        } else {
-            if (threadIdx.x < kT) {
-                const int64_t pos = c.beg + threadIdx.x;
-                const int32_t row = pos < c.end ? (p.order ? p.order[pos] : (int32_t)pos) : -1;
-                s_row[threadIdx.x] = row >= 0 && row < p.m ? row : -1;
+    const int col_tiles = (cols + C::BC - 1) / C::BC;
+    const int row_tiles = MODE == kDw ? (p.n + C::BR - 1) / C::BR : 1;
+    for (int64_t b = blockIdx.x;; b += gridDim.x) {
+        TileAt t;
+        const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, MODE == kDw ? 1 : 0,
+                                    (int64_t)col_tiles * row_tiles, b, t);
+        if (found < 0) return;
+        if (!found) continue;
+        if (MODE == kDw && t.chunk >= p.limit) continue;     // offsets that overlap
+        const bool grouped = t.g < p.n_groups;
+        const int r0 = MODE == kDw ? t.col % row_tiles * C::BR : 0;
+        const int c0 = (MODE == kDw ? t.col / row_tiles : t.col) * C::BC;
+        __syncthreads();                     // the tile before is read and stored
+        if (MODE != kDw) {
+            for (int i = threadIdx.x; i < C::BR; i += NT) {
+                const int64_t pos = t.beg + i;
+                const int32_t row = pos < t.end ? (p.order ? p.order[pos] : (int32_t)pos) : -1;
+                s_row[i] = row >= 0 && row < p.m ? row : -1;
+            }
+            __syncthreads();
+        }
+        f32x4 acc[C::TC][C::TR];
+#pragma unroll
+        for (int i = 0; i < C::TC; ++i)
+#pragma unroll
+            for (int j = 0; j < C::TR; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const int64_t len = !grouped ? 0 : (MODE == kFwd ? p.k : (MODE == kDx ? p.n : t.end - t.beg));
+        const int64_t wg = grouped ? (int64_t)t.g * p.n * p.k : 0;
+        // rows of this wave that exist
+        const bool busy = (MODE == kDw ? r0 + wr < p.n : t.beg + wr < t.end) && c0 + wc < cols;
+        if (len > 0) {
+            auto row_operand = [&]() {
+                if constexpr (MODE == kDw) {
+                    Across<ES, C::BR, NT, ASYNC, true> o;
+                    o.begin((const char*)p.a + (int64_t)r0 * ES, p.lda * ES, p.n - r0, p.order, t.beg, p.m, len);
+                    return o;
+                } else {
+                    Along<ES, C::BR, NT, ASYNC> o;
+                    // a row that is not there is read as the first that may be: its products are not stored
+                    o.begin([&](int r) {
+                        const int64_t row = s_row[r] < 0 ? 0 : s_row[r];
+                        return (const char*)p.a + row * p.lda * ES;
+                    });
+                    return o;
+                }
+            };
+            auto col_operand = [&]() {
+                if constexpr (MODE == kFwd) {
+                    Along<ES, C::BC, NT, ASYNC> o;
+                    o.begin([&](int c) {
+                        const int n = c0 + c < p.n ? c0 + c : p.n - 1;
+                        return (const char*)p.b + (wg + (int64_t)n * p.k) * ES;
+                    });
+                    return o;
+                } else {
+                    Across<ES, C::BC, NT, ASYNC, MODE == kDw> o;
+                    if (MODE == kDx) o.begin((const char*)p.b + (wg + c0) * ES, (int64_t)p.k * ES, p.k - c0, nullptr, 0, 0, len);
+                    else o.begin((const char*)p.b + (int64_t)c0 * ES, p.ldb * ES, p.k - c0, p.order, t.beg, p.m, len);
+                    return o;
+                }
+            };
+            auto ro = row_operand();
+            auto co = col_operand();
+            // the products of the step in `cur`, while the next one's operands come into `nxt`
+            auto step = [&](const char* __restrict cur, char* __restrict nxt, int64_t e0) __attribute__((always_inline)) {
+                const bool more = e0 < len;
+                if (more) {
+                    ro.load(nxt, e0, len);
+                    co.load(nxt + C::BR * 128, e0, len);
+                }
+                if (busy && e0 > 0) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        Frag<T> fc[C::TC], fr[C::TR];
+#pragma unroll
+                        for (int i = 0; i < C::TC; ++i) {
+                            if constexpr (MODE == kFwd) frag_along<T>(cur + C::BR * 128, wc + i * 16, half, fc[i]);
+                            else frag_across<C::BC>(cur + C::BR * 128, wc + i * 16, half, fc[i]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < C::TR; ++j) {
+                            if constexpr (MODE == kDw) frag_across<C::BR>(cur, wr + j * 16, half, fr[j]);
+                            else frag_along<T>(cur, wr + j * 16, half, fr[j]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < C::TR; ++j)
+#pragma unroll
+                            for (int i = 0; i < C::TC; ++i) multiply(fc[i], fr[j], acc[i][j]);
+                    }
+                }
+                if (more) {
+                    ro.store(nxt);
+                    co.store(nxt + C::BR * 128);
+                }
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                __syncthreads();
+            };
+            int64_t e0 = 0;
+            for (;; e0 += 2 * kStep) {
+                step(lds1, lds0, e0);
+                if (e0 >= len) break;
+                step(lds0, lds1, e0 + kStep);
+                if (e0 + kStep >= len) break;
             }
         }
-        const int64_t len = MODE == kFwd ? p.k : (MODE == kDx ? p.n : c.end - c.beg);
-        f32x4 acc[4];
-    #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = {0.0f, 0.0f, 0.0f, 0.0f};
-        const int64_t wg = grouped ? (int64_t)c.g * p.n * p.k : 0;
-        for (int64_t e0 = 0; grouped && e0 < len; e0 += kE) {
-            __syncthreads();
+        if (!busy) continue;
+        // lane: output row l % 16, four columns from (l / 16) * 4 on, of each 16 x 16
+        const int ld = MODE == kDw ? p.k : cols;
+#pragma unroll
+        for (int j = 0; j < C::TR; ++j) {
+            const int r = wr + j * 16 + (lane & 15);
+            char* dst;
             if (MODE == kDw) {
-                for (int i = threadIdx.x; i < kT * kE; i += 256) {
-                    const int e = i / kT, q = i % kT;
-                    const int64_t pos = c.beg + e0 + e;
-                    const int64_t row = pos < c.end ? (p.order ? p.order[pos] : pos) : -1;
-                    const bool in = row >= 0 && row < p.m;
-                    sa[q][e] = in && r0 + q < p.n ? elem_at<T>(p.a, row * p.lda + r0 + q) : 0.0f;
-                    sb[q][e] = in && c0 + q < p.k ? elem_at<T>(p.b, row * p.ldb + c0 + q) : 0.0f;
-                }
+                if (r0 + r >= p.n) continue;
+                float* to = t.count == 1 ? (float*)p.out + wg : p.partial + t.chunk * p.n * p.k;
+                dst = (char*)(to + (int64_t)(r0 + r) * ld);
             } else {
-                for (int i = threadIdx.x; i < kT * kE; i += 256) {
-                    const int q = i / kE, e = i % kE;
-                    const int32_t row = s_row[q];
-                    sa[q][e] = row >= 0 && e0 + e < len ? elem_at<T>(p.a, row * p.lda + e0 + e) : 0.0f;
-                }
-                for (int i = threadIdx.x; i < kT * kE; i += 256) {
-                    // along the weight's rows in both cases
-                    const int q = MODE == kFwd ? i / kE : i % kT, e = MODE == kFwd ? i % kE : i / kT;
-                    const bool in = c0 + q < cols && e0 + e < len;
-                    const int64_t at = MODE == kFwd ? wg + (int64_t)(c0 + q) * p.k + e0 + e
-                                                    : wg + (e0 + e) * p.k + c0 + q;
-                    sb[q][e] = in ? elem_at<T>(p.b, at) : 0.0f;
-                }
+                const int row = s_row[r];
+                if (row < 0) continue;
+                dst = (char*)p.out + (int64_t)row * ld * (p.out_f32 ? 4 : 2);
             }
-            __syncthreads();
-            // wave wv: rows 16 wv .. + 16; lane l: element l / 16 of four
-    #pragma unroll
-            for (int e = 0; e < kE; e += 4) {
-                const float va = sa[wv * 16 + (lane & 15)][e + (lane >> 4)];
-    #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(va, sb[t * 16 + (lane & 15)][e + (lane >> 4)], acc[t], 0,
-                                                                  0, 0);
+#pragma unroll
+            for (int i = 0; i < C::TC; ++i) {
+                const int col = c0 + wc + i * 16 + (lane >> 4) * 4;
+                const f32x4 v = acc[i][j];
+                if (MODE == kDw || p.out_f32) {
+                    float* o = (float*)dst + col;
+                    if (p.out_vec) {
+                        if (col < cols) *(f32x4*)o = v;
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (col + q < cols) o[q] = v[q];
+                    }
+                } else {
+                    uint16_t* o = (uint16_t*)dst + col;
+                    if (p.out_vec) {
+                        if (col < cols) *(u32x2*)o = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (col + q < cols) o[q] = (uint16_t)f32_to_bf16_bits(v[q]);
+                    }
+                }
             }
         }
-        __syncthreads();
-    #pragma unroll
-        for (int t = 0; t < 4; ++t)
-    #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int q = wv * 16 + (lane >> 4) * 4 + j, col = c0 + t * 16 + (lane & 15);
-                if (col >= cols) continue;
-                if (MODE == kDw) {
-                    if (r0 + q >= p.n) continue;
-                    float* dst = c.count == 1 ? (float*)p.out + wg : p.partial + chunk * p.n * p.k;
-                    dst[(int64_t)(r0 + q) * p.k + col] = acc[t][j];
-                } else if (s_row[q] >= 0) {
-                    const int64_t at = (int64_t)s_row[q] * cols + col;
-                    if (p.out_f32) ((float*)p.out)[at] = acc[t][j];
-                    else ((uint16_t*)p.out)[at] = (uint16_t)f32_to_bf16_bits(acc[t][j]);
-                }
-            }
     }
 }
+
+typedef Tile<256, 256, 2, 4> Big;
+typedef Tile<128, 128, 2, 2> Mid;
+typedef Tile<32, 128, 1, 4> Small;
+
+int elem(htl_dtype t) { return t == HTL_F32 ? 4 : 2; }
+bool known(htl_dtype t) { return t == HTL_F32 || t == HTL_BF16; }
+
+// chunks: at most this many in all
+template <int T, int MODE, class C, bool ASYNC>
+void launch(const ProdArgs& p, int64_t chunks, hipStream_t s) {
+    const int64_t cols = ceil_div(MODE == kFwd ? p.n : p.k, C::BC) * (MODE == kDw ? ceil_div(p.n, C::BR) : 1);
+    const dim3 grid(grid_for(align_up((size_t)(chunks * cols), kXcds), 1));
+    hipLaunchKernelGGL((k_product<T, MODE, C, ASYNC>), grid, dim3(C::kThreads), 0, s, p);
+}
+
+// Forward product or dx: `cols` outputs a row, reduced over `len`.
+template <int MODE> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s) {
+    const int cols = MODE == kFwd ? p.n : p.k, es = elem(dtype);
+    const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && (int64_t)p.k * es % 16 == 0 &&
+                      (MODE == kFwd || (int64_t)p.n * es % 16 == 0) && aligned(p.b, 16);
+    p.out_vec = cols % 4 == 0 && aligned(p.out, p.out_f32 ? 16 : 8);
+    const int64_t each = p.m / p.n_groups;
+    int tile = each <= 48 ? 32 : 128;
+    if (tile == 128 && dtype == HTL_BF16 && fast && ceil_div(p.m, 256) * ceil_div(cols, 256) >= 512 && each >= 256) tile = 256;
+    p.rows = (uint32_t)tile;
+    const int64_t chunks = p.m / tile + p.n_groups + 1;
+    if (dtype == HTL_BF16) {
+        if (tile == 256) launch<kSrcBf16, MODE, Big, true>(p, chunks, s);
+        else if (tile == 128 && fast) launch<kSrcBf16, MODE, Mid, true>(p, chunks, s);
+        else if (tile == 128) launch<kSrcBf16, MODE, Mid, false>(p, chunks, s);
+        else if (fast) launch<kSrcBf16, MODE, Small, true>(p, chunks, s);
+        else launch<kSrcBf16, MODE, Small, false>(p, chunks, s);
+    } else {
+        if (tile == 128 && fast) launch<kSrcF32, MODE, Mid, true>(p, chunks, s);
+        else if (tile == 128) launch<kSrcF32, MODE, Mid, false>(p, chunks, s);
+        else if (fast) launch<kSrcF32, MODE, Small, true>(p, chunks, s);
+        else launch<kSrcF32, MODE, Small, false>(p, chunks, s);
+    }
+}
+
+constexpr int kT = 128;
 
 // Rows per chunk of dw's sums: chunks times tiles fill the device a few
 // times over, and a chunk is long against the partial sums it leaves.
@@ -137,9 +479,6 @@ uint32_t dw_chunk_rows(int64_t m, int n_groups, int n, int k) {
     return (uint32_t)r;
 }
 int64_t dw_chunks(int64_t m, int n_groups, int n, int k) { return m / dw_chunk_rows(m, n_groups, n, k) + n_groups + 1; }
-
-int elem(htl_dtype t) { return t == HTL_F32 ? 4 : 2; }
-bool known(htl_dtype t) { return t == HTL_F32 || t == HTL_BF16; }
 
 }  // namespace
 }  // namespace htl
@@ -165,11 +504,8 @@ extern "C" htl_status grouped_mm(const void* x, int64_t ldx, const void* w, htl_
     const int es = elem(dtype);
     HTL_REQUIRE(x && w && y, "grouped_mm: null pointer");
     HTL_REQUIRE(aligned(x, es) && aligned(w, es) && aligned(y, elem(y_dtype)), "grouped_mm: misaligned pointer");
-    ProdArgs p = {x, w, y, order, offsets, m, ldx, k, n, k, n_groups, (uint32_t)kT,
-                  m / kT + n_groups + 1, nullptr, y_dtype == HTL_F32};
-    const dim3 grid(grid_for(p.chunks * ceil_div(n, kT), 1));
-    if (dtype == HTL_F32) hipLaunchKernelGGL((k_product_any<kSrcF32, kFwd>), grid, dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL((k_product_any<kSrcBf16, kFwd>), grid, dim3(256), 0, stream, p);
+    ProdArgs p = {x, w, y, order, offsets, m, ldx, k, n, k, n_groups, 0, nullptr, y_dtype == HTL_F32, 0, 0};
+    launch_rows<kFwd>(p, dtype, stream);
     return check_launch("grouped_mm");
 }
 
@@ -196,21 +532,24 @@ extern "C" htl_status grouped_mm_backward(const void* dy, int64_t ld_dy, const v
     HTL_REQUIRE(!dw || (ws && aligned(ws, 256) && ws_bytes >= grouped_mm_backward_workspace_bytes(m, n_groups, n, k)),
                 "grouped_mm_backward: workspace too small or misaligned");
     if (dx && m > 0) {
-        ProdArgs p = {dy, w, dx, order, offsets, m, ld_dy, k, n, k, n_groups, (uint32_t)kT,
-                      m / kT + n_groups + 1, nullptr, dx_dtype == HTL_F32};
-        const dim3 grid(grid_for(p.chunks * ceil_div(k, kT), 1));
-        if (dtype == HTL_F32) hipLaunchKernelGGL((k_product_any<kSrcF32, kDx>), grid, dim3(256), 0, stream, p);
-        else hipLaunchKernelGGL((k_product_any<kSrcBf16, kDx>), grid, dim3(256), 0, stream, p);
+        const ProdArgs p = {dy, w, dx, order, offsets, m, ld_dy, k, n, k, n_groups, 0, nullptr, dx_dtype == HTL_F32, 0, 0};
+        launch_rows<kDx>(p, dtype, stream);
         const htl_status st = check_launch("grouped_mm_backward");
         if (st != HTL_OK) return st;
     }
     if (!dw) return HTL_OK;
-    ProdArgs p = {dy, x, dw, order, offsets, m, ld_dy, ldx, n, k, n_groups, dw_chunk_rows(m, n_groups, n, k),
-                  dw_chunks(m, n_groups, n, k), (float*)ws, 1};
-    const dim3 grid(grid_for(p.chunks * ceil_div(n, kT) * ceil_div(k, kT), 1));
-    if (dtype == HTL_F32) hipLaunchKernelGGL((k_product_any<kSrcF32, kDw>), grid, dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL((k_product_any<kSrcBf16, kDw>), grid, dim3(256), 0, stream, p);
+    const ProdArgs p = {dy, x, dw, order, offsets, m, ld_dy, ldx, n, k, n_groups, dw_chunk_rows(m, n_groups, n, k),
+                        (float*)ws, 1, k % 4 == 0 && aligned(dw, 16), dw_chunks(m, n_groups, n, k)};
+    const bool fast = ld_dy * es % 16 == 0 && ldx * es % 16 == 0 && aligned(dy, 16) && aligned(x, 16) &&
+                      (int64_t)n * es % 16 == 0 && (int64_t)k * es % 16 == 0;
+    if (dtype == HTL_BF16) {
+        if (fast) launch<kSrcBf16, kDw, Mid, true>(p, p.limit, stream);
+        else launch<kSrcBf16, kDw, Mid, false>(p, p.limit, stream);
+    } else {
+        if (fast) launch<kSrcF32, kDw, Mid, true>(p, p.limit, stream);
+        else launch<kSrcF32, kDw, Mid, false>(p, p.limit, stream);
+    }
     const htl_status st = check_launch("grouped_mm_backward");
     if (st != HTL_OK) return st;
-    return sum_chunks(p.partial, dw, offsets, n_groups, m, p.rows, (int64_t)n * k, stream);
+    return sum_chunks(p.partial, p.limit, dw, offsets, n_groups, m, p.rows, (int64_t)n * k, stream);
 }
