@@ -15,6 +15,7 @@ constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 4096;   // row positions are i
 enum { kSrcF32 = 0, kSrcBf16 = 1, kSrcRows8 = 2 };
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // Rows in device memory.  vec: every row starts 16-byte aligned (8-byte for
 // codes) and holds whole groups of eight elements, so a lane moves its eight

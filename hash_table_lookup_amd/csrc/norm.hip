@@ -187,6 +187,35 @@ __global__ __launch_bounds__(1024) void k_sum_chunks(const float* __restrict__ p
     }
 }
 
+// Wide rows (a matrix each): four columns per thread.
+__global__ __launch_bounds__(256) void k_sum_wide(const float* __restrict__ partial, int64_t limit,
+                                                  float* __restrict__ out, const int32_t* __restrict__ offsets,
+                                                  int n_groups, int64_t m, uint32_t R, int64_t width) {
+    const int g = blockIdx.y;
+    int64_t first;
+    int count;
+    chunks_of_group(offsets, n_groups, m, R, 1, g, first, count);
+    if (count == 1) return;
+    if (first + count > limit) count = first < limit ? (int)(limit - first) : 0;   // offsets that overlap
+    for (int64_t d = (blockIdx.x * 256ll + threadIdx.x) * 4; d < width; d += gridDim.x * 1024ll) {
+        const float* p = partial + first * width + d;
+        float* o = out + g * width + d;
+        if (width % 4 == 0) {
+            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+            for (int c = 0; c < count; ++c) v += *(const f32x4*)(p + c * width);
+            __builtin_memcpy(__builtin_assume_aligned(o, 4), &v, 16);
+        } else {
+            for (int j = 0; j < 4 && d + j < width; ++j) {
+                float v = 0.0f;
+#pragma unroll 8
+                for (int c = 0; c < count; ++c) v += p[c * width + j];
+                o[j] = v;
+            }
+        }
+    }
+}
+
 // Positions per chunk: about kChunks chunks in all, at least four rows for
 // each team.
 constexpr int64_t kChunks = 2048;
@@ -205,6 +234,12 @@ uint32_t norm_rows_per_chunk(int64_t m, int dim) { return norm_chunk_rows(m, dim
 htl_status sum_chunks(const float* partial, int64_t limit, float* out, const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
                       int64_t width, hipStream_t stream) {
     if (m <= (int64_t)R) return HTL_OK;      // every group is one chunk
+    if (width >= 4096) {
+        const int64_t blocks = ceil_div(width, 1024), most = ceil_div(4096, n_groups);
+        hipLaunchKernelGGL(k_sum_wide, dim3((unsigned)(blocks < most ? blocks : most), (unsigned)n_groups), dim3(256), 0,
+                           stream, partial, limit, out, offsets, n_groups, m, R, width);
+        return check_launch("partial sums");
+    }
     const int64_t cols = ceil_div(width, 64);
     hipLaunchKernelGGL(k_sum_chunks, dim3((unsigned)(cols < 4096 ? cols : 4096), (unsigned)n_groups), dim3(1024), 0,
                        stream, partial, limit, out, offsets, n_groups, m, R, width);

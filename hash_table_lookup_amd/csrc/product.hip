@@ -8,10 +8,11 @@
 // through the plan's order, so nothing is sorted or copied around the product.
 #include "dense.h"
 
+#include <type_traits>
+
 namespace htl {
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -74,7 +75,13 @@ template <int ES> __device__ __forceinline__ u32x4 held_piece(const char* src, i
     return v;
 }
 
-template <int ES> __device__ __forceinline__ int swap_along(int r) { return (r >> 1) & 7; }
+template <int NT, bool ASYNC, int N> __device__ __forceinline__ void store_pieces(const u32x4* held, char* lds) {
+    if (ASYNC) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) *(u32x4*)(lds + (i * NT + threadIdx.x) * 16) = held[i];
+}
+
+__device__ __forceinline__ int swap_along(int r) { return (r >> 1) & 7; }
 // Rows of at least 16 pieces.  bf16: 32 lanes read 32 bytes of rows 0..3 and
 // 8..11 (and the next 32 of rows 16 on); fp32: 64 lanes read 64 bytes of each
 // of four rows 4 apart.
@@ -82,7 +89,15 @@ template <int ES> __device__ __forceinline__ int swap_across(int e) {
     return ES == 4 ? ((e >> 2) & 3) << 2 : ((e & 3) | ((e >> 3) & 1) << 2) << 1;
 }
 
-// One operand's share of a step, kN pieces per thread.
+// Keeps the compiler from holding every address that follows from v in a
+// register of its own across the loop.
+template <class V> __device__ __forceinline__ V recompute(V v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// One operand's share of a step, kN pieces per thread, from rows that
+// `row_start` names (rows of x or dy).
 template <int ES, int B, int NT, bool ASYNC> struct Along {
     static constexpr int kN = B * 8 / NT, VE = 16 / ES;
     static_assert(kN * NT == B * 8, "whole passes");
@@ -90,7 +105,7 @@ template <int ES, int B, int NT, bool ASYNC> struct Along {
     int slot;
     u32x4 held[ASYNC ? 1 : kN];
     template <class F> __device__ __forceinline__ void begin(F row_start) {
-        slot = (threadIdx.x & 7) ^ swap_along<ES>(threadIdx.x >> 3);   // passes are 16 rows or more apart
+        slot = (threadIdx.x & 7) ^ swap_along(threadIdx.x >> 3);   // passes are 16 rows or more apart
 #pragma unroll
         for (int i = 0; i < kN; ++i) src[i] = row_start((int)(i * (NT / 8) + (threadIdx.x >> 3))) + slot * 16;
     }
@@ -104,62 +119,82 @@ template <int ES, int B, int NT, bool ASYNC> struct Along {
             else held[i] = held_piece<ES>(s, left);
         }
     }
-    __device__ __forceinline__ void store(char* lds) {
-        if (ASYNC) return;
+    __device__ __forceinline__ void store(char* lds) { store_pieces<NT, ASYNC, kN>(held, lds); }
+};
+
+// The same from consecutive rows (of w), zeros from row `rows` on.
+template <int ES, int B, int NT, bool ASYNC> struct AlongRows {
+    static constexpr int kN = B * 8 / NT, VE = 16 / ES;
+    const char* src;
+    int64_t ld;              // bytes
+    int slot, rows;
+    u32x4 held[ASYNC ? 1 : kN];
+    __device__ __forceinline__ void begin(const char* p, int64_t ld_bytes, int rows_left) {
+        slot = (threadIdx.x & 7) ^ swap_along(threadIdx.x >> 3);
+        ld = ld_bytes;
+        rows = rows_left - (int)(threadIdx.x >> 3);
+        src = p + (threadIdx.x >> 3) * ld + slot * 16;
+    }
+    __device__ __forceinline__ void load(char* lds, int64_t e0, int64_t len) {
+        const int64_t left = len - e0 - slot * VE;
+        char* at = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+        const char* s0 = recompute(src) + e0 * ES;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) *(u32x4*)(lds + (i * NT + threadIdx.x) * 16) = held[i];
+        for (int i = 0; i < kN; ++i) {
+            const char* s = s0 + i * (NT / 8) * ld;
+            const int64_t have = i * (NT / 8) < rows ? left : 0;
+            if (ASYNC) load_piece(have > 0 ? s : (const char*)&g_zeros, at + i * NT * 16);
+            else held[i] = held_piece<ES>(s, have);
+        }
+    }
+    __device__ __forceinline__ void store(char* lds) { store_pieces<NT, ASYNC, kN>(held, lds); }
+};
+
+// Rows of consecutive positions of a chunk, found through order one step
+// ahead of their use.
+template <int ES, int B, int NT> struct Rows {
+    static constexpr int kN = B * 8 / NT, kRows = NT / (B * ES / 16);
+    const int32_t* order;
+    int64_t pos, m;
+    int32_t row[kN];
+    __device__ __forceinline__ void find(int64_t e0, int64_t len) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int64_t e = e0 + (int)(threadIdx.x / (B * ES / 16)) + i * kRows;
+            const int64_t r = e < len ? (order ? (int64_t)order[pos + e] : pos + e) : -1;
+            row[i] = r < m ? (int32_t)r : -1;
+        }
     }
 };
 
-// ROWS: reduction element e is a row of the matrix at e rows from `base`
-// (w), else the row of position e of the chunk, through order.
+// One operand's share of a step whose reduction runs across the rows of a
+// matrix: those that Rows found (GATHER), or row e0 + e from `base` on.
 template <int ES, int B, int NT, bool ASYNC, bool GATHER> struct Across {
     static constexpr int kN = B * 8 / NT, VE = 16 / ES, S = B * ES / 16, kRows = NT / S;
     static_assert(kN * NT == B * 8 && S >= 16, "whole passes");
     const char* base;
     int64_t ld;              // bytes
     int cols;                // elements of a row from this tile's first on
-    const int32_t* order;
-    int64_t pos, m;
-    int32_t row[GATHER ? kN : 1];
     u32x4 held[ASYNC ? 1 : kN];
-    __device__ __forceinline__ int first() const { return threadIdx.x / S; }
-    __device__ __forceinline__ void begin(const char* p, int64_t ld_bytes, int cols_left, const int32_t* ord,
-                                          int64_t beg, int64_t rows, int64_t len) {
-        base = p;
+    __device__ __forceinline__ void begin(const char* p, int64_t ld_bytes, int cols_left) {
+        base = GATHER ? p : p + (threadIdx.x / S) * ld_bytes;
         ld = ld_bytes;
         cols = cols_left;
-        order = ord;
-        pos = beg;
-        m = rows;
-        next_rows(0, len);
     }
-    __device__ __forceinline__ void next_rows(int64_t e0, int64_t len) {
-        if (!GATHER) return;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int64_t e = e0 + first() + i * kRows;
-            row[i] = e < len ? (order ? order[pos + e] : (int32_t)(pos + e)) : -1;
-        }
-    }
-    __device__ __forceinline__ void load(char* lds, int64_t e0, int64_t len) {
+    __device__ __forceinline__ void load(char* lds, int64_t e0, int64_t len, const int32_t* row) {
         char* at = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+        const int t = recompute((int)threadIdx.x);
+        const char* s0 = GATHER ? base : recompute(base) + e0 * ld;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const int e = first() + i * kRows, col = ((int)(threadIdx.x % S) ^ swap_across<ES>(e)) * VE;
-            const int64_t r = GATHER ? (int64_t)row[i] : e0 + e;
-            const int64_t left = (GATHER ? r >= 0 && r < m : r < len) ? cols - col : 0;
-            const char* s = base + r * ld + col * ES;
+            const int e = t / S + i * kRows, col = ((t % S) ^ swap_across<ES>(e)) * VE;
+            const int64_t left = (GATHER ? row[i] >= 0 : e0 + e < len) ? cols - col : 0;
+            const char* s = s0 + (GATHER ? row[i] * ld : i * kRows * ld) + col * ES;
             if (ASYNC) load_piece(left > 0 ? s : (const char*)&g_zeros, at + i * NT * 16);
             else held[i] = held_piece<ES>(s, left);
         }
-        next_rows(e0 + 128 / ES, len);
     }
-    __device__ __forceinline__ void store(char* lds) {
-        if (ASYNC) return;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) *(u32x4*)(lds + (i * NT + threadIdx.x) * 16) = held[i];
-    }
+    __device__ __forceinline__ void store(char* lds) { store_pieces<NT, ASYNC, kN>(held, lds); }
 };
 
 template <int T> struct Frag;
@@ -169,26 +204,35 @@ template <> struct Frag<kSrcF32> { f32x4 v; };
 // What a lane gives a matrix instruction of 16 tile rows from r0 on: row
 // r0 + l % 16, elements (l / 16) * 8 .. + 8 of the half step's 32 in bf16,
 // (l / 16) * 4 .. + 4 of 16 in fp32.
-template <int T> __device__ __forceinline__ void frag_along(const char* lds, int r0, int half, Frag<T>& f) {
-    const int lane = __lane_id(), r = r0 + (lane & 15);
-    f.v = *(const decltype(f.v)*)(lds + r * 128 + ((half * 4 + (lane >> 4)) ^ swap_along<1>(lane & 15)) * 16);
+// at: lane_along / lane_across of the lane, once for a tile; i: which 16 rows.
+__device__ __forceinline__ int lane_along(int r0) {
+    const int lane = __lane_id();
+    return (r0 + (lane & 15)) * 128 + ((lane >> 4) ^ swap_along(lane & 15)) * 16;
 }
-template <int B> __device__ __forceinline__ void frag_across(const char* lds, int r0, int half, Frag<kSrcBf16>& f) {
-    // 16 lanes read four rows of 16 elements and each gets one column
-    const int lane = __lane_id(), q = lane >> 4, e = q * 8 + ((lane & 15) >> 2);
-    const char* at = lds + (half * 32 + e) * (B * 2) + (((r0 >> 3) + ((lane & 3) >> 1)) ^ swap_across<2>(e)) * 16 + (lane & 1) * 8;
+template <int T> __device__ __forceinline__ void frag_along(const char* lds, int at, int i, int half, Frag<T>& f) {
+    f.v = *(const decltype(f.v)*)(lds + (at ^ half * 64) + i * 2048);
+}
+// bf16: 16 lanes read four rows of 16 elements, and each gets one column.
+template <int T, int B> __device__ __forceinline__ int lane_across(int r0) {
+    const int lane = __lane_id(), q = lane >> 4;
+    if (T == kSrcBf16) {
+        const int e = q * 8 + ((lane & 15) >> 2);
+        return e * B * 2 + (((r0 >> 3) + ((lane & 3) >> 1)) ^ swap_across<2>(e)) * 16 + (lane & 1) * 8;
+    }
+    return q * 4 * B * 4 + (((r0 >> 2) + ((lane & 15) >> 2)) ^ swap_across<4>(q * 4)) * 16 + (lane & 3) * 4;
+}
+template <int B> __device__ __forceinline__ void frag_across(const char* lds, int at, int i, int half, Frag<kSrcBf16>& f) {
+    const char* p = lds + (at ^ i * 32) + half * 32 * B * 2;
     typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
     union { i16x4 h[2]; bf16x8 v; } u;
-    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)at);
-    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(at + 4 * B * 2));
+    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
+    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 4 * B * 2));
     f.v = u.v;
 }
-template <int B> __device__ __forceinline__ void frag_across(const char* lds, int r0, int half, Frag<kSrcF32>& f) {
-    const int lane = __lane_id(), q = lane >> 4;
-    const char* at = lds + (half * 16 + q * 4) * (B * 4) + (((r0 >> 2) + ((lane & 15) >> 2)) ^ swap_across<4>(q * 4)) * 16 +
-                     (lane & 3) * 4;
+template <int B> __device__ __forceinline__ void frag_across(const char* lds, int at, int i, int half, Frag<kSrcF32>& f) {
+    const char* p = lds + (at ^ i * 64) + half * 16 * B * 4;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f.v[j] = *(const float*)(at + j * B * 4);
+    for (int j = 0; j < 4; ++j) f.v[j] = *(const float*)(p + j * B * 4);
 }
 
 __device__ __forceinline__ void multiply(const Frag<kSrcBf16>& c, const Frag<kSrcBf16>& r, f32x4& acc) {
@@ -203,7 +247,9 @@ __device__ __forceinline__ void multiply(const Frag<kSrcF32>& c, const Frag<kSrc
 // to one XCD (workgroups go round the eight of them), so that its L2 serves
 // what neighbours share.  Tiles run group by group, within a group over blocks
 // of kBlock chunks, in a block column by column: what is at work at one time
-// shares a few chunks' rows and a few columns of the group's matrix.
+// shares a few chunks' rows and a few columns of the group's matrix.  Sums
+// over rows (min_chunks 1) take time by their chunk's length, which differs
+// from group to group, so their tiles are dealt out in smaller lots.
 struct TileAt {
     int g;
     int64_t beg, end;       // positions
@@ -235,9 +281,17 @@ __device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, i
         total += s;
     }
     total *= cols;
-    const int64_t each = total / kXcds, extra = total % kXcds, x = b % kXcds, i = b / kXcds;
-    if (i >= each + (x < extra)) return i > each ? -1 : 0;
-    const int64_t item = x * each + (x < extra ? x : extra) + i;
+    const int64_t x = b % kXcds, i = b / kXcds;
+    int64_t item;
+    if (min_chunks) {
+        const int64_t deal = cols < 2 * kXcds ? 1 : (cols < 16 * kXcds ? cols / kXcds : 16);
+        item = (i / deal * kXcds + x) * deal + i % deal;
+        if (item >= total) return i / deal * kXcds * deal >= total ? -1 : 0;
+    } else {
+        const int64_t each = total / kXcds, extra = total % kXcds;
+        if (i >= each + (x < extra)) return i > each ? -1 : 0;
+        item = x * each + (x < extra ? x : extra) + i;
+    }
     int64_t run = 0;
     for (int g0 = 0; g0 <= n_groups; g0 += 64) {
         const int cnt = chunks_at(g0 + lane, beg, end);
@@ -270,7 +324,7 @@ __device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, i
 }
 
 template <int T, int MODE, class C, bool ASYNC>
-__global__ __launch_bounds__(C::kThreads) void k_product(ProdArgs p) {
+__global__ __launch_bounds__(C::kThreads, 2) void k_product(ProdArgs p) {
     constexpr int ES = T == kSrcF32 ? 4 : 2, NT = C::kThreads, kStep = 128 / ES;
     __shared__ __attribute__((aligned(128))) char lds0[(C::BR + C::BC) * 128];
     __shared__ __attribute__((aligned(128))) char lds1[(C::BR + C::BC) * 128];
@@ -309,63 +363,83 @@ __global__ __launch_bounds__(C::kThreads) void k_product(ProdArgs p) {
         // rows of this wave that exist
         const bool busy = (MODE == kDw ? r0 + wr < p.n : t.beg + wr < t.end) && c0 + wc < cols;
         if (len > 0) {
-            auto row_operand = [&]() {
-                if constexpr (MODE == kDw) {
-                    Across<ES, C::BR, NT, ASYNC, true> o;
-                    o.begin((const char*)p.a + (int64_t)r0 * ES, p.lda * ES, p.n - r0, p.order, t.beg, p.m, len);
-                    return o;
-                } else {
-                    Along<ES, C::BR, NT, ASYNC> o;
-                    // a row that is not there is read as the first that may be: its products are not stored
-                    o.begin([&](int r) {
-                        const int64_t row = s_row[r] < 0 ? 0 : s_row[r];
-                        return (const char*)p.a + row * p.lda * ES;
-                    });
-                    return o;
-                }
-            };
-            auto col_operand = [&]() {
-                if constexpr (MODE == kFwd) {
-                    Along<ES, C::BC, NT, ASYNC> o;
-                    o.begin([&](int c) {
-                        const int n = c0 + c < p.n ? c0 + c : p.n - 1;
-                        return (const char*)p.b + (wg + (int64_t)n * p.k) * ES;
-                    });
-                    return o;
-                } else {
-                    Across<ES, C::BC, NT, ASYNC, MODE == kDw> o;
-                    if (MODE == kDx) o.begin((const char*)p.b + (wg + c0) * ES, (int64_t)p.k * ES, p.k - c0, nullptr, 0, 0, len);
-                    else o.begin((const char*)p.b + (int64_t)c0 * ES, p.ldb * ES, p.k - c0, p.order, t.beg, p.m, len);
-                    return o;
-                }
-            };
-            auto ro = row_operand();
-            auto co = col_operand();
+            using RowOp = typename std::conditional<MODE == kDw, Across<ES, C::BR, NT, ASYNC, true>,
+                                                    Along<ES, C::BR, NT, ASYNC>>::type;
+            using ColOp = typename std::conditional<MODE == kFwd, AlongRows<ES, C::BC, NT, ASYNC>,
+                                                    Across<ES, C::BC, NT, ASYNC, MODE == kDw>>::type;
+            static_assert(MODE != kDw || C::BR == C::BC, "both operands of dw take the same rows");
+            RowOp ro;
+            ColOp co;
+            Rows<ES, C::BC, NT> rows;
+            int ro_at, co_at;
+            if constexpr (MODE == kDw) {
+                rows.order = p.order;
+                rows.pos = t.beg;
+                rows.m = p.m;
+                rows.find(0, len);
+                ro.begin((const char*)p.a + (int64_t)r0 * ES, p.lda * ES, p.n - r0);
+                co.begin((const char*)p.b + (int64_t)c0 * ES, p.ldb * ES, p.k - c0);
+                ro_at = lane_across<T, C::BR>(wr);
+            } else {
+                // a row that is not there is read as the first that may be: its products are not stored
+                ro.begin([&](int r) {
+                    const int64_t row = s_row[r] < 0 ? 0 : s_row[r];
+                    return (const char*)p.a + row * p.lda * ES;
+                });
+                ro_at = lane_along(wr);
+                if constexpr (MODE == kFwd)
+                    co.begin((const char*)p.b + (wg + (int64_t)c0 * p.k) * ES, (int64_t)p.k * ES, p.n - c0);
+                else
+                    co.begin((const char*)p.b + (wg + c0) * ES, (int64_t)p.k * ES, p.k - c0);
+            }
+            if constexpr (MODE == kFwd) co_at = lane_along(C::BR + wc);
+            else co_at = C::BR * 128 + lane_across<T, C::BC>(wc);
             // the products of the step in `cur`, while the next one's operands come into `nxt`
             auto step = [&](const char* __restrict cur, char* __restrict nxt, int64_t e0) __attribute__((always_inline)) {
                 const bool more = e0 < len;
                 if (more) {
-                    ro.load(nxt, e0, len);
-                    co.load(nxt + C::BR * 128, e0, len);
+                    if constexpr (MODE == kDw) {
+                        ro.load(nxt, e0, len, rows.row);
+                        co.load(nxt + C::BR * 128, e0, len, rows.row);
+                        rows.find(e0 + kStep, len);
+                    } else {
+                        ro.load(nxt, e0, len);
+                        if constexpr (MODE == kFwd) co.load(nxt + C::BR * 128, e0, len);
+                        else co.load(nxt + C::BR * 128, e0, len, nullptr);
+                    }
                 }
                 if (busy && e0 > 0) {
+                    const int ra = recompute(ro_at), ca = recompute(co_at);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         Frag<T> fc[C::TC], fr[C::TR];
 #pragma unroll
                         for (int i = 0; i < C::TC; ++i) {
-                            if constexpr (MODE == kFwd) frag_along<T>(cur + C::BR * 128, wc + i * 16, half, fc[i]);
-                            else frag_across<C::BC>(cur + C::BR * 128, wc + i * 16, half, fc[i]);
+                            if constexpr (MODE == kFwd) frag_along<T>(cur, ca, i, half, fc[i]);
+                            else frag_across<C::BC>(cur, ca, i, half, fc[i]);
                         }
 #pragma unroll
                         for (int j = 0; j < C::TR; ++j) {
-                            if constexpr (MODE == kDw) frag_across<C::BR>(cur, wr + j * 16, half, fr[j]);
-                            else frag_along<T>(cur, wr + j * 16, half, fr[j]);
+                            if constexpr (MODE == kDw) frag_across<C::BR>(cur, ra, j, half, fr[j]);
+                            else frag_along<T>(cur, ra, j, half, fr[j]);
                         }
 #pragma unroll
                         for (int j = 0; j < C::TR; ++j)
 #pragma unroll
                             for (int i = 0; i < C::TC; ++i) multiply(fc[i], fr[j], acc[i][j]);
+                    }
+                    if constexpr (T == kSrcBf16 && C::TR >= 4) {
+                        constexpr int RC = MODE == kFwd ? 1 : 2, RR = MODE == kDw ? 2 : 1;   // reads per piece
+                        __builtin_amdgcn_sched_group_barrier(0x100, C::TC * RC + 2 * RR, 0);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                            for (int j = 0; j < C::TR; ++j) {
+                                __builtin_amdgcn_sched_group_barrier(0x008, C::TC, 0);
+                                if (j < C::TR - 2) __builtin_amdgcn_sched_group_barrier(0x100, RR, 0);
+                                else if (half == 0) __builtin_amdgcn_sched_group_barrier(0x100, C::TC / 2 * RC + RR, 0);
+                            }
+                        }
                     }
                 }
                 if (more) {
@@ -427,6 +501,132 @@ __global__ __launch_bounds__(C::kThreads) void k_product(ProdArgs p) {
     }
 }
 
+// 16 neighbouring outputs of a lane, `left` of them in the row.
+__device__ __forceinline__ void store16(void* out, bool f32, int64_t at, int left, const f32x4* v) {
+    if (f32) {
+        float* o = (float*)out + at;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q * 4 + 4 <= left) {
+                __builtin_memcpy(__builtin_assume_aligned(o + q * 4, 4), &v[q], 16);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (q * 4 + r < left) o[q * 4 + r] = v[q][r];
+            }
+        }
+    } else {
+        uint16_t* o = (uint16_t*)out + at;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f32x4 a = v[2 * h], b = v[2 * h + 1];
+            const u32x4 w = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])};
+            if (h * 8 + 8 <= left) {
+                __builtin_memcpy(__builtin_assume_aligned(o + h * 8, 2), &w, 16);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (h * 8 + r < left) o[h * 8 + r] = (uint16_t)(w[r >> 1] >> (16 * (r & 1)));
+            }
+        }
+    }
+}
+
+// Products whose matrix fits in LDS (the projections of a feature table's
+// rows): a workgroup loads its group's matrix once and its waves then walk
+// the chunk's rows, 32 at a time and without waiting for each other, from
+// global memory to registers, through the matrix, and out.
+//
+// LDS holds one row of LP * 32 elements per output, zeros beyond the matrix,
+// 16 bytes apart so that 16 rows read together hit different banks, and in
+// such an order that a lane ends up with 16 neighbouring outputs.
+template <int LP, int BYTES, int MODE>
+__global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resident(ProdArgs p) {
+    constexpr int kLd = LP * 64 + 16;
+    __shared__ __attribute__((aligned(16))) char lds[BYTES];
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int cols = MODE == kFwd ? p.n : p.k, len = MODE == kFwd ? p.k : p.n;
+    const int blocks = (cols + 63) / 64;
+    auto place = [](int c) { return (c & ~63) + ((c >> 2) & 3) * 16 + ((c >> 4) & 3) * 4 + (c & 3); };
+    for (int64_t b = blockIdx.x;; b += gridDim.x) {
+        TileAt t;
+        const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, 0, 1, b, t);
+        if (found < 0) return;
+        if (!found) continue;
+        const bool grouped = t.g < p.n_groups;
+        auto row_at = [&](int64_t pos) {
+            const int32_t row = pos < t.end ? (p.order ? p.order[pos] : (int32_t)pos) : -1;
+            return row >= 0 && row < p.m ? row : -1;
+        };
+        int64_t pos = t.beg + wv * 32;
+        int32_t row[2] = {row_at(pos + (lane & 15)), row_at(pos + 16 + (lane & 15))};
+        __syncthreads();                     // the matrix before is read
+        if (grouped) {
+            const char* w = (const char*)p.b + (int64_t)t.g * p.n * p.k * 2;
+            if (MODE == kFwd) {
+                for (int i = threadIdx.x; i < blocks * 64 * LP * 4; i += 512) {
+                    const int c = i / (LP * 4), e = i % (LP * 4) * 8;
+                    *(u32x4*)(lds + place(c) * kLd + e * 2) =
+                        held_piece<2>(w + ((int64_t)c * p.k + e) * 2, c < p.n ? p.k - e : 0);
+                }
+            } else {
+                // two rows of w and eight columns: pairs of neighbours in eight rows of LDS
+                for (int i = threadIdx.x; i < LP * 16 * blocks * 8; i += 512) {
+                    const int e = i / (blocks * 8) * 2, c = i % (blocks * 8) * 8;
+                    const char* at = w + ((int64_t)e * p.k + c) * 2;
+                    const u32x4 lo = held_piece<2>(at, e < p.n ? p.k - c : 0);
+                    const u32x4 hi = held_piece<2>(at + p.k * 2, e + 1 < p.n ? p.k - c : 0);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t a = lo[j >> 1] >> (16 * (j & 1)) & 0xFFFFu, d = hi[j >> 1] >> (16 * (j & 1));
+                        *(uint32_t*)(lds + place(c + j) * kLd + e * 2) = a | d << 16;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        for (; pos < t.end; pos += 256) {
+            Frag<kSrcBf16> x[2][LP];
+#pragma unroll
+            for (int l = 0; l < LP; ++l)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int e = l * 32 + (lane >> 4) * 8;
+                    const char* at = (const char*)p.a + (row[j] * p.lda + e) * 2;
+                    const u32x4 v = held_piece<2>(at, grouped && row[j] >= 0 ? len - e : 0);
+                    __builtin_memcpy(&x[j][l].v, &v, 16);
+                }
+            const int32_t next[2] = {row_at(pos + 256 + (lane & 15)), row_at(pos + 272 + (lane & 15))};
+            for (int nb = 0; nb < blocks; ++nb) {
+                f32x4 acc[2][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[j][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                if (grouped) {
+#pragma unroll
+                    for (int l = 0; l < LP; ++l)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            Frag<kSrcBf16> c;
+                            c.v = *(const bf16x8*)(lds + (nb * 64 + q * 16 + (lane & 15)) * kLd + l * 64 + (lane >> 4) * 16);
+                            multiply(c, x[0][l], acc[0][q]);
+                            multiply(c, x[1][l], acc[1][q]);
+                        }
+                }
+                const int col = nb * 64 + (lane >> 4) * 16;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (row[j] < 0) continue;
+                    store16(p.out, p.out_f32, (int64_t)row[j] * cols + col, cols - col, acc[j]);
+                }
+            }
+            row[0] = next[0];
+            row[1] = next[1];
+        }
+    }
+}
+
 typedef Tile<256, 256, 2, 4> Big;
 typedef Tile<128, 128, 2, 2> Mid;
 typedef Tile<32, 128, 1, 4> Small;
@@ -442,6 +642,12 @@ void launch(const ProdArgs& p, int64_t chunks, hipStream_t s) {
     hipLaunchKernelGGL((k_product<T, MODE, C, ASYNC>), grid, dim3(C::kThreads), 0, s, p);
 }
 
+template <int MODE, int LP> void launch_resident(const ProdArgs& p, int64_t chunks, int64_t bytes, hipStream_t s) {
+    const dim3 grid(grid_for(align_up((size_t)chunks, kXcds), 1));
+    if (bytes <= 81920) hipLaunchKernelGGL((k_resident<LP, 81920, MODE>), grid, dim3(512), 0, s, p);
+    else hipLaunchKernelGGL((k_resident<LP, 163840, MODE>), grid, dim3(512), 0, s, p);
+}
+
 // Forward product or dx: `cols` outputs a row, reduced over `len`.
 template <int MODE> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s) {
     const int cols = MODE == kFwd ? p.n : p.k, es = elem(dtype);
@@ -449,6 +655,17 @@ template <int MODE> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s)
                       (MODE == kFwd || (int64_t)p.n * es % 16 == 0) && aligned(p.b, 16);
     p.out_vec = cols % 4 == 0 && aligned(p.out, p.out_f32 ? 16 : 8);
     const int64_t each = p.m / p.n_groups;
+    const int len = MODE == kFwd ? p.k : p.n, lp = len <= 32 ? 1 : len <= 64 ? 2 : len <= 128 ? 4 : 8;
+    const int64_t bytes = ceil_div(cols, 64) * 64 * (lp * 64 + 16);
+    if (dtype == HTL_BF16 && len <= 256 && bytes <= 163840 && each >= 512) {
+        p.rows = (uint32_t)align_up((size_t)ceil_div(p.m, 1024), 256);
+        const int64_t chunks = p.m / p.rows + p.n_groups + 1;
+        if (lp == 1) launch_resident<MODE, 1>(p, chunks, bytes, s);
+        else if (lp == 2) launch_resident<MODE, 2>(p, chunks, bytes, s);
+        else if (lp == 4) launch_resident<MODE, 4>(p, chunks, bytes, s);
+        else launch_resident<MODE, 8>(p, chunks, bytes, s);
+        return;
+    }
     int tile = each <= 48 ? 32 : 128;
     if (tile == 128 && dtype == HTL_BF16 && fast && ceil_div(p.m, 256) * ceil_div(cols, 256) >= 512 && each >= 256) tile = 256;
     p.rows = (uint32_t)tile;
@@ -467,18 +684,17 @@ template <int MODE> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s)
     }
 }
 
-constexpr int kT = 128;
-
 // Rows per chunk of dw's sums: chunks times tiles fill the device a few
 // times over, and a chunk is long against the partial sums it leaves.
-uint32_t dw_chunk_rows(int64_t m, int n_groups, int n, int k) {
-    const int64_t tiles = ceil_div(n, kT) * ceil_div(k, kT);
-    int64_t r = ceil_div(m * tiles, 2048);
+uint32_t dw_chunk_rows(int64_t m, int n, int k) {
+    const int side = n >= 256 && k >= 256 ? 256 : 128;
+    const int64_t tiles = ceil_div(n, side) * ceil_div(k, side);
+    int64_t r = ceil_div(m * tiles, side == 256 ? 512 : 1024);
     if (r < 256) r = 256;
     if (r > m) r = m < 1 ? 1 : m;
     return (uint32_t)r;
 }
-int64_t dw_chunks(int64_t m, int n_groups, int n, int k) { return m / dw_chunk_rows(m, n_groups, n, k) + n_groups + 1; }
+int64_t dw_chunks(int64_t m, int n_groups, int n, int k) { return m / dw_chunk_rows(m, n, k) + n_groups + 1; }
 
 }  // namespace
 }  // namespace htl
@@ -513,7 +729,7 @@ extern "C" size_t grouped_mm_backward_workspace_bytes(int64_t m, int n_groups, i
     if (m < 0 || m > kMaxRows || n_groups < 1 || n_groups > kMaxGroups || n < 1 || n > HTL_MAX_PRODUCT_DIM || k < 1 ||
         k > HTL_MAX_PRODUCT_DIM)
         return 0;
-    if (m <= (int64_t)dw_chunk_rows(m, n_groups, n, k)) return 256;
+    if (m <= (int64_t)dw_chunk_rows(m, n, k)) return 256;
     return align_up((size_t)dw_chunks(m, n_groups, n, k) * n * k * 4, 256);
 }
 
@@ -538,12 +754,13 @@ extern "C" htl_status grouped_mm_backward(const void* dy, int64_t ld_dy, const v
         if (st != HTL_OK) return st;
     }
     if (!dw) return HTL_OK;
-    const ProdArgs p = {dy, x, dw, order, offsets, m, ld_dy, ldx, n, k, n_groups, dw_chunk_rows(m, n_groups, n, k),
+    const ProdArgs p = {dy, x, dw, order, offsets, m, ld_dy, ldx, n, k, n_groups, dw_chunk_rows(m, n, k),
                         (float*)ws, 1, k % 4 == 0 && aligned(dw, 16), dw_chunks(m, n_groups, n, k)};
     const bool fast = ld_dy * es % 16 == 0 && ldx * es % 16 == 0 && aligned(dy, 16) && aligned(x, 16) &&
                       (int64_t)n * es % 16 == 0 && (int64_t)k * es % 16 == 0;
     if (dtype == HTL_BF16) {
-        if (fast) launch<kSrcBf16, kDw, Mid, true>(p, p.limit, stream);
+        if (fast && n >= 256 && k >= 256) launch<kSrcBf16, kDw, Big, true>(p, p.limit, stream);
+        else if (fast) launch<kSrcBf16, kDw, Mid, true>(p, p.limit, stream);
         else launch<kSrcBf16, kDw, Mid, false>(p, p.limit, stream);
     } else {
         if (fast) launch<kSrcF32, kDw, Mid, true>(p, p.limit, stream);
