@@ -150,25 +150,38 @@ template <int ES, int B, int NT, bool ASYNC> struct AlongRows {
     __device__ __forceinline__ void store(char* lds) { store_pieces<NT, ASYNC, kN>(held, lds); }
 };
 
-// Rows of consecutive positions of a chunk, found through order one step
-// ahead of their use.
+// Rows of consecutive positions of a chunk.  order is read one step ahead of
+// its use, without branches and looked at only then, so that nothing waits
+// for it; without order a word of zeros stands in.
 template <int ES, int B, int NT> struct Rows {
     static constexpr int kN = B * 8 / NT, kRows = NT / (B * ES / 16);
-    const int32_t* order;
+    const int32_t* at;
     int64_t pos, m;
-    int32_t row[kN];
-    __device__ __forceinline__ void find(int64_t e0, int64_t len) {
+    bool ordered;
+    int32_t raw[kN];
+    __device__ __forceinline__ void begin(const int32_t* order, int64_t beg, int64_t rows) {
+        ordered = order != nullptr;
+        at = ordered ? order + beg : (const int32_t*)&g_zeros;
+        pos = beg;
+        m = rows;
+    }
+    __device__ __forceinline__ void read(int64_t e0, int64_t len) {
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int64_t e = e0 + (int)(threadIdx.x / (B * ES / 16)) + i * kRows;
-            const int64_t r = e < len ? (order ? (int64_t)order[pos + e] : pos + e) : -1;
-            row[i] = r < m ? (int32_t)r : -1;
+            raw[i] = at[ordered && e < len ? e : 0];
         }
+    }
+    // The row of pass i, or -1.
+    __device__ __forceinline__ int32_t row(int i, int64_t e0, int64_t len) const {
+        const int64_t e = e0 + (int)(threadIdx.x / (B * ES / 16)) + i * kRows;
+        const int32_t r = ordered ? raw[i] : (int32_t)(pos + e);
+        return e < len && r < m ? r : -1;
     }
 };
 
 // One operand's share of a step whose reduction runs across the rows of a
-// matrix: those that Rows found (GATHER), or row e0 + e from `base` on.
+// matrix: those that Rows names (GATHER), or row e0 + e from `base` on.
 template <int ES, int B, int NT, bool ASYNC, bool GATHER> struct Across {
     static constexpr int kN = B * 8 / NT, VE = 16 / ES, S = B * ES / 16, kRows = NT / S;
     static_assert(kN * NT == B * 8 && S >= 16, "whole passes");
@@ -181,15 +194,16 @@ template <int ES, int B, int NT, bool ASYNC, bool GATHER> struct Across {
         ld = ld_bytes;
         cols = cols_left;
     }
-    __device__ __forceinline__ void load(char* lds, int64_t e0, int64_t len, const int32_t* row) {
+    template <class R> __device__ __forceinline__ void load(char* lds, int64_t e0, int64_t len, const R& rows) {
         char* at = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
         const int t = recompute((int)threadIdx.x);
         const char* s0 = GATHER ? base : recompute(base) + e0 * ld;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int e = t / S + i * kRows, col = ((t % S) ^ swap_across<ES>(e)) * VE;
-            const int64_t left = (GATHER ? row[i] >= 0 : e0 + e < len) ? cols - col : 0;
-            const char* s = s0 + (GATHER ? row[i] * ld : i * kRows * ld) + col * ES;
+            const int32_t row = GATHER ? rows.row(i, e0, len) : 0;
+            const int64_t left = (GATHER ? row >= 0 : e0 + e < len) ? cols - col : 0;
+            const char* s = s0 + (GATHER ? row * ld : i * kRows * ld) + col * ES;
             if (ASYNC) load_piece(left > 0 ? s : (const char*)&g_zeros, at + i * NT * 16);
             else held[i] = held_piece<ES>(s, left);
         }
@@ -235,12 +249,13 @@ template <int B> __device__ __forceinline__ void frag_across(const char* lds, in
     for (int j = 0; j < 4; ++j) f.v[j] = *(const float*)(p + j * B * 4);
 }
 
-__device__ __forceinline__ void multiply(const Frag<kSrcBf16>& c, const Frag<kSrcBf16>& r, f32x4& acc) {
+// Step e of kSteps<T>: one matrix instruction.
+template <int T> constexpr int kSteps = T == kSrcF32 ? 4 : 1;
+__device__ __forceinline__ void multiply(const Frag<kSrcBf16>& c, const Frag<kSrcBf16>& r, int, f32x4& acc) {
     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c.v, r.v, acc, 0, 0, 0);
 }
-__device__ __forceinline__ void multiply(const Frag<kSrcF32>& c, const Frag<kSrcF32>& r, f32x4& acc) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(c.v[j], r.v[j], acc, 0, 0, 0);
+__device__ __forceinline__ void multiply(const Frag<kSrcF32>& c, const Frag<kSrcF32>& r, int e, f32x4& acc) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(c.v[e], r.v[e], acc, 0, 0, 0);
 }
 
 // The tile that workgroup number b of the launch takes: consecutive tiles go
@@ -314,8 +329,10 @@ __device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, i
             const int64_t index = block * kBlock + (in - t.col * width);
             t.chunk = before + index;
             const int64_t gb = (int64_t)__shfl((int)beg, l), ge = (int64_t)__shfl((int)end, l);
-            t.beg = gb + index * R;
-            t.end = t.beg + R < ge ? t.beg + R : ge;
+            // sums over rows: chunks of about the same length
+            const int64_t len = min_chunks ? ((uint32_t)((ge - gb + t.count - 1) / t.count) + 63u) / 64 * 64 : R;
+            t.beg = gb + index * len < ge ? gb + index * len : ge;
+            t.end = t.beg + len < ge ? t.beg + len : ge;
             return 1;
         }
         run += __shfl(incl, 63);
@@ -373,10 +390,8 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(ProdArgs p) {
             Rows<ES, C::BC, NT> rows;
             int ro_at, co_at;
             if constexpr (MODE == kDw) {
-                rows.order = p.order;
-                rows.pos = t.beg;
-                rows.m = p.m;
-                rows.find(0, len);
+                rows.begin(p.order, t.beg, p.m);
+                rows.read(0, len);
                 ro.begin((const char*)p.a + (int64_t)r0 * ES, p.lda * ES, p.n - r0);
                 co.begin((const char*)p.b + (int64_t)c0 * ES, p.ldb * ES, p.k - c0);
                 ro_at = lane_across<T, C::BR>(wr);
@@ -399,13 +414,13 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(ProdArgs p) {
                 const bool more = e0 < len;
                 if (more) {
                     if constexpr (MODE == kDw) {
-                        ro.load(nxt, e0, len, rows.row);
-                        co.load(nxt + C::BR * 128, e0, len, rows.row);
-                        rows.find(e0 + kStep, len);
+                        ro.load(nxt, e0, len, rows);
+                        co.load(nxt + C::BR * 128, e0, len, rows);
+                        rows.read(e0 + kStep, len);
                     } else {
                         ro.load(nxt, e0, len);
                         if constexpr (MODE == kFwd) co.load(nxt + C::BR * 128, e0, len);
-                        else co.load(nxt + C::BR * 128, e0, len, nullptr);
+                        else co.load(nxt + C::BR * 128, e0, len, rows);
                     }
                 }
                 if (busy && e0 > 0) {
@@ -424,9 +439,11 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(ProdArgs p) {
                             else frag_along<T>(cur, ra, j, half, fr[j]);
                         }
 #pragma unroll
-                        for (int j = 0; j < C::TR; ++j)
+                        for (int e = 0; e < kSteps<T>; ++e)
 #pragma unroll
-                            for (int i = 0; i < C::TC; ++i) multiply(fc[i], fr[j], acc[i][j]);
+                            for (int j = 0; j < C::TR; ++j)
+#pragma unroll
+                                for (int i = 0; i < C::TC; ++i) multiply(fc[i], fr[j], e, acc[i][j]);
                     }
                     if constexpr (T == kSrcBf16 && C::TR >= 4) {
                         constexpr int RC = MODE == kFwd ? 1 : 2, RR = MODE == kDw ? 2 : 1;   // reads per piece
@@ -610,8 +627,8 @@ __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resi
                         for (int q = 0; q < 4; ++q) {
                             Frag<kSrcBf16> c;
                             c.v = *(const bf16x8*)(lds + (nb * 64 + q * 16 + (lane & 15)) * kLd + l * 64 + (lane >> 4) * 16);
-                            multiply(c, x[0][l], acc[0][q]);
-                            multiply(c, x[1][l], acc[1][q]);
+                            multiply(c, x[0][l], 0, acc[0][q]);
+                            multiply(c, x[1][l], 0, acc[1][q]);
                         }
                 }
                 const int col = nb * 64 + (lane >> 4) * 16;
