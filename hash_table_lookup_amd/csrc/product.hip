@@ -34,29 +34,37 @@ struct ProdArgs {
 enum { kFwd = 0, kDx = 1, kDw = 2 };
 
 // The output is cut into tiles of BR x BC: rows are x's (dy's) rows of one
-// group and columns n (k), or n and k for dw.  A tile is reduced 128 bytes of
-// each operand row at a time (kStep elements), in LDS twice over so that the
-// next step's loads run under this step's products.
+// group and columns n (k), or n and k for dw.  A tile is reduced 64 bytes of
+// each operand row at a time (a step: 32 bf16 elements or 16 fp32), through a
+// ring of four steps in LDS: two steps' loads are under way while a third
+// lies ready and the fourth is multiplied, with one barrier a step.
 //
 // An operand whose reduction runs along its rows in memory ("along") is kept
-// as [tile row][128 bytes]; one whose reduction runs across them ("across":
-// w in dx, both operands in dw) as [kStep][tile row], and is transposed on
-// the way to the registers.  In both, 16-byte pieces of a row are permuted by
-// an exclusive or with row bits, so that the lanes that a read serves
-// together hit different banks.
+// as [tile row][64 bytes]; one whose reduction runs across them ("across": w
+// in dx, both operands in dw) as [step's elements][tile row], and is
+// transposed on the way to the registers.  In both, 16-byte pieces of a row
+// are permuted by an exclusive or with row bits, so that the lanes that a
+// read serves together hit different banks (no conflict is left by count).
+constexpr int kStepBytes = 64, kRing = 4;
 template <int BR_, int BC_, int WR_, int WC_> struct Tile {
     static constexpr int BR = BR_, BC = BC_, WR = WR_, WC = WC_;
     static constexpr int kThreads = 64 * WR_ * WC_;
     static constexpr int TR = BR_ / WR_ / 16, TC = BC_ / WC_ / 16;   // 16 x 16 outputs per wave
 };
 
-__device__ u32x4 g_zeros;    // what a piece outside an operand is loaded from
-
+// An operand in global memory, below 4 GiB: pieces come by 32-bit offset, and
+// one at kOutside (beyond `bytes`) is zeros.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+constexpr uint32_t kOutside = 0xFFFFFFF0u;
+constexpr int64_t kBufferBytes = 0xFFFF0000ll;
+__device__ __forceinline__ Buffer buffer_of(const void* p, int64_t bytes) {
+    // raw 32-bit data, no stride: offsets are in bytes and checked against `bytes`
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)(uint32_t)bytes, 0x00020000);
+}
 // A 16-byte piece from global memory straight into LDS: lane l of the wave
 // writes lds + 16 l.
-__device__ __forceinline__ void load_piece(const char* src, char* lds) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                     (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+__device__ __forceinline__ void load_piece(Buffer b, uint32_t at, uint32_t add, char* lds) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)lds, 16, (int)at, (int)add, 0, 0);
 }
 // `left` elements of a piece at any alignment of the element, zeros beyond.
 template <int ES> __device__ __forceinline__ u32x4 held_piece(const char* src, int64_t left) {
@@ -75,13 +83,21 @@ template <int ES> __device__ __forceinline__ u32x4 held_piece(const char* src, i
     return v;
 }
 
-template <int NT, bool ASYNC, int N> __device__ __forceinline__ void store_pieces(const u32x4* held, char* lds) {
+// Piece number of pass i of a tile of N pieces; with fewer pieces than
+// threads some are loaded twice over, so that every wave has the same number
+// of loads under way.
+template <int NT, int N> __device__ __forceinline__ int piece_at(int i, int t) { return N < NT ? t % N : i * NT + t; }
+template <int NT, int N, bool ASYNC> __device__ __forceinline__ void store_pieces(const u32x4* held, char* lds) {
     if (ASYNC) return;
 #pragma unroll
-    for (int i = 0; i < N; ++i) *(u32x4*)(lds + (i * NT + threadIdx.x) * 16) = held[i];
+    for (int i = 0; i < (N + NT - 1) / NT; ++i) *(u32x4*)(lds + piece_at<NT, N>(i, threadIdx.x) * 16) = held[i];
+}
+// The wave's first piece of pass i, in bytes.
+template <int NT, int N> __device__ __forceinline__ int wave_bytes(int i) {
+    return __builtin_amdgcn_readfirstlane(piece_at<NT, N>(i, threadIdx.x & ~63)) * 16;
 }
 
-__device__ __forceinline__ int swap_along(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int swap_along(int r) { return (r >> 2) & 3; }
 // Rows of at least 16 pieces.  bf16: 32 lanes read 32 bytes of rows 0..3 and
 // 8..11 (and the next 32 of rows 16 on); fp32: 64 lanes read 64 bytes of each
 // of four rows 4 apart.
@@ -96,135 +112,159 @@ template <class V> __device__ __forceinline__ V recompute(V v) {
     return v;
 }
 
-// One operand's share of a step, kN pieces per thread, from rows that
-// `row_start` names (rows of x or dy).
+// One operand's share of a step, kN pieces per thread, from rows (of x or dy)
+// that `row_at` names.  ASYNC: whole pieces, 16-byte aligned, straight into
+// LDS; otherwise by way of registers.
 template <int ES, int B, int NT, bool ASYNC> struct Along {
-    static constexpr int kN = B * 8 / NT, VE = 16 / ES;
-    static_assert(kN * NT == B * 8, "whole passes");
-    const char* src[kN];
+    static constexpr int N = B * 4, kN = (N + NT - 1) / NT, VE = 16 / ES;
+    static_assert(N % NT == 0 || NT % N == 0, "whole passes");
+    Buffer buf;
+    uint32_t at[ASYNC ? kN : 1];
+    const char* src[ASYNC ? 1 : kN];
     int slot;
     u32x4 held[ASYNC ? 1 : kN];
-    template <class F> __device__ __forceinline__ void begin(F row_start) {
-        slot = (threadIdx.x & 7) ^ swap_along(threadIdx.x >> 3);   // passes are 16 rows or more apart
+    template <class F> __device__ __forceinline__ void begin(const void* p, int64_t ld_bytes, int64_t rows, F row_at) {
+        // passes are a multiple of 16 rows apart: one permutation for all
+        slot = (threadIdx.x & 3) ^ swap_along(threadIdx.x >> 2);
+        if (ASYNC) buf = buffer_of(p, rows * ld_bytes);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) src[i] = row_start((int)(i * (NT / 8) + (threadIdx.x >> 3))) + slot * 16;
+        for (int i = 0; i < kN; ++i) {
+            const int64_t row = row_at(piece_at<NT, N>(i, threadIdx.x) >> 2);
+            if (ASYNC) at[i] = (uint32_t)row * (uint32_t)ld_bytes + slot * 16;
+            else src[i] = (const char*)p + row * ld_bytes + slot * 16;
+        }
     }
     __device__ __forceinline__ void load(char* lds, int64_t e0, int64_t len) {
         const int64_t left = len - e0 - slot * VE;
-        char* at = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const char* s = src[i] + e0 * ES;
-            if (ASYNC) load_piece(left > 0 ? s : (const char*)&g_zeros, at + i * NT * 16);
-            else held[i] = held_piece<ES>(s, left);
+            if (ASYNC) load_piece(buf, left > 0 ? at[i] : kOutside, (uint32_t)e0 * ES, lds + wave_bytes<NT, N>(i));
+            else held[i] = held_piece<ES>(src[i] + e0 * ES, left);
         }
     }
-    __device__ __forceinline__ void store(char* lds) { store_pieces<NT, ASYNC, kN>(held, lds); }
+    __device__ __forceinline__ void store(char* lds) { store_pieces<NT, N, ASYNC>(held, lds); }
 };
 
 // The same from consecutive rows (of w), zeros from row `rows` on.
 template <int ES, int B, int NT, bool ASYNC> struct AlongRows {
-    static constexpr int kN = B * 8 / NT, VE = 16 / ES;
+    static constexpr int N = B * 4, kN = (N + NT - 1) / NT, VE = 16 / ES;
+    static_assert(N % NT == 0, "whole passes");
+    Buffer buf;
+    uint32_t at;
     const char* src;
     int64_t ld;              // bytes
     int slot, rows;
     u32x4 held[ASYNC ? 1 : kN];
     __device__ __forceinline__ void begin(const char* p, int64_t ld_bytes, int rows_left) {
-        slot = (threadIdx.x & 7) ^ swap_along(threadIdx.x >> 3);
+        slot = (threadIdx.x & 3) ^ swap_along(threadIdx.x >> 2);
         ld = ld_bytes;
-        rows = rows_left - (int)(threadIdx.x >> 3);
-        src = p + (threadIdx.x >> 3) * ld + slot * 16;
+        rows = rows_left - (int)(threadIdx.x >> 2);
+        if (ASYNC) {
+            buf = buffer_of(p, rows_left * ld);
+            at = (threadIdx.x >> 2) * (uint32_t)ld + slot * 16;
+        } else {
+            src = p + (threadIdx.x >> 2) * ld + slot * 16;
+        }
     }
     __device__ __forceinline__ void load(char* lds, int64_t e0, int64_t len) {
         const int64_t left = len - e0 - slot * VE;
-        char* at = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
-        const char* s0 = recompute(src) + e0 * ES;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const char* s = s0 + i * (NT / 8) * ld;
-            const int64_t have = i * (NT / 8) < rows ? left : 0;
-            if (ASYNC) load_piece(have > 0 ? s : (const char*)&g_zeros, at + i * NT * 16);
-            else held[i] = held_piece<ES>(s, have);
+            const int64_t have = i * (NT / 4) < rows ? left : 0;
+            if (ASYNC)
+                load_piece(buf, have > 0 ? at : kOutside, (uint32_t)e0 * ES + i * (NT / 4) * (uint32_t)ld,
+                           lds + wave_bytes<NT, N>(i));
+            else
+                held[i] = held_piece<ES>(src + e0 * ES + i * (NT / 4) * ld, have);
         }
     }
-    __device__ __forceinline__ void store(char* lds) { store_pieces<NT, ASYNC, kN>(held, lds); }
+    __device__ __forceinline__ void store(char* lds) { store_pieces<NT, N, ASYNC>(held, lds); }
 };
 
-// Rows of consecutive positions of a chunk.  order is read one step ahead of
-// its use, without branches and looked at only then, so that nothing waits
-// for it; without order a word of zeros stands in.
-template <int ES, int B, int NT> struct Rows {
-    static constexpr int kN = B * 8 / NT, kRows = NT / (B * ES / 16);
-    const int32_t* at;
+// Rows of consecutive positions of a chunk, kIds at a time in LDS: a block is
+// on its way in registers while the one before is used.
+constexpr int kIds = 1024;
+template <int NT> struct Rows {
+    static constexpr int kN = kIds / NT;
+    const int32_t* order;
     int64_t pos, m;
-    bool ordered;
     int32_t raw[kN];
-    __device__ __forceinline__ void begin(const int32_t* order, int64_t beg, int64_t rows) {
-        ordered = order != nullptr;
-        at = ordered ? order + beg : (const int32_t*)&g_zeros;
+    __device__ __forceinline__ void begin(const int32_t* ord, int64_t beg, int64_t rows) {
+        order = ord;
         pos = beg;
         m = rows;
     }
     __device__ __forceinline__ void read(int64_t e0, int64_t len) {
+        const int64_t e = e0 + threadIdx.x;
+        if (order) {
+            const int32_t* at = order + pos;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int64_t e = e0 + (int)(threadIdx.x / (B * ES / 16)) + i * kRows;
-            raw[i] = at[ordered && e < len ? e : 0];
+            for (int i = 0; i < kN; ++i) raw[i] = at[e + i * NT < len ? e + i * NT : 0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) raw[i] = (int32_t)(pos + e) + i * NT;
         }
     }
-    // The row of pass i, or -1.
-    __device__ __forceinline__ int32_t row(int i, int64_t e0, int64_t len) const {
-        const int64_t e = e0 + (int)(threadIdx.x / (B * ES / 16)) + i * kRows;
-        const int32_t r = ordered ? raw[i] : (int32_t)(pos + e);
-        return e < len && r < m ? r : -1;
+    // -1: no row
+    __device__ __forceinline__ void store(int32_t* ids, int64_t e0, int64_t len) const {
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            ids[threadIdx.x + i * NT] = e0 + threadIdx.x + i * NT < len && raw[i] < m ? raw[i] : -1;
     }
 };
 
 // One operand's share of a step whose reduction runs across the rows of a
-// matrix: those that Rows names (GATHER), or row e0 + e from `base` on.
+// matrix: those that ids names (GATHER), or row e0 + e from `base` on.
 template <int ES, int B, int NT, bool ASYNC, bool GATHER> struct Across {
-    static constexpr int kN = B * 8 / NT, VE = 16 / ES, S = B * ES / 16, kRows = NT / S;
-    static_assert(kN * NT == B * 8 && S >= 16, "whole passes");
+    static constexpr int N = B * 4, kN = N / NT, VE = 16 / ES, S = B * ES / 16, kRows = NT / S;
+    static_assert(kN * NT == N && S >= 16, "whole passes");
+    Buffer buf;
     const char* base;
     int64_t ld;              // bytes
     int cols;                // elements of a row from this tile's first on
     u32x4 held[ASYNC ? 1 : kN];
-    __device__ __forceinline__ void begin(const char* p, int64_t ld_bytes, int cols_left) {
-        base = GATHER ? p : p + (threadIdx.x / S) * ld_bytes;
+    // p: the matrix of `rows` rows, c0: the tile's first column
+    __device__ __forceinline__ void begin(const void* p, int64_t ld_bytes, int64_t rows, int c0, int cols_in_all) {
+        if (ASYNC) buf = buffer_of(p, rows * ld_bytes);
+        base = (const char*)p + (int64_t)c0 * ES;
+        first = c0 * ES;
         ld = ld_bytes;
-        cols = cols_left;
+        cols = cols_in_all - c0;
     }
-    template <class R> __device__ __forceinline__ void load(char* lds, int64_t e0, int64_t len, const R& rows) {
-        char* at = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+    // ids: of the step's elements
+    __device__ __forceinline__ void load(char* lds, int64_t e0, int64_t len, const int32_t* ids) {
         const int t = recompute((int)threadIdx.x);
-        const char* s0 = GATHER ? base : recompute(base) + e0 * ld;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int e = t / S + i * kRows, col = ((t % S) ^ swap_across<ES>(e)) * VE;
-            const int32_t row = GATHER ? rows.row(i, e0, len) : 0;
-            const int64_t left = (GATHER ? row >= 0 : e0 + e < len) ? cols - col : 0;
-            const char* s = s0 + (GATHER ? row * ld : i * kRows * ld) + col * ES;
-            if (ASYNC) load_piece(left > 0 ? s : (const char*)&g_zeros, at + i * NT * 16);
-            else held[i] = held_piece<ES>(s, left);
+            const int32_t row = GATHER ? ids[e] : 0;
+            const int64_t left = (!GATHER || row >= 0) && e0 + e < len ? cols - col : 0;
+            if (ASYNC) {
+                const uint32_t at = (GATHER ? (uint32_t)row : (uint32_t)(t / S)) * (uint32_t)ld + (uint32_t)first + col * ES;
+                load_piece(buf, left > 0 ? at : kOutside, GATHER ? 0 : (uint32_t)(e0 + i * kRows) * (uint32_t)ld,
+                           lds + wave_bytes<NT, N>(i));
+            } else {
+                held[i] = held_piece<ES>(base + (GATHER ? (int64_t)row : e0 + e) * ld + col * ES, left);
+            }
         }
     }
-    __device__ __forceinline__ void store(char* lds) { store_pieces<NT, ASYNC, kN>(held, lds); }
+    __device__ __forceinline__ void store(char* lds) { store_pieces<NT, N, ASYNC>(held, lds); }
+    int first;
 };
 
 template <int T> struct Frag;
 template <> struct Frag<kSrcBf16> { bf16x8 v; };
 template <> struct Frag<kSrcF32> { f32x4 v; };
 
-// What a lane gives a matrix instruction of 16 tile rows from r0 on: row
-// r0 + l % 16, elements (l / 16) * 8 .. + 8 of the half step's 32 in bf16,
-// (l / 16) * 4 .. + 4 of 16 in fp32.
+// What a lane gives a matrix instruction of 16 tile rows: row l % 16, elements
+// (l / 16) * 8 .. + 8 of the step in bf16, (l / 16) * 4 .. + 4 in fp32.
 // at: lane_along / lane_across of the lane, once for a tile; i: which 16 rows.
 __device__ __forceinline__ int lane_along(int r0) {
     const int lane = __lane_id();
-    return (r0 + (lane & 15)) * 128 + ((lane >> 4) ^ swap_along(lane & 15)) * 16;
+    return (r0 + (lane & 15)) * 64 + ((lane >> 4) ^ swap_along(lane & 15)) * 16;
 }
-template <int T> __device__ __forceinline__ void frag_along(const char* lds, int at, int i, int half, Frag<T>& f) {
-    f.v = *(const decltype(f.v)*)(lds + (at ^ half * 64) + i * 2048);
+template <int T> __device__ __forceinline__ void frag_along(const char* lds, int at, int i, Frag<T>& f) {
+    f.v = *(const decltype(f.v)*)(lds + at + i * 1024);
 }
 // bf16: 16 lanes read four rows of 16 elements, and each gets one column.
 template <int T, int B> __device__ __forceinline__ int lane_across(int r0) {
@@ -235,16 +275,16 @@ template <int T, int B> __device__ __forceinline__ int lane_across(int r0) {
     }
     return q * 4 * B * 4 + (((r0 >> 2) + ((lane & 15) >> 2)) ^ swap_across<4>(q * 4)) * 16 + (lane & 3) * 4;
 }
-template <int B> __device__ __forceinline__ void frag_across(const char* lds, int at, int i, int half, Frag<kSrcBf16>& f) {
-    const char* p = lds + (at ^ i * 32) + half * 32 * B * 2;
+template <int B> __device__ __forceinline__ void frag_across(const char* lds, int at, int i, Frag<kSrcBf16>& f) {
+    const char* p = lds + (at ^ i * 32);
     typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
     union { i16x4 h[2]; bf16x8 v; } u;
     u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
     u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 4 * B * 2));
     f.v = u.v;
 }
-template <int B> __device__ __forceinline__ void frag_across(const char* lds, int at, int i, int half, Frag<kSrcF32>& f) {
-    const char* p = lds + (at ^ i * 64) + half * 16 * B * 4;
+template <int B> __device__ __forceinline__ void frag_across(const char* lds, int at, int i, Frag<kSrcF32>& f) {
+    const char* p = lds + (at ^ i * 64);
 #pragma unroll
     for (int j = 0; j < 4; ++j) f.v[j] = *(const float*)(p + j * B * 4);
 }
@@ -274,7 +314,7 @@ struct TileAt {
 };
 constexpr int kBlock = 8, kXcds = 8;
 // 1: found; 0: nothing at this b; -1: nothing at this or any later b.
-__device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, int64_t m, uint32_t R, int min_chunks,
+__device__ __forceinline__ int search_tile(const int32_t* offsets, int n_groups, int64_t m, uint32_t R, int min_chunks,
                                          int64_t cols, int64_t b, TileAt& t) {
     const int lane = __lane_id();
     auto chunks_at = [&](int g, int64_t& beg, int64_t& end) {
@@ -319,20 +359,22 @@ __device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, i
         const uint64_t past = __ballot((run + incl) * cols > item);
         if (past) {
             const int l = __ffsll((unsigned long long)past) - 1;
-            t.g = __builtin_amdgcn_readfirstlane(g0 + l);
-            t.count = __builtin_amdgcn_readfirstlane(__shfl(cnt, l));
+            t.g = g0 + l;
+            t.count = __shfl(cnt, l);
             const int64_t before = run + __shfl(incl, l) - t.count;
             const int64_t local = item - before * cols;
             const int64_t block = local / (cols * kBlock), in = local - block * cols * kBlock;
             const int64_t left = t.count - block * kBlock, width = left < kBlock ? left : kBlock;
-            t.col = (int)(in / width);
-            const int64_t index = block * kBlock + (in - t.col * width);
-            t.chunk = before + index;
+            const int col = (int)(in / width);
+            const int64_t index = block * kBlock + (in - col * width);
             const int64_t gb = (int64_t)__shfl((int)beg, l), ge = (int64_t)__shfl((int)end, l);
             // sums over rows: chunks of about the same length
             const int64_t len = min_chunks ? ((uint32_t)((ge - gb + t.count - 1) / t.count) + 63u) / 64 * 64 : R;
-            t.beg = gb + index * len < ge ? gb + index * len : ge;
-            t.end = t.beg + len < ge ? t.beg + len : ge;
+            const int64_t b0 = gb + index * len < ge ? gb + index * len : ge;
+            t.col = col;
+            t.chunk = before + index;
+            t.beg = b0;
+            t.end = b0 + len < ge ? b0 + len : ge;
             return 1;
         }
         run += __shfl(incl, 63);
@@ -340,12 +382,35 @@ __device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, i
     return -1;
 }
 
+// The same, said to be the same in every lane: what follows from it stays in
+// scalar registers.
+__device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, int64_t m, uint32_t R, int min_chunks,
+                                         int64_t cols, int64_t b, TileAt& t) {
+    TileAt v = {};
+    const int found = search_tile(offsets, n_groups, m, R, min_chunks, cols, b, v);
+    t.g = __builtin_amdgcn_readfirstlane(v.g);
+    t.beg = __builtin_amdgcn_readfirstlane((int)v.beg);
+    t.end = __builtin_amdgcn_readfirstlane((int)v.end);
+    t.chunk = __builtin_amdgcn_readfirstlane((int)v.chunk);
+    t.count = __builtin_amdgcn_readfirstlane(v.count);
+    t.col = __builtin_amdgcn_readfirstlane(v.col);
+    return __builtin_amdgcn_readfirstlane(found);
+}
+
 template <int T, int MODE, class C, bool ASYNC>
 __global__ __launch_bounds__(C::kThreads, 2) void k_product(ProdArgs p) {
-    constexpr int ES = T == kSrcF32 ? 4 : 2, NT = C::kThreads, kStep = 128 / ES;
-    __shared__ __attribute__((aligned(128))) char lds0[(C::BR + C::BC) * 128];
-    __shared__ __attribute__((aligned(128))) char lds1[(C::BR + C::BC) * 128];
+    // Slots of the ring as variables of their own: the compiler then makes a
+    // read of one wait for that slot's loads alone, not for every load into
+    // LDS under way.
+    constexpr int kSlot = (C::BR + C::BC) * kStepBytes;
+    __shared__ int32_t s_ids[MODE == kDw ? 2 * kIds : 1];
     __shared__ int32_t s_row[MODE == kDw ? 1 : C::BR];
+    __shared__ __attribute__((aligned(128))) char ring0[kSlot];
+    __shared__ __attribute__((aligned(128))) char ring1[kSlot];
+    __shared__ __attribute__((aligned(128))) char ring2[kSlot];
+    __shared__ __attribute__((aligned(128))) char ring3[kSlot];
+    constexpr int ES = T == kSrcF32 ? 4 : 2, NT = C::kThreads, kStep = kStepBytes / ES;
+    constexpr int kCols = C::BR * kStepBytes;
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wr = wv / C::WC * (C::TR * 16), wc = wv % C::WC * (C::TC * 16);
     const int cols = MODE == kFwd ? p.n : p.k;
@@ -384,95 +449,135 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(ProdArgs p) {
                                                     Along<ES, C::BR, NT, ASYNC>>::type;
             using ColOp = typename std::conditional<MODE == kFwd, AlongRows<ES, C::BC, NT, ASYNC>,
                                                     Across<ES, C::BC, NT, ASYNC, MODE == kDw>>::type;
-            static_assert(MODE != kDw || C::BR == C::BC, "both operands of dw take the same rows");
             RowOp ro;
             ColOp co;
-            Rows<ES, C::BC, NT> rows;
+            Rows<NT> rows;
             int ro_at, co_at;
             if constexpr (MODE == kDw) {
                 rows.begin(p.order, t.beg, p.m);
                 rows.read(0, len);
-                ro.begin((const char*)p.a + (int64_t)r0 * ES, p.lda * ES, p.n - r0);
-                co.begin((const char*)p.b + (int64_t)c0 * ES, p.ldb * ES, p.k - c0);
+                ro.begin(p.a, p.lda * ES, p.m, r0, p.n);
+                co.begin(p.b, p.ldb * ES, p.m, c0, p.k);
                 ro_at = lane_across<T, C::BR>(wr);
+                rows.store(s_ids, 0, len);
+                rows.read(kIds, len);
+                __syncthreads();
             } else {
                 // a row that is not there is read as the first that may be: its products are not stored
-                ro.begin([&](int r) {
-                    const int64_t row = s_row[r] < 0 ? 0 : s_row[r];
-                    return (const char*)p.a + row * p.lda * ES;
-                });
+                ro.begin(p.a, p.lda * ES, p.m, [&](int r) { return s_row[r] < 0 ? 0 : s_row[r]; });
                 ro_at = lane_along(wr);
                 if constexpr (MODE == kFwd)
                     co.begin((const char*)p.b + (wg + (int64_t)c0 * p.k) * ES, (int64_t)p.k * ES, p.n - c0);
                 else
-                    co.begin((const char*)p.b + (wg + c0) * ES, (int64_t)p.k * ES, p.k - c0);
+                    co.begin((const char*)p.b + wg * ES, (int64_t)p.k * ES, p.n, c0, p.k);
             }
             if constexpr (MODE == kFwd) co_at = lane_along(C::BR + wc);
-            else co_at = C::BR * 128 + lane_across<T, C::BC>(wc);
-            // the products of the step in `cur`, while the next one's operands come into `nxt`
-            auto step = [&](const char* __restrict cur, char* __restrict nxt, int64_t e0) __attribute__((always_inline)) {
-                const bool more = e0 < len;
-                if (more) {
-                    if constexpr (MODE == kDw) {
-                        ro.load(nxt, e0, len, rows);
-                        co.load(nxt + C::BR * 128, e0, len, rows);
-                        rows.read(e0 + kStep, len);
-                    } else {
-                        ro.load(nxt, e0, len);
-                        if constexpr (MODE == kFwd) co.load(nxt + C::BR * 128, e0, len);
-                        else co.load(nxt + C::BR * 128, e0, len, rows);
-                    }
+            else co_at = kCols + lane_across<T, C::BC>(wc);
+            const int steps = (int)((len + kStep - 1) / kStep);
+            auto load = [&](char* to, const int32_t* ids, int s) __attribute__((always_inline)) {
+                const int64_t e0 = (int64_t)s * kStep;
+                if constexpr (MODE == kDw) {
+                    ids += (int)(e0 % (2 * kIds));
+                    ro.load(to, e0, len, ids);
+                    co.load(to + kCols, e0, len, ids);
+                } else {
+                    ro.load(to, e0, len);
+                    if constexpr (MODE == kFwd) co.load(to + kCols, e0, len);
+                    else co.load(to + kCols, e0, len, ids);
                 }
-                if (busy && e0 > 0) {
-                    const int ra = recompute(ro_at), ca = recompute(co_at);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        Frag<T> fc[C::TC], fr[C::TR];
-#pragma unroll
-                        for (int i = 0; i < C::TC; ++i) {
-                            if constexpr (MODE == kFwd) frag_along<T>(cur, ca, i, half, fc[i]);
-                            else frag_across<C::BC>(cur, ca, i, half, fc[i]);
-                        }
-#pragma unroll
-                        for (int j = 0; j < C::TR; ++j) {
-                            if constexpr (MODE == kDw) frag_across<C::BR>(cur, ra, j, half, fr[j]);
-                            else frag_along<T>(cur, ra, j, half, fr[j]);
-                        }
-#pragma unroll
-                        for (int e = 0; e < kSteps<T>; ++e)
-#pragma unroll
-                            for (int j = 0; j < C::TR; ++j)
-#pragma unroll
-                                for (int i = 0; i < C::TC; ++i) multiply(fc[i], fr[j], e, acc[i][j]);
-                    }
-                    if constexpr (T == kSrcBf16 && C::TR >= 4) {
-                        constexpr int RC = MODE == kFwd ? 1 : 2, RR = MODE == kDw ? 2 : 1;   // reads per piece
-                        __builtin_amdgcn_sched_group_barrier(0x100, C::TC * RC + 2 * RR, 0);
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                            for (int j = 0; j < C::TR; ++j) {
-                                __builtin_amdgcn_sched_group_barrier(0x008, C::TC, 0);
-                                if (j < C::TR - 2) __builtin_amdgcn_sched_group_barrier(0x100, RR, 0);
-                                else if (half == 0) __builtin_amdgcn_sched_group_barrier(0x100, C::TC / 2 * RC + RR, 0);
-                            }
-                        }
-                    }
-                }
-                if (more) {
-                    ro.store(nxt);
-                    co.store(nxt + C::BR * 128);
-                }
-                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-                __syncthreads();
             };
-            int64_t e0 = 0;
-            for (;; e0 += 2 * kStep) {
-                step(lds1, lds0, e0);
-                if (e0 >= len) break;
-                step(lds0, lds1, e0 + kStep);
-                if (e0 + kStep >= len) break;
+            auto store = [&](char* to) __attribute__((always_inline)) {
+                ro.store(to);
+                co.store(to + kCols);
+            };
+            // Held from step to step: the next one's first pieces.
+            constexpr int kHeld = C::TR > 4 ? 3 : 2;
+            struct First { Frag<T> c[C::TC], r[kHeld]; } even, odd;
+            auto row_frag = [&](const char* at, int j, Frag<T>& f) __attribute__((always_inline)) {
+                const int ra = recompute(ro_at);
+                if constexpr (MODE == kDw) frag_across<C::BR>(at, ra, j, f);
+                else frag_along<T>(at, ra, j, f);
+            };
+            auto first_frags = [&](const char* at, First& f) __attribute__((always_inline)) {
+                const int ca = recompute(co_at);
+#pragma unroll
+                for (int i = 0; i < C::TC; ++i) {
+                    if constexpr (MODE == kFwd) frag_along<T>(at, ca, i, f.c[i]);
+                    else frag_across<C::BC>(at, ca, i, f.c[i]);
+                }
+#pragma unroll
+                for (int j = 0; j < kHeld; ++j) row_frag(at, j, f.r[j]);
+            };
+            constexpr int kAhead = ASYNC ? kRing - 1 : 2, kLoads = RowOp::kN + ColOp::kN;
+            // Step s, which lies in `cur`: its products, the next one's first pieces
+            // from `next`, and the loads of a later one under way into `to`.
+            auto step = [&](const char* cur, const char* next, char* to, int s, First& now, First& then)
+                __attribute__((always_inline)) {
+                if (s >= -1) {
+                    // this wave's loads of step s + 1 are in, and then the other waves' are
+                    // (products before this point have what they read from the slot before)
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (ASYNC) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+                    else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                }
+                if constexpr (MODE == kDw) {
+                    // the block of ids after the one that the loads now leave
+                    constexpr int kEvery = kIds / kStep;
+                    if (s >= 0 && s % kEvery == 0 && (int64_t)(s / kEvery + 1) * kIds < len) {
+                        const int64_t e0 = (int64_t)(s / kEvery + 1) * kIds;
+                        rows.store(s_ids + (s / kEvery + 1) % 2 * kIds, e0, len);
+                        rows.read(e0 + kIds, len);
+                    }
+                }
+                // past the last step pieces of zeros: every step has the same loads under way
+                if (ASYNC || s + kAhead < steps) load(to, s_ids, s + kAhead);
+                if (busy && s == -1) {
+                    first_frags(next, then);
+                } else if (busy && s >= 0) {
+                    Frag<T> r[C::TR];
+#pragma unroll
+                    for (int j = kHeld; j < C::TR; ++j) row_frag(cur, j, r[j]);
+                    first_frags(next, then);
+#pragma unroll
+                    for (int e = 0; e < kSteps<T>; ++e)
+#pragma unroll
+                        for (int j = 0; j < C::TR; ++j)
+#pragma unroll
+                            for (int i = 0; i < C::TC; ++i) multiply(now.c[i], j < kHeld ? now.r[j < kHeld ? j : 0] : r[j], e, acc[i][j]);
+                    if constexpr (T == kSrcBf16 && C::TR >= 4) {
+                        // a row piece is read kHeld rows of products ahead; then the next step's first
+                        constexpr int RC = MODE == kFwd ? 1 : 2, RR = MODE == kDw ? 2 : 1;   // reads per piece
+#pragma unroll
+                        for (int j = 0; j < C::TR - kHeld; ++j) {
+                            __builtin_amdgcn_sched_group_barrier(0x100, RR, 0);
+                            __builtin_amdgcn_sched_group_barrier(0x008, C::TC, 0);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kHeld; ++j) {
+                            __builtin_amdgcn_sched_group_barrier(0x100, (C::TC * RC + kHeld * RR + kHeld - 1) / kHeld, 0);
+                            __builtin_amdgcn_sched_group_barrier(0x008, C::TC, 0);
+                        }
+                    }
+                }
+                if (!ASYNC && s + kAhead < steps) store(to);
+            };
+            static_assert(kRing == 4, "step s lies in slot s % 4");
+            if (ASYNC) step(ring1, ring2, ring0, -3, odd, even);
+            step(ring2, ring3, ASYNC ? ring1 : ring0, -2, even, odd);
+            step(ring3, ring0, ASYNC ? ring2 : ring1, -1, odd, even);
+            for (int s = 0;; s += 4) {
+                step(ring0, ring1, ASYNC ? ring3 : ring2, s, even, odd);
+                if (s + 1 >= steps) break;
+                step(ring1, ring2, ASYNC ? ring0 : ring3, s + 1, odd, even);
+                if (s + 2 >= steps) break;
+                step(ring2, ring3, ASYNC ? ring1 : ring0, s + 2, even, odd);
+                if (s + 3 >= steps) break;
+                step(ring3, ring0, ASYNC ? ring2 : ring1, s + 3, odd, even);
+                if (s + 4 >= steps) break;
             }
+            __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0): nothing comes into LDS any more
         }
         if (!busy) continue;
         // lane: output row l % 16, four columns from (l / 16) * 4 on, of each 16 x 16
@@ -669,7 +774,8 @@ template <int MODE, int LP> void launch_resident(const ProdArgs& p, int64_t chun
 template <int MODE> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s) {
     const int cols = MODE == kFwd ? p.n : p.k, es = elem(dtype);
     const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && (int64_t)p.k * es % 16 == 0 &&
-                      (MODE == kFwd || (int64_t)p.n * es % 16 == 0) && aligned(p.b, 16);
+                      (MODE == kFwd || (int64_t)p.n * es % 16 == 0) && aligned(p.b, 16) &&
+                      p.m * p.lda * es <= kBufferBytes && (int64_t)p.n * p.k * es <= kBufferBytes;
     p.out_vec = cols % 4 == 0 && aligned(p.out, p.out_f32 ? 16 : 8);
     const int64_t each = p.m / p.n_groups;
     const int len = MODE == kFwd ? p.k : p.n, lp = len <= 32 ? 1 : len <= 64 ? 2 : len <= 128 ? 4 : 8;
@@ -774,7 +880,8 @@ extern "C" htl_status grouped_mm_backward(const void* dy, int64_t ld_dy, const v
     const ProdArgs p = {dy, x, dw, order, offsets, m, ld_dy, ldx, n, k, n_groups, dw_chunk_rows(m, n, k),
                         (float*)ws, 1, k % 4 == 0 && aligned(dw, 16), dw_chunks(m, n_groups, n, k)};
     const bool fast = ld_dy * es % 16 == 0 && ldx * es % 16 == 0 && aligned(dy, 16) && aligned(x, 16) &&
-                      (int64_t)n * es % 16 == 0 && (int64_t)k * es % 16 == 0;
+                      (int64_t)n * es % 16 == 0 && (int64_t)k * es % 16 == 0 && m * ld_dy * es <= kBufferBytes &&
+                      m * ldx * es <= kBufferBytes;
     if (dtype == HTL_BF16) {
         if (fast && n >= 256 && k >= 256) launch<kSrcBf16, kDw, Big, true>(p, p.limit, stream);
         else if (fast) launch<kSrcBf16, kDw, Mid, true>(p, p.limit, stream);
