@@ -144,8 +144,15 @@ def _check(status: int):
         raise HTLError(status, msg.decode() if msg else "")
 
 
+# The current stream's handle without building a Stream object (0.3 us a call
+# against 2.8, of the 10 or so that a call on a few rows takes).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -171,7 +178,7 @@ def _workspace(tag: str, nbytes: int, device) -> torch.Tensor:
     not race.  A buffer that has to grow is replaced on the stream that uses
     it -- torch's allocator hands freed memory out again only in that
     stream's order -- so no work still queued reads a freed buffer."""
-    key = (tag, str(device), _stream())
+    key = (tag, device.index if isinstance(device, torch.device) else str(device), _stream())
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)

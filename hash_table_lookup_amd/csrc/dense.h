@@ -17,21 +17,39 @@ enum { kSrcF32 = 0, kSrcBf16 = 1, kSrcRows8 = 2 };
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// Rows in device memory.  vec: every row starts 16-byte aligned (8-byte for
-// codes) and holds whole groups of eight elements, so a lane moves its eight
-// at once; otherwise they move one at a time.
+// Rows in device memory, at any alignment of the element: a lane moves eight
+// elements at once wherever they start (the memory system takes a 16-byte
+// access at any byte; rows of odd length ran 4 times slower element by
+// element), and one at a time only past the last whole eight of a row.
 struct RowsIn {
     const void* p;
     const uint8_t* scales;   // 8-bit rows only: [rows][ceil(dim / 32)]
     int64_t ld;              // elements from row to row
     int fmt;                 // 8-bit rows only: HTL_ROWS8_*
-    int vec;
 };
 struct RowsOut {
     void* p;
     int64_t ld;
-    int vec;
 };
+
+// Lanes exchanged without LDS, within 16: x of lane l ^ 1 or l ^ 2 (of a
+// quad), or of the lane that mirrors l in its 8 or 16, which stands for l ^ 4
+// and l ^ 8 where the lanes of a quad, or of 8, hold the same.
+enum { kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140 };
+template <int HOW> __device__ __forceinline__ int move_lanes(int x) {
+    return __builtin_amdgcn_update_dpp(0, x, HOW, 0xF, 0xF, true);
+}
+template <int HOW> __device__ __forceinline__ float add_moved(float x) {
+    return x + __int_as_float(move_lanes<HOW>(__float_as_int(x)));
+}
+
+// A vector at any address that is a multiple of A.
+template <int A, class V> __device__ __forceinline__ void load_at(const void* p, V& v) {
+    __builtin_memcpy(&v, __builtin_assume_aligned(p, A), sizeof(V));
+}
+template <int A, class V> __device__ __forceinline__ void store_at(void* p, const V& v) {
+    __builtin_memcpy(__builtin_assume_aligned(p, A), &v, sizeof(V));
+}
 
 template <int SRC> struct Raw8;
 template <> struct Raw8<kSrcF32> { u32x4 lo, hi; };
@@ -48,12 +66,10 @@ __device__ __forceinline__ u32x4 zeros4() {
 __device__ __forceinline__ void load8(const RowsIn& r, int64_t row, int col, int dim, Raw8<kSrcF32>& o) {
     const float* p = (const float*)r.p + row * r.ld + col;
     o.lo = o.hi = zeros4();
-    if (r.vec) {
-        if (col < dim) {
-            o.lo = *(const u32x4*)p;
-            o.hi = *(const u32x4*)(p + 4);
-        }
-    } else {
+    if (col + 8 <= dim) {
+        load_at<4>(p, o.lo);
+        load_at<4>(p + 4, o.hi);
+    } else if (col < dim) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (col + j < dim) o.lo[j] = __float_as_uint(p[j]);
@@ -64,9 +80,9 @@ __device__ __forceinline__ void load8(const RowsIn& r, int64_t row, int col, int
 __device__ __forceinline__ void load8(const RowsIn& r, int64_t row, int col, int dim, Raw8<kSrcBf16>& o) {
     const uint16_t* p = (const uint16_t*)r.p + row * r.ld + col;
     o.w = zeros4();
-    if (r.vec) {
-        if (col < dim) o.w = *(const u32x4*)p;
-    } else {
+    if (col + 8 <= dim) {
+        load_at<2>(p, o.w);
+    } else if (col < dim) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (col + j < dim) o.w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
@@ -77,9 +93,9 @@ __device__ __forceinline__ void load8(const RowsIn& r, int64_t row, int col, int
     o.c = {0u, 0u};
     o.scale = 0;
     if (col < dim) o.scale = r.scales[row * ((dim + 31) >> 5) + (col >> 5)];
-    if (r.vec) {
-        if (col < dim) o.c = *(const u32x2*)p;
-    } else {
+    if (col + 8 <= dim) {
+        load_at<1>(p, o.c);
+    } else if (col < dim) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (col + j < dim) o.c[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
@@ -130,43 +146,42 @@ __device__ __forceinline__ void unpack8(const RowsIn& r, const Raw8<kSrcRows8>& 
     }
 }
 
+// Rounded to nearest even by the one instruction that converts a pair (the
+// bit arithmetic costs ten, and the norms are bound by instructions).
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const f32x2 f = {lo, hi};
+    const bf16x2 b = __builtin_convertvector(f, bf16x2);
+    uint32_t w;
+    __builtin_memcpy(&w, &b, 4);
+    return w;
 }
 
 template <int DST>
 __device__ __forceinline__ void store8(const RowsOut& r, int64_t row, int col, int dim, const float* v) {
     if (DST == kSrcF32) {
         float* p = (float*)r.p + row * r.ld + col;
-        if (r.vec) {
-            if (col < dim) {
-                u32x4 a, b;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    a[j] = __float_as_uint(v[j]);
-                    b[j] = __float_as_uint(v[4 + j]);
-                }
-                *(u32x4*)p = a;
-                *(u32x4*)(p + 4) = b;
-            }
-        } else {
+        if (col + 8 <= dim) {
+            const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+            store_at<4>(p, a);
+            store_at<4>(p + 4, b);
+        } else if (col < dim) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (col + j < dim) p[j] = v[j];
         }
     } else {
         uint16_t* p = (uint16_t*)r.p + row * r.ld + col;
-        if (r.vec) {
-            if (col < dim) {
-                u32x4 a;
+        u32x4 a;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) a[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-                *(u32x4*)p = a;
-            }
-        } else {
+        for (int j = 0; j < 4; ++j) a[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+        if (col + 8 <= dim) {
+            store_at<2>(p, a);
+        } else if (col < dim) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (col + j < dim) p[j] = (uint16_t)f32_to_bf16_bits(v[j]);
+                if (col + j < dim) p[j] = (uint16_t)(a[j >> 1] >> (16 * (j & 1)));
         }
     }
 }
@@ -176,7 +191,6 @@ struct Rows8Out {
     uint8_t* codes;
     uint8_t* scales;
     int fmt;
-    int vec;
 };
 // Four neighbouring lanes (col = 8 * lane) hold a block of 32 and call this
 // together; columns from dim on hold zeros.
@@ -187,11 +201,10 @@ __device__ __forceinline__ void save8(const Rows8Out& r, int64_t row, int col, i
         const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
         top = a > top ? a : top;
     }
-#pragma unroll
-    for (int off = 1; off < 4; off <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)top, off);
-        top = o > top ? o : top;
-    }
+    uint32_t o = (uint32_t)move_lanes<kXor1>((int)top);
+    top = o > top ? o : top;
+    o = (uint32_t)move_lanes<kXor2>((int)top);
+    top = o > top ? o : top;
     const bool i8 = r.fmt == HTL_ROWS8_I8;
     // top = f * 2^k with f in [1, 2): e = k - 6 while f <= 127/64 (0x7E0000
     // is 127/64's fraction), or k - 8 while f <= 448/256 (0x600000), else one
@@ -204,7 +217,14 @@ __device__ __forceinline__ void save8(const Rows8Out& r, int64_t row, int col, i
     if (finite) {
         if (i8) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) c[j >> 2] |= ((uint32_t)(int)rintf(v[j] * inv) & 0xFFu) << (8 * (j & 3));
+            for (int h = 0; h < 2; ++h) {
+                // 1.5 * 2^23 + q: the sum is rounded to a whole q, to even, and its low byte is q's
+                uint32_t q[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q[j] = __float_as_uint(__builtin_fmaf(v[4 * h + j], inv, 12582912.0f));
+                c[h] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(q[3], q[2], 0x0C0C0400u),
+                                             __builtin_amdgcn_perm(q[1], q[0], 0x0C0C0400u), 0x05040100u);
+            }
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -218,8 +238,8 @@ __device__ __forceinline__ void save8(const Rows8Out& r, int64_t row, int col, i
         if ((col & 31) == 0)
             r.scales[row * ((dim + 31) >> 5) + (col >> 5)] = finite ? (uint8_t)(e + 127) : (uint8_t)255;
         uint8_t* p = r.codes + row * (int64_t)dim + col;
-        if (r.vec) {
-            *(u32x2*)p = c;
+        if (col + 8 <= dim) {
+            store_at<1>(p, c);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -229,41 +249,53 @@ __device__ __forceinline__ void save8(const Rows8Out& r, int64_t row, int col, i
 }
 
 // Eight floats of a parameter row (fp32 [groups][dim]), zeros from dim on.
-__device__ __forceinline__ void load_param(const float* p, bool vec, int g, int col, int dim, float* v) {
-    const float* q = p + (int64_t)g * dim + col;
-    if (vec) {
-        u32x4 a = zeros4(), b = zeros4();
-        if (col < dim) {
-            a = *(const u32x4*)q;
-            b = *(const u32x4*)(q + 4);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = __uint_as_float(a[j]);
-            v[4 + j] = __uint_as_float(b[j]);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = col + j < dim ? q[j] : 0.0f;
-    }
+__device__ __forceinline__ void load_param(const float* p, int g, int col, int dim, float* v) {
+    const RowsIn r = {p, nullptr, dim, 0};
+    Raw8<kSrcF32> raw;
+    load8(r, g, col, dim, raw);
+    unpack8(r, raw, v);
 }
 
 // ---------------------------------------------------- teams of lanes ----
-// Sum over a team of L lanes (L <= 64: aligned lanes of one wave; larger: the
-// whole workgroup of L threads, through LDS), the same in every lane.
-template <int L>
-__device__ __forceinline__ float team_sum(float v, float* s_red) {
+// Sums over a team of L lanes (L <= 64: aligned lanes of one wave; larger: the
+// whole workgroup of L threads, through LDS), the same in every lane.  Two
+// places in LDS take turns, so that one barrier a sum is enough: whoever
+// writes a place again has passed the barrier of the sum between, and with it
+// every wave's reading.
+constexpr int kSumWords = 2 * 2 * 16;
+struct Sums {
+    float* lds;              // kSumWords
+    int turn;
+};
+template <int L, int N> __device__ __forceinline__ void team_sums(float (&v)[N], Sums& s) {
 #pragma unroll
-    for (int off = 1; off < (L < 64 ? L : 64); off <<= 1) v += __shfl_xor(v, off);
-    if (L > 64) {
-        __syncthreads();                 // the previous sum's readers are done
-        if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < L / 64; ++w) v += s_red[w];
+    for (int n = 0; n < N; ++n) {
+        v[n] = add_moved<kXor2>(add_moved<kXor1>(v[n]));
+        if (L >= 8) v[n] = add_moved<kMirror8>(v[n]);
+        if (L >= 16) v[n] = add_moved<kMirror16>(v[n]);
+        if (L >= 32) v[n] += __shfl_xor(v[n], 16);
+        if (L >= 64) v[n] += __shfl_xor(v[n], 32);
     }
-    return v;
+    if (L > 64) {
+        float* at = s.lds + s.turn * 32;
+        s.turn ^= 1;
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) at[n * 16 + (threadIdx.x >> 6)] = v[n];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            v[n] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < L / 64; ++w) v[n] += at[n * 16 + w];
+        }
+    }
+}
+template <int L> __device__ __forceinline__ float team_sum(float v, Sums& s) {
+    float a[1] = {v};
+    team_sums<L>(a, s);
+    return a[0];
 }
 
 // How a row is held: L lanes with I groups of eight elements each, so a row of
@@ -273,43 +305,59 @@ template <int L_, int I_> struct Hold {
     static constexpr int L = L_, I = I_;
     static constexpr int kThreads = L_ > 64 ? L_ : 256;
     static constexpr int kTeams = kThreads / L_;
+    // A workgroup that is one team waits at barriers, and few such fit: the
+    // next row's loads run ahead.  Waves that hold rows of their own hide one
+    // another's waiting better than they could with the registers for that
+    // (dim 128: 441 us without, 517 with, in norm_rows_backward of 1.7M rows).
+    static constexpr bool kAhead = L_ > 64;
+    static constexpr int kGrid = kAhead ? 524288 / kThreads : 1 << 20;   // workgroups of a launch at most
+    static constexpr int kChunks = kAhead ? 262144 / kThreads : 2048;    // chunks of rows, about
 };
 // Calls f with the smallest Hold for a row of dim elements (<= kMaxNormDim).
 template <class F> void with_hold(int dim, F&& f) {
-    if (dim <= 64) f(Hold<8, 1>());
+    if (dim <= 32) f(Hold<4, 1>());
+    else if (dim <= 64) f(Hold<8, 1>());
     else if (dim <= 128) f(Hold<16, 1>());
     else if (dim <= 256) f(Hold<32, 1>());
     else if (dim <= 512) f(Hold<64, 1>());
     else if (dim <= 1024) f(Hold<64, 2>());
-    else if (dim <= 2048) f(Hold<64, 4>());
-    else if (dim <= 4096) f(Hold<256, 2>());
-    else if (dim <= 8192) f(Hold<256, 4>());
-    else f(Hold<512, 4>());
+    else if (dim <= 2048) f(Hold<256, 1>());
+    else if (dim <= 4096) f(Hold<512, 1>());
+    else if (dim <= 8192) f(Hold<1024, 1>());
+    else f(Hold<1024, 2>());
 }
 
 // 1 / deviation and, in v, the centred and scaled row: v <- (v - [mean]) * r.
 // The mean is taken out before the squares are summed, both in fp32: a row
 // far from zero keeps its deviation.
 template <class H>
-__device__ __forceinline__ float normalize(float v[][8], bool center, int tl, int dim, float eps, float* s_red) {
+__device__ __forceinline__ float normalize(float v[][8], bool center, int tl, int dim, float eps, Sums& sums) {
     if (center) {
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < H::I; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) s += v[i][j];
-        const float mean = team_sum<H::L>(s, s_red) / (float)dim;   // divided: exact for a constant row
+        const float mean = team_sum<H::L>(s, sums) / (float)dim;   // divided: exact for a constant row
 #pragma unroll
-        for (int i = 0; i < H::I; ++i)
+        for (int i = 0; i < H::I; ++i) {
+            const int col = (i * H::L + tl) * 8;
+            const float mid = col < dim ? mean : 0.0f;             // columns past the row stay zeros
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = (i * H::L + tl) * 8 + j < dim ? v[i][j] - mean : 0.0f;
+            for (int j = 0; j < 8; ++j) v[i][j] -= mid;
+            if (dim % 8 != 0 && col + 8 > dim) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (col + j >= dim) v[i][j] = 0.0f;
+            }
+        }
     }
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < H::I; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) q += v[i][j] * v[i][j];
-    const float r = 1.0f / sqrtf(team_sum<H::L>(q, s_red) / (float)dim + eps);
+    const float r = 1.0f / sqrtf(team_sum<H::L>(q, sums) / (float)dim + eps);
 #pragma unroll
     for (int i = 0; i < H::I; ++i)
 #pragma unroll
@@ -322,7 +370,7 @@ __device__ __forceinline__ float normalize(float v[][8], bool center, int tl, in
 // first, then the waves through s_col (kThreads / 64 rows of 8 * L * I
 // floats; none needed when one team fills the workgroup).
 template <class H>
-__device__ __forceinline__ void write_columns(float acc[][8], int tl, int dim, bool vec, float* s_col, float* dst) {
+__device__ __forceinline__ void write_columns(float acc[][8], int tl, int dim, float* s_col, float* dst) {
     constexpr int kWaves = H::kThreads / 64;
     if (H::L <= 64) {
 #pragma unroll
@@ -346,7 +394,7 @@ __device__ __forceinline__ void write_columns(float acc[][8], int tl, int dim, b
             dst[d] = s;
         }
     } else {
-        const RowsOut o = {dst, 0, vec};
+        const RowsOut o = {dst, 0};
 #pragma unroll
         for (int i = 0; i < H::I; ++i) store8<kSrcF32>(o, 0, (i * H::L + tl) * 8, dim, acc[i]);
     }
@@ -432,10 +480,6 @@ __device__ __forceinline__ void chunks_of_group(const int32_t* offsets, int n_gr
     group_range(offsets, n_groups, m, g, beg, end);
     count = (int)(((uint32_t)(end - beg) + R - 1u) / R);
     if (count < min_chunks) count = min_chunks;
-}
-
-inline bool vec_ok(const void* p, int64_t ld, int dim, int elem) {
-    return dim % 8 == 0 && (ld * elem) % 16 == 0 && aligned(p, 16);
 }
 
 // Sums of a group's partial rows: out[g][d] = sum over its chunks of

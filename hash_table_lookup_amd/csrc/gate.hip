@@ -44,25 +44,25 @@ struct GateArgs {
     const float* bias;       // nullable
     const int32_t* ids;      // nullable: one group
     int64_t m;
-    int dim, n_groups, pvec, act;
+    int dim, n_groups, act;
     float eps, scale;
     bool center;
 };
 
 template <class H, int TX, int TZ>
 __global__ __launch_bounds__(H::kThreads) void k_gate(GateArgs a) {
-    __shared__ float s_red[8];
+    __shared__ float s_sum[kSumWords];
+    Sums sums = {s_sum, 0};
     const int tl = threadIdx.x % H::L;
     const int64_t teams = (int64_t)gridDim.x * H::kTeams;
-    for (int64_t row0 = (int64_t)blockIdx.x * H::kTeams; row0 < a.m; row0 += teams) {
-        const int64_t row = row0 + threadIdx.x / H::L;
-        const bool in = row < a.m;
-        const int64_t r = in ? row : a.m - 1;
-        const int g = a.ids ? a.ids[r] : 0;
-        const bool grouped = (uint32_t)g < (uint32_t)a.n_groups;
-        Raw8<TZ> rz[H::I], ru[H::I];
-        Raw8<TX> rx[H::I];
-        float v[H::I][8];
+    int64_t row0 = (int64_t)blockIdx.x * H::kTeams;
+    if (row0 >= a.m) return;
+    Raw8<TZ> rz[H::I], ru[H::I];
+    Raw8<TX> rx[H::I];
+    int g;
+    auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+        const int64_t r = row < a.m ? row : a.m - 1;
+        g = a.ids ? a.ids[r] : 0;
 #pragma unroll
         for (int i = 0; i < H::I; ++i) {
             const int col = (i * H::L + tl) * 8;
@@ -70,35 +70,49 @@ __global__ __launch_bounds__(H::kThreads) void k_gate(GateArgs a) {
             load8(a.u, r, col, a.dim, ru[i]);
             load8(a.x, r, col, a.dim, rx[i]);
         }
+    };
+    if (H::kAhead) fetch(row0 + threadIdx.x / H::L);
+    for (; row0 < a.m; row0 += teams) {
+        const int64_t row = row0 + threadIdx.x / H::L;
+        const bool in = row < a.m;
+        if (!H::kAhead) fetch(row);
+        const bool grouped = (uint32_t)g < (uint32_t)a.n_groups;
+        float v[H::I][8], w[H::I][8], b[H::I][8], u[H::I][8];
+        Raw8<TX> xs[H::I];
 #pragma unroll
-        for (int i = 0; i < H::I; ++i) unpack8(a.z, rz[i], v[i]);
+        for (int i = 0; i < H::I; ++i) {
+            const int col = (i * H::L + tl) * 8;
+            load_param(a.weight, grouped ? g : 0, col, a.dim, w[i]);
+            if (a.bias) load_param(a.bias, grouped ? g : 0, col, a.dim, b[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < H::I; ++i) {
+            unpack8(a.z, rz[i], v[i]);
+            unpack8(a.u, ru[i], u[i]);
+            xs[i] = rx[i];
+        }
+        if (H::kAhead && row0 + teams < a.m) fetch(row + teams);
         if (a.save_z.codes) {
 #pragma unroll
             for (int i = 0; i < H::I; ++i) {
                 const int col = in ? (i * H::L + tl) * 8 : a.dim;
-                float u[8];
-                unpack8(a.u, ru[i], u);
-                save8(a.save_z, r, col, a.dim, v[i]);
-                save8(a.save_u, r, col, a.dim, u);
+                save8(a.save_z, in ? row : 0, col, a.dim, v[i]);
+                save8(a.save_u, in ? row : 0, col, a.dim, u[i]);
             }
         }
-        normalize<H>(v, a.center, tl, a.dim, a.eps, s_red);
+        normalize<H>(v, a.center, tl, a.dim, a.eps, sums);
 #pragma unroll
         for (int i = 0; i < H::I; ++i) {
-            const int col = (i * H::L + tl) * 8;
-            float w[8], b[8], u[8], x[8];
-            load_param(a.weight, a.pvec, grouped ? g : 0, col, a.dim, w);
-            if (a.bias) load_param(a.bias, a.pvec, grouped ? g : 0, col, a.dim, b);
-            unpack8(a.u, ru[i], u);
-            unpack8(a.x, rx[i], x);
+            float x[8];
+            unpack8(a.x, xs[i], x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float y = v[i][j] * w[j], slope;
-                if (a.bias) y += b[j];
-                y = a.scale * gate_act(u[j], a.act, slope) * y;
+                float y = v[i][j] * w[i][j], slope;
+                if (a.bias) y += b[i][j];
+                y = a.scale * gate_act(u[i][j], a.act, slope) * y;
                 v[i][j] = grouped ? x[j] + y : x[j];
             }
-            if (in) store8<TX>(a.out, row, col, a.dim, v[i]);
+            if (in) store8<TX>(a.out, row, (i * H::L + tl) * 8, a.dim, v[i]);
         }
     }
 }
@@ -115,7 +129,7 @@ struct GateBackArgs {
     float* partial;          // [chunks][dim], dbias's after dweight's
     int64_t chunks;
     int64_t m;
-    int dim, n_groups, pvec, gvec, act;
+    int dim, n_groups, act;
     uint32_t rows;           // positions per chunk
     float eps, scale;
     bool center;
@@ -123,85 +137,100 @@ struct GateBackArgs {
 
 template <class H, int TD, int TZ, int TG>
 __global__ __launch_bounds__(H::kThreads) void k_gate_back(GateBackArgs a) {
-    __shared__ float s_red[8];
+    __shared__ float s_sum[kSumWords];
     __shared__ float s_col[H::L <= 64 ? (H::kThreads / 64) * H::I * H::L * 8 : 1];
+    Sums sums = {s_sum, 0};
     const int tl = threadIdx.x % H::L;
     const float inv_dim = 1.0f / (float)a.dim;
     Chunk c;
     if (!find_chunk(a.offsets, a.n_groups, a.m, a.rows, 1, blockIdx.x, c)) return;
     const bool grouped = c.g < a.n_groups;
     float w[H::I][8], b[H::I][8], sw[H::I][8], sb[H::I][8];
+    int64_t row = -1, next = -1;
+    Raw8<TZ> rz[H::I], ru[H::I];
+    Raw8<TD> rd[H::I];
+    auto place = [&](int64_t p) {
+        const int64_t r = p < c.end ? (a.order ? a.order[p] : p) : -1;
+        return r < a.m ? r : -1;
+    };
+    auto fetch = [&](int64_t r) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < H::I; ++i) {
+            const int col = r >= 0 ? (i * H::L + tl) * 8 : a.dim;
+            load8(a.z, r < 0 ? 0 : r, col, a.dim, rz[i]);
+            load8(a.u, r < 0 ? 0 : r, col, a.dim, ru[i]);
+            load8(a.dout, r < 0 ? 0 : r, col, a.dim, rd[i]);
+        }
+    };
+    const int64_t first_p = c.beg + threadIdx.x / H::L;
+    row = place(first_p);
+    next = place(first_p + H::kTeams);
+    if (H::kAhead) fetch(row);
 #pragma unroll
     for (int i = 0; i < H::I; ++i) {
         const int col = (i * H::L + tl) * 8;
-        load_param(a.weight, a.pvec, grouped ? c.g : 0, col, a.dim, w[i]);
+        load_param(a.weight, grouped ? c.g : 0, col, a.dim, w[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sw[i][j] = sb[i][j] = b[i][j] = 0.0f;
-        if (a.bias) load_param(a.bias, a.pvec, grouped ? c.g : 0, col, a.dim, b[i]);
+        if (a.bias) load_param(a.bias, grouped ? c.g : 0, col, a.dim, b[i]);
     }
     for (int64_t p0 = c.beg; p0 < c.end; p0 += H::kTeams) {
-        const int64_t p = p0 + threadIdx.x / H::L;
-        int64_t row = p < c.end ? (a.order ? a.order[p] : p) : -1;
-        const bool in = row >= 0 && row < a.m;
-        if (!in) row = 0;
-        Raw8<TZ> rz[H::I], ru[H::I];
-        Raw8<TD> rd[H::I];
-        float v[H::I][8], d[H::I][8];
-#pragma unroll
-        for (int i = 0; i < H::I; ++i) {
-            const int col = in ? (i * H::L + tl) * 8 : a.dim;
-            load8(a.z, row, col, a.dim, rz[i]);
-            load8(a.u, row, col, a.dim, ru[i]);
-            load8(a.dout, row, col, a.dim, rd[i]);
-        }
+        const bool in = row >= 0;
+        const int64_t at = row;
+        if (!H::kAhead) fetch(row);
+        float v[H::I][8], d[H::I][8], u[H::I][8];
 #pragma unroll
         for (int i = 0; i < H::I; ++i) {
             unpack8(a.z, rz[i], v[i]);
+            unpack8(a.u, ru[i], u[i]);
             unpack8(a.dout, rd[i], d[i]);
         }
-        const float r = normalize<H>(v, a.center, tl, a.dim, a.eps, s_red);
-        float c1 = 0.0f, c2 = 0.0f;
+        row = next;
+        if (p0 + H::kTeams < c.end) {
+            if (H::kAhead) fetch(row);
+            next = place(p0 + 2 * H::kTeams + threadIdx.x / H::L);
+        }
+        const float r = normalize<H>(v, a.center, tl, a.dim, a.eps, sums);
+        float c12[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < H::I; ++i) {
-            float u[8], du[8];
-            unpack8(a.u, ru[i], u);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 float slope;
-                const float D = a.scale * d[i][j], act = gate_act(u[j], a.act, slope), e = D * act;
-                du[j] = grouped ? D * slope * (v[i][j] * w[i][j] + b[i][j]) : 0.0f;
+                const float D = a.scale * d[i][j], act = gate_act(u[i][j], a.act, slope), e = D * act;
+                u[i][j] = grouped ? D * slope * (v[i][j] * w[i][j] + b[i][j]) : 0.0f;
                 if (in) {                // a row left out must not bring a NaN
                     sw[i][j] += e * v[i][j];
                     sb[i][j] += e;
                 }
                 d[i][j] = e * w[i][j];
-                c1 += d[i][j];
-                c2 += d[i][j] * v[i][j];
+                c12[0] += d[i][j];
+                c12[1] += d[i][j] * v[i][j];
             }
-            if (in) store8<TG>(a.du, row, (i * H::L + tl) * 8, a.dim, du);
+            if (in) store8<TG>(a.du, at, (i * H::L + tl) * 8, a.dim, u[i]);
         }
-        c1 = a.center ? team_sum<H::L>(c1, s_red) * inv_dim : 0.0f;
-        c2 = team_sum<H::L>(c2, s_red) * inv_dim;
+        team_sums<H::L>(c12, sums);
+        const float c1 = a.center ? c12[0] * inv_dim : 0.0f, c2 = c12[1] * inv_dim;
 #pragma unroll
         for (int i = 0; i < H::I; ++i) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) d[i][j] = grouped ? r * (d[i][j] - c1 - v[i][j] * c2) : 0.0f;
-            if (in) store8<TG>(a.dz, row, (i * H::L + tl) * 8, a.dim, d[i]);
+            if (in) store8<TG>(a.dz, at, (i * H::L + tl) * 8, a.dim, d[i]);
         }
     }
     if (!grouped) return;
     const bool alone = c.count == 1;
     const int64_t first = (int64_t)blockIdx.x * a.dim, whole = (int64_t)c.g * a.dim;
-    write_columns<H>(sw, tl, a.dim, a.gvec, s_col, alone ? a.dweight + whole : a.partial + first);
+    write_columns<H>(sw, tl, a.dim, s_col, alone ? a.dweight + whole : a.partial + first);
     if (a.dbias)
-        write_columns<H>(sb, tl, a.dim, a.gvec, s_col, alone ? a.dbias + whole : a.partial + a.chunks * a.dim + first);
+        write_columns<H>(sb, tl, a.dim, s_col, alone ? a.dbias + whole : a.partial + a.chunks * a.dim + first);
 }
 
 int elem(htl_dtype t) { return t == HTL_F32 ? 4 : 2; }
 bool known(htl_dtype t) { return t == HTL_F32 || t == HTL_BF16; }
 
 template <class H, int TX, int TZ> void launch_gate(const GateArgs& a, hipStream_t s) {
-    const dim3 grid(grid_for(a.m, H::kTeams, 1 << 16)), block(H::kThreads);
+    const dim3 grid(grid_for(a.m, H::kTeams, H::kGrid)), block(H::kThreads);
     hipLaunchKernelGGL((k_gate<H, TX, TZ>), grid, block, 0, s, a);
 }
 
@@ -241,19 +270,18 @@ extern "C" htl_status norm_gate(const void* x, htl_dtype x_dtype, int64_t ldx, c
                     aligned(bias, 4) && aligned(ids, 4),
                 "norm_gate: misaligned pointer");
     GateArgs a;
-    a.x = {x, nullptr, ldx, 0, vec_ok(x, ldx, dim, xe)};
-    a.z = {z, nullptr, ldz, 0, vec_ok(z, ldz, dim, ze)};
-    a.u = {u, nullptr, ldu, 0, vec_ok(u, ldu, dim, ze)};
-    a.out = {out, dim, vec_ok(out, dim, dim, xe)};
-    a.save_z = {z_codes, z_scales, (int)fmt, dim % 8 == 0 && aligned(z_codes, 8)};
-    a.save_u = {u_codes, u_scales, (int)fmt, dim % 8 == 0 && aligned(u_codes, 8)};
+    a.x = {x, nullptr, ldx, 0};
+    a.z = {z, nullptr, ldz, 0};
+    a.u = {u, nullptr, ldu, 0};
+    a.out = {out, dim};
+    a.save_z = {z_codes, z_scales, (int)fmt};
+    a.save_u = {u_codes, u_scales, (int)fmt};
     a.weight = weight;
     a.bias = bias;
     a.ids = ids;
     a.m = m;
     a.dim = dim;
     a.n_groups = n_groups;
-    a.pvec = vec_ok(weight, dim, dim, 4) && aligned(bias, 16);
     a.act = (int)act;
     a.eps = eps;
     a.center = kind == HTL_NORM_LAYER;
@@ -299,11 +327,11 @@ extern "C" htl_status norm_gate_backward(const void* dout, htl_dtype dout_dtype,
     HTL_REQUIRE(ws && aligned(ws, 256) && ws_bytes >= norm_back_workspace_bytes(m, n_groups, dim),
                 "norm_gate_backward: workspace too small or misaligned");
     GateBackArgs a;
-    a.dout = {dout, nullptr, ld_dout, 0, vec_ok(dout, ld_dout, dim, de)};
-    a.z = {z, z_scales, ldz, (int)fmt, q ? (dim % 8 == 0 && ldz % 8 == 0 && aligned(z, 8)) : vec_ok(z, ldz, dim, ze)};
-    a.u = {u, u_scales, ldu, (int)fmt, q ? (dim % 8 == 0 && ldu % 8 == 0 && aligned(u, 8)) : vec_ok(u, ldu, dim, ze)};
-    a.dz = {dz, dim, vec_ok(dz, dim, dim, ge)};
-    a.du = {du, dim, vec_ok(du, dim, dim, ge)};
+    a.dout = {dout, nullptr, ld_dout, 0};
+    a.z = {z, z_scales, ldz, (int)fmt};
+    a.u = {u, u_scales, ldu, (int)fmt};
+    a.dz = {dz, dim};
+    a.du = {du, dim};
     a.weight = weight;
     a.bias = bias;
     a.order = order;
@@ -316,8 +344,6 @@ extern "C" htl_status norm_gate_backward(const void* dout, htl_dtype dout_dtype,
     a.m = m;
     a.dim = dim;
     a.n_groups = n_groups;
-    a.pvec = vec_ok(weight, dim, dim, 4) && aligned(bias, 16);
-    a.gvec = vec_ok(dweight, dim, dim, 4) && aligned(dbias, 16);
     a.act = (int)act;
     a.eps = eps;
     a.center = kind == HTL_NORM_LAYER;

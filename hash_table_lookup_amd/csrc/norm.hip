@@ -22,46 +22,59 @@ struct NormArgs {
     const float* bias;       // nullable
     const int32_t* ids;      // nullable: one group
     int64_t m;
-    int dim, n_groups, pvec;
+    int dim, n_groups;
     float eps;
     bool center;
 };
 
+// A team per row.
 template <class H, int TX, int TY>
 __global__ __launch_bounds__(H::kThreads) void k_norm(NormArgs a) {
-    __shared__ float s_red[8];
+    __shared__ float s_sum[kSumWords];
+    Sums sums = {s_sum, 0};
     const int tl = threadIdx.x % H::L;
     const int64_t teams = (int64_t)gridDim.x * H::kTeams;
-    for (int64_t row0 = (int64_t)blockIdx.x * H::kTeams; row0 < a.m; row0 += teams) {
-        const int64_t row = row0 + threadIdx.x / H::L;
-        const bool in = row < a.m;       // lanes of a wave stay together for the sums
-        const int64_t r = in ? row : a.m - 1;
-        const int g = a.ids ? a.ids[r] : 0;
-        const bool grouped = (uint32_t)g < (uint32_t)a.n_groups;
-        Raw8<TX> raw[H::I];
-        float v[H::I][8];
+    int64_t row0 = (int64_t)blockIdx.x * H::kTeams;
+    if (row0 >= a.m) return;
+    Raw8<TX> raw[H::I];
+    int g;
+    auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+        const int64_t r = row < a.m ? row : a.m - 1;    // lanes of a wave stay together for the sums
+        g = a.ids ? a.ids[r] : 0;
 #pragma unroll
         for (int i = 0; i < H::I; ++i) load8(a.x, r, (i * H::L + tl) * 8, a.dim, raw[i]);
-#pragma unroll
-        for (int i = 0; i < H::I; ++i) unpack8(a.x, raw[i], v[i]);
-        if (a.save.codes) {
-#pragma unroll
-            for (int i = 0; i < H::I; ++i) save8(a.save, r, in ? (i * H::L + tl) * 8 : a.dim, a.dim, v[i]);
-        }
-        normalize<H>(v, a.center, tl, a.dim, a.eps, s_red);
+    };
+    if (H::kAhead) fetch(row0 + threadIdx.x / H::L);
+    for (; row0 < a.m; row0 += teams) {
+        const int64_t row = row0 + threadIdx.x / H::L;
+        const bool in = row < a.m;
+        if (!H::kAhead) fetch(row);
+        const bool grouped = (uint32_t)g < (uint32_t)a.n_groups;
+        float v[H::I][8], w[H::I][8], b[H::I][8];
 #pragma unroll
         for (int i = 0; i < H::I; ++i) {
             const int col = (i * H::L + tl) * 8;
-            float w[8], b[8];
-            load_param(a.weight, a.pvec, grouped ? g : 0, col, a.dim, w);
-            if (a.bias) load_param(a.bias, a.pvec, grouped ? g : 0, col, a.dim, b);
+            load_param(a.weight, grouped ? g : 0, col, a.dim, w[i]);
+            if (a.bias) load_param(a.bias, grouped ? g : 0, col, a.dim, b[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < H::I; ++i) unpack8(a.x, raw[i], v[i]);
+        if (H::kAhead && row0 + teams < a.m) fetch(row + teams);
+        if (a.save.codes) {
+#pragma unroll
+            for (int i = 0; i < H::I; ++i)
+                save8(a.save, in ? row : 0, in ? (i * H::L + tl) * 8 : a.dim, a.dim, v[i]);
+        }
+        normalize<H>(v, a.center, tl, a.dim, a.eps, sums);
+#pragma unroll
+        for (int i = 0; i < H::I; ++i) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float y = v[i][j] * w[j];
-                if (a.bias) y += b[j];
+                float y = v[i][j] * w[i][j];
+                if (a.bias) y += b[i][j];
                 v[i][j] = grouped ? y : 0.0f;
             }
-            if (in) store8<TY>(a.y, row, col, a.dim, v[i]);
+            if (in) store8<TY>(a.y, row, (i * H::L + tl) * 8, a.dim, v[i]);
         }
     }
 }
@@ -77,53 +90,72 @@ struct NormBackArgs {
     float* partial;          // [chunks][dim], dbias's after dweight's
     int64_t chunks;
     int64_t m;
-    int dim, n_groups, pvec, gvec;
+    int dim, n_groups;
     uint32_t rows;           // positions per chunk
     float eps;
     bool center;
 };
 
 // One workgroup per chunk of a group's rows, so the group's weights and the
-// column sums stay in registers over the chunk.
+// column sums stay in registers over the chunk.  A row's place in order is
+// read a row ahead.
 template <class H, int TD, int TX, int TR>
 __global__ __launch_bounds__(H::kThreads) void k_norm_back(NormBackArgs a) {
-    __shared__ float s_red[8];
+    __shared__ float s_sum[kSumWords];
     __shared__ float s_col[H::L <= 64 ? (H::kThreads / 64) * H::I * H::L * 8 : 1];
+    Sums sums = {s_sum, 0};
     const int tl = threadIdx.x % H::L;
     const float inv_dim = 1.0f / (float)a.dim;
     Chunk c;
     if (!find_chunk(a.offsets, a.n_groups, a.m, a.rows, 1, blockIdx.x, c)) return;
     const bool grouped = c.g < a.n_groups;
     float w[H::I][8], sw[H::I][8], sb[H::I][8];
+    int64_t row = -1, next = -1;
+    Raw8<TX> rx[H::I];
+    Raw8<TD> rd[H::I];
+    Raw8<TR> rr[H::I];
+    auto place = [&](int64_t p) {
+        const int64_t r = p < c.end ? (a.order ? a.order[p] : p) : -1;
+        return r < a.m ? r : -1;
+    };
+    auto fetch = [&](int64_t r) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < H::I; ++i) {
+            const int col = r >= 0 ? (i * H::L + tl) * 8 : a.dim;
+            load8(a.x, r < 0 ? 0 : r, col, a.dim, rx[i]);
+            load8(a.dy, r < 0 ? 0 : r, col, a.dim, rd[i]);
+            if (a.dres.p) load8(a.dres, r < 0 ? 0 : r, col, a.dim, rr[i]);
+        }
+    };
+    const int64_t first_p = c.beg + threadIdx.x / H::L;
+    row = place(first_p);
+    next = place(first_p + H::kTeams);
+    if (H::kAhead) fetch(row);
 #pragma unroll
     for (int i = 0; i < H::I; ++i) {
-        load_param(a.weight, a.pvec, grouped ? c.g : 0, (i * H::L + tl) * 8, a.dim, w[i]);
+        load_param(a.weight, grouped ? c.g : 0, (i * H::L + tl) * 8, a.dim, w[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sw[i][j] = sb[i][j] = 0.0f;
     }
     for (int64_t p0 = c.beg; p0 < c.end; p0 += H::kTeams) {
-        const int64_t p = p0 + threadIdx.x / H::L;
-        int64_t row = p < c.end ? (a.order ? a.order[p] : p) : -1;
-        const bool in = row >= 0 && row < a.m;
-        if (!in) row = 0;
-        Raw8<TX> rx[H::I];
-        Raw8<TD> rd[H::I];
-        Raw8<TR> rr[H::I];
+        const bool in = row >= 0;
+        const int64_t at = row;
+        if (!H::kAhead) fetch(row);
         float v[H::I][8], d[H::I][8];
-#pragma unroll
-        for (int i = 0; i < H::I; ++i) {
-            const int col = in ? (i * H::L + tl) * 8 : a.dim;
-            load8(a.x, row, col, a.dim, rx[i]);
-            load8(a.dy, row, col, a.dim, rd[i]);
-            if (a.dres.p) load8(a.dres, row, col, a.dim, rr[i]);
-        }
+        Raw8<TR> res[H::I];
 #pragma unroll
         for (int i = 0; i < H::I; ++i) {
             unpack8(a.x, rx[i], v[i]);
             unpack8(a.dy, rd[i], d[i]);
+            res[i] = rr[i];
         }
-        const float r = normalize<H>(v, a.center, tl, a.dim, a.eps, s_red);
-        float c1 = 0.0f, c2 = 0.0f;
+        row = next;
+        if (p0 + H::kTeams < c.end) {
+            if (H::kAhead) fetch(row);
+            next = place(p0 + 2 * H::kTeams + threadIdx.x / H::L);
+        }
+        const float r = normalize<H>(v, a.center, tl, a.dim, a.eps, sums);
+        float c12[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < H::I; ++i)
 #pragma unroll
@@ -133,29 +165,29 @@ __global__ __launch_bounds__(H::kThreads) void k_norm_back(NormBackArgs a) {
                     sb[i][j] += d[i][j];
                 }
                 d[i][j] *= w[i][j];
-                c1 += d[i][j];
-                c2 += d[i][j] * v[i][j];
+                c12[0] += d[i][j];
+                c12[1] += d[i][j] * v[i][j];
             }
-        c1 = a.center ? team_sum<H::L>(c1, s_red) * inv_dim : 0.0f;
-        c2 = team_sum<H::L>(c2, s_red) * inv_dim;
+        team_sums<H::L>(c12, sums);
+        const float c1 = a.center ? c12[0] * inv_dim : 0.0f, c2 = c12[1] * inv_dim;
 #pragma unroll
         for (int i = 0; i < H::I; ++i) {
-            float res[8];
-            if (a.dres.p) unpack8(a.dres, rr[i], res);
+            float add[8];
+            if (a.dres.p) unpack8(a.dres, res[i], add);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float g = grouped ? r * (d[i][j] - c1 - v[i][j] * c2) : 0.0f;
-                d[i][j] = a.dres.p ? res[j] + g : g;
+                const float g = grouped ? r * (d[i][j] - c1 - v[i][j] * c2) : 0.0f;   // (the same for the whole chunk)
+                d[i][j] = a.dres.p ? add[j] + g : g;
             }
-            if (in) store8<TR>(a.dx, row, (i * H::L + tl) * 8, a.dim, d[i]);
+            if (in) store8<TR>(a.dx, at, (i * H::L + tl) * 8, a.dim, d[i]);
         }
     }
     if (!grouped) return;
     const bool alone = c.count == 1;
     const int64_t first = (int64_t)blockIdx.x * a.dim, whole = (int64_t)c.g * a.dim;
-    write_columns<H>(sw, tl, a.dim, a.gvec, s_col, alone ? a.dweight + whole : a.partial + first);
+    write_columns<H>(sw, tl, a.dim, s_col, alone ? a.dweight + whole : a.partial + first);
     if (a.dbias)
-        write_columns<H>(sb, tl, a.dim, a.gvec, s_col, alone ? a.dbias + whole : a.partial + a.chunks * a.dim + first);
+        write_columns<H>(sb, tl, a.dim, s_col, alone ? a.dbias + whole : a.partial + a.chunks * a.dim + first);
 }
 
 // 64 columns per workgroup; its 16 waves take every 16th chunk of the group.
@@ -216,14 +248,15 @@ __global__ __launch_bounds__(256) void k_sum_wide(const float* __restrict__ part
     }
 }
 
-// Positions per chunk: about kChunks chunks in all, at least four rows for
-// each team.
-constexpr int64_t kChunks = 2048;
+// Positions per chunk: about H::kChunks chunks, at least four rows for each team.
 uint32_t norm_chunk_rows(int64_t m, int dim) {
-    int teams = 1;
-    with_hold(dim, [&](auto h) { teams = decltype(h)::kTeams; });
-    int64_t r = ceil_div(m, teams > 1 ? kChunks : kChunks / 2);
-    return (uint32_t)(r < teams * 4 ? teams * 4 : r);
+    int64_t r = 0;
+    with_hold(dim, [&](auto h) {
+        using H = decltype(h);
+        r = ceil_div(m, H::kChunks);
+        if (r < H::kTeams * 4) r = H::kTeams * 4;
+    });
+    return (uint32_t)r;
 }
 
 }  // namespace
@@ -234,7 +267,7 @@ uint32_t norm_rows_per_chunk(int64_t m, int dim) { return norm_chunk_rows(m, dim
 htl_status sum_chunks(const float* partial, int64_t limit, float* out, const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
                       int64_t width, hipStream_t stream) {
     if (m <= (int64_t)R) return HTL_OK;      // every group is one chunk
-    if (width >= 4096) {
+    if (width >= 65536) {
         const int64_t blocks = ceil_div(width, 1024), most = ceil_div(4096, n_groups);
         hipLaunchKernelGGL(k_sum_wide, dim3((unsigned)(blocks < most ? blocks : most), (unsigned)n_groups), dim3(256), 0,
                            stream, partial, limit, out, offsets, n_groups, m, R, width);
@@ -256,7 +289,7 @@ int elem(htl_dtype t) { return t == HTL_F32 ? 4 : 2; }
 bool known(htl_dtype t) { return t == HTL_F32 || t == HTL_BF16; }
 
 template <class H> void launch_norm(const NormArgs& a, int tx, int ty, hipStream_t s) {
-    const dim3 grid(grid_for(a.m, H::kTeams, 1 << 16)), block(H::kThreads);
+    const dim3 grid(grid_for(a.m, H::kTeams, H::kGrid)), block(H::kThreads);
 #define NORM_CASE(TX, TY) hipLaunchKernelGGL((k_norm<H, TX, TY>), grid, block, 0, s, a)
     if (tx == kSrcF32 && ty == kSrcF32) NORM_CASE(kSrcF32, kSrcF32);
     else if (tx == kSrcF32) NORM_CASE(kSrcF32, kSrcBf16);
@@ -299,17 +332,15 @@ extern "C" htl_status norm_rows(const void* x, htl_dtype x_dtype, int64_t ldx, c
     HTL_REQUIRE(aligned(x, xe) && aligned(y, ye) && aligned(weight, 4) && aligned(bias, 4) && aligned(ids, 4),
                 "norm_rows: misaligned pointer");
     NormArgs a;
-    a.x = {x, x_scales, ldx, (int)x_fmt,
-           x_scales ? (dim % 8 == 0 && ldx % 8 == 0 && aligned(x, 8)) : vec_ok(x, ldx, dim, xe)};
-    a.y = {y, dim, vec_ok(y, dim, dim, ye)};
-    a.save = {codes, scales, (int)fmt, dim % 8 == 0 && aligned(codes, 8)};
+    a.x = {x, x_scales, ldx, (int)x_fmt};
+    a.y = {y, dim};
+    a.save = {codes, scales, (int)fmt};
     a.weight = weight;
     a.bias = bias;
     a.ids = ids;
     a.m = m;
     a.dim = dim;
     a.n_groups = n_groups;
-    a.pvec = vec_ok(weight, dim, dim, 4) && aligned(bias, 16);
     a.eps = eps;
     a.center = kind == HTL_NORM_LAYER;
     const int tx = x_scales ? kSrcRows8 : (int)x_dtype;
@@ -347,11 +378,10 @@ extern "C" htl_status norm_rows_backward(const void* dy, htl_dtype dy_dtype, int
     HTL_REQUIRE(ws && aligned(ws, 256) && ws_bytes >= norm_back_workspace_bytes(m, n_groups, dim),
                 "norm_rows_backward: workspace too small or misaligned");
     NormBackArgs a;
-    a.dy = {dy, nullptr, ld_dy, 0, vec_ok(dy, ld_dy, dim, de)};
-    a.x = {x, x_scales, ldx, (int)x_fmt,
-           x_scales ? (dim % 8 == 0 && ldx % 8 == 0 && aligned(x, 8)) : vec_ok(x, ldx, dim, xe)};
-    a.dres = {dres, nullptr, ld_dres, 0, dres ? vec_ok(dres, ld_dres, dim, re) : 0};
-    a.dx = {dx, dim, vec_ok(dx, dim, dim, re)};
+    a.dy = {dy, nullptr, ld_dy, 0};
+    a.x = {x, x_scales, ldx, (int)x_fmt};
+    a.dres = {dres, nullptr, ld_dres, 0};
+    a.dx = {dx, dim};
     a.weight = weight;
     a.order = order;
     a.offsets = offsets;
@@ -363,8 +393,6 @@ extern "C" htl_status norm_rows_backward(const void* dy, htl_dtype dy_dtype, int
     a.m = m;
     a.dim = dim;
     a.n_groups = n_groups;
-    a.pvec = vec_ok(weight, dim, dim, 4);
-    a.gvec = vec_ok(dweight, dim, dim, 4) && aligned(dbias, 16);
     a.eps = eps;
     a.center = kind == HTL_NORM_LAYER;
     const bool d32 = dy_dtype == HTL_F32, x32 = x_dtype == HTL_F32;

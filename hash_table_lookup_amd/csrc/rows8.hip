@@ -75,8 +75,8 @@ extern "C" htl_status rows8_save(const void* x, htl_dtype dtype, int64_t ldx, in
     const int es = dtype == HTL_F32 ? 4 : 2;
     HTL_REQUIRE(ldx >= dim, "rows8_save: row stride below dim");
     HTL_REQUIRE(x && codes && scales && aligned(x, es), "rows8_save: null or misaligned pointer");
-    const RowsIn in = {x, nullptr, ldx, 0, vec_ok(x, ldx, dim, es)};
-    const Rows8Out out = {codes, scales, (int)fmt, dim % 8 == 0 && aligned(codes, 8)};
+    const RowsIn in = {x, nullptr, ldx, 0};
+    const Rows8Out out = {codes, scales, (int)fmt};
     const int lanes = (dim + 31) / 32 * 4;
     const dim3 grid(grid_for(m * lanes, kThreads, 1 << 22));
     if (dtype == HTL_F32)
@@ -93,8 +93,8 @@ extern "C" htl_status rows8_load(const uint8_t* codes, const uint8_t* scales, ht
     if (m == 0) return HTL_OK;
     const int es = dtype == HTL_F32 ? 4 : 2;
     HTL_REQUIRE(y && codes && scales && aligned(y, es), "rows8_load: null or misaligned pointer");
-    const RowsIn in = {codes, scales, dim, (int)fmt, dim % 8 == 0 && aligned(codes, 8)};
-    const RowsOut out = {y, dim, vec_ok(y, dim, dim, es)};
+    const RowsIn in = {codes, scales, dim, (int)fmt};
+    const RowsOut out = {y, dim};
     const int lanes = (dim + 7) / 8;
     const dim3 grid(grid_for(m * lanes, kThreads, 1 << 22));
     if (dtype == HTL_F32)

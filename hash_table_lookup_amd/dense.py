@@ -51,17 +51,20 @@ def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None, dtype
     """A 2-D GPU tensor of f32 or bf16 and its row stride; rows may be strided, elements of a row may not."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
-    if like is not None and t.shape != like.shape:
-        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        t = t.contiguous()
-    return t, t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    d, shape = t.dtype, t.shape
+    if d != torch.float32 and d != torch.bfloat16:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {d}")
+    if dtype is not None and d != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {d}")
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, got {len(shape)}")
+    if like is not None and shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(shape)}")
+    m, n = shape
+    ld, step = t.stride()
+    if n > 1 and step != 1 or m > 1 and ld < n:
+        t, ld = t.contiguous(), n
+    return t, ld if m > 1 else n
 
 
 def _params(weight, bias, groups, dim: int):
