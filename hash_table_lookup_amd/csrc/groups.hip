@@ -8,18 +8,21 @@
 // the ids alone: ranks come from ballots and prefix sums, never from the
 // order in which atomics land.
 //
-// Bound: 8 bytes per row and the latency of dependent launches.  Up to
-// kOneBlockRows rows one workgroup does all in one launch; beyond, a count
-// per (group, block), a prefix sum over them, and the placement.
+// Bound: the latency of dependent launches (8 bytes a row are little).  Up to
+// kOneBlockRows rows one workgroup does all in one launch.  Beyond, a count
+// per (group, block) and the placement, whose blocks each add up the counts of
+// those before them; where that would be too many counts to read in every
+// block, a prefix sum over them in between.
 #include "dense.h"
 #include "scan.h"
 
 namespace htl {
 namespace {
 
-constexpr int64_t kOneBlockRows = 16384;
-constexpr int64_t kMinBlockRows = 4096;
-constexpr int kMaxBlocks = 512;
+constexpr int64_t kOneBlockRows = 4096;
+constexpr int64_t kBlockRows = 1024;
+constexpr int kMaxBlocks = 512, kSumBlocks = 256;
+constexpr int64_t kSumCounts = 16384;      // counts that every block may read
 constexpr int64_t kScanOneBlock = 4095;    // entries the prefix sum handles in one launch
 
 __device__ __forceinline__ int bin_of(int32_t id, int n_groups) {
@@ -42,13 +45,15 @@ __global__ __launch_bounds__(1024) void k_group_count(const int32_t* __restrict_
 // Each wave takes a contiguous run of the block's rows, so ranks within a
 // wave, then waves in order, then blocks in order give the stable place.
 // s_pos[wave][bin]: first the wave's counts, then the next place of the bin.
-// base: the scanned counts; null when one block holds every row and scans
-// its own bins (then n_groups < blockDim.x).
+// base: the scanned counts.  Without them the block adds up counts (null when
+// one block holds every row) and scans its bins itself (n_groups < 1024 then,
+// and 1,024 threads).
 __global__ __launch_bounds__(1024) void k_group_place(const int32_t* __restrict__ ids, int64_t m, int64_t per_block,
                                                      int n_groups, int id_bits, const int32_t* __restrict__ base,
+                                                     const int32_t* __restrict__ counts,
                                                      int32_t* __restrict__ order, int32_t* __restrict__ offsets) {
     extern __shared__ int32_t s_pos[];
-    __shared__ int32_t s_wave[16];
+    __shared__ int32_t s_wave[16], s_before[1024], s_total[1024];
     const int nw = blockDim.x >> 6, w = threadIdx.x >> 6, lane = __lane_id();
     const int nb = n_groups + 1;
     for (int b = threadIdx.x; b < nw * nb; b += blockDim.x) s_pos[b] = 0;
@@ -57,7 +62,23 @@ __global__ __launch_bounds__(1024) void k_group_place(const int32_t* __restrict_
     const int64_t run = ((uint32_t)(end - beg) / nw / 64 + 1) * 64;
     const int64_t wbeg = beg + w * run < end ? beg + w * run : end;
     const int64_t wend = wbeg + run < end ? wbeg + run : end;
-    for (int64_t i = wbeg + lane; i < wend; i += 64) atomicAdd(&s_pos[w * nb + bin_of(ids[i], n_groups)], 1);
+    // eight loads at a time: one after the other, they were most of the time
+    int bin[8];
+    auto read = [&](int64_t i0) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int64_t i = i0 + q * 64 + lane;
+            bin[q] = i < wend ? ids[i] : 0;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) bin[q] = bin_of(bin[q], n_groups);
+    };
+    for (int64_t i0 = wbeg; i0 < wend; i0 += 512) {
+        read(i0);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (i0 + q * 64 + lane < wend) atomicAdd(&s_pos[w * nb + bin[q]], 1);
+    }
     __syncthreads();
     if (base) {
         for (int b = threadIdx.x; b < nb; b += blockDim.x) {
@@ -70,10 +91,33 @@ __global__ __launch_bounds__(1024) void k_group_place(const int32_t* __restrict_
             }
         }
     } else {
+        if (counts) {                       // a wave per bin
+            for (int b = w; b < nb; b += nw) {
+                int32_t before = 0, total = 0;
+                for (int q = lane; q < (int)gridDim.x; q += 64) {
+                    const int32_t c = counts[(int64_t)b * gridDim.x + q];
+                    total += c;
+                    if (q < (int)blockIdx.x) before += c;
+                }
+#pragma unroll
+                for (int off = 1; off < 64; off <<= 1) {
+                    total += __shfl_xor(total, off);
+                    before += __shfl_xor(before, off);
+                }
+                if (lane == 0) {
+                    s_total[b] = total;
+                    s_before[b] = before;
+                }
+            }
+            __syncthreads();
+        }
         const int b = threadIdx.x;
         int32_t total = 0;
-        if (b < nb)
-            for (int q = 0; q < nw; ++q) total += s_pos[q * nb + b];
+        if (b < nb) {
+            if (counts) total = s_total[b];
+            else
+                for (int q = 0; q < nw; ++q) total += s_pos[q * nb + b];
+        }
         int32_t incl = total;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
@@ -85,7 +129,8 @@ __global__ __launch_bounds__(1024) void k_group_place(const int32_t* __restrict_
         int32_t at = incl - total;
         for (int q = 0; q < w; ++q) at += s_wave[q];
         if (b < nb) {
-            offsets[b] = at;
+            if (blockIdx.x == 0) offsets[b] = at;
+            if (counts) at += s_before[b];
             for (int q = 0; q < nw; ++q) {
                 const int32_t c = s_pos[q * nb + b];
                 s_pos[q * nb + b] = at;
@@ -94,27 +139,38 @@ __global__ __launch_bounds__(1024) void k_group_place(const int32_t* __restrict_
         }
     }
     __syncthreads();
-    for (int64_t i0 = wbeg; i0 < wend; i0 += 64) {
-        const int64_t i = i0 + lane;
-        const bool in = i < wend;
-        const int b = in ? bin_of(ids[i], n_groups) : 0;
-        uint64_t same = __ballot(in);       // lanes of the same bin
-        for (int k = 0; k < id_bits; ++k) {
-            const bool bit = (b >> k) & 1;
-            const uint64_t v = __ballot(bit);
-            same &= bit ? v : ~v;
+    for (int64_t i0 = wbeg; i0 < wend; i0 += 512) {
+        if (run > 512) read(i0);            // else they are there from the count
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int64_t i = i0 + q * 64 + lane;
+            if (i - lane >= wend) break;
+            const bool in = i < wend;
+            const int b = bin[q];
+            uint64_t same = __ballot(in);       // lanes of the same bin
+            for (int k = 0; k < id_bits; ++k) {
+                const bool bit = (b >> k) & 1;
+                const uint64_t v = __ballot(bit);
+                same &= bit ? v : ~v;
+            }
+            const int first = __ffsll((unsigned long long)same) - 1;
+            int32_t at = 0;
+            if (in && lane == first) at = atomicAdd(&s_pos[w * nb + b], __popcll(same));
+            at = __shfl(at, in ? first : lane);
+            if (in) order[at + __popcll(same & lanemask_lt())] = (int32_t)i;
         }
-        const int first = __ffsll((unsigned long long)same) - 1;
-        int32_t at = 0;
-        if (in && lane == first) at = atomicAdd(&s_pos[w * nb + b], __popcll(same));
-        at = __shfl(at, in ? first : lane);
-        if (in) order[at + __popcll(same & lanemask_lt())] = (int32_t)i;
     }
 }
 
-int64_t group_blocks(int64_t m, int n_groups) {
-    int64_t nb = m / kMinBlockRows;
+// Blocks of rows, and whether the placement adds up their counts itself.
+int64_t group_blocks(int64_t m, int n_groups, bool& summed) {
+    int64_t nb = m / kBlockRows;
     nb = nb < 1 ? 1 : (nb > kMaxBlocks ? kMaxBlocks : nb);
+    int64_t most = kSumCounts / (n_groups + 1);
+    if (most > kSumBlocks) most = kSumBlocks;
+    summed = n_groups < 1024 && (most >= nb || most >= 128);
+    if (summed) return nb < most ? nb : most;
+    nb = nb < m / 4096 ? nb : (m / 4096 < 1 ? 1 : m / 4096);
     // a prefix sum of one launch, where that leaves blocks enough to fill the device
     const int64_t one = kScanOneBlock / (n_groups + 1);
     return nb > one && one >= 128 ? one : nb;
@@ -127,7 +183,8 @@ using namespace htl;
 
 extern "C" size_t row_groups_workspace_bytes(int64_t m, int n_groups) {
     if (m < 0 || m > kMaxRows || n_groups < 1 || n_groups > kMaxGroups) return 0;
-    const int64_t entries = (int64_t)(n_groups + 1) * group_blocks(m, n_groups);
+    bool summed;
+    const int64_t entries = (int64_t)(n_groups + 1) * group_blocks(m, n_groups, summed);
     return align_up((size_t)entries * 4, 256) + align_up((size_t)(entries + 1) * 4, 256) +
            align_up(scan_temp_bytes(entries), 256);
 }
@@ -148,19 +205,25 @@ extern "C" htl_status row_groups(const int32_t* ids, int64_t m, int n_groups, in
     const size_t lds = (size_t)(threads / 64) * (n_groups + 1) * 4;
     if (m <= kOneBlockRows && n_groups < 1024) {
         hipLaunchKernelGGL(k_group_place, dim3(1), dim3(threads), lds, stream, ids, m, m, n_groups, bits,
-                           (const int32_t*)nullptr, order, offsets);
+                           (const int32_t*)nullptr, (const int32_t*)nullptr, order, offsets);
         return check_launch("row_groups");
     }
-    const int64_t nb = group_blocks(m, n_groups), per = ceil_div(m, nb);
+    bool summed;
+    const int64_t nb = group_blocks(m, n_groups, summed), per = ceil_div(m, nb);
     const int64_t entries = (int64_t)(n_groups + 1) * nb;
     int32_t* counts = (int32_t*)ws;
     int32_t* base = (int32_t*)((char*)ws + align_up((size_t)entries * 4, 256));
     void* tmp = (char*)base + align_up((size_t)(entries + 1) * 4, 256);
     hipLaunchKernelGGL(k_group_count, dim3((unsigned)nb), dim3(1024), (size_t)(n_groups + 1) * 4, stream, ids, m, per,
                        n_groups, counts);
+    if (summed) {
+        hipLaunchKernelGGL(k_group_place, dim3((unsigned)nb), dim3(threads), lds, stream, ids, m, per, n_groups, bits,
+                           (const int32_t*)nullptr, (const int32_t*)counts, order, offsets);
+        return check_launch("row_groups");
+    }
     const htl_status st = scan_exclusive_i32(counts, base, entries, nullptr, kScanIdentity, 0, tmp, stream);
     if (st != HTL_OK) return st;
     hipLaunchKernelGGL(k_group_place, dim3((unsigned)nb), dim3(threads), lds, stream, ids, m, per, n_groups, bits,
-                       (const int32_t*)base, order, offsets);
+                       (const int32_t*)base, (const int32_t*)nullptr, order, offsets);
     return check_launch("row_groups");
 }
