@@ -485,8 +485,9 @@ __device__ __forceinline__ void chunks_of_group(const int32_t* offsets, int n_gr
 // Sums of a group's partial rows: out[g][d] = sum over its chunks of
 // partial[item][d], for the groups with more than one chunk (a lone chunk
 // writes its sums itself).  Chunks are added in order, so the result does
-// not depend on which workgroup ended first.  limit: rows that partial holds.
-htl_status sum_chunks(const float* partial, int64_t limit, float* out, const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
-                      int64_t width, hipStream_t stream);
+// not depend on which workgroup ended first.  limit: rows that partial holds;
+// a second set of sums (out2, nullable) has its partial rows after those.
+htl_status sum_chunks(const float* partial, int64_t limit, float* out, float* out2, const int32_t* offsets,
+                      int n_groups, int64_t m, uint32_t R, int64_t width, hipStream_t stream);
 
 }  // namespace htl

@@ -365,7 +365,5 @@ extern "C" htl_status norm_gate_backward(const void* dout, htl_dtype dout_dtype,
     });
     const htl_status st = check_launch("norm_gate_backward");
     if (st != HTL_OK) return st;
-    const htl_status s1 = sum_chunks(a.partial, a.chunks, dweight, offsets, n_groups, m, a.rows, dim, stream);
-    if (s1 != HTL_OK || !dbias) return s1;
-    return sum_chunks(a.partial + a.chunks * dim, a.chunks, dbias, offsets, n_groups, m, a.rows, dim, stream);
+    return sum_chunks(a.partial, a.chunks, dweight, dbias, offsets, n_groups, m, a.rows, dim, stream);
 }

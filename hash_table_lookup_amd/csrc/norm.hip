@@ -192,10 +192,14 @@ __global__ __launch_bounds__(H::kThreads) void k_norm_back(NormBackArgs a) {
 
 // 64 columns per workgroup; its 16 waves take every 16th chunk of the group.
 __global__ __launch_bounds__(1024) void k_sum_chunks(const float* __restrict__ partial, int64_t limit,
-                                                    float* __restrict__ out,
+                                                    float* __restrict__ out, float* __restrict__ out2,
                                                     const int32_t* __restrict__ offsets, int n_groups, int64_t m,
                                                     uint32_t R, int64_t width) {
     __shared__ float s[16][64];
+    if (blockIdx.z) {                        // the second set of sums
+        partial += limit * width;
+        out = out2;
+    }
     const int g = blockIdx.y, w = threadIdx.x >> 6, lane = threadIdx.x & 63;
     int64_t first;
     int count;
@@ -264,18 +268,18 @@ uint32_t norm_chunk_rows(int64_t m, int dim) {
 int64_t norm_chunks(int64_t m, int n_groups, int dim) { return m / norm_chunk_rows(m, dim) + n_groups + 1; }
 uint32_t norm_rows_per_chunk(int64_t m, int dim) { return norm_chunk_rows(m, dim); }
 
-htl_status sum_chunks(const float* partial, int64_t limit, float* out, const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
+htl_status sum_chunks(const float* partial, int64_t limit, float* out, float* out2, const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
                       int64_t width, hipStream_t stream) {
     if (m <= (int64_t)R) return HTL_OK;      // every group is one chunk
-    if (width >= 65536) {
+    if (width >= 65536 && !out2) {
         const int64_t blocks = ceil_div(width, 1024), most = ceil_div(4096, n_groups);
         hipLaunchKernelGGL(k_sum_wide, dim3((unsigned)(blocks < most ? blocks : most), (unsigned)n_groups), dim3(256), 0,
                            stream, partial, limit, out, offsets, n_groups, m, R, width);
         return check_launch("partial sums");
     }
     const int64_t cols = ceil_div(width, 64);
-    hipLaunchKernelGGL(k_sum_chunks, dim3((unsigned)(cols < 4096 ? cols : 4096), (unsigned)n_groups), dim3(1024), 0,
-                       stream, partial, limit, out, offsets, n_groups, m, R, width);
+    hipLaunchKernelGGL(k_sum_chunks, dim3((unsigned)(cols < 4096 ? cols : 4096), (unsigned)n_groups, out2 ? 2 : 1),
+                       dim3(1024), 0, stream, partial, limit, out, out2, offsets, n_groups, m, R, width);
     return check_launch("partial sums");
 }
 
@@ -412,7 +416,5 @@ extern "C" htl_status norm_rows_backward(const void* dy, htl_dtype dy_dtype, int
     });
     const htl_status st = check_launch("norm_rows_backward");
     if (st != HTL_OK) return st;
-    const htl_status s1 = sum_chunks(a.partial, a.chunks, dweight, offsets, n_groups, m, a.rows, dim, stream);
-    if (s1 != HTL_OK || !dbias) return s1;
-    return sum_chunks(a.partial + a.chunks * dim, a.chunks, dbias, offsets, n_groups, m, a.rows, dim, stream);
+    return sum_chunks(a.partial, a.chunks, dweight, dbias, offsets, n_groups, m, a.rows, dim, stream);
 }

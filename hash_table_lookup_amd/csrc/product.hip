@@ -892,5 +892,5 @@ extern "C" htl_status grouped_mm_backward(const void* dy, int64_t ld_dy, const v
     }
     const htl_status st = check_launch("grouped_mm_backward");
     if (st != HTL_OK) return st;
-    return sum_chunks(p.partial, p.limit, dw, offsets, n_groups, m, p.rows, (int64_t)n * k, stream);
+    return sum_chunks(p.partial, p.limit, dw, nullptr, offsets, n_groups, m, p.rows, (int64_t)n * k, stream);
 }
