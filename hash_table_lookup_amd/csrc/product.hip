@@ -623,32 +623,34 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(ProdArgs p) {
     }
 }
 
-// 16 neighbouring outputs of a lane, `left` of them in the row.
+// A lane's 16 outputs of 64: eight from `at` on and eight 32 further, so that
+// four lanes fill 64 bytes of a bf16 row in one store; `left` of the row from
+// `at` on.
 __device__ __forceinline__ void store16(void* out, bool f32, int64_t at, int left, const f32x4* v) {
-    if (f32) {
-        float* o = (float*)out + at;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (q * 4 + 4 <= left) {
-                __builtin_memcpy(__builtin_assume_aligned(o + q * 4, 4), &v[q], 16);
-            } else {
+    for (int h = 0; h < 2; ++h, at += 32, left -= 32) {
+        if (f32) {
+            float* o = (float*)out + at;
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (q * 4 + r < left) o[q * 4 + r] = v[q][r];
+            for (int q = 0; q < 2; ++q) {
+                if (q * 4 + 4 <= left) {
+                    store_at<4>(o + q * 4, v[2 * h + q]);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (q * 4 + r < left) o[q * 4 + r] = v[2 * h + q][r];
+                }
             }
-        }
-    } else {
-        uint16_t* o = (uint16_t*)out + at;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        } else {
+            uint16_t* o = (uint16_t*)out + at;
             const f32x4 a = v[2 * h], b = v[2 * h + 1];
             const u32x4 w = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])};
-            if (h * 8 + 8 <= left) {
-                __builtin_memcpy(__builtin_assume_aligned(o + h * 8, 2), &w, 16);
+            if (8 <= left) {
+                store_at<2>(o, w);
             } else {
 #pragma unroll
                 for (int r = 0; r < 8; ++r)
-                    if (h * 8 + r < left) o[h * 8 + r] = (uint16_t)(w[r >> 1] >> (16 * (r & 1)));
+                    if (r < left) o[r] = (uint16_t)(w[r >> 1] >> (16 * (r & 1)));
             }
         }
     }
@@ -661,7 +663,7 @@ __device__ __forceinline__ void store16(void* out, bool f32, int64_t at, int lef
 //
 // LDS holds one row of LP * 32 elements per output, zeros beyond the matrix,
 // 16 bytes apart so that 16 rows read together hit different banks, and in
-// such an order that a lane ends up with 16 neighbouring outputs.
+// such an order that a lane ends up with twice eight neighbouring outputs.
 template <int LP, int BYTES, int MODE>
 __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resident(ProdArgs p) {
     constexpr int kLd = LP * 64 + 16;
@@ -669,7 +671,7 @@ __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resi
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cols = MODE == kFwd ? p.n : p.k, len = MODE == kFwd ? p.k : p.n;
     const int blocks = (cols + 63) / 64;
-    auto place = [](int c) { return (c & ~63) + ((c >> 2) & 3) * 16 + ((c >> 4) & 3) * 4 + (c & 3); };
+    auto place = [](int c) { return (c & ~31) + ((c >> 2) & 1) * 16 + ((c >> 3) & 3) * 4 + (c & 3); };
     for (int64_t b = blockIdx.x;; b += gridDim.x) {
         TileAt t;
         const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, 0, 1, b, t);
@@ -709,15 +711,24 @@ __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resi
         __syncthreads();
         for (; pos < t.end; pos += 256) {
             Frag<kSrcBf16> x[2][LP];
+            if (len == LP * 32) {            // every piece whole; a row that is not there is read as the first
 #pragma unroll
-            for (int l = 0; l < LP; ++l)
+                for (int l = 0; l < LP; ++l)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int e = l * 32 + (lane >> 4) * 8;
-                    const char* at = (const char*)p.a + (row[j] * p.lda + e) * 2;
-                    const u32x4 v = held_piece<2>(at, grouped && row[j] >= 0 ? len - e : 0);
-                    __builtin_memcpy(&x[j][l].v, &v, 16);
-                }
+                    for (int j = 0; j < 2; ++j)
+                        load_at<2>((const char*)p.a + ((row[j] < 0 ? 0 : row[j]) * p.lda + l * 32 + (lane >> 4) * 8) * 2,
+                                   x[j][l].v);
+            } else {
+#pragma unroll
+                for (int l = 0; l < LP; ++l)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int e = l * 32 + (lane >> 4) * 8;
+                        const char* at = (const char*)p.a + (row[j] * p.lda + e) * 2;
+                        const u32x4 v = held_piece<2>(at, row[j] >= 0 ? len - e : 0);
+                        __builtin_memcpy(&x[j][l].v, &v, 16);
+                    }
+            }
             const int32_t next[2] = {row_at(pos + 256 + (lane & 15)), row_at(pos + 272 + (lane & 15))};
             for (int nb = 0; nb < blocks; ++nb) {
                 f32x4 acc[2][4];
@@ -736,7 +747,7 @@ __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resi
                             multiply(c, x[1][l], 0, acc[1][q]);
                         }
                 }
-                const int col = nb * 64 + (lane >> 4) * 16;
+                const int col = nb * 64 + (lane >> 4) * 8;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     if (row[j] < 0) continue;
