@@ -551,3 +551,87 @@ def test_rows_past_32_bits(htl):
     dx, dw = htl.grouped_mm_backward(x, y, mat)
     assert torch.equal(dx[-1000:], htl.grouped_mm_backward(tail, ty, mat)[0])
     assert torch.isfinite(dw).all()
+
+
+# ------------------------------------------------- each kernel's own sizes --
+@pytest.mark.parametrize("m", [4096, 4097, 5000, 131073, 300000])
+@pytest.mark.parametrize("g,kind", [(5, "sorted"), (26, "tables"), (64, "dropped"), (127, "dropped"), (128, "one"),
+                                    (500, "dropped")])
+def test_group_rows_over_blocks(htl, m, g, kind):
+    ids = _ids(np.random.default_rng(m * g), m, g, kind)
+    plan = _plan(htl, ids, g)
+    key = np.where((ids < 0) | (ids >= g), g, ids)
+    assert np.array_equal(plan.order.cpu().numpy(), np.argsort(key, kind="stable"))
+    want = np.concatenate([[0], np.cumsum(np.bincount(key, minlength=g + 1)[:g])])
+    assert np.array_equal(plan.offsets.cpu().numpy(), want)
+
+
+# matrices kept in LDS (reductions of at most 32, 64, 128 and 256, in either LDS size), tiles of 256 x 256
+# in the forward product and in the input gradient, long reductions over rows
+@pytest.mark.parametrize("m,g,k,n", [(1100, 2, 32, 1100), (1100, 2, 64, 600), (1100, 2, 128, 300), (1100, 2, 200, 136),
+                                     (1100, 2, 31, 33), (1600, 3, 100, 50), (1200, 2, 250, 20), (8300, 3, 136, 4104),
+                                     (8300, 3, 4104, 136), (9000, 2, 264, 264)])
+@pytest.mark.parametrize("kind", ["tables", "dropped"])
+def test_grouped_mm_kernels(htl, m, g, k, n, kind):
+    ids = _ids(np.random.default_rng(m + k + n), m, g, kind)
+    _product_check(htl, m, g, k, n, torch.bfloat16, ids, m + k)
+
+
+def test_grouped_mm_rows_far_apart(htl):
+    """Operands that span more than 4 GiB take 64-bit addresses, with the same result to the bit."""
+    m, k, n, ld = 66000, 264, 272, 33000
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    wide = torch.empty(m, ld, dtype=torch.bfloat16, device="cuda")
+    x, dy = wide[:, 8:8 + k], wide[:, 1000:1000 + n]
+    x.normal_(generator=gen)
+    dy.normal_(generator=gen)
+    ids = torch.randint(-1, 3, (m,), device="cuda", generator=gen).to(torch.int32)
+    plan = htl.group_rows(ids, 3)
+    w = torch.randn(3, n, k, device="cuda", generator=gen).bfloat16()
+    xc, dyc = x.contiguous(), dy.contiguous()
+    assert torch.equal(htl.grouped_mm(x, w, plan), htl.grouped_mm(xc, w, plan))
+    a, b = htl.grouped_mm_backward(dy, x, w, plan), htl.grouped_mm_backward(dyc, xc, w, plan)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("m,dim,g", [(3000, 4104, 3), (1500, 9000, 1), (5000, 2048, 26), (20000, 20, 4), (9000, 600, 2)])
+def test_norms_over_many_rows(htl, m, dim, g):
+    """More rows than a launch has teams: every row of the outputs, and the sums over chunks."""
+    gen, ids = _inputs(m, dim, g, 5 * m + 1)                  # ids with dropped rows
+    x = torch.randn(m, dim, generator=gen)
+    z, u = torch.randn(m, dim, generator=gen), torch.randn(m, dim, generator=gen)
+    weight, b = 1 + 0.1 * torch.randn(g, dim, generator=gen), 0.1 * torch.randn(g, dim, generator=gen)
+    plan = _plan(htl, ids, g)
+    kw = dict(groups=plan, kind="layer", eps=EPS)
+    w, on = _param_of(weight, ids, g)
+    bw = _param_of(b, ids, g)[0]
+    y, _ = htl.norm_rows(x.cuda(), weight.cuda(), b.cuda(), **kw)
+    N = Norm(x, "layer")
+    want = torch.where(on, N.n * w + bw, 0.0)
+    _close(y, want, w.abs() * N.e_n + 2 * U * ((N.n * w).abs() + bw.abs()) + U * want.abs() + 1e-37, "y")
+    dy = torch.randn(m, dim, generator=gen)
+    dx, dw, db = htl.norm_rows_backward(dy.cuda(), x.cuda(), weight.cuda(), bias=True, **kw)
+    d = torch.where(on, dy.double(), 0.0)
+    gx, e = N.back(d * w, U * (d * w).abs())
+    want = torch.where(on, gx, 0.0)
+    _close(dx, want, e + 3 * U * want.abs() + 1e-37, "dx")
+    _close(dw, *_sum_of(d * N.n, d.abs() * N.e_n, ids, g), "dweight")
+    _close(db, *_sum_of(d, torch.zeros_like(d), ids, g), "dbias")
+    del dx, y, want, gx, e
+    out, _, _ = htl.norm_gate(x.cuda(), z.cuda(), u.cuda(), weight.cuda(), b.cuda(), act="sigmoid", **kw)
+    N = Norm(z, "layer")
+    v = N.n * w + bw
+    e_v = w.abs() * N.e_n + 2 * U * ((N.n * w).abs() + bw.abs())
+    a, slope = _act(u.double(), "sigmoid")
+    add = torch.where(on, a * v, 0.0)
+    want = x.double() + add
+    _close(out, want, a * e_v + 20 * U * add.abs() + 2 * U * want.abs() + 1e-37, "out")
+    dz, du, dw, db = htl.norm_gate_backward(dy.cuda(), z.cuda(), u.cuda(), weight.cuda(), b.cuda(), act="sigmoid", **kw)
+    want = d * slope * v
+    _close(du, want, d.abs() * (16 * U * a * v.abs() + (slope + 16 * U * a) * e_v) + 6 * U * want.abs() + 1e-37, "dgate")
+    t = d * a
+    gz, err = N.back(t * w, 20 * U * (t * w).abs())
+    gz = torch.where(on, gz, 0.0)
+    _close(dz, gz, err + 3 * U * gz.abs() + 1e-37, "dz")
+    _close(dw, *_sum_of(t * N.n, t.abs() * N.e_n + 20 * U * (t * N.n).abs(), ids, g), "dweight")
+    _close(db, *_sum_of(t, 20 * U * t.abs(), ids, g), "dbias")
