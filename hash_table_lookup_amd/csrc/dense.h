@@ -50,6 +50,11 @@ template <int A, class V> __device__ __forceinline__ void load_at(const void* p,
 template <int A, class V> __device__ __forceinline__ void store_at(void* p, const V& v) {
     __builtin_memcpy(__builtin_assume_aligned(p, A), &v, sizeof(V));
 }
+// The same past the caches: rows of a result, of which nothing is read again here.
+template <int A, class V> __device__ __forceinline__ void stream_at(void* p, const V& v) {
+    typedef V Loose __attribute__((aligned(A)));
+    __builtin_nontemporal_store(v, (Loose*)p);
+}
 
 template <int SRC> struct Raw8;
 template <> struct Raw8<kSrcF32> { u32x4 lo, hi; };
@@ -164,8 +169,8 @@ __device__ __forceinline__ void store8(const RowsOut& r, int64_t row, int col, i
         float* p = (float*)r.p + row * r.ld + col;
         if (col + 8 <= dim) {
             const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
-            store_at<4>(p, a);
-            store_at<4>(p + 4, b);
+            stream_at<4>(p, a);
+            stream_at<4>(p + 4, b);
         } else if (col < dim) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -177,7 +182,7 @@ __device__ __forceinline__ void store8(const RowsOut& r, int64_t row, int col, i
 #pragma unroll
         for (int j = 0; j < 4; ++j) a[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
         if (col + 8 <= dim) {
-            store_at<2>(p, a);
+            stream_at<2>(p, a);
         } else if (col < dim) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -239,7 +244,7 @@ __device__ __forceinline__ void save8(const Rows8Out& r, int64_t row, int col, i
             r.scales[row * ((dim + 31) >> 5) + (col >> 5)] = finite ? (uint8_t)(e + 127) : (uint8_t)255;
         uint8_t* p = r.codes + row * (int64_t)dim + col;
         if (col + 8 <= dim) {
-            store_at<1>(p, c);
+            stream_at<1>(p, c);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)

@@ -52,8 +52,9 @@ template <int BR_, int BC_, int WR_, int WC_> struct Tile {
     static constexpr int TR = BR_ / WR_ / 16, TC = BC_ / WC_ / 16;   // 16 x 16 outputs per wave
 };
 
-// An operand in global memory, below 4 GiB: pieces come by 32-bit offset, and
-// one at kOutside (beyond `bytes`) is zeros.
+// An operand in global memory, below 4 GiB: pieces come by 32-bit offset (a
+// lane's and the wave's; the wave's stays within the operand), and one at
+// kOutside (beyond `bytes`) is zeros.
 typedef __amdgpu_buffer_rsrc_t Buffer;
 constexpr uint32_t kOutside = 0xFFFFFFF0u;
 constexpr int64_t kBufferBytes = 0xFFFF0000ll;
@@ -138,7 +139,7 @@ template <int ES, int B, int NT, bool ASYNC> struct Along {
         const int64_t left = len - e0 - slot * VE;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            if (ASYNC) load_piece(buf, left > 0 ? at[i] : kOutside, (uint32_t)e0 * ES, lds + wave_bytes<NT, N>(i));
+            if (ASYNC) load_piece(buf, left > 0 ? at[i] : kOutside, e0 < len ? (uint32_t)e0 * ES : 0, lds + wave_bytes<NT, N>(i));
             else held[i] = held_piece<ES>(src[i] + e0 * ES, left);
         }
     }
@@ -153,11 +154,12 @@ template <int ES, int B, int NT, bool ASYNC> struct AlongRows {
     uint32_t at;
     const char* src;
     int64_t ld;              // bytes
-    int slot, rows;
+    int slot, rows, all;     // rows: from this lane's first on; all: from the tile's
     u32x4 held[ASYNC ? 1 : kN];
     __device__ __forceinline__ void begin(const char* p, int64_t ld_bytes, int rows_left) {
         slot = (threadIdx.x & 3) ^ swap_along(threadIdx.x >> 2);
         ld = ld_bytes;
+        all = rows_left;
         rows = rows_left - (int)(threadIdx.x >> 2);
         if (ASYNC) {
             buf = buffer_of(p, rows_left * ld);
@@ -172,7 +174,8 @@ template <int ES, int B, int NT, bool ASYNC> struct AlongRows {
         for (int i = 0; i < kN; ++i) {
             const int64_t have = i * (NT / 4) < rows ? left : 0;
             if (ASYNC)
-                load_piece(buf, have > 0 ? at : kOutside, (uint32_t)e0 * ES + i * (NT / 4) * (uint32_t)ld,
+                load_piece(buf, have > 0 ? at : kOutside,
+                           e0 < len && i * (NT / 4) < all ? (uint32_t)e0 * ES + i * (NT / 4) * (uint32_t)ld : 0,
                            lds + wave_bytes<NT, N>(i));
             else
                 held[i] = held_piece<ES>(src + e0 * ES + i * (NT / 4) * ld, have);
@@ -241,7 +244,8 @@ template <int ES, int B, int NT, bool ASYNC, bool GATHER> struct Across {
             const int64_t left = (!GATHER || row >= 0) && e0 + e < len ? cols - col : 0;
             if (ASYNC) {
                 const uint32_t at = (GATHER ? (uint32_t)row : (uint32_t)(t / S)) * (uint32_t)ld + (uint32_t)first + col * ES;
-                load_piece(buf, left > 0 ? at : kOutside, GATHER ? 0 : (uint32_t)(e0 + i * kRows) * (uint32_t)ld,
+                load_piece(buf, left > 0 ? at : kOutside,
+                           GATHER || e0 + i * kRows >= len ? 0 : (uint32_t)(e0 + i * kRows) * (uint32_t)ld,
                            lds + wave_bytes<NT, N>(i));
             } else {
                 held[i] = held_piece<ES>(base + (GATHER ? (int64_t)row : e0 + e) * ld + col * ES, left);

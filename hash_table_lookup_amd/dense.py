@@ -41,6 +41,14 @@ class Rows8(NamedTuple):
     dtype: torch.dtype
 
 
+def _scratch(tag: str, nbytes: int, device) -> torch.Tensor:
+    """A call's workspace: the stream's cached one, or, into a graph being captured, one of the graph's own (the
+    cached one may be replaced by a larger one while the graph lives)."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    return _workspace(tag, nbytes, device)
+
+
 def _choice(table: dict, value, name: str) -> int:
     if value not in table:
         raise ValueError(f"{name} must be one of {', '.join(table)}, got {value!r}")
@@ -114,7 +122,7 @@ def group_rows(ids: torch.Tensor, n_groups: int) -> RowGroups:
     order = torch.empty(m, dtype=torch.int32, device=d)
     offsets = torch.empty(max(int(n_groups), 0) + 1, dtype=torch.int32, device=d)
     nb = lib().row_groups_workspace_bytes(m, n_groups)
-    ws = _workspace("row_groups", nb, d)
+    ws = _scratch("row_groups", nb, d)
     _check(lib().row_groups(_ptr(ids), m, n_groups, _ptr(order), _ptr(offsets), _ptr(ws), nb, _stream()))
     return RowGroups(ids, order, offsets, int(n_groups))
 
@@ -193,7 +201,7 @@ def norm_rows_backward(dy: torch.Tensor, kept: Union[torch.Tensor, Rows8], weigh
     dweight = torch.empty((n, dim), dtype=torch.float32, device=d)
     dbias = torch.empty((n, dim), dtype=torch.float32, device=d) if bias else None
     nb = lib().norm_back_workspace_bytes(m, n, dim)
-    ws = _workspace("norm_back", nb, d)
+    ws = _scratch("norm_back", nb, d)
     _check(lib().norm_rows_backward(_ptr(dy), _dtype_code(dy.dtype), ld_dy, _ptr(src), _dtype_code(kept.dtype), ldx,
                                     _ptr(scales), fmt, _ptr(res), ld_res, m, dim, _ptr(weight), order, offsets, n,
                                     kind_code, eps, _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws), nb, _stream()))
@@ -260,7 +268,7 @@ def norm_gate_backward(dout: torch.Tensor, kept_z: Union[torch.Tensor, Rows8], k
     dweight = torch.empty((n, dim), dtype=torch.float32, device=d)
     dbias = None if bias is None else torch.empty((n, dim), dtype=torch.float32, device=d)
     nb = lib().norm_back_workspace_bytes(m, n, dim)
-    ws = _workspace("norm_back", nb, d)
+    ws = _scratch("norm_back", nb, d)
     _check(lib().norm_gate_backward(_ptr(dout), _dtype_code(dout.dtype), ld, _ptr(z), ldz, _ptr(zs), _ptr(u), ldu,
                                     _ptr(us), _dtype_code(dtype), fmt, m, dim, _ptr(weight), _ptr(bias), order,
                                     offsets, n, kind_code, eps, act_code, scale, _ptr(dz), _ptr(du), _ptr(dweight),
@@ -313,7 +321,7 @@ def grouped_mm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, grou
     dx = torch.empty((m, k), dtype=_TORCH_DTYPE[code], device=d) if need_dx else None
     dw = torch.empty((g, n, k), dtype=torch.float32, device=d) if need_dw else None
     nb = lib().grouped_mm_backward_workspace_bytes(m, g, n, k) if need_dw else 0
-    ws = _workspace("grouped_mm_backward", nb, d) if need_dw else None
+    ws = _scratch("grouped_mm_backward", nb, d) if need_dw else None
     _check(lib().grouped_mm_backward(_ptr(dy), ld_dy, _ptr(x), ldx, _ptr(w), _dtype_code(x.dtype), m, n, k, order,
                                      offsets, g, _ptr(dx), code, _ptr(dw), _ptr(ws), nb, _stream()))
     return dx, dw
