@@ -34,8 +34,9 @@ struct RowsOut {
 
 // Lanes exchanged without LDS, within 16: x of lane l ^ 1 or l ^ 2 (of a
 // quad), or of the lane that mirrors l in its 8 or 16, which stands for l ^ 4
-// and l ^ 8 where the lanes of a quad, or of 8, hold the same.
-enum { kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140 };
+// and l ^ 8 where the lanes of a quad, or of 8, hold the same; rotated by 8 of
+// 16, of lane l ^ 8.
+enum { kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140, kRotate8 = 0x128 };
 template <int HOW> __device__ __forceinline__ int move_lanes(int x) {
     return __builtin_amdgcn_update_dpp(0, x, HOW, 0xF, 0xF, true);
 }

@@ -27,7 +27,6 @@ struct ProdArgs {
     uint32_t rows;           // positions per chunk
     float* partial;          // dw: [chunks][n][k]
     int out_f32;
-    int out_vec;             // four outputs of a lane are stored at once
     int64_t limit;           // dw: chunks that `partial` has room for
 };
 
@@ -401,6 +400,73 @@ __device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, i
     return __builtin_amdgcn_readfirstlane(found);
 }
 
+// Writes 16 rows of F * 16 outputs that begin at column `col` of rows of `cols`:
+// lane l holds four neighbours of row l % 16 in each of F matrix results, `row`
+// being where that row goes (-1: nowhere).  In bf16 four neighbours are 8
+// bytes, and a row's 32 bytes of one result would be a store of their own.
+// Lanes first exchange, without LDS: between 16s of lanes two results for
+// eight neighbours of one, and between row r's lane and row r + 8's, so that
+// one store fills whole 128-byte lines of eight rows.  (Half lines cost the
+// 1.7M x 256 outputs of 26 feature tables 300 us by themselves.)
+template <int F>
+__device__ __forceinline__ void store_rows(void* out, bool f32, int64_t row, int col, int cols, const f32x4* v) {
+    const int lane = __lane_id(), q = lane >> 4;
+    if (f32) {
+        if (row < 0) return;
+        float* o = (float*)out + row * cols;
+#pragma unroll
+        for (int t = 0; t < F; ++t) {
+            const int c = col + t * 16 + q * 4;
+            if (c + 4 <= cols) {
+                store_at<4>(o + c, v[t]);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (c + r < cols) o[c + r] = v[t][r];
+            }
+        }
+        return;
+    }
+    auto put = [&](int64_t r, int c, const u32x4& w) __attribute__((always_inline)) {
+        if (r < 0 || c >= cols) return;
+        uint16_t* o = (uint16_t*)out + r * cols + c;
+        if (c + 8 <= cols) {
+            store_at<2>(o, w);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < cols) o[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        }
+    };
+    u32x4 eight[F / 2];      // result 2 h + q % 2, neighbours q / 2 * 8 on
+#pragma unroll
+    for (int h = 0; h < F / 2; ++h) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(v[2 * h][2 * e], v[2 * h][2 * e + 1]),
+                                                            pack_bf16(v[2 * h + 1][2 * e], v[2 * h + 1][2 * e + 1]), false, false);
+            eight[h][e] = x[0];
+            eight[h][2 + e] = x[1];
+        }
+    }
+    const int c = col + (q & 1) * 16 + (q >> 1) * 8;
+    if constexpr (F == 2) {
+        put(row, c, eight[0]);
+    } else {
+        const bool high = lane & 8;
+        const int other = move_lanes<kRotate8>((int)row);
+        u32x4 first, second;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t got = (uint32_t)move_lanes<kRotate8>((int)(high ? eight[0][e] : eight[1][e]));
+            first[e] = high ? got : eight[0][e];
+            second[e] = high ? eight[1][e] : got;
+        }
+        put(high ? (int64_t)other : row, c + (high ? 32 : 0), first);
+        put(high ? row : (int64_t)other, c + (high ? 32 : 0), second);
+    }
+}
+
 template <int T, int MODE, class C, bool ASYNC>
 __global__ __launch_bounds__(C::kThreads, 2) void k_product(ProdArgs p) {
     // Slots of the ring as variables of their own: the compiler then makes a
@@ -584,78 +650,15 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(ProdArgs p) {
             __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0): nothing comes into LDS any more
         }
         if (!busy) continue;
-        // lane: output row l % 16, four columns from (l / 16) * 4 on, of each 16 x 16
-        const int ld = MODE == kDw ? p.k : cols;
+        void* to = MODE != kDw ? p.out : (t.count == 1 ? (float*)p.out + wg : p.partial + t.chunk * p.n * p.k);
 #pragma unroll
         for (int j = 0; j < C::TR; ++j) {
             const int r = wr + j * 16 + (lane & 15);
-            char* dst;
-            if (MODE == kDw) {
-                if (r0 + r >= p.n) continue;
-                float* to = t.count == 1 ? (float*)p.out + wg : p.partial + t.chunk * p.n * p.k;
-                dst = (char*)(to + (int64_t)(r0 + r) * ld);
-            } else {
-                const int row = s_row[r];
-                if (row < 0) continue;
-                dst = (char*)p.out + (int64_t)row * ld * (p.out_f32 ? 4 : 2);
-            }
+            const int row = MODE != kDw ? s_row[r] : (r0 + r < p.n ? r0 + r : -1);
+            f32x4 v[C::TC];
 #pragma unroll
-            for (int i = 0; i < C::TC; ++i) {
-                const int col = c0 + wc + i * 16 + (lane >> 4) * 4;
-                const f32x4 v = acc[i][j];
-                if (MODE == kDw || p.out_f32) {
-                    float* o = (float*)dst + col;
-                    if (p.out_vec) {
-                        if (col < cols) *(f32x4*)o = v;
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (col + q < cols) o[q] = v[q];
-                    }
-                } else {
-                    uint16_t* o = (uint16_t*)dst + col;
-                    if (p.out_vec) {
-                        if (col < cols) *(u32x2*)o = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (col + q < cols) o[q] = (uint16_t)f32_to_bf16_bits(v[q]);
-                    }
-                }
-            }
-        }
-    }
-}
-
-// A lane's 16 outputs of 64: eight from `at` on and eight 32 further, so that
-// four lanes fill 64 bytes of a bf16 row in one store; `left` of the row from
-// `at` on.
-__device__ __forceinline__ void store16(void* out, bool f32, int64_t at, int left, const f32x4* v) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h, at += 32, left -= 32) {
-        if (f32) {
-            float* o = (float*)out + at;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (q * 4 + 4 <= left) {
-                    store_at<4>(o + q * 4, v[2 * h + q]);
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (q * 4 + r < left) o[q * 4 + r] = v[2 * h + q][r];
-                }
-            }
-        } else {
-            uint16_t* o = (uint16_t*)out + at;
-            const f32x4 a = v[2 * h], b = v[2 * h + 1];
-            const u32x4 w = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])};
-            if (8 <= left) {
-                store_at<2>(o, w);
-            } else {
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < left) o[r] = (uint16_t)(w[r >> 1] >> (16 * (r & 1)));
-            }
+            for (int i = 0; i < C::TC; ++i) v[i] = acc[i][j];
+            store_rows<C::TC>(to, MODE == kDw || p.out_f32, row, c0 + wc, cols, v);
         }
     }
 }
@@ -666,8 +669,7 @@ __device__ __forceinline__ void store16(void* out, bool f32, int64_t at, int lef
 // global memory to registers, through the matrix, and out.
 //
 // LDS holds one row of LP * 32 elements per output, zeros beyond the matrix,
-// 16 bytes apart so that 16 rows read together hit different banks, and in
-// such an order that a lane ends up with twice eight neighbouring outputs.
+// 16 bytes apart so that 16 rows read together hit different banks.
 template <int LP, int BYTES, int MODE>
 __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resident(ProdArgs p) {
     constexpr int kLd = LP * 64 + 16;
@@ -675,7 +677,6 @@ __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resi
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cols = MODE == kFwd ? p.n : p.k, len = MODE == kFwd ? p.k : p.n;
     const int blocks = (cols + 63) / 64;
-    auto place = [](int c) { return (c & ~31) + ((c >> 2) & 1) * 16 + ((c >> 3) & 3) * 4 + (c & 3); };
     for (int64_t b = blockIdx.x;; b += gridDim.x) {
         TileAt t;
         const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, 0, 1, b, t);
@@ -694,7 +695,7 @@ __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resi
             if (MODE == kFwd) {
                 for (int i = threadIdx.x; i < blocks * 64 * LP * 4; i += 512) {
                     const int c = i / (LP * 4), e = i % (LP * 4) * 8;
-                    *(u32x4*)(lds + place(c) * kLd + e * 2) =
+                    *(u32x4*)(lds + c * kLd + e * 2) =
                         held_piece<2>(w + ((int64_t)c * p.k + e) * 2, c < p.n ? p.k - e : 0);
                 }
             } else {
@@ -707,7 +708,7 @@ __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resi
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const uint32_t a = lo[j >> 1] >> (16 * (j & 1)) & 0xFFFFu, d = hi[j >> 1] >> (16 * (j & 1));
-                        *(uint32_t*)(lds + place(c + j) * kLd + e * 2) = a | d << 16;
+                        *(uint32_t*)(lds + (c + j) * kLd + e * 2) = a | d << 16;
                     }
                 }
             }
@@ -751,11 +752,9 @@ __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resi
                             multiply(c, x[1][l], 0, acc[1][q]);
                         }
                 }
-                const int col = nb * 64 + (lane >> 4) * 8;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    if (row[j] < 0) continue;
-                    store16(p.out, p.out_f32, (int64_t)row[j] * cols + col, cols - col, acc[j]);
+                    store_rows<4>(p.out, p.out_f32, row[j], nb * 64, cols, acc[j]);
                 }
             }
             row[0] = next[0];
@@ -791,7 +790,6 @@ template <int MODE> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s)
     const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && (int64_t)p.k * es % 16 == 0 &&
                       (MODE == kFwd || (int64_t)p.n * es % 16 == 0) && aligned(p.b, 16) &&
                       p.m * p.lda * es <= kBufferBytes && (int64_t)p.n * p.k * es <= kBufferBytes;
-    p.out_vec = cols % 4 == 0 && aligned(p.out, p.out_f32 ? 16 : 8);
     const int64_t each = p.m / p.n_groups;
     const int len = MODE == kFwd ? p.k : p.n, lp = len <= 32 ? 1 : len <= 64 ? 2 : len <= 128 ? 4 : 8;
     const int64_t bytes = ceil_div(cols, 64) * 64 * (lp * 64 + 16);
@@ -858,7 +856,7 @@ extern "C" htl_status grouped_mm(const void* x, int64_t ldx, const void* w, htl_
     const int es = elem(dtype);
     HTL_REQUIRE(x && w && y, "grouped_mm: null pointer");
     HTL_REQUIRE(aligned(x, es) && aligned(w, es) && aligned(y, elem(y_dtype)), "grouped_mm: misaligned pointer");
-    ProdArgs p = {x, w, y, order, offsets, m, ldx, k, n, k, n_groups, 0, nullptr, y_dtype == HTL_F32, 0, 0};
+    ProdArgs p = {x, w, y, order, offsets, m, ldx, k, n, k, n_groups, 0, nullptr, y_dtype == HTL_F32, 0};
     launch_rows<kFwd>(p, dtype, stream);
     return check_launch("grouped_mm");
 }
@@ -886,14 +884,14 @@ extern "C" htl_status grouped_mm_backward(const void* dy, int64_t ld_dy, const v
     HTL_REQUIRE(!dw || (ws && aligned(ws, 256) && ws_bytes >= grouped_mm_backward_workspace_bytes(m, n_groups, n, k)),
                 "grouped_mm_backward: workspace too small or misaligned");
     if (dx && m > 0) {
-        const ProdArgs p = {dy, w, dx, order, offsets, m, ld_dy, k, n, k, n_groups, 0, nullptr, dx_dtype == HTL_F32, 0, 0};
+        const ProdArgs p = {dy, w, dx, order, offsets, m, ld_dy, k, n, k, n_groups, 0, nullptr, dx_dtype == HTL_F32, 0};
         launch_rows<kDx>(p, dtype, stream);
         const htl_status st = check_launch("grouped_mm_backward");
         if (st != HTL_OK) return st;
     }
     if (!dw) return HTL_OK;
     const ProdArgs p = {dy, x, dw, order, offsets, m, ld_dy, ldx, n, k, n_groups, dw_chunk_rows(m, n, k),
-                        (float*)ws, 1, k % 4 == 0 && aligned(dw, 16), dw_chunks(m, n_groups, n, k)};
+                        (float*)ws, 1, dw_chunks(m, n_groups, n, k)};
     const bool fast = ld_dy * es % 16 == 0 && ldx * es % 16 == 0 && aligned(dy, 16) && aligned(x, 16) &&
                       (int64_t)n * es % 16 == 0 && (int64_t)k * es % 16 == 0 && m * ld_dy * es <= kBufferBytes &&
                       m * ldx * es <= kBufferBytes;
