@@ -404,26 +404,50 @@ __device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, i
 // lane l holds four neighbours of row l % 16 in each of F matrix results, `row`
 // being where that row goes (-1: nowhere).  In bf16 four neighbours are 8
 // bytes, and a row's 32 bytes of one result would be a store of their own.
-// Lanes first exchange, without LDS: between 16s of lanes two results for
-// eight neighbours of one, and between row r's lane and row r + 8's, so that
-// one store fills whole 128-byte lines of eight rows.  (Half lines cost the
+// Lanes first exchange, without LDS: in bf16 between 16s of lanes two results
+// for eight neighbours of one, then between row r's lane and row r + 8's, so
+// that one store fills whole 128-byte lines of eight rows.  (Half lines cost the
 // 1.7M x 256 outputs of 26 feature tables 300 us by themselves.)
 template <int F>
 __device__ __forceinline__ void store_rows(void* out, bool f32, int64_t row, int col, int cols, const f32x4* v) {
     const int lane = __lane_id(), q = lane >> 4;
-    if (f32) {
-        if (row < 0) return;
-        float* o = (float*)out + row * cols;
+    const bool high = lane & 8;
+    const int64_t other = move_lanes<kRotate8>((int)row);
+    const int64_t low_row = high ? other : row, high_row = high ? row : other;
+    // a and b of row r's lane (low) and of row r + 8's (high): after it both lanes hold parts of row r in a,
+    // the low lane its a and the high lane the low one's b, and parts of row r + 8 in b
+    auto exchange = [&](u32x4& a, u32x4& b) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < F; ++t) {
-            const int c = col + t * 16 + q * 4;
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t got = (uint32_t)move_lanes<kRotate8>((int)(high ? a[e] : b[e]));
+            a[e] = high ? got : a[e];
+            b[e] = high ? b[e] : got;
+        }
+    };
+    if (f32) {
+        auto put = [&](int64_t r, int c, const u32x4& w) __attribute__((always_inline)) {
+            if (r < 0 || c >= cols) return;
+            uint32_t* o = (uint32_t*)out + r * cols + c;
             if (c + 4 <= cols) {
-                store_at<4>(o + c, v[t]);
+                store_at<4>(o, w);
             } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (c + r < cols) o[c + r] = v[t][r];
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < cols) o[e] = w[e];
             }
+        };
+#pragma unroll
+        for (int t = 0; t < F; t += 2) {
+            u32x4 a, b;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                a[e] = __float_as_uint(v[t][e]);
+                b[e] = __float_as_uint(v[t + 1][e]);
+            }
+            exchange(a, b);
+            const int c = col + t * 16 + (high ? 16 : 0) + q * 4;
+            put(low_row, c, a);
+            put(high_row, c, b);
         }
         return;
     }
@@ -453,17 +477,9 @@ __device__ __forceinline__ void store_rows(void* out, bool f32, int64_t row, int
     if constexpr (F == 2) {
         put(row, c, eight[0]);
     } else {
-        const bool high = lane & 8;
-        const int other = move_lanes<kRotate8>((int)row);
-        u32x4 first, second;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t got = (uint32_t)move_lanes<kRotate8>((int)(high ? eight[0][e] : eight[1][e]));
-            first[e] = high ? got : eight[0][e];
-            second[e] = high ? eight[1][e] : got;
-        }
-        put(high ? (int64_t)other : row, c + (high ? 32 : 0), first);
-        put(high ? row : (int64_t)other, c + (high ? 32 : 0), second);
+        exchange(eight[0], eight[1]);
+        put(low_row, c + (high ? 32 : 0), eight[0]);
+        put(high_row, c + (high ? 32 : 0), eight[1]);
     }
 }
 
