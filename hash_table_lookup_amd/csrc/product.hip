@@ -709,6 +709,7 @@ __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resi
         if (grouped) {
             const char* w = (const char*)p.b + (int64_t)t.g * p.n * p.k * 2;
             if (MODE == kFwd) {
+#pragma unroll 4
                 for (int i = threadIdx.x; i < blocks * 64 * LP * 4; i += 512) {
                     const int c = i / (LP * 4), e = i % (LP * 4) * 8;
                     *(u32x4*)(lds + c * kLd + e * 2) =
@@ -716,6 +717,7 @@ __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resi
                 }
             } else {
                 // two rows of w and eight columns: pairs of neighbours in eight rows of LDS
+#pragma unroll 2
                 for (int i = threadIdx.x; i < LP * 16 * blocks * 8; i += 512) {
                     const int e = i / (blocks * 8) * 2, c = i % (blocks * 8) * 8;
                     const char* at = w + ((int64_t)e * p.k + c) * 2;
@@ -800,7 +802,17 @@ template <int MODE, int LP> void launch_resident(const ProdArgs& p, int64_t chun
     else hipLaunchKernelGGL((k_resident<LP, 163840, MODE>), grid, dim3(512), 0, s, p);
 }
 
-// Forward product or dx: `cols` outputs a row, reduced over `len`.
+// Forward product or dx: `cols` outputs a row, reduced over `len`.  The kernel
+// goes by size (us, forward / dx, bf16, groups x rows, k -> n):
+// - a matrix kept in LDS pays its loading back over many rows: 26 x 65,536,
+//   128 -> 256: 315 / 302 against 512 / 361 in tiles; 26 x 4,096: 26 / 36
+//   against 32 / 27; 26 x 1,024: 16 / 17 against 11 / 11.  (The transposed
+//   matrix of 256 reduced elements takes longest to load: from 2^20 rows on.)
+// - tiles of 32 rows where groups have few rows, or the output few tiles:
+//   8 x 128, 1,024 -> 1,024: 11 / 15 against 15 / 20 with 128; 8 x 512: 28 / 30
+//   against 18 / 22.
+// - tiles of 256 x 256 once they fill the device: 8 x 2,048, 1,024 -> 1,024:
+//   43 / 47 against 51 / 53 with 128; 8 x 1,024: 37 / 38 against 28 / 28.
 template <int MODE> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s) {
     const int cols = MODE == kFwd ? p.n : p.k, es = elem(dtype);
     const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && (int64_t)p.k * es % 16 == 0 &&
@@ -809,7 +821,7 @@ template <int MODE> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s)
     const int64_t each = p.m / p.n_groups;
     const int len = MODE == kFwd ? p.k : p.n, lp = len <= 32 ? 1 : len <= 64 ? 2 : len <= 128 ? 4 : 8;
     const int64_t bytes = ceil_div(cols, 64) * 64 * (lp * 64 + 16);
-    if (dtype == HTL_BF16 && len <= 256 && bytes <= 163840 && each >= 512) {
+    if (dtype == HTL_BF16 && len <= 256 && bytes <= 163840 && each >= 512 && p.m >= (lp == 8 ? 1 << 20 : 1 << 16)) {
         p.rows = (uint32_t)align_up((size_t)ceil_div(p.m, 1024), 256);
         const int64_t chunks = p.m / p.rows + p.n_groups + 1;
         if (lp == 1) launch_resident<MODE, 1>(p, chunks, bytes, s);
@@ -818,8 +830,8 @@ template <int MODE> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s)
         else launch_resident<MODE, 8>(p, chunks, bytes, s);
         return;
     }
-    int tile = each <= 48 ? 32 : 128;
-    if (tile == 128 && dtype == HTL_BF16 && fast && ceil_div(p.m, 256) * ceil_div(cols, 256) >= 512 && each >= 256) tile = 256;
+    int tile = each <= 48 || (ceil_div(p.m, 32) + p.n_groups) * ceil_div(cols, 128) <= 512 ? 32 : 128;
+    if (dtype == HTL_BF16 && fast && ceil_div(p.m, 256) * ceil_div(cols, 256) >= 224 && each >= 256) tile = 256;
     p.rows = (uint32_t)tile;
     const int64_t chunks = p.m / tile + p.n_groups + 1;
     if (dtype == HTL_BF16) {

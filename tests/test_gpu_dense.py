@@ -566,8 +566,7 @@ def test_group_rows_over_blocks(htl, m, g, kind):
     assert np.array_equal(plan.offsets.cpu().numpy(), want)
 
 
-# matrices kept in LDS (reductions of at most 32, 64, 128 and 256, in either LDS size), tiles of 256 x 256
-# in the forward product and in the input gradient, long reductions over rows
+# short reductions, tiles of 256 x 256 in the forward product and in the input gradient, long sums over rows
 @pytest.mark.parametrize("m,g,k,n", [(1100, 2, 32, 1100), (1100, 2, 64, 600), (1100, 2, 128, 300), (1100, 2, 200, 136),
                                      (1100, 2, 31, 33), (1600, 3, 100, 50), (1200, 2, 250, 20), (8300, 3, 136, 4104),
                                      (8300, 3, 4104, 136), (9000, 2, 264, 264)])
@@ -575,6 +574,29 @@ def test_group_rows_over_blocks(htl, m, g, kind):
 def test_grouped_mm_kernels(htl, m, g, k, n, kind):
     ids = _ids(np.random.default_rng(m + k + n), m, g, kind)
     _product_check(htl, m, g, k, n, torch.bfloat16, ids, m + k)
+
+
+@pytest.mark.parametrize("m,k,n", [(70001, 32, 1100), (70001, 64, 600), (70001, 128, 300), (70001, 31, 33),
+                                   (70001, 100, 50), (1050000, 200, 136), (1050000, 136, 72)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_grouped_mm_many_rows(htl, m, k, n, out):
+    """Products of many rows, whose matrices stay in LDS, against the same rows in slices, which take tiles: a
+    row's product is summed in the same order, so the bits are the same."""
+    g = 3
+    gen = torch.Generator(device="cuda").manual_seed(m + k)
+    ids = torch.randint(-1, g, (m,), device="cuda", generator=gen).to(torch.int32)
+    x = torch.randn(m, k, device="cuda", generator=gen).bfloat16()
+    dy = torch.randn(m, n, device="cuda", generator=gen).bfloat16()
+    w = torch.randn(g, n, k, device="cuda", generator=gen).bfloat16()
+    plan = htl.group_rows(ids, g)
+    y = htl.grouped_mm(x, w, plan, out_dtype=out)
+    dx, _ = htl.grouped_mm_backward(dy, x, w, plan, dx_dtype=out, need_dw=False)
+    for a in (0, 30000, m - 3001):
+        rows = slice(a, a + 3001)
+        part = htl.group_rows(ids[rows], g)
+        assert torch.equal(y[rows], htl.grouped_mm(x[rows], w, part, out_dtype=out))
+        assert torch.equal(dx[rows], htl.grouped_mm_backward(dy[rows], x[rows], w, part, dx_dtype=out, need_dw=False)[0])
+    assert torch.isfinite(y).all() and torch.isfinite(dx).all() and not y[ids < 0].any()
 
 
 def test_grouped_mm_rows_far_apart(htl):
