@@ -848,12 +848,16 @@ template <int MODE> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s)
     }
 }
 
-// Rows per chunk of dw's sums: chunks times tiles fill the device a few
-// times over, and a chunk is long against the partial sums it leaves.
+// Rows per chunk of dw's sums.  A tile of a chunk leaves a partial sum to be
+// written and read again, so chunks are as long as fills the device once with
+// tiles of 256 x 256 (16 ragged experts, 2,048 x 4,096: 391 us, with twice as
+// many 469; 8 x 1,024 rows, 1,024 x 1,024: 67 against 94), and twice with those
+// that move by way of registers (100,001 rows, 513 x 777: 495 us, once 560) or
+// a few times over with small matrices, whose partial sums are small.
 uint32_t dw_chunk_rows(int64_t m, int n, int k) {
     const int side = n >= 256 && k >= 256 ? 256 : 128;
     const int64_t tiles = ceil_div(n, side) * ceil_div(k, side);
-    int64_t r = ceil_div(m * tiles, side == 256 ? 512 : 1024);
+    int64_t r = ceil_div(m * tiles, side == 128 ? 1024 : (n % 8 == 0 && k % 8 == 0 ? 256 : 512));
     if (r < 256) r = 256;
     if (r > m) r = m < 1 ? 1 : m;
     return (uint32_t)r;
