@@ -10,7 +10,10 @@
 // (the gradient of x is dout itself).  act: u, 1 / (1 + exp(-u)), or
 // u / (1 + exp(-u)), as the gates of [MTGR] section 4's encoder (silu) are.
 //
-// Bound: bytes, as norm.hip.
+// Bound: bytes, and in the backward pass instructions, as norm.hip.  16,384
+// bf16 rows of 4,096: forward 121 us (537 MB: 4.4 TB/s), backward 167 us (671
+// MB: 4.0 TB/s); 426,000 rows of 128 in 26 groups, fp32 residual, e4m3 copies:
+// 151 us (766 MB: 5.1 TB/s) and 153 us (548 MB: 3.6 TB/s).
 #include "dense.h"
 
 namespace htl {

