@@ -568,7 +568,9 @@ htl_status emb_grad_segment_sum_adam(htl_table* t, const int32_t* slots, const f
  * Shared by all of them:
  *   - Rows are row-major with a row stride in elements (ld >= row length);
  *     outputs are dense.  Any row length and alignment of at least the
- *     element size is right; row lengths in multiples of 8 with 16-byte aligned rows are fast.
+ *     element size is right.  Products are fastest where rows are 16-byte
+ *     aligned, row lengths are multiples of 8 (fp32: 4) and an operand spans
+ *     less than 4 GiB; the norms take any row length about as well.
  *   - Statistics, sums and products accumulate in fp32; a bf16 result is
  *     rounded once, to nearest even.  Results depend on the inputs alone,
  *     not on the order in which workgroups run.

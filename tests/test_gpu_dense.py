@@ -657,3 +657,31 @@ def test_norms_over_many_rows(htl, m, dim, g):
     _close(dz, gz, err + 3 * U * gz.abs() + 1e-37, "dz")
     _close(dw, *_sum_of(t * N.n, t.abs() * N.e_n + 20 * U * (t * N.n).abs(), ids, g), "dweight")
     _close(db, *_sum_of(t, 20 * U * t.abs(), ids, g), "dbias")
+
+
+def test_product_gradients_against_differences(htl):
+    """f = sum(c y) is linear in each of x and w, so central differences are exact but for rounding: y is off by
+    (k + 2) u of the products' magnitudes, twice, over 2 h; a gradient by its own sum's (rows or n, below 32 terms)."""
+    m, k, n, g, h = 9, 24, 10, 2, 0.125
+    gen = torch.Generator().manual_seed(7)
+    ids = np.array([0, 1, 1, -1, 0, 1, 0, 5, 1], np.int32)
+    plan = _plan(htl, ids, g)
+    x, w, c = torch.randn(m, k, generator=gen), torch.randn(g, n, k, generator=gen), torch.randn(m, n, generator=gen)
+
+    def f(x, w):
+        return htl.grouped_mm(x.cuda(), w.cuda(), plan).cpu().double().mul(c).sum()
+
+    dx, dw = htl.grouped_mm_backward(c.cuda(), x.cuda(), w.cuda(), plan)
+    size = sum(float((c[r].double().abs() @ (w[int(i)].double().abs() + h) @ (x[r].double().abs() + h)))
+               for r, i in enumerate(ids) if 0 <= i < g)
+    tol = (k + 2) * U * size / h + 40 * U * size
+    for arg, grad in ((0, dx), (1, dw)):
+        base = (x, w)[arg]
+        for flat in (0, 5, k + 3, 3 * k + 1, 7 * k, base.numel() - 1):
+            at = np.unravel_index(flat, base.shape)
+            up, dn = base.clone(), base.clone()
+            up[at] += h
+            dn[at] -= h
+            args = [(up, w), (dn, w)] if arg == 0 else [(x, up), (x, dn)]
+            want = float((f(*args[0]) - f(*args[1])) / ((up[at] - dn[at]).double()))
+            assert abs(float(grad[at]) - want) <= tol, (arg, at, float(grad[at]), want, tol)
