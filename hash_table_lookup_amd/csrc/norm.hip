@@ -178,13 +178,17 @@ __global__ __launch_bounds__(H::kThreads) void k_norm_back(NormBackArgs a) {
 #pragma unroll
         for (int i = 0; i < H::I; ++i) {
             float add[8];
-            if (a.dres.p) unpack8(a.dres, res[i], add);
+            if (a.dres.p) {
+                unpack8(a.dres, res[i], add);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float g = grouped ? r * (d[i][j] - c1 - v[i][j] * c2) : 0.0f;   // (the same for the whole chunk)
-                d[i][j] = a.dres.p ? add[j] + g : g;
+                for (int j = 0; j < 8; ++j) add[j] = 0.0f;
             }
-            if (in) store8<TR>(a.dx, at, (i * H::L + tl) * 8, a.dim, d[i]);
+            if (grouped) {                   // (the same for the whole chunk)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) add[j] += r * (d[i][j] - c1 - v[i][j] * c2);
+            }
+            if (in) store8<TR>(a.dx, at, (i * H::L + tl) * 8, a.dim, add);
         }
     }
     if (!grouped) return;
