@@ -11,9 +11,9 @@
 // u / (1 + exp(-u)), as the gates of [MTGR] section 4's encoder (silu) are.
 //
 // Bound: bytes, and in the backward pass instructions, as norm.hip.  16,384
-// bf16 rows of 4,096: forward 121 us (537 MB: 4.4 TB/s), backward 167 us (671
-// MB: 4.0 TB/s); 426,000 rows of 128 in 26 groups, fp32 residual, e4m3 copies:
-// 151 us (766 MB: 5.1 TB/s) and 153 us (548 MB: 3.6 TB/s).
+// bf16 rows of 4,096: forward 104-120 us (537 MB: 4.5-5.2 TB/s), backward 150-171
+// (671 MB: 3.9-4.5 TB/s); 426,000 rows of 128 in 26 groups, fp32 residual, e4m3
+// copies: 147-152 us (766 MB: 5.0-5.2 TB/s) and 141-157 (548 MB: 3.5-3.9 TB/s).
 #include "dense.h"
 
 namespace htl {
