@@ -18,6 +18,7 @@ from ._binding import _TORCH_DTYPE, _check, _dev, _dtype_code, _ptr, _stream, _w
 _FMT = {"i8": 0, "e4m3": 1}
 _KIND = {"rms": 0, "layer": 1}
 _ACT = {"none": 0, "sigmoid": 1, "silu": 2}
+_INT32 = torch.int32
 
 
 class RowGroups(NamedTuple):
@@ -90,13 +91,24 @@ def _params(weight, bias, groups, dim: int):
     return out[0], out[1], n
 
 
-def _plan(groups: Optional[RowGroups], m: int):
-    """Pointers (ids, order, offsets) of a plan for m rows."""
+def _index(t: Optional[torch.Tensor], n: int, name: str) -> Optional[torch.Tensor]:
+    if t is None:
+        return None
+    if t.dtype is not _INT32 or t.numel() != n or not t.is_cuda:
+        raise ValueError(f"groups.{name} must be a GPU tensor of {n} int32, got {t.numel()} {t.dtype} on {t.device}")
+    return t.contiguous()
+
+
+def _ids(groups: Optional[RowGroups], m: int) -> Optional[torch.Tensor]:
+    """Each row's group, for m rows."""
+    return None if groups is None else _index(groups.ids, m, "ids")
+
+
+def _plan(groups: Optional[RowGroups], m: int) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """(order, offsets) of a plan for m rows."""
     if groups is None:
-        return None, None, None
-    if groups.ids.numel() != m:
-        raise ValueError(f"the groups are of {groups.ids.numel()} rows, the tensors of {m}")
-    return _ptr(groups.ids), _ptr(groups.order), _ptr(groups.offsets)
+        return None, None
+    return _index(groups.order, m, "order"), _index(groups.offsets, groups.n_groups + 1, "offsets")
 
 
 def _new_rows8(m: int, dim: int, fmt: str, dtype, device) -> Rows8:
@@ -166,13 +178,13 @@ def norm_rows(x: Union[torch.Tensor, Rows8], weight: torch.Tensor, bias: Optiona
         src, scales, fmt = x, None, 0
     m, dim = src.shape
     weight, bias, n = _params(weight, bias, groups, dim)
-    ids, _, _ = _plan(groups, m)
+    ids = _ids(groups, m)
     code = _dtype_code(x.dtype if out_dtype is None else out_dtype)
     kept = x if save is None else _new_rows8(m, dim, save, x.dtype, src.device)
     codes, out_scales = (None, None) if save is None else (kept.codes, kept.scales)
     y = torch.empty((m, dim), dtype=_TORCH_DTYPE[code], device=src.device)
     _check(lib().norm_rows(_ptr(src), _dtype_code(x.dtype), ld, _ptr(scales), fmt, m, dim, _ptr(weight), _ptr(bias),
-                           ids, n, kind_code, eps, _ptr(y), code, _ptr(codes), _ptr(out_scales),
+                           _ptr(ids), n, kind_code, eps, _ptr(y), code, _ptr(codes), _ptr(out_scales),
                            0 if save is None else _FMT[save], _stream()))
     return y, kept
 
@@ -195,7 +207,7 @@ def norm_rows_backward(dy: torch.Tensor, kept: Union[torch.Tensor, Rows8], weigh
     m, dim = src.shape
     res, ld_res = (None, 0) if dresidual is None else _rows(dresidual, "dresidual", src, kept.dtype)
     weight, _, n = _params(weight, None, groups, dim)
-    _, order, offsets = _plan(groups, m)
+    order, offsets = _plan(groups, m)
     d = src.device
     dx = torch.empty((m, dim), dtype=kept.dtype, device=d)
     dweight = torch.empty((n, dim), dtype=torch.float32, device=d)
@@ -203,8 +215,9 @@ def norm_rows_backward(dy: torch.Tensor, kept: Union[torch.Tensor, Rows8], weigh
     nb = lib().norm_back_workspace_bytes(m, n, dim)
     ws = _scratch("norm_back", nb, d)
     _check(lib().norm_rows_backward(_ptr(dy), _dtype_code(dy.dtype), ld_dy, _ptr(src), _dtype_code(kept.dtype), ldx,
-                                    _ptr(scales), fmt, _ptr(res), ld_res, m, dim, _ptr(weight), order, offsets, n,
-                                    kind_code, eps, _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws), nb, _stream()))
+                                    _ptr(scales), fmt, _ptr(res), ld_res, m, dim, _ptr(weight), _ptr(order),
+                                    _ptr(offsets), n, kind_code, eps, _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws),
+                                    nb, _stream()))
     return dx, dweight, dbias
 
 
@@ -221,7 +234,7 @@ def norm_gate(x: torch.Tensor, z: torch.Tensor, gate: torch.Tensor, weight: torc
     gate, ldu = _rows(gate, "gate", x, z.dtype)
     m, dim = x.shape
     weight, bias, n = _params(weight, bias, groups, dim)
-    ids, _, _ = _plan(groups, m)
+    ids = _ids(groups, m)
     kept_z, kept_u = z, gate
     codes = (None,) * 4
     if save is not None:
@@ -230,7 +243,7 @@ def norm_gate(x: torch.Tensor, z: torch.Tensor, gate: torch.Tensor, weight: torc
         codes = (kept_z.codes, kept_z.scales, kept_u.codes, kept_u.scales)
     out = torch.empty((m, dim), dtype=x.dtype, device=x.device)
     _check(lib().norm_gate(_ptr(x), _dtype_code(x.dtype), ldx, _ptr(z), ldz, _ptr(gate), ldu, _dtype_code(z.dtype), m,
-                           dim, _ptr(weight), _ptr(bias), ids, n, kind_code, eps, act_code, scale, _ptr(out),
+                           dim, _ptr(weight), _ptr(bias), _ptr(ids), n, kind_code, eps, act_code, scale, _ptr(out),
                            *(_ptr(c) for c in codes), 0 if save is None else _FMT[save], _stream()))
     return out, kept_z, kept_u
 
@@ -261,7 +274,7 @@ def norm_gate_backward(dout: torch.Tensor, kept_z: Union[torch.Tensor, Rows8], k
     dout, ld = _rows(dout, "dout", z)
     m, dim = z.shape
     weight, bias, n = _params(weight, bias, groups, dim)
-    _, order, offsets = _plan(groups, m)
+    order, offsets = _plan(groups, m)
     d = z.device
     dz = torch.empty((m, dim), dtype=dtype, device=d)
     du = torch.empty((m, dim), dtype=dtype, device=d)
@@ -270,9 +283,9 @@ def norm_gate_backward(dout: torch.Tensor, kept_z: Union[torch.Tensor, Rows8], k
     nb = lib().norm_back_workspace_bytes(m, n, dim)
     ws = _scratch("norm_back", nb, d)
     _check(lib().norm_gate_backward(_ptr(dout), _dtype_code(dout.dtype), ld, _ptr(z), ldz, _ptr(zs), _ptr(u), ldu,
-                                    _ptr(us), _dtype_code(dtype), fmt, m, dim, _ptr(weight), _ptr(bias), order,
-                                    offsets, n, kind_code, eps, act_code, scale, _ptr(dz), _ptr(du), _ptr(dweight),
-                                    _ptr(dbias), _ptr(ws), nb, _stream()))
+                                    _ptr(us), _dtype_code(dtype), fmt, m, dim, _ptr(weight), _ptr(bias), _ptr(order),
+                                    _ptr(offsets), n, kind_code, eps, act_code, scale, _ptr(dz), _ptr(du),
+                                    _ptr(dweight), _ptr(dbias), _ptr(ws), nb, _stream()))
     return dz, du, dweight, dbias
 
 
@@ -297,11 +310,11 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, groups: Optional[RowGroups] = N
     n = w.shape[1]
     if w.shape[2] != k:
         raise ValueError(f"x has rows of {k}, w of {w.shape[2]}")
-    _, order, offsets = _plan(groups, m)
+    order, offsets = _plan(groups, m)
     code = _dtype_code(x.dtype if out_dtype is None else out_dtype)
     y = torch.empty((m, n), dtype=_TORCH_DTYPE[code], device=x.device)
-    _check(lib().grouped_mm(_ptr(x), ldx, _ptr(w), _dtype_code(x.dtype), m, n, k, order, offsets, g, _ptr(y), code,
-                            _stream()))
+    _check(lib().grouped_mm(_ptr(x), ldx, _ptr(w), _dtype_code(x.dtype), m, n, k, _ptr(order), _ptr(offsets), g,
+                            _ptr(y), code, _stream()))
     return y
 
 
@@ -315,13 +328,13 @@ def grouped_mm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, grou
     n = w.shape[1]
     if w.shape[2] != k or tuple(dy.shape) != (m, n):
         raise ValueError(f"dy {tuple(dy.shape)}, x {tuple(x.shape)} and w {tuple(w.shape)} do not fit")
-    _, order, offsets = _plan(groups, m)
+    order, offsets = _plan(groups, m)
     code = _dtype_code(dy.dtype if dx_dtype is None else dx_dtype)
     d = x.device
     dx = torch.empty((m, k), dtype=_TORCH_DTYPE[code], device=d) if need_dx else None
     dw = torch.empty((g, n, k), dtype=torch.float32, device=d) if need_dw else None
     nb = lib().grouped_mm_backward_workspace_bytes(m, g, n, k) if need_dw else 0
     ws = _scratch("grouped_mm_backward", nb, d) if need_dw else None
-    _check(lib().grouped_mm_backward(_ptr(dy), ld_dy, _ptr(x), ldx, _ptr(w), _dtype_code(x.dtype), m, n, k, order,
-                                     offsets, g, _ptr(dx), code, _ptr(dw), _ptr(ws), nb, _stream()))
+    _check(lib().grouped_mm_backward(_ptr(dy), ld_dy, _ptr(x), ldx, _ptr(w), _dtype_code(x.dtype), m, n, k, _ptr(order),
+                                     _ptr(offsets), g, _ptr(dx), code, _ptr(dw), _ptr(ws), nb, _stream()))
     return dx, dw

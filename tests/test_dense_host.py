@@ -124,3 +124,37 @@ def test_binding_refuses():
         htl.norm_rows(r._replace(fmt="i8"), w, save="i8")
     with pytest.raises(ValueError, match="both"):
         htl.norm_gate_backward(x, r._replace(fmt="i8"), x, w)
+
+
+class _OnGpu:
+    """What the checks of a plan ask of a tensor."""
+    is_cuda, device = True, "cuda:0"
+
+    def __init__(self, n, dtype=torch.int32):
+        self.n, self.dtype = n, dtype
+
+    def numel(self):
+        return self.n
+
+    def contiguous(self):
+        return self
+
+
+def test_plans_are_checked():
+    """A plan's tensors are read by address: their type, size and place are checked before."""
+    import hash_table_lookup_amd as htl
+    from hash_table_lookup_amd import dense
+    good = htl.RowGroups(_OnGpu(6), _OnGpu(6), _OnGpu(4), 3)
+    assert dense._ids(good, 6) is good.ids and dense._plan(good, 6) == (good.order, good.offsets)
+    assert dense._plan(good._replace(order=None), 6) == (None, good.offsets)
+    assert dense._ids(None, 6) is None and dense._plan(None, 6) == (None, None)
+    for bad in (_OnGpu(6, torch.int64), _OnGpu(5), _OnGpu(7), torch.zeros(6, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="groups.ids must be a GPU tensor of 6 int32"):
+            dense._ids(good._replace(ids=bad), 6)
+        with pytest.raises(ValueError, match="groups.order must be a GPU tensor of 6 int32"):
+            dense._plan(good._replace(order=bad), 6)
+    for bad in (_OnGpu(4, torch.int64), _OnGpu(3), _OnGpu(5), torch.zeros(4, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="groups.offsets must be a GPU tensor of 4 int32"):
+            dense._plan(good._replace(offsets=bad), 6)
+    with pytest.raises(ValueError, match="offsets"):
+        dense._plan(good._replace(n_groups=5), 6)

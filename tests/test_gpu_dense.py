@@ -685,3 +685,36 @@ def test_product_gradients_against_differences(htl):
             args = [(up, w), (dn, w)] if arg == 0 else [(x, up), (x, dn)]
             want = float((f(*args[0]) - f(*args[1])) / ((up[at] - dn[at]).double()))
             assert abs(float(grad[at]) - want) <= tol, (arg, at, float(grad[at]), want, tol)
+
+
+# ------------------------------------------------------- plans of one's own --
+def test_plans_of_other_types_and_sizes_are_refused(htl):
+    """What torch's own sorts and sums give (int64), and plans of other rows, are refused before a launch; strided
+    int32 tensors are read as what they hold."""
+    m, g, k = 90, 3, 16
+    gen = torch.Generator().manual_seed(11)
+    plan = _plan(htl, _ids(np.random.default_rng(3), m, g, "dropped"), g)
+    x = torch.randn(m, k, generator=gen).cuda()
+    w, p = torch.randn(g, k, k, generator=gen).cuda(), torch.ones(g, k, device="cuda")
+    forward = (lambda q: htl.norm_rows(x, p, groups=q)[0], lambda q: htl.norm_gate(x, x, x, p, groups=q)[0])
+    planned = (lambda q: htl.grouped_mm(x, w, q), lambda q: htl.grouped_mm_backward(x, x, w, q)[1],
+               lambda q: htl.norm_rows_backward(x, x, p, groups=q)[1], lambda q: htl.norm_gate_backward(x, x, x, p, groups=q)[2])
+    for f in forward:
+        for bad in (plan.ids.long(), plan.ids[:-1], plan.ids.cpu()):
+            with pytest.raises(ValueError, match="groups.ids"):
+                f(plan._replace(ids=bad))
+    for f in planned:
+        for bad in (plan.order.long(), plan.order[:-1], plan.order.cpu()):
+            with pytest.raises(ValueError, match="groups.order"):
+                f(plan._replace(order=bad))
+        for bad in (plan.offsets.long(), plan.offsets[:-1], plan.offsets.cpu()):
+            with pytest.raises(ValueError, match="groups.offsets"):
+                f(plan._replace(offsets=bad))
+
+    def strided(t):
+        return torch.stack([t, torch.full_like(t, -7)], 1)[:, 0]
+
+    wide = htl.RowGroups(strided(plan.ids), strided(plan.order), strided(plan.offsets), g)
+    assert not wide.order.is_contiguous()
+    for f in forward + planned:
+        assert torch.equal(f(wide), f(plan))
