@@ -19,6 +19,7 @@ _FMT = {"i8": 0, "e4m3": 1}
 _KIND = {"rms": 0, "layer": 1}
 _ACT = {"none": 0, "sigmoid": 1, "silu": 2}
 _INT32 = torch.int32
+_INT_MAX = 2**31 - 1          # of the library's group counts and row lengths
 
 
 class RowGroups(NamedTuple):
@@ -70,6 +71,8 @@ def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None, dtype
     if like is not None and shape != like.shape:
         raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(shape)}")
     m, n = shape
+    if n > _INT_MAX:
+        raise ValueError(f"{name} must have rows of at most {_INT_MAX} elements, got {n}")
     ld, step = t.stride()
     if n > 1 and step != 1 or m > 1 and ld < n:
         t, ld = t.contiguous(), n
@@ -124,11 +127,15 @@ def _check_rows8(r: Rows8, name: str) -> Rows8:
     codes, scales = _dev(r.codes, torch.uint8, name + ".codes"), _dev(r.scales, torch.uint8, name + ".scales")
     if codes.dim() != 2 or tuple(scales.shape) != (codes.shape[0], (codes.shape[1] + 31) // 32):
         raise ValueError(f"{name}: scales must have shape [rows, ceil(dim / 32)]")
+    if codes.shape[1] > _INT_MAX:
+        raise ValueError(f"{name} must have rows of at most {_INT_MAX} elements, got {codes.shape[1]}")
     return Rows8(codes, scales, r.fmt, r.dtype)
 
 
 def group_rows(ids: torch.Tensor, n_groups: int) -> RowGroups:
     """The plan of rows by group: a stable sort of ``ids`` (int32), rows of no group last (row_groups)."""
+    if n_groups > _INT_MAX:
+        raise ValueError(f"n_groups must be at most {_INT_MAX}, got {n_groups}")
     ids = _dev(ids, torch.int32, "ids").view(-1)
     m, d = ids.numel(), ids.device
     order = torch.empty(m, dtype=torch.int32, device=d)
@@ -296,6 +303,8 @@ def _weights(w: torch.Tensor, groups: Optional[RowGroups], dtype) -> Tuple[torch
         w = w.unsqueeze(0)
     if w.dim() != 3 or w.shape[0] != n:
         raise ValueError(f"w must have shape [{n}, n, k], got {tuple(w.shape)}")
+    if w.shape[1] > _INT_MAX:
+        raise ValueError(f"w must have at most {_INT_MAX} outputs, got {w.shape[1]}")
     return w, n
 
 

@@ -158,3 +158,32 @@ def test_plans_are_checked():
             dense._plan(good._replace(offsets=bad), 6)
     with pytest.raises(ValueError, match="offsets"):
         dense._plan(good._replace(n_groups=5), 6)
+
+
+class _Shaped(_OnGpu):
+    def __init__(self, shape, dtype):
+        super().__init__(0, dtype)
+        self.shape = shape
+
+    def stride(self):
+        return self.shape[-1], 1
+
+    def dim(self):
+        return len(self.shape)
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Row lengths and group counts go to the library as int32: none may be cut to its low bits on the way."""
+    import hash_table_lookup_amd as htl
+    from hash_table_lookup_amd import dense
+    big = 2**32 + 8
+    with pytest.raises(ValueError, match="n_groups"):
+        htl.group_rows(torch.zeros(4, dtype=torch.int32), big)
+    assert dense._rows(_Shaped((2, 8), torch.float32), "x")[1] == 8
+    with pytest.raises(ValueError, match="rows of at most"):
+        dense._rows(_Shaped((2, big), torch.float32), "x")
+    with pytest.raises(ValueError, match="at most .* outputs"):
+        dense._weights(_Shaped((1, big, 1), torch.float32), None, torch.float32)
+    kept = htl.Rows8(_Shaped((2, big), torch.uint8), _Shaped((2, (big + 31) // 32), torch.uint8), "i8", torch.float32)
+    with pytest.raises(ValueError, match="rows of at most"):
+        dense._check_rows8(kept, "kept")
