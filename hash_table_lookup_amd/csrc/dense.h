@@ -126,8 +126,10 @@ __device__ __forceinline__ void unpack8(const RowsIn&, const Raw8<kSrcBf16>& r, 
 // The 8-bit row format.  A block of 32 elements of one row shares the scale
 // 2^e, with e >= -126 the least that brings the block's largest magnitude to
 // at most 127 (HTL_ROWS8_I8) or 448 (HTL_ROWS8_E4M3); an element x is kept as
-// the nearest integer, or the nearest e4m3 number, to x / 2^e, ties to even.
-// The scale byte is e + 127 (1..248), or 255 for a block that holds an
+// the nearest integer, or the nearest e4m3 number, to x / 2^e, ties to even,
+// or as the nearest that stands for a finite value: with the largest scales
+// 64 * 2^122 and 256 * 2^120 would be infinities, so 63 and 240 are the last.
+// The scale byte is e + 127 (1..249), or 255 for a block that holds an
 // infinity or a NaN, which reads back as NaN throughout.  A power of two
 // costs up to one bit of the code's range against a free scale, and in
 // return multiplying by it is exact: codes times scales have at most 8
@@ -237,6 +239,14 @@ __device__ __forceinline__ void save8(const Rows8Out& r, int64_t row, int col, i
                 int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h] * inv, v[4 * h + 1] * inv, 0, false);
                 w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2] * inv, v[4 * h + 3] * inv, w, true);
                 c[h] = (uint32_t)w;
+            }
+        }
+        if (e > (i8 ? 121 : 119)) {      // +-64 (0x40, 0xC0) to +-63, or +-256 (0x78, 0xF8) to +-240
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t w = c[h], ones = 0x01010101u;
+                if (i8) c[h] = w - (w >> 6 & ~(w >> 7) & ones) + (w >> 7 & ~((w & 63u * ones) + 63u * ones >> 6) & ones);
+                else c[h] = w - (w >> 6 & w >> 5 & w >> 4 & w >> 3 & ones);
             }
         }
     }

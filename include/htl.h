@@ -603,7 +603,8 @@ htl_status row_groups(const int32_t* ids, int64_t m, int n_groups, int32_t* orde
  * of 32 elements of a row (the last may be shorter) shares the scale 2^e, e
  * >= -126 the least with which its largest magnitude is at most 127 * 2^e
  * (HTL_ROWS8_I8) or 448 * 2^e (HTL_ROWS8_E4M3); an element is kept as the
- * nearest integer, or e4m3 number, to x / 2^e (ties to even).
+ * nearest integer, or e4m3 number, to x / 2^e (ties to even), or the nearest
+ * that stands for a finite fp32 value.
  *   x, y     dtype[m][dim], 1 <= dim <= 65536; ldx the row stride of x.
  *   codes    uint8[m][dim]; scales uint8[m][ceil(dim / 32)]: e + 127, or 255
  *            for a block with an infinity or NaN, which reads back as NaN.

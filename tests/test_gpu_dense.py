@@ -718,3 +718,31 @@ def test_plans_of_other_types_and_sizes_are_refused(htl):
     assert not wide.order.is_contiguous()
     for f in forward + planned:
         assert torch.equal(f(wide), f(plan))
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows8_keeps_the_largest_values_finite(htl, fmt, dtype):
+    """Up to the largest finite number: the nearest code, or the last one whose value is finite (63 * 2^122 in
+    integers, 240 * 2^120 in e4m3), by saving alone and beside a norm."""
+    most = torch.finfo(dtype).max
+    top = torch.tensor([most, 3.39e38, 3.38e38, 3.377e38, 3.375e38, 3.35e38, 3.3e38, 3.29e38, 3.0e38, 2.98e38, 2.97e38,
+                        1.7e38], dtype=torch.float64)
+    gen = torch.Generator().manual_seed(12)
+    x = torch.rand(2 * len(top), 70, generator=gen, dtype=torch.float64) * 2 - 1
+    x *= torch.cat([top, top])[:, None]
+    x[:len(top), 3], x[len(top):, 40] = top, -top
+    x[0, 64:] = most
+    x = x.clamp(-most, most).to(dtype)
+    assert torch.isfinite(x).all()
+    want, scales = _rows8(x, fmt)
+    last = 63.0 * 2.0**122 if fmt == "i8" else 240.0 * 2.0**120
+    big = scales.repeat_interleave(32, 1)[:, :70] == (249 if fmt == "i8" else 247)
+    assert big.any() and (want[big].abs() > last).any()
+    want = torch.where(big, want.clamp(-last, last), want)
+    w = torch.ones(70).cuda()
+    for kept in (htl.save_rows8(x.cuda(), fmt), htl.norm_rows(x.cuda(), w, save=fmt)[1],
+                 htl.norm_gate(x.cuda(), x.cuda(), x.cuda(), w, save=fmt)[2]):
+        assert torch.equal(kept.scales.cpu(), scales)
+        for out in (torch.float32, torch.bfloat16):
+            assert torch.equal(htl.load_rows8(kept, out).cpu().double(), want)
