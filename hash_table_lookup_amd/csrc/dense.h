@@ -344,17 +344,23 @@ template <class F> void with_hold(int dim, F&& f) {
 }
 
 // 1 / deviation and, in v, the centred and scaled row: v <- (v - [mean]) * r.
-// The mean is taken out before the squares are summed, both in fp32: a row
-// far from zero keeps its deviation.
+// The mean is taken out before the squares are summed, so a row far from zero
+// keeps its deviation.  The mean itself is off by the rounding of its sum,
+// which is in units of the row's distance from zero: at 10,000 it would be
+// 1e-3, beside deviations as small as that.  So what is left of it after the
+// first subtraction is summed with the squares and taken out too:
+//   c = x - mean,  v = c - mean(c),  var = mean(c^2) - mean(c)^2.
 template <class H>
 __device__ __forceinline__ float normalize(float v[][8], bool center, int tl, int dim, float eps, Sums& sums) {
+    float var, rest = 0.0f;
     if (center) {
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < H::I; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) s += v[i][j];
-        const float mean = team_sum<H::L>(s, sums) / (float)dim;   // divided: exact for a constant row
+        const float mean = team_sum<H::L>(s, sums) / (float)dim;   // divided: exact for a constant row of few bits
+        float cq[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < H::I; ++i) {
             const int col = (i * H::L + tl) * 8;
@@ -366,18 +372,30 @@ __device__ __forceinline__ float normalize(float v[][8], bool center, int tl, in
                 for (int j = 0; j < 8; ++j)
                     if (col + j >= dim) v[i][j] = 0.0f;
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                cq[0] += v[i][j];
+                cq[1] += v[i][j] * v[i][j];
+            }
         }
+        team_sums<H::L>(cq, sums);
+        const float inv_dim = 1.0f / (float)dim;                   // (the same for every row)
+        rest = cq[0] * inv_dim;
+        var = __builtin_fmaf(-rest, rest, cq[1] * inv_dim);        // (an infinite sum of squares stays one)
+        var = var < 0.0f ? 0.0f : var;
+    } else {
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < H::I; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q += v[i][j] * v[i][j];
+        var = team_sum<H::L>(q, sums) / (float)dim;
     }
-    float q = 0.0f;
+    const float r = 1.0f / sqrtf(var + eps), shift = rest != 0.0f ? -rest * r : -0.0f;   // (r may be infinite)
 #pragma unroll
     for (int i = 0; i < H::I; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q += v[i][j] * v[i][j];
-    const float r = 1.0f / sqrtf(team_sum<H::L>(q, sums) / (float)dim + eps);
-#pragma unroll
-    for (int i = 0; i < H::I; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] *= r;
+        for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(v[i][j], r, shift);
     return r;
 }
 

@@ -746,3 +746,72 @@ def test_rows8_keeps_the_largest_values_finite(htl, fmt, dtype):
         assert torch.equal(kept.scales.cpu(), scales)
         for out in (torch.float32, torch.bfloat16):
             assert torch.equal(htl.load_rows8(kept, out).cpu().double(), want)
+
+
+# ------------------------------------------------------ rows far from zero --
+class FarNorm(Norm):
+    """A layer norm whose mean is taken out in two steps, the second by the sum of what the first left.
+
+    A lane adds up at most 16 elements, then 64 lanes in 6 steps, then 16 waves: no element goes through more than
+    h = 40 additions, so a sum is off by h u of its magnitudes.  With A the row's mean magnitude, the first mean is off
+    by at most s = (h + 4) u A, so what is summed then is of size C = s + |x - mean|, and the centre is off by (h + 5) u
+    mean(C), an element by 3 u C beside.  The squares' mean, var + s^2 at most, is off by (h + 12) u of itself: e_r,
+    relative, is how far 1 / deviation is off."""
+
+    def __init__(self, x):
+        super().__init__(x, "layer")
+        x = x.double()
+        h = min(x.shape[1], 40)
+        dev = (x - x.mean(1, keepdim=True)).abs()
+        var = (dev * dev).mean(1, keepdim=True)
+        s = (h + 4) * U * x.abs().mean(1, keepdim=True)
+        size = s + dev
+        self.e_r = (h + 12) * U * (var + s * s) / (var + EPS) + 4 * U
+        self.e_n = self.r * ((h + 5) * U * size.mean(1, keepdim=True) + 3 * U * size) + self.n.abs() * (self.e_r + 4 * U)
+
+    def back(self, dn, e_dn):
+        g, e = super().back(dn, e_dn)
+        return g, e + self.e_r * g.abs()
+
+
+@pytest.mark.parametrize("dim", [7, 77, 100, 128, 250, 500, 1000, 2000, 4100, 5001, 9000])
+@pytest.mark.parametrize("save", [None, "i8"])
+def test_layer_norm_far_from_zero(htl, dim, save):
+    """Constant rows and rows of small deviation, far from zero: n is 0, or the deviation's own, not what the
+    rounding of the mean leaves."""
+    gen = torch.Generator().manual_seed(dim)
+    far = torch.tensor([1000.1, 10000.1, 54321.7, -10000.1, 777777.7, 0.1])
+    rows = [far[:, None].expand(6, dim)]
+    rows += [far[:, None] + s * far[:, None].abs() * torch.randn(6, dim, generator=gen) for s in (1e-6, 1e-4, 1e-2)]
+    x = torch.cat(rows)
+    m, g = x.shape[0], 2
+    ids = (np.arange(m) % g).astype(np.int32)
+    plan = _plan(htl, ids, g)
+    weight, b = 1 + 0.1 * torch.randn(g, dim, generator=gen), 0.1 * torch.randn(g, dim, generator=gen)
+    w, bw = weight.double()[ids.astype(np.int64)], b.double()[ids.astype(np.int64)]
+    dy = torch.randn(m, dim, generator=gen)
+    kw = dict(groups=plan, kind="layer", eps=EPS)
+    y, kept = htl.norm_rows(x.cuda(), weight.cuda(), b.cuda(), save=save, **kw)
+    out, kz, ku = htl.norm_gate(dy.cuda(), x.cuda(), dy.cuda(), weight.cuda(), b.cuda(), act="none", save=save, **kw)
+    N = FarNorm(x)
+    e_v = w.abs() * N.e_n + 2 * U * ((N.n * w).abs() + bw.abs())
+    v = N.n * w + bw
+    _close(y, v, e_v + U * v.abs(), "y")
+    assert float(N.e_n[:5].max()) < 0.05                       # what is told apart: they were off by up to 1
+    d = dy.double()
+    _close(out, d + d * v, d.abs() * e_v + 4 * U * (d * v).abs() + 2 * U * d.abs(), "out")
+    src = x if save is None else _rows8(x, save)[0]
+    us = dy if save is None else _rows8(dy, save)[0]
+    N = FarNorm(src)
+    dx, dw, db = htl.norm_rows_backward(dy.cuda(), kept, weight.cuda(), bias=True, **kw)
+    gx, e = N.back(d * w, U * (d * w).abs())
+    _close(dx, gx, e + 3 * U * gx.abs(), "dx")
+    _close(dw, *_sum_of(d * N.n, d.abs() * N.e_n, ids, g), "dweight")
+    dz, du, dw, db = htl.norm_gate_backward(dy.cuda(), kz, ku, weight.cuda(), b.cuda(), act="none", **kw)
+    t = d * us.double()
+    gz, e = N.back(t * w, 3 * U * (t * w).abs())
+    _close(dz, gz, e + 3 * U * gz.abs(), "dz")
+    v = N.n * w + bw
+    e_v = w.abs() * N.e_n + 2 * U * ((N.n * w).abs() + bw.abs())
+    _close(du, d * v, d.abs() * e_v + 4 * U * (d * v).abs(), "dgate")
+    _close(dw, *_sum_of(t * N.n, t.abs() * N.e_n + 3 * U * (t * N.n).abs(), ids, g), "dweight")
