@@ -455,15 +455,27 @@ __device__ __forceinline__ void group_range(const int32_t* offsets, int n_groups
 // the rows of no group follow as group n_groups.  count: chunks of the group.
 // All lanes of a wave call it together with the same arguments.  Returns
 // false past the last chunk.
+//
+// A group of one chunk writes its sums itself; the chunks of the others leave
+// partial sums, and slots number those chunks alone (split_chunks bounds
+// them), so that partial sums take room by the rows, however many groups
+// there are.
 struct Chunk {
     int g;
     int64_t beg, end;
     int index, count;       // which of the group's chunks
+    int64_t slot;           // of its partial sums, where count > 1
 };
+// Chunks of groups that have several, at most: such a group has more than R
+// rows, so there are at most m / R of them, each with one chunk that is not full.
+inline int64_t split_chunks(int64_t m, int n_groups, int64_t R) {
+    const int64_t full = m / R;
+    return full + (n_groups < full ? n_groups : full);
+}
 __device__ __forceinline__ bool find_chunk(const int32_t* offsets, int n_groups, int64_t m, uint32_t R, int min_chunks,
                                            int64_t item, Chunk& c) {
     const int lane = __lane_id();
-    int64_t run = 0;
+    int64_t run = 0, alone = 0;          // chunks before, and those that are their group's only one
     for (int g0 = 0; g0 <= n_groups; g0 += 64) {
         const int g = g0 + lane;
         int64_t beg = 0, end = 0;
@@ -479,9 +491,10 @@ __device__ __forceinline__ bool find_chunk(const int32_t* offsets, int n_groups,
             const int y = __shfl_up(incl, off);
             if (lane >= off) incl += y;
         }
-        const uint64_t past = __ballot(run + incl > item);
+        const uint64_t past = __ballot(run + incl > item), one = __ballot(cnt == 1);
         if (past) {
             const int l = __ffsll((unsigned long long)past) - 1;
+            c.slot = item - alone - __popcll(one & ((1ull << l) - 1));
             c.g = g0 + l;
             c.count = __shfl(cnt, l);
             c.index = (int)(item - run) - (__shfl(incl, l) - c.count);
@@ -491,11 +504,12 @@ __device__ __forceinline__ bool find_chunk(const int32_t* offsets, int n_groups,
             return true;
         }
         run += __shfl(incl, 63);
+        alone += __popcll(one);
     }
     return false;
 }
 
-// The first work item of group g and how many it has, as find_chunk numbers them.
+// The slot of group g's first chunk and how many it has, as find_chunk numbers them.
 __device__ __forceinline__ void chunks_of_group(const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
                                                 int min_chunks, int g, int64_t& first, int& count) {
     const int lane = __lane_id();
@@ -504,7 +518,7 @@ __device__ __forceinline__ void chunks_of_group(const int32_t* offsets, int n_gr
         int64_t beg, end;
         group_range(offsets, n_groups, m, q, beg, end);
         const int c = (int)(((uint32_t)(end - beg) + R - 1u) / R);
-        sum += c < min_chunks ? min_chunks : c;
+        sum += c > 1 ? c : 0;
     }
     int s = (int)sum;
 #pragma unroll
@@ -517,7 +531,7 @@ __device__ __forceinline__ void chunks_of_group(const int32_t* offsets, int n_gr
 }
 
 // Sums of a group's partial rows: out[g][d] = sum over its chunks of
-// partial[item][d], for the groups with more than one chunk (a lone chunk
+// partial[slot][d], for the groups with more than one chunk (a lone chunk
 // writes its sums itself).  Chunks are added in order, so the result does
 // not depend on which workgroup ended first.  limit: rows that partial holds;
 // a second set of sums (out2, nullable) has its partial rows after those.

@@ -19,6 +19,7 @@
 namespace htl {
 
 int64_t norm_chunks(int64_t m, int n_groups, int dim);
+int64_t norm_slots(int64_t m, int n_groups, int dim);
 uint32_t norm_rows_per_chunk(int64_t m, int dim);
 
 namespace {
@@ -129,8 +130,8 @@ struct GateBackArgs {
     const int32_t* offsets;  // nullable: one group
     float* dweight;          // [n_groups][dim]
     float* dbias;            // nullable
-    float* partial;          // [chunks][dim], dbias's after dweight's
-    int64_t chunks;
+    float* partial;          // [limit][dim], dbias's after dweight's
+    int64_t chunks, limit;
     int64_t m;
     int dim, n_groups, act;
     uint32_t rows;           // positions per chunk
@@ -231,10 +232,11 @@ __global__ __launch_bounds__(H::kThreads) void k_gate_back(GateBackArgs a) {
     }
     if (!grouped) return;
     const bool alone = c.count == 1;
-    const int64_t first = (int64_t)blockIdx.x * a.dim, whole = (int64_t)c.g * a.dim;
+    if (!alone && c.slot >= a.limit) return;                 // offsets that overlap
+    const int64_t first = c.slot * a.dim, whole = (int64_t)c.g * a.dim;
     write_columns<H>(sw, tl, a.dim, s_col, alone ? a.dweight + whole : a.partial + first);
     if (a.dbias)
-        write_columns<H>(sb, tl, a.dim, s_col, alone ? a.dbias + whole : a.partial + a.chunks * a.dim + first);
+        write_columns<H>(sb, tl, a.dim, s_col, alone ? a.dbias + whole : a.partial + a.limit * a.dim + first);
 }
 
 int elem(htl_dtype t) { return t == HTL_F32 ? 4 : 2; }
@@ -352,6 +354,7 @@ extern "C" htl_status norm_gate_backward(const void* dout, htl_dtype dout_dtype,
     a.partial = (float*)ws;
     a.rows = norm_rows_per_chunk(m, dim);
     a.chunks = norm_chunks(m, n_groups, dim);
+    a.limit = norm_slots(m, n_groups, dim);
     a.m = m;
     a.dim = dim;
     a.n_groups = n_groups;
@@ -376,5 +379,5 @@ extern "C" htl_status norm_gate_backward(const void* dout, htl_dtype dout_dtype,
     });
     const htl_status st = check_launch("norm_gate_backward");
     if (st != HTL_OK) return st;
-    return sum_chunks(a.partial, a.chunks, dweight, dbias, offsets, n_groups, m, a.rows, dim, stream);
+    return sum_chunks(a.partial, a.limit, dweight, dbias, offsets, n_groups, m, a.rows, dim, stream);
 }

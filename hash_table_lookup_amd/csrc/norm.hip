@@ -92,8 +92,8 @@ struct NormBackArgs {
     const int32_t* offsets;  // nullable: one group
     float* dweight;          // [n_groups][dim]
     float* dbias;            // nullable
-    float* partial;          // [chunks][dim], dbias's after dweight's
-    int64_t chunks;
+    float* partial;          // [limit][dim], dbias's after dweight's
+    int64_t chunks, limit;
     int64_t m;
     int dim, n_groups;
     uint32_t rows;           // positions per chunk
@@ -193,10 +193,11 @@ __global__ __launch_bounds__(H::kThreads) void k_norm_back(NormBackArgs a) {
     }
     if (!grouped) return;
     const bool alone = c.count == 1;
-    const int64_t first = (int64_t)blockIdx.x * a.dim, whole = (int64_t)c.g * a.dim;
+    if (!alone && c.slot >= a.limit) return;                 // offsets that overlap
+    const int64_t first = c.slot * a.dim, whole = (int64_t)c.g * a.dim;
     write_columns<H>(sw, tl, a.dim, s_col, alone ? a.dweight + whole : a.partial + first);
     if (a.dbias)
-        write_columns<H>(sb, tl, a.dim, s_col, alone ? a.dbias + whole : a.partial + a.chunks * a.dim + first);
+        write_columns<H>(sb, tl, a.dim, s_col, alone ? a.dbias + whole : a.partial + a.limit * a.dim + first);
 }
 
 // 64 columns per workgroup; its 16 waves take every 16th chunk of the group.
@@ -275,6 +276,7 @@ uint32_t norm_chunk_rows(int64_t m, int dim) {
 }  // namespace
 
 int64_t norm_chunks(int64_t m, int n_groups, int dim) { return m / norm_chunk_rows(m, dim) + n_groups + 1; }
+int64_t norm_slots(int64_t m, int n_groups, int dim) { return split_chunks(m, n_groups, norm_chunk_rows(m, dim)); }
 uint32_t norm_rows_per_chunk(int64_t m, int dim) { return norm_chunk_rows(m, dim); }
 
 htl_status sum_chunks(const float* partial, int64_t limit, float* out, float* out2, const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
@@ -363,8 +365,8 @@ extern "C" htl_status norm_rows(const void* x, htl_dtype x_dtype, int64_t ldx, c
 
 extern "C" size_t norm_back_workspace_bytes(int64_t m, int n_groups, int dim) {
     if (m < 0 || m > kMaxRows || n_groups < 1 || n_groups > kMaxGroups || dim < 1 || dim > kMaxNormDim) return 0;
-    // partial sums of the weight's and the bias's gradients, a row per chunk each
-    return align_up((size_t)(2 * norm_chunks(m, n_groups, dim) * dim) * 4, 256);
+    // partial sums of the weight's and the bias's gradients, a row per chunk of a split group each
+    return align_up((size_t)(2 * norm_slots(m, n_groups, dim) * dim) * 4 + 1, 256);
 }
 
 extern "C" htl_status norm_rows_backward(const void* dy, htl_dtype dy_dtype, int64_t ld_dy, const void* x,
@@ -403,6 +405,7 @@ extern "C" htl_status norm_rows_backward(const void* dy, htl_dtype dy_dtype, int
     a.partial = (float*)ws;
     a.rows = norm_rows_per_chunk(m, dim);
     a.chunks = norm_chunks(m, n_groups, dim);
+    a.limit = norm_slots(m, n_groups, dim);
     a.m = m;
     a.dim = dim;
     a.n_groups = n_groups;
@@ -425,5 +428,5 @@ extern "C" htl_status norm_rows_backward(const void* dy, htl_dtype dy_dtype, int
     });
     const htl_status st = check_launch("norm_rows_backward");
     if (st != HTL_OK) return st;
-    return sum_chunks(a.partial, a.chunks, dweight, dbias, offsets, n_groups, m, a.rows, dim, stream);
+    return sum_chunks(a.partial, a.limit, dweight, dbias, offsets, n_groups, m, a.rows, dim, stream);
 }

@@ -36,9 +36,9 @@ struct ProdArgs {
     int64_t m, lda, ldb;     // ldb: row stride of x in dw
     int n, k, n_groups;
     uint32_t rows;           // positions per chunk
-    float* partial;          // dw: [chunks][n][k]
+    float* partial;          // dw: [limit][n][k]
     int out_f32;
-    int64_t limit;           // dw: chunks that `partial` has room for
+    int64_t limit;           // dw: chunks of split groups that `partial` has room for
 };
 
 enum { kFwd = 0, kDx = 1, kDw = 2 };
@@ -322,7 +322,7 @@ __device__ __forceinline__ void multiply(const Frag<kSrcF32>& c, const Frag<kSrc
 struct TileAt {
     int g;
     int64_t beg, end;       // positions
-    int64_t chunk;          // among all groups' chunks
+    int64_t slot;           // of its partial sums, where count > 1 (sums over rows)
     int count;              // chunks of the group
     int col;                // which of the `cols` tiles beside each other
 };
@@ -361,7 +361,7 @@ __device__ __forceinline__ int search_tile(const int32_t* offsets, int n_groups,
         if (i >= each + (x < extra)) return i > each ? -1 : 0;
         item = x * each + (x < extra ? x : extra) + i;
     }
-    int64_t run = 0;
+    int64_t run = 0, alone = 0;
     for (int g0 = 0; g0 <= n_groups; g0 += 64) {
         const int cnt = chunks_at(g0 + lane, beg, end);
         int incl = cnt;
@@ -370,7 +370,7 @@ __device__ __forceinline__ int search_tile(const int32_t* offsets, int n_groups,
             const int y = __shfl_up(incl, off);
             if (lane >= off) incl += y;
         }
-        const uint64_t past = __ballot((run + incl) * cols > item);
+        const uint64_t past = __ballot((run + incl) * cols > item), one = __ballot(cnt == 1);
         if (past) {
             const int l = __ffsll((unsigned long long)past) - 1;
             t.g = g0 + l;
@@ -386,12 +386,13 @@ __device__ __forceinline__ int search_tile(const int32_t* offsets, int n_groups,
             const int64_t len = min_chunks ? ((uint32_t)((ge - gb + t.count - 1) / t.count) + 63u) / 64 * 64 : R;
             const int64_t b0 = gb + index * len < ge ? gb + index * len : ge;
             t.col = col;
-            t.chunk = before + index;
+            t.slot = before + index - alone - __popcll(one & ((1ull << l) - 1));
             t.beg = b0;
             t.end = b0 + len < ge ? b0 + len : ge;
             return 1;
         }
         run += __shfl(incl, 63);
+        alone += __popcll(one);
     }
     return -1;
 }
@@ -405,7 +406,7 @@ __device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, i
     t.g = __builtin_amdgcn_readfirstlane(v.g);
     t.beg = __builtin_amdgcn_readfirstlane((int)v.beg);
     t.end = __builtin_amdgcn_readfirstlane((int)v.end);
-    t.chunk = __builtin_amdgcn_readfirstlane((int)v.chunk);
+    t.slot = __builtin_amdgcn_readfirstlane((int)v.slot);
     t.count = __builtin_amdgcn_readfirstlane(v.count);
     t.col = __builtin_amdgcn_readfirstlane(v.col);
     return __builtin_amdgcn_readfirstlane(found);
@@ -519,7 +520,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(ProdArgs p) {
                                     (int64_t)col_tiles * row_tiles, b, t);
         if (found < 0) return;
         if (!found) continue;
-        if (MODE == kDw && t.chunk >= p.limit) continue;     // offsets that overlap
+        if (MODE == kDw && t.count > 1 && t.slot >= p.limit) continue;   // offsets that overlap
         const bool grouped = t.g < p.n_groups;
         const int r0 = MODE == kDw ? t.col % row_tiles * C::BR : 0;
         const int c0 = (MODE == kDw ? t.col / row_tiles : t.col) * C::BC;
@@ -677,7 +678,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(ProdArgs p) {
             __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0): nothing comes into LDS any more
         }
         if (!busy) continue;
-        void* to = MODE != kDw ? p.out : (t.count == 1 ? (float*)p.out + wg : p.partial + t.chunk * p.n * p.k);
+        void* to = MODE != kDw ? p.out : (t.count == 1 ? (float*)p.out + wg : p.partial + t.slot * p.n * p.k);
 #pragma unroll
         for (int j = 0; j < C::TR; ++j) {
             const int r = wr + j * 16 + (lane & 15);
@@ -874,6 +875,7 @@ uint32_t dw_chunk_rows(int64_t m, int n, int k) {
     return (uint32_t)r;
 }
 int64_t dw_chunks(int64_t m, int n_groups, int n, int k) { return m / dw_chunk_rows(m, n, k) + n_groups + 1; }
+int64_t dw_slots(int64_t m, int n_groups, int n, int k) { return split_chunks(m, n_groups, dw_chunk_rows(m, n, k)); }
 
 }  // namespace
 }  // namespace htl
@@ -909,7 +911,7 @@ extern "C" size_t grouped_mm_backward_workspace_bytes(int64_t m, int n_groups, i
         k > HTL_MAX_PRODUCT_DIM)
         return 0;
     if (m <= (int64_t)dw_chunk_rows(m, n, k)) return 256;
-    return align_up((size_t)dw_chunks(m, n_groups, n, k) * n * k * 4, 256);
+    return align_up((size_t)dw_slots(m, n_groups, n, k) * n * k * 4, 256);
 }
 
 extern "C" htl_status grouped_mm_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, const void* w,
@@ -934,17 +936,18 @@ extern "C" htl_status grouped_mm_backward(const void* dy, int64_t ld_dy, const v
     }
     if (!dw) return HTL_OK;
     const ProdArgs p = {dy, x, dw, order, offsets, m, ld_dy, ldx, n, k, n_groups, dw_chunk_rows(m, n, k),
-                        (float*)ws, 1, dw_chunks(m, n_groups, n, k)};
+                        (float*)ws, 1, dw_slots(m, n_groups, n, k)};
+    const int64_t chunks = dw_chunks(m, n_groups, n, k);
     const bool fast = ld_dy * es % 16 == 0 && ldx * es % 16 == 0 && aligned(dy, 16) && aligned(x, 16) &&
                       (int64_t)n * es % 16 == 0 && (int64_t)k * es % 16 == 0 && m * ld_dy * es <= kBufferBytes &&
                       m * ldx * es <= kBufferBytes;
     if (dtype == HTL_BF16) {
-        if (fast && n >= 256 && k >= 256) launch<kSrcBf16, kDw, Big, true>(p, p.limit, stream);
-        else if (fast) launch<kSrcBf16, kDw, Mid, true>(p, p.limit, stream);
-        else launch<kSrcBf16, kDw, Mid, false>(p, p.limit, stream);
+        if (fast && n >= 256 && k >= 256) launch<kSrcBf16, kDw, Big, true>(p, chunks, stream);
+        else if (fast) launch<kSrcBf16, kDw, Mid, true>(p, chunks, stream);
+        else launch<kSrcBf16, kDw, Mid, false>(p, chunks, stream);
     } else {
-        if (fast) launch<kSrcF32, kDw, Mid, true>(p, p.limit, stream);
-        else launch<kSrcF32, kDw, Mid, false>(p, p.limit, stream);
+        if (fast) launch<kSrcF32, kDw, Mid, true>(p, chunks, stream);
+        else launch<kSrcF32, kDw, Mid, false>(p, chunks, stream);
     }
     const htl_status st = check_launch("grouped_mm_backward");
     if (st != HTL_OK) return st;

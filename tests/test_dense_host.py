@@ -187,3 +187,16 @@ def test_sizes_past_32_bits_are_refused():
     kept = htl.Rows8(_Shaped((2, big), torch.uint8), _Shaped((2, (big + 31) // 32), torch.uint8), "i8", torch.float32)
     with pytest.raises(ValueError, match="rows of at most"):
         dense._check_rows8(kept, "kept")
+
+
+def test_workspaces_of_sums_go_by_rows(L):
+    """Partial sums take room for the chunks of groups that have several, not for every group."""
+    mm, norm = L.grouped_mm_backward_workspace_bytes, L.norm_back_workspace_bytes
+    # 16 experts, 2,048 -> 4,096: at most four chunks of split groups (a group's matrix is 33.6 MB)
+    assert mm(16384, 16, 4096, 2048) <= 4 * 4096 * 2048 * 4 + 256
+    assert mm(16384, 256, 1024, 1024) <= 256 * 1024 * 1024 * 4 // 4
+    for m, n, k in ((16384, 1024, 1024), (100001, 513, 777), (1 << 20, 128, 256), (5000, 64, 64)):
+        assert mm(m, 1, n, k) <= mm(m, 300, n, k) <= mm(m, 4095, n, k) <= 2 * mm(m, 1, n, k)
+    for m, dim in ((8192, 16384), (1 << 20, 128), (100, 4096)):
+        assert norm(m, 4095, dim) <= 2 * norm(m, 1, dim) and norm(m, 4095, dim) % 256 == 0
+    assert mm(10, 4095, 512, 512) == norm(10, 4095, 128) == 256

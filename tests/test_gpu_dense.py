@@ -815,3 +815,83 @@ def test_layer_norm_far_from_zero(htl, dim, save):
     e_v = w.abs() * N.e_n + 2 * U * ((N.n * w).abs() + bw.abs())
     _close(du, d * v, d.abs() * e_v + 4 * U * (d * v).abs(), "dgate")
     _close(dw, *_sum_of(t * N.n, t.abs() * N.e_n + 3 * U * (t * N.n).abs(), ids, g), "dweight")
+
+
+# -------------------------------------------------- what lies around results --
+class Guarded:
+    """A tensor of a pattern with margins of the same before and after it; changed() names what else was written."""
+    MARGIN = 1 << 16
+
+    def __init__(self, *shape, dtype=torch.float32):
+        n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+        self.raw = torch.full((n + 2 * self.MARGIN,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.t = self.raw[self.MARGIN:self.MARGIN + n].view(dtype).view(*shape)
+
+    @property
+    def ptr(self):
+        return self.t.data_ptr()
+
+    def intact(self):
+        return bool((self.raw[:self.MARGIN] == 0xA5).all()) and bool((self.raw[-self.MARGIN:] == 0xA5).all())
+
+
+def _sizes_plan(htl, sizes, seed):
+    """A plan of groups of the sizes given, rows shuffled, 37 of no group."""
+    ids = np.repeat(np.arange(len(sizes)), sizes)
+    ids = np.concatenate([ids, np.full(37, -1)]).astype(np.int32)
+    np.random.default_rng(seed).shuffle(ids)
+    return ids, _plan(htl, ids, len(sizes))
+
+
+SPLIT = [[5000, 1, 0, 700, 300, 9000, 2, 256, 257], [1] * 70 + [6000] + [0] * 70 + [300] * 3 + [7000, 1], [20000]]
+
+
+@pytest.mark.parametrize("sizes", SPLIT, ids=["mixed", "150 groups", "one"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,k", [(40, 72), (264, 520)])
+def test_product_sums_of_split_and_whole_groups(htl, sizes, dtype, n, k):
+    """Groups of one chunk, of several and of none side by side, in a workspace of exactly the size asked for."""
+    ids, plan = _sizes_plan(htl, sizes, n)
+    m, g, L = len(ids), len(sizes), htl.lib()
+    gen = torch.Generator().manual_seed(n + g)
+    x, dy = torch.randn(m, k, generator=gen).to(dtype), torch.randn(m, n, generator=gen).to(dtype)
+    xc, dyc = x.cuda(), dy.cuda()
+    nb = L.grouped_mm_backward_workspace_bytes(m, g, n, k)
+    dw, ws = Guarded(g, n, k), Guarded(nb, dtype=torch.uint8)
+    code = 0 if dtype == torch.float32 else 1
+    assert L.grouped_mm_backward(dyc.data_ptr(), n, xc.data_ptr(), k, None, code, m, n, k, plan.order.data_ptr(),
+                                 plan.offsets.data_ptr(), g, None, code, dw.ptr, ws.ptr, nb, 0) == 0
+    torch.cuda.synchronize()
+    assert dw.intact() and ws.intact()
+    for i, rows in enumerate(_members(ids, g)):
+        a, d = x[rows].double(), dy[rows].double()
+        _close(dw.t[i], d.t() @ a, (len(rows) + 2) * U * (d.abs().t() @ a.abs()) + 1e-37, ("dw", i))
+
+
+@pytest.mark.parametrize("sizes", SPLIT, ids=["mixed", "150 groups", "one"])
+@pytest.mark.parametrize("dim", [24, 200, 1000, 4100])
+def test_norm_sums_of_split_and_whole_groups(htl, sizes, dim):
+    ids, plan = _sizes_plan(htl, sizes, dim)
+    m, g, L = len(ids), len(sizes), htl.lib()
+    gen = torch.Generator().manual_seed(dim + g)
+    x, dy = torch.randn(m, dim, generator=gen), torch.randn(m, dim, generator=gen)
+    w, xc, dyc = torch.ones(g, dim, device="cuda"), x.cuda(), dy.cuda()
+    nb = L.norm_back_workspace_bytes(m, g, dim)
+    N = Norm(x, "rms")
+    d = dy.double()
+    want = [_sum_of(d * N.n, d.abs() * N.e_n, ids, g), _sum_of(d, torch.zeros_like(d), ids, g)]
+    order, offsets = plan.order.data_ptr(), plan.offsets.data_ptr()
+    for gate in (False, True):
+        dx, du, dw, db, ws = Guarded(m, dim), Guarded(m, dim), Guarded(g, dim), Guarded(g, dim), Guarded(nb, dtype=torch.uint8)
+        if gate:                              # no activation, a gate of ones
+            ones = torch.ones(m, dim, device="cuda")
+            status = L.norm_gate_backward(dyc.data_ptr(), 0, dim, xc.data_ptr(), dim, None, ones.data_ptr(), dim, None, 0,
+                                          0, m, dim, w.data_ptr(), None, order, offsets, g, 0, EPS, 0, 1.0, dx.ptr, du.ptr,
+                                          dw.ptr, db.ptr, ws.ptr, nb, 0)
+        else:
+            status = L.norm_rows_backward(dyc.data_ptr(), 0, dim, xc.data_ptr(), 0, dim, None, 0, None, 0, m, dim,
+                                          w.data_ptr(), order, offsets, g, 0, EPS, dx.ptr, dw.ptr, db.ptr, ws.ptr, nb, 0)
+        torch.cuda.synchronize()
+        assert status == 0 and all(t.intact() for t in (dx, du, dw, db, ws))
+        for got, (s, e), what in zip((dw.t, db.t), want, ("dweight", "dbias")):
+            _close(got, s, e + 2 * U * s.abs(), (what, gate))
