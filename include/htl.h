@@ -645,7 +645,9 @@ htl_status norm_rows_backward(const void* dy, htl_dtype dy_dtype, int64_t ld_dy,
 /* norm_gate -- the end of a block: out = x + scale * act(u) * (n w_g + b_g),
  * n the norm of z as in norm_rows; a row of no group gives out = x.
  *   x, out     x_dtype[m][dim]; z, u z_dtype[m][dim].
- *   act        u itself, 1 / (1 + exp(-u)), or u / (1 + exp(-u)).
+ *   act        u itself, 1 / (1 + exp(-u)), or u / (1 + exp(-u)); the last two
+ *              and their slopes are within a few last places of fp32 for any
+ *              finite u (below 2^-126 they may be 0).
  *   z_codes, z_scales, u_codes, u_scales  all null, or the 8-bit copies of z
  *              and u, as rows8_save writes them. */
 htl_status norm_gate(const void* x, htl_dtype x_dtype, int64_t ldx, const void* z, int64_t ldz, const void* u,

@@ -895,3 +895,81 @@ def test_norm_sums_of_split_and_whole_groups(htl, sizes, dim):
         assert status == 0 and all(t.intact() for t in (dx, du, dw, db, ws))
         for got, (s, e), what in zip((dw.t, db.t), want, ("dweight", "dbias")):
             _close(got, s, e + 2 * U * s.abs(), (what, gate))
+
+
+# ---------------------------------------------------------- gates far open --
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+@pytest.mark.parametrize("zd", [torch.float32, torch.bfloat16])
+def test_gates_far_from_zero(htl, act, zd):
+    """Gates up to the largest finite numbers: out, and the slope relative to itself.
+
+    With e = exp(-|u|) the sigmoid is 1 / (1 + e) or e / (1 + e), its slope e / (1 + e)^2: an exponential and four
+    operations of fp32, 16 u of their value at most.  silu's slope is s (1 + u t): 16 u of s (1 + |u| t).  Below 2^-126
+    values may go to zero."""
+    m, dim = 64, 40
+    gen = torch.Generator().manual_seed(21)
+    u = torch.randn(m, dim, generator=gen)
+    top = float(torch.finfo(zd).max)
+    for i, v in enumerate([8.0, 10.0, 12.0, 15.0, 17.0, 18.0, 20.0, 30.0, 50.0, 80.0, 87.0, 88.0, 89.0, 100.0, 1e4, 1e20, top]):
+        u[2 * i], u[2 * i + 1] = v, -v
+    u = u.to(zd)
+    x, z = torch.zeros(m, dim), torch.randn(m, dim, generator=gen).to(zd)
+    w, b = torch.ones(1, dim), 0.5 * torch.ones(1, dim)
+    dout = (1 + torch.rand(m, dim, generator=gen)).to(torch.float32)
+    scale = 2.0**-10                                           # out stays finite
+    kw = dict(kind="rms", eps=EPS, act=act, scale=scale)
+    out, _, _ = htl.norm_gate(x.cuda(), z.cuda(), u.cuda(), w.cuda(), b.cuda(), **kw)
+    dz, du, dw, db = htl.norm_gate_backward(dout.cuda(), z.cuda(), u.cuda(), w.cuda(), b.cuda(), **kw)
+    N = Norm(z, "rms")
+    v, e_v = N.n + 0.5, N.e_n + 2 * U * (N.n.abs() + 0.5)
+    uu = u.double()
+    e = torch.exp(-uu.abs())
+    s = torch.where(uu < 0, e / (1 + e), 1 / (1 + e))
+    t = torch.where(uu < 0, 1 / (1 + e), e / (1 + e))
+    a, slope, mag = (s, s * t, s * t) if act == "sigmoid" else (uu * s, s * (1 + uu * t), s * (1 + uu.abs() * t))
+    D = scale * dout.double()
+    small = 2.0**-126 * (1 + v.abs()) * 4 * (1 if act == "sigmoid" else 200.0)
+    _close(out, scale * a * v, scale * (a.abs() * e_v + 20 * U * (a * v).abs()) + small, "out")
+    want = D * slope * v
+    _close(du, want, D * (16 * U * mag * v.abs() + (slope.abs() + 16 * U * mag) * e_v)
+           + (4 * U + HALF[zd]) * want.abs() + small, "dgate")
+    assert torch.isfinite(out).all() and torch.isfinite(du).all()
+    ea = D * a
+    keep = torch.isfinite(ea.float()).all(1) & (ea.abs().amax(1) < 1e18)       # (beyond, the sums of dz pass fp32)
+    gz, err = N.back(ea, 20 * U * ea.abs())
+    gz, err = gz[keep], err[keep]
+    _close(dz[keep.cuda()], gz, err + HALF[zd] * gz.abs() * 1.01 + 1e-30, "dz")
+
+
+def test_infinite_gates_stay_in_their_elements(htl):
+    """A gate of +-infinity, or NaN, reaches its own element's output and gate gradient, its row's dz and the sums, and
+    no other row; in a row of no group, nothing."""
+    m, dim, g = 30, 48, 2
+    gen = torch.Generator().manual_seed(22)
+    ids = (np.arange(m) % 3).astype(np.int32)                  # id 2: no group
+    plan = _plan(htl, ids, g)
+    x, z, u, dout = (torch.randn(m, dim, generator=gen) for _ in range(4))
+    w = torch.ones(g, dim).cuda()
+
+    def both(u, act):
+        kw = dict(groups=plan, act=act, eps=EPS)
+        out = htl.norm_gate(x.cuda(), z.cuda(), u.cuda(), w, **kw)[0].cpu()
+        return (out, *(t.cpu() for t in htl.norm_gate_backward(dout.cuda(), z.cuda(), u.cuda(), w, **kw)[:3]))
+
+    inf, nan = float("inf"), float("nan")
+    for act in ("none", "sigmoid", "silu"):
+        clean = both(u, act)
+        bad = u.clone()
+        bad[2, 3], bad[5, 4], bad[8] = inf, -inf, nan
+        assert all(torch.equal(a, b) for a, b in zip(both(bad, act), clean))
+        bad[0, 1], bad[3, 2], bad[6, 7] = inf, -inf, nan       # rows of group 0
+        out, dz, du, dw = both(bad, act)
+        rows = [i for i in range(m) if i not in (0, 3, 6)]
+        assert torch.equal(out[rows], clean[0][rows]) and torch.equal(dz[rows], clean[1][rows])
+        assert torch.equal(du[rows], clean[2][rows]) and torch.equal(dw[1], clean[3][1])
+        for r, c in ((0, 1), (3, 2), (6, 7)):
+            cols = [j for j in range(dim) if j != c]
+            assert torch.equal(out[r, cols], clean[0][r, cols]) and torch.equal(du[r, cols], clean[2][r, cols])
+        assert torch.isnan(out[6, 7]) and torch.isnan(du[6, 7]).item() == (act != "none")
+        if act == "sigmoid":                                   # limits: 1 and 0, slope 0
+            assert torch.isfinite(out[0]).all() and out[3, 2] == x[3, 2] and du[0, 1] == 0 and du[3, 2] == 0
