@@ -819,20 +819,25 @@ def test_layer_norm_far_from_zero(htl, dim, save):
 
 # -------------------------------------------------- what lies around results --
 class Guarded:
-    """A tensor of a pattern with margins of the same before and after it; changed() names what else was written."""
-    MARGIN = 1 << 16
+    """A tensor with margins of a byte pattern before and after it, itself of the pattern or of what it is given."""
+    MARGIN = 1 << 17
 
-    def __init__(self, *shape, dtype=torch.float32):
+    def __init__(self, *shape, dtype=torch.float32, pattern=0xA5, values=None):
+        if values is not None:
+            shape, dtype = values.shape, values.dtype
         n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
-        self.raw = torch.full((n + 2 * self.MARGIN,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.pattern = pattern
+        self.raw = torch.full((n + 2 * self.MARGIN,), pattern, dtype=torch.uint8, device="cuda")
         self.t = self.raw[self.MARGIN:self.MARGIN + n].view(dtype).view(*shape)
+        if values is not None:
+            self.t.copy_(values)
 
     @property
     def ptr(self):
         return self.t.data_ptr()
 
     def intact(self):
-        return bool((self.raw[:self.MARGIN] == 0xA5).all()) and bool((self.raw[-self.MARGIN:] == 0xA5).all())
+        return all(bool((side == self.pattern).all()) for side in (self.raw[:self.MARGIN], self.raw[-self.MARGIN:]))
 
 
 def _sizes_plan(htl, sizes, seed):
@@ -973,3 +978,143 @@ def test_infinite_gates_stay_in_their_elements(htl):
         assert torch.isnan(out[6, 7]) and torch.isnan(du[6, 7]).item() == (act != "none")
         if act == "sigmoid":                                   # limits: 1 and 0, slope 0
             assert torch.isfinite(out[0]).all() and out[3, 2] == x[3, 2] and du[0, 1] == 0 and du[3, 2] == 0
+
+
+def _broken_plan(m, g, seed):
+    """ids, order and offsets that break every rule: entries below and past the rows, offsets that decrease and overlap."""
+    rng = np.random.default_rng(seed)
+    ids = rng.integers(-3, g + 3, m)
+    order = rng.integers(-15, m + 15, m)
+    offsets = rng.integers(-100, m + 200, g + 1)
+    if seed % 2:
+        ids[::7], order[::7], offsets[1] = 2**31 - 1, -2**31, 2**31 - 1
+    else:
+        ids[::7], order[::7], offsets[1] = -2**31, 2**31 - 1, -2**31
+    return [Guarded(values=torch.from_numpy(t.astype(np.int32))) for t in (ids, order, offsets)]
+
+
+def _nan_around(values):
+    return Guarded(values=values, pattern=0xFF)              # 0xFF bytes: NaN in fp32 and bf16
+
+
+# tiles of 32, 128 and 256 rows, matrices kept in LDS; lengths of whole and of odd pieces
+@pytest.mark.parametrize("m,k,n", [(500, 64, 72), (700, 33, 77), (20000, 64, 136), (20000, 63, 135), (14600, 264, 1024),
+                                   (14600, 1024, 264), (70000, 64, 72), (70000, 33, 50)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_products_of_broken_plans_keep_to_their_rows(htl, m, k, n, dtype):
+    """Nothing is written outside the results and the workspace, and nothing read outside the operands: the NaN there
+    would show in the results, or in rows that no entry names, which keep their finite pattern."""
+    g, L = 5, htl.lib()
+    gen = torch.Generator().manual_seed(m + k)
+    code = 0 if dtype == torch.float32 else 1
+    for seed in (m, m + 1):
+        _, order, offsets = _broken_plan(m, g, seed)
+        x, dy, w = (_nan_around(torch.randn(*s, generator=gen).to(dtype)) for s in ((m, k), (m, n), (g, n, k)))
+        nb = L.grouped_mm_backward_workspace_bytes(m, g, n, k)
+        y, dx = Guarded(m, n, dtype=dtype), Guarded(m, k, dtype=dtype)
+        dw, ws = Guarded(g, n, k), Guarded(nb, dtype=torch.uint8)
+        for o in (order.ptr, None):
+            assert L.grouped_mm(x.ptr, k, w.ptr, code, m, n, k, o, offsets.ptr, g, y.ptr, code, 0) == 0
+            assert L.grouped_mm_backward(dy.ptr, n, x.ptr, k, w.ptr, code, m, n, k, o, offsets.ptr, g, dx.ptr, code,
+                                         dw.ptr, ws.ptr, nb, 0) == 0
+            torch.cuda.synchronize()
+            for name, t in dict(x=x, dy=dy, w=w, y=y, dx=dx, dw=dw, ws=ws, order=order, offsets=offsets).items():
+                assert t.intact(), name
+            assert all(torch.isfinite(t.t).all() for t in (y, dx, dw))
+
+
+@pytest.mark.parametrize("m,dim", [(500, 24), (500, 77), (9000, 128), (700, 600), (300, 2000), (200, 5001), (100, 9001)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norms_of_broken_plans_keep_to_their_rows(htl, m, dim, dtype):
+    g, L = 5, htl.lib()
+    gen = torch.Generator().manual_seed(m + dim)
+    code = 0 if dtype == torch.float32 else 1
+    blocks = (dim + 31) // 32
+    for seed in (m, m + 1):
+        ids, order, offsets = _broken_plan(m, g, seed)
+        x, z, u, d = (_nan_around(torch.randn(m, dim, generator=gen).to(dtype)) for _ in range(4))
+        w, b = (_nan_around(torch.randn(g, dim, generator=gen)) for _ in range(2))
+        nb = L.norm_back_workspace_bytes(m, g, dim)
+        rows = [Guarded(m, dim, dtype=dtype) for _ in range(5)]
+        sums = [Guarded(g, dim) for _ in range(2)]
+        codes = [Guarded(m, dim, dtype=torch.uint8) for _ in range(2)]
+        scales = [Guarded(m, blocks, dtype=torch.uint8) for _ in range(2)]
+        ws = Guarded(nb, dtype=torch.uint8)
+        y, dx, out, dz, du = rows
+        assert L.norm_rows(x.ptr, code, dim, None, 0, m, dim, w.ptr, b.ptr, ids.ptr, g, 1, EPS, y.ptr, code, codes[0].ptr,
+                           scales[0].ptr, 0, 0) == 0
+        assert L.norm_gate(x.ptr, code, dim, z.ptr, dim, u.ptr, dim, code, m, dim, w.ptr, b.ptr, ids.ptr, g, 1, EPS, 2, 1.0,
+                           out.ptr, codes[0].ptr, scales[0].ptr, codes[1].ptr, scales[1].ptr, 1, 0) == 0
+        torch.cuda.synchronize()
+        assert all(torch.isfinite(t.t).all() for t in (y, out))
+        for o in (order.ptr, None):
+            assert L.norm_rows_backward(d.ptr, code, dim, x.ptr, code, dim, None, 0, u.ptr, dim, m, dim, w.ptr, o, offsets.ptr,
+                                        g, 1, EPS, dx.ptr, sums[0].ptr, sums[1].ptr, ws.ptr, nb, 0) == 0
+            torch.cuda.synchronize()
+            assert all(t.intact() and torch.isfinite(t.t).all() for t in (dx, *sums))
+            assert L.norm_gate_backward(d.ptr, code, dim, codes[0].ptr, dim, scales[0].ptr, codes[1].ptr, dim, scales[1].ptr,
+                                        code, 1, m, dim, w.ptr, b.ptr, o, offsets.ptr, g, 1, EPS, 2, 1.0, dz.ptr, du.ptr,
+                                        sums[0].ptr, sums[1].ptr, ws.ptr, nb, 0) == 0
+            torch.cuda.synchronize()
+            assert all(t.intact() and torch.isfinite(t.t).all() for t in (dz, du, *sums))
+        for t in (ids, order, offsets, x, z, u, d, w, b, ws, *rows, *codes, *scales):
+            assert t.intact()
+
+
+def test_sums_past_32_bits(htl):
+    """Gradients over more than 2^32 elements that come from the last rows alone: the incoming gradient is zero in all
+    others, so that an address cut short reads zeros, or other rows."""
+    m, dim, n = (1 << 25) + 65, 136, 1000
+    x = torch.empty(m, dim, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, m, 1 << 23):
+        x[a:a + (1 << 23)].normal_()
+    dy = torch.zeros(m, dim, dtype=torch.bfloat16, device="cuda")
+    dy[-n:].normal_()
+    w = torch.ones(2, dim).cuda()
+    mat = torch.zeros(2, dim, dim, dtype=torch.bfloat16, device="cuda")
+    ids = torch.ones(m, dtype=torch.int32, device="cuda")
+    ids[:1 << 24] = -1                                        # the rest is of group 1, group 0 is empty
+    plan = htl.group_rows(ids, 2)
+    a, d = x[-n:].cpu().double(), dy[-n:].cpu().double()
+    N = Norm(a, "rms")
+    whole = torch.ones(n, dtype=torch.int64).numpy()
+    sums = _sum_of(d * N.n, d.abs() * N.e_n, whole, 2), _sum_of(d, torch.zeros_like(d), whole, 2)
+    for groups, p in ((None, w[:1]), (plan, w)):
+        _, dw, db = htl.norm_rows_backward(dy, x, p, groups=groups, eps=EPS, bias=True)
+        _close(dw[-1:], sums[0][0][1:], sums[0][1][1:], "dweight")
+        _close(db[-1:], sums[1][0][1:], sums[1][1][1:], "dbias")
+        _, du, dw, _ = htl.norm_gate_backward(dy, x, dy, p, groups=groups, eps=EPS, act="none")
+        s, t = _sum_of(d * d * N.n, d * d * N.e_n + 3 * U * (d * d * N.n).abs(), whole, 2)
+        _close(dw[-1:], s[1:], t[1:], "gate's dweight")
+        assert not du[:-n].any()
+        _close(du[-n:], d * N.n, d.abs() * N.e_n + (3 * U + HALF[torch.bfloat16]) * (d * N.n).abs(), "dgate")
+        del du
+        _, dw = htl.grouped_mm_backward(dy, x, mat[:p.shape[0]], groups, need_dx=False)
+        _close(dw[-1], d.t() @ a, (n + 2) * U * (d.abs().t() @ a.abs()), "dw")
+        if groups is not None:
+            assert not dw[0].any()
+
+
+@pytest.mark.parametrize("g", [71, 1000, 4095])
+def test_many_groups(htl, g):
+    """As many groups as there may be, most of them of a few rows or none."""
+    m = 9000
+    ids = _ids(np.random.default_rng(g), m, g, "dropped")
+    for dtype in (torch.bfloat16, torch.float32):
+        _product_check(htl, m, g, 16, 24, dtype, ids, g)
+    gen = torch.Generator().manual_seed(g)
+    dim = 40
+    x, dy = torch.randn(m, dim, generator=gen), torch.randn(m, dim, generator=gen)
+    weight = 1 + 0.1 * torch.randn(g, dim, generator=gen)
+    kw = dict(groups=_plan(htl, ids, g), kind="layer", eps=EPS)
+    w, on = _param_of(weight, ids, g)
+    N = Norm(x, "layer")
+    want = torch.where(on, N.n * w, 0.0)
+    _close(htl.norm_rows(x.cuda(), weight.cuda(), **kw)[0], want, w.abs() * N.e_n + 4 * U * want.abs() + 1e-37, "y")
+    dx, dw, db = htl.norm_rows_backward(dy.cuda(), x.cuda(), weight.cuda(), bias=True, **kw)
+    d = torch.where(on, dy.double(), 0.0)
+    gx, e = N.back(d * w, U * (d * w).abs())
+    want = torch.where(on, gx, 0.0)
+    _close(dx, want, e + 3 * U * want.abs() + 1e-37, "dx")
+    _close(dw, *_sum_of(d * N.n, d.abs() * N.e_n, ids, g), "dweight")
+    _close(db, *_sum_of(d, torch.zeros_like(d), ids, g), "dbias")
