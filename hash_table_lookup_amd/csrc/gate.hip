@@ -11,9 +11,9 @@
 // u / (1 + exp(-u)), as the gates of [MTGR] section 4's encoder (silu) are.
 //
 // Bound: bytes, and in the backward pass instructions, as norm.hip.  16,384
-// bf16 rows of 4,096: forward 104-120 us (537 MB: 4.5-5.2 TB/s), backward 150-171
-// (671 MB: 3.9-4.5 TB/s); 426,000 rows of 128 in 26 groups, fp32 residual, e4m3
-// copies: 147-152 us (766 MB: 5.0-5.2 TB/s) and 141-157 (548 MB: 3.5-3.9 TB/s).
+// bf16 rows of 4,096: forward 110 us (107-126; 537 MB: 4.9 TB/s), backward 153
+// (151-157; 671 MB: 4.4 TB/s); 426,000 rows of 128 in 26 groups, fp32 residual,
+// e4m3 copies: 147 us (766 MB: 5.2 TB/s) and 144 (548 MB: 3.8 TB/s).
 #include "dense.h"
 
 namespace htl {

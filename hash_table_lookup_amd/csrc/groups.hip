@@ -8,13 +8,16 @@
 // the ids alone: ranks come from ballots and prefix sums, never from the
 // order in which atomics land.
 //
-// Bound: the latency of dependent launches (8 bytes a row are little).  Up to
+// Bound: latency (8 bytes a row are little): of launches on few rows, of the
+// placement on many, which for every 64 ids of a wave is a chain of ballots and
+// an LDS update, then 4-byte stores into the groups' runs.  Up to
 // kOneBlockRows rows one workgroup does all in one launch.  Beyond, a count
 // per (group, block) and the placement, whose blocks each add up the counts of
 // those before them; where that would be too many counts to read in every
 // block, a prefix sum over them in between.  1,000 rows: 4 us on the device;
-// 16,384 in 16 groups: 2.5 + 6 (one workgroup alone: 18); 1.7M in 26: 3 + 13
-// (with a prefix sum between: 3 + 5 + 14, and its launch).
+// 16,384 in 16 groups: 13 us the call (one workgroup alone: 18 on the device);
+// 1.7M in 26: 4 + 13.6 on the device (with a prefix sum between 5 more, and its
+// launch).
 #include "dense.h"
 #include "scan.h"
 

@@ -8,11 +8,11 @@
 //   dw_g = sum dy n,  db_g = sum dy;        rows of no group: dx = dres
 //
 // Bound: bytes and instructions alike.  On 1.7M bf16 rows of 128 in 26 groups
-// the forward pass with its 8-bit copy takes 235-260 us (1,097 MB: 4.2-4.7
-// TB/s), the backward pass from that copy with a residual gradient 330-350
-// (1,533 MB: 4.4-4.6 TB/s; 530 with bit arithmetic for bf16, LDS shuffles and
-// selects in every element, which the lanes do without now).  On long rows
-// bytes decide.  A row is read once into registers (see Hold in dense.h) and
+// the forward pass with its 8-bit copy takes 242 us (238-267; 1,097 MB: 4.5
+// TB/s), from that copy 158 (668 MB: 4.2 TB/s), the backward pass from that
+// copy with a residual gradient 332 (1,533 MB: 4.6 TB/s; 530 with bit
+// arithmetic for bf16, LDS shuffles and selects in every element, which the
+// lanes do without now).  On long rows bytes decide.  A row is read once into registers (see Hold in dense.h) and
 // its statistics are recomputed in the backward pass rather than kept.
 #include "dense.h"
 

@@ -8,15 +8,19 @@
 // through the plan's order, so nothing is sorted or copied around the product.
 //
 // Measured: 16,384 bf16 rows in 16 ragged groups, 2,048 -> 4,096: forward
-// 310-370 us from run to run (740-890 TFLOP/s), dx 373-430, dw 391-428 (with 537 MB of
-// fp32 results); one group, 32,768 rows, 2,048 -> 2,048: 261, 280 and 300 us
-// (915-1,050 TFLOP/s, where the library's product of such sizes reaches
+// 321 us (316-330; 860 TFLOP/s), dx 349 (348-354), dw 388 (385-392, with 537 MB of
+// fp32 results); one group, 32,768 rows, 2,048 -> 2,048: 260, 270 and 292 us
+// (940-1,060 TFLOP/s, where the library's product of such sizes reaches
 // 1,340-1,600).  Without its loads the forward kernel runs at 1,450-1,550: it
 // is bound by how soon operands arrive in LDS (a request takes 577 cycles
 // against 282 in the library's kernel of the same tile, at equal hits in L2).
-// 1.7M rows in 26 groups, 128 -> 256: 320, 305 and 360 us, bound by bytes
-// (1,308 MB each: 3.6-4.3 TB/s; the results alone are 2.9 TB/s of scattered rows).
-// fp32: 100-107 TFLOP/s of 157 on 20,000 rows, 1,024 x 1,024.
+// Counted from the code, a step of a 256 x 256 tile moves 96 KiB out of LDS and
+// 32 KiB into it, 1,024 cycles at 128 bytes each, and its matrix instructions
+// take as many: loads find LDS busy.
+// 1.7M rows in 26 groups, 128 -> 256: 312, 303 and 353 us, bound by bytes
+// (1,308 MB each: 3.7-4.3 TB/s; the results alone are 2.9 TB/s of scattered rows);
+// 66 of the last are the sums of its partial sums.
+// fp32: 20,000 rows, 1,024 x 1,024: 328, 348 and 370 us (113-128 TFLOP/s of 157).
 #include "dense.h"
 
 #include <type_traits>
@@ -308,6 +312,12 @@ template <int T> constexpr int kSteps = T == kSrcF32 ? 4 : 1;
 __device__ __forceinline__ void multiply(const Frag<kSrcBf16>& c, const Frag<kSrcBf16>& r, int, f32x4& acc) {
     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c.v, r.v, acc, 0, 0, 0);
 }
+// fp32 sums are one chain over the reduction.  Their error is 9.6 u of the
+// results at 1,024 elements and 19 u at 4,096 (u = 2^-24, root mean squares),
+// as the library's fp32 products' is where they do not split the reduction
+// (4.9 and 9.6 u where they do).  Sums put aside every 256 elements leave 4.9 u
+// at any length, but registers do not hold a second set of them: 20,000 rows,
+// 1,024 x 1,024, 331 -> 465 us.
 __device__ __forceinline__ void multiply(const Frag<kSrcF32>& c, const Frag<kSrcF32>& r, int e, f32x4& acc) {
     acc = __builtin_amdgcn_mfma_f32_16x16x4f32(c.v[e], r.v[e], acc, 0, 0, 0);
 }

@@ -1,9 +1,9 @@
 // Rows kept in 8 bits (activations held for a backward pass at half of bf16's
 // bytes) and read back: the format is at dense.h's unpack8 / save8.
 //
-// Bound: bytes.  1.7M bf16 rows of 128: 128 us to write (661 MB: 5.2 TB/s) and
-// 124 to read back (5.3 TB/s).  A lane moves eight elements (16 or 32 bytes in, 8 codes
-// out); four lanes share a block's scale.
+// Bound: bytes.  1.7M bf16 rows of 128: 131 us to write (661 MB: 5.0 TB/s), 245
+// to write and read back (5.4 TB/s).  A lane moves eight elements (16 or 32
+// bytes in, 8 codes out); four lanes share a block's scale.
 #include "dense.h"
 
 namespace htl {

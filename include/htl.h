@@ -616,7 +616,8 @@ htl_status rows8_load(const uint8_t* codes, const uint8_t* scales, htl_rows8_fmt
 
 /* norm_rows -- y = n w_g + b_g with n = (x - mean) / sqrt(var + eps)
  * (HTL_NORM_LAYER) or x / sqrt(mean(x^2) + eps) (HTL_NORM_RMS); a row of no
- * group gives zeros.
+ * group gives zeros.  A layer norm keeps the deviation of rows far from zero;
+ * a row's sum and sum of squares have to stay within fp32's range.
  *   x          x_dtype[m][dim], 1 <= dim <= HTL_MAX_NORM_DIM; with x_scales,
  *              x holds 8-bit codes of format x_fmt (a norm recomputed from
  *              what was kept).
