@@ -27,16 +27,18 @@ from ._binding import (  # noqa: F401
 )
 
 from .dense import (  # noqa: F401
-    RowGroups, Rows8, group_rows, grouped_mm, grouped_mm_backward, load_rows8, norm_gate, norm_gate_backward,
-    norm_rows, norm_rows_backward, save_rows8,
+    RowGroups, Rows8, gated_mm, gated_mm_backward, group_rows, grouped_mm, grouped_mm_backward, load_rows8, norm_gate,
+    norm_gate_backward, norm_rows, norm_rows_backward, save_rows8,
 )
+from .scores import distill_loss, distill_loss_backward, softmax_loss, softmax_loss_backward  # noqa: F401
 from .pipeline import LookupPipeline, PipelineBatch  # noqa: F401
 
 __all__ = [
     "Table", "DedupPlan", "LookupPipeline", "PipelineBatch", "dedup_unique_inverse", "gather", "gather_pool", "segment_sum", "rowwise_adam",
     "segment_sum_adam", "lookup", "lookup_fused", "lookup_slots", "lib", "release_workspaces", "HTLError", "FOUND", "INSERTED", "FULL", "RESERVED", "NOT_FOUND", "ERASED",
     "RowGroups", "Rows8", "group_rows", "grouped_mm", "grouped_mm_backward", "save_rows8", "load_rows8", "norm_rows",
-    "norm_rows_backward", "norm_gate", "norm_gate_backward",
+    "norm_rows_backward", "norm_gate", "norm_gate_backward", "gated_mm", "gated_mm_backward", "softmax_loss",
+    "softmax_loss_backward", "distill_loss", "distill_loss_backward",
 ]
 
 

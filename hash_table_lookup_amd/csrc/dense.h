@@ -272,6 +272,38 @@ __device__ __forceinline__ void load_param(const float* p, int g, int col, int d
     unpack8(r, raw, v);
 }
 
+// -------------------------------------------------------------- gates ----
+// exp(-x) for x >= 0, within two last places, 0 below 2^-126: 2^h with h the
+// product x log2(e) rounded, times 1 + l ln 2 with l what the rounding left.
+__device__ __forceinline__ float exp_down(float x) {
+    const float y = x > 128.0f ? 128.0f : x;                       // (an infinity less an infinity)
+    const float kLog2e = 1.44269502f, kRest = 1.92596299e-8f;      // log2(e) in two parts
+    const float h = -y * kLog2e, l = __builtin_fmaf(-y, kRest, __builtin_fmaf(-y, kLog2e, -h));
+    const float e = __builtin_amdgcn_exp2f(h);
+    return __builtin_fmaf(e, l * 0.693147182f, e);
+}
+
+// act(u) and its slope.  The sigmoid s and t = 1 - s come from exp(-|u|), which
+// does not overflow, and neither is a difference: 1 - s would have no digits
+// left of the slope s t of an open gate (none at all from u = 17 on).  The
+// reciprocal is refined by one step to fp32's last place or so; a division
+// costs ten instructions.
+__device__ __forceinline__ float gate_act(float u, int act, float& slope) {
+    if (act == HTL_ACT_NONE) {
+        slope = 1.0f;
+        return u;
+    }
+    const float e = exp_down(fabsf(u)), d = 1.0f + e, q0 = __builtin_amdgcn_rcpf(d);
+    const float q = __builtin_fmaf(q0, __builtin_fmaf(-d, q0, 1.0f), q0), eq = e * q;
+    const float s = u < 0.0f ? eq : q, t = u < 0.0f ? q : eq;
+    if (act == HTL_ACT_SIGMOID) {
+        slope = s * t;
+        return s;
+    }
+    slope = s * (1.0f + u * t);
+    return u * s;
+}
+
 // ---------------------------------------------------- teams of lanes ----
 // Sums over a team of L lanes (L <= 64: aligned lanes of one wave; larger: the
 // whole workgroup of L threads, through LDS), the same in every lane.  Two
@@ -535,7 +567,8 @@ __device__ __forceinline__ void chunks_of_group(const int32_t* offsets, int n_gr
 // writes its sums itself).  Chunks are added in order, so the result does
 // not depend on which workgroup ended first.  limit: rows that partial holds;
 // a second set of sums (out2, nullable) has its partial rows after those.
-htl_status sum_chunks(const float* partial, int64_t limit, float* out, float* out2, const int32_t* offsets,
-                      int n_groups, int64_t m, uint32_t R, int64_t width, hipStream_t stream);
+// out is fp32, or with bf16 (and no second set) rounded.
+htl_status sum_chunks(const float* partial, int64_t limit, void* out, float* out2, const int32_t* offsets,
+                      int n_groups, int64_t m, uint32_t R, int64_t width, hipStream_t stream, bool bf16 = false);
 
 }  // namespace htl

@@ -1,0 +1,260 @@
+// Gated projections by group: both projections of a feed-forward block, the
+// activation and the product in one kernel, and the backward pass.
+//
+//   [z_i; u_i] = w_g x_i      (x [m][k], w [groups][2 n][k]: n rows of z's, n of u's)
+//   y_i  = act(z_i) u_i
+//   dz_i = dy_i u_i act'(z_i),  du_i = dy_i act(z_i)
+//   dx_i = w_g^T [dz_i; du_i],  dw_g = sum over the group's rows of [dz_i; du_i] x_i^T
+// Rows of no group: y = 0, dx = 0.  z and u are formed in fp32 and only what is
+// kept of them, y, and dz and du (operands of the matrix instructions that
+// follow) are rounded to the rows' type.
+#include "tile.h"
+
+namespace htl {
+namespace {
+
+// The end of a tile of pairs: a wave's first TC / 2 results of a row are z and
+// the others u of the same columns.
+template <class C> struct GatedEnd {
+    static constexpr bool kPairs = true;
+    static constexpr int F = C::TC / 2;
+    int n, act;
+    void* y;                 // [m][n]
+    bool y_f32, row_f32;
+    void* kept;              // nullable: [m][2 n] of the rows' type
+    template <class RowOf>
+    __device__ __forceinline__ void operator()(const TileAt&, bool, int, int c0, int, int wc, RowOf row_of,
+                                               f32x4 (&acc)[C::TC][C::TR]) const {
+        const int col = c0 + wc / 2;
+#pragma unroll
+        for (int j = 0; j < C::TR; ++j) {
+            const int64_t row = row_of(j * 16 + (__lane_id() & 15));
+            f32x4 z[F], u[F], v[F];
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                z[i] = acc[i][j];
+                u[i] = acc[F + i][j];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float slope;
+                    v[i][e] = gate_act(z[i][e], act, slope) * u[i][e];
+                }
+            }
+            store_rows<F>(y, y_f32, row, n, col, n, v);
+            if (kept) {
+                store_rows<F>(kept, row_f32, row, 2 * (int64_t)n, col, n, z);
+                store_rows<F>((char*)kept + n * (row_f32 ? 4ll : 2ll), row_f32, row, 2 * (int64_t)n, col, n, u);
+            }
+        }
+    }
+};
+
+// The same with dy: dz and du, [m][2 n] of the rows' type.
+template <class C, int T> struct GatedBackEnd {
+    static constexpr bool kPairs = true;
+    static constexpr int F = C::TC / 2;
+    int n, act;
+    RowsIn dy;
+    void* d;
+    template <class RowOf>
+    __device__ __forceinline__ void operator()(const TileAt&, bool grouped, int, int c0, int, int wc, RowOf row_of,
+                                               f32x4 (&acc)[C::TC][C::TR]) const {
+        if (!grouped) return;                // nothing reads their gradients
+        const int col = c0 + wc / 2;
+#pragma unroll
+        for (int j = 0; j < C::TR; ++j) {
+            const int64_t row = row_of(j * 16 + (__lane_id() & 15));
+            f32x4 dz[F], du[F];
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                const int c = col + i * 16 + (__lane_id() >> 4) * 4;
+                float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (row >= 0) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (c + e < n)
+                            g[e] = T == kSrcF32 ? ((const float*)dy.p)[row * dy.ld + c + e]
+                                                : bf16_lo(((const uint16_t*)dy.p)[row * dy.ld + c + e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float slope;
+                    const float a = gate_act(acc[i][j][e], act, slope);
+                    dz[i][e] = g[e] * acc[F + i][j][e] * slope;
+                    du[i][e] = g[e] * a;
+                }
+            }
+            store_rows<F>(d, T == kSrcF32, row, 2 * (int64_t)n, col, n, dz);
+            store_rows<F>((char*)d + n * (T == kSrcF32 ? 4ll : 2ll), T == kSrcF32, row, 2 * (int64_t)n, col, n, du);
+        }
+    }
+};
+
+template <int T, class C, bool ASYNC>
+__global__ __launch_bounds__(C::kThreads, 2) void k_gated(ProdArgs p, GatedEnd<C> end) {
+    product_tiles<T, kFwd, C, ASYNC>(p, end);
+}
+template <int T, class C, bool ASYNC>
+__global__ __launch_bounds__(C::kThreads, 2) void k_gated_back(ProdArgs p, GatedBackEnd<C, T> end) {
+    product_tiles<T, kFwd, C, ASYNC>(p, end);
+}
+
+// dz and du from what was kept of z and u: eight columns a lane.
+template <int T>
+__global__ __launch_bounds__(256) void k_gated_slopes(RowsIn dy, RowsIn kept, RowsOut d, int64_t m, int n, int act) {
+    const int64_t each = (n + 7) / 8, all = m * each;
+    const RowsIn up = {(const char*)kept.p + n * (T == kSrcF32 ? 4ll : 2ll), nullptr, kept.ld, 0};
+    const RowsOut du = {(char*)d.p + n * (T == kSrcF32 ? 4ll : 2ll), d.ld};
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
+        const int64_t row = i / each;
+        const int col = (int)(i - row * each) * 8;
+        Raw8<T> rg, rz, ru;
+        load8(dy, row, col, n, rg);
+        load8(kept, row, col, n, rz);
+        load8(up, row, col, n, ru);
+        float g[8], z[8], u[8];
+        unpack8(dy, rg, g);
+        unpack8(kept, rz, z);
+        unpack8(up, ru, u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float slope;
+            const float a = gate_act(z[e], act, slope);
+            z[e] = g[e] * u[e] * slope;
+            u[e] = g[e] * a;
+        }
+        store8<T>(d, row, col, n, z);
+        store8<T>(du, row, col, n, u);
+    }
+}
+
+template <int T, class C, bool ASYNC>
+void launch_gated(const ProdArgs& p, int64_t chunks, const GatedEnd<C>* fwd, const GatedBackEnd<C, T>* back, hipStream_t s) {
+    const dim3 grid(grid_for(align_up((size_t)(chunks * ceil_div(p.n, C::BC / 2)), kXcds), 1));
+    if (fwd) hipLaunchKernelGGL((k_gated<T, C, ASYNC>), grid, dim3(C::kThreads), 0, s, p, *fwd);
+    else hipLaunchKernelGGL((k_gated_back<T, C, ASYNC>), grid, dim3(C::kThreads), 0, s, p, *back);
+}
+
+struct GatedCall {
+    int act;
+    void* y;
+    bool y_f32;
+    void* kept;
+    RowsIn dy;               // null: forward
+    void* d;
+};
+
+// The kernel by size, as the plain products' (product.hip) at twice the columns.
+void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s) {
+    const int es = elem(dtype);
+    const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && (int64_t)p.k * es % 16 == 0 && aligned(p.b, 16) &&
+                      p.m * p.lda * es <= kBufferBytes && 2 * (int64_t)p.n * p.k * es <= kBufferBytes;
+    const int64_t each = p.m / p.n_groups;
+    int tile = each <= 48 || (ceil_div(p.m, 32) + p.n_groups) * ceil_div(p.n, 64) <= 512 ? 32 : 128;
+    if (dtype == HTL_BF16 && fast && ceil_div(p.m, 256) * ceil_div(p.n, 128) >= 224 && each >= 256) tile = 256;
+    p.rows = (uint32_t)tile;
+    const int64_t chunks = p.m / tile + p.n_groups + 1;
+    auto go = [&](auto t, auto shape, auto async) {
+        constexpr int T = decltype(t)::value;
+        using C = decltype(shape);
+        const GatedEnd<C> fwd = {p.n, c.act, c.y, c.y_f32, T == kSrcF32, c.kept};
+        const GatedBackEnd<C, T> back = {p.n, c.act, c.dy, c.d};
+        launch_gated<T, C, decltype(async)::value>(p, chunks, c.dy.p ? nullptr : &fwd, c.dy.p ? &back : nullptr, s);
+    };
+    using F32 = std::integral_constant<int, kSrcF32>;
+    using B16 = std::integral_constant<int, kSrcBf16>;
+    using Yes = std::true_type;
+    using No = std::false_type;
+    if (dtype == HTL_BF16) {
+        if (tile == 256) go(B16(), Big(), Yes());
+        else if (tile == 128 && fast) go(B16(), Mid(), Yes());
+        else if (tile == 128) go(B16(), Mid(), No());
+        else if (fast) go(B16(), Small(), Yes());
+        else go(B16(), Small(), No());
+    } else {
+        if (tile == 128 && fast) go(F32(), Mid(), Yes());
+        else if (tile == 128) go(F32(), Mid(), No());
+        else if (fast) go(F32(), Small(), Yes());
+        else go(F32(), Small(), No());
+    }
+}
+
+}  // namespace
+}  // namespace htl
+
+using namespace htl;
+
+#define GATED_CHECK(name)                                                                                        \
+    HTL_REQUIRE(m >= 0 && m <= kMaxRows, name ": row count out of range");                                       \
+    HTL_REQUIRE(n >= 1 && n <= HTL_MAX_PRODUCT_DIM / 2 && k >= 1 && k <= HTL_MAX_PRODUCT_DIM, name ": n or k out of range"); \
+    HTL_REQUIRE(n_groups >= 1 && n_groups <= kMaxGroups, name ": group count out of range");                     \
+    HTL_REQUIRE(known(dtype), name ": dtype must be HTL_F32 or HTL_BF16");                                       \
+    HTL_REQUIRE(act == HTL_ACT_NONE || act == HTL_ACT_SIGMOID || act == HTL_ACT_SILU, name ": unknown activation"); \
+    HTL_REQUIRE(offsets || (n_groups == 1 && !order), name ": several groups need offsets");                     \
+    HTL_REQUIRE(aligned(order, 4) && aligned(offsets, 4), name ": misaligned pointer")
+
+extern "C" htl_status gated_mm(const void* x, int64_t ldx, const void* w, htl_dtype dtype, int64_t m, int n, int k,
+                               const int32_t* order, const int32_t* offsets, int n_groups, htl_act act, void* y,
+                               htl_dtype y_dtype, void* kept, hipStream_t stream) {
+    clear_error();
+    GATED_CHECK("gated_mm");
+    HTL_REQUIRE(known(y_dtype), "gated_mm: dtype must be HTL_F32 or HTL_BF16");
+    HTL_REQUIRE(ldx >= k, "gated_mm: row stride below k");
+    if (m == 0) return HTL_OK;
+    const int es = elem(dtype);
+    HTL_REQUIRE(x && w && y, "gated_mm: null pointer");
+    HTL_REQUIRE(aligned(x, es) && aligned(w, es) && aligned(y, elem(y_dtype)) && aligned(kept, es),
+                "gated_mm: misaligned pointer");
+    const ProdArgs p = {x, w, nullptr, order, offsets, m, ldx, k, k, n, k, n_groups, 0, nullptr, 0, 0};
+    launch_pairs(p, dtype, {(int)act, y, y_dtype == HTL_F32, kept, {}, nullptr}, stream);
+    return check_launch("gated_mm");
+}
+
+extern "C" size_t gated_mm_backward_workspace_bytes(int64_t m, int n_groups, int n, int k, htl_dtype dtype) {
+    if (m < 0 || m > kMaxRows || n_groups < 1 || n_groups > kMaxGroups || n < 1 || n > HTL_MAX_PRODUCT_DIM / 2 || k < 1 ||
+        k > HTL_MAX_PRODUCT_DIM || !known(dtype))
+        return 0;
+    return align_up((size_t)m * 2 * n * elem(dtype) + 1, 256) + sums_dw_bytes(m, n_groups, 2 * n, k);
+}
+
+extern "C" htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, const void* w,
+                                        htl_dtype dtype, const void* kept, int64_t m, int n, int k, const int32_t* order,
+                                        const int32_t* offsets, int n_groups, htl_act act, void* dx, htl_dtype dx_dtype,
+                                        void* dw, void* ws, size_t ws_bytes, hipStream_t stream) {
+    clear_error();
+    GATED_CHECK("gated_mm_backward");
+    HTL_REQUIRE(known(dx_dtype), "gated_mm_backward: dtype must be HTL_F32 or HTL_BF16");
+    HTL_REQUIRE(ld_dy >= n && ldx >= k, "gated_mm_backward: row stride below the row's length");
+    if (!dx && !dw) return HTL_OK;
+    const int es = elem(dtype);
+    HTL_REQUIRE(m == 0 || (dy && w && x), "gated_mm_backward: null pointer");
+    HTL_REQUIRE(aligned(dy, es) && aligned(x, es) && aligned(w, es) && aligned(kept, es) && aligned(dx, elem(dx_dtype)) &&
+                    aligned(dw, es),
+                "gated_mm_backward: misaligned pointer");
+    HTL_REQUIRE(ws && aligned(ws, 256) && ws_bytes >= gated_mm_backward_workspace_bytes(m, n_groups, n, k, dtype),
+                "gated_mm_backward: workspace too small or misaligned");
+    void* d = ws;
+    void* sums = (char*)ws + align_up((size_t)m * 2 * n * es + 1, 256);
+    if (m > 0) {
+        const RowsIn in = {dy, nullptr, ld_dy, 0};
+        if (kept) {
+            const RowsIn from = {kept, nullptr, 2 * (int64_t)n, 0};
+            const RowsOut to = {d, 2 * (int64_t)n};
+            const dim3 grid(grid_for(m * ceil_div(n, 8), 256));
+            if (dtype == HTL_F32) hipLaunchKernelGGL(k_gated_slopes<kSrcF32>, grid, dim3(256), 0, stream, in, from, to, m, n, (int)act);
+            else hipLaunchKernelGGL(k_gated_slopes<kSrcBf16>, grid, dim3(256), 0, stream, in, from, to, m, n, (int)act);
+        } else {
+            const ProdArgs p = {x, w, nullptr, order, offsets, m, ldx, k, k, n, k, n_groups, 0, nullptr, 0, 0};
+            launch_pairs(p, dtype, {(int)act, nullptr, false, nullptr, in, d}, stream);
+        }
+        const htl_status st = check_launch("gated_mm_backward");
+        if (st != HTL_OK) return st;
+    }
+    if (dx) {
+        const htl_status st = rows_dx(d, 2 * (int64_t)n, w, k, dtype, m, 2 * n, k, order, offsets, n_groups, dx, dx_dtype,
+                                      false, stream);
+        if (st != HTL_OK) return st;
+    }
+    if (!dw) return HTL_OK;
+    return sums_dw(d, 2 * (int64_t)n, x, ldx, dtype, m, 2 * n, k, order, offsets, n_groups, dw, dtype, sums, stream);
+}

@@ -233,9 +233,10 @@ __global__ __launch_bounds__(1024) void k_sum_chunks(const float* __restrict__ p
     }
 }
 
-// Wide rows (a matrix each): four columns per thread.
+// Wide rows (a matrix each): four columns per thread, in fp32 or rounded to bf16.
+template <bool BF16>
 __global__ __launch_bounds__(256) void k_sum_wide(const float* __restrict__ partial, int64_t limit,
-                                                  float* __restrict__ out, const int32_t* __restrict__ offsets,
+                                                  void* __restrict__ out, const int32_t* __restrict__ offsets,
                                                   int n_groups, int64_t m, uint32_t R, int64_t width) {
     const int g = blockIdx.y;
     int64_t first;
@@ -245,18 +246,24 @@ __global__ __launch_bounds__(256) void k_sum_wide(const float* __restrict__ part
     if (first + count > limit) count = first < limit ? (int)(limit - first) : 0;   // offsets that overlap
     for (int64_t d = (blockIdx.x * 256ll + threadIdx.x) * 4; d < width; d += gridDim.x * 1024ll) {
         const float* p = partial + first * width + d;
-        float* o = out + g * width + d;
+        const int64_t at = g * width + d;
         if (width % 4 == 0) {
             f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
             for (int c = 0; c < count; ++c) v += *(const f32x4*)(p + c * width);
-            __builtin_memcpy(__builtin_assume_aligned(o, 4), &v, 16);
+            if (BF16) {
+                const u32x2 b = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                store_at<2>((uint16_t*)out + at, b);
+            } else {
+                store_at<4>((float*)out + at, v);
+            }
         } else {
             for (int j = 0; j < 4 && d + j < width; ++j) {
                 float v = 0.0f;
 #pragma unroll 8
                 for (int c = 0; c < count; ++c) v += p[c * width + j];
-                o[j] = v;
+                if (BF16) ((uint16_t*)out)[at + j] = (uint16_t)f32_to_bf16_bits(v);
+                else ((float*)out)[at + j] = v;
             }
         }
     }
@@ -279,18 +286,19 @@ int64_t norm_chunks(int64_t m, int n_groups, int dim) { return m / norm_chunk_ro
 int64_t norm_slots(int64_t m, int n_groups, int dim) { return split_chunks(m, n_groups, norm_chunk_rows(m, dim)); }
 uint32_t norm_rows_per_chunk(int64_t m, int dim) { return norm_chunk_rows(m, dim); }
 
-htl_status sum_chunks(const float* partial, int64_t limit, float* out, float* out2, const int32_t* offsets, int n_groups, int64_t m, uint32_t R,
-                      int64_t width, hipStream_t stream) {
+htl_status sum_chunks(const float* partial, int64_t limit, void* out, float* out2, const int32_t* offsets, int n_groups,
+                      int64_t m, uint32_t R, int64_t width, hipStream_t stream, bool bf16) {
     if (m <= (int64_t)R) return HTL_OK;      // every group is one chunk
-    if (width >= 65536 && !out2) {
+    if (bf16 || (width >= 65536 && !out2)) {
         const int64_t blocks = ceil_div(width, 1024), most = ceil_div(4096, n_groups);
-        hipLaunchKernelGGL(k_sum_wide, dim3((unsigned)(blocks < most ? blocks : most), (unsigned)n_groups), dim3(256), 0,
-                           stream, partial, limit, out, offsets, n_groups, m, R, width);
+        const dim3 grid((unsigned)(blocks < most ? blocks : most), (unsigned)n_groups);
+        if (bf16) hipLaunchKernelGGL(k_sum_wide<true>, grid, dim3(256), 0, stream, partial, limit, out, offsets, n_groups, m, R, width);
+        else hipLaunchKernelGGL(k_sum_wide<false>, grid, dim3(256), 0, stream, partial, limit, out, offsets, n_groups, m, R, width);
         return check_launch("partial sums");
     }
     const int64_t cols = ceil_div(width, 64);
     hipLaunchKernelGGL(k_sum_chunks, dim3((unsigned)(cols < 4096 ? cols : 4096), (unsigned)n_groups, out2 ? 2 : 1),
-                       dim3(1024), 0, stream, partial, limit, out, out2, offsets, n_groups, m, R, width);
+                       dim3(1024), 0, stream, partial, limit, (float*)out, out2, offsets, n_groups, m, R, width);
     return check_launch("partial sums");
 }
 

@@ -1,0 +1,632 @@
+// Losses of a softmax over a whole vocabulary, which never hold the scores of
+// a row with all of it, and their gradients.
+//
+//   s_iv = x_i w_v / T                  (x [m][k], w [vocab][k], T the temperature)
+//   lse_i = log sum_v exp(s_iv)
+//   loss_i = lse_i - s_i,target         (softmax_loss)
+//   p_i = softmax over a teacher's listed items of its logits / T
+//   loss_i = lse_i + sum_j p_ij (log p_ij - s_i,item j)       (distill_loss)
+//   d_iv = (exp(s_iv - lse_i) - p_iv) dloss_i / T             (p 1 at the target)
+//   dx_i = sum_v d_iv w_v,   dw_v = sum_i d_iv x_i
+//
+// Forward: tiles of the product x w^T whose end leaves, for each row and each
+// of its waves' columns, the largest score and the sum of exponentials below
+// it; a second kernel joins these.  Backward: pieces of the vocabulary, each
+// three products: the scores again, their end writing d in the rows' type (an
+// operand of the matrix instructions that follow), then dx += d w and dw = d^T x.
+#include "tile.h"
+
+namespace htl {
+namespace {
+
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+
+// Indices of items, int32 or int64; -1 for one outside the vocabulary.
+struct Items {
+    const void* p;
+    bool wide;
+    int vocab;
+    __device__ __forceinline__ int at(int64_t i) const {
+        const int64_t v = wide ? ((const int64_t*)p)[i] : (int64_t)((const int32_t*)p)[i];
+        return v >= 0 && v < vocab ? (int)v : -1;
+    }
+};
+
+struct Best {                // of some scores, in units of ln 2: the largest, and the sum of 2^(score - largest)
+    float top, sum;
+};
+__device__ __forceinline__ Best join(const Best& a, const Best& b) {
+    const float top = fmaxf(a.top, b.top), at = top == -INFINITY ? 0.0f : top;
+    return {top, a.sum * __builtin_amdgcn_exp2f(a.top - at) + b.sum * __builtin_amdgcn_exp2f(b.top - at)};
+}
+
+// Forward end: partial[block][row] of each wave's columns, and the target's score.
+template <class C> struct ScoreEnd {
+    static constexpr bool kPairs = false;
+    int64_t m;
+    int cols, v0, block0;    // columns of this piece, its first item and its first block
+    float scale;             // 1 / T
+    Best* partial;           // [blocks][m]
+    Items targets;           // p null: none
+    float* target_score;     // [m]
+    template <class RowOf>
+    __device__ __forceinline__ void operator()(const TileAt&, bool grouped, int, int c0, int, int wc, RowOf row_of,
+                                               f32x4 (&acc)[C::TC][C::TR]) const {
+        if (!grouped) return;
+        constexpr int W = C::TC * 16;
+        const int first = c0 + wc, q = __lane_id() >> 4;
+        const bool whole = first + W <= cols;
+        const float unit = scale * kLog2e;
+#pragma unroll
+        for (int j = 0; j < C::TR; ++j) {
+            const int64_t row = row_of(j * 16 + (__lane_id() & 15));
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < C::TC; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (first + i * 16 + q * 4 + e >= cols) acc[i][j][e] = -INFINITY;
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < C::TC; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, acc[i][j][e]);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float high = top * unit, at = top == -INFINITY ? 0.0f : high;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < C::TC; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], unit, -at));
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (row < 0) continue;
+            if (q == 0) partial[(int64_t)(block0 + first / W) * m + row] = {high, sum};
+            if (targets.p) {
+                const int t = targets.at(row) - v0 - first;
+                if ((uint32_t)t < (uint32_t)W) {
+#pragma unroll
+                    for (int i = 0; i < C::TC; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (i * 16 + q * 4 + e == t) target_score[row] = acc[i][j][e] * scale;
+                }
+            }
+        }
+    }
+};
+
+// Backward end: d of a piece's columns, [m][ld] of the rows' type.
+template <class C> struct SlopeEnd {
+    static constexpr bool kPairs = false;
+    int cols, v0;
+    int64_t ld;
+    float scale;
+    const float* lse;
+    const float* dloss;
+    Items targets;           // p null: none (a teacher's items are put in afterwards)
+    void* d;
+    bool f32;
+    template <class RowOf>
+    __device__ __forceinline__ void operator()(const TileAt&, bool grouped, int, int c0, int, int wc, RowOf row_of,
+                                               f32x4 (&acc)[C::TC][C::TR]) const {
+        if (!grouped) return;
+        constexpr int W = C::TC * 16;
+        const int first = c0 + wc, q = __lane_id() >> 4;
+        const float unit = scale * kLog2e;
+#pragma unroll
+        for (int j = 0; j < C::TR; ++j) {
+            const int64_t row = row_of(j * 16 + (__lane_id() & 15));
+            const float at = row < 0 ? 0.0f : lse[row] * kLog2e, g = row < 0 ? 0.0f : dloss[row] * scale;
+            f32x4 v[C::TC];
+#pragma unroll
+            for (int i = 0; i < C::TC; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], unit, -at));
+            if (targets.p && row >= 0) {
+                const int t = targets.at(row) - v0 - first;
+                if ((uint32_t)t < (uint32_t)W) {
+#pragma unroll
+                    for (int i = 0; i < C::TC; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (i * 16 + q * 4 + e == t) v[i][e] -= 1.0f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < C::TC; ++i) v[i] *= g;
+            store_rows<C::TC>(d, f32, row, ld, first, cols, v);
+        }
+    }
+};
+
+template <int T, class C, bool ASYNC, class End>
+__global__ __launch_bounds__(C::kThreads, 2) void k_scores(ProdArgs p, End end) {
+    product_tiles<T, kFwd, C, ASYNC>(p, end);
+}
+
+// lse of 16 rows from their partial sums, and the losses: 16 threads a row.
+__global__ __launch_bounds__(256) void k_softmax_finish(const Best* __restrict__ partial, int blocks, int64_t m,
+                                                        Items targets, const float* __restrict__ target_score,
+                                                        float* __restrict__ loss, float* __restrict__ lse) {
+    __shared__ Best s[16][16];
+    const int r = threadIdx.x & 15, part = threadIdx.x >> 4;
+    const int64_t row = blockIdx.x * 16ll + r;
+    const bool on = row < m && targets.at(row) >= 0;
+    Best b = {-INFINITY, 0.0f};
+    if (on)
+        for (int i = part; i < blocks; i += 16) b = join(b, partial[(int64_t)i * m + row]);
+    s[part][r] = b;
+    __syncthreads();
+    if (part || row >= m) return;
+    for (int i = 1; i < 16; ++i) b = join(b, s[i][r]);
+    const float l = (b.top + __builtin_amdgcn_logf(b.sum)) * kLn2;
+    lse[row] = on ? l : 0.0f;
+    loss[row] = on ? l - target_score[row] : 0.0f;
+}
+
+// A wave's dot product of two rows, the same in every lane.
+template <int T> __device__ __forceinline__ float row_dot(const RowsIn& a, int64_t i, const RowsIn& b, int64_t j, int k) {
+    float s = 0.0f;
+    for (int c = __lane_id() * 8; c < k; c += 512) {
+        Raw8<T> ra, rb;
+        float va[8], vb[8];
+        load8(a, i, c, k, ra);
+        load8(b, j, c, k, rb);
+        unpack8(a, ra, va);
+        unpack8(b, rb, vb);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = __builtin_fmaf(va[e], vb[e], s);
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) s += __shfl_xor(s, off);
+    return s;
+}
+
+// Scores of a teacher's items: a wave an entry.
+template <int T>
+__global__ __launch_bounds__(256) void k_item_scores(RowsIn x, RowsIn w, int64_t m, int k, Items items, int top,
+                                                     float scale, float* __restrict__ scores) {
+    const int64_t all = m * top;
+    for (int64_t i = blockIdx.x * 4ll + (threadIdx.x >> 6); i < all; i += gridDim.x * 4ll) {
+        const int v = items.at(i);
+        const float s = v >= 0 ? row_dot<T>(x, i / top, w, v, k) * scale : 0.0f;
+        if (__lane_id() == 0) scores[i] = s;
+    }
+}
+
+struct Teacher {
+    Items items;
+    const void* logits;
+    int64_t ld;              // of logits' rows
+    bool f32;
+    int top;
+    float scale;             // 1 / T
+    // logit / T in units of ln 2; -inf for an entry that is not there
+    __device__ __forceinline__ float logit(int64_t row, int j) const {
+        if (items.at(row * top + j) < 0) return -INFINITY;
+        const float v = f32 ? ((const float*)logits)[row * ld + j] : bf16_lo(((const uint16_t*)logits)[row * ld + j]);
+        return v * scale * kLog2e;
+    }
+};
+// log2 of the sum of the teacher's exponentials of a row, one wave; false where no entry is there.
+__device__ __forceinline__ bool teacher_sum(const Teacher& t, int64_t row, float& sum) {
+    float top = -INFINITY;
+    for (int j = __lane_id(); j < t.top; j += 64) {
+        const float v = t.logit(row, j);
+        top = v != v ? INFINITY : fmaxf(top, v);             // (a NaN makes the sum one)
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
+    if (top == -INFINITY) return false;
+    float s = 0.0f;
+    for (int j = __lane_id(); j < t.top; j += 64) s += __builtin_amdgcn_exp2f(t.logit(row, j) - top);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) s += __shfl_xor(s, off);
+    sum = top + __builtin_amdgcn_logf(s);
+    return true;
+}
+
+// lse and loss against a teacher: a wave a row.
+__global__ __launch_bounds__(256) void k_distill_finish(const Best* __restrict__ partial, int blocks, int64_t m, Teacher t,
+                                                        const float* __restrict__ scores, float* __restrict__ loss,
+                                                        float* __restrict__ lse) {
+    const int64_t row = blockIdx.x * 4ll + (threadIdx.x >> 6);
+    if (row >= m) return;
+    float all;
+    if (!teacher_sum(t, row, all)) {
+        if (__lane_id() == 0) loss[row] = lse[row] = 0.0f;
+        return;
+    }
+    Best b = {-INFINITY, 0.0f};
+    for (int i = __lane_id(); i < blocks; i += 64) b = join(b, partial[(int64_t)i * m + row]);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) b = join(b, {__shfl_xor(b.top, off), __shfl_xor(b.sum, off)});
+    const float l = (b.top + __builtin_amdgcn_logf(b.sum)) * kLn2;
+    float sum = 0.0f;
+    for (int j = __lane_id(); j < t.top; j += 64) {
+        const float logp = t.logit(row, j) - all;
+        if (logp > -INFINITY || logp != logp)                // an entry of share 0 adds nothing
+            sum += __builtin_amdgcn_exp2f(logp) * (logp * kLn2 + (l - scores[row * t.top + j]));
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
+    if (__lane_id() == 0) {
+        loss[row] = sum;
+        lse[row] = l;
+    }
+}
+
+// Which rows take part (0, or -1: none), and, of a teacher's entries, d: an
+// item listed twice has the shares of both in each.  A wave a row.
+__global__ __launch_bounds__(256) void k_active(int64_t m, Items targets, int32_t* __restrict__ ids) {
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < m; i += gridDim.x * 256ll) ids[i] = targets.at(i) >= 0 ? 0 : -1;
+}
+__global__ __launch_bounds__(256) void k_teach(int64_t m, Teacher t, const float* __restrict__ scores,
+                                               const float* __restrict__ lse, const float* __restrict__ dloss,
+                                               int32_t* __restrict__ ids, float* __restrict__ d) {
+    const int64_t row = blockIdx.x * 4ll + (threadIdx.x >> 6);
+    if (row >= m) return;
+    float all;
+    const bool on = teacher_sum(t, row, all);
+    if (__lane_id() == 0) ids[row] = on ? 0 : -1;
+    if (!on) return;
+    const float g = dloss[row] * t.scale, l = lse[row];
+    for (int j0 = 0; j0 < t.top; j0 += 64) {
+        const int j = j0 + __lane_id();
+        const int item = j < t.top ? t.items.at(row * t.top + j) : -1;
+        float share = 0.0f;
+        for (int i0 = 0; i0 < t.top; i0 += 64) {
+            const int i = i0 + __lane_id();
+            const int other = i < t.top ? t.items.at(row * t.top + i) : -1;
+            const float p = other >= 0 ? __builtin_amdgcn_exp2f(t.logit(row, i) - all) : 0.0f;
+            const int count = t.top - i0 < 64 ? t.top - i0 : 64;
+            for (int n = 0; n < count; ++n) {
+                const int it = __shfl(other, n);
+                const float pn = __shfl(p, n);
+                if (it == item) share += pn;
+            }
+        }
+        if (item >= 0)
+            d[row * t.top + j] = (__builtin_amdgcn_exp2f((scores[row * t.top + j] - l) * kLog2e) - share) * g;
+    }
+}
+// Puts the teacher's entries of a piece of the vocabulary into d.
+template <int T>
+__global__ __launch_bounds__(256) void k_put_items(int64_t m, Items items, int top, const int32_t* __restrict__ ids,
+                                                   const float* __restrict__ entries, int v0, int cols, int64_t ld,
+                                                   void* __restrict__ d) {
+    const int64_t all = m * top;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
+        const int64_t row = i / top;
+        const int c = items.at(i) - v0;
+        if ((uint32_t)c >= (uint32_t)cols || items.at(i) < 0 || ids[row] != 0) continue;
+        if (T == kSrcF32) ((float*)d)[row * ld + c] = entries[i];
+        else ((uint16_t*)d)[row * ld + c] = (uint16_t)f32_to_bf16_bits(entries[i]);
+    }
+}
+
+__global__ __launch_bounds__(256) void k_round_rows(const float* __restrict__ in, uint16_t* __restrict__ out, int64_t n) {
+    for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 4; i < n; i += gridDim.x * 1024ll) {
+        if (i + 4 <= n) {
+            f32x4 v;
+            load_at<4>(in + i, v);
+            const u32x2 b = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+            store_at<2>(out + i, b);
+        } else {
+            for (int64_t e = i; e < n; ++e) out[e] = (uint16_t)f32_to_bf16_bits(in[e]);
+        }
+    }
+}
+
+// ------------------------------------------------------------ launches ----
+struct Rows2 {               // x and w as the calls have them
+    const void* x;
+    const void* w;
+    int64_t ldx, ldw, m;
+    int vocab, k;
+    htl_dtype dtype;
+};
+
+// The product x w^T of `cols` items from v0 on, with an end made by `make` for
+// the tile's shape.  Tiles by size, as the plain products' (product.hip).
+constexpr int64_t kFewRows = 48;
+int tile_of(const Rows2& r, int cols, bool& fast) {
+    const int es = elem(r.dtype);
+    fast = r.ldx * es % 16 == 0 && r.ldw * es % 16 == 0 && (int64_t)r.k * es % 16 == 0 && aligned(r.x, 16) &&
+           aligned(r.w, 16) && r.m * r.ldx * es <= kBufferBytes && cols * r.ldw * es <= kBufferBytes;
+    if (r.dtype == HTL_BF16 && fast && r.m >= 256 && ceil_div(r.m, 256) * ceil_div(cols, 256) >= 224) return 256;
+    return r.m <= kFewRows ? 32 : 128;
+}
+// A wave's columns: those of a block of partial sums.
+int wave_cols(int64_t m) { return m <= kFewRows ? Small::TC * 16 : Mid::TC * 16; }
+static_assert(Mid::TC == Big::TC, "blocks of partial sums");
+
+template <class Make>
+void launch_scores(const Rows2& r, int tile, bool fast, int v0, int cols, const int32_t* order, const int32_t* offsets,
+                   Make make, hipStream_t s) {
+    const char* w = (const char*)r.w + (int64_t)v0 * r.ldw * elem(r.dtype);
+    const ProdArgs p = {r.x, w, nullptr, order, offsets, r.m, r.ldx, r.ldw, r.ldw, cols, r.k, 1, (uint32_t)tile, nullptr, 0, 0};
+    auto go = [&](auto t, auto shape, auto async) {
+        using C = decltype(shape);
+        const auto end = make(shape);
+        const dim3 grid(grid_for(align_up((size_t)((r.m / tile + 2) * ceil_div(cols, C::BC)), kXcds), 1));
+        hipLaunchKernelGGL((k_scores<decltype(t)::value, C, decltype(async)::value, decltype(end)>), grid,
+                           dim3(C::kThreads), 0, s, p, end);
+    };
+    using F32 = std::integral_constant<int, kSrcF32>;
+    using B16 = std::integral_constant<int, kSrcBf16>;
+    using Yes = std::true_type;
+    using No = std::false_type;
+    if (r.dtype == HTL_BF16) {
+        if (tile == 256) go(B16(), Big(), Yes());
+        else if (tile == 128 && fast) go(B16(), Mid(), Yes());
+        else if (tile == 128) go(B16(), Mid(), No());
+        else if (fast) go(B16(), Small(), Yes());
+        else go(B16(), Small(), No());
+    } else {
+        if (tile == 128 && fast) go(F32(), Mid(), Yes());
+        else if (tile == 128) go(F32(), Mid(), No());
+        else if (fast) go(F32(), Small(), Yes());
+        else go(F32(), Small(), No());
+    }
+}
+
+// Items whose matrix rows span less than 4 GiB (buffer offsets have 32 bits).
+int most_cols(const Rows2& r) {
+    const int64_t c = (kBufferBytes / (r.ldw * elem(r.dtype))) & ~255ll;
+    return (int)(c < 256 ? 256 : c > (1 << 30) ? 1 << 30 : c);
+}
+
+struct Carve {               // a workspace cut into 256-byte aligned parts
+    char* p;
+    size_t at;
+    template <class V> V* take(int64_t count) {
+        V* v = (V*)(p + at);
+        at += align_up((size_t)count * sizeof(V) + 1, 256);
+        return p ? v : nullptr;
+    }
+};
+
+struct ForwardSpace {
+    Best* partial;
+    float* target_score;
+    size_t bytes;
+    ForwardSpace(void* ws, int64_t m, int vocab) {
+        Carve c = {(char*)ws, 0};
+        partial = c.take<Best>(m * ceil_div(vocab, wave_cols(m)));
+        target_score = c.take<float>(m);
+        bytes = c.at;
+    }
+};
+
+// Scores of d held at a time: columns of a piece of the vocabulary.
+constexpr int64_t kPieceBytes = 512ll << 20;
+int piece_cols(int64_t m, int vocab, htl_dtype dtype) {
+    int64_t c = kPieceBytes / (elem(dtype) * (m < 1 ? 1 : m)) / 256 * 256;
+    if (c < 256) c = 256;
+    if (c > HTL_MAX_PRODUCT_DIM) c = HTL_MAX_PRODUCT_DIM;
+    return (int)(c < vocab ? c : vocab);
+}
+
+struct BackwardSpace {
+    int32_t *ids, *order, *offsets;
+    void* groups;
+    size_t group_bytes;
+    float *entries, *sum;
+    char *d, *sums;
+    size_t bytes;
+    BackwardSpace(void* ws, int64_t m, int vocab, int k, int top, htl_dtype dtype) {
+        const int cols = piece_cols(m, vocab, dtype), last = vocab % cols;
+        Carve c = {(char*)ws, 0};
+        ids = c.take<int32_t>(m);
+        order = c.take<int32_t>(m);
+        offsets = c.take<int32_t>(2);
+        group_bytes = row_groups_workspace_bytes(m, 1);
+        groups = c.take<char>(group_bytes);
+        entries = c.take<float>(m * top);
+        sum = c.take<float>(cols < vocab ? m * k : 0);
+        d = c.take<char>(m * align_up(cols, 8) * elem(dtype));
+        const size_t a = sums_dw_bytes(m, 1, cols, k), b = last ? sums_dw_bytes(m, 1, last, k) : 0;
+        sums = c.take<char>(a > b ? a : b);
+        bytes = c.at;
+    }
+};
+
+bool sizes_ok(int64_t m, int vocab, int k) {
+    return m >= 0 && m <= kMaxRows && vocab >= 1 && vocab <= HTL_MAX_VOCAB && k >= 1 && k <= HTL_MAX_PRODUCT_DIM;
+}
+
+template <class Targets>
+htl_status forward_scores(const Rows2& r, float scale, const ForwardSpace& s, const Targets& targets, int& blocks,
+                          hipStream_t stream) {
+    const int step = most_cols(r);
+    bool fast;
+    const int tile = tile_of(r, r.vocab < step ? r.vocab : step, fast), W = wave_cols(r.m);
+    blocks = (int)ceil_div(r.vocab, W);
+    for (int v0 = 0; v0 < r.vocab;) {
+        const int cols = r.vocab - v0 < step ? r.vocab - v0 : step;
+        launch_scores(r, tile, fast, v0, cols, nullptr, nullptr, [&](auto shape) {
+            return ScoreEnd<decltype(shape)>{r.m, cols, v0, v0 / W, scale, s.partial, targets, s.target_score};
+        }, stream);
+        v0 += cols;
+    }
+    return check_launch("scores");
+}
+
+// All of a backward pass once ids and the teacher's entries stand.
+htl_status backward_pieces(const Rows2& r, float scale, const BackwardSpace& s, const Items& targets, const Items& items,
+                           int top, const float* lse, const float* dloss, void* dx, htl_dtype dx_dtype, void* dw,
+                           hipStream_t stream) {
+    const int64_t m = r.m;
+    const int step = piece_cols(m, r.vocab, r.dtype), es = elem(r.dtype);
+    htl_status st = row_groups(s.ids, m, 1, s.order, s.offsets, s.groups, s.group_bytes, stream);
+    if (st != HTL_OK) return st;
+    const int64_t ld = align_up(step, 8);
+    bool fast;
+    const int tile = tile_of(r, step, fast);
+    float* sum = dx_dtype == HTL_F32 || step == r.vocab ? (float*)dx : s.sum;
+    for (int v0 = 0; v0 < r.vocab;) {
+        const int cols = r.vocab - v0 < step ? r.vocab - v0 : step;
+        launch_scores(r, tile, fast, v0, cols, s.order, s.offsets, [&](auto shape) {
+            return SlopeEnd<decltype(shape)>{cols, v0, ld, scale, lse, dloss, targets, s.d, r.dtype == HTL_F32};
+        }, stream);
+        if (top) {
+            const dim3 grid(grid_for(m * top, 256));
+            if (r.dtype == HTL_F32)
+                hipLaunchKernelGGL(k_put_items<kSrcF32>, grid, dim3(256), 0, stream, m, items, top, s.ids, s.entries, v0, cols, ld, s.d);
+            else
+                hipLaunchKernelGGL(k_put_items<kSrcBf16>, grid, dim3(256), 0, stream, m, items, top, s.ids, s.entries, v0, cols, ld, s.d);
+        }
+        st = check_launch("slopes");
+        if (st != HTL_OK) return st;
+        if (dx) {
+            st = rows_dx(s.d, ld, (const char*)r.w + (int64_t)v0 * r.ldw * es, r.ldw, r.dtype, m, cols, r.k, s.order, s.offsets,
+                         1, sum, step == r.vocab ? dx_dtype : HTL_F32, v0 > 0, stream);
+            if (st != HTL_OK) return st;
+        }
+        if (dw) {
+            st = sums_dw(s.d, ld, r.x, r.ldx, r.dtype, m, cols, r.k, s.order, s.offsets, 1,
+                         (char*)dw + (int64_t)v0 * r.k * es, r.dtype, s.sums, stream);
+            if (st != HTL_OK) return st;
+        }
+        v0 += cols;
+    }
+    if (dx && sum != (float*)dx && m > 0) {
+        hipLaunchKernelGGL(k_round_rows, dim3(grid_for(m * r.k, 1024, 1 << 14)), dim3(256), 0, stream, sum, (uint16_t*)dx, m * r.k);
+        return check_launch("dx");
+    }
+    return HTL_OK;
+}
+
+}  // namespace
+}  // namespace htl
+
+using namespace htl;
+
+#define SCORE_CHECK(name)                                                                                    \
+    HTL_REQUIRE(m >= 0 && m <= kMaxRows, name ": row count out of range");                                   \
+    HTL_REQUIRE(vocab >= 1 && vocab <= HTL_MAX_VOCAB, name ": vocabulary size out of range");                \
+    HTL_REQUIRE(k >= 1 && k <= HTL_MAX_PRODUCT_DIM, name ": k out of range");                                \
+    HTL_REQUIRE(known(dtype), name ": dtype must be HTL_F32 or HTL_BF16");                                   \
+    HTL_REQUIRE(ldx >= k && ldw >= k, name ": row stride below k");                                          \
+    HTL_REQUIRE(temperature > 0.0f && temperature <= 3.0e38f, name ": temperature must be positive and finite"); \
+    HTL_REQUIRE(index_bits == 32 || index_bits == 64, name ": indices have 32 or 64 bits")
+#define SCORE_POINTERS(name, index)                                                                          \
+    HTL_REQUIRE(w && (m == 0 || (x && index)), name ": null pointer");                                       \
+    HTL_REQUIRE(aligned(x, elem(dtype)) && aligned(w, elem(dtype)) && aligned(index, index_bits / 8), name ": misaligned pointer")
+#define SCORE_SPACE(name, bytes) \
+    HTL_REQUIRE(ws && aligned(ws, 256) && ws_bytes >= (bytes), name ": workspace too small or misaligned")
+
+extern "C" size_t softmax_loss_workspace_bytes(int64_t m, int vocab) {
+    return sizes_ok(m, vocab, 1) ? ForwardSpace(nullptr, m, vocab).bytes : 0;
+}
+
+extern "C" htl_status softmax_loss(const void* x, int64_t ldx, const void* w, int64_t ldw, htl_dtype dtype, int64_t m,
+                                   int vocab, int k, const void* targets, int index_bits, float temperature, float* loss,
+                                   float* lse, void* ws, size_t ws_bytes, hipStream_t stream) {
+    clear_error();
+    SCORE_CHECK("softmax_loss");
+    SCORE_POINTERS("softmax_loss", targets);
+    HTL_REQUIRE(m == 0 || (loss && lse), "softmax_loss: null pointer");
+    HTL_REQUIRE(aligned(loss, 4) && aligned(lse, 4), "softmax_loss: misaligned pointer");
+    SCORE_SPACE("softmax_loss", softmax_loss_workspace_bytes(m, vocab));
+    if (m == 0) return HTL_OK;
+    const Rows2 r = {x, w, ldx, ldw, m, vocab, k, dtype};
+    const Items t = {targets, index_bits == 64, vocab};
+    const ForwardSpace s(ws, m, vocab);
+    int blocks;
+    const htl_status st = forward_scores(r, 1.0f / temperature, s, t, blocks, stream);
+    if (st != HTL_OK) return st;
+    hipLaunchKernelGGL(k_softmax_finish, dim3((unsigned)ceil_div(m, 16)), dim3(256), 0, stream, s.partial, blocks, m, t,
+                       s.target_score, loss, lse);
+    return check_launch("softmax_loss");
+}
+
+extern "C" size_t softmax_loss_backward_workspace_bytes(int64_t m, int vocab, int k, htl_dtype dtype) {
+    return sizes_ok(m, vocab, k) && known(dtype) ? BackwardSpace(nullptr, m, vocab, k, 0, dtype).bytes : 0;
+}
+
+extern "C" htl_status softmax_loss_backward(const float* dloss, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                            htl_dtype dtype, int64_t m, int vocab, int k, const void* targets,
+                                            int index_bits, const float* lse, float temperature, void* dx,
+                                            htl_dtype dx_dtype, void* dw, void* ws, size_t ws_bytes, hipStream_t stream) {
+    clear_error();
+    SCORE_CHECK("softmax_loss_backward");
+    SCORE_POINTERS("softmax_loss_backward", targets);
+    HTL_REQUIRE(m == 0 || (dloss && lse), "softmax_loss_backward: null pointer");
+    HTL_REQUIRE(known(dx_dtype), "softmax_loss_backward: dtype must be HTL_F32 or HTL_BF16");
+    HTL_REQUIRE(aligned(dloss, 4) && aligned(lse, 4) && aligned(dx, elem(dx_dtype)) && aligned(dw, elem(dtype)),
+                "softmax_loss_backward: misaligned pointer");
+    SCORE_SPACE("softmax_loss_backward", softmax_loss_backward_workspace_bytes(m, vocab, k, dtype));
+    if (!dx && !dw) return HTL_OK;
+    const Rows2 r = {x, w, ldx, ldw, m, vocab, k, dtype};
+    const Items t = {targets, index_bits == 64, vocab};
+    const BackwardSpace s(ws, m, vocab, k, 0, dtype);
+    if (m > 0) hipLaunchKernelGGL(k_active, dim3(grid_for(m, 256, 1 << 12)), dim3(256), 0, stream, m, t, s.ids);
+    return backward_pieces(r, 1.0f / temperature, s, t, t, 0, lse, dloss, dx, dx_dtype, dw, stream);
+}
+
+#define DISTILL_CHECK(name)                                                                                  \
+    SCORE_CHECK(name);                                                                                       \
+    HTL_REQUIRE(top >= 1 && top <= HTL_MAX_TOP, name ": list length out of range");                          \
+    HTL_REQUIRE(ld_logits >= top, name ": row stride below the list's length");                              \
+    HTL_REQUIRE(known(logits_dtype), name ": dtype must be HTL_F32 or HTL_BF16");                            \
+    SCORE_POINTERS(name, items);                                                                             \
+    HTL_REQUIRE(m == 0 || (logits && scores && lse), name ": null pointer");                                 \
+    HTL_REQUIRE(aligned(logits, elem(logits_dtype)) && aligned(scores, 4) && aligned(lse, 4), name ": misaligned pointer")
+
+extern "C" htl_status distill_loss(const void* x, int64_t ldx, const void* w, int64_t ldw, htl_dtype dtype, int64_t m,
+                                   int vocab, int k, const void* items, int index_bits, const void* logits,
+                                   htl_dtype logits_dtype, int64_t ld_logits, int top, float temperature, float* loss,
+                                   float* lse, float* scores, void* ws, size_t ws_bytes, hipStream_t stream) {
+    clear_error();
+    DISTILL_CHECK("distill_loss");
+    HTL_REQUIRE(m == 0 || loss, "distill_loss: null pointer");
+    HTL_REQUIRE(aligned(loss, 4), "distill_loss: misaligned pointer");
+    SCORE_SPACE("distill_loss", softmax_loss_workspace_bytes(m, vocab));
+    if (m == 0) return HTL_OK;
+    const Rows2 r = {x, w, ldx, ldw, m, vocab, k, dtype};
+    const float scale = 1.0f / temperature;
+    const Teacher t = {{items, index_bits == 64, vocab}, logits, ld_logits, logits_dtype == HTL_F32, top, scale};
+    const ForwardSpace s(ws, m, vocab);
+    int blocks;
+    const htl_status st = forward_scores(r, scale, s, Items{nullptr, false, vocab}, blocks, stream);
+    if (st != HTL_OK) return st;
+    const RowsIn xr = {x, nullptr, ldx, 0}, wr = {w, nullptr, ldw, 0};
+    const dim3 grid(grid_for(m * top, 4));
+    if (dtype == HTL_F32) hipLaunchKernelGGL(k_item_scores<kSrcF32>, grid, dim3(256), 0, stream, xr, wr, m, k, t.items, top, scale, scores);
+    else hipLaunchKernelGGL(k_item_scores<kSrcBf16>, grid, dim3(256), 0, stream, xr, wr, m, k, t.items, top, scale, scores);
+    hipLaunchKernelGGL(k_distill_finish, dim3((unsigned)ceil_div(m, 4)), dim3(256), 0, stream, s.partial, blocks, m, t, scores,
+                       loss, lse);
+    return check_launch("distill_loss");
+}
+
+extern "C" size_t distill_loss_backward_workspace_bytes(int64_t m, int vocab, int k, int top, htl_dtype dtype) {
+    return sizes_ok(m, vocab, k) && known(dtype) && top >= 1 && top <= HTL_MAX_TOP
+               ? BackwardSpace(nullptr, m, vocab, k, top, dtype).bytes : 0;
+}
+
+extern "C" htl_status distill_loss_backward(const float* dloss, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                            htl_dtype dtype, int64_t m, int vocab, int k, const void* items, int index_bits,
+                                            const void* logits, htl_dtype logits_dtype, int64_t ld_logits, int top,
+                                            const float* lse, const float* scores, float temperature, void* dx,
+                                            htl_dtype dx_dtype, void* dw, void* ws, size_t ws_bytes, hipStream_t stream) {
+    clear_error();
+    DISTILL_CHECK("distill_loss_backward");
+    HTL_REQUIRE(m == 0 || dloss, "distill_loss_backward: null pointer");
+    HTL_REQUIRE(known(dx_dtype), "distill_loss_backward: dtype must be HTL_F32 or HTL_BF16");
+    HTL_REQUIRE(aligned(dloss, 4) && aligned(dx, elem(dx_dtype)) && aligned(dw, elem(dtype)),
+                "distill_loss_backward: misaligned pointer");
+    SCORE_SPACE("distill_loss_backward", distill_loss_backward_workspace_bytes(m, vocab, k, top, dtype));
+    if (!dx && !dw) return HTL_OK;
+    const Rows2 r = {x, w, ldx, ldw, m, vocab, k, dtype};
+    const float scale = 1.0f / temperature;
+    const Teacher t = {{items, index_bits == 64, vocab}, logits, ld_logits, logits_dtype == HTL_F32, top, scale};
+    const BackwardSpace s(ws, m, vocab, k, top, dtype);
+    if (m > 0)
+        hipLaunchKernelGGL(k_teach, dim3((unsigned)ceil_div(m, 4)), dim3(256), 0, stream, m, t, scores, lse, dloss, s.ids, s.entries);
+    return backward_pieces(r, scale, s, Items{nullptr, false, vocab}, t.items, top, lse, dloss, dx, dx_dtype, dw, stream);
+}

@@ -296,6 +296,14 @@ def norm_gate_backward(dout: torch.Tensor, kept_z: Union[torch.Tensor, Rows8], k
     return dz, du, dweight, dbias
 
 
+def _here(*tensors: Optional[torch.Tensor]) -> None:
+    """Refuses tensors that are not on the current device, whose stream the call goes to."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+
+
 def _weights(w: torch.Tensor, groups: Optional[RowGroups], dtype) -> Tuple[torch.Tensor, int]:
     w = _dev(w, dtype, "w")
     n = 1 if groups is None else groups.n_groups
@@ -346,4 +354,64 @@ def grouped_mm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, grou
     ws = _scratch("grouped_mm_backward", nb, d) if need_dw else None
     _check(lib().grouped_mm_backward(_ptr(dy), ld_dy, _ptr(x), ldx, _ptr(w), _dtype_code(x.dtype), m, n, k, _ptr(order),
                                      _ptr(offsets), g, _ptr(dx), code, _ptr(dw), _ptr(ws), nb, _stream()))
+    return dx, dw
+
+
+def _gated_weights(w: torch.Tensor, groups: Optional[RowGroups], dtype, k: int) -> Tuple[torch.Tensor, int, int]:
+    """(w, n_groups, n) of both projections."""
+    w, g = _weights(w, groups, dtype)
+    if w.shape[1] % 2 or not w.shape[1]:
+        raise ValueError(f"w must have shape [{g}, 2 n, k], got {tuple(w.shape)}")
+    if w.shape[2] != k:
+        raise ValueError(f"x has rows of {k}, w of {w.shape[2]}")
+    return w, g, w.shape[1] // 2
+
+
+def gated_mm(x: torch.Tensor, w: torch.Tensor, groups: Optional[RowGroups] = None, act: str = "silu", out_dtype=None,
+             keep: bool = False):
+    """Both projections of a gated block in one kernel: y[i] = act(z) * u with z and u the first and the last n of
+    w[g] @ x[i], g the group of row i; zeros for rows of no group (gated_mm).
+
+    x [m, k] and w [n_groups, 2 n, k] of one type (w [2 n, k] without groups). Returns (y, kept): y [m, n] in
+    ``out_dtype`` (x's); kept, what gated_mm_backward takes, is None (it computes z and u again) or with ``keep``
+    [m, 2 n] of x's type."""
+    act_code = _choice(_ACT, act, "act")
+    x, ldx = _rows(x, "x")
+    m, k = x.shape
+    w, g, n = _gated_weights(w, groups, x.dtype, k)
+    order, offsets = _plan(groups, m)
+    _here(x, w, order, offsets)
+    code = _dtype_code(x.dtype if out_dtype is None else out_dtype)
+    y = torch.empty((m, n), dtype=_TORCH_DTYPE[code], device=x.device)
+    kept = torch.empty((m, 2 * n), dtype=x.dtype, device=x.device) if keep else None
+    _check(lib().gated_mm(_ptr(x), ldx, _ptr(w), _dtype_code(x.dtype), m, n, k, _ptr(order), _ptr(offsets), g, act_code,
+                          _ptr(y), code, _ptr(kept), _stream()))
+    return y, kept
+
+
+def gated_mm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, kept: Optional[torch.Tensor] = None,
+                      groups: Optional[RowGroups] = None, act: str = "silu", dx_dtype=None, need_dx: bool = True,
+                      need_dw: bool = True):
+    """(dx [m, k] in ``dx_dtype`` (x's), dw [n_groups, 2 n, k] in w's type) of gated_mm; None for one not needed."""
+    act_code = _choice(_ACT, act, "act")
+    x, ldx = _rows(x, "x")
+    m, k = x.shape
+    w, g, n = _gated_weights(w, groups, x.dtype, k)
+    dy, ld_dy = _rows(dy, "dy", dtype=x.dtype)
+    if tuple(dy.shape) != (m, n):
+        raise ValueError(f"dy must have shape {(m, n)}, got {tuple(dy.shape)}")
+    if kept is not None:
+        kept = _dev(kept, x.dtype, "kept")
+        if tuple(kept.shape) != (m, 2 * n):
+            raise ValueError(f"kept must have shape {(m, 2 * n)}, got {tuple(kept.shape)}")
+    order, offsets = _plan(groups, m)
+    _here(x, dy, w, kept, order, offsets)
+    code, d = _dtype_code(x.dtype if dx_dtype is None else dx_dtype), x.device
+    dx = torch.empty((m, k), dtype=_TORCH_DTYPE[code], device=d) if need_dx else None
+    dw = torch.empty((g, 2 * n, k), dtype=x.dtype, device=d) if need_dw else None
+    nb = lib().gated_mm_backward_workspace_bytes(m, g, n, k, _dtype_code(x.dtype))
+    ws = _scratch("gated_mm_backward", nb, d)
+    _check(lib().gated_mm_backward(_ptr(dy), ld_dy, _ptr(x), ldx, _ptr(w), _dtype_code(x.dtype), _ptr(kept), m, n, k,
+                                   _ptr(order), _ptr(offsets), g, act_code, _ptr(dx), code, _ptr(dw), _ptr(ws), nb,
+                                   _stream()))
     return dx, dw

@@ -689,6 +689,95 @@ htl_status grouped_mm_backward(const void* dy, int64_t ld_dy, const void* x, int
                                const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype, float* dw,
                                void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* gated_mm -- both projections of a gated feed-forward block in one kernel:
+ * y[i] = act(z) u with z the first n and u the last n of w[g] x[i], g the group
+ * of row i; zeros for a row of no group.
+ *   x          dtype[m][k]; w dtype[n_groups][2 n][k] dense; y y_dtype[m][n];
+ *              1 <= n <= HTL_MAX_PRODUCT_DIM / 2, 1 <= k <= HTL_MAX_PRODUCT_DIM.
+ *   act        as norm_gate's.
+ *   kept       nullable dtype[m][2 n]: z and u, rounded to dtype, for the
+ *              backward pass. */
+htl_status gated_mm(const void* x, int64_t ldx, const void* w, htl_dtype dtype, int64_t m, int n, int k,
+                    const int32_t* order, const int32_t* offsets, int n_groups, htl_act act, void* y,
+                    htl_dtype y_dtype, void* kept, hipStream_t stream);
+
+/* gated_mm_backward -- gradients of gated_mm: with dz = dy u act'(z) and du =
+ * dy act(z), dx[i] = w[g]^T [dz; du] (dx nullable: not wanted) and dw[g] = the sum
+ * over the group's rows of [dz; du] x^T (dw nullable; zeros for a group of no
+ * rows).  dz and du are rounded to dtype (the products that follow take them),
+ * sums are fp32, and dw is rounded to dtype.
+ *   kept       what gated_mm wrote; null: z and u are computed again, in fp32.
+ *   dy         dtype[m][n]; dx dx_dtype[m][k]; dw dtype[n_groups][2 n][k].
+ *   ws         at least gated_mm_backward_workspace_bytes(m, n_groups, n, k,
+ *              dtype) bytes, 256-byte aligned. */
+size_t gated_mm_backward_workspace_bytes(int64_t m, int n_groups, int n, int k, htl_dtype dtype);
+htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, const void* w,
+                             htl_dtype dtype, const void* kept, int64_t m, int n, int k, const int32_t* order,
+                             const int32_t* offsets, int n_groups, htl_act act, void* dx, htl_dtype dx_dtype,
+                             void* dw, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------- losses over a vocabulary --
+ * The head of a model over an embedding lookup scores a row against every row
+ * of a vocabulary (the items that can follow): s[i][v] = x[i] . w[v] / T.  The
+ * calls below never hold the scores of all rows with all items: memory beside
+ * the operands is bounded by pieces of the vocabulary (about 512 MiB), and the
+ * backward pass computes the scores again.
+ *
+ * Shared by both losses:
+ *   x          dtype[m][k], w dtype[vocab][k] with row strides ldx, ldw >= k;
+ *              1 <= vocab <= HTL_MAX_VOCAB, 1 <= k <= HTL_MAX_PRODUCT_DIM.
+ *   indices    of index_bits 32 or 64; one outside [0, vocab) is none.
+ *   temperature  T, positive and finite.
+ *   loss, lse  float[m] out: the loss, and log sum_v exp(s[i][v]), which the
+ *              backward pass takes; both 0 for a row without a target.
+ *   dloss      float[m]: the gradient of each row's loss.
+ *   dx, dw     nullable (not wanted) dx_dtype[m][k], dtype[vocab][k].
+ * A row without a target takes no part: whatever it holds, dx is 0 there and dw
+ * does not have it.  Scores, exponentials and sums are fp32; the scores'
+ * gradients are rounded to dtype (the products that follow take them), results
+ * once more.  Results depend on the inputs alone. */
+#define HTL_MAX_VOCAB (1 << 30)
+#define HTL_MAX_TOP 1024
+
+/* softmax_loss, softmax_loss_backward -- loss[i] = lse[i] - s[i][targets[i]].
+ *   ws         at least softmax_loss_workspace_bytes(m, vocab), or
+ *              softmax_loss_backward_workspace_bytes(m, vocab, k, dtype)
+ *              bytes, 256-byte aligned (0 for arguments out of range). */
+size_t softmax_loss_workspace_bytes(int64_t m, int vocab);
+htl_status softmax_loss(const void* x, int64_t ldx, const void* w, int64_t ldw, htl_dtype dtype, int64_t m, int vocab,
+                        int k, const void* targets, int index_bits, float temperature, float* loss, float* lse,
+                        void* ws, size_t ws_bytes, hipStream_t stream);
+size_t softmax_loss_backward_workspace_bytes(int64_t m, int vocab, int k, htl_dtype dtype);
+htl_status softmax_loss_backward(const float* dloss, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                 htl_dtype dtype, int64_t m, int vocab, int k, const void* targets, int index_bits,
+                                 const float* lse, float temperature, void* dx, htl_dtype dx_dtype, void* dw, void* ws,
+                                 size_t ws_bytes, hipStream_t stream);
+
+/* distill_loss, distill_loss_backward -- the divergence of a row's softmax from
+ * a teacher's top logits: p[i] is the softmax of the listed logits / T, and
+ * loss[i] = sum_j p[i][j] (log p[i][j] - s[i][items[i][j]] + lse[i]).
+ *   items      [m][top], 1 <= top <= HTL_MAX_TOP, dense: the teacher's items of
+ *              each row, in any order; one that is none is not there, and an
+ *              item that is listed twice has the shares of both.
+ *   logits     logits_dtype[m][top], row stride ld_logits; -inf: share 0.
+ *   scores     float[m][top] out: s at the listed items (0 where none is), which
+ *              the backward pass takes.
+ * A row with no item of a logit above -inf has no target.  No gradient reaches
+ * the teacher's logits.
+ *   ws         at least softmax_loss_workspace_bytes(m, vocab), or
+ *              distill_loss_backward_workspace_bytes(m, vocab, k, top, dtype)
+ *              bytes, 256-byte aligned. */
+htl_status distill_loss(const void* x, int64_t ldx, const void* w, int64_t ldw, htl_dtype dtype, int64_t m, int vocab,
+                        int k, const void* items, int index_bits, const void* logits, htl_dtype logits_dtype,
+                        int64_t ld_logits, int top, float temperature, float* loss, float* lse, float* scores,
+                        void* ws, size_t ws_bytes, hipStream_t stream);
+size_t distill_loss_backward_workspace_bytes(int64_t m, int vocab, int k, int top, htl_dtype dtype);
+htl_status distill_loss_backward(const float* dloss, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                 htl_dtype dtype, int64_t m, int vocab, int k, const void* items, int index_bits,
+                                 const void* logits, htl_dtype logits_dtype, int64_t ld_logits, int top,
+                                 const float* lse, const float* scores, float temperature, void* dx,
+                                 htl_dtype dx_dtype, void* dw, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* htl_copy_probe -- a plain streaming device-to-device copy (one 16-byte
  * vector per thread, full grid), the achievable-bandwidth reference against
  * which the lookup kernels' HBM rates are read.  A measurement aid, not a

@@ -1,0 +1,347 @@
+"""Losses over a vocabulary against plain 64-bit forms.
+
+Tolerances are derived, not fitted.  With u = 2^-24, a score of k products is
+off by at most e = (k + 6) u times the sum of their magnitudes / T (scaling and
+the change to base 2 among it).  An exponential of it is off by e and by the
+rounding of its argument, 4 u of the largest score, relative; a sum of V such
+by (V + 64) u more.  So lse is off by r = max e + 8 u max |s| + (V + 64) u + 2 u
+|lse|, the shares q = exp(s - lse) by 2 r relative (r small), d = (q - p) g by
+|g| (2 r q + 8 u p (1 + the teacher's logits' size)) + 2 u |d|, and where d is
+kept in bf16 by half a step, 2^-8 |d|; products with d add theirs as above.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = {torch.float32: U, torch.bfloat16: 2.0 ** -8}
+
+
+def _close(got, want, tol, what):
+    got = got.detach().cpu().double()
+    bad = ~((got - want).abs() <= tol)
+    bad &= ~(torch.isnan(got) & torch.isnan(want))
+    assert not bad.any(), (what, int(bad.sum()), float((got - want).abs()[bad].max()), float(tol[bad].min()))
+
+
+class Want:
+    """Losses and gradients in fp64 with their bounds: items [m, t] and the log shares [m, t] of each row."""
+
+    def __init__(self, x, w, items, logp, heat, dloss=None, size=0.0, dx=None):
+        m, v, dt = x.shape[0], w.shape[0], x.dtype
+        k, half, dh = x.shape[1], HALF[dt], HALF[dx or dt]
+        here = (items >= 0) & (items < v) & (logp > -math.inf)
+        on = here.any(1)
+        p = torch.where(here, torch.exp(logp), 0.0)
+        x, w = x.double(), w.double()
+        x = torch.where(on[:, None], x, 0.0)
+        s, e = x @ w.t() / heat, (k + 6) * U * (x.abs() @ w.abs().t()) / heat
+        lse = torch.logsumexp(s, 1)
+        r = e.amax(1) + (8 * s.abs().amax(1) + v + 64 + 2 * lse.abs()) * U
+        at = items.clamp(0, v - 1).long()
+        terms = torch.where(here, p * (torch.where(here, logp, 0.0) - s.gather(1, at) + lse[:, None]), 0.0)
+        each = e.gather(1, at) + r[:, None] + 8 * U * (size + logp.abs().nan_to_num(posinf=0.0) + s.gather(1, at).abs() + lse.abs()[:, None])
+        rel = (items.shape[1] + 8 + 8 * size) * U
+        self.loss = torch.where(on, terms.sum(1), 0.0)
+        self.tloss = torch.where(on, (p * each).sum(1) + rel * terms.abs().sum(1), 0.0)
+        self.lse, self.tlse = torch.where(on, lse, 0.0), torch.where(on, r, 0.0)
+        if dloss is None:
+            return
+        g = torch.where(on, dloss.double() / heat, 0.0)[:, None]
+        q = torch.exp(s - lse[:, None])
+        share = torch.zeros_like(q).scatter_add_(1, at, p)
+        d = (q - share) * g
+        ed = g.abs() * (2 * r[:, None] * q + (16 + 8 * size) * U * share) + 2 * U * d.abs()
+        ed = ed + half * (d.abs() + ed)
+        self.dx = d @ w
+        t = ed @ w.abs() + (v + 2) * U * ((d.abs() + ed) @ w.abs())
+        self.tdx = t + dh * (self.dx.abs() + t)
+        self.dw = d.t() @ x
+        t = ed.t() @ x.abs() + (m + 2) * U * ((d.abs() + ed).t() @ x.abs())
+        self.tdw = t + half * (self.dw.abs() + t)
+
+
+def _data(m, v, k, dtype, seed=0, spread=2.0):
+    gen = torch.Generator().manual_seed(1000 * m + 10 * v + k + seed)
+    x = torch.randn(m, k, generator=gen).to(dtype)
+    w = (torch.randn(v, k, generator=gen) * (spread / k ** 0.5)).to(dtype)
+    targets = torch.randint(0, v, (m,), generator=gen)
+    targets[torch.rand(m, generator=gen) < 0.15] = -100
+    targets[torch.rand(m, generator=gen) < 0.05] = v
+    dloss = (torch.rand(m, generator=gen) - 0.3) / max(m, 1)
+    return x, w, targets, dloss
+
+
+def _teacher(m, v, t, seed=0):
+    gen = torch.Generator().manual_seed(77 * m + v + t + seed)
+    items = torch.stack([torch.randperm(v, generator=gen)[:t] for _ in range(m)]) if m else torch.zeros(0, t, dtype=torch.int64)
+    logits = torch.randn(m, t, generator=gen) * 3.0
+    items[torch.rand(m, t, generator=gen) < 0.1] = -1
+    logits[torch.rand(m, t, generator=gen) < 0.05] = -math.inf
+    if m > 3:
+        items[1] = -1                           # no entry at all
+        logits[2] = -math.inf                   # entries of no share
+        items[3, :] = items[3, 0].clamp(min=0)  # one item, listed over and over
+    return items, logits
+
+
+def _log_shares(items, logits, v, heat):
+    a = torch.where((items >= 0) & (items < v), logits.double() / heat, -math.inf)
+    top = a.amax(1, keepdim=True)
+    top = torch.where(top == -math.inf, 0.0, top)
+    return a - top - torch.exp(a - top).sum(1, keepdim=True).log()
+
+
+SIZES = [(0, 5, 8), (1, 1, 1), (1, 70, 16), (3, 2, 7), (7, 1000, 40), (48, 129, 64), (49, 257, 24), (130, 640, 72),
+         (200, 1023, 31), (257, 2049, 130), (600, 300, 256), (64, 20000, 96)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,v,k", SIZES)
+def test_softmax(htl, m, v, k, dtype):
+    heat = (1.0, 0.5, 2.0)[(m + v) % 3]
+    x, w, targets, dloss = _data(m, v, k, dtype)
+    if m % 2:
+        targets = targets.to(torch.int32)
+    items = targets.long()[:, None]
+    want = Want(x, w, items, torch.zeros(m, 1).double(), heat, dloss)
+    xc, wc, tc = x.cuda(), w.cuda(), targets.cuda()
+    loss, lse = htl.softmax_loss(xc, wc, tc, temperature=heat)
+    _close(lse, want.lse, want.tlse, "lse")
+    _close(loss, want.loss, want.tloss, "loss")
+    dx, dw = htl.softmax_loss_backward(dloss.cuda(), xc, wc, tc, lse, temperature=heat)
+    assert dx.dtype == dtype and dw.dtype == dtype
+    _close(dx, want.dx, want.tdx, "dx")
+    _close(dw, want.dw, want.tdw, "dw")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,v,k,t", [(0, 5, 8, 2), (1, 1, 1, 1), (5, 33, 16, 33), (40, 500, 24, 7), (60, 700, 40, 64),
+                                     (130, 640, 72, 65), (257, 2049, 130, 100), (20, 3000, 64, 1024)])
+def test_distill(htl, m, v, k, t, dtype):
+    heat = (1.0, 2.0)[(m + v) % 2]
+    x, w, _, dloss = _data(m, v, k, dtype)
+    items, logits = _teacher(m, v, t)
+    if m % 2:
+        items = items.to(torch.int32)
+    if v % 2:
+        logits = logits.bfloat16()
+    size = float(logits.float()[logits > -math.inf].abs().max()) / heat if (logits > -math.inf).any() else 0.0
+    want = Want(x, w, items.long(), _log_shares(items, logits, v, heat), heat, dloss, size)
+    xc, wc, ic, lc = x.cuda(), w.cuda(), items.cuda(), logits.cuda()
+    loss, kept = htl.distill_loss(xc, wc, ic, lc, temperature=heat)
+    _close(kept[0], want.lse, want.tlse, "lse")
+    _close(loss, want.loss, want.tloss, "loss")
+    dx, dw = htl.distill_loss_backward(dloss.cuda(), xc, wc, ic, lc, kept, temperature=heat)
+    assert dx.dtype == dtype and dw.dtype == dtype
+    _close(dx, want.dx, want.tdx, "dx")
+    _close(dw, want.dw, want.tdw, "dw")
+
+
+@pytest.mark.parametrize("m,v,k", [(1100, 20000, 256), (3000, 5000, 264), (1030, 7001, 130)])
+def test_large_tiles(htl, m, v, k):
+    x, w, targets, dloss = _data(m, v, k, torch.bfloat16)
+    want = Want(x, w, targets[:, None], torch.zeros(m, 1).double(), 1.0, dloss)
+    loss, lse = htl.softmax_loss(x.cuda(), w.cuda(), targets.cuda())
+    _close(lse, want.lse, want.tlse, "lse")
+    _close(loss, want.loss, want.tloss, "loss")
+    dx, dw = htl.softmax_loss_backward(dloss.cuda(), x.cuda(), w.cuda(), targets.cuda(), lse)
+    _close(dx, want.dx, want.tdx, "dx")
+    _close(dw, want.dw, want.tdw, "dw")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_without_a_target(htl, dtype):
+    """They may hold anything: nothing of it reaches a result."""
+    m, v, k = 150, 300, 40
+    x, w, targets, dloss = _data(m, v, k, dtype)
+    off = (targets < 0) | (targets >= v)
+    want = Want(x, w, targets[:, None], torch.zeros(m, 1).double(), 1.0, dloss)
+    x[off], dloss[off] = float("nan"), float("inf")
+    loss, lse = htl.softmax_loss(x.cuda(), w.cuda(), targets.cuda())
+    _close(loss, want.loss, want.tloss, "loss")
+    dx, dw = htl.softmax_loss_backward(dloss.cuda(), x.cuda(), w.cuda(), targets.cuda(), lse)
+    _close(dx, want.dx, want.tdx, "dx")
+    _close(dw, want.dw, want.tdw, "dw")
+    items = torch.where(off, -1, targets)[:, None].repeat(1, 2)
+    logits = torch.full((m, 2), float("nan"))
+    logits[~off] = 0.5
+    loss, kept = htl.distill_loss(x.cuda(), w.cuda(), items.cuda(), logits.cuda())
+    # one item listed twice with a half each: the loss is less by log 2, off by 64 u for the halves' logarithms
+    _close(loss, torch.where(off, 0.0, want.loss - math.log(2.0)), want.tloss + 64 * U, "loss of halves")
+    dx2, dw2 = htl.distill_loss_backward(dloss.cuda(), x.cuda(), w.cuda(), items.cuda(), logits.cuda(), kept)
+    _close(dx2, want.dx, want.tdx, "dx")
+    _close(dw2, want.dw, want.tdw, "dw")
+
+
+def test_no_row_has_a_target(htl):
+    x, w, targets, dloss = _data(30, 100, 24, torch.bfloat16)
+    targets[:] = -100
+    loss, lse = htl.softmax_loss(x.cuda(), w.cuda(), targets.cuda())
+    dx, dw = htl.softmax_loss_backward(dloss.cuda(), x.cuda(), w.cuda(), targets.cuda(), lse)
+    for t in (loss, lse, dx, dw):
+        assert not t.any()
+
+
+def test_nan_stays_in_its_row(htl):
+    m, v, k = 70, 200, 32
+    x, w, targets, dloss = _data(m, v, k, torch.float32)
+    targets[:] = 3
+    want = Want(x, w, targets[:, None], torch.zeros(m, 1).double(), 1.0, dloss)
+    x[11, 5] = float("nan")
+    loss, lse = htl.softmax_loss(x.cuda(), w.cuda(), targets.cuda())
+    rest = torch.arange(m) != 11
+    assert torch.isnan(loss[11]) and torch.isnan(lse[11])
+    _close(loss[rest], want.loss[rest], want.tloss[rest], "loss")
+    dx, dw = htl.softmax_loss_backward(dloss.cuda(), x.cuda(), w.cuda(), targets.cuda(), lse)
+    assert torch.isnan(dx[11]).all() and torch.isnan(dw).all()
+    _close(dx[rest], want.dx[rest], want.tdx[rest], "dx")
+
+
+def test_scores_of_any_size(htl):
+    """Scores in the thousands, one far above the others, and a temperature near zero: nothing overflows."""
+    m, v, k = 40, 500, 16
+    x, w, targets, dloss = _data(m, v, k, torch.float32, spread=400.0)
+    for heat in (1.0, 0.01):
+        want = Want(x, w, targets[:, None], torch.zeros(m, 1).double(), heat, dloss)
+        loss, lse = htl.softmax_loss(x.cuda(), w.cuda(), targets.cuda(), temperature=heat)
+        assert torch.isfinite(loss).all()
+        _close(lse, want.lse, want.tlse, "lse")
+        _close(loss, want.loss, want.tloss, "loss")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_strides_and_types(htl, dtype):
+    m, v, k = 90, 333, 56
+    x, w, targets, dloss = _data(m, v, k, dtype)
+    other = torch.float32 if dtype == torch.bfloat16 else torch.bfloat16
+    want = Want(x, w, targets[:, None], torch.zeros(m, 1).double(), 1.0, dloss, dx=other)
+    for pad, first in ((9, 1), (8, 0)):
+        wide, wide_w = torch.full((m, k + pad), float("nan"), dtype=dtype), torch.full((v, k + pad), float("nan"), dtype=dtype)
+        wide[:, first:k + first], wide_w[:, first:k + first] = x, w
+        xs, ws = wide.cuda()[:, first:k + first], wide_w.cuda()[:, first:k + first]
+        loss, lse = htl.softmax_loss(xs, ws, targets.cuda())
+        _close(loss, want.loss, want.tloss, "loss")
+        dx, dw = htl.softmax_loss_backward(dloss.cuda(), xs, ws, targets.cuda(), lse, dx_dtype=other)
+        assert dx.dtype == other
+        _close(dx, want.dx, want.tdx, "dx")
+        _close(dw, want.dw, want.tdw, "dw")
+    a, none = htl.softmax_loss_backward(dloss.cuda(), xs, ws, targets.cuda(), lse, dx_dtype=other, need_dw=False)
+    assert none is None and torch.equal(a, dx)
+    none, b = htl.softmax_loss_backward(dloss.cuda(), xs, ws, targets.cuda(), lse, need_dx=False)
+    assert none is None and torch.equal(b, dw)
+
+
+def test_teacher_with_one_item_is_cross_entropy(htl):
+    m, v, k = 120, 700, 64
+    x, w, targets, dloss = _data(m, v, k, torch.float32)
+    xc, wc, tc, dc = x.cuda(), w.cuda(), targets.cuda(), dloss.cuda()
+    want = Want(x, w, targets[:, None], torch.zeros(m, 1).double(), 1.0, dloss)
+    loss, kept = htl.distill_loss(xc, wc, tc[:, None], torch.full((m, 1), 3.0, device="cuda"))
+    _close(loss, want.loss, want.tloss, "loss")
+    dx, dw = htl.distill_loss_backward(dc, xc, wc, tc[:, None], torch.full((m, 1), 3.0, device="cuda"), kept)
+    _close(dx, want.dx, want.tdx, "dx")
+    _close(dw, want.dw, want.tdw, "dw")
+
+
+def test_differences(htl):
+    """The gradients against central differences of the losses."""
+    m, v, k, step = 6, 50, 9, 2.0 ** -6
+    x, w, targets, _ = _data(m, v, k, torch.float32)
+    items, logits = _teacher(m, v, 5)
+    ones = torch.ones(m).cuda()
+    heads = (lambda a, b: htl.softmax_loss(a.cuda(), b.cuda(), targets.cuda()),
+             lambda a, b: htl.distill_loss(a.cuda(), b.cuda(), items.cuda(), logits.cuda()))
+    backs = (lambda kept: htl.softmax_loss_backward(ones, x.cuda(), w.cuda(), targets.cuda(), kept),
+             lambda kept: htl.distill_loss_backward(ones, x.cuda(), w.cuda(), items.cuda(), logits.cuda(), kept))
+    # along one coordinate a loss has a third derivative of at most |x|^3 (or |w|^3) < 64 a row, m rows, and is off by
+    # 200 u: differences are off by step^2 / 6 * 64 m + 200 m u / step
+    tol = step ** 2 / 6 * 64 * m + 200 * m * U / step
+    for head, back in zip(heads, backs):
+        dx, dw = (t.cpu() for t in back(head(x, w)[1]))
+        for t, d in ((x, dx), (w, dw)):
+            for i in range(0, t.numel(), max(1, t.numel() // 25)):
+                a, b = t.clone(), t.clone()
+                a.view(-1)[i] += step
+                b.view(-1)[i] -= step
+                up, down = (head(a, w)[0], head(b, w)[0]) if t is x else (head(x, a)[0], head(x, b)[0])
+                diff = float((up.cpu().double() - down.cpu().double()).sum()) / (2 * step)
+                assert abs(diff - float(d.view(-1)[i])) <= tol
+
+
+def test_repeats_are_equal(htl):
+    x, w, targets, dloss = (t.cuda() for t in _data(700, 3000, 136, torch.bfloat16))
+    first = None
+    for _ in range(3):
+        loss, lse = htl.softmax_loss(x, w, targets)
+        got = (loss, lse, *htl.softmax_loss_backward(dloss, x, w, targets, lse))
+        if first is None:
+            first = got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def test_graph_and_streams(htl):
+    """Both losses' steps captured and replayed with new inputs, beside eager calls, and on another stream."""
+    m, v, k, t = 200, 900, 72, 6
+    x, w, targets, dloss = (a.cuda() for a in _data(m, v, k, torch.bfloat16))
+    items, logits = (a.cuda() for a in _teacher(m, v, t))
+
+    def step():
+        loss, lse = htl.softmax_loss(x, w, targets)
+        l2, kept = htl.distill_loss(x, w, items, logits)
+        return (loss, lse, *htl.softmax_loss_backward(dloss, x, w, targets, lse), l2,
+                *htl.distill_loss_backward(dloss, x, w, items, logits, kept))
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for seed in range(3):
+        for a, b in zip((x, w, targets, dloss), _data(m, v, k, torch.bfloat16, seed)):
+            a.copy_(b)
+        graph.replay()
+        eager = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, eager))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = step()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(other, eager))
+
+
+def test_block_and_head(htl):
+    """Looked-up rows through a gated block and the head, forward and backward, as a model runs them."""
+    from_, v, k, n, m = 512, 600, 64, 96, 300
+    table = htl.Table(12, k, "f32", init_seed=3)
+    rng = np.random.default_rng(5)
+    keys = torch.from_numpy(rng.integers(0, from_, m)).cuda()
+    x = htl.lookup(table, keys)[0].bfloat16() * 200.0
+    gen = torch.Generator().manual_seed(9)
+    wg = (torch.randn(2 * n, k, generator=gen) / k ** 0.5).bfloat16()
+    wo = (torch.randn(1, k, n, generator=gen) / n ** 0.5).bfloat16()
+    w = (torch.randn(v, k, generator=gen) / k ** 0.5).bfloat16()
+    targets = torch.randint(0, v, (m,), generator=gen)
+    y, kept = htl.gated_mm(x, wg.cuda(), keep=True)
+    h = htl.grouped_mm(y, wo.cuda())
+    loss, lse = htl.softmax_loss(h, w.cuda(), targets.cuda())
+    dloss = torch.full((m,), 1.0 / m, device="cuda")
+    dh, dw = htl.softmax_loss_backward(dloss, h, w.cuda(), targets.cuda(), lse)
+    dy, dwo = htl.grouped_mm_backward(dh, y, wo.cuda())
+    dx, dwg = htl.gated_mm_backward(dy, x, wg.cuda(), kept)
+    # autograd's in fp64 on the CPU; each of the chain's seven roundings to bf16 is off by 2^-8 of values of the
+    # result's own size, so norms are off by at most 8 * 2^-8
+    a = [t.double().requires_grad_() for t in (x.cpu(), wg, wo, w)]
+    z = a[0] @ a[1].t()
+    hh = (torch.nn.functional.silu(z[:, :n]) * z[:, n:]) @ a[2][0].t()
+    want = torch.nn.functional.cross_entropy(hh @ a[3].t(), targets)
+    want.backward()
+    assert abs(float(loss.double().mean()) - want.item()) <= 8 * 2.0 ** -8 * (1 + want.item())
+    for got, p in zip((dx, dwg, dwo, dw), a):
+        got = got.cpu().double().reshape(p.grad.shape)
+        assert float((got - p.grad).norm()) <= 8 * 2.0 ** -8 * float(p.grad.norm())
