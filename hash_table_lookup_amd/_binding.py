@@ -106,7 +106,7 @@ _SIGNATURES = {
     "gated_mm_backward_workspace_bytes": [_I64, _I32, _I32, _I32, _I32],
     "gated_mm_backward": [_P, _I64, _P, _I64, _P, _I32, _P, _I64, _I32, _I32, _P, _P, _I32, _I32, _P, _I32, _P, _P, _SZ,
                           _P],
-    "softmax_loss_workspace_bytes": [_I64, _I32],
+    "softmax_loss_workspace_bytes": [_I64, _I32, _I32, _I32],
     "softmax_loss": [_P, _I64, _P, _I64, _I32, _I64, _I32, _I32, _P, _I32, _F, _P, _P, _P, _SZ, _P],
     "softmax_loss_backward_workspace_bytes": [_I64, _I32, _I32, _I32],
     "softmax_loss_backward": [_P, _P, _I64, _P, _I64, _I32, _I64, _I32, _I32, _P, _I32, _P, _F, _P, _I32, _P, _P, _SZ, _P],

@@ -21,7 +21,7 @@ ARCH = os.environ.get("HTL_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["table.hip", "dedup.hip", "lookup.hip", "gather.hip", "pool.hip", "scan.hip", "backward.hip", "lru.hip",
            "copy.hip", "noalloc.hip", "debug.hip", "groups.hip", "rows8.hip", "norm.hip", "gate.hip", "product.hip",
-           "gated.hip", "scores.hip"]
+           "wide.hip", "gated.hip", "scores.hip"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",

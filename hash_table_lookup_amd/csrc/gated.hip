@@ -8,7 +8,7 @@
 // Rows of no group: y = 0, dx = 0.  z and u are formed in fp32 and only what is
 // kept of them, y, and dz and du (operands of the matrix instructions that
 // follow) are rounded to the rows' type.
-#include "tile.h"
+#include "wide.h"
 
 namespace htl {
 namespace {
@@ -22,71 +22,67 @@ template <class C> struct GatedEnd {
     void* y;                 // [m][n]
     bool y_f32, row_f32;
     void* kept;              // nullable: [m][2 n] of the rows' type
-    template <class RowOf>
-    __device__ __forceinline__ void operator()(const TileAt&, bool, int, int c0, int, int wc, RowOf row_of,
-                                               f32x4 (&acc)[C::TC][C::TR]) const {
-        const int col = c0 + wc / 2;
+    __device__ __forceinline__ void operator()(const TileAt&, bool, int, int64_t row, int col, f32x4 (&v)[C::TC]) const {
+        f32x4 out[F];
 #pragma unroll
-        for (int j = 0; j < C::TR; ++j) {
-            const int64_t row = row_of(j * 16 + (__lane_id() & 15));
-            f32x4 z[F], u[F], v[F];
+        for (int i = 0; i < F; ++i)
 #pragma unroll
-            for (int i = 0; i < F; ++i) {
-                z[i] = acc[i][j];
-                u[i] = acc[F + i][j];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float slope;
-                    v[i][e] = gate_act(z[i][e], act, slope) * u[i][e];
-                }
+            for (int e = 0; e < 4; ++e) {
+                float slope;
+                out[i][e] = gate_act(v[i][e], act, slope) * v[F + i][e];
             }
-            store_rows<F>(y, y_f32, row, n, col, n, v);
-            if (kept) {
-                store_rows<F>(kept, row_f32, row, 2 * (int64_t)n, col, n, z);
-                store_rows<F>((char*)kept + n * (row_f32 ? 4ll : 2ll), row_f32, row, 2 * (int64_t)n, col, n, u);
-            }
+        store_rows<F>(y, y_f32, row, n, col, n, out);
+        if (kept) {
+            store_rows<F>(kept, row_f32, row, 2 * (int64_t)n, col, n, v);
+            store_rows<F>((char*)kept + n * (row_f32 ? 4ll : 2ll), row_f32, row, 2 * (int64_t)n, col, n, v + F);
         }
     }
 };
 
-// The same with dy: dz and du, [m][2 n] of the rows' type.
+// The same with dy: dz and du, rows of 2 n of the rows' type, `ld` apart, by
+// row or (packed) by position in the plan.
 template <class C, int T> struct GatedBackEnd {
     static constexpr bool kPairs = true;
     static constexpr int F = C::TC / 2;
     int n, act;
     RowsIn dy;
     void* d;
-    template <class RowOf>
-    __device__ __forceinline__ void operator()(const TileAt&, bool grouped, int, int c0, int, int wc, RowOf row_of,
-                                               f32x4 (&acc)[C::TC][C::TR]) const {
+    int64_t ld;
+    bool packed;
+    __device__ __forceinline__ void operator()(const TileAt& t, bool grouped, int r, int64_t row, int col,
+                                               f32x4 (&v)[C::TC]) const {
         if (!grouped) return;                // nothing reads their gradients
-        const int col = c0 + wc / 2;
 #pragma unroll
-        for (int j = 0; j < C::TR; ++j) {
-            const int64_t row = row_of(j * 16 + (__lane_id() & 15));
-            f32x4 dz[F], du[F];
-#pragma unroll
-            for (int i = 0; i < F; ++i) {
-                const int c = col + i * 16 + (__lane_id() >> 4) * 4;
-                float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (row >= 0) {
+        for (int i = 0; i < F; ++i) {
+            const int c = col + i * 16 + (__lane_id() >> 4) * 4;
+            float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (row >= 0) {
+                const char* at = (const char*)dy.p + (row * dy.ld + c) * (T == kSrcF32 ? 4 : 2);
+                if (c + 4 <= n) {
+                    if (T == kSrcF32) {
+                        load_at<4>(at, g);
+                    } else {
+                        u32x2 w;
+                        load_at<2>(at, w);
+                        g[0] = bf16_lo(w[0]), g[1] = bf16_hi(w[0]), g[2] = bf16_lo(w[1]), g[3] = bf16_hi(w[1]);
+                    }
+                } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (c + e < n)
-                            g[e] = T == kSrcF32 ? ((const float*)dy.p)[row * dy.ld + c + e]
-                                                : bf16_lo(((const uint16_t*)dy.p)[row * dy.ld + c + e]);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float slope;
-                    const float a = gate_act(acc[i][j][e], act, slope);
-                    dz[i][e] = g[e] * acc[F + i][j][e] * slope;
-                    du[i][e] = g[e] * a;
+                        if (c + e < n) g[e] = T == kSrcF32 ? ((const float*)at)[e] : bf16_lo(((const uint16_t*)at)[e]);
                 }
             }
-            store_rows<F>(d, T == kSrcF32, row, 2 * (int64_t)n, col, n, dz);
-            store_rows<F>((char*)d + n * (T == kSrcF32 ? 4ll : 2ll), T == kSrcF32, row, 2 * (int64_t)n, col, n, du);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float slope;
+                const float a = gate_act(v[i][e], act, slope);
+                v[i][e] = g[e] * v[F + i][e] * slope;
+                v[F + i][e] = g[e] * a;
+            }
         }
+        const int64_t to = row < 0 || !packed ? row : t.beg + r;
+        store_rows<F>(d, T == kSrcF32, to, ld, col, n, v);
+        store_rows<F>((char*)d + n * (T == kSrcF32 ? 4ll : 2ll), T == kSrcF32, to, ld, col, n, v + F);
     }
 };
 
@@ -99,15 +95,23 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_gated_back(ProdArgs p, Gated
     product_tiles<T, kFwd, C, ASYNC>(p, end);
 }
 
-// dz and du from what was kept of z and u: eight columns a lane.
+__global__ __launch_bounds__(256, 1) void k_gated_wide(ProdArgs p, GatedEnd<Wide> end) { wide_tiles<kFwd>(p, 1, end); }
+__global__ __launch_bounds__(256, 1) void k_gated_back_wide(ProdArgs p, GatedBackEnd<Wide, kSrcBf16> end) {
+    wide_tiles<kFwd>(p, 1, end);
+}
+
+// dz and du from what was kept of z and u: eight columns a lane.  order
+// (nullable): d's rows lie by position in it.
 template <int T>
-__global__ __launch_bounds__(256) void k_gated_slopes(RowsIn dy, RowsIn kept, RowsOut d, int64_t m, int n, int act) {
+__global__ __launch_bounds__(256) void k_gated_slopes(RowsIn dy, RowsIn kept, RowsOut d, const int32_t* __restrict__ order,
+                                                      int64_t m, int n, int act) {
     const int64_t each = (n + 7) / 8, all = m * each;
     const RowsIn up = {(const char*)kept.p + n * (T == kSrcF32 ? 4ll : 2ll), nullptr, kept.ld, 0};
     const RowsOut du = {(char*)d.p + n * (T == kSrcF32 ? 4ll : 2ll), d.ld};
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
-        const int64_t row = i / each;
-        const int col = (int)(i - row * each) * 8;
+        const int64_t to = i / each, row = order ? (int64_t)order[to] : to;
+        const int col = (int)(i - to * each) * 8;
+        if (row < 0 || row >= m) continue;
         Raw8<T> rg, rz, ru;
         load8(dy, row, col, n, rg);
         load8(kept, row, col, n, rz);
@@ -123,8 +127,8 @@ __global__ __launch_bounds__(256) void k_gated_slopes(RowsIn dy, RowsIn kept, Ro
             z[e] = g[e] * u[e] * slope;
             u[e] = g[e] * a;
         }
-        store8<T>(d, row, col, n, z);
-        store8<T>(du, row, col, n, u);
+        store8<T>(d, to, col, n, z);
+        store8<T>(du, to, col, n, u);
     }
 }
 
@@ -142,7 +146,12 @@ struct GatedCall {
     void* kept;
     RowsIn dy;               // null: forward
     void* d;
+    int64_t ld;
+    bool packed;             // d by position
 };
+
+// Whether wide.h's tiles fill the device (`tiles` of them) with whole rows.
+bool many(int64_t m, int n_groups, int64_t tiles) { return tiles >= 224 && m / n_groups >= 256; }
 
 // The kernel by size, as the plain products' (product.hip) at twice the columns.
 void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s) {
@@ -150,15 +159,26 @@ void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s
     const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && (int64_t)p.k * es % 16 == 0 && aligned(p.b, 16) &&
                       p.m * p.lda * es <= kBufferBytes && 2 * (int64_t)p.n * p.k * es <= kBufferBytes;
     const int64_t each = p.m / p.n_groups;
+    if (p.packed || (dtype == HTL_BF16 && fast && many(p.m, p.n_groups, ceil_div(p.m, 256) * ceil_div(p.n, 128)))) {
+        p.rows = 256;
+        const dim3 grid(grid_for(align_up((size_t)((p.m / 256 + p.n_groups + 1) * ceil_div(p.n, 128)), kXcds), 1));
+        if (c.dy.p) {
+            const GatedBackEnd<Wide, kSrcBf16> end = {p.n, c.act, c.dy, c.d, c.ld, c.packed};
+            hipLaunchKernelGGL(k_gated_back_wide, grid, dim3(Wide::kThreads), 0, s, p, end);
+        } else {
+            const GatedEnd<Wide> end = {p.n, c.act, c.y, c.y_f32, false, c.kept};
+            hipLaunchKernelGGL(k_gated_wide, grid, dim3(Wide::kThreads), 0, s, p, end);
+        }
+        return;
+    }
     int tile = each <= 48 || (ceil_div(p.m, 32) + p.n_groups) * ceil_div(p.n, 64) <= 512 ? 32 : 128;
-    if (dtype == HTL_BF16 && fast && ceil_div(p.m, 256) * ceil_div(p.n, 128) >= 224 && each >= 256) tile = 256;
     p.rows = (uint32_t)tile;
     const int64_t chunks = p.m / tile + p.n_groups + 1;
     auto go = [&](auto t, auto shape, auto async) {
         constexpr int T = decltype(t)::value;
         using C = decltype(shape);
         const GatedEnd<C> fwd = {p.n, c.act, c.y, c.y_f32, T == kSrcF32, c.kept};
-        const GatedBackEnd<C, T> back = {p.n, c.act, c.dy, c.d};
+        const GatedBackEnd<C, T> back = {p.n, c.act, c.dy, c.d, c.ld, c.packed};
         launch_gated<T, C, decltype(async)::value>(p, chunks, c.dy.p ? nullptr : &fwd, c.dy.p ? &back : nullptr, s);
     };
     using F32 = std::integral_constant<int, kSrcF32>;
@@ -166,8 +186,7 @@ void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s
     using Yes = std::true_type;
     using No = std::false_type;
     if (dtype == HTL_BF16) {
-        if (tile == 256) go(B16(), Big(), Yes());
-        else if (tile == 128 && fast) go(B16(), Mid(), Yes());
+        if (tile == 128 && fast) go(B16(), Mid(), Yes());
         else if (tile == 128) go(B16(), Mid(), No());
         else if (fast) go(B16(), Small(), Yes());
         else go(B16(), Small(), No());
@@ -178,6 +197,34 @@ void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s
         else go(F32(), Small(), No());
     }
 }
+
+struct BackSpace {
+    bool wide;
+    int64_t ld;              // of d
+    int splits;
+    char *d, *sums, *x, *w;
+    float* parts;
+    size_t bytes;
+    // tiles: whether wide.h's may be used
+    BackSpace(void* ws, int64_t m, int n_groups, int n, int k, htl_dtype dtype, bool tiles) {
+        wide = tiles && dtype == HTL_BF16 && k >= 256 && n >= 128 && 4 * n * packed_ld(k) <= kBufferBytes &&
+               many(m, n_groups, ceil_div(m, 256) * ceil_div(2 * n, 256));
+        ld = wide ? packed_ld(2 * n) : 2 * (int64_t)n;
+        splits = wide ? wide_dx_splits(m, 2 * n, k) : 1;
+        size_t at = 0;
+        auto take = [&](size_t b) {
+            char* p = (char*)ws + at;
+            at += align_up(b + 1, 256);
+            return p;
+        };
+        d = take((size_t)m * ld * elem(dtype));
+        sums = take(wide ? wide_dw_bytes(m, n_groups, 2 * n, k) : sums_dw_bytes(m, n_groups, 2 * n, k));
+        x = take(wide ? (size_t)m * packed_ld(k) * 2 : 0);
+        w = take(wide && k % 8 ? (size_t)n_groups * 2 * n * packed_ld(k) * 2 : 0);
+        parts = (float*)take(splits > 1 ? (size_t)splits * m * k * 4 : 0);
+        bytes = at;
+    }
+};
 
 }  // namespace
 }  // namespace htl
@@ -206,7 +253,7 @@ extern "C" htl_status gated_mm(const void* x, int64_t ldx, const void* w, htl_dt
     HTL_REQUIRE(aligned(x, es) && aligned(w, es) && aligned(y, elem(y_dtype)) && aligned(kept, es),
                 "gated_mm: misaligned pointer");
     const ProdArgs p = {x, w, nullptr, order, offsets, m, ldx, k, k, n, k, n_groups, 0, nullptr, 0, 0};
-    launch_pairs(p, dtype, {(int)act, y, y_dtype == HTL_F32, kept, {}, nullptr}, stream);
+    launch_pairs(p, dtype, {(int)act, y, y_dtype == HTL_F32, kept, {}, nullptr, 0, false}, stream);
     return check_launch("gated_mm");
 }
 
@@ -214,7 +261,9 @@ extern "C" size_t gated_mm_backward_workspace_bytes(int64_t m, int n_groups, int
     if (m < 0 || m > kMaxRows || n_groups < 1 || n_groups > kMaxGroups || n < 1 || n > HTL_MAX_PRODUCT_DIM / 2 || k < 1 ||
         k > HTL_MAX_PRODUCT_DIM || !known(dtype))
         return 0;
-    return align_up((size_t)m * 2 * n * elem(dtype) + 1, 256) + sums_dw_bytes(m, n_groups, 2 * n, k);
+    const size_t a = BackSpace(nullptr, m, n_groups, n, k, dtype, true).bytes;
+    const size_t b = BackSpace(nullptr, m, n_groups, n, k, dtype, false).bytes;
+    return a > b ? a : b;
 }
 
 extern "C" htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, const void* w,
@@ -233,28 +282,48 @@ extern "C" htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const voi
                 "gated_mm_backward: misaligned pointer");
     HTL_REQUIRE(ws && aligned(ws, 256) && ws_bytes >= gated_mm_backward_workspace_bytes(m, n_groups, n, k, dtype),
                 "gated_mm_backward: workspace too small or misaligned");
-    void* d = ws;
-    void* sums = (char*)ws + align_up((size_t)m * 2 * n * es + 1, 256);
+    const BackSpace s(ws, m, n_groups, n, k, dtype, k % 8 || aligned(w, 16));
+    htl_status st = HTL_OK;
+    if (s.wide && k % 8) {                   // rows that whole pieces do not make up: copied, with zeros behind them
+        st = pack_rows(w, k, nullptr, (int64_t)n_groups * 2 * n, (int64_t)n_groups * 2 * n, k, s.w, packed_ld(k), stream);
+        if (st != HTL_OK) return st;
+    }
+    // x by position in the plan
+    const bool as_is = s.wide && !order && packed_as_is(x, ldx, k);
+    if (s.wide && !as_is) {
+        st = pack_rows(x, ldx, order, m, m, k, s.x, packed_ld(k), stream);
+        if (st != HTL_OK) return st;
+    }
+    const void* xs = !s.wide || as_is ? x : s.x;
+    const void* wp = s.wide && k % 8 ? s.w : w;
+    const int64_t ldxs = !s.wide || as_is ? ldx : packed_ld(k), ldw = s.wide && k % 8 ? packed_ld(k) : k;
     if (m > 0) {
         const RowsIn in = {dy, nullptr, ld_dy, 0};
         if (kept) {
             const RowsIn from = {kept, nullptr, 2 * (int64_t)n, 0};
-            const RowsOut to = {d, 2 * (int64_t)n};
+            const RowsOut to = {s.d, s.ld};
+            const int32_t* by = s.wide ? order : nullptr;
             const dim3 grid(grid_for(m * ceil_div(n, 8), 256));
-            if (dtype == HTL_F32) hipLaunchKernelGGL(k_gated_slopes<kSrcF32>, grid, dim3(256), 0, stream, in, from, to, m, n, (int)act);
-            else hipLaunchKernelGGL(k_gated_slopes<kSrcBf16>, grid, dim3(256), 0, stream, in, from, to, m, n, (int)act);
+            if (dtype == HTL_F32) hipLaunchKernelGGL(k_gated_slopes<kSrcF32>, grid, dim3(256), 0, stream, in, from, to, by, m, n, (int)act);
+            else hipLaunchKernelGGL(k_gated_slopes<kSrcBf16>, grid, dim3(256), 0, stream, in, from, to, by, m, n, (int)act);
         } else {
-            const ProdArgs p = {x, w, nullptr, order, offsets, m, ldx, k, k, n, k, n_groups, 0, nullptr, 0, 0};
-            launch_pairs(p, dtype, {(int)act, nullptr, false, nullptr, in, d}, stream);
+            ProdArgs p = {xs, wp, nullptr, order, offsets, m, ldxs, k, ldw, n, k, n_groups, 0, nullptr, 0, 0};
+            p.packed = s.wide;
+            launch_pairs(p, dtype, {(int)act, nullptr, false, nullptr, in, s.d, s.ld, s.wide}, stream);
         }
-        const htl_status st = check_launch("gated_mm_backward");
+        st = check_launch("gated_mm_backward");
+        if (st == HTL_OK && s.wide) st = zero_behind(s.d, m, 2 * n, s.ld, stream);
         if (st != HTL_OK) return st;
     }
-    if (dx) {
-        const htl_status st = rows_dx(d, 2 * (int64_t)n, w, k, dtype, m, 2 * n, k, order, offsets, n_groups, dx, dx_dtype,
-                                      false, stream);
-        if (st != HTL_OK) return st;
+    if (dx && s.wide) {
+        st = wide_dx(s.d, s.ld, wp, ldw, m, 2 * n, k, order, offsets, n_groups, dx, dx_dtype,
+                     s.splits > 1 ? s.parts : nullptr, s.splits, false, stream);
+        if (st == HTL_OK && s.splits > 1)
+            st = sum_parts(s.parts, s.splits, m, k, order, offsets ? offsets + n_groups : nullptr, dx, dx_dtype, stream);
+    } else if (dx) {
+        st = rows_dx(s.d, s.ld, w, k, dtype, m, 2 * n, k, order, offsets, n_groups, dx, dx_dtype, false, stream);
     }
-    if (!dw) return HTL_OK;
-    return sums_dw(d, 2 * (int64_t)n, x, ldx, dtype, m, 2 * n, k, order, offsets, n_groups, dw, dtype, sums, stream);
+    if (st != HTL_OK || !dw) return st;
+    if (s.wide) return wide_dw(s.d, s.ld, xs, ldxs, m, 2 * n, k, offsets, n_groups, dw, dtype, s.sums, stream);
+    return sums_dw(s.d, s.ld, x, ldx, dtype, m, 2 * n, k, order, offsets, n_groups, dw, dtype, s.sums, stream);
 }

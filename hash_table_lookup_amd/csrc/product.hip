@@ -26,9 +26,9 @@
 namespace htl {
 namespace {
 
-template <int T, int MODE, class C, bool ASYNC, bool ADD = false>
+template <int T, int MODE, class C, bool ASYNC, bool ADD = false, bool BF16 = false>
 __global__ __launch_bounds__(C::kThreads, 2) void k_product(ProdArgs p) {
-    product_tiles<T, MODE, C, ASYNC>(p, StoreRows<MODE, C, ADD>{p});
+    product_tiles<T, MODE, C, ASYNC>(p, StoreRows<MODE, C, ADD, BF16>{p});
 }
 
 // Products whose matrix fits in LDS (the projections of a feature table's
@@ -134,11 +134,11 @@ __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resi
 }
 
 // chunks: at most this many in all
-template <int T, int MODE, class C, bool ASYNC, bool ADD = false>
+template <int T, int MODE, class C, bool ASYNC, bool ADD = false, bool BF16 = false>
 void launch(const ProdArgs& p, int64_t chunks, hipStream_t s) {
     const int64_t cols = ceil_div(MODE == kFwd ? p.n : p.k, C::BC) * (MODE == kDw ? ceil_div(p.n, C::BR) : 1);
     const dim3 grid(grid_for(align_up((size_t)(chunks * cols), kXcds), 1));
-    hipLaunchKernelGGL((k_product<T, MODE, C, ASYNC, ADD>), grid, dim3(C::kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_product<T, MODE, C, ASYNC, ADD, BF16>), grid, dim3(C::kThreads), 0, s, p);
 }
 
 template <int MODE, int LP> void launch_resident(const ProdArgs& p, int64_t chunks, int64_t bytes, hipStream_t s) {
@@ -237,7 +237,11 @@ htl_status sums_dw(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, ht
     const bool fast = ld_dy * es % 16 == 0 && ldx * es % 16 == 0 && aligned(dy, 16) && aligned(x, 16) &&
                       (int64_t)n * es % 16 == 0 && (int64_t)k * es % 16 == 0 && m * ld_dy * es <= kBufferBytes &&
                       m * ldx * es <= kBufferBytes;
-    if (dtype == HTL_BF16) {
+    if (dw_dtype == HTL_BF16) {              // of bf16 operands
+        if (fast && n >= 256 && k >= 256) launch<kSrcBf16, kDw, Big, true, false, true>(p, chunks, stream);
+        else if (fast) launch<kSrcBf16, kDw, Mid, true, false, true>(p, chunks, stream);
+        else launch<kSrcBf16, kDw, Mid, false, false, true>(p, chunks, stream);
+    } else if (dtype == HTL_BF16) {
         if (fast && n >= 256 && k >= 256) launch<kSrcBf16, kDw, Big, true>(p, chunks, stream);
         else if (fast) launch<kSrcBf16, kDw, Mid, true>(p, chunks, stream);
         else launch<kSrcBf16, kDw, Mid, false>(p, chunks, stream);

@@ -14,7 +14,7 @@
 // it; a second kernel joins these.  Backward: pieces of the vocabulary, each
 // three products: the scores again, their end writing d in the rows' type (an
 // operand of the matrix instructions that follow), then dx += d w and dw = d^T x.
-#include "tile.h"
+#include "wide.h"
 
 namespace htl {
 namespace {
@@ -49,56 +49,50 @@ template <class C> struct ScoreEnd {
     Best* partial;           // [blocks][m]
     Items targets;           // p null: none
     float* target_score;     // [m]
-    template <class RowOf>
-    __device__ __forceinline__ void operator()(const TileAt&, bool grouped, int, int c0, int, int wc, RowOf row_of,
-                                               f32x4 (&acc)[C::TC][C::TR]) const {
+    __device__ __forceinline__ void operator()(const TileAt&, bool grouped, int, int64_t row, int col, f32x4 (&v)[C::TC]) const {
         if (!grouped) return;
         constexpr int W = C::TC * 16;
-        const int first = c0 + wc, q = __lane_id() >> 4;
-        const bool whole = first + W <= cols;
+        const int q = __lane_id() >> 4;
         const float unit = scale * kLog2e;
+        if (col + W > cols) {
 #pragma unroll
-        for (int j = 0; j < C::TR; ++j) {
-            const int64_t row = row_of(j * 16 + (__lane_id() & 15));
-            if (!whole) {
+            for (int i = 0; i < C::TC; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + i * 16 + q * 4 + e >= cols) v[i][e] = -INFINITY;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < C::TC; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, v[i][e]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float high = top * unit, at = top == -INFINITY ? 0.0f : high;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < C::TC; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(v[i][e], unit, -at));
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (row < 0) return;
+        if (q == 0) partial[(int64_t)(block0 + col / W) * m + row] = {high, sum};
+        if (targets.p) {
+            const int t = targets.at(row) - v0 - col;
+            if ((uint32_t)t < (uint32_t)W) {
 #pragma unroll
                 for (int i = 0; i < C::TC; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (first + i * 16 + q * 4 + e >= cols) acc[i][j][e] = -INFINITY;
-            }
-            float top = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < C::TC; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = fmaxf(top, acc[i][j][e]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float high = top * unit, at = top == -INFINITY ? 0.0f : high;
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < C::TC; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], unit, -at));
-            sum += __shfl_xor(sum, 16);
-            sum += __shfl_xor(sum, 32);
-            if (row < 0) continue;
-            if (q == 0) partial[(int64_t)(block0 + first / W) * m + row] = {high, sum};
-            if (targets.p) {
-                const int t = targets.at(row) - v0 - first;
-                if ((uint32_t)t < (uint32_t)W) {
-#pragma unroll
-                    for (int i = 0; i < C::TC; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (i * 16 + q * 4 + e == t) target_score[row] = acc[i][j][e] * scale;
-                }
+                        if (i * 16 + q * 4 + e == t) target_score[row] = v[i][e] * scale;
             }
         }
     }
 };
 
-// Backward end: d of a piece's columns, [m][ld] of the rows' type.
+// Backward end: d of a piece's columns, rows of the rows' type `ld` apart, by
+// row or (packed) by position in the plan.
 template <class C> struct SlopeEnd {
     static constexpr bool kPairs = false;
     int cols, v0;
@@ -108,43 +102,42 @@ template <class C> struct SlopeEnd {
     const float* dloss;
     Items targets;           // p null: none (a teacher's items are put in afterwards)
     void* d;
-    bool f32;
-    template <class RowOf>
-    __device__ __forceinline__ void operator()(const TileAt&, bool grouped, int, int c0, int, int wc, RowOf row_of,
-                                               f32x4 (&acc)[C::TC][C::TR]) const {
+    bool f32, packed;
+    __device__ __forceinline__ void operator()(const TileAt& t, bool grouped, int r, int64_t row, int col,
+                                               f32x4 (&v)[C::TC]) const {
         if (!grouped) return;
         constexpr int W = C::TC * 16;
-        const int first = c0 + wc, q = __lane_id() >> 4;
+        const int q = __lane_id() >> 4;
         const float unit = scale * kLog2e;
+        const float at = row < 0 ? 0.0f : lse[row] * kLog2e, g = row < 0 ? 0.0f : dloss[row] * scale;
 #pragma unroll
-        for (int j = 0; j < C::TR; ++j) {
-            const int64_t row = row_of(j * 16 + (__lane_id() & 15));
-            const float at = row < 0 ? 0.0f : lse[row] * kLog2e, g = row < 0 ? 0.0f : dloss[row] * scale;
-            f32x4 v[C::TC];
+        for (int i = 0; i < C::TC; ++i)
 #pragma unroll
-            for (int i = 0; i < C::TC; ++i)
+            for (int e = 0; e < 4; ++e) v[i][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[i][e], unit, -at));
+        if (targets.p && row >= 0) {
+            const int at_target = targets.at(row) - v0 - col;
+            if ((uint32_t)at_target < (uint32_t)W) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[i][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], unit, -at));
-            if (targets.p && row >= 0) {
-                const int t = targets.at(row) - v0 - first;
-                if ((uint32_t)t < (uint32_t)W) {
+                for (int i = 0; i < C::TC; ++i)
 #pragma unroll
-                    for (int i = 0; i < C::TC; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (i * 16 + q * 4 + e == t) v[i][e] -= 1.0f;
-                }
+                    for (int e = 0; e < 4; ++e)
+                        if (i * 16 + q * 4 + e == at_target) v[i][e] -= 1.0f;
             }
-#pragma unroll
-            for (int i = 0; i < C::TC; ++i) v[i] *= g;
-            store_rows<C::TC>(d, f32, row, ld, first, cols, v);
         }
+#pragma unroll
+        for (int i = 0; i < C::TC; ++i) v[i] *= g;
+        store_rows<C::TC>(d, f32, row < 0 || !packed ? row : t.beg + r, ld, col, cols, v);
     }
 };
 
 template <int T, class C, bool ASYNC, class End>
 __global__ __launch_bounds__(C::kThreads, 2) void k_scores(ProdArgs p, End end) {
     product_tiles<T, kFwd, C, ASYNC>(p, end);
+}
+
+template <class End>
+__global__ __launch_bounds__(256, 1) void k_scores_wide(ProdArgs p, End end) {
+    wide_tiles<kFwd>(p, 1, end);
 }
 
 // lse of 16 rows from their partial sums, and the losses: 16 threads a row.
@@ -293,31 +286,29 @@ __global__ __launch_bounds__(256) void k_teach(int64_t m, Teacher t, const float
             d[row * t.top + j] = (__builtin_amdgcn_exp2f((scores[row * t.top + j] - l) * kLog2e) - share) * g;
     }
 }
-// Puts the teacher's entries of a piece of the vocabulary into d.
+// Which rows a teacher has entries for.
+__global__ __launch_bounds__(256) void k_taught(int64_t m, Teacher t, int32_t* __restrict__ ids) {
+    const int64_t row = blockIdx.x * 4ll + (threadIdx.x >> 6);
+    if (row >= m) return;
+    bool on = false;
+    for (int j = __lane_id(); j < t.top; j += 64) on |= t.logit(row, j) != -INFINITY;
+    const bool any = __ballot(on) != 0;
+    if (__lane_id() == 0) ids[row] = any ? 0 : -1;
+}
+// Puts the teacher's entries of a piece of the vocabulary into d, of which rows
+// lie by row or (packed) by position.
 template <int T>
-__global__ __launch_bounds__(256) void k_put_items(int64_t m, Items items, int top, const int32_t* __restrict__ ids,
+__global__ __launch_bounds__(256) void k_put_items(int64_t m, Items items, int top, const int32_t* __restrict__ order,
+                                                   const int32_t* __restrict__ offsets, bool packed,
                                                    const float* __restrict__ entries, int v0, int cols, int64_t ld,
                                                    void* __restrict__ d) {
-    const int64_t all = m * top;
+    const int64_t all = (int64_t)offsets[1] * top;
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
-        const int64_t row = i / top;
-        const int c = items.at(i) - v0;
-        if ((uint32_t)c >= (uint32_t)cols || items.at(i) < 0 || ids[row] != 0) continue;
-        if (T == kSrcF32) ((float*)d)[row * ld + c] = entries[i];
-        else ((uint16_t*)d)[row * ld + c] = (uint16_t)f32_to_bf16_bits(entries[i]);
-    }
-}
-
-__global__ __launch_bounds__(256) void k_round_rows(const float* __restrict__ in, uint16_t* __restrict__ out, int64_t n) {
-    for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 4; i < n; i += gridDim.x * 1024ll) {
-        if (i + 4 <= n) {
-            f32x4 v;
-            load_at<4>(in + i, v);
-            const u32x2 b = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-            store_at<2>(out + i, b);
-        } else {
-            for (int64_t e = i; e < n; ++e) out[e] = (uint16_t)f32_to_bf16_bits(in[e]);
-        }
+        const int64_t pos = i / top, row = order[pos], at = row * top + (i - pos * top), to = packed ? pos : row;
+        const int item = items.at(at), c = item - v0;
+        if (item < 0 || (uint32_t)c >= (uint32_t)cols) continue;
+        if (T == kSrcF32) ((float*)d)[to * ld + c] = entries[at];
+        else ((uint16_t*)d)[to * ld + c] = (uint16_t)f32_to_bf16_bits(entries[at]);
     }
 }
 
@@ -337,12 +328,14 @@ int tile_of(const Rows2& r, int cols, bool& fast) {
     const int es = elem(r.dtype);
     fast = r.ldx * es % 16 == 0 && r.ldw * es % 16 == 0 && (int64_t)r.k * es % 16 == 0 && aligned(r.x, 16) &&
            aligned(r.w, 16) && r.m * r.ldx * es <= kBufferBytes && cols * r.ldw * es <= kBufferBytes;
-    if (r.dtype == HTL_BF16 && fast && r.m >= 256 && ceil_div(r.m, 256) * ceil_div(cols, 256) >= 224) return 256;
     return r.m <= kFewRows ? 32 : 128;
 }
+// Whether wide.h's tiles fill the device.
+bool wide_of(int64_t m, int vocab, htl_dtype dtype) {
+    return dtype == HTL_BF16 && m >= 256 && ceil_div(m, 256) * ceil_div(vocab, 256) >= 224;
+}
 // A wave's columns: those of a block of partial sums.
-int wave_cols(int64_t m) { return m <= kFewRows ? Small::TC * 16 : Mid::TC * 16; }
-static_assert(Mid::TC == Big::TC, "blocks of partial sums");
+int wave_cols(int64_t m, bool wide) { return wide ? Wide::TC * 16 : m <= kFewRows ? Small::TC * 16 : Mid::TC * 16; }
 
 template <class Make>
 void launch_scores(const Rows2& r, int tile, bool fast, int v0, int cols, const int32_t* order, const int32_t* offsets,
@@ -361,8 +354,7 @@ void launch_scores(const Rows2& r, int tile, bool fast, int v0, int cols, const 
     using Yes = std::true_type;
     using No = std::false_type;
     if (r.dtype == HTL_BF16) {
-        if (tile == 256) go(B16(), Big(), Yes());
-        else if (tile == 128 && fast) go(B16(), Mid(), Yes());
+        if (tile == 128 && fast) go(B16(), Mid(), Yes());
         else if (tile == 128) go(B16(), Mid(), No());
         else if (fast) go(B16(), Small(), Yes());
         else go(B16(), Small(), No());
@@ -390,36 +382,57 @@ struct Carve {               // a workspace cut into 256-byte aligned parts
     }
 };
 
+// Items whose copied matrix rows are held at a time.
+constexpr int kPackCols = 65536;
+int pack_cols(int vocab) { return vocab < kPackCols ? vocab : kPackCols; }
+
 struct ForwardSpace {
+    bool wide;
     Best* partial;
     float* target_score;
+    int32_t *ids, *order, *offsets;
+    void* groups;
+    size_t group_bytes;
+    char *x, *w;
     size_t bytes;
-    ForwardSpace(void* ws, int64_t m, int vocab) {
+    ForwardSpace(void* ws, int64_t m, int vocab, int k, htl_dtype dtype) {
+        wide = wide_of(m, vocab, dtype);
         Carve c = {(char*)ws, 0};
-        partial = c.take<Best>(m * ceil_div(vocab, wave_cols(m)));
+        partial = c.take<Best>(m * ceil_div(vocab, wave_cols(m, wide)));
         target_score = c.take<float>(m);
+        ids = c.take<int32_t>(wide ? m : 0);
+        order = c.take<int32_t>(wide ? m : 0);
+        offsets = c.take<int32_t>(2);
+        group_bytes = wide ? row_groups_workspace_bytes(m, 1) : 0;
+        groups = c.take<char>(group_bytes);
+        x = c.take<char>(wide ? m * packed_ld(k) * 2 : 0);
+        w = c.take<char>(wide ? pack_cols(vocab) * packed_ld(k) * 2 : 0);
         bytes = c.at;
     }
 };
 
-// Scores of d held at a time: columns of a piece of the vocabulary.
+// Gradients of scores held at a time: columns of a piece of the vocabulary.
 constexpr int64_t kPieceBytes = 512ll << 20;
 int piece_cols(int64_t m, int vocab, htl_dtype dtype) {
     int64_t c = kPieceBytes / (elem(dtype) * (m < 1 ? 1 : m)) / 256 * 256;
     if (c < 256) c = 256;
-    if (c > HTL_MAX_PRODUCT_DIM) c = HTL_MAX_PRODUCT_DIM;
+    if (c > kPackCols) c = kPackCols;
     return (int)(c < vocab ? c : vocab);
 }
 
 struct BackwardSpace {
+    bool wide;
+    int step, splits;        // columns of a piece, parts of dx's sums
     int32_t *ids, *order, *offsets;
     void* groups;
     size_t group_bytes;
-    float *entries, *sum;
-    char *d, *sums;
+    float *entries, *parts;
+    char *d, *sums, *x, *w;
     size_t bytes;
     BackwardSpace(void* ws, int64_t m, int vocab, int k, int top, htl_dtype dtype) {
-        const int cols = piece_cols(m, vocab, dtype), last = vocab % cols;
+        wide = wide_of(m, vocab, dtype);
+        step = piece_cols(m, vocab, dtype);
+        splits = wide ? wide_dx_splits(m, step, k) : 1;
         Carve c = {(char*)ws, 0};
         ids = c.take<int32_t>(m);
         order = c.take<int32_t>(m);
@@ -427,10 +440,14 @@ struct BackwardSpace {
         group_bytes = row_groups_workspace_bytes(m, 1);
         groups = c.take<char>(group_bytes);
         entries = c.take<float>(m * top);
-        sum = c.take<float>(cols < vocab ? m * k : 0);
-        d = c.take<char>(m * align_up(cols, 8) * elem(dtype));
-        const size_t a = sums_dw_bytes(m, 1, cols, k), b = last ? sums_dw_bytes(m, 1, last, k) : 0;
+        parts = c.take<float>(step < vocab || splits > 1 ? splits * m * k : 0);
+        d = c.take<char>(m * packed_ld(step) * elem(dtype));
+        const int last = vocab % step ? vocab % step : step;
+        const size_t a = wide ? wide_dw_bytes(m, 1, step, k) : sums_dw_bytes(m, 1, step, k);
+        const size_t b = wide ? wide_dw_bytes(m, 1, last, k) : sums_dw_bytes(m, 1, last, k);
         sums = c.take<char>(a > b ? a : b);
+        x = c.take<char>(wide ? m * packed_ld(k) * 2 : 0);
+        w = c.take<char>(wide ? step * packed_ld(k) * 2 : 0);
         bytes = c.at;
     }
 };
@@ -439,13 +456,54 @@ bool sizes_ok(int64_t m, int vocab, int k) {
     return m >= 0 && m <= kMaxRows && vocab >= 1 && vocab <= HTL_MAX_VOCAB && k >= 1 && k <= HTL_MAX_PRODUCT_DIM;
 }
 
-template <class Targets>
-htl_status forward_scores(const Rows2& r, float scale, const ForwardSpace& s, const Targets& targets, int& blocks,
+// The same in wide.h's tiles; w: the piece's rows.
+template <class End>
+void launch_wide(const void* x, int64_t ldx, bool packed, const void* w, int64_t ldw, int64_t m, int cols, int k,
+                 const int32_t* order, const int32_t* offsets, const End& end, hipStream_t s) {
+    const ProdArgs p = {x, w, nullptr, order, offsets, m, ldx, 0, ldw, cols, k, 1, 256, nullptr, 0, 0, packed};
+    const dim3 grid(grid_for(align_up((size_t)((m / 256 + 2) * ceil_div(cols, 256)), kXcds), 1));
+    hipLaunchKernelGGL(k_scores_wide<End>, grid, dim3(Wide::kThreads), 0, s, p, end);
+}
+
+// A piece of w as an operand of wide.h's tiles: as it lies, or copied to `room`.
+htl_status piece_of(const Rows2& r, int v0, int cols, char* room, const void*& w, int64_t& ldw, hipStream_t stream) {
+    w = (const char*)r.w + (int64_t)v0 * r.ldw * 2;
+    ldw = r.ldw;
+    if (packed_as_is(r.w, r.ldw, r.k) && cols * r.ldw * 2 <= kBufferBytes) return HTL_OK;
+    const htl_status st = pack_rows(w, r.ldw, nullptr, cols, cols, r.k, room, packed_ld(r.k), stream);
+    w = room;
+    ldw = packed_ld(r.k);
+    return st;
+}
+
+// Partial sums of all scores' exponentials; ids (wide tiles only): which rows take part.
+htl_status forward_scores(const Rows2& r, float scale, const ForwardSpace& s, const Items& targets, int& blocks,
                           hipStream_t stream) {
+    const int W = wave_cols(r.m, s.wide);
+    blocks = (int)ceil_div(r.vocab, W);
+    if (s.wide) {
+        htl_status st = row_groups(s.ids, r.m, 1, s.order, s.offsets, s.groups, s.group_bytes, stream);
+        if (st != HTL_OK) return st;
+        const bool as_is = packed_as_is(r.x, r.ldx, r.k) && r.m * r.ldx * 2 <= kBufferBytes;
+        if (!as_is) st = pack_rows(r.x, r.ldx, s.order, r.m, r.m, r.k, s.x, packed_ld(r.k), stream);
+        const int most = packed_as_is(r.w, r.ldw, r.k) && kPackCols * r.ldw * 2 <= kBufferBytes ? most_cols(r) : kPackCols;
+        for (int v0 = 0; v0 < r.vocab && st == HTL_OK;) {
+            const int cols = r.vocab - v0 < most ? r.vocab - v0 : most;
+            const void* w;
+            int64_t ldw;
+            st = piece_of(r, v0, cols, s.w, w, ldw, stream);
+            if (st != HTL_OK) return st;
+            const ScoreEnd<Wide> end = {r.m, cols, v0, v0 / W, scale, s.partial, targets, s.target_score};
+            launch_wide(as_is ? r.x : s.x, as_is ? r.ldx : packed_ld(r.k), !as_is, w, ldw, r.m, cols, r.k, s.order, s.offsets,
+                        end, stream);
+            st = check_launch("scores");
+            v0 += cols;
+        }
+        return st;
+    }
     const int step = most_cols(r);
     bool fast;
-    const int tile = tile_of(r, r.vocab < step ? r.vocab : step, fast), W = wave_cols(r.m);
-    blocks = (int)ceil_div(r.vocab, W);
+    const int tile = tile_of(r, r.vocab < step ? r.vocab : step, fast);
     for (int v0 = 0; v0 < r.vocab;) {
         const int cols = r.vocab - v0 < step ? r.vocab - v0 : step;
         launch_scores(r, tile, fast, v0, cols, nullptr, nullptr, [&](auto shape) {
@@ -460,45 +518,61 @@ htl_status forward_scores(const Rows2& r, float scale, const ForwardSpace& s, co
 htl_status backward_pieces(const Rows2& r, float scale, const BackwardSpace& s, const Items& targets, const Items& items,
                            int top, const float* lse, const float* dloss, void* dx, htl_dtype dx_dtype, void* dw,
                            hipStream_t stream) {
-    const int64_t m = r.m;
-    const int step = piece_cols(m, r.vocab, r.dtype), es = elem(r.dtype);
+    const int64_t m = r.m, ld = packed_ld(s.step);
+    const int es = elem(r.dtype);
     htl_status st = row_groups(s.ids, m, 1, s.order, s.offsets, s.groups, s.group_bytes, stream);
+    if (st == HTL_OK && s.wide) st = pack_rows(r.x, r.ldx, s.order, m, m, r.k, s.x, packed_ld(r.k), stream);
     if (st != HTL_OK) return st;
-    const int64_t ld = align_up(step, 8);
     bool fast;
-    const int tile = tile_of(r, step, fast);
-    float* sum = dx_dtype == HTL_F32 || step == r.vocab ? (float*)dx : s.sum;
+    const int tile = tile_of(r, s.step, fast);
+    // dx in parts, by position, or whole
+    float* parts = s.wide ? (s.step < r.vocab || s.splits > 1 ? s.parts : nullptr)
+                          : (s.step == r.vocab ? nullptr : dx_dtype == HTL_F32 ? (float*)dx : s.parts);
     for (int v0 = 0; v0 < r.vocab;) {
-        const int cols = r.vocab - v0 < step ? r.vocab - v0 : step;
-        launch_scores(r, tile, fast, v0, cols, s.order, s.offsets, [&](auto shape) {
-            return SlopeEnd<decltype(shape)>{cols, v0, ld, scale, lse, dloss, targets, s.d, r.dtype == HTL_F32};
-        }, stream);
+        const int cols = r.vocab - v0 < s.step ? r.vocab - v0 : s.step;
+        const void* w = (const char*)r.w + (int64_t)v0 * r.ldw * es;
+        int64_t ldw = r.ldw;
+        if (s.wide) {
+            st = piece_of(r, v0, cols, s.w, w, ldw, stream);
+            if (st != HTL_OK) return st;
+            const SlopeEnd<Wide> end = {cols, v0, ld, scale, lse, dloss, targets, s.d, false, true};
+            launch_wide(s.x, packed_ld(r.k), true, w, ldw, m, cols, r.k, s.order, s.offsets, end, stream);
+        } else {
+            launch_scores(r, tile, fast, v0, cols, s.order, s.offsets, [&](auto shape) {
+                return SlopeEnd<decltype(shape)>{cols, v0, ld, scale, lse, dloss, targets, s.d, r.dtype == HTL_F32, false};
+            }, stream);
+        }
         if (top) {
             const dim3 grid(grid_for(m * top, 256));
             if (r.dtype == HTL_F32)
-                hipLaunchKernelGGL(k_put_items<kSrcF32>, grid, dim3(256), 0, stream, m, items, top, s.ids, s.entries, v0, cols, ld, s.d);
+                hipLaunchKernelGGL(k_put_items<kSrcF32>, grid, dim3(256), 0, stream, m, items, top, s.order, s.offsets, s.wide,
+                                   s.entries, v0, cols, ld, s.d);
             else
-                hipLaunchKernelGGL(k_put_items<kSrcBf16>, grid, dim3(256), 0, stream, m, items, top, s.ids, s.entries, v0, cols, ld, s.d);
+                hipLaunchKernelGGL(k_put_items<kSrcBf16>, grid, dim3(256), 0, stream, m, items, top, s.order, s.offsets, s.wide,
+                                   s.entries, v0, cols, ld, s.d);
         }
         st = check_launch("slopes");
+        if (st == HTL_OK && s.wide) st = zero_behind(s.d, m, cols, ld, stream);
+        if (st == HTL_OK && dx) {
+            if (s.wide)
+                st = wide_dx(s.d, ld, w, ldw, m, cols, r.k, s.order, s.offsets, 1, dx, dx_dtype, parts, s.splits, v0 > 0, stream);
+            else
+                st = rows_dx(s.d, ld, w, ldw, r.dtype, m, cols, r.k, s.order, s.offsets, 1, parts ? parts : dx,
+                             parts ? HTL_F32 : dx_dtype, v0 > 0, stream);
+        }
+        if (st == HTL_OK && dw) {
+            char* to = (char*)dw + (int64_t)v0 * r.k * es;
+            if (s.wide)
+                st = wide_dw(s.d, ld, s.x, packed_ld(r.k), m, cols, r.k, s.offsets, 1, to, r.dtype, s.sums, stream);
+            else
+                st = sums_dw(s.d, ld, r.x, r.ldx, r.dtype, m, cols, r.k, s.order, s.offsets, 1, to, r.dtype, s.sums, stream);
+        }
         if (st != HTL_OK) return st;
-        if (dx) {
-            st = rows_dx(s.d, ld, (const char*)r.w + (int64_t)v0 * r.ldw * es, r.ldw, r.dtype, m, cols, r.k, s.order, s.offsets,
-                         1, sum, step == r.vocab ? dx_dtype : HTL_F32, v0 > 0, stream);
-            if (st != HTL_OK) return st;
-        }
-        if (dw) {
-            st = sums_dw(s.d, ld, r.x, r.ldx, r.dtype, m, cols, r.k, s.order, s.offsets, 1,
-                         (char*)dw + (int64_t)v0 * r.k * es, r.dtype, s.sums, stream);
-            if (st != HTL_OK) return st;
-        }
         v0 += cols;
     }
-    if (dx && sum != (float*)dx && m > 0) {
-        hipLaunchKernelGGL(k_round_rows, dim3(grid_for(m * r.k, 1024, 1 << 14)), dim3(256), 0, stream, sum, (uint16_t*)dx, m * r.k);
-        return check_launch("dx");
-    }
-    return HTL_OK;
+    if (!dx || !parts || (void*)parts == dx) return HTL_OK;
+    return s.wide ? sum_parts(parts, s.splits, m, r.k, s.order, s.offsets + 1, dx, dx_dtype, stream)
+                  : sum_parts(parts, 1, m, r.k, nullptr, nullptr, dx, dx_dtype, stream);
 }
 
 }  // namespace
@@ -520,8 +594,8 @@ using namespace htl;
 #define SCORE_SPACE(name, bytes) \
     HTL_REQUIRE(ws && aligned(ws, 256) && ws_bytes >= (bytes), name ": workspace too small or misaligned")
 
-extern "C" size_t softmax_loss_workspace_bytes(int64_t m, int vocab) {
-    return sizes_ok(m, vocab, 1) ? ForwardSpace(nullptr, m, vocab).bytes : 0;
+extern "C" size_t softmax_loss_workspace_bytes(int64_t m, int vocab, int k, htl_dtype dtype) {
+    return sizes_ok(m, vocab, k) && known(dtype) ? ForwardSpace(nullptr, m, vocab, k, dtype).bytes : 0;
 }
 
 extern "C" htl_status softmax_loss(const void* x, int64_t ldx, const void* w, int64_t ldw, htl_dtype dtype, int64_t m,
@@ -532,12 +606,13 @@ extern "C" htl_status softmax_loss(const void* x, int64_t ldx, const void* w, in
     SCORE_POINTERS("softmax_loss", targets);
     HTL_REQUIRE(m == 0 || (loss && lse), "softmax_loss: null pointer");
     HTL_REQUIRE(aligned(loss, 4) && aligned(lse, 4), "softmax_loss: misaligned pointer");
-    SCORE_SPACE("softmax_loss", softmax_loss_workspace_bytes(m, vocab));
+    SCORE_SPACE("softmax_loss", softmax_loss_workspace_bytes(m, vocab, k, dtype));
     if (m == 0) return HTL_OK;
     const Rows2 r = {x, w, ldx, ldw, m, vocab, k, dtype};
     const Items t = {targets, index_bits == 64, vocab};
-    const ForwardSpace s(ws, m, vocab);
+    const ForwardSpace s(ws, m, vocab, k, dtype);
     int blocks;
+    if (s.wide) hipLaunchKernelGGL(k_active, dim3(grid_for(m, 256, 1 << 12)), dim3(256), 0, stream, m, t, s.ids);
     const htl_status st = forward_scores(r, 1.0f / temperature, s, t, blocks, stream);
     if (st != HTL_OK) return st;
     hipLaunchKernelGGL(k_softmax_finish, dim3((unsigned)ceil_div(m, 16)), dim3(256), 0, stream, s.partial, blocks, m, t,
@@ -586,13 +661,14 @@ extern "C" htl_status distill_loss(const void* x, int64_t ldx, const void* w, in
     DISTILL_CHECK("distill_loss");
     HTL_REQUIRE(m == 0 || loss, "distill_loss: null pointer");
     HTL_REQUIRE(aligned(loss, 4), "distill_loss: misaligned pointer");
-    SCORE_SPACE("distill_loss", softmax_loss_workspace_bytes(m, vocab));
+    SCORE_SPACE("distill_loss", softmax_loss_workspace_bytes(m, vocab, k, dtype));
     if (m == 0) return HTL_OK;
     const Rows2 r = {x, w, ldx, ldw, m, vocab, k, dtype};
     const float scale = 1.0f / temperature;
     const Teacher t = {{items, index_bits == 64, vocab}, logits, ld_logits, logits_dtype == HTL_F32, top, scale};
-    const ForwardSpace s(ws, m, vocab);
+    const ForwardSpace s(ws, m, vocab, k, dtype);
     int blocks;
+    if (s.wide) hipLaunchKernelGGL(k_taught, dim3((unsigned)ceil_div(m, 4)), dim3(256), 0, stream, m, t, s.ids);
     const htl_status st = forward_scores(r, scale, s, Items{nullptr, false, vocab}, blocks, stream);
     if (st != HTL_OK) return st;
     const RowsIn xr = {x, nullptr, ldx, 0}, wr = {w, nullptr, ldw, 0};

@@ -27,6 +27,7 @@ struct ProdArgs {
     float* partial;          // dw: [limit][n][k]
     int out_f32;
     int64_t limit;           // dw: chunks of split groups that `partial` has room for
+    bool packed;             // wide.h: a's rows lie by position in the plan
 };
 
 enum { kFwd = 0, kDx = 1, kDw = 2 };
@@ -96,7 +97,7 @@ template <int NT, int N> __device__ __forceinline__ int wave_bytes(int i) {
     return __builtin_amdgcn_readfirstlane(piece_at<NT, N>(i, threadIdx.x & ~63)) * 16;
 }
 
-__device__ __forceinline__ int swap_along(int r) { return (r >> 2) & 3; }
+__device__ __forceinline__ int swap_along(int r) { return (r >> 1) & 3; }
 // Rows of at least 16 pieces.  bf16: 32 lanes read 32 bytes of rows 0..3 and
 // 8..11 (and the next 32 of rows 16 on); fp32: 64 lanes read 64 bytes of each
 // of four rows 4 apart.
@@ -462,6 +463,11 @@ __device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, i
 template <int F>
 __device__ __forceinline__ void store_rows(void* out, bool f32, int64_t row, int64_t ld, int col, int cols,
                                            const f32x4* v) {
+    if constexpr (F > 4) {
+        store_rows<4>(out, f32, row, ld, col, cols, v);
+        store_rows<F - 4>(out, f32, row, ld, col + 64, cols, v + 4);
+        return;
+    }
     const int lane = __lane_id(), q = lane >> 4;
     const bool high = lane & 8;
     const int64_t other = move_lanes<kRotate8>((int)row);
@@ -557,12 +563,12 @@ __device__ __forceinline__ void store_rows(void* out, bool f32, int64_t row, int
 }
 
 // The tiles of a launch, one after another: products, and then End, which a
-// wave calls with its part of a tile,
-//   end(t, grouped, r0, c0, wr, wc, row_of, acc):
-// acc[i][j] holds 16 x 16 outputs, lane l's four at rows wr + 16 j + l % 16
-// and columns wc + 16 i + l / 16 * 4 of the tile at (r0, c0); row_of(r) is
-// where row wr + r of it goes (-1: nowhere).  End::kPairs: the columns are
-// pairs of two projections (AlongPairs), p.n of each.
+// wave calls for every 16 rows of its part of a tile,
+//   end(t, grouped, r, row, col, v):
+// v[i] holds 16 x 16 outputs, lane l's four at row r (of the tile, the wave's
+// lane's own) and columns col + 16 i + l / 16 * 4; row is where row r goes (-1:
+// nowhere).  End::kPairs: the columns are pairs of two projections (AlongPairs),
+// p.n of each, v's second half those of the first half's columns.
 template <int T, int MODE, class C, bool ASYNC, class End>
 __device__ __forceinline__ void product_tiles(const ProdArgs& p, const End& end) {
     // Slots of the ring as variables of their own: the compiler then makes a
@@ -751,49 +757,52 @@ __device__ __forceinline__ void product_tiles(const ProdArgs& p, const End& end)
             __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0): nothing comes into LDS any more
         }
         if (!busy) continue;
-        end(t, grouped, r0, c0, wr, wc, [&](int r) {
-            return MODE != kDw ? s_row[wr + r] : (r0 + wr + r < p.n ? r0 + wr + r : -1);
-        }, acc);
+#pragma unroll
+        for (int j = 0; j < C::TR; ++j) {
+            const int r = wr + j * 16 + (__lane_id() & 15);
+            f32x4 v[C::TC];
+#pragma unroll
+            for (int i = 0; i < C::TC; ++i) v[i] = acc[i][j];
+            end(t, grouped, r0 + r, MODE != kDw ? (int64_t)s_row[MODE == kDw ? 0 : r] : (int64_t)(r0 + r < p.n ? r0 + r : -1),
+                c0 + (kPairs ? wc / 2 : wc), v);
+        }
+    }
+}
+
+// The same as store_rows, added to fp32 rows.
+template <int F> __device__ __forceinline__ void add_rows(float* out, int64_t row, int64_t ld, int col, int cols, f32x4* v) {
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+        const int c = col + i * 16 + (__lane_id() >> 4) * 4;
+        float* at = out + row * ld + c;
+        if (row >= 0 && c + 4 <= cols) {
+            f32x4 had;
+            load_at<4>(at, had);
+            store_at<4>(at, had + v[i]);
+        } else if (row >= 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < cols) at[e] += v[i][e];
+        }
     }
 }
 
 // The products themselves: rows of p.out, or added to them (ADD: fp32 rows);
-// sums over rows (kDw) go to p.out where they are whole, else to p.partial.
-template <int MODE, class C, bool ADD> struct StoreRows {
+// sums over rows (kDw) go to p.out where they are whole (in bf16 with BF16), else
+// to p.partial.
+template <int MODE, class C, bool ADD, bool BF16> struct StoreRows {
     static constexpr bool kPairs = false;
     const ProdArgs& p;
-    template <class RowOf>
-    __device__ __forceinline__ void operator()(const TileAt& t, bool grouped, int r0, int c0, int wr, int wc, RowOf row_of,
-                                               f32x4 (&acc)[C::TC][C::TR]) const {
+    __device__ __forceinline__ void operator()(const TileAt& t, bool grouped, int, int64_t row, int col,
+                                               f32x4 (&v)[C::TC]) const {
         const int cols = MODE == kFwd ? p.n : p.k;
         const int64_t wg = grouped ? (int64_t)t.g * p.n * p.k : 0;
-        const bool whole = MODE != kDw || t.count == 1, f32 = p.out_f32 || !whole;
-        void* to = MODE != kDw ? p.out : (whole ? (char*)p.out + wg * (f32 ? 4 : 2) : (char*)(p.partial + t.slot * p.n * p.k));
-        if (ADD && !grouped) return;
-#pragma unroll
-        for (int j = 0; j < C::TR; ++j) {
-            const int64_t row = row_of(j * 16 + (__lane_id() & 15));
-            if (ADD) {
-#pragma unroll
-                for (int i = 0; i < C::TC; ++i) {
-                    const int c = c0 + wc + i * 16 + (__lane_id() >> 4) * 4;
-                    float* at = (float*)p.out + row * cols + c;
-                    if (row >= 0 && c + 4 <= cols) {
-                        f32x4 v;
-                        load_at<4>(at, v);
-                        store_at<4>(at, v + acc[i][j]);
-                    } else if (row >= 0) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (c + e < cols) at[e] += acc[i][j][e];
-                    }
-                }
-            } else {
-                f32x4 v[C::TC];
-#pragma unroll
-                for (int i = 0; i < C::TC; ++i) v[i] = acc[i][j];
-                store_rows<C::TC>(to, f32, row, cols, c0 + wc, cols, v);
-            }
+        const bool whole = MODE != kDw || t.count == 1;
+        void* to = MODE != kDw ? p.out : (whole ? (char*)p.out + wg * (BF16 ? 2 : 4) : (char*)(p.partial + t.slot * p.n * p.k));
+        if (!ADD) {
+            store_rows<C::TC>(to, MODE != kDw ? (bool)p.out_f32 : !BF16 || !whole, row, cols, col, cols, v);
+        } else if (grouped) {
+            add_rows<C::TC>((float*)p.out, row, cols, col, cols, v);
         }
     }
 };

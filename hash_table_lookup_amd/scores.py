@@ -67,7 +67,7 @@ def softmax_loss(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, temper
     targets, bits = _indices(targets, (m,), "targets")
     _here(x, w, targets)
     loss, lse = torch.empty((2, m), dtype=torch.float32, device=x.device)
-    nb = lib().softmax_loss_workspace_bytes(m, w.shape[0])
+    nb = lib().softmax_loss_workspace_bytes(m, w.shape[0], k, _dtype_code(x.dtype))
     ws = _scratch("softmax_loss", nb, x.device)
     _check(lib().softmax_loss(_ptr(x), ldx, _ptr(w), ldw, _dtype_code(x.dtype), m, w.shape[0], k, _ptr(targets), bits,
                               heat, _ptr(loss), _ptr(lse), _ptr(ws), nb, _stream()))
@@ -126,7 +126,7 @@ def distill_loss(x: torch.Tensor, w: torch.Tensor, top: torch.Tensor, top_logits
     _here(x, w, items, logits)
     loss, lse = torch.empty((2, m), dtype=torch.float32, device=x.device)
     scores = torch.empty((m, t), dtype=torch.float32, device=x.device)
-    nb = lib().softmax_loss_workspace_bytes(m, w.shape[0])
+    nb = lib().softmax_loss_workspace_bytes(m, w.shape[0], k, _dtype_code(x.dtype))
     ws = _scratch("softmax_loss", nb, x.device)
     _check(lib().distill_loss(_ptr(x), ldx, _ptr(w), ldw, _dtype_code(x.dtype), m, w.shape[0], k, _ptr(items), bits,
                               _ptr(logits), _dtype_code(logits.dtype), ld, t, heat, _ptr(loss), _ptr(lse), _ptr(scores),

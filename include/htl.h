@@ -740,10 +740,10 @@ htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const void* x, int64
 #define HTL_MAX_TOP 1024
 
 /* softmax_loss, softmax_loss_backward -- loss[i] = lse[i] - s[i][targets[i]].
- *   ws         at least softmax_loss_workspace_bytes(m, vocab), or
- *              softmax_loss_backward_workspace_bytes(m, vocab, k, dtype)
- *              bytes, 256-byte aligned (0 for arguments out of range). */
-size_t softmax_loss_workspace_bytes(int64_t m, int vocab);
+ *   ws         at least softmax_loss_workspace_bytes(m, vocab, k, dtype), or
+ *              softmax_loss_backward_workspace_bytes of them, bytes,
+ *              256-byte aligned (0 for arguments out of range). */
+size_t softmax_loss_workspace_bytes(int64_t m, int vocab, int k, htl_dtype dtype);
 htl_status softmax_loss(const void* x, int64_t ldx, const void* w, int64_t ldw, htl_dtype dtype, int64_t m, int vocab,
                         int k, const void* targets, int index_bits, float temperature, float* loss, float* lse,
                         void* ws, size_t ws_bytes, hipStream_t stream);
@@ -764,7 +764,7 @@ htl_status softmax_loss_backward(const float* dloss, const void* x, int64_t ldx,
  *              the backward pass takes.
  * A row with no item of a logit above -inf has no target.  No gradient reaches
  * the teacher's logits.
- *   ws         at least softmax_loss_workspace_bytes(m, vocab), or
+ *   ws         at least softmax_loss_workspace_bytes(m, vocab, k, dtype), or
  *              distill_loss_backward_workspace_bytes(m, vocab, k, top, dtype)
  *              bytes, 256-byte aligned. */
 htl_status distill_loss(const void* x, int64_t ldx, const void* w, int64_t ldw, htl_dtype dtype, int64_t m, int vocab,
