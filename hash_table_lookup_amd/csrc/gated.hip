@@ -95,9 +95,9 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_gated_back(ProdArgs p, Gated
     product_tiles<T, kFwd, C, ASYNC>(p, end);
 }
 
-__global__ __launch_bounds__(256, 1) void k_gated_wide(ProdArgs p, GatedEnd<Wide> end) { wide_tiles<kFwd>(p, 1, end); }
+__global__ __launch_bounds__(256, 1) void k_gated_wide(ProdArgs p, GatedEnd<Wide> end) { wide_tiles<kFwd>(p, end); }
 __global__ __launch_bounds__(256, 1) void k_gated_back_wide(ProdArgs p, GatedBackEnd<Wide, kSrcBf16> end) {
-    wide_tiles<kFwd>(p, 1, end);
+    wide_tiles<kFwd>(p, end);
 }
 
 // dz and du from what was kept of z and u: eight columns a lane.  order
@@ -159,15 +159,21 @@ void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s
     const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && (int64_t)p.k * es % 16 == 0 && aligned(p.b, 16) &&
                       p.m * p.lda * es <= kBufferBytes && 2 * (int64_t)p.n * p.k * es <= kBufferBytes;
     const int64_t each = p.m / p.n_groups;
-    if (p.packed || (dtype == HTL_BF16 && fast && many(p.m, p.n_groups, ceil_div(p.m, 256) * ceil_div(p.n, 128)))) {
+    // (pairs of less than 256 elements: 426,000 rows, 128 -> 256, 446 us against 300 in tiles of 128)
+    if (p.packed || (p.k >= 256 && dtype == HTL_BF16 && fast && many(p.m, p.n_groups, ceil_div(p.m, 256) * ceil_div(p.n, 128)))) {
         p.rows = 256;
-        const dim3 grid(grid_for(align_up((size_t)((p.m / 256 + p.n_groups + 1) * ceil_div(p.n, 128)), kXcds), 1));
+        p.no_rest = true;
+        const dim3 grid(grid_for(align_up((size_t)((p.m / 256 + p.n_groups) * ceil_div(p.n, 128)), kXcds), 1));
         if (c.dy.p) {
             const GatedBackEnd<Wide, kSrcBf16> end = {p.n, c.act, c.dy, c.d, c.ld, c.packed};
             hipLaunchKernelGGL(k_gated_back_wide, grid, dim3(Wide::kThreads), 0, s, p, end);
         } else {
             const GatedEnd<Wide> end = {p.n, c.act, c.y, c.y_f32, false, c.kept};
             hipLaunchKernelGGL(k_gated_wide, grid, dim3(Wide::kThreads), 0, s, p, end);
+            if (p.offsets) {
+                zero_rest(c.y, (int64_t)p.n * (c.y_f32 ? 4 : 2), p.m, p.order, p.offsets + p.n_groups, s);
+                if (c.kept) zero_rest(c.kept, (int64_t)p.n * 4, p.m, p.order, p.offsets + p.n_groups, s);
+            }
         }
         return;
     }
@@ -209,7 +215,7 @@ struct BackSpace {
     BackSpace(void* ws, int64_t m, int n_groups, int n, int k, htl_dtype dtype, bool tiles) {
         wide = tiles && dtype == HTL_BF16 && k >= 256 && n >= 128 && 4 * n * packed_ld(k) <= kBufferBytes &&
                many(m, n_groups, ceil_div(m, 256) * ceil_div(2 * n, 256));
-        ld = wide ? packed_ld(2 * n) : 2 * (int64_t)n;
+        ld = wide ? spread_ld(2 * n) : 2 * (int64_t)n;
         splits = wide ? wide_dx_splits(m, 2 * n, k) : 1;
         size_t at = 0;
         auto take = [&](size_t b) {
@@ -219,7 +225,7 @@ struct BackSpace {
         };
         d = take((size_t)m * ld * elem(dtype));
         sums = take(wide ? wide_dw_bytes(m, n_groups, 2 * n, k) : sums_dw_bytes(m, n_groups, 2 * n, k));
-        x = take(wide ? (size_t)m * packed_ld(k) * 2 : 0);
+        x = take(wide ? (size_t)m * spread_ld(k) * 2 : 0);
         w = take(wide && k % 8 ? (size_t)n_groups * 2 * n * packed_ld(k) * 2 : 0);
         parts = (float*)take(splits > 1 ? (size_t)splits * m * k * 4 : 0);
         bytes = at;
@@ -291,12 +297,12 @@ extern "C" htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const voi
     // x by position in the plan
     const bool as_is = s.wide && !order && packed_as_is(x, ldx, k);
     if (s.wide && !as_is) {
-        st = pack_rows(x, ldx, order, m, m, k, s.x, packed_ld(k), stream);
+        st = pack_rows(x, ldx, order, m, m, k, s.x, spread_ld(k), stream);
         if (st != HTL_OK) return st;
     }
     const void* xs = !s.wide || as_is ? x : s.x;
     const void* wp = s.wide && k % 8 ? s.w : w;
-    const int64_t ldxs = !s.wide || as_is ? ldx : packed_ld(k), ldw = s.wide && k % 8 ? packed_ld(k) : k;
+    const int64_t ldxs = !s.wide || as_is ? ldx : spread_ld(k), ldw = s.wide && k % 8 ? packed_ld(k) : k;
     if (m > 0) {
         const RowsIn in = {dy, nullptr, ld_dy, 0};
         if (kept) {
@@ -319,9 +325,11 @@ extern "C" htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const voi
         st = wide_dx(s.d, s.ld, wp, ldw, m, 2 * n, k, order, offsets, n_groups, dx, dx_dtype,
                      s.splits > 1 ? s.parts : nullptr, s.splits, false, stream);
         if (st == HTL_OK && s.splits > 1)
-            st = sum_parts(s.parts, s.splits, m, k, order, offsets ? offsets + n_groups : nullptr, dx, dx_dtype, stream);
+            st = sum_parts(s.parts, s.splits, false, m, k, order, offsets ? offsets + n_groups : nullptr, dx, dx_dtype, stream);
+        else if (st == HTL_OK && offsets)
+            st = zero_rest(dx, (int64_t)k * elem(dx_dtype), m, order, offsets + n_groups, stream);
     } else if (dx) {
-        st = rows_dx(s.d, s.ld, w, k, dtype, m, 2 * n, k, order, offsets, n_groups, dx, dx_dtype, false, stream);
+        st = rows_dx(s.d, s.ld, w, k, dtype, m, 2 * n, k, order, offsets, n_groups, dx, dx_dtype, stream);
     }
     if (st != HTL_OK || !dw) return st;
     if (s.wide) return wide_dw(s.d, s.ld, xs, ldxs, m, 2 * n, k, offsets, n_groups, dw, dtype, s.sums, stream);

@@ -26,9 +26,12 @@
 namespace htl {
 namespace {
 
-template <int T, int MODE, class C, bool ASYNC, bool ADD = false, bool BF16 = false>
+template <int T, int MODE, class C, bool ASYNC, bool BF16 = false>
 __global__ __launch_bounds__(C::kThreads, 2) void k_product(ProdArgs p) {
-    product_tiles<T, MODE, C, ASYNC>(p, StoreRows<MODE, C, ADD, BF16>{p});
+    product_tiles<T, MODE, C, ASYNC>(p, StoreRows<MODE, C, BF16>{p});
+}
+template <int T, class C, bool ASYNC, bool ADD> __global__ __launch_bounds__(C::kThreads, 2) void k_dx_parts(ProdArgs p) {
+    product_tiles<T, kDx, C, ASYNC, true>(p, StoreParts<C, ADD>{p});
 }
 
 // Products whose matrix fits in LDS (the projections of a feature table's
@@ -47,7 +50,7 @@ __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resi
     const int blocks = (cols + 63) / 64;
     for (int64_t b = blockIdx.x;; b += gridDim.x) {
         TileAt t;
-        const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, 0, 1, b, t);
+        const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, 0, false, 1, b, t);
         if (found < 0) return;
         if (!found) continue;
         const bool grouped = t.g < p.n_groups;
@@ -134,11 +137,11 @@ __global__ __launch_bounds__(512, BYTES <= 81920 && LP <= 4 ? 4 : 2) void k_resi
 }
 
 // chunks: at most this many in all
-template <int T, int MODE, class C, bool ASYNC, bool ADD = false, bool BF16 = false>
+template <int T, int MODE, class C, bool ASYNC, bool BF16 = false>
 void launch(const ProdArgs& p, int64_t chunks, hipStream_t s) {
     const int64_t cols = ceil_div(MODE == kFwd ? p.n : p.k, C::BC) * (MODE == kDw ? ceil_div(p.n, C::BR) : 1);
     const dim3 grid(grid_for(align_up((size_t)(chunks * cols), kXcds), 1));
-    hipLaunchKernelGGL((k_product<T, MODE, C, ASYNC, ADD, BF16>), grid, dim3(C::kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_product<T, MODE, C, ASYNC, BF16>), grid, dim3(C::kThreads), 0, s, p);
 }
 
 template <int MODE, int LP> void launch_resident(const ProdArgs& p, int64_t chunks, int64_t bytes, hipStream_t s) {
@@ -158,7 +161,7 @@ template <int MODE, int LP> void launch_resident(const ProdArgs& p, int64_t chun
 //   against 18 / 22.
 // - tiles of 256 x 256 once they fill the device: 8 x 2,048, 1,024 -> 1,024:
 //   43 / 47 against 51 / 53 with 128; 8 x 1,024: 37 / 38 against 28 / 28.
-template <int MODE, bool ADD = false> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s) {
+template <int MODE> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s) {
     const int cols = MODE == kFwd ? p.n : p.k, es = elem(dtype);
     const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && (int64_t)p.k * es % 16 == 0 && p.ldw * es % 16 == 0 &&
                       (MODE == kFwd || (int64_t)p.n * es % 16 == 0) && aligned(p.b, 16) &&
@@ -166,7 +169,7 @@ template <int MODE, bool ADD = false> void launch_rows(ProdArgs p, htl_dtype dty
     const int64_t each = p.m / p.n_groups;
     const int len = MODE == kFwd ? p.k : p.n, lp = len <= 32 ? 1 : len <= 64 ? 2 : len <= 128 ? 4 : 8;
     const int64_t bytes = ceil_div(cols, 64) * 64 * (lp * 64 + 16);
-    if (!ADD && dtype == HTL_BF16 && p.ldw == p.k && len <= 256 && bytes <= 163840 && each >= 512 && p.m >= (lp == 8 ? 1 << 20 : 1 << 16)) {
+    if (dtype == HTL_BF16 && p.ldw == p.k && len <= 256 && bytes <= 163840 && each >= 512 && p.m >= (lp == 8 ? 1 << 20 : 1 << 16)) {
         p.rows = (uint32_t)align_up((size_t)ceil_div(p.m, 1024), 256);
         const int64_t chunks = p.m / p.rows + p.n_groups + 1;
         if (lp == 1) launch_resident<MODE, 1>(p, chunks, bytes, s);
@@ -180,16 +183,16 @@ template <int MODE, bool ADD = false> void launch_rows(ProdArgs p, htl_dtype dty
     p.rows = (uint32_t)tile;
     const int64_t chunks = p.m / tile + p.n_groups + 1;
     if (dtype == HTL_BF16) {
-        if (tile == 256) launch<kSrcBf16, MODE, Big, true, ADD>(p, chunks, s);
-        else if (tile == 128 && fast) launch<kSrcBf16, MODE, Mid, true, ADD>(p, chunks, s);
-        else if (tile == 128) launch<kSrcBf16, MODE, Mid, false, ADD>(p, chunks, s);
-        else if (fast) launch<kSrcBf16, MODE, Small, true, ADD>(p, chunks, s);
-        else launch<kSrcBf16, MODE, Small, false, ADD>(p, chunks, s);
+        if (tile == 256) launch<kSrcBf16, MODE, Big, true>(p, chunks, s);
+        else if (tile == 128 && fast) launch<kSrcBf16, MODE, Mid, true>(p, chunks, s);
+        else if (tile == 128) launch<kSrcBf16, MODE, Mid, false>(p, chunks, s);
+        else if (fast) launch<kSrcBf16, MODE, Small, true>(p, chunks, s);
+        else launch<kSrcBf16, MODE, Small, false>(p, chunks, s);
     } else {
-        if (tile == 128 && fast) launch<kSrcF32, MODE, Mid, true, ADD>(p, chunks, s);
-        else if (tile == 128) launch<kSrcF32, MODE, Mid, false, ADD>(p, chunks, s);
-        else if (fast) launch<kSrcF32, MODE, Small, true, ADD>(p, chunks, s);
-        else launch<kSrcF32, MODE, Small, false, ADD>(p, chunks, s);
+        if (tile == 128 && fast) launch<kSrcF32, MODE, Mid, true>(p, chunks, s);
+        else if (tile == 128) launch<kSrcF32, MODE, Mid, false>(p, chunks, s);
+        else if (fast) launch<kSrcF32, MODE, Small, true>(p, chunks, s);
+        else launch<kSrcF32, MODE, Small, false>(p, chunks, s);
     }
 }
 
@@ -213,12 +216,49 @@ int64_t dw_slots(int64_t m, int n_groups, int n, int k) { return split_chunks(m,
 }  // namespace
 
 htl_status rows_dx(const void* dy, int64_t ld_dy, const void* w, int64_t ldw, htl_dtype dtype, int64_t m, int n, int k,
-                   const int32_t* order, const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype, bool add,
+                   const int32_t* order, const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype,
                    hipStream_t stream) {
     if (m == 0) return HTL_OK;
     const ProdArgs p = {dy, w, dx, order, offsets, m, ld_dy, k, ldw, n, k, n_groups, 0, nullptr, dx_dtype == HTL_F32, 0};
-    if (add) launch_rows<kDx, true>(p, dtype, stream);
-    else launch_rows<kDx>(p, dtype, stream);
+    launch_rows<kDx>(p, dtype, stream);
+    return check_launch("input gradients");
+}
+
+// Parts of at least 256 elements that fill the device with tiles three times
+// over, and sums of at most 256 MiB.
+int rows_dx_splits(int64_t m, int n, int k) {
+    const int64_t tiles = ceil_div(m, 128) * ceil_div(k, 128);
+    int64_t s = 768 / (tiles < 1 ? 1 : tiles);
+    if (s > n / 256) s = n / 256;
+    if (m > 0 && s > (64 << 20) / (m * k)) s = (64 << 20) / (m * k);
+    return s < 1 ? 1 : (int)s;
+}
+
+htl_status rows_dx_parts(const void* dy, int64_t ld_dy, const void* w, int64_t ldw, htl_dtype dtype, int64_t m, int n, int k,
+                         const int32_t* order, const int32_t* offsets, int n_groups, float* parts, int splits, bool add,
+                         hipStream_t stream) {
+    if (m == 0) return HTL_OK;
+    const int es = elem(dtype);
+    const bool fast = ld_dy * es % 16 == 0 && aligned(dy, 16) && (int64_t)n * es % 16 == 0 && (int64_t)k * es % 16 == 0 &&
+                      ldw * es % 16 == 0 && aligned(w, 16) && m * ld_dy * es <= kBufferBytes && n * ldw * es <= kBufferBytes;
+    ProdArgs p = {dy, w, nullptr, order, offsets, m, ld_dy, k, ldw, n, k, n_groups, 128, parts, 1, 0};
+    p.splits = splits;
+    const int64_t tiles = (m / 128 + n_groups + 1) * ceil_div(k, 128) * splits;
+    const dim3 grid(grid_for(align_up((size_t)tiles, kXcds), 1));
+    auto go = [&](auto t, auto async, auto adds) {
+        hipLaunchKernelGGL((k_dx_parts<decltype(t)::value, Mid, decltype(async)::value, decltype(adds)::value>), grid,
+                           dim3(Mid::kThreads), 0, stream, p);
+    };
+    auto with = [&](auto t) {
+        using Yes = std::true_type;
+        using No = std::false_type;
+        if (fast && add) go(t, Yes(), Yes());
+        else if (fast) go(t, Yes(), No());
+        else if (add) go(t, No(), Yes());
+        else go(t, No(), No());
+    };
+    if (dtype == HTL_F32) with(std::integral_constant<int, kSrcF32>());
+    else with(std::integral_constant<int, kSrcBf16>());
     return check_launch("input gradients");
 }
 
@@ -238,9 +278,9 @@ htl_status sums_dw(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, ht
                       (int64_t)n * es % 16 == 0 && (int64_t)k * es % 16 == 0 && m * ld_dy * es <= kBufferBytes &&
                       m * ldx * es <= kBufferBytes;
     if (dw_dtype == HTL_BF16) {              // of bf16 operands
-        if (fast && n >= 256 && k >= 256) launch<kSrcBf16, kDw, Big, true, false, true>(p, chunks, stream);
-        else if (fast) launch<kSrcBf16, kDw, Mid, true, false, true>(p, chunks, stream);
-        else launch<kSrcBf16, kDw, Mid, false, false, true>(p, chunks, stream);
+        if (fast && n >= 256 && k >= 256) launch<kSrcBf16, kDw, Big, true, true>(p, chunks, stream);
+        else if (fast) launch<kSrcBf16, kDw, Mid, true, true>(p, chunks, stream);
+        else launch<kSrcBf16, kDw, Mid, false, true>(p, chunks, stream);
     } else if (dtype == HTL_BF16) {
         if (fast && n >= 256 && k >= 256) launch<kSrcBf16, kDw, Big, true>(p, chunks, stream);
         else if (fast) launch<kSrcBf16, kDw, Mid, true>(p, chunks, stream);
@@ -305,7 +345,7 @@ extern "C" htl_status grouped_mm_backward(const void* dy, int64_t ld_dy, const v
     HTL_REQUIRE(!dw || (ws && aligned(ws, 256) && ws_bytes >= grouped_mm_backward_workspace_bytes(m, n_groups, n, k)),
                 "grouped_mm_backward: workspace too small or misaligned");
     if (dx && m > 0) {
-        const htl_status st = rows_dx(dy, ld_dy, w, k, dtype, m, n, k, order, offsets, n_groups, dx, dx_dtype, false, stream);
+        const htl_status st = rows_dx(dy, ld_dy, w, k, dtype, m, n, k, order, offsets, n_groups, dx, dx_dtype, stream);
         if (st != HTL_OK) return st;
     }
     if (!dw) return HTL_OK;

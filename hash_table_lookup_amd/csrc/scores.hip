@@ -137,26 +137,53 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_scores(ProdArgs p, End end) 
 
 template <class End>
 __global__ __launch_bounds__(256, 1) void k_scores_wide(ProdArgs p, End end) {
-    wide_tiles<kFwd>(p, 1, end);
+    wide_tiles<kFwd>(p, end);
 }
 
-// lse of 16 rows from their partial sums, and the losses: 16 threads a row.
+// A row's partial sums joined by the workgroup, the same in every thread.
+__device__ __forceinline__ Best row_best(const Best* partial, int blocks, int64_t m, int64_t row, Best* s) {
+    Best b = {-INFINITY, 0.0f};
+#pragma unroll 4
+    for (int i = threadIdx.x; i < blocks; i += 256) b = join(b, partial[(int64_t)i * m + row]);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) b = join(b, {__shfl_xor(b.top, off), __shfl_xor(b.sum, off)});
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = b;
+    __syncthreads();
+    return join(join(s[0], s[1]), join(s[2], s[3]));
+}
+__device__ __forceinline__ float lse_of(const Best& b) { return (b.top + __builtin_amdgcn_logf(b.sum)) * kLn2; }
+
+// lse of rows from their partial sums, and the losses: a row a workgroup, or
+// (many rows: whole lines of partial sums are read) 16.
 __global__ __launch_bounds__(256) void k_softmax_finish(const Best* __restrict__ partial, int blocks, int64_t m,
                                                         Items targets, const float* __restrict__ target_score,
                                                         float* __restrict__ loss, float* __restrict__ lse) {
+    __shared__ Best s[4];
+    const int64_t row = blockIdx.x;
+    const bool on = targets.at(row) >= 0;                // (the same for the workgroup)
+    const float l = on ? lse_of(row_best(partial, blocks, m, row, s)) : 0.0f;
+    if (threadIdx.x) return;
+    lse[row] = l;
+    loss[row] = on ? l - target_score[row] : 0.0f;
+}
+__global__ __launch_bounds__(256) void k_softmax_finish16(const Best* __restrict__ partial, int blocks, int64_t m,
+                                                          Items targets, const float* __restrict__ target_score,
+                                                          float* __restrict__ loss, float* __restrict__ lse) {
     __shared__ Best s[16][16];
     const int r = threadIdx.x & 15, part = threadIdx.x >> 4;
     const int64_t row = blockIdx.x * 16ll + r;
     const bool on = row < m && targets.at(row) >= 0;
     Best b = {-INFINITY, 0.0f};
-    if (on)
+    if (on) {
+#pragma unroll 4
         for (int i = part; i < blocks; i += 16) b = join(b, partial[(int64_t)i * m + row]);
+    }
     s[part][r] = b;
     __syncthreads();
     if (part || row >= m) return;
     for (int i = 1; i < 16; ++i) b = join(b, s[i][r]);
-    const float l = (b.top + __builtin_amdgcn_logf(b.sum)) * kLn2;
-    lse[row] = on ? l : 0.0f;
+    const float l = on ? lse_of(b) : 0.0f;
+    lse[row] = l;
     loss[row] = on ? l - target_score[row] : 0.0f;
 }
 
@@ -222,34 +249,30 @@ __device__ __forceinline__ bool teacher_sum(const Teacher& t, int64_t row, float
     return true;
 }
 
-// lse and loss against a teacher: a wave a row.
+// lse and loss against a teacher: a row a workgroup.
 __global__ __launch_bounds__(256) void k_distill_finish(const Best* __restrict__ partial, int blocks, int64_t m, Teacher t,
                                                         const float* __restrict__ scores, float* __restrict__ loss,
                                                         float* __restrict__ lse) {
-    const int64_t row = blockIdx.x * 4ll + (threadIdx.x >> 6);
-    if (row >= m) return;
+    __shared__ Best s[4];
+    const int64_t row = blockIdx.x;
     float all;
-    if (!teacher_sum(t, row, all)) {
-        if (__lane_id() == 0) loss[row] = lse[row] = 0.0f;
+    if (!teacher_sum(t, row, all)) {                     // (every wave finds the same)
+        if (threadIdx.x == 0) loss[row] = lse[row] = 0.0f;
         return;
     }
-    Best b = {-INFINITY, 0.0f};
-    for (int i = __lane_id(); i < blocks; i += 64) b = join(b, partial[(int64_t)i * m + row]);
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) b = join(b, {__shfl_xor(b.top, off), __shfl_xor(b.sum, off)});
-    const float l = (b.top + __builtin_amdgcn_logf(b.sum)) * kLn2;
+    const float l = lse_of(row_best(partial, blocks, m, row, s));
+    if (threadIdx.x >= 64) return;
     float sum = 0.0f;
-    for (int j = __lane_id(); j < t.top; j += 64) {
+    for (int j = threadIdx.x; j < t.top; j += 64) {
         const float logp = t.logit(row, j) - all;
-        if (logp > -INFINITY || logp != logp)                // an entry of share 0 adds nothing
+        if (logp > -INFINITY || logp != logp)            // an entry of share 0 adds nothing
             sum += __builtin_amdgcn_exp2f(logp) * (logp * kLn2 + (l - scores[row * t.top + j]));
     }
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
-    if (__lane_id() == 0) {
-        loss[row] = sum;
-        lse[row] = l;
-    }
+    if (threadIdx.x) return;
+    loss[row] = sum;
+    lse[row] = l;
 }
 
 // Which rows take part (0, or -1: none), and, of a teacher's entries, d: an
@@ -405,7 +428,7 @@ struct ForwardSpace {
         offsets = c.take<int32_t>(2);
         group_bytes = wide ? row_groups_workspace_bytes(m, 1) : 0;
         groups = c.take<char>(group_bytes);
-        x = c.take<char>(wide ? m * packed_ld(k) * 2 : 0);
+        x = c.take<char>(wide ? m * spread_ld(k) * 2 : 0);
         w = c.take<char>(wide ? pack_cols(vocab) * packed_ld(k) * 2 : 0);
         bytes = c.at;
     }
@@ -432,7 +455,7 @@ struct BackwardSpace {
     BackwardSpace(void* ws, int64_t m, int vocab, int k, int top, htl_dtype dtype) {
         wide = wide_of(m, vocab, dtype);
         step = piece_cols(m, vocab, dtype);
-        splits = wide ? wide_dx_splits(m, step, k) : 1;
+        splits = wide ? wide_dx_splits(m, step, k) : rows_dx_splits(m, step, k);
         Carve c = {(char*)ws, 0};
         ids = c.take<int32_t>(m);
         order = c.take<int32_t>(m);
@@ -441,12 +464,12 @@ struct BackwardSpace {
         groups = c.take<char>(group_bytes);
         entries = c.take<float>(m * top);
         parts = c.take<float>(step < vocab || splits > 1 ? splits * m * k : 0);
-        d = c.take<char>(m * packed_ld(step) * elem(dtype));
+        d = c.take<char>(m * spread_ld(step) * elem(dtype));
         const int last = vocab % step ? vocab % step : step;
         const size_t a = wide ? wide_dw_bytes(m, 1, step, k) : sums_dw_bytes(m, 1, step, k);
         const size_t b = wide ? wide_dw_bytes(m, 1, last, k) : sums_dw_bytes(m, 1, last, k);
         sums = c.take<char>(a > b ? a : b);
-        x = c.take<char>(wide ? m * packed_ld(k) * 2 : 0);
+        x = c.take<char>(wide ? m * spread_ld(k) * 2 : 0);
         w = c.take<char>(wide ? step * packed_ld(k) * 2 : 0);
         bytes = c.at;
     }
@@ -460,8 +483,8 @@ bool sizes_ok(int64_t m, int vocab, int k) {
 template <class End>
 void launch_wide(const void* x, int64_t ldx, bool packed, const void* w, int64_t ldw, int64_t m, int cols, int k,
                  const int32_t* order, const int32_t* offsets, const End& end, hipStream_t s) {
-    const ProdArgs p = {x, w, nullptr, order, offsets, m, ldx, 0, ldw, cols, k, 1, 256, nullptr, 0, 0, packed};
-    const dim3 grid(grid_for(align_up((size_t)((m / 256 + 2) * ceil_div(cols, 256)), kXcds), 1));
+    const ProdArgs p = {x, w, nullptr, order, offsets, m, ldx, 0, ldw, cols, k, 1, 256, nullptr, 0, 0, packed, true};
+    const dim3 grid(grid_for(align_up((size_t)((m / 256 + 1) * ceil_div(cols, 256)), kXcds), 1));
     hipLaunchKernelGGL(k_scores_wide<End>, grid, dim3(Wide::kThreads), 0, s, p, end);
 }
 
@@ -485,7 +508,7 @@ htl_status forward_scores(const Rows2& r, float scale, const ForwardSpace& s, co
         htl_status st = row_groups(s.ids, r.m, 1, s.order, s.offsets, s.groups, s.group_bytes, stream);
         if (st != HTL_OK) return st;
         const bool as_is = packed_as_is(r.x, r.ldx, r.k) && r.m * r.ldx * 2 <= kBufferBytes;
-        if (!as_is) st = pack_rows(r.x, r.ldx, s.order, r.m, r.m, r.k, s.x, packed_ld(r.k), stream);
+        if (!as_is) st = pack_rows(r.x, r.ldx, s.order, r.m, r.m, r.k, s.x, spread_ld(r.k), stream);
         const int most = packed_as_is(r.w, r.ldw, r.k) && kPackCols * r.ldw * 2 <= kBufferBytes ? most_cols(r) : kPackCols;
         for (int v0 = 0; v0 < r.vocab && st == HTL_OK;) {
             const int cols = r.vocab - v0 < most ? r.vocab - v0 : most;
@@ -494,7 +517,7 @@ htl_status forward_scores(const Rows2& r, float scale, const ForwardSpace& s, co
             st = piece_of(r, v0, cols, s.w, w, ldw, stream);
             if (st != HTL_OK) return st;
             const ScoreEnd<Wide> end = {r.m, cols, v0, v0 / W, scale, s.partial, targets, s.target_score};
-            launch_wide(as_is ? r.x : s.x, as_is ? r.ldx : packed_ld(r.k), !as_is, w, ldw, r.m, cols, r.k, s.order, s.offsets,
+            launch_wide(as_is ? r.x : s.x, as_is ? r.ldx : spread_ld(r.k), !as_is, w, ldw, r.m, cols, r.k, s.order, s.offsets,
                         end, stream);
             st = check_launch("scores");
             v0 += cols;
@@ -518,16 +541,15 @@ htl_status forward_scores(const Rows2& r, float scale, const ForwardSpace& s, co
 htl_status backward_pieces(const Rows2& r, float scale, const BackwardSpace& s, const Items& targets, const Items& items,
                            int top, const float* lse, const float* dloss, void* dx, htl_dtype dx_dtype, void* dw,
                            hipStream_t stream) {
-    const int64_t m = r.m, ld = packed_ld(s.step);
+    const int64_t m = r.m, ld = spread_ld(s.step);
     const int es = elem(r.dtype);
     htl_status st = row_groups(s.ids, m, 1, s.order, s.offsets, s.groups, s.group_bytes, stream);
-    if (st == HTL_OK && s.wide) st = pack_rows(r.x, r.ldx, s.order, m, m, r.k, s.x, packed_ld(r.k), stream);
+    if (st == HTL_OK && s.wide) st = pack_rows(r.x, r.ldx, s.order, m, m, r.k, s.x, spread_ld(r.k), stream);
     if (st != HTL_OK) return st;
     bool fast;
     const int tile = tile_of(r, s.step, fast);
-    // dx in parts, by position, or whole
-    float* parts = s.wide ? (s.step < r.vocab || s.splits > 1 ? s.parts : nullptr)
-                          : (s.step == r.vocab ? nullptr : dx_dtype == HTL_F32 ? (float*)dx : s.parts);
+    // dx in parts (wide tiles: by position) or whole
+    float* parts = s.step < r.vocab || s.splits > 1 ? s.parts : nullptr;
     for (int v0 = 0; v0 < r.vocab;) {
         const int cols = r.vocab - v0 < s.step ? r.vocab - v0 : s.step;
         const void* w = (const char*)r.w + (int64_t)v0 * r.ldw * es;
@@ -536,7 +558,7 @@ htl_status backward_pieces(const Rows2& r, float scale, const BackwardSpace& s, 
             st = piece_of(r, v0, cols, s.w, w, ldw, stream);
             if (st != HTL_OK) return st;
             const SlopeEnd<Wide> end = {cols, v0, ld, scale, lse, dloss, targets, s.d, false, true};
-            launch_wide(s.x, packed_ld(r.k), true, w, ldw, m, cols, r.k, s.order, s.offsets, end, stream);
+            launch_wide(s.x, spread_ld(r.k), true, w, ldw, m, cols, r.k, s.order, s.offsets, end, stream);
         } else {
             launch_scores(r, tile, fast, v0, cols, s.order, s.offsets, [&](auto shape) {
                 return SlopeEnd<decltype(shape)>{cols, v0, ld, scale, lse, dloss, targets, s.d, r.dtype == HTL_F32, false};
@@ -557,22 +579,22 @@ htl_status backward_pieces(const Rows2& r, float scale, const BackwardSpace& s, 
             if (s.wide)
                 st = wide_dx(s.d, ld, w, ldw, m, cols, r.k, s.order, s.offsets, 1, dx, dx_dtype, parts, s.splits, v0 > 0, stream);
             else
-                st = rows_dx(s.d, ld, w, ldw, r.dtype, m, cols, r.k, s.order, s.offsets, 1, parts ? parts : dx,
-                             parts ? HTL_F32 : dx_dtype, v0 > 0, stream);
+                st = parts ? rows_dx_parts(s.d, ld, w, ldw, r.dtype, m, cols, r.k, s.order, s.offsets, 1, parts, s.splits, v0 > 0, stream)
+                           : rows_dx(s.d, ld, w, ldw, r.dtype, m, cols, r.k, s.order, s.offsets, 1, dx, dx_dtype, stream);
         }
         if (st == HTL_OK && dw) {
             char* to = (char*)dw + (int64_t)v0 * r.k * es;
             if (s.wide)
-                st = wide_dw(s.d, ld, s.x, packed_ld(r.k), m, cols, r.k, s.offsets, 1, to, r.dtype, s.sums, stream);
+                st = wide_dw(s.d, ld, s.x, spread_ld(r.k), m, cols, r.k, s.offsets, 1, to, r.dtype, s.sums, stream);
             else
                 st = sums_dw(s.d, ld, r.x, r.ldx, r.dtype, m, cols, r.k, s.order, s.offsets, 1, to, r.dtype, s.sums, stream);
         }
         if (st != HTL_OK) return st;
         v0 += cols;
     }
-    if (!dx || !parts || (void*)parts == dx) return HTL_OK;
-    return s.wide ? sum_parts(parts, s.splits, m, r.k, s.order, s.offsets + 1, dx, dx_dtype, stream)
-                  : sum_parts(parts, 1, m, r.k, nullptr, nullptr, dx, dx_dtype, stream);
+    if (!dx) return HTL_OK;
+    if (parts) return sum_parts(parts, s.splits, !s.wide, m, r.k, s.order, s.offsets + 1, dx, dx_dtype, stream);
+    return s.wide ? zero_rest(dx, (int64_t)r.k * elem(dx_dtype), m, s.order, s.offsets + 1, stream) : HTL_OK;
 }
 
 }  // namespace
@@ -615,8 +637,12 @@ extern "C" htl_status softmax_loss(const void* x, int64_t ldx, const void* w, in
     if (s.wide) hipLaunchKernelGGL(k_active, dim3(grid_for(m, 256, 1 << 12)), dim3(256), 0, stream, m, t, s.ids);
     const htl_status st = forward_scores(r, 1.0f / temperature, s, t, blocks, stream);
     if (st != HTL_OK) return st;
-    hipLaunchKernelGGL(k_softmax_finish, dim3((unsigned)ceil_div(m, 16)), dim3(256), 0, stream, s.partial, blocks, m, t,
-                       s.target_score, loss, lse);
+    // 8 rows of 2,048 blocks: 34 us at 16 rows a workgroup
+    if (m < 2048)
+        hipLaunchKernelGGL(k_softmax_finish, dim3((unsigned)m), dim3(256), 0, stream, s.partial, blocks, m, t, s.target_score, loss, lse);
+    else
+        hipLaunchKernelGGL(k_softmax_finish16, dim3((unsigned)ceil_div(m, 16)), dim3(256), 0, stream, s.partial, blocks, m, t,
+                           s.target_score, loss, lse);
     return check_launch("softmax_loss");
 }
 
@@ -675,7 +701,7 @@ extern "C" htl_status distill_loss(const void* x, int64_t ldx, const void* w, in
     const dim3 grid(grid_for(m * top, 4));
     if (dtype == HTL_F32) hipLaunchKernelGGL(k_item_scores<kSrcF32>, grid, dim3(256), 0, stream, xr, wr, m, k, t.items, top, scale, scores);
     else hipLaunchKernelGGL(k_item_scores<kSrcBf16>, grid, dim3(256), 0, stream, xr, wr, m, k, t.items, top, scale, scores);
-    hipLaunchKernelGGL(k_distill_finish, dim3((unsigned)ceil_div(m, 4)), dim3(256), 0, stream, s.partial, blocks, m, t, scores,
+    hipLaunchKernelGGL(k_distill_finish, dim3((unsigned)m), dim3(256), 0, stream, s.partial, blocks, m, t, scores,
                        loss, lse);
     return check_launch("distill_loss");
 }

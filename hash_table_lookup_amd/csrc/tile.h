@@ -28,7 +28,15 @@ struct ProdArgs {
     int out_f32;
     int64_t limit;           // dw: chunks of split groups that `partial` has room for
     bool packed;             // wide.h: a's rows lie by position in the plan
+    bool no_rest;            // no tiles for the rows of no group
+    int splits;              // parts of a reduction
 };
+// The part that a split reduction's tile has: elements [first, first + len) of it, whole steps of `unit`.
+__device__ __forceinline__ void part_of(int part, int splits, int unit, int& first, int& len) {
+    const int each = ((len + splits - 1) / splits + unit - 1) / unit * unit;
+    first = part * each < len ? part * each : len;
+    len = len - first < each ? len - first : each;
+}
 
 enum { kFwd = 0, kDx = 1, kDw = 2 };
 
@@ -369,7 +377,7 @@ struct TileAt {
 constexpr int kBlock = 8, kXcds = 8;
 // 1: found; 0: nothing at this b; -1: nothing at this or any later b.
 __device__ __forceinline__ int search_tile(const int32_t* offsets, int n_groups, int64_t m, uint32_t R, int min_chunks,
-                                         int64_t cols, int64_t b, TileAt& t) {
+                                           bool no_rest, int64_t cols, int64_t b, TileAt& t) {
     const int lane = __lane_id();
     auto chunks_at = [&](int g, int64_t& beg, int64_t& end) {
         beg = end = 0;
@@ -378,7 +386,7 @@ __device__ __forceinline__ int search_tile(const int32_t* offsets, int n_groups,
             group_range(offsets, n_groups, m, g, beg, end);
             cnt = (int)(((uint32_t)(end - beg) + R - 1u) / R);
             if (g < n_groups && cnt < min_chunks) cnt = min_chunks;
-            if (g == n_groups && min_chunks) cnt = 0;        // sums leave out the rows of no group
+            if (g == n_groups && (min_chunks || no_rest)) cnt = 0;   // sums leave out the rows of no group
         }
         return cnt;
     };
@@ -440,9 +448,9 @@ __device__ __forceinline__ int search_tile(const int32_t* offsets, int n_groups,
 // The same, said to be the same in every lane: what follows from it stays in
 // scalar registers.
 __device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, int64_t m, uint32_t R, int min_chunks,
-                                         int64_t cols, int64_t b, TileAt& t) {
+                                         bool no_rest, int64_t cols, int64_t b, TileAt& t) {
     TileAt v = {};
-    const int found = search_tile(offsets, n_groups, m, R, min_chunks, cols, b, v);
+    const int found = search_tile(offsets, n_groups, m, R, min_chunks, no_rest, cols, b, v);
     t.g = __builtin_amdgcn_readfirstlane(v.g);
     t.beg = __builtin_amdgcn_readfirstlane((int)v.beg);
     t.end = __builtin_amdgcn_readfirstlane((int)v.end);
@@ -569,7 +577,8 @@ __device__ __forceinline__ void store_rows(void* out, bool f32, int64_t row, int
 // lane's own) and columns col + 16 i + l / 16 * 4; row is where row r goes (-1:
 // nowhere).  End::kPairs: the columns are pairs of two projections (AlongPairs),
 // p.n of each, v's second half those of the first half's columns.
-template <int T, int MODE, class C, bool ASYNC, class End>
+// PARTS (kDx): the reduction is cut into p.splits parts, a tile each, whose number is t.slot.
+template <int T, int MODE, class C, bool ASYNC, bool PARTS = false, class End>
 __device__ __forceinline__ void product_tiles(const ProdArgs& p, const End& end) {
     // Slots of the ring as variables of their own: the compiler then makes a
     // read of one wait for that slot's loads alone, not for every load into
@@ -589,17 +598,17 @@ __device__ __forceinline__ void product_tiles(const ProdArgs& p, const End& end)
     constexpr int BC = kPairs ? C::BC / 2 : C::BC;       // outputs of a tile beside each other
     const int cols = MODE == kFwd ? p.n : p.k;
     const int col_tiles = (cols + BC - 1) / BC;
-    const int row_tiles = MODE == kDw ? (p.n + C::BR - 1) / C::BR : 1;
+    const int row_tiles = MODE == kDw ? (p.n + C::BR - 1) / C::BR : (PARTS ? p.splits : 1);
     for (int64_t b = blockIdx.x;; b += gridDim.x) {
         TileAt t;
-        const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, MODE == kDw ? 1 : 0,
+        const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, MODE == kDw ? 1 : 0, PARTS,
                                     (int64_t)col_tiles * row_tiles, b, t);
         if (found < 0) return;
         if (!found) continue;
         if (MODE == kDw && t.count > 1 && t.slot >= p.limit) continue;   // offsets that overlap
         const bool grouped = t.g < p.n_groups;
         const int r0 = MODE == kDw ? t.col % row_tiles * C::BR : 0;
-        const int c0 = (MODE == kDw ? t.col / row_tiles : t.col) * BC;
+        const int c0 = (MODE == kDw ? t.col / row_tiles : PARTS ? t.col % col_tiles : t.col) * BC;
         __syncthreads();                     // the tile before is read and stored
         if (MODE != kDw) {
             for (int i = threadIdx.x; i < C::BR; i += NT) {
@@ -614,7 +623,14 @@ __device__ __forceinline__ void product_tiles(const ProdArgs& p, const End& end)
         for (int i = 0; i < C::TC; ++i)
 #pragma unroll
             for (int j = 0; j < C::TR; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const int64_t len = !grouped ? 0 : (MODE == kFwd ? p.k : (MODE == kDx ? p.n : t.end - t.beg));
+        int64_t len = !grouped ? 0 : (MODE == kFwd ? p.k : (MODE == kDx ? p.n : t.end - t.beg));
+        int first = 0;                       // (PARTS) of the reduction
+        if constexpr (PARTS) {
+            int part = (int)len;
+            t.slot = t.col / col_tiles;
+            part_of((int)t.slot, p.splits, kStep, first, part);
+            len = part;
+        }
         const int64_t wg = grouped ? (int64_t)t.g * (kPairs ? 2 : 1) * p.n * p.ldw : 0;
         // rows of this wave that exist
         const bool busy = (MODE == kDw ? r0 + wr < p.n : t.beg + wr < t.end) && c0 + (kPairs ? wc / 2 : wc) < cols;
@@ -639,14 +655,14 @@ __device__ __forceinline__ void product_tiles(const ProdArgs& p, const End& end)
                 __syncthreads();
             } else {
                 // a row that is not there is read as the first that may be: its products are not stored
-                ro.begin(p.a, p.lda * ES, p.m, [&](int r) { return s_row[r] < 0 ? 0 : s_row[r]; });
+                ro.begin((const char*)p.a + first * ES, p.lda * ES, p.m, [&](int r) { return s_row[r] < 0 ? 0 : s_row[r]; });
                 ro_at = lane_along(wr);
                 if constexpr (kPairs)
                     co.begin((const char*)p.b + wg * ES, p.ldw * ES, p.n, c0);
                 else if constexpr (MODE == kFwd)
                     co.begin((const char*)p.b + (wg + (int64_t)c0 * p.ldw) * ES, p.ldw * ES, p.n - c0);
                 else
-                    co.begin((const char*)p.b + wg * ES, p.ldw * ES, p.n, c0, p.k);
+                    co.begin((const char*)p.b + (wg + first * p.ldw) * ES, p.ldw * ES, PARTS ? (int)len : p.n, c0, p.k);
             }
             if constexpr (MODE == kFwd) co_at = lane_along(C::BR + wc);
             else co_at = kCols + lane_across<T, C::BC>(wc);
@@ -787,10 +803,19 @@ template <int F> __device__ __forceinline__ void add_rows(float* out, int64_t ro
     }
 }
 
-// The products themselves: rows of p.out, or added to them (ADD: fp32 rows);
-// sums over rows (kDw) go to p.out where they are whole (in bf16 with BF16), else
-// to p.partial.
-template <int MODE, class C, bool ADD, bool BF16> struct StoreRows {
+// Parts of input gradients (splits of a reduction): p.partial is [splits][m][k].
+template <class C, bool ADD> struct StoreParts {
+    static constexpr bool kPairs = false;
+    const ProdArgs& p;
+    __device__ __forceinline__ void operator()(const TileAt& t, bool, int, int64_t row, int col, f32x4 (&v)[C::TC]) const {
+        float* part = p.partial + t.slot * p.m * p.k;
+        if (ADD) add_rows<C::TC>(part, row, p.k, col, p.k, v);
+        else store_rows<C::TC>(part, true, row, p.k, col, p.k, v);
+    }
+};
+// The products themselves: rows of p.out; sums over rows (kDw) go to p.out where
+// they are whole (in bf16 with BF16), else to p.partial.
+template <int MODE, class C, bool BF16> struct StoreRows {
     static constexpr bool kPairs = false;
     const ProdArgs& p;
     __device__ __forceinline__ void operator()(const TileAt& t, bool grouped, int, int64_t row, int col,
@@ -799,11 +824,7 @@ template <int MODE, class C, bool ADD, bool BF16> struct StoreRows {
         const int64_t wg = grouped ? (int64_t)t.g * p.n * p.k : 0;
         const bool whole = MODE != kDw || t.count == 1;
         void* to = MODE != kDw ? p.out : (whole ? (char*)p.out + wg * (BF16 ? 2 : 4) : (char*)(p.partial + t.slot * p.n * p.k));
-        if (!ADD) {
-            store_rows<C::TC>(to, MODE != kDw ? (bool)p.out_f32 : !BF16 || !whole, row, cols, col, cols, v);
-        } else if (grouped) {
-            add_rows<C::TC>((float*)p.out, row, cols, col, cols, v);
-        }
+        store_rows<C::TC>(to, MODE != kDw ? (bool)p.out_f32 : !BF16 || !whole, row, cols, col, cols, v);
     }
 };
 
@@ -816,13 +837,18 @@ inline bool known(htl_dtype t) { return t == HTL_F32 || t == HTL_BF16; }
 
 }  // namespace
 
-// Products of product.hip for operators that end in them.  dx[i] = w_g^T dy[i]
-// (add: added to what dx, then fp32, holds; rows of no group are left alone),
-// and dw[g] = sum of dy[i] x[i]^T in dw_dtype, with sums_dw_bytes of workspace.
+// Products of product.hip for operators that end in them.  dx[i] = w_g^T dy[i],
+// whole, or in parts of the reduction: parts is float[splits][m][k], by row, of
+// which rows of a group are written, or (add) added to, for sum_parts to join.
+// And dw[g] = sum of dy[i] x[i]^T in dw_dtype, with sums_dw_bytes of workspace.
 // Arguments are the caller's to check.
 htl_status rows_dx(const void* dy, int64_t ld_dy, const void* w, int64_t ldw, htl_dtype dtype, int64_t m, int n, int k,
-                   const int32_t* order, const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype, bool add,
+                   const int32_t* order, const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype,
                    hipStream_t stream);
+int rows_dx_splits(int64_t m, int n, int k);
+htl_status rows_dx_parts(const void* dy, int64_t ld_dy, const void* w, int64_t ldw, htl_dtype dtype, int64_t m, int n, int k,
+                         const int32_t* order, const int32_t* offsets, int n_groups, float* parts, int splits, bool add,
+                         hipStream_t stream);
 size_t sums_dw_bytes(int64_t m, int n_groups, int n, int k);
 htl_status sums_dw(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, htl_dtype dtype, int64_t m, int n, int k,
                    const int32_t* order, const int32_t* offsets, int n_groups, void* dw, htl_dtype dw_dtype, void* ws,

@@ -96,10 +96,9 @@ struct WideAcross {
     }
 };
 
-// splits (kDx): the reduction is cut into so many parts, a tile each; end's
-// t.slot is the part.
-template <int MODE, class End>
-__device__ __forceinline__ void wide_tiles(const ProdArgs& p, int splits, const End& end) {
+// kDx: the reduction is cut into p.splits parts, a tile each, whose number is
+// t.slot.
+template <int MODE, class End> __device__ __forceinline__ void wide_tiles(const ProdArgs& p, const End& end) {
     using C = Wide;
     constexpr bool kPairs = End::kPairs;
     constexpr int BC = kPairs ? C::BC / 2 : C::BC;
@@ -112,16 +111,18 @@ __device__ __forceinline__ void wide_tiles(const ProdArgs& p, int splits, const 
     const int wr = wv / C::WC * 128, wc = wv % C::WC * 128;
     const int cols = MODE == kFwd ? p.n : p.k;
     const int col_tiles = (cols + BC - 1) / BC;
-    const int row_tiles = MODE == kDw ? (p.n + C::BR - 1) / C::BR : splits;
+    const int row_tiles = MODE == kDw ? (p.n + C::BR - 1) / C::BR : MODE == kDx ? p.splits : 1;
     for (int64_t b = blockIdx.x;; b += gridDim.x) {
         TileAt t;
-        const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, MODE == kDw ? 1 : 0, (int64_t)col_tiles * row_tiles, b, t);
+        const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, MODE == kDw ? 1 : 0, p.no_rest,
+                                    (int64_t)col_tiles * row_tiles, b, t);
         if (found < 0) return;
         if (!found) continue;
         if (MODE == kDw && t.count > 1 && t.slot >= p.limit) continue;   // offsets that overlap
         const bool grouped = t.g < p.n_groups;
-        const int part = t.col % row_tiles, r0 = MODE == kDw ? part * C::BR : 0, c0 = t.col / row_tiles * BC;
-        if (MODE == kDx) t.slot = part;
+        const int r0 = MODE == kDw ? t.col % row_tiles * C::BR : 0;
+        const int c0 = (MODE == kDw ? t.col / row_tiles : t.col % col_tiles) * BC;
+        if (MODE == kDx) t.slot = t.col / col_tiles;     // a part's tiles lie together
         if (MODE != kDw) {
             __syncthreads();                             // the rows before are stored
             const int64_t pos = t.beg + threadIdx.x;
@@ -136,11 +137,7 @@ __device__ __forceinline__ void wide_tiles(const ProdArgs& p, int splits, const 
             for (int j = 0; j < C::TR; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         const int64_t wg = grouped ? (int64_t)t.g * (kPairs ? 2 : 1) * p.n * p.ldw : 0;
         int first = 0, len = !grouped ? 0 : (MODE == kFwd ? p.k : (MODE == kDx ? p.n : (int)(t.end - t.beg)));
-        if (MODE == kDx && splits > 1) {                 // whole stages a part
-            const int each = ((len + splits - 1) / splits + kStage - 1) / kStage * kStage;
-            first = part * each < len ? part * each : len;
-            len = len - first < each ? len - first : each;
-        }
+        if (MODE == kDx) part_of((int)t.slot, p.splits, kStage, first, len);
         if (len > 0) {
             using RowOp = typename std::conditional<MODE == kDw, WideAcross, WideAlong>::type;
             using ColOp = typename std::conditional<MODE == kFwd, WideAlong, WideAcross>::type;
@@ -264,21 +261,26 @@ __device__ __forceinline__ void wide_tiles(const ProdArgs& p, int splits, const 
 htl_status pack_rows(const void* x, int64_t ldx, const int32_t* order, int64_t m, int64_t src_rows, int k, void* out,
                      int64_t ld, hipStream_t stream);
 inline __host__ __device__ int64_t packed_ld(int64_t k) { return (k + 7) / 8 * 8; }
+// The same for rows laid out here: rows whole KiB apart share L2 channels (d of 32,768
+// columns, dx's product: 874 us, with 64 elements more 808).
+inline int64_t spread_ld(int64_t k) { return packed_ld(k) + (packed_ld(k) % 512 ? 0 : 64); }
 // Zeros between the `cols` elements of each row and the next multiple of 8.
 htl_status zero_behind(void* d, int64_t m, int cols, int64_t ld, hipStream_t stream);
 // Whether rows can be an operand as they lie.
 inline bool packed_as_is(const void* p, int64_t ld, int k) { return ld % 8 == 0 && k % 8 == 0 && aligned(p, 16); }
 
-// dx[row] = w_g^T d[pos], in `splits` parts of the reduction.  With sums
-// (float[splits][m][k], by position) the parts are put there (add: added to
-// what is there) for sum_parts to join; without (splits 1) dx is written.
+// dx[row] = w_g^T d[pos] in `splits` parts of the reduction.  With parts
+// (float[splits][m][k], by position) they are put there (add: added to what is
+// there) for sum_parts to join; without (splits 1) rows of a group are written.
 int wide_dx_splits(int64_t m, int n, int k);
 htl_status wide_dx(const void* d, int64_t ldd, const void* w, int64_t ldw, int64_t m, int n, int k, const int32_t* order,
-                   const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype, float* sums, int splits, bool add,
+                   const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype, float* parts, int splits, bool add,
                    hipStream_t stream);
-// dx[order[pos]] = the sum of the parts' rows pos; zeros from position *count on (null: m).
-htl_status sum_parts(const float* sums, int splits, int64_t m, int k, const int32_t* order, const int32_t* count, void* dx,
-                     htl_dtype dx_dtype, hipStream_t stream);
+// dx[order[pos]] = the sum of the parts' rows pos or (by_row) order[pos]; zeros from position *count on (null: m).
+htl_status sum_parts(const float* parts, int splits, bool by_row, int64_t m, int k, const int32_t* order,
+                     const int32_t* count, void* dx, htl_dtype dx_dtype, hipStream_t stream);
+// Zeros for rows order[pos] of `bytes` each, from position *count on.
+htl_status zero_rest(void* out, int64_t bytes, int64_t m, const int32_t* order, const int32_t* count, hipStream_t stream);
 
 // dw_g = sum of d[pos] x[pos]^T over the group's positions.
 size_t wide_dw_bytes(int64_t m, int n_groups, int n, int k);

@@ -10,17 +10,16 @@ struct DxEnd {
     static constexpr bool kPairs = false;
     void* dx;
     bool f32;
-    float* sums;             // nullable
+    float* parts;            // nullable
     bool add;
     int64_t m;
     int k;
-    __device__ __forceinline__ void operator()(const TileAt& t, bool grouped, int r, int64_t row, int col, f32x4 (&v)[8]) const {
-        if (!sums) {
+    __device__ __forceinline__ void operator()(const TileAt& t, bool, int r, int64_t row, int col, f32x4 (&v)[8]) const {
+        if (!parts) {
             store_rows<8>(dx, f32, row, k, col, k, v);
             return;
         }
-        if (!grouped) return;                            // (sum_parts writes their zeros)
-        float* part = sums + t.slot * m * k;
+        float* part = parts + t.slot * m * k;
         const int64_t pos = row < 0 ? -1 : t.beg + r;
         if (add) add_rows<8>(part, pos, k, col, k, v);
         else store_rows<8>(part, true, pos, k, col, k, v);
@@ -41,8 +40,8 @@ struct DwEnd {
     }
 };
 
-__global__ __launch_bounds__(256, 1) void k_wide_dx(ProdArgs p, int splits, DxEnd end) { wide_tiles<kDx>(p, splits, end); }
-__global__ __launch_bounds__(256, 1) void k_wide_dw(ProdArgs p, DwEnd end) { wide_tiles<kDw>(p, 1, end); }
+__global__ __launch_bounds__(256, 1) void k_wide_dx(ProdArgs p, DxEnd end) { wide_tiles<kDx>(p, end); }
+__global__ __launch_bounds__(256, 1) void k_wide_dw(ProdArgs p, DwEnd end) { wide_tiles<kDw>(p, end); }
 
 // Eight elements a thread.
 __global__ __launch_bounds__(256) void k_pack_rows(RowsIn x, const int32_t* __restrict__ order, int64_t m, int64_t src_rows,
@@ -65,8 +64,8 @@ __global__ __launch_bounds__(256) void k_zero_behind(uint16_t* __restrict__ d, i
 
 // Four columns a thread.
 template <bool BF16>
-__global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ sums, int splits, int64_t m, int k,
-                                                   const int32_t* __restrict__ order, const int32_t* __restrict__ count,
+__global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ parts, int splits, bool by_row,
+                                                   int64_t m, int k, const int32_t* __restrict__ order, const int32_t* __restrict__ count,
                                                    void* __restrict__ dx) {
     const int64_t each = (k + 3) / 4, all = m * each, on = count ? (int64_t)*count : m;
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
@@ -77,7 +76,7 @@ __global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ sum
         const int have = k - col < 4 ? k - col : 4;
         if (pos < on) {
             for (int s = 0; s < splits; ++s) {
-                const float* at = sums + ((int64_t)s * m + pos) * k + col;
+                const float* at = parts + ((int64_t)s * m + (by_row ? row : pos)) * k + col;
                 if (have == 4) {
                     f32x4 a;
                     load_at<4>(at, a);
@@ -99,6 +98,19 @@ __global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ sum
             else
                 for (int e = 0; e < have; ++e) o[e] = v[e];
         }
+    }
+}
+
+// 16 bytes a thread, or two.
+__global__ __launch_bounds__(256) void k_zero_rest(char* __restrict__ out, int64_t bytes, int64_t m,
+                                                   const int32_t* __restrict__ order, const int32_t* __restrict__ count) {
+    const int64_t from = *count < 0 ? 0 : *count, unit = bytes % 16 || !((uintptr_t)out % 16 == 0) ? 2 : 16, each = bytes / unit;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < (m - from) * each; i += gridDim.x * 256ll) {
+        const int64_t pos = from + i / each, row = order ? (int64_t)order[pos] : pos;
+        if (row < 0 || row >= m) continue;
+        char* o = out + row * bytes + i % each * unit;
+        if (unit == 16) *(u32x4*)o = zeros4();
+        else *(uint16_t*)o = 0;
     }
 }
 
@@ -139,23 +151,30 @@ int wide_dx_splits(int64_t m, int n, int k) {
 }
 
 htl_status wide_dx(const void* d, int64_t ldd, const void* w, int64_t ldw, int64_t m, int n, int k, const int32_t* order,
-                   const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype, float* sums, int splits, bool add,
+                   const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype, float* parts, int splits, bool add,
                    hipStream_t stream) {
     if (m == 0) return HTL_OK;
-    const ProdArgs p = {d, w, nullptr, order, offsets, m, ldd, 0, ldw, n, k, n_groups, 256, nullptr, 0, 0, true};
-    const DxEnd end = {dx, dx_dtype == HTL_F32, sums, add, m, k};
-    const dim3 grid(grid_for(align_up((size_t)((m / 256 + n_groups + 1) * ceil_div(k, 256) * splits), kXcds), 1));
-    hipLaunchKernelGGL(k_wide_dx, grid, dim3(Wide::kThreads), 0, stream, p, splits, end);
+    const ProdArgs p = {d, w, nullptr, order, offsets, m, ldd, 0, ldw, n, k, n_groups, 256, nullptr, 0, 0, true, true, splits};
+    const DxEnd end = {dx, dx_dtype == HTL_F32, parts, add, m, k};
+    const dim3 grid(grid_for(align_up((size_t)((m / 256 + n_groups) * ceil_div(k, 256) * splits), kXcds), 1));
+    hipLaunchKernelGGL(k_wide_dx, grid, dim3(Wide::kThreads), 0, stream, p, end);
     return check_launch("input gradients");
 }
 
-htl_status sum_parts(const float* sums, int splits, int64_t m, int k, const int32_t* order, const int32_t* count, void* dx,
-                     htl_dtype dx_dtype, hipStream_t stream) {
+htl_status sum_parts(const float* parts, int splits, bool by_row, int64_t m, int k, const int32_t* order,
+                     const int32_t* count, void* dx, htl_dtype dx_dtype, hipStream_t stream) {
     if (m == 0) return HTL_OK;
     const dim3 grid(grid_for(m * ceil_div(k, 4), 256, 1 << 16));
-    if (dx_dtype == HTL_F32) hipLaunchKernelGGL(k_sum_parts<false>, grid, dim3(256), 0, stream, sums, splits, m, k, order, count, dx);
-    else hipLaunchKernelGGL(k_sum_parts<true>, grid, dim3(256), 0, stream, sums, splits, m, k, order, count, dx);
+    if (dx_dtype == HTL_F32) hipLaunchKernelGGL(k_sum_parts<false>, grid, dim3(256), 0, stream, parts, splits, by_row, m, k, order, count, dx);
+    else hipLaunchKernelGGL(k_sum_parts<true>, grid, dim3(256), 0, stream, parts, splits, by_row, m, k, order, count, dx);
     return check_launch("input gradients");
+}
+
+htl_status zero_rest(void* out, int64_t bytes, int64_t m, const int32_t* order, const int32_t* count, hipStream_t stream) {
+    if (m == 0) return HTL_OK;
+    hipLaunchKernelGGL(k_zero_rest, dim3(grid_for(m * ceil_div(bytes, 16), 4096, 1 << 12)), dim3(256), 0, stream, (char*)out,
+                       bytes, m, order, count);
+    return check_launch("rows of no group");
 }
 
 size_t wide_dw_bytes(int64_t m, int n_groups, int n, int k) {
