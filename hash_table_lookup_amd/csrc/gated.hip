@@ -8,6 +8,7 @@
 // Rows of no group: y = 0, dx = 0.  z and u are formed in fp32 and only what is
 // kept of them, y, and dz and du (operands of the matrix instructions that
 // follow) are rounded to the rows' type.
+#include "few.h"
 #include "wide.h"
 
 namespace htl {
@@ -132,6 +133,10 @@ __global__ __launch_bounds__(256) void k_gated_slopes(RowsIn dy, RowsIn kept, Ro
     }
 }
 
+template <int T, int KS, class C, class End> __global__ __launch_bounds__(kFewThreads) void k_gated_few(ProdArgs p, End end) {
+    few_tiles<T, KS, C>(p, end);
+}
+
 template <int T, class C, bool ASYNC>
 void launch_gated(const ProdArgs& p, int64_t chunks, const GatedEnd<C>* fwd, const GatedBackEnd<C, T>* back, hipStream_t s) {
     const dim3 grid(grid_for(align_up((size_t)(chunks * ceil_div(p.n, C::BC / 2)), kXcds), 1));
@@ -152,6 +157,33 @@ struct GatedCall {
 
 // Whether wide.h's tiles fill the device (`tiles` of them) with whole rows.
 bool many(int64_t m, int n_groups, int64_t tiles) { return tiles >= 224 && m / n_groups >= 256; }
+
+// Rows that few.h's kernel is for (all of them in one group, or few in each).
+bool few(int64_t m, int n_groups) { return m <= 32 || m / n_groups <= 8; }
+template <int T> void launch_few(const ProdArgs& p, const GatedCall& c, hipStream_t s) {
+    auto go = [&](auto shape, auto splits) {
+        using C = decltype(shape);
+        constexpr int KS = decltype(splits)::value;
+        const int64_t tiles = (p.m / C::BR + p.n_groups + 1) * ceil_div(p.n, 16 * (4 / KS));
+        const dim3 grid(grid_for(align_up((size_t)tiles, kXcds), 1));
+        if (c.dy.p) {
+            const GatedBackEnd<C, T> end = {p.n, c.act, c.dy, c.d, c.ld, c.packed};
+            hipLaunchKernelGGL((k_gated_few<T, KS, C, GatedBackEnd<C, T>>), grid, dim3(kFewThreads), 0, s, p, end);
+        } else {
+            const GatedEnd<C> end = {p.n, c.act, c.y, c.y_f32, T == kSrcF32, c.kept};
+            hipLaunchKernelGGL((k_gated_few<T, KS, C, GatedEnd<C>>), grid, dim3(kFewThreads), 0, s, p, end);
+        }
+    };
+    const int64_t groups = p.m < p.n_groups ? p.m : p.n_groups;
+    const int splits = few_splits(groups * ceil_div(p.n, 16), (int64_t)p.k * (T == kSrcF32 ? 4 : 2));
+    auto with = [&](auto shape) {
+        if (splits == 4) go(shape, std::integral_constant<int, 4>());
+        else if (splits == 2) go(shape, std::integral_constant<int, 2>());
+        else go(shape, std::integral_constant<int, 1>());
+    };
+    if (p.m <= 16 || p.m / p.n_groups <= 8) with(Few<1>());
+    else with(Few<2>());
+}
 
 // The kernel by size, as the plain products' (product.hip) at twice the columns.
 void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s) {
@@ -175,6 +207,11 @@ void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s
                 if (c.kept) zero_rest(c.kept, (int64_t)p.n * 4, p.m, p.order, p.offsets + p.n_groups, s);
             }
         }
+        return;
+    }
+    if (few(p.m, p.n_groups)) {
+        if (dtype == HTL_F32) launch_few<kSrcF32>(p, c, s);
+        else launch_few<kSrcBf16>(p, c, s);
         return;
     }
     int tile = each <= 48 || (ceil_div(p.m, 32) + p.n_groups) * ceil_div(p.n, 64) <= 512 ? 32 : 128;

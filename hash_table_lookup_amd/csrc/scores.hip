@@ -14,6 +14,7 @@
 // it; a second kernel joins these.  Backward: pieces of the vocabulary, each
 // three products: the scores again, their end writing d in the rows' type (an
 // operand of the matrix instructions that follow), then dx += d w and dw = d^T x.
+#include "few.h"
 #include "wide.h"
 
 namespace htl {
@@ -135,6 +136,9 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_scores(ProdArgs p, End end) 
     product_tiles<T, kFwd, C, ASYNC>(p, end);
 }
 
+template <int T, int KS, class C, class End> __global__ __launch_bounds__(kFewThreads) void k_scores_few(ProdArgs p, End end) {
+    few_tiles<T, KS, C>(p, end);
+}
 template <class End>
 __global__ __launch_bounds__(256, 1) void k_scores_wide(ProdArgs p, End end) {
     wide_tiles<kFwd>(p, end);
@@ -365,6 +369,20 @@ void launch_scores(const Rows2& r, int tile, bool fast, int v0, int cols, const 
                    Make make, hipStream_t s) {
     const char* w = (const char*)r.w + (int64_t)v0 * r.ldw * elem(r.dtype);
     const ProdArgs p = {r.x, w, nullptr, order, offsets, r.m, r.ldx, r.ldw, r.ldw, cols, r.k, 1, (uint32_t)tile, nullptr, 0, 0};
+    auto few = [&](auto t, auto shape) {                 // (tile: rows)
+        constexpr int T = decltype(t)::value;
+        using C = decltype(shape);
+        const auto end = make(shape);
+        auto with = [&](auto splits) {
+            constexpr int KS = decltype(splits)::value;
+            const dim3 grid(grid_for(align_up((size_t)((r.m / C::BR + 2) * ceil_div(cols, 32 * (4 / KS))), kXcds), 1));
+            hipLaunchKernelGGL((k_scores_few<T, KS, C, decltype(end)>), grid, dim3(kFewThreads), 0, s, p, end);
+        };
+        const int splits = few_splits(ceil_div(cols, 32), (int64_t)r.k * (T == kSrcF32 ? 4 : 2));
+        if (splits == 4) with(std::integral_constant<int, 4>());
+        else if (splits == 2) with(std::integral_constant<int, 2>());
+        else with(std::integral_constant<int, 1>());
+    };
     auto go = [&](auto t, auto shape, auto async) {
         using C = decltype(shape);
         const auto end = make(shape);
@@ -376,6 +394,11 @@ void launch_scores(const Rows2& r, int tile, bool fast, int v0, int cols, const 
     using B16 = std::integral_constant<int, kSrcBf16>;
     using Yes = std::true_type;
     using No = std::false_type;
+    if (r.m <= 32) {
+        if (r.dtype == HTL_BF16) r.m <= 16 ? few(B16(), Few<1>()) : few(B16(), Few<2>());
+        else r.m <= 16 ? few(F32(), Few<1>()) : few(F32(), Few<2>());
+        return;
+    }
     if (r.dtype == HTL_BF16) {
         if (tile == 128 && fast) go(B16(), Mid(), Yes());
         else if (tile == 128) go(B16(), Mid(), No());
