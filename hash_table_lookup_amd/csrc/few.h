@@ -24,7 +24,7 @@ constexpr int kFewThreads = 256;
 template <int T, int KS, class C, class End>
 __device__ __forceinline__ void few_tiles(const ProdArgs& p, const End& end) {
     constexpr bool kPairs = End::kPairs;
-    constexpr int ES = T == kSrcF32 ? 4 : 2, VE = 16 / ES, kStep = 8 * VE, kBatch = C::TR == 1 ? 4 : 2;
+    constexpr int ES = T == kSrcF32 ? 4 : 2, VE = 16 / ES, kStep = 8 * VE, kBatch = 2;
     constexpr int kWaves = kFewThreads / 64, WC = kWaves / KS, kCols = kPairs ? 16 : 32;   // columns a wave
     __shared__ f32x4 s_part[KS > 1 ? KS - 1 : 1][WC][C::TC * C::TR][64];
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
@@ -32,9 +32,18 @@ __device__ __forceinline__ void few_tiles(const ProdArgs& p, const End& end) {
     const int col_tiles = (p.n + WC * kCols - 1) / (WC * kCols);
     for (int64_t b = blockIdx.x;; b += gridDim.x) {
         TileAt t;
-        const int found = find_tile(p.offsets, p.n_groups, p.m, C::BR, 0, false, col_tiles, b, t);
-        if (found < 0) return;
-        if (!found) continue;
+        if (p.offsets) {
+            const int found = find_tile(p.offsets, p.n_groups, p.m, C::BR, 0, false, col_tiles, b, t);
+            if (found < 0) return;
+            if (!found) continue;
+        } else {                                         // one group: no search (it takes as long as a short reduction)
+            const uint32_t chunk = (uint32_t)b / (uint32_t)col_tiles;
+            t.g = 0;
+            t.col = (int)((uint32_t)b - chunk * (uint32_t)col_tiles);
+            t.beg = (int64_t)chunk * C::BR;
+            t.end = t.beg + C::BR < p.m ? t.beg + C::BR : p.m;
+            if (t.beg >= p.m) return;
+        }
         const bool grouped = t.g < p.n_groups;
         const int c0 = (t.col * WC + wc) * kCols;
         int64_t row[C::TR];
@@ -150,11 +159,21 @@ __device__ __forceinline__ void few_tiles(const ProdArgs& p, const End& end) {
     }
 }
 
-// Waves that share a reduction: four until there are workgroups enough to fill
-// the device four times over, and with less than 256 bytes a wave never.
+// Waves that share a reduction, by the waves that there would be without and
+// the length of a row (us, with 1, 2, 4: one row, 4,096 x 2 rows of 4 KiB 20.9,
+// 13.4, 9.7; 64 rows in 16 groups of as many 81, 78, 83; 16 rows, 65,536 rows of
+// 2 KiB 26, 27, 30; 8 rows, 65,536 of 256 bytes 6.1, 8.1, 12.1).  Two steps ahead
+// are as good as four (9.7, 78, 28, 7.5): more waves fit.
 inline int few_splits(int64_t waves, int64_t row_bytes) {
-    return waves >= 4096 || row_bytes < 512 ? 1 : row_bytes < 1024 || waves >= 2048 ? 2 : 4;
+    if (row_bytes < 1024) return 1;
+    return waves >= 1024 ? 2 : 4;
 }
+template <class F> void with_splits(int splits, F&& f) {
+    if (splits == 4) f(std::integral_constant<int, 4>());
+    else if (splits == 2) f(std::integral_constant<int, 2>());
+    else f(std::integral_constant<int, 1>());
+}
+template <int KS> constexpr int few_waves = 4 / KS;   // of a workgroup beside each other
 
 }  // namespace
 }  // namespace htl

@@ -164,7 +164,7 @@ template <int T> void launch_few(const ProdArgs& p, const GatedCall& c, hipStrea
     auto go = [&](auto shape, auto splits) {
         using C = decltype(shape);
         constexpr int KS = decltype(splits)::value;
-        const int64_t tiles = (p.m / C::BR + p.n_groups + 1) * ceil_div(p.n, 16 * (4 / KS));
+        const int64_t tiles = (p.m / C::BR + p.n_groups + 1) * ceil_div(p.n, 16 * few_waves<KS>);
         const dim3 grid(grid_for(align_up((size_t)tiles, kXcds), 1));
         if (c.dy.p) {
             const GatedBackEnd<C, T> end = {p.n, c.act, c.dy, c.d, c.ld, c.packed};
@@ -177,9 +177,7 @@ template <int T> void launch_few(const ProdArgs& p, const GatedCall& c, hipStrea
     const int64_t groups = p.m < p.n_groups ? p.m : p.n_groups;
     const int splits = few_splits(groups * ceil_div(p.n, 16), (int64_t)p.k * (T == kSrcF32 ? 4 : 2));
     auto with = [&](auto shape) {
-        if (splits == 4) go(shape, std::integral_constant<int, 4>());
-        else if (splits == 2) go(shape, std::integral_constant<int, 2>());
-        else go(shape, std::integral_constant<int, 1>());
+        with_splits(splits, [&](auto ks) { go(shape, ks); });
     };
     if (p.m <= 16 || p.m / p.n_groups <= 8) with(Few<1>());
     else with(Few<2>());

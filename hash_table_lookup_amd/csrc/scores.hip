@@ -191,33 +191,28 @@ __global__ __launch_bounds__(256) void k_softmax_finish16(const Best* __restrict
     loss[row] = on ? l - target_score[row] : 0.0f;
 }
 
-// A wave's dot product of two rows, the same in every lane.
-template <int T> __device__ __forceinline__ float row_dot(const RowsIn& a, int64_t i, const RowsIn& b, int64_t j, int k) {
-    float s = 0.0f;
+// A wave's dot products of row i with two rows, the same in every lane.
+template <int T>
+__device__ __forceinline__ void row_dots(const RowsIn& a, int64_t i, const RowsIn& b, const int64_t (&j)[2], int k, float (&s)[2]) {
+    s[0] = s[1] = 0.0f;
     for (int c = __lane_id() * 8; c < k; c += 512) {
-        Raw8<T> ra, rb;
+        Raw8<T> ra, rb[2];
         float va[8], vb[8];
         load8(a, i, c, k, ra);
-        load8(b, j, c, k, rb);
+        load8(b, j[0], c, k, rb[0]);
+        load8(b, j[1], c, k, rb[1]);
         unpack8(a, ra, va);
-        unpack8(b, rb, vb);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = __builtin_fmaf(va[e], vb[e], s);
+        for (int h = 0; h < 2; ++h) {
+            unpack8(b, rb[h], vb);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[h] = __builtin_fmaf(va[e], vb[e], s[h]);
+        }
     }
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) s += __shfl_xor(s, off);
-    return s;
-}
-
-// Scores of a teacher's items: a wave an entry.
-template <int T>
-__global__ __launch_bounds__(256) void k_item_scores(RowsIn x, RowsIn w, int64_t m, int k, Items items, int top,
-                                                     float scale, float* __restrict__ scores) {
-    const int64_t all = m * top;
-    for (int64_t i = blockIdx.x * 4ll + (threadIdx.x >> 6); i < all; i += gridDim.x * 4ll) {
-        const int v = items.at(i);
-        const float s = v >= 0 ? row_dot<T>(x, i / top, w, v, k) * scale : 0.0f;
-        if (__lane_id() == 0) scores[i] = s;
+    for (int off = 1; off < 64; off <<= 1) {
+        s[0] += __shfl_xor(s[0], off);
+        s[1] += __shfl_xor(s[1], off);
     }
 }
 
@@ -253,14 +248,31 @@ __device__ __forceinline__ bool teacher_sum(const Teacher& t, int64_t row, float
     return true;
 }
 
-// lse and loss against a teacher: a row a workgroup.
-__global__ __launch_bounds__(256) void k_distill_finish(const Best* __restrict__ partial, int blocks, int64_t m, Teacher t,
-                                                        const float* __restrict__ scores, float* __restrict__ loss,
-                                                        float* __restrict__ lse) {
+// The scores of a teacher's items, lse and the loss: a row a workgroup.
+template <int T>
+__global__ __launch_bounds__(256) void k_distill_finish(RowsIn x, RowsIn w, int k, const Best* __restrict__ partial,
+                                                        int blocks, int64_t m, Teacher t, float* __restrict__ scores,
+                                                        float* __restrict__ loss, float* __restrict__ lse) {
     __shared__ Best s[4];
+    __shared__ float s_score[HTL_MAX_TOP];
     const int64_t row = blockIdx.x;
     float all;
-    if (!teacher_sum(t, row, all)) {                     // (every wave finds the same)
+    const bool on = teacher_sum(t, row, all);            // (every wave finds the same)
+    for (int j = (threadIdx.x >> 6) * 2; j < t.top; j += 8) {
+        const int v[2] = {t.items.at(row * t.top + j), j + 1 < t.top ? t.items.at(row * t.top + j + 1) : -1};
+        float d[2] = {0.0f, 0.0f};
+        if (on && (v[0] >= 0 || v[1] >= 0)) {
+            const int64_t at[2] = {v[0] < 0 ? v[1] : v[0], v[1] < 0 ? v[0] : v[1]};
+            row_dots<T>(x, row, w, at, k, d);
+        }
+        if (__lane_id() < 2 && j + __lane_id() < t.top) {
+            const float d_ = __lane_id() ? d[1] : d[0];
+            const float score = (__lane_id() ? v[1] : v[0]) < 0 ? 0.0f : d_ * t.scale;
+            scores[row * t.top + j + __lane_id()] = score;
+            s_score[j + __lane_id()] = score;
+        }
+    }
+    if (!on) {
         if (threadIdx.x == 0) loss[row] = lse[row] = 0.0f;
         return;
     }
@@ -270,7 +282,7 @@ __global__ __launch_bounds__(256) void k_distill_finish(const Best* __restrict__
     for (int j = threadIdx.x; j < t.top; j += 64) {
         const float logp = t.logit(row, j) - all;
         if (logp > -INFINITY || logp != logp)            // an entry of share 0 adds nothing
-            sum += __builtin_amdgcn_exp2f(logp) * (logp * kLn2 + (l - scores[row * t.top + j]));
+            sum += __builtin_amdgcn_exp2f(logp) * (logp * kLn2 + (l - s_score[j]));
     }
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
@@ -373,15 +385,11 @@ void launch_scores(const Rows2& r, int tile, bool fast, int v0, int cols, const 
         constexpr int T = decltype(t)::value;
         using C = decltype(shape);
         const auto end = make(shape);
-        auto with = [&](auto splits) {
+        with_splits(few_splits(ceil_div(cols, 32), (int64_t)r.k * (T == kSrcF32 ? 4 : 2)), [&](auto splits) {
             constexpr int KS = decltype(splits)::value;
-            const dim3 grid(grid_for(align_up((size_t)((r.m / C::BR + 2) * ceil_div(cols, 32 * (4 / KS))), kXcds), 1));
+            const dim3 grid(grid_for(align_up((size_t)((r.m / C::BR + 2) * ceil_div(cols, 32 * few_waves<KS>)), kXcds), 1));
             hipLaunchKernelGGL((k_scores_few<T, KS, C, decltype(end)>), grid, dim3(kFewThreads), 0, s, p, end);
-        };
-        const int splits = few_splits(ceil_div(cols, 32), (int64_t)r.k * (T == kSrcF32 ? 4 : 2));
-        if (splits == 4) with(std::integral_constant<int, 4>());
-        else if (splits == 2) with(std::integral_constant<int, 2>());
-        else with(std::integral_constant<int, 1>());
+        });
     };
     auto go = [&](auto t, auto shape, auto async) {
         using C = decltype(shape);
@@ -721,11 +729,11 @@ extern "C" htl_status distill_loss(const void* x, int64_t ldx, const void* w, in
     const htl_status st = forward_scores(r, scale, s, Items{nullptr, false, vocab}, blocks, stream);
     if (st != HTL_OK) return st;
     const RowsIn xr = {x, nullptr, ldx, 0}, wr = {w, nullptr, ldw, 0};
-    const dim3 grid(grid_for(m * top, 4));
-    if (dtype == HTL_F32) hipLaunchKernelGGL(k_item_scores<kSrcF32>, grid, dim3(256), 0, stream, xr, wr, m, k, t.items, top, scale, scores);
-    else hipLaunchKernelGGL(k_item_scores<kSrcBf16>, grid, dim3(256), 0, stream, xr, wr, m, k, t.items, top, scale, scores);
-    hipLaunchKernelGGL(k_distill_finish, dim3((unsigned)m), dim3(256), 0, stream, s.partial, blocks, m, t, scores,
-                       loss, lse);
+    const dim3 grid((unsigned)m);
+    if (dtype == HTL_F32)
+        hipLaunchKernelGGL(k_distill_finish<kSrcF32>, grid, dim3(256), 0, stream, xr, wr, k, s.partial, blocks, m, t, scores, loss, lse);
+    else
+        hipLaunchKernelGGL(k_distill_finish<kSrcBf16>, grid, dim3(256), 0, stream, xr, wr, k, s.partial, blocks, m, t, scores, loss, lse);
     return check_launch("distill_loss");
 }
 

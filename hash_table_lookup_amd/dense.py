@@ -13,7 +13,7 @@ from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 
-from ._binding import _TORCH_DTYPE, _check, _dev, _dtype_code, _ptr, _stream, _workspace, lib
+from ._binding import _TORCH_DTYPE, _check, _dev, _device, _dtype_code, _ptr, _stream, _workspace, lib
 
 _FMT = {"i8": 0, "e4m3": 1}
 _KIND = {"rms": 0, "layer": 1}
@@ -298,9 +298,9 @@ def norm_gate_backward(dout: torch.Tensor, kept_z: Union[torch.Tensor, Rows8], k
 
 def _here(*tensors: Optional[torch.Tensor]) -> None:
     """Refuses tensors that are not on the current device, whose stream the call goes to."""
-    here = torch.cuda.current_device()
+    here = _device()
     for t in tensors:
-        if t is not None and t.device.index != here:
+        if t is not None and t.get_device() != here:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
 
 

@@ -66,7 +66,7 @@ def softmax_loss(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, temper
     m, k = x.shape
     targets, bits = _indices(targets, (m,), "targets")
     _here(x, w, targets)
-    loss, lse = torch.empty((2, m), dtype=torch.float32, device=x.device)
+    loss, lse = (torch.empty(m, dtype=torch.float32, device=x.device) for _ in range(2))
     nb = lib().softmax_loss_workspace_bytes(m, w.shape[0], k, _dtype_code(x.dtype))
     ws = _scratch("softmax_loss", nb, x.device)
     _check(lib().softmax_loss(_ptr(x), ldx, _ptr(w), ldw, _dtype_code(x.dtype), m, w.shape[0], k, _ptr(targets), bits,
@@ -124,7 +124,7 @@ def distill_loss(x: torch.Tensor, w: torch.Tensor, top: torch.Tensor, top_logits
     m, k = x.shape
     items, bits, logits, ld, t = _lists(top, top_logits, m)
     _here(x, w, items, logits)
-    loss, lse = torch.empty((2, m), dtype=torch.float32, device=x.device)
+    loss, lse = (torch.empty(m, dtype=torch.float32, device=x.device) for _ in range(2))
     scores = torch.empty((m, t), dtype=torch.float32, device=x.device)
     nb = lib().softmax_loss_workspace_bytes(m, w.shape[0], k, _dtype_code(x.dtype))
     ws = _scratch("softmax_loss", nb, x.device)
