@@ -102,7 +102,8 @@ _SIGNATURES = {
     "grouped_mm": [_P, _I64, _P, _I32, _I64, _I32, _I32, _P, _P, _I32, _P, _I32, _P],
     "grouped_mm_backward_workspace_bytes": [_I64, _I32, _I32, _I32],
     "grouped_mm_backward": [_P, _I64, _P, _I64, _P, _I32, _I64, _I32, _I32, _P, _P, _I32, _P, _I32, _P, _P, _SZ, _P],
-    "gated_mm": [_P, _I64, _P, _I32, _I64, _I32, _I32, _P, _P, _I32, _I32, _P, _I32, _P, _P],
+    "gated_mm_workspace_bytes": [_I64, _I32, _I32, _I32, _I32],
+    "gated_mm": [_P, _I64, _P, _I32, _I64, _I32, _I32, _P, _P, _I32, _I32, _P, _I32, _P, _P, _SZ, _P],
     "gated_mm_backward_workspace_bytes": [_I64, _I32, _I32, _I32, _I32],
     "gated_mm_backward": [_P, _I64, _P, _I64, _P, _I32, _P, _I64, _I32, _I32, _P, _P, _I32, _I32, _P, _I32, _P, _P, _SZ,
                           _P],
@@ -121,7 +122,7 @@ _SIGNATURES = {
 _SIZE_FUNCS = {"lru_workspace_bytes", "dedup_workspace_bytes", "segsum_workspace_bytes",
                "segsum_adam_workspace_bytes", "emb_lookup_workspace_bytes", "row_groups_workspace_bytes",
                "norm_back_workspace_bytes", "grouped_mm_backward_workspace_bytes",
-               "gated_mm_backward_workspace_bytes", "softmax_loss_workspace_bytes",
+               "gated_mm_workspace_bytes", "gated_mm_backward_workspace_bytes", "softmax_loss_workspace_bytes",
                "softmax_loss_backward_workspace_bytes", "distill_loss_backward_workspace_bytes"}
 EXPORTED = tuple(_SIGNATURES)
 

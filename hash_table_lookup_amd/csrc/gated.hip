@@ -184,12 +184,13 @@ template <int T> void launch_few(const ProdArgs& p, const GatedCall& c, hipStrea
 }
 
 // The kernel by size, as the plain products' (product.hip) at twice the columns.
+// Few fp32 rows a tile leave the device's last round almost empty: 5,001 rows,
+// 513 -> 777 pairs, 137 us in tiles of 128 rows, 127 in tiles of 32.
 void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s) {
     const int es = elem(dtype);
-    const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && (int64_t)p.k * es % 16 == 0 && aligned(p.b, 16) &&
-                      p.m * p.lda * es <= kBufferBytes && 2 * (int64_t)p.n * p.k * es <= kBufferBytes;
+    const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && p.ldw * es % 16 == 0 && (int64_t)p.k * es % 16 == 0 &&
+                      aligned(p.b, 16) && p.m * p.lda * es <= kBufferBytes && 2 * (int64_t)p.n * p.ldw * es <= kBufferBytes;
     const int64_t each = p.m / p.n_groups;
-    // (pairs of less than 256 elements: 426,000 rows, 128 -> 256, 446 us against 300 in tiles of 128)
     if (p.packed || (p.k >= 256 && dtype == HTL_BF16 && fast && many(p.m, p.n_groups, ceil_div(p.m, 256) * ceil_div(p.n, 128)))) {
         p.rows = 256;
         p.no_rest = true;
@@ -212,7 +213,8 @@ void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s
         else launch_few<kSrcBf16>(p, c, s);
         return;
     }
-    int tile = each <= 48 || (ceil_div(p.m, 32) + p.n_groups) * ceil_div(p.n, 64) <= 512 ? 32 : 128;
+    const int64_t small = (ceil_div(p.m, 32) + p.n_groups) * ceil_div(p.n, 64);
+    const int tile = each <= 48 || small <= (dtype == HTL_F32 ? 4096 : 512) ? 32 : 128;
     p.rows = (uint32_t)tile;
     const int64_t chunks = p.m / tile + p.n_groups + 1;
     auto go = [&](auto t, auto shape, auto async) {
@@ -239,8 +241,19 @@ void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s
     }
 }
 
+// Copies of x and w whose rows whole 16-byte pieces make up, for rows that they
+// do not: tiles' loads then go straight to LDS.  With few rows a matrix is read
+// once, and they cost more than they save.
+bool copies(int64_t m, int n_groups, int k, htl_dtype dtype) {
+    return k % (dtype == HTL_F32 ? 4 : 8) && m / n_groups >= 64;
+}
+size_t x_copy_bytes(int64_t m, int k, htl_dtype dtype) { return align_up((size_t)m * spread_ld(k) * elem(dtype), 256); }
+size_t w_copy_bytes(int n_groups, int n, int k, htl_dtype dtype) {
+    return align_up((size_t)n_groups * 2 * n * packed_ld(k) * elem(dtype), 256);
+}
+
 struct BackSpace {
-    bool wide;
+    bool wide, copied;
     int64_t ld;              // of d
     int splits;
     char *d, *sums, *x, *w;
@@ -250,7 +263,8 @@ struct BackSpace {
     BackSpace(void* ws, int64_t m, int n_groups, int n, int k, htl_dtype dtype, bool tiles) {
         wide = tiles && dtype == HTL_BF16 && k >= 256 && n >= 128 && 4 * n * packed_ld(k) <= kBufferBytes &&
                many(m, n_groups, ceil_div(m, 256) * ceil_div(2 * n, 256));
-        ld = wide ? spread_ld(2 * n) : 2 * (int64_t)n;
+        copied = copies(m, n_groups, k, dtype);
+        ld = wide || copied ? spread_ld(2 * n) : 2 * (int64_t)n;
         splits = wide ? wide_dx_splits(m, 2 * n, k) : 1;
         size_t at = 0;
         auto take = [&](size_t b) {
@@ -260,8 +274,8 @@ struct BackSpace {
         };
         d = take((size_t)m * ld * elem(dtype));
         sums = take(wide ? wide_dw_bytes(m, n_groups, 2 * n, k) : sums_dw_bytes(m, n_groups, 2 * n, k));
-        x = take(wide ? (size_t)m * spread_ld(k) * 2 : 0);
-        w = take(wide && k % 8 ? (size_t)n_groups * 2 * n * packed_ld(k) * 2 : 0);
+        x = take(wide || copied ? x_copy_bytes(m, k, dtype) : 0);
+        w = take(copied ? w_copy_bytes(n_groups, n, k, dtype) : 0);
         parts = (float*)take(splits > 1 ? (size_t)splits * m * k * 4 : 0);
         bytes = at;
     }
@@ -281,9 +295,16 @@ using namespace htl;
     HTL_REQUIRE(offsets || (n_groups == 1 && !order), name ": several groups need offsets");                     \
     HTL_REQUIRE(aligned(order, 4) && aligned(offsets, 4), name ": misaligned pointer")
 
+extern "C" size_t gated_mm_workspace_bytes(int64_t m, int n_groups, int n, int k, htl_dtype dtype) {
+    if (m < 0 || m > kMaxRows || n_groups < 1 || n_groups > kMaxGroups || n < 1 || n > HTL_MAX_PRODUCT_DIM / 2 || k < 1 ||
+        k > HTL_MAX_PRODUCT_DIM || !known(dtype))
+        return 0;
+    return 256 + (copies(m, n_groups, k, dtype) ? x_copy_bytes(m, k, dtype) + w_copy_bytes(n_groups, n, k, dtype) : 0);
+}
+
 extern "C" htl_status gated_mm(const void* x, int64_t ldx, const void* w, htl_dtype dtype, int64_t m, int n, int k,
                                const int32_t* order, const int32_t* offsets, int n_groups, htl_act act, void* y,
-                               htl_dtype y_dtype, void* kept, hipStream_t stream) {
+                               htl_dtype y_dtype, void* kept, void* ws, size_t ws_bytes, hipStream_t stream) {
     clear_error();
     GATED_CHECK("gated_mm");
     HTL_REQUIRE(known(y_dtype), "gated_mm: dtype must be HTL_F32 or HTL_BF16");
@@ -293,7 +314,18 @@ extern "C" htl_status gated_mm(const void* x, int64_t ldx, const void* w, htl_dt
     HTL_REQUIRE(x && w && y, "gated_mm: null pointer");
     HTL_REQUIRE(aligned(x, es) && aligned(w, es) && aligned(y, elem(y_dtype)) && aligned(kept, es),
                 "gated_mm: misaligned pointer");
-    const ProdArgs p = {x, w, nullptr, order, offsets, m, ldx, k, k, n, k, n_groups, 0, nullptr, 0, 0};
+    HTL_REQUIRE(ws && aligned(ws, 256) && ws_bytes >= gated_mm_workspace_bytes(m, n_groups, n, k, dtype),
+                "gated_mm: workspace too small or misaligned");
+    ProdArgs p = {x, w, nullptr, order, offsets, m, ldx, k, k, n, k, n_groups, 0, nullptr, 0, 0};
+    if (copies(m, n_groups, k, dtype)) {
+        char* const xc = (char*)ws;
+        char* const wc = xc + x_copy_bytes(m, k, dtype);
+        const int64_t rows = (int64_t)n_groups * 2 * n;
+        htl_status st = pack_rows(x, ldx, dtype, nullptr, m, m, k, xc, spread_ld(k), stream);
+        if (st == HTL_OK) st = pack_rows(w, k, dtype, nullptr, rows, rows, k, wc, packed_ld(k), stream);
+        if (st != HTL_OK) return st;
+        p = {xc, wc, nullptr, order, offsets, m, spread_ld(k), k, packed_ld(k), n, (int)packed_ld(k), n_groups, 0, nullptr, 0, 0};
+    }
     launch_pairs(p, dtype, {(int)act, y, y_dtype == HTL_F32, kept, {}, nullptr, 0, false}, stream);
     return check_launch("gated_mm");
 }
@@ -325,19 +357,16 @@ extern "C" htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const voi
                 "gated_mm_backward: workspace too small or misaligned");
     const BackSpace s(ws, m, n_groups, n, k, dtype, k % 8 || aligned(w, 16));
     htl_status st = HTL_OK;
-    if (s.wide && k % 8) {                   // rows that whole pieces do not make up: copied, with zeros behind them
-        st = pack_rows(w, k, nullptr, (int64_t)n_groups * 2 * n, (int64_t)n_groups * 2 * n, k, s.w, packed_ld(k), stream);
-        if (st != HTL_OK) return st;
-    }
-    // x by position in the plan
-    const bool as_is = s.wide && !order && packed_as_is(x, ldx, k);
-    if (s.wide && !as_is) {
-        st = pack_rows(x, ldx, order, m, m, k, s.x, spread_ld(k), stream);
-        if (st != HTL_OK) return st;
-    }
-    const void* xs = !s.wide || as_is ? x : s.x;
-    const void* wp = s.wide && k % 8 ? s.w : w;
-    const int64_t ldxs = !s.wide || as_is ? ldx : spread_ld(k), ldw = s.wide && k % 8 ? packed_ld(k) : k;
+    const int64_t rows = (int64_t)n_groups * 2 * n;
+    if (s.copied) st = pack_rows(w, k, dtype, nullptr, rows, rows, k, s.w, packed_ld(k), stream);
+    // wide.h takes x by position in the plan
+    const bool as_is = s.wide ? !order && packed_as_is(x, ldx, k) : !s.copied;
+    if (st == HTL_OK && !as_is)
+        st = pack_rows(x, ldx, dtype, s.wide ? order : nullptr, m, m, k, s.x, spread_ld(k), stream);
+    if (st != HTL_OK) return st;
+    const void* xs = as_is ? x : s.x;
+    const void* wp = s.copied ? s.w : w;
+    const int64_t ldxs = as_is ? ldx : spread_ld(k), ldw = s.copied ? packed_ld(k) : k;
     if (m > 0) {
         const RowsIn in = {dy, nullptr, ld_dy, 0};
         if (kept) {
@@ -348,12 +377,12 @@ extern "C" htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const voi
             if (dtype == HTL_F32) hipLaunchKernelGGL(k_gated_slopes<kSrcF32>, grid, dim3(256), 0, stream, in, from, to, by, m, n, (int)act);
             else hipLaunchKernelGGL(k_gated_slopes<kSrcBf16>, grid, dim3(256), 0, stream, in, from, to, by, m, n, (int)act);
         } else {
-            ProdArgs p = {xs, wp, nullptr, order, offsets, m, ldxs, k, ldw, n, k, n_groups, 0, nullptr, 0, 0};
+            ProdArgs p = {xs, wp, nullptr, order, offsets, m, ldxs, k, ldw, n, s.copied ? (int)ldw : k, n_groups, 0, nullptr, 0, 0};
             p.packed = s.wide;
             launch_pairs(p, dtype, {(int)act, nullptr, false, nullptr, in, s.d, s.ld, s.wide}, stream);
         }
         st = check_launch("gated_mm_backward");
-        if (st == HTL_OK && s.wide) st = zero_behind(s.d, m, 2 * n, s.ld, stream);
+        if (st == HTL_OK && s.ld > 2 * n) st = zero_behind(s.d, dtype, m, 2 * n, s.ld, stream);
         if (st != HTL_OK) return st;
     }
     if (dx && s.wide) {
@@ -364,9 +393,9 @@ extern "C" htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const voi
         else if (st == HTL_OK && offsets)
             st = zero_rest(dx, (int64_t)k * elem(dx_dtype), m, order, offsets + n_groups, stream);
     } else if (dx) {
-        st = rows_dx(s.d, s.ld, w, k, dtype, m, 2 * n, k, order, offsets, n_groups, dx, dx_dtype, stream);
+        st = rows_dx(s.d, s.ld, wp, ldw, dtype, m, 2 * n, k, order, offsets, n_groups, dx, dx_dtype, s.copied, stream);
     }
     if (st != HTL_OK || !dw) return st;
     if (s.wide) return wide_dw(s.d, s.ld, xs, ldxs, m, 2 * n, k, offsets, n_groups, dw, dtype, s.sums, stream);
-    return sums_dw(s.d, s.ld, x, ldx, dtype, m, 2 * n, k, order, offsets, n_groups, dw, dtype, s.sums, stream);
+    return sums_dw(s.d, s.ld, xs, ldxs, dtype, m, 2 * n, k, order, offsets, n_groups, dw, dtype, s.sums, s.copied, stream);
 }

@@ -161,10 +161,10 @@ template <int MODE, int LP> void launch_resident(const ProdArgs& p, int64_t chun
 //   against 18 / 22.
 // - tiles of 256 x 256 once they fill the device: 8 x 2,048, 1,024 -> 1,024:
 //   43 / 47 against 51 / 53 with 128; 8 x 1,024: 37 / 38 against 28 / 28.
-template <int MODE> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s) {
+template <int MODE> void launch_rows(ProdArgs p, htl_dtype dtype, hipStream_t s, bool padded = false) {
     const int cols = MODE == kFwd ? p.n : p.k, es = elem(dtype);
-    const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && (int64_t)p.k * es % 16 == 0 && p.ldw * es % 16 == 0 &&
-                      (MODE == kFwd || (int64_t)p.n * es % 16 == 0) && aligned(p.b, 16) &&
+    const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && p.ldw * es % 16 == 0 && aligned(p.b, 16) &&
+                      (padded || ((int64_t)p.k * es % 16 == 0 && (MODE == kFwd || (int64_t)p.n * es % 16 == 0))) &&
                       p.m * p.lda * es <= kBufferBytes && (int64_t)p.n * p.ldw * es <= kBufferBytes;
     const int64_t each = p.m / p.n_groups;
     const int len = MODE == kFwd ? p.k : p.n, lp = len <= 32 ? 1 : len <= 64 ? 2 : len <= 128 ? 4 : 8;
@@ -216,11 +216,11 @@ int64_t dw_slots(int64_t m, int n_groups, int n, int k) { return split_chunks(m,
 }  // namespace
 
 htl_status rows_dx(const void* dy, int64_t ld_dy, const void* w, int64_t ldw, htl_dtype dtype, int64_t m, int n, int k,
-                   const int32_t* order, const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype,
+                   const int32_t* order, const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype, bool padded,
                    hipStream_t stream) {
     if (m == 0) return HTL_OK;
     const ProdArgs p = {dy, w, dx, order, offsets, m, ld_dy, k, ldw, n, k, n_groups, 0, nullptr, dx_dtype == HTL_F32, 0};
-    launch_rows<kDx>(p, dtype, stream);
+    launch_rows<kDx>(p, dtype, stream, padded);
     return check_launch("input gradients");
 }
 
@@ -236,11 +236,11 @@ int rows_dx_splits(int64_t m, int n, int k) {
 
 htl_status rows_dx_parts(const void* dy, int64_t ld_dy, const void* w, int64_t ldw, htl_dtype dtype, int64_t m, int n, int k,
                          const int32_t* order, const int32_t* offsets, int n_groups, float* parts, int splits, bool add,
-                         hipStream_t stream) {
+                         bool padded, hipStream_t stream) {
     if (m == 0) return HTL_OK;
     const int es = elem(dtype);
-    const bool fast = ld_dy * es % 16 == 0 && aligned(dy, 16) && (int64_t)n * es % 16 == 0 && (int64_t)k * es % 16 == 0 &&
-                      ldw * es % 16 == 0 && aligned(w, 16) && m * ld_dy * es <= kBufferBytes && n * ldw * es <= kBufferBytes;
+    const bool fast = ld_dy * es % 16 == 0 && aligned(dy, 16) &&
+                      (padded || ((int64_t)n * es % 16 == 0 && (int64_t)k * es % 16 == 0)) && ldw * es % 16 == 0 && aligned(w, 16) && m * ld_dy * es <= kBufferBytes && n * ldw * es <= kBufferBytes;
     ProdArgs p = {dy, w, nullptr, order, offsets, m, ld_dy, k, ldw, n, k, n_groups, 128, parts, 1, 0};
     p.splits = splits;
     const int64_t tiles = (m / 128 + n_groups + 1) * ceil_div(k, 128) * splits;
@@ -269,13 +269,13 @@ size_t sums_dw_bytes(int64_t m, int n_groups, int n, int k) {
 
 htl_status sums_dw(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, htl_dtype dtype, int64_t m, int n, int k,
                    const int32_t* order, const int32_t* offsets, int n_groups, void* dw, htl_dtype dw_dtype, void* ws,
-                   hipStream_t stream) {
+                   bool padded, hipStream_t stream) {
     const int es = elem(dtype);
     const ProdArgs p = {dy, x, dw, order, offsets, m, ld_dy, ldx, k, n, k, n_groups, dw_chunk_rows(m, n, k),
                         (float*)ws, dw_dtype == HTL_F32, dw_slots(m, n_groups, n, k)};
     const int64_t chunks = dw_chunks(m, n_groups, n, k);
     const bool fast = ld_dy * es % 16 == 0 && ldx * es % 16 == 0 && aligned(dy, 16) && aligned(x, 16) &&
-                      (int64_t)n * es % 16 == 0 && (int64_t)k * es % 16 == 0 && m * ld_dy * es <= kBufferBytes &&
+                      (padded || ((int64_t)n * es % 16 == 0 && (int64_t)k * es % 16 == 0)) && m * ld_dy * es <= kBufferBytes &&
                       m * ldx * es <= kBufferBytes;
     if (dw_dtype == HTL_BF16) {              // of bf16 operands
         if (fast && n >= 256 && k >= 256) launch<kSrcBf16, kDw, Big, true, true>(p, chunks, stream);
@@ -345,9 +345,9 @@ extern "C" htl_status grouped_mm_backward(const void* dy, int64_t ld_dy, const v
     HTL_REQUIRE(!dw || (ws && aligned(ws, 256) && ws_bytes >= grouped_mm_backward_workspace_bytes(m, n_groups, n, k)),
                 "grouped_mm_backward: workspace too small or misaligned");
     if (dx && m > 0) {
-        const htl_status st = rows_dx(dy, ld_dy, w, k, dtype, m, n, k, order, offsets, n_groups, dx, dx_dtype, stream);
+        const htl_status st = rows_dx(dy, ld_dy, w, k, dtype, m, n, k, order, offsets, n_groups, dx, dx_dtype, false, stream);
         if (st != HTL_OK) return st;
     }
     if (!dw) return HTL_OK;
-    return sums_dw(dy, ld_dy, x, ldx, dtype, m, n, k, order, offsets, n_groups, dw, HTL_F32, ws, stream);
+    return sums_dw(dy, ld_dy, x, ldx, dtype, m, n, k, order, offsets, n_groups, dw, HTL_F32, ws, false, stream);
 }

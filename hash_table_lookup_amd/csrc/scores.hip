@@ -360,10 +360,10 @@ struct Rows2 {               // x and w as the calls have them
     htl_dtype dtype;
 };
 
-// The product x w^T of `cols` items from v0 on, with an end made by `make` for
-// the tile's shape.  Tiles by size, as the plain products' (product.hip).
+// The product x w^T of `cols` items (r.w: the first one's row), with an end made
+// by `make` for the tile's shape.  Tiles by size, as the plain products' (product.hip).
 constexpr int64_t kFewRows = 48;
-int tile_of(const Rows2& r, int cols, bool& fast) {
+int tile_of(const Rows2& r, int64_t cols, bool& fast) {
     const int es = elem(r.dtype);
     fast = r.ldx * es % 16 == 0 && r.ldw * es % 16 == 0 && (int64_t)r.k * es % 16 == 0 && aligned(r.x, 16) &&
            aligned(r.w, 16) && r.m * r.ldx * es <= kBufferBytes && cols * r.ldw * es <= kBufferBytes;
@@ -377,10 +377,9 @@ bool wide_of(int64_t m, int vocab, htl_dtype dtype) {
 int wave_cols(int64_t m, bool wide) { return wide ? Wide::TC * 16 : m <= kFewRows ? Small::TC * 16 : Mid::TC * 16; }
 
 template <class Make>
-void launch_scores(const Rows2& r, int tile, bool fast, int v0, int cols, const int32_t* order, const int32_t* offsets,
-                   Make make, hipStream_t s) {
-    const char* w = (const char*)r.w + (int64_t)v0 * r.ldw * elem(r.dtype);
-    const ProdArgs p = {r.x, w, nullptr, order, offsets, r.m, r.ldx, r.ldw, r.ldw, cols, r.k, 1, (uint32_t)tile, nullptr, 0, 0};
+void launch_scores(const Rows2& r, int tile, bool fast, int cols, const int32_t* order, const int32_t* offsets, Make make,
+                   hipStream_t s) {
+    const ProdArgs p = {r.x, r.w, nullptr, order, offsets, r.m, r.ldx, r.ldw, r.ldw, cols, r.k, 1, (uint32_t)tile, nullptr, 0, 0};
     auto few = [&](auto t, auto shape) {                 // (tile: rows)
         constexpr int T = decltype(t)::value;
         using C = decltype(shape);
@@ -436,12 +435,16 @@ struct Carve {               // a workspace cut into 256-byte aligned parts
     }
 };
 
+// Whether tiles take copies of x and w, whose rows whole 16-byte pieces make up,
+// where theirs do not: loads then go straight to LDS.
+bool copied_of(int64_t m, int k, htl_dtype dtype) { return m > kFewRows && k % (dtype == HTL_F32 ? 4 : 8); }
+
 // Items whose copied matrix rows are held at a time.
 constexpr int kPackCols = 65536;
 int pack_cols(int vocab) { return vocab < kPackCols ? vocab : kPackCols; }
 
 struct ForwardSpace {
-    bool wide;
+    bool wide, copied;
     Best* partial;
     float* target_score;
     int32_t *ids, *order, *offsets;
@@ -459,8 +462,9 @@ struct ForwardSpace {
         offsets = c.take<int32_t>(2);
         group_bytes = wide ? row_groups_workspace_bytes(m, 1) : 0;
         groups = c.take<char>(group_bytes);
-        x = c.take<char>(wide ? m * spread_ld(k) * 2 : 0);
-        w = c.take<char>(wide ? pack_cols(vocab) * packed_ld(k) * 2 : 0);
+        copied = copied_of(m, k, dtype);
+        x = c.take<char>(wide || copied ? m * spread_ld(k) * elem(dtype) : 0);
+        w = c.take<char>(wide || copied ? pack_cols(vocab) * packed_ld(k) * elem(dtype) : 0);
         bytes = c.at;
     }
 };
@@ -475,7 +479,7 @@ int piece_cols(int64_t m, int vocab, htl_dtype dtype) {
 }
 
 struct BackwardSpace {
-    bool wide;
+    bool wide, copied;
     int step, splits;        // columns of a piece, parts of dx's sums
     int32_t *ids, *order, *offsets;
     void* groups;
@@ -500,8 +504,9 @@ struct BackwardSpace {
         const size_t a = wide ? wide_dw_bytes(m, 1, step, k) : sums_dw_bytes(m, 1, step, k);
         const size_t b = wide ? wide_dw_bytes(m, 1, last, k) : sums_dw_bytes(m, 1, last, k);
         sums = c.take<char>(a > b ? a : b);
-        x = c.take<char>(wide ? m * spread_ld(k) * 2 : 0);
-        w = c.take<char>(wide ? step * packed_ld(k) * 2 : 0);
+        copied = copied_of(m, k, dtype);
+        x = c.take<char>(wide || copied ? m * spread_ld(k) * elem(dtype) : 0);
+        w = c.take<char>(wide || copied ? step * packed_ld(k) * elem(dtype) : 0);
         bytes = c.at;
     }
 };
@@ -519,12 +524,12 @@ void launch_wide(const void* x, int64_t ldx, bool packed, const void* w, int64_t
     hipLaunchKernelGGL(k_scores_wide<End>, grid, dim3(Wide::kThreads), 0, s, p, end);
 }
 
-// A piece of w as an operand of wide.h's tiles: as it lies, or copied to `room`.
+// A piece of w as an operand of tiles: as it lies, or copied to `room`.
 htl_status piece_of(const Rows2& r, int v0, int cols, char* room, const void*& w, int64_t& ldw, hipStream_t stream) {
-    w = (const char*)r.w + (int64_t)v0 * r.ldw * 2;
+    w = (const char*)r.w + (int64_t)v0 * r.ldw * elem(r.dtype);
     ldw = r.ldw;
-    if (packed_as_is(r.w, r.ldw, r.k) && cols * r.ldw * 2 <= kBufferBytes) return HTL_OK;
-    const htl_status st = pack_rows(w, r.ldw, nullptr, cols, cols, r.k, room, packed_ld(r.k), stream);
+    if (packed_as_is(r.w, r.ldw, r.k, r.dtype) && cols * r.ldw * elem(r.dtype) <= kBufferBytes) return HTL_OK;
+    const htl_status st = pack_rows(w, r.ldw, r.dtype, nullptr, cols, cols, r.k, room, packed_ld(r.k), stream);
     w = room;
     ldw = packed_ld(r.k);
     return st;
@@ -539,7 +544,7 @@ htl_status forward_scores(const Rows2& r, float scale, const ForwardSpace& s, co
         htl_status st = row_groups(s.ids, r.m, 1, s.order, s.offsets, s.groups, s.group_bytes, stream);
         if (st != HTL_OK) return st;
         const bool as_is = packed_as_is(r.x, r.ldx, r.k) && r.m * r.ldx * 2 <= kBufferBytes;
-        if (!as_is) st = pack_rows(r.x, r.ldx, s.order, r.m, r.m, r.k, s.x, spread_ld(r.k), stream);
+        if (!as_is) st = pack_rows(r.x, r.ldx, r.dtype, s.order, r.m, r.m, r.k, s.x, spread_ld(r.k), stream);
         const int most = packed_as_is(r.w, r.ldw, r.k) && kPackCols * r.ldw * 2 <= kBufferBytes ? most_cols(r) : kPackCols;
         for (int v0 = 0; v0 < r.vocab && st == HTL_OK;) {
             const int cols = r.vocab - v0 < most ? r.vocab - v0 : most;
@@ -555,17 +560,29 @@ htl_status forward_scores(const Rows2& r, float scale, const ForwardSpace& s, co
         }
         return st;
     }
-    const int step = most_cols(r);
-    bool fast;
-    const int tile = tile_of(r, r.vocab < step ? r.vocab : step, fast);
-    for (int v0 = 0; v0 < r.vocab;) {
+    Rows2 t = r;                             // operands as the tiles take them
+    htl_status st = HTL_OK;
+    if (s.copied) {
+        st = pack_rows(r.x, r.ldx, r.dtype, nullptr, r.m, r.m, r.k, s.x, spread_ld(r.k), stream);
+        t.x = s.x;
+        t.ldx = spread_ld(r.k);
+        t.k = (int)packed_ld(r.k);
+    }
+    const int step = s.copied ? pack_cols(r.vocab) : most_cols(r);
+    for (int v0 = 0; v0 < r.vocab && st == HTL_OK;) {
         const int cols = r.vocab - v0 < step ? r.vocab - v0 : step;
-        launch_scores(r, tile, fast, v0, cols, nullptr, nullptr, [&](auto shape) {
+        if (s.copied) st = piece_of(r, v0, cols, s.w, t.w, t.ldw, stream);
+        else t.w = (const char*)r.w + (int64_t)v0 * r.ldw * elem(r.dtype);
+        if (st != HTL_OK) return st;
+        bool fast;
+        const int tile = tile_of(t, cols, fast);
+        launch_scores(t, tile, fast, cols, nullptr, nullptr, [&](auto shape) {
             return ScoreEnd<decltype(shape)>{r.m, cols, v0, v0 / W, scale, s.partial, targets, s.target_score};
         }, stream);
+        st = check_launch("scores");
         v0 += cols;
     }
-    return check_launch("scores");
+    return st;
 }
 
 // All of a backward pass once ids and the teacher's entries stand.
@@ -575,23 +592,31 @@ htl_status backward_pieces(const Rows2& r, float scale, const BackwardSpace& s, 
     const int64_t m = r.m, ld = spread_ld(s.step);
     const int es = elem(r.dtype);
     htl_status st = row_groups(s.ids, m, 1, s.order, s.offsets, s.groups, s.group_bytes, stream);
-    if (st == HTL_OK && s.wide) st = pack_rows(r.x, r.ldx, s.order, m, m, r.k, s.x, spread_ld(r.k), stream);
+    if (st == HTL_OK && (s.wide || s.copied)) st = pack_rows(r.x, r.ldx, r.dtype, s.wide ? s.order : nullptr, m, m, r.k, s.x, spread_ld(r.k), stream);
     if (st != HTL_OK) return st;
-    bool fast;
-    const int tile = tile_of(r, s.step, fast);
+    Rows2 t = r;                             // operands as the tiles take them
+    if (s.copied) {
+        t.x = s.x;
+        t.ldx = spread_ld(r.k);
+        t.k = (int)packed_ld(r.k);
+    }
     // dx in parts (wide tiles: by position) or whole
     float* parts = s.step < r.vocab || s.splits > 1 ? s.parts : nullptr;
     for (int v0 = 0; v0 < r.vocab;) {
         const int cols = r.vocab - v0 < s.step ? r.vocab - v0 : s.step;
         const void* w = (const char*)r.w + (int64_t)v0 * r.ldw * es;
         int64_t ldw = r.ldw;
+        if (s.wide || s.copied) st = piece_of(r, v0, cols, s.w, w, ldw, stream);
+        if (st != HTL_OK) return st;
         if (s.wide) {
-            st = piece_of(r, v0, cols, s.w, w, ldw, stream);
-            if (st != HTL_OK) return st;
             const SlopeEnd<Wide> end = {cols, v0, ld, scale, lse, dloss, targets, s.d, false, true};
             launch_wide(s.x, spread_ld(r.k), true, w, ldw, m, cols, r.k, s.order, s.offsets, end, stream);
         } else {
-            launch_scores(r, tile, fast, v0, cols, s.order, s.offsets, [&](auto shape) {
+            t.w = w;
+            t.ldw = ldw;
+            bool fast;
+            const int tile = tile_of(t, cols, fast);
+            launch_scores(t, tile, fast, cols, s.order, s.offsets, [&](auto shape) {
                 return SlopeEnd<decltype(shape)>{cols, v0, ld, scale, lse, dloss, targets, s.d, r.dtype == HTL_F32, false};
             }, stream);
         }
@@ -605,20 +630,22 @@ htl_status backward_pieces(const Rows2& r, float scale, const BackwardSpace& s, 
                                    s.entries, v0, cols, ld, s.d);
         }
         st = check_launch("slopes");
-        if (st == HTL_OK && s.wide) st = zero_behind(s.d, m, cols, ld, stream);
+        if (st == HTL_OK) st = zero_behind(s.d, r.dtype, m, cols, ld, stream);
+        // rows of d have zeros behind them; those of x and w are copies, or whole pieces
+        const bool whole = s.copied || (packed_as_is(r.x, r.ldx, r.k, r.dtype) && packed_as_is(r.w, r.ldw, r.k, r.dtype));
         if (st == HTL_OK && dx) {
             if (s.wide)
                 st = wide_dx(s.d, ld, w, ldw, m, cols, r.k, s.order, s.offsets, 1, dx, dx_dtype, parts, s.splits, v0 > 0, stream);
             else
-                st = parts ? rows_dx_parts(s.d, ld, w, ldw, r.dtype, m, cols, r.k, s.order, s.offsets, 1, parts, s.splits, v0 > 0, stream)
-                           : rows_dx(s.d, ld, w, ldw, r.dtype, m, cols, r.k, s.order, s.offsets, 1, dx, dx_dtype, stream);
+                st = parts ? rows_dx_parts(s.d, ld, w, ldw, r.dtype, m, cols, r.k, s.order, s.offsets, 1, parts, s.splits, v0 > 0, whole, stream)
+                           : rows_dx(s.d, ld, w, ldw, r.dtype, m, cols, r.k, s.order, s.offsets, 1, dx, dx_dtype, whole, stream);
         }
         if (st == HTL_OK && dw) {
             char* to = (char*)dw + (int64_t)v0 * r.k * es;
             if (s.wide)
                 st = wide_dw(s.d, ld, s.x, spread_ld(r.k), m, cols, r.k, s.offsets, 1, to, r.dtype, s.sums, stream);
             else
-                st = sums_dw(s.d, ld, r.x, r.ldx, r.dtype, m, cols, r.k, s.order, s.offsets, 1, to, r.dtype, s.sums, stream);
+                st = sums_dw(s.d, ld, t.x, t.ldx, r.dtype, m, cols, r.k, s.order, s.offsets, 1, to, r.dtype, s.sums, whole, stream);
         }
         if (st != HTL_OK) return st;
         v0 += cols;

@@ -375,6 +375,43 @@ struct TileAt {
     int col;                // which of the `cols` tiles beside each other
 };
 constexpr int kBlock = 8, kXcds = 8;
+// Which of `total` tiles workgroup b takes.  1: item; 0: nothing at this b; -1:
+// nothing at this or any later b.
+template <class V> __device__ __forceinline__ int deal_tile(V total, V cols, int min_chunks, V b, V& item) {
+    const V x = b % kXcds, i = b / kXcds;
+    if (min_chunks) {
+        const V deal = cols < 2 * kXcds ? 1 : (cols < 16 * kXcds ? cols / kXcds : 16);
+        item = (i / deal * kXcds + x) * deal + i % deal;
+        if (item >= total) return i / deal * kXcds * deal >= total ? -1 : 0;
+    } else {
+        const V each = total / kXcds, extra = total % kXcds;
+        if (i >= each + (x < extra)) return i > each ? -1 : 0;
+        item = x * each + (x < extra ? x : extra) + i;
+    }
+    return 1;
+}
+// The same tiles for one group: no search, and 32-bit divisions (a search and its
+// 64-bit ones take as long as a short reduction).
+__device__ __forceinline__ int tile_of_one(int64_t gb, int64_t ge, uint32_t R, int min_chunks, uint32_t cols, uint32_t b,
+                                           TileAt& t) {
+    uint32_t count = ((uint32_t)(ge - gb) + R - 1u) / R;
+    if ((int)count < min_chunks) count = min_chunks;
+    uint32_t item;
+    const int dealt = deal_tile<uint32_t>(count * cols, cols, min_chunks, b, item);
+    if (dealt < 1) return dealt;
+    const uint32_t block = item / (cols * kBlock), in = item - block * cols * kBlock;
+    const uint32_t left = count - block * kBlock, width = left < kBlock ? left : kBlock;
+    const uint32_t col = in / width, index = block * kBlock + (in - col * width);
+    const int64_t len = min_chunks ? ((uint32_t)((ge - gb + count - 1) / count) + 63u) / 64 * 64 : R;
+    const int64_t b0 = gb + index * len < ge ? gb + index * len : ge;
+    t.g = 0;
+    t.count = (int)count;
+    t.col = (int)col;
+    t.slot = index;
+    t.beg = b0;
+    t.end = b0 + len < ge ? b0 + len : ge;
+    return 1;
+}
 // 1: found; 0: nothing at this b; -1: nothing at this or any later b.
 __device__ __forceinline__ int search_tile(const int32_t* offsets, int n_groups, int64_t m, uint32_t R, int min_chunks,
                                            bool no_rest, int64_t cols, int64_t b, TileAt& t) {
@@ -398,17 +435,9 @@ __device__ __forceinline__ int search_tile(const int32_t* offsets, int n_groups,
         total += s;
     }
     total *= cols;
-    const int64_t x = b % kXcds, i = b / kXcds;
     int64_t item;
-    if (min_chunks) {
-        const int64_t deal = cols < 2 * kXcds ? 1 : (cols < 16 * kXcds ? cols / kXcds : 16);
-        item = (i / deal * kXcds + x) * deal + i % deal;
-        if (item >= total) return i / deal * kXcds * deal >= total ? -1 : 0;
-    } else {
-        const int64_t each = total / kXcds, extra = total % kXcds;
-        if (i >= each + (x < extra)) return i > each ? -1 : 0;
-        item = x * each + (x < extra ? x : extra) + i;
-    }
+    const int dealt = deal_tile(total, cols, min_chunks, b, item);
+    if (dealt < 1) return dealt;
     int64_t run = 0, alone = 0;
     for (int g0 = 0; g0 <= n_groups; g0 += 64) {
         const int cnt = chunks_at(g0 + lane, beg, end);
@@ -450,7 +479,14 @@ __device__ __forceinline__ int search_tile(const int32_t* offsets, int n_groups,
 __device__ __forceinline__ int find_tile(const int32_t* offsets, int n_groups, int64_t m, uint32_t R, int min_chunks,
                                          bool no_rest, int64_t cols, int64_t b, TileAt& t) {
     TileAt v = {};
-    const int found = search_tile(offsets, n_groups, m, R, min_chunks, no_rest, cols, b, v);
+    int found;
+    if (n_groups == 1 && (!offsets || no_rest || min_chunks) && cols < 1 << 16 && m <= (int64_t)R << 14) {
+        int64_t beg, end;
+        group_range(offsets, 1, m, 0, beg, end);
+        found = tile_of_one(beg, end, R, min_chunks, (uint32_t)cols, (uint32_t)b, v);
+    } else {
+        found = search_tile(offsets, n_groups, m, R, min_chunks, no_rest, cols, b, v);
+    }
     t.g = __builtin_amdgcn_readfirstlane(v.g);
     t.beg = __builtin_amdgcn_readfirstlane((int)v.beg);
     t.end = __builtin_amdgcn_readfirstlane((int)v.end);
@@ -841,17 +877,18 @@ inline bool known(htl_dtype t) { return t == HTL_F32 || t == HTL_BF16; }
 // whole, or in parts of the reduction: parts is float[splits][m][k], by row, of
 // which rows of a group are written, or (add) added to, for sum_parts to join.
 // And dw[g] = sum of dy[i] x[i]^T in dw_dtype, with sums_dw_bytes of workspace.
-// Arguments are the caller's to check.
+// padded: what lies between the length of a row of dy, w or x and the next 16
+// bytes may be read, and is zero in dy.  Arguments are the caller's to check.
 htl_status rows_dx(const void* dy, int64_t ld_dy, const void* w, int64_t ldw, htl_dtype dtype, int64_t m, int n, int k,
-                   const int32_t* order, const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype,
+                   const int32_t* order, const int32_t* offsets, int n_groups, void* dx, htl_dtype dx_dtype, bool padded,
                    hipStream_t stream);
 int rows_dx_splits(int64_t m, int n, int k);
 htl_status rows_dx_parts(const void* dy, int64_t ld_dy, const void* w, int64_t ldw, htl_dtype dtype, int64_t m, int n, int k,
                          const int32_t* order, const int32_t* offsets, int n_groups, float* parts, int splits, bool add,
-                         hipStream_t stream);
+                         bool padded, hipStream_t stream);
 size_t sums_dw_bytes(int64_t m, int n_groups, int n, int k);
 htl_status sums_dw(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, htl_dtype dtype, int64_t m, int n, int k,
                    const int32_t* order, const int32_t* offsets, int n_groups, void* dw, htl_dtype dw_dtype, void* ws,
-                   hipStream_t stream);
+                   bool padded, hipStream_t stream);
 
 }  // namespace htl

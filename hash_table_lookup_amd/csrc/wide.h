@@ -257,17 +257,20 @@ template <int MODE, class End> __device__ __forceinline__ void wide_tiles(const 
 // 16-byte aligned, and what lies between a row's length and the next multiple
 // of 8 is zero in d and finite elsewhere.
 
-// Rows by position, `ld` >= k apart (a multiple of 8), with zeros behind their k elements.
-htl_status pack_rows(const void* x, int64_t ldx, const int32_t* order, int64_t m, int64_t src_rows, int k, void* out,
-                     int64_t ld, hipStream_t stream);
+// Rows (order nullable: by position in it), `ld` >= k apart (a multiple of 8), with zeros behind their k elements.
+htl_status pack_rows(const void* x, int64_t ldx, htl_dtype dtype, const int32_t* order, int64_t m, int64_t src_rows, int k,
+                     void* out, int64_t ld, hipStream_t stream);
 inline __host__ __device__ int64_t packed_ld(int64_t k) { return (k + 7) / 8 * 8; }
 // The same for rows laid out here: rows whole KiB apart share L2 channels (d of 32,768
 // columns, dx's product: 874 us, with 64 elements more 808).
 inline int64_t spread_ld(int64_t k) { return packed_ld(k) + (packed_ld(k) % 512 ? 0 : 64); }
 // Zeros between the `cols` elements of each row and the next multiple of 8.
-htl_status zero_behind(void* d, int64_t m, int cols, int64_t ld, hipStream_t stream);
+htl_status zero_behind(void* d, htl_dtype dtype, int64_t m, int cols, int64_t ld, hipStream_t stream);
 // Whether rows can be an operand as they lie.
-inline bool packed_as_is(const void* p, int64_t ld, int k) { return ld % 8 == 0 && k % 8 == 0 && aligned(p, 16); }
+inline bool packed_as_is(const void* p, int64_t ld, int k, htl_dtype dtype = HTL_BF16) {
+    const int piece = dtype == HTL_F32 ? 4 : 8;
+    return ld % piece == 0 && k % piece == 0 && aligned(p, 16);
+}
 
 // dx[row] = w_g^T d[pos] in `splits` parts of the reduction.  With parts
 // (float[splits][m][k], by position) they are put there (add: added to what is

@@ -43,21 +43,22 @@ struct DwEnd {
 __global__ __launch_bounds__(256, 1) void k_wide_dx(ProdArgs p, DxEnd end) { wide_tiles<kDx>(p, end); }
 __global__ __launch_bounds__(256, 1) void k_wide_dw(ProdArgs p, DwEnd end) { wide_tiles<kDw>(p, end); }
 
-// Eight elements a thread.
-__global__ __launch_bounds__(256) void k_pack_rows(RowsIn x, const int32_t* __restrict__ order, int64_t m, int64_t src_rows,
-                                                   int k, uint16_t* __restrict__ out, int64_t ld) {
-    const int64_t each = ld / 8, all = m * each;
+// 16 bytes a thread.
+template <int ES>
+__global__ __launch_bounds__(256) void k_pack_rows(const char* __restrict__ x, int64_t ldx, const int32_t* __restrict__ order,
+                                                   int64_t m, int64_t src_rows, int k, char* __restrict__ out, int64_t ld) {
+    constexpr int VE = 16 / ES;
+    const int64_t each = ld / VE, all = m * each;
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
         const int64_t pos = i / each, row = order ? (int64_t)order[pos] : pos;
-        const int col = (int)(i - pos * each) * 8;
-        Raw8<kSrcBf16> v;
-        v.w = zeros4();
-        if (row >= 0 && row < src_rows) load8(x, row, col, k, v);
-        *(u32x4*)(out + pos * ld + col) = v.w;
+        const int col = (int)(i - pos * each) * VE;
+        const int64_t left = row >= 0 && row < src_rows ? k - col : 0;
+        *(u32x4*)(out + (pos * ld + col) * ES) = held_piece<ES>(x + (row * ldx + col) * ES, left);
     }
 }
 
-__global__ __launch_bounds__(256) void k_zero_behind(uint16_t* __restrict__ d, int64_t m, int cols, int64_t ld) {
+template <class E>
+__global__ __launch_bounds__(256) void k_zero_behind(E* __restrict__ d, int64_t m, int cols, int64_t ld) {
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < m; i += gridDim.x * 256ll)
         for (int64_t c = cols; c < packed_ld(cols); ++c) d[i * ld + c] = 0;
 }
@@ -75,15 +76,17 @@ __global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ par
         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
         const int have = k - col < 4 ? k - col : 4;
         if (pos < on) {
-            for (int s = 0; s < splits; ++s) {
-                const float* at = parts + ((int64_t)s * m + (by_row ? row : pos)) * k + col;
-                if (have == 4) {
+            const float* at = parts + (by_row ? row : pos) * k + col;
+            if (have == 4) {
+#pragma unroll 8
+                for (int s = 0; s < splits; ++s) {
                     f32x4 a;
-                    load_at<4>(at, a);
+                    load_at<4>(at + (int64_t)s * m * k, a);
                     v += a;
-                } else {
-                    for (int e = 0; e < have; ++e) v[e] += at[e];
                 }
+            } else {
+                for (int s = 0; s < splits; ++s)
+                    for (int e = 0; e < have; ++e) v[e] += at[(int64_t)s * m * k + e];
             }
         }
         if (BF16) {
@@ -127,18 +130,22 @@ uint32_t wide_dw_rows(int64_t m, int n, int k) {
 
 }  // namespace
 
-htl_status pack_rows(const void* x, int64_t ldx, const int32_t* order, int64_t m, int64_t src_rows, int k, void* out,
-                     int64_t ld, hipStream_t stream) {
+htl_status pack_rows(const void* x, int64_t ldx, htl_dtype dtype, const int32_t* order, int64_t m, int64_t src_rows, int k,
+                     void* out, int64_t ld, hipStream_t stream) {
     if (m == 0) return HTL_OK;
-    const RowsIn in = {x, nullptr, ldx, 0};
-    hipLaunchKernelGGL(k_pack_rows, dim3(grid_for(m * (ld / 8), 256, 1 << 16)), dim3(256), 0, stream, in, order, m, src_rows, k,
-                       (uint16_t*)out, ld);
+    const dim3 grid(grid_for(m * (ld / 4), 256, 1 << 16));
+    if (dtype == HTL_F32)
+        hipLaunchKernelGGL(k_pack_rows<4>, grid, dim3(256), 0, stream, (const char*)x, ldx, order, m, src_rows, k, (char*)out, ld);
+    else
+        hipLaunchKernelGGL(k_pack_rows<2>, grid, dim3(256), 0, stream, (const char*)x, ldx, order, m, src_rows, k, (char*)out, ld);
     return check_launch("pack rows");
 }
 
-htl_status zero_behind(void* d, int64_t m, int cols, int64_t ld, hipStream_t stream) {
+htl_status zero_behind(void* d, htl_dtype dtype, int64_t m, int cols, int64_t ld, hipStream_t stream) {
     if (cols % 8 == 0 || m == 0) return HTL_OK;
-    hipLaunchKernelGGL(k_zero_behind, dim3(grid_for(m, 256, 1 << 14)), dim3(256), 0, stream, (uint16_t*)d, m, cols, ld);
+    const dim3 grid(grid_for(m, 256, 1 << 14));
+    if (dtype == HTL_F32) hipLaunchKernelGGL(k_zero_behind<uint32_t>, grid, dim3(256), 0, stream, (uint32_t*)d, m, cols, ld);
+    else hipLaunchKernelGGL(k_zero_behind<uint16_t>, grid, dim3(256), 0, stream, (uint16_t*)d, m, cols, ld);
     return check_launch("zeros behind rows");
 }
 

@@ -384,8 +384,11 @@ def gated_mm(x: torch.Tensor, w: torch.Tensor, groups: Optional[RowGroups] = Non
     code = _dtype_code(x.dtype if out_dtype is None else out_dtype)
     y = torch.empty((m, n), dtype=_TORCH_DTYPE[code], device=x.device)
     kept = torch.empty((m, 2 * n), dtype=x.dtype, device=x.device) if keep else None
-    _check(lib().gated_mm(_ptr(x), ldx, _ptr(w), _dtype_code(x.dtype), m, n, k, _ptr(order), _ptr(offsets), g, act_code,
-                          _ptr(y), code, _ptr(kept), _stream()))
+    dtype = _dtype_code(x.dtype)
+    nb = lib().gated_mm_workspace_bytes(m, g, n, k, dtype)
+    ws = _scratch("gated_mm", nb, x.device)
+    _check(lib().gated_mm(_ptr(x), ldx, _ptr(w), dtype, m, n, k, _ptr(order), _ptr(offsets), g, act_code, _ptr(y), code,
+                          _ptr(kept), _ptr(ws), nb, _stream()))
     return y, kept
 
 

@@ -696,10 +696,13 @@ htl_status grouped_mm_backward(const void* dy, int64_t ld_dy, const void* x, int
  *              1 <= n <= HTL_MAX_PRODUCT_DIM / 2, 1 <= k <= HTL_MAX_PRODUCT_DIM.
  *   act        as norm_gate's.
  *   kept       nullable dtype[m][2 n]: z and u, rounded to dtype, for the
- *              backward pass. */
+ *              backward pass.
+ *   ws         at least gated_mm_workspace_bytes(m, n_groups, n, k, dtype)
+ *              bytes, 256-byte aligned. */
+size_t gated_mm_workspace_bytes(int64_t m, int n_groups, int n, int k, htl_dtype dtype);
 htl_status gated_mm(const void* x, int64_t ldx, const void* w, htl_dtype dtype, int64_t m, int n, int k,
                     const int32_t* order, const int32_t* offsets, int n_groups, htl_act act, void* y,
-                    htl_dtype y_dtype, void* kept, hipStream_t stream);
+                    htl_dtype y_dtype, void* kept, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* gated_mm_backward -- gradients of gated_mm: with dz = dy u act'(z) and du =
  * dy act(z), dx[i] = w[g]^T [dz; du] (dx nullable: not wanted) and dw[g] = the sum
