@@ -370,6 +370,11 @@ int tile_of(const Rows2& r, int64_t cols, bool& fast) {
     return r.m <= kFewRows ? 32 : 128;
 }
 // Whether wide.h's tiles fill the device.
+// Scores of rows shorter than this run as well or better in tiles of 128, of which
+// two fill a unit and one's end passes under the other's products (4,096 rows
+// against 65,536, step: 801 and 830 us of 128 elements, 953 and 967 of 256, but 1,639
+// and 1,448 of 504).
+constexpr int kWideK = 384;
 bool wide_of(int64_t m, int vocab, htl_dtype dtype) {
     return dtype == HTL_BF16 && m >= 256 && ceil_div(m, 256) * ceil_div(vocab, 256) >= 224;
 }
@@ -378,8 +383,10 @@ int wave_cols(int64_t m, bool wide) { return wide ? Wide::TC * 16 : m <= kFewRow
 
 template <class Make>
 void launch_scores(const Rows2& r, int tile, bool fast, int cols, const int32_t* order, const int32_t* offsets, Make make,
-                   hipStream_t s) {
-    const ProdArgs p = {r.x, r.w, nullptr, order, offsets, r.m, r.ldx, r.ldw, r.ldw, cols, r.k, 1, (uint32_t)tile, nullptr, 0, 0};
+                   hipStream_t s, bool packed = false) {
+    ProdArgs p = {r.x, r.w, nullptr, order, offsets, r.m, r.ldx, r.ldw, r.ldw, cols, r.k, 1, (uint32_t)tile, nullptr, 0, 0};
+    p.packed = packed;
+    p.no_rest = offsets != nullptr;
     auto few = [&](auto t, auto shape) {                 // (tile: rows)
         constexpr int T = decltype(t)::value;
         using C = decltype(shape);
@@ -453,7 +460,7 @@ struct ForwardSpace {
     char *x, *w;
     size_t bytes;
     ForwardSpace(void* ws, int64_t m, int vocab, int k, htl_dtype dtype) {
-        wide = wide_of(m, vocab, dtype);
+        wide = wide_of(m, vocab, dtype) && k >= kWideK;
         Carve c = {(char*)ws, 0};
         partial = c.take<Best>(m * ceil_div(vocab, wave_cols(m, wide)));
         target_score = c.take<float>(m);
@@ -595,7 +602,7 @@ htl_status backward_pieces(const Rows2& r, float scale, const BackwardSpace& s, 
     if (st == HTL_OK && (s.wide || s.copied)) st = pack_rows(r.x, r.ldx, r.dtype, s.wide ? s.order : nullptr, m, m, r.k, s.x, spread_ld(r.k), stream);
     if (st != HTL_OK) return st;
     Rows2 t = r;                             // operands as the tiles take them
-    if (s.copied) {
+    if (s.wide || s.copied) {
         t.x = s.x;
         t.ldx = spread_ld(r.k);
         t.k = (int)packed_ld(r.k);
@@ -608,7 +615,7 @@ htl_status backward_pieces(const Rows2& r, float scale, const BackwardSpace& s, 
         int64_t ldw = r.ldw;
         if (s.wide || s.copied) st = piece_of(r, v0, cols, s.w, w, ldw, stream);
         if (st != HTL_OK) return st;
-        if (s.wide) {
+        if (s.wide && r.k >= kWideK) {
             const SlopeEnd<Wide> end = {cols, v0, ld, scale, lse, dloss, targets, s.d, false, true};
             launch_wide(s.x, spread_ld(r.k), true, w, ldw, m, cols, r.k, s.order, s.offsets, end, stream);
         } else {
@@ -617,8 +624,8 @@ htl_status backward_pieces(const Rows2& r, float scale, const BackwardSpace& s, 
             bool fast;
             const int tile = tile_of(t, cols, fast);
             launch_scores(t, tile, fast, cols, s.order, s.offsets, [&](auto shape) {
-                return SlopeEnd<decltype(shape)>{cols, v0, ld, scale, lse, dloss, targets, s.d, r.dtype == HTL_F32, false};
-            }, stream);
+                return SlopeEnd<decltype(shape)>{cols, v0, ld, scale, lse, dloss, targets, s.d, r.dtype == HTL_F32, s.wide};
+            }, stream, s.wide);
         }
         if (top) {
             const dim3 grid(grid_for(m * top, 256));

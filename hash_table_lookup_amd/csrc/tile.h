@@ -27,7 +27,7 @@ struct ProdArgs {
     float* partial;          // dw: [limit][n][k]
     int out_f32;
     int64_t limit;           // dw: chunks of split groups that `partial` has room for
-    bool packed;             // wide.h: a's rows lie by position in the plan
+    bool packed;             // a's rows lie by position in the plan
     bool no_rest;            // no tiles for the rows of no group
     int splits;              // parts of a reduction
 };
@@ -637,7 +637,7 @@ __device__ __forceinline__ void product_tiles(const ProdArgs& p, const End& end)
     const int row_tiles = MODE == kDw ? (p.n + C::BR - 1) / C::BR : (PARTS ? p.splits : 1);
     for (int64_t b = blockIdx.x;; b += gridDim.x) {
         TileAt t;
-        const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, MODE == kDw ? 1 : 0, PARTS,
+        const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, MODE == kDw ? 1 : 0, PARTS || p.no_rest,
                                     (int64_t)col_tiles * row_tiles, b, t);
         if (found < 0) return;
         if (!found) continue;
@@ -691,7 +691,7 @@ __device__ __forceinline__ void product_tiles(const ProdArgs& p, const End& end)
                 __syncthreads();
             } else {
                 // a row that is not there is read as the first that may be: its products are not stored
-                ro.begin((const char*)p.a + first * ES, p.lda * ES, p.m, [&](int r) { return s_row[r] < 0 ? 0 : s_row[r]; });
+                ro.begin((const char*)p.a + first * ES, p.lda * ES, p.m, [&](int r) { return s_row[r] < 0 ? 0 : p.packed ? t.beg + r : (int64_t)s_row[r]; });
                 ro_at = lane_along(wr);
                 if constexpr (kPairs)
                     co.begin((const char*)p.b + wg * ES, p.ldw * ES, p.n, c0);

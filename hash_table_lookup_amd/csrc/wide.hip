@@ -149,12 +149,14 @@ htl_status zero_behind(void* d, htl_dtype dtype, int64_t m, int cols, int64_t ld
     return check_launch("zeros behind rows");
 }
 
-// Tiles enough for the device once, of at least 1,024 elements of the reduction each.
+// Tiles enough for the device once, of at least 1,024 elements of the reduction
+// each, and parts of at most 256 MiB.
 int wide_dx_splits(int64_t m, int n, int k) {
     const int64_t tiles = ceil_div(m, 256) * ceil_div(k, 256);
     int64_t s = 256 / (tiles < 1 ? 1 : tiles);
     if (s > n / 1024) s = n / 1024;
-    return s < 1 ? 1 : s > 16 ? 16 : (int)s;
+    if (m > 0 && s > (64 << 20) / (m * k)) s = (64 << 20) / (m * k);
+    return s < 1 ? 1 : (int)s;
 }
 
 htl_status wide_dx(const void* d, int64_t ldd, const void* w, int64_t ldw, int64_t m, int n, int k, const int32_t* order,
