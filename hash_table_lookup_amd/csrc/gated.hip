@@ -194,7 +194,7 @@ void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s
     if (p.packed || (p.k >= 256 && dtype == HTL_BF16 && fast && many(p.m, p.n_groups, ceil_div(p.m, 256) * ceil_div(p.n, 128)))) {
         p.rows = 256;
         p.no_rest = true;
-        const dim3 grid(grid_for(align_up((size_t)((p.m / 256 + p.n_groups) * ceil_div(p.n, 128)), kXcds), 1));
+        const dim3 grid(wide_grid((p.m / 256 + p.n_groups) * ceil_div(p.n, 128)));
         if (c.dy.p) {
             const GatedBackEnd<Wide, kSrcBf16> end = {p.n, c.act, c.dy, c.d, c.ld, c.packed};
             hipLaunchKernelGGL(k_gated_back_wide, grid, dim3(Wide::kThreads), 0, s, p, end);

@@ -527,7 +527,7 @@ template <class End>
 void launch_wide(const void* x, int64_t ldx, bool packed, const void* w, int64_t ldw, int64_t m, int cols, int k,
                  const int32_t* order, const int32_t* offsets, const End& end, hipStream_t s) {
     const ProdArgs p = {x, w, nullptr, order, offsets, m, ldx, 0, ldw, cols, k, 1, 256, nullptr, 0, 0, packed, true};
-    const dim3 grid(grid_for(align_up((size_t)((m / 256 + 1) * ceil_div(cols, 256)), kXcds), 1));
+    const dim3 grid(wide_grid((m / 256 + 1) * ceil_div(cols, 256)));
     hipLaunchKernelGGL(k_scores_wide<End>, grid, dim3(Wide::kThreads), 0, s, p, end);
 }
 

@@ -96,81 +96,125 @@ struct WideAcross {
     }
 };
 
+// A tile and its operands' places.
+template <int MODE, bool PAIRS> struct WideTile {
+    using RowOp = typename std::conditional<MODE == kDw, WideAcross, WideAlong>::type;
+    using ColOp = typename std::conditional<MODE == kFwd, WideAlong, WideAcross>::type;
+    static constexpr int BC = PAIRS ? Wide::BC / 2 : Wide::BC;
+    TileAt t;
+    bool grouped;
+    int r0, c0, len;
+    RowOp ro;
+    ColOp co;
+
+    // The first tile from workgroup number b on, which it leaves at that tile's; false past the last.
+    __device__ __forceinline__ bool find(const ProdArgs& p, int64_t& b) {
+        const int cols = MODE == kFwd ? p.n : p.k, col_tiles = (cols + BC - 1) / BC;
+        const int row_tiles = MODE == kDw ? (p.n + Wide::BR - 1) / Wide::BR : MODE == kDx ? p.splits : 1;
+        for (;; b += gridDim.x) {
+            const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, MODE == kDw ? 1 : 0, p.no_rest,
+                                        (int64_t)col_tiles * row_tiles, b, t);
+            if (found < 0) return false;
+            if (!found) continue;
+            if (MODE == kDw && t.count > 1 && t.slot >= p.limit) continue;   // offsets that overlap
+            break;
+        }
+        grouped = t.g < p.n_groups;
+        r0 = MODE == kDw ? t.col % row_tiles * Wide::BR : 0;
+        c0 = (MODE == kDw ? t.col / row_tiles : t.col % col_tiles) * BC;
+        if (MODE == kDx) t.slot = t.col / col_tiles;     // a part's tiles lie together
+        return true;
+    }
+    // Its operands, and where its rows go.
+    __device__ __forceinline__ void begin(const ProdArgs& p, int32_t* s_row) {
+        auto row_at = [&](int r) {
+            const int64_t pos = t.beg + r;
+            const int32_t row = pos < t.end ? (p.order ? p.order[pos] : (int32_t)pos) : -1;
+            return row >= 0 && row < p.m ? row : -1;
+        };
+        if (MODE != kDw) s_row[threadIdx.x] = row_at(threadIdx.x);
+        const int64_t wg = grouped ? (int64_t)t.g * (PAIRS ? 2 : 1) * p.n * p.ldw : 0;
+        int first = 0;
+        len = !grouped ? 0 : (MODE == kFwd ? p.k : (MODE == kDx ? p.n : (int)(t.end - t.beg)));
+        if (MODE == kDx) part_of((int)t.slot, p.splits, kStage, first, len);
+        if (len <= 0) return;
+        const char* a = (const char*)p.a;
+        const char* w = (const char*)p.b;
+        if constexpr (MODE == kFwd) {
+            if (p.packed) {
+                const int rows = (int)(t.end - t.beg);
+                ro.begin(a + t.beg * p.lda * 2, p.lda * 2, rows, [&](int r) { return r < rows ? (int64_t)r : -1; });
+            } else {
+                ro.begin(a, p.lda * 2, p.m, [&](int r) { return (int64_t)row_at(r); });
+            }
+        } else if constexpr (MODE == kDx) {
+            const int rows = (int)(t.end - t.beg);
+            ro.begin(a + (t.beg * p.lda + first) * 2, p.lda * 2, rows, [&](int r) { return r < rows ? (int64_t)r : -1; });
+        } else {
+            ro.begin(a + t.beg * p.lda * 2, p.lda * 2, len, r0, p.n);
+        }
+        if constexpr (PAIRS) {
+            const int n = p.n;                           // of every 128 rows 64 of each half
+            co.begin(w + wg * 2, p.ldw * 2, 2 * (int64_t)n, [&](int r) {
+                const int col = c0 + r / 128 * 64 + r % 64;
+                return col < n ? (int64_t)(r % 128 < 64 ? 0 : n) + col : -1;
+            });
+        } else if constexpr (MODE == kFwd) {
+            const int rows = p.n - c0 < Wide::BC ? p.n - c0 : Wide::BC;
+            co.begin(w + (wg + (int64_t)c0 * p.ldw) * 2, p.ldw * 2, rows, [&](int r) { return r < rows ? (int64_t)r : -1; });
+        } else if constexpr (MODE == kDx) {
+            co.begin(w + (wg + first * p.ldw) * 2, p.ldw * 2, len, c0, p.k);
+        } else {
+            co.begin(w + t.beg * p.ldb * 2, p.ldb * 2, len, c0, p.k);
+        }
+    }
+    __device__ __forceinline__ void load(int i, char* rows, char* cls, int stage) const {
+        ro.load(i, rows, stage * kStage, len);
+        co.load(i, cls, stage * kStage, len);
+    }
+};
+
 // kDx: the reduction is cut into p.splits parts, a tile each, whose number is
 // t.slot.
+//
+// A workgroup takes one tile after another, and the next one's first two stages
+// are under way while a tile's end runs (a tile of 2,048 elements took 66 us
+// beside 55 of products where it began with the search and those loads).
 template <int MODE, class End> __device__ __forceinline__ void wide_tiles(const ProdArgs& p, const End& end) {
     using C = Wide;
     constexpr bool kPairs = End::kPairs;
-    constexpr int BC = kPairs ? C::BC / 2 : C::BC;
     __shared__ __attribute__((aligned(128))) char row0[kStageBytes];
     __shared__ __attribute__((aligned(128))) char col0[kStageBytes];
     __shared__ __attribute__((aligned(128))) char row1[kStageBytes];
     __shared__ __attribute__((aligned(128))) char col1[kStageBytes];
-    __shared__ int32_t s_row[MODE == kDw ? 1 : C::BR];
+    __shared__ int32_t s_rows[2][MODE == kDw ? 1 : C::BR];
+    using Tile_ = WideTile<MODE, kPairs>;
+    using RowOp = typename Tile_::RowOp;
+    using ColOp = typename Tile_::ColOp;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wr = wv / C::WC * 128, wc = wv % C::WC * 128;
     const int cols = MODE == kFwd ? p.n : p.k;
-    const int col_tiles = (cols + BC - 1) / BC;
-    const int row_tiles = MODE == kDw ? (p.n + C::BR - 1) / C::BR : MODE == kDx ? p.splits : 1;
-    for (int64_t b = blockIdx.x;; b += gridDim.x) {
-        TileAt t;
-        const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, MODE == kDw ? 1 : 0, p.no_rest,
-                                    (int64_t)col_tiles * row_tiles, b, t);
-        if (found < 0) return;
-        if (!found) continue;
-        if (MODE == kDw && t.count > 1 && t.slot >= p.limit) continue;   // offsets that overlap
-        const bool grouped = t.g < p.n_groups;
-        const int r0 = MODE == kDw ? t.col % row_tiles * C::BR : 0;
-        const int c0 = (MODE == kDw ? t.col / row_tiles : t.col % col_tiles) * BC;
-        if (MODE == kDx) t.slot = t.col / col_tiles;     // a part's tiles lie together
-        if (MODE != kDw) {
-            __syncthreads();                             // the rows before are stored
-            const int64_t pos = t.beg + threadIdx.x;
-            const int32_t row = pos < t.end ? (p.order ? p.order[pos] : (int32_t)pos) : -1;
-            s_row[threadIdx.x] = row >= 0 && row < p.m ? row : -1;
-            __syncthreads();
-        }
+    const int ro_at = RowOp::lane(wr), co_at = ColOp::lane(wc);
+    Tile_ cur;
+    int64_t b = blockIdx.x;
+    if (!cur.find(p, b)) return;
+    auto first_loads = [&](const Tile_& o) __attribute__((always_inline)) {
+        if (o.len <= 0) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o.load(i, row0, col0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o.load(i, row1, col1, 1);
+    };
+    cur.begin(p, s_rows[0]);
+    first_loads(cur);
+    for (int turn = 0;; turn ^= 1) {
         f32x4 acc[C::TC][C::TR];
 #pragma unroll
         for (int i = 0; i < C::TC; ++i)
 #pragma unroll
             for (int j = 0; j < C::TR; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const int64_t wg = grouped ? (int64_t)t.g * (kPairs ? 2 : 1) * p.n * p.ldw : 0;
-        int first = 0, len = !grouped ? 0 : (MODE == kFwd ? p.k : (MODE == kDx ? p.n : (int)(t.end - t.beg)));
-        if (MODE == kDx) part_of((int)t.slot, p.splits, kStage, first, len);
-        if (len > 0) {
-            using RowOp = typename std::conditional<MODE == kDw, WideAcross, WideAlong>::type;
-            using ColOp = typename std::conditional<MODE == kFwd, WideAlong, WideAcross>::type;
-            RowOp ro;
-            ColOp co;
-            const char* a = (const char*)p.a;
-            const char* w = (const char*)p.b;
-            if constexpr (MODE == kFwd) {
-                const int64_t from = p.packed ? t.beg : 0;
-                ro.begin(a + from * p.lda * 2, p.lda * 2, p.packed ? t.end - t.beg : p.m,
-                         [&](int r) { return s_row[r] < 0 || !p.packed ? (int64_t)s_row[r] : (int64_t)r; });
-            } else if constexpr (MODE == kDx) {
-                const int rows = (int)(t.end - t.beg);
-                ro.begin(a + (t.beg * p.lda + first) * 2, p.lda * 2, rows, [&](int r) { return r < rows ? (int64_t)r : -1; });
-            } else {
-                ro.begin(a + t.beg * p.lda * 2, p.lda * 2, len, r0, p.n);
-            }
-            if constexpr (kPairs) {
-                const int n = p.n;                       // of every 128 rows 64 of each half
-                co.begin(w + wg * 2, p.ldw * 2, 2 * (int64_t)n, [&](int r) {
-                    const int col = c0 + r / 128 * 64 + r % 64;
-                    return col < n ? (int64_t)(r % 128 < 64 ? 0 : n) + col : -1;
-                });
-            } else if constexpr (MODE == kFwd) {
-                const int rows = p.n - c0 < C::BC ? p.n - c0 : C::BC;
-                co.begin(w + (wg + (int64_t)c0 * p.ldw) * 2, p.ldw * 2, rows, [&](int r) { return r < rows ? (int64_t)r : -1; });
-            } else if constexpr (MODE == kDx) {
-                co.begin(w + (wg + first * p.ldw) * 2, p.ldw * 2, len, c0, p.k);
-            } else {
-                co.begin(w + t.beg * p.ldb * 2, p.ldb * 2, len, c0, p.k);
-            }
-            const int ro_at = RowOp::lane(wr), co_at = ColOp::lane(wc);
-            const int stages = (len + kStage - 1) / kStage;
+        if (cur.len > 0) {
+            const int stages = (cur.len + kStage - 1) / kStage;
             struct Pieces { Frag<kSrcBf16> r[8], c[8]; } f0, f1;
             // Read q of a half's 16: the columns' pieces, all of which each row's products need, come first.
             auto read = [&](const char* rows, const char* cls, int q, int half, Pieces& f) __attribute__((always_inline)) {
@@ -197,29 +241,16 @@ template <int MODE, class End> __device__ __forceinline__ void wide_tiles(const 
                 asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
-                const int e0 = (s + 2) * kStage;         // (past the last stage: zeros)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    ro.load(j, rows, e0, len);
-                    co.load(j, cls, e0, len);
+                    cur.load(j, rows, cls, s + 2);       // (past the last stage: zeros)
 #pragma unroll
                     for (int q = 0; q < 3; ++q) read(next_rows, next_cls, j * 3 + q, 0, f0);
                     products(f1, j);
                 }
             };
-            // (the tile before has waited for its last loads, and its reads are done)
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                ro.load(i, row0, 0, len);
-                co.load(i, col0, 0, len);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                ro.load(i, row1, kStage, len);
-                co.load(i, col1, kStage, len);
-            }
-            asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+            // the first two stages are in, and what the tile before left to be stored is on its way
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
 #pragma unroll
@@ -231,24 +262,40 @@ template <int MODE, class End> __device__ __forceinline__ void wide_tiles(const 
             // nothing comes into LDS any more, and the last products' results stand before anything reads them
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_nop 15\n\ts_nop 15" ::: "memory");
         }
-        const bool busy = (MODE == kDw ? r0 + wr < p.n : t.beg + wr < t.end) && c0 + (kPairs ? wc / 2 : wc) < cols;
-        if (!busy) continue;
-        for_each<8>([&](auto which) __attribute__((always_inline)) {
-            constexpr int j = decltype(which)::value;
-            // one row's results leave the products' registers at a time
-            __builtin_amdgcn_sched_barrier(0);
-            asm volatile("" : "+a"(acc[0][j]), "+a"(acc[1][j]), "+a"(acc[2][j]), "+a"(acc[3][j]), "+a"(acc[4][j]),
-                              "+a"(acc[5][j]), "+a"(acc[6][j]), "+a"(acc[7][j]));
-            const int r = wr + j * 16 + (__lane_id() & 15);
-            f32x4 v[8];
+        __syncthreads();                                 // all waves have read the last stage
+        Tile_ next;
+        b += gridDim.x;
+        const bool more = next.find(p, b);
+        if (more) {
+            next.begin(p, s_rows[turn ^ 1]);
+            first_loads(next);
+        }
+        const bool busy = (MODE == kDw ? cur.r0 + wr < p.n : cur.t.beg + wr < cur.t.end) &&
+                          cur.c0 + (kPairs ? wc / 2 : wc) < cols;
+        if (busy) {
+            for_each<8>([&](auto which) __attribute__((always_inline)) {
+                constexpr int j = decltype(which)::value;
+                // one row's results leave the products' registers at a time
+                __builtin_amdgcn_sched_barrier(0);
+                asm volatile("" : "+a"(acc[0][j]), "+a"(acc[1][j]), "+a"(acc[2][j]), "+a"(acc[3][j]), "+a"(acc[4][j]),
+                                  "+a"(acc[5][j]), "+a"(acc[6][j]), "+a"(acc[7][j]));
+                const int r = wr + j * 16 + (__lane_id() & 15);
+                f32x4 v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = acc[i][j];
-            end(t, grouped, r0 + r, MODE != kDw ? (int64_t)s_row[MODE == kDw ? 0 : r] : (int64_t)(r0 + r < p.n ? r0 + r : -1),
-                c0 + (kPairs ? wc / 2 : wc), v);
-            __builtin_amdgcn_sched_barrier(0);
-        });
+                for (int i = 0; i < 8; ++i) v[i] = acc[i][j];
+                end(cur.t, cur.grouped, cur.r0 + r,
+                    MODE != kDw ? (int64_t)s_rows[turn][MODE == kDw ? 0 : r] : (int64_t)(cur.r0 + r < p.n ? cur.r0 + r : -1),
+                    cur.c0 + (kPairs ? wc / 2 : wc), v);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        }
+        if (!more) return;
+        cur = next;
     }
 }
+
+// Workgroups for `tiles` of about the same length: one a unit, which takes them in turn.
+inline unsigned wide_grid(int64_t tiles) { return grid_for(align_up((size_t)(tiles < 256 ? tiles : 256), kXcds), 1); }
 
 }  // namespace
 

@@ -165,7 +165,7 @@ htl_status wide_dx(const void* d, int64_t ldd, const void* w, int64_t ldw, int64
     if (m == 0) return HTL_OK;
     const ProdArgs p = {d, w, nullptr, order, offsets, m, ldd, 0, ldw, n, k, n_groups, 256, nullptr, 0, 0, true, true, splits};
     const DxEnd end = {dx, dx_dtype == HTL_F32, parts, add, m, k};
-    const dim3 grid(grid_for(align_up((size_t)((m / 256 + n_groups) * ceil_div(k, 256) * splits), kXcds), 1));
+    const dim3 grid(wide_grid((m / 256 + n_groups) * ceil_div(k, 256) * splits));
     hipLaunchKernelGGL(k_wide_dx, grid, dim3(Wide::kThreads), 0, stream, p, end);
     return check_launch("input gradients");
 }
@@ -198,7 +198,9 @@ htl_status wide_dw(const void* d, int64_t ldd, const void* x, int64_t ldx, int64
     const ProdArgs p = {d, x, nullptr, nullptr, offsets, m, ldd, ldx, 0, n, k, n_groups, r, nullptr, 0, split_chunks(m, n_groups, r), true};
     const DwEnd end = {dw, dw_dtype == HTL_F32, (float*)ws, n, k};
     const int64_t tiles = (m / r + n_groups + 1) * ceil_div(n, 256) * ceil_div(k, 256);
-    hipLaunchKernelGGL(k_wide_dw, dim3(grid_for(align_up((size_t)tiles, kXcds), 1)), dim3(Wide::kThreads), 0, stream, p, end);
+    // (groups differ in length: their tiles are dealt out as units come free)
+    const unsigned grid = n_groups == 1 ? wide_grid(tiles) : grid_for(align_up((size_t)tiles, kXcds), 1);
+    hipLaunchKernelGGL(k_wide_dw, dim3(grid), dim3(Wide::kThreads), 0, stream, p, end);
     const htl_status st = check_launch("weight gradients");
     if (st != HTL_OK) return st;
     return sum_chunks((const float*)ws, p.limit, dw, nullptr, offsets, n_groups, m, r, (int64_t)n * k, stream, dw_dtype == HTL_BF16);
