@@ -137,6 +137,92 @@ template <int T, int KS, class C, class End> __global__ __launch_bounds__(kFewTh
     few_tiles<T, KS, C>(p, end);
 }
 
+// Projections that fit in LDS (a feature table's block): a workgroup loads its
+// group's once, and its waves walk the chunk's rows, 32 at a time and without
+// waiting for each other, as product.hip's kernel for such matrices does.  LDS
+// holds for every 64 outputs (whole lines of y) their rows of z's and then of u's,
+// LP * 32 elements each, zeros beyond the matrix, 16 bytes apart so that 16 rows
+// read together hit different banks.  Bound: bytes.
+struct Resident {
+    static constexpr int TC = 8;
+};
+template <int LP, int BYTES>
+__global__ __launch_bounds__(512, 2) void k_gated_resident(ProdArgs p, GatedEnd<Resident> end) {
+    constexpr int kLd = LP * 64 + 16;
+    __shared__ __attribute__((aligned(16))) char lds[BYTES];
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int blocks = (p.n + 63) / 64;
+    for (int64_t b = blockIdx.x;; b += gridDim.x) {
+        TileAt t;
+        const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, 0, false, 1, b, t);
+        if (found < 0) return;
+        if (!found) continue;
+        const bool grouped = t.g < p.n_groups;
+        auto row_at = [&](int64_t pos) {
+            const int32_t row = pos < t.end ? (p.order ? p.order[pos] : (int32_t)pos) : -1;
+            return row >= 0 && row < p.m ? row : -1;
+        };
+        int64_t pos = t.beg + wv * 32;
+        int32_t row[2] = {row_at(pos + (lane & 15)), row_at(pos + 16 + (lane & 15))};
+        __syncthreads();                     // the matrix before is read
+        if (grouped) {
+            const char* w = (const char*)p.b + (int64_t)t.g * 2 * p.n * p.ldw * 2;
+#pragma unroll 4
+            for (int i = threadIdx.x; i < blocks * 128 * LP * 4; i += 512) {
+                const int c = i / (LP * 4), e = i % (LP * 4) * 8, col = c / 128 * 64 + c % 64;
+                const int64_t at = (int64_t)(c % 128 < 64 ? 0 : p.n) + col;
+                *(u32x4*)(lds + c * kLd + e * 2) = held_piece<2>(w + (at * p.ldw + e) * 2, col < p.n ? p.k - e : 0);
+            }
+        }
+        __syncthreads();
+        for (; pos < t.end; pos += 256) {
+            Frag<kSrcBf16> x[2][LP];
+#pragma unroll
+            for (int l = 0; l < LP; ++l)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int e = l * 32 + (lane >> 4) * 8;
+                    const char* at = (const char*)p.a + ((row[j] < 0 ? 0 : row[j]) * p.lda + e) * 2;
+                    if (p.k == LP * 32) {    // every piece whole; a row that is not there is read as the first
+                        load_at<2>(at, x[j][l].v);
+                    } else {
+                        const u32x4 v = held_piece<2>(at, p.k - e);
+                        __builtin_memcpy(&x[j][l].v, &v, 16);
+                    }
+                }
+            const int32_t next[2] = {row_at(pos + 256 + (lane & 15)), row_at(pos + 272 + (lane & 15))};
+            for (int nb = 0; nb < blocks; ++nb) {
+                f32x4 acc[2][8];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) acc[j][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                if (grouped) {
+#pragma unroll
+                    for (int l = 0; l < LP; ++l)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            Frag<kSrcBf16> c;
+                            c.v = *(const bf16x8*)(lds + (nb * 128 + q * 16 + (lane & 15)) * kLd + l * 64 + (lane >> 4) * 16);
+                            multiply(c, x[0][l], 0, acc[0][q]);
+                            multiply(c, x[1][l], 0, acc[1][q]);
+                        }
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) end(t, grouped, j * 16 + (lane & 15), row[j], nb * 64, acc[j]);
+            }
+            row[0] = next[0];
+            row[1] = next[1];
+        }
+    }
+}
+template <int LP> void launch_resident(ProdArgs p, int64_t bytes, const GatedEnd<Resident>& end, hipStream_t s) {
+    const int64_t chunks = p.m / p.rows + p.n_groups + 1;
+    const dim3 grid(grid_for(align_up((size_t)chunks, kXcds), 1));
+    if (bytes <= 81920) hipLaunchKernelGGL((k_gated_resident<LP, 81920>), grid, dim3(512), 0, s, p, end);
+    else hipLaunchKernelGGL((k_gated_resident<LP, 163840>), grid, dim3(512), 0, s, p, end);
+}
+
 template <int T, class C, bool ASYNC>
 void launch_gated(const ProdArgs& p, int64_t chunks, const GatedEnd<C>* fwd, const GatedBackEnd<C, T>* back, hipStream_t s) {
     const dim3 grid(grid_for(align_up((size_t)(chunks * ceil_div(p.n, C::BC / 2)), kXcds), 1));
@@ -191,6 +277,17 @@ void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s
     const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && p.ldw * es % 16 == 0 && (int64_t)p.k * es % 16 == 0 &&
                       aligned(p.b, 16) && p.m * p.lda * es <= kBufferBytes && 2 * (int64_t)p.n * p.ldw * es <= kBufferBytes;
     const int64_t each = p.m / p.n_groups;
+    const int lp = p.k <= 32 ? 1 : p.k <= 64 ? 2 : p.k <= 128 ? 4 : 8;
+    const int64_t bytes = ceil_div(p.n, 64) * 128 * (lp * 64 + 16);
+    if (!c.dy.p && dtype == HTL_BF16 && p.k <= 256 && bytes <= 163840 && each >= 512 && p.m >= 1 << 16) {
+        p.rows = (uint32_t)align_up((size_t)ceil_div(p.m, 1024), 256);
+        const GatedEnd<Resident> end = {p.n, c.act, c.y, c.y_f32, false, c.kept};
+        if (lp == 1) launch_resident<1>(p, bytes, end, s);
+        else if (lp == 2) launch_resident<2>(p, bytes, end, s);
+        else if (lp == 4) launch_resident<4>(p, bytes, end, s);
+        else launch_resident<8>(p, bytes, end, s);
+        return;
+    }
     if (p.packed || (p.k >= 256 && dtype == HTL_BF16 && fast && many(p.m, p.n_groups, ceil_div(p.m, 256) * ceil_div(p.n, 128)))) {
         p.rows = 256;
         p.no_rest = true;

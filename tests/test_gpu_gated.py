@@ -233,3 +233,19 @@ def test_graph_and_streams(htl):
     side.synchronize()
     for a, b in ((s_y, e_y), (s_dx, e_dx), (s_dw, e_dw)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("m,n,k,g", [(70000, 256, 128, 26), (66000, 40, 31, 3), (65536, 33, 64, 1), (68000, 72, 200, 5)])
+def test_many_rows_of_small_blocks(htl, m, n, k, g):
+    """Projections that stay in LDS: every 37th row against its own, and those of no group."""
+    ids = _ids(np.random.default_rng(m), m, g, "dropped" if g > 1 else "one")
+    x, w, dy = _data(m, n, k, g, torch.bfloat16)
+    groups = htl.group_rows(torch.from_numpy(ids).cuda(), g)
+    y, kept = htl.gated_mm(x.cuda(), w.cuda(), groups, act="sigmoid", keep=True)
+    some = torch.arange(0, m, 37)
+    want = Want(x[some], w, dy[some], ids[some.numpy()], "sigmoid", False)
+    _close(y[some], want.y, want.ty, "y")
+    _close(kept[some], want.kept, want.tkept, "kept")
+    dx, dw = htl.gated_mm_backward(dy.cuda(), x.cuda(), w.cuda(), kept, groups, act="sigmoid")
+    want = Want(x[some], w, dy[some], ids[some.numpy()], "sigmoid", True)
+    _close(dx[some], want.dx, want.tdx, "dx")
