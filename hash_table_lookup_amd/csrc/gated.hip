@@ -81,7 +81,8 @@ template <class C, int T> struct GatedBackEnd {
                 v[F + i][e] = g[e] * a;
             }
         }
-        const int64_t to = row < 0 || !packed ? row : t.beg + r;
+        // (a position that names no row has zeros: sums over positions read it)
+        const int64_t to = !packed ? row : t.beg + r < t.end ? t.beg + r : -1;
         store_rows<F>(d, T == kSrcF32, to, ld, col, n, v);
         store_rows<F>((char*)d + n * (T == kSrcF32 ? 4ll : 2ll), T == kSrcF32, to, ld, col, n, v + F);
     }
@@ -112,11 +113,13 @@ __global__ __launch_bounds__(256) void k_gated_slopes(RowsIn dy, RowsIn kept, Ro
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
         const int64_t to = i / each, row = order ? (int64_t)order[to] : to;
         const int col = (int)(i - to * each) * 8;
-        if (row < 0 || row >= m) continue;
+        const bool in = row >= 0 && row < m;             // (a position that names no row: zeros)
+        const int have = in ? n : 0;
+        const int64_t from = in ? row : 0;
         Raw8<T> rg, rz, ru;
-        load8(dy, row, col, n, rg);
-        load8(kept, row, col, n, rz);
-        load8(up, row, col, n, ru);
+        load8(dy, from, col, have, rg);
+        load8(kept, from, col, have, rz);
+        load8(up, from, col, have, ru);
         float g[8], z[8], u[8];
         unpack8(dy, rg, g);
         unpack8(kept, rz, z);

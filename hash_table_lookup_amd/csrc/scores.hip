@@ -127,7 +127,7 @@ template <class C> struct SlopeEnd {
         }
 #pragma unroll
         for (int i = 0; i < C::TC; ++i) v[i] *= g;
-        store_rows<C::TC>(d, f32, row < 0 || !packed ? row : t.beg + r, ld, col, cols, v);
+        store_rows<C::TC>(d, f32, !packed ? row : t.beg + r < t.end ? t.beg + r : -1, ld, col, cols, v);
     }
 };
 
@@ -151,6 +151,7 @@ __device__ __forceinline__ Best row_best(const Best* partial, int blocks, int64_
     for (int i = threadIdx.x; i < blocks; i += 256) b = join(b, partial[(int64_t)i * m + row]);
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) b = join(b, {__shfl_xor(b.top, off), __shfl_xor(b.sum, off)});
+    __syncthreads();                                     // (the row before is read)
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = b;
     __syncthreads();
     return join(join(s[0], s[1]), join(s[2], s[3]));
@@ -175,20 +176,23 @@ __global__ __launch_bounds__(256) void k_softmax_finish16(const Best* __restrict
                                                           float* __restrict__ loss, float* __restrict__ lse) {
     __shared__ Best s[16][16];
     const int r = threadIdx.x & 15, part = threadIdx.x >> 4;
-    const int64_t row = blockIdx.x * 16ll + r;
-    const bool on = row < m && targets.at(row) >= 0;
-    Best b = {-INFINITY, 0.0f};
-    if (on) {
+    for (int64_t row0 = blockIdx.x * 16ll; row0 < m; row0 += gridDim.x * 16ll) {
+        const int64_t row = row0 + r;
+        const bool on = row < m && targets.at(row) >= 0;
+        Best b = {-INFINITY, 0.0f};
+        if (on) {
 #pragma unroll 4
-        for (int i = part; i < blocks; i += 16) b = join(b, partial[(int64_t)i * m + row]);
+            for (int i = part; i < blocks; i += 16) b = join(b, partial[(int64_t)i * m + row]);
+        }
+        __syncthreads();                                 // the rows before are read
+        s[part][r] = b;
+        __syncthreads();
+        if (part || row >= m) continue;
+        for (int i = 1; i < 16; ++i) b = join(b, s[i][r]);
+        const float l = on ? lse_of(b) : 0.0f;
+        lse[row] = l;
+        loss[row] = on ? l - target_score[row] : 0.0f;
     }
-    s[part][r] = b;
-    __syncthreads();
-    if (part || row >= m) return;
-    for (int i = 1; i < 16; ++i) b = join(b, s[i][r]);
-    const float l = on ? lse_of(b) : 0.0f;
-    lse[row] = l;
-    loss[row] = on ? l - target_score[row] : 0.0f;
 }
 
 // A wave's dot products of row i with two rows, the same in every lane.
@@ -255,40 +259,42 @@ __global__ __launch_bounds__(256) void k_distill_finish(RowsIn x, RowsIn w, int 
                                                         float* __restrict__ loss, float* __restrict__ lse) {
     __shared__ Best s[4];
     __shared__ float s_score[HTL_MAX_TOP];
-    const int64_t row = blockIdx.x;
-    float all;
-    const bool on = teacher_sum(t, row, all);            // (every wave finds the same)
-    for (int j = (threadIdx.x >> 6) * 2; j < t.top; j += 8) {
-        const int v[2] = {t.items.at(row * t.top + j), j + 1 < t.top ? t.items.at(row * t.top + j + 1) : -1};
-        float d[2] = {0.0f, 0.0f};
-        if (on && (v[0] >= 0 || v[1] >= 0)) {
-            const int64_t at[2] = {v[0] < 0 ? v[1] : v[0], v[1] < 0 ? v[0] : v[1]};
-            row_dots<T>(x, row, w, at, k, d);
+    for (int64_t row = blockIdx.x; row < m; row += gridDim.x) {
+        float all;
+        const bool on = teacher_sum(t, row, all);        // (every wave finds the same)
+        __syncthreads();                                 // the scores before are read
+        for (int j = (threadIdx.x >> 6) * 2; j < t.top; j += 8) {
+            const int v[2] = {t.items.at(row * t.top + j), j + 1 < t.top ? t.items.at(row * t.top + j + 1) : -1};
+            float d[2] = {0.0f, 0.0f};
+            if (on && (v[0] >= 0 || v[1] >= 0)) {
+                const int64_t at[2] = {v[0] < 0 ? v[1] : v[0], v[1] < 0 ? v[0] : v[1]};
+                row_dots<T>(x, row, w, at, k, d);
+            }
+            if (__lane_id() < 2 && j + __lane_id() < t.top) {
+                const float dot = __lane_id() ? d[1] : d[0];
+                const float score = (__lane_id() ? v[1] : v[0]) < 0 ? 0.0f : dot * t.scale;
+                scores[row * t.top + j + __lane_id()] = score;
+                s_score[j + __lane_id()] = score;
+            }
         }
-        if (__lane_id() < 2 && j + __lane_id() < t.top) {
-            const float d_ = __lane_id() ? d[1] : d[0];
-            const float score = (__lane_id() ? v[1] : v[0]) < 0 ? 0.0f : d_ * t.scale;
-            scores[row * t.top + j + __lane_id()] = score;
-            s_score[j + __lane_id()] = score;
+        if (!on) {
+            if (threadIdx.x == 0) loss[row] = lse[row] = 0.0f;
+            continue;
         }
-    }
-    if (!on) {
-        if (threadIdx.x == 0) loss[row] = lse[row] = 0.0f;
-        return;
-    }
-    const float l = lse_of(row_best(partial, blocks, m, row, s));
-    if (threadIdx.x >= 64) return;
-    float sum = 0.0f;
-    for (int j = threadIdx.x; j < t.top; j += 64) {
-        const float logp = t.logit(row, j) - all;
-        if (logp > -INFINITY || logp != logp)            // an entry of share 0 adds nothing
-            sum += __builtin_amdgcn_exp2f(logp) * (logp * kLn2 + (l - s_score[j]));
-    }
+        const float l = lse_of(row_best(partial, blocks, m, row, s));
+        if (threadIdx.x >= 64) continue;
+        float sum = 0.0f;
+        for (int j = threadIdx.x; j < t.top; j += 64) {
+            const float logp = t.logit(row, j) - all;
+            if (logp > -INFINITY || logp != logp)        // an entry of share 0 adds nothing
+                sum += __builtin_amdgcn_exp2f(logp) * (logp * kLn2 + (l - s_score[j]));
+        }
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
-    if (threadIdx.x) return;
-    loss[row] = sum;
-    lse[row] = l;
+        for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
+        if (threadIdx.x) continue;
+        loss[row] = sum;
+        lse[row] = l;
+    }
 }
 
 // Which rows take part (0, or -1: none), and, of a teacher's entries, d: an
@@ -299,40 +305,40 @@ __global__ __launch_bounds__(256) void k_active(int64_t m, Items targets, int32_
 __global__ __launch_bounds__(256) void k_teach(int64_t m, Teacher t, const float* __restrict__ scores,
                                                const float* __restrict__ lse, const float* __restrict__ dloss,
                                                int32_t* __restrict__ ids, float* __restrict__ d) {
-    const int64_t row = blockIdx.x * 4ll + (threadIdx.x >> 6);
-    if (row >= m) return;
-    float all;
-    const bool on = teacher_sum(t, row, all);
-    if (__lane_id() == 0) ids[row] = on ? 0 : -1;
-    if (!on) return;
-    const float g = dloss[row] * t.scale, l = lse[row];
-    for (int j0 = 0; j0 < t.top; j0 += 64) {
-        const int j = j0 + __lane_id();
-        const int item = j < t.top ? t.items.at(row * t.top + j) : -1;
-        float share = 0.0f;
-        for (int i0 = 0; i0 < t.top; i0 += 64) {
-            const int i = i0 + __lane_id();
-            const int other = i < t.top ? t.items.at(row * t.top + i) : -1;
-            const float p = other >= 0 ? __builtin_amdgcn_exp2f(t.logit(row, i) - all) : 0.0f;
-            const int count = t.top - i0 < 64 ? t.top - i0 : 64;
-            for (int n = 0; n < count; ++n) {
-                const int it = __shfl(other, n);
-                const float pn = __shfl(p, n);
-                if (it == item) share += pn;
+    for (int64_t row = blockIdx.x * 4ll + (threadIdx.x >> 6); row < m; row += gridDim.x * 4ll) {
+        float all;
+        const bool on = teacher_sum(t, row, all);
+        if (__lane_id() == 0) ids[row] = on ? 0 : -1;
+        if (!on) continue;
+        const float g = dloss[row] * t.scale, l = lse[row];
+        for (int j0 = 0; j0 < t.top; j0 += 64) {
+            const int j = j0 + __lane_id();
+            const int item = j < t.top ? t.items.at(row * t.top + j) : -1;
+            float share = 0.0f;
+            for (int i0 = 0; i0 < t.top; i0 += 64) {
+                const int i = i0 + __lane_id();
+                const int other = i < t.top ? t.items.at(row * t.top + i) : -1;
+                const float p = other >= 0 ? __builtin_amdgcn_exp2f(t.logit(row, i) - all) : 0.0f;
+                const int count = t.top - i0 < 64 ? t.top - i0 : 64;
+                for (int n = 0; n < count; ++n) {
+                    const int it = __shfl(other, n);
+                    const float pn = __shfl(p, n);
+                    if (it == item) share += pn;
+                }
             }
+            if (item >= 0)
+                d[row * t.top + j] = (__builtin_amdgcn_exp2f((scores[row * t.top + j] - l) * kLog2e) - share) * g;
         }
-        if (item >= 0)
-            d[row * t.top + j] = (__builtin_amdgcn_exp2f((scores[row * t.top + j] - l) * kLog2e) - share) * g;
     }
 }
 // Which rows a teacher has entries for.
 __global__ __launch_bounds__(256) void k_taught(int64_t m, Teacher t, int32_t* __restrict__ ids) {
-    const int64_t row = blockIdx.x * 4ll + (threadIdx.x >> 6);
-    if (row >= m) return;
-    bool on = false;
-    for (int j = __lane_id(); j < t.top; j += 64) on |= t.logit(row, j) != -INFINITY;
-    const bool any = __ballot(on) != 0;
-    if (__lane_id() == 0) ids[row] = any ? 0 : -1;
+    for (int64_t row = blockIdx.x * 4ll + (threadIdx.x >> 6); row < m; row += gridDim.x * 4ll) {
+        bool on = false;
+        for (int j = __lane_id(); j < t.top; j += 64) on |= t.logit(row, j) != -INFINITY;
+        const bool any = __ballot(on) != 0;
+        if (__lane_id() == 0) ids[row] = any ? 0 : -1;
+    }
 }
 // Puts the teacher's entries of a piece of the vocabulary into d, of which rows
 // lie by row or (packed) by position.
@@ -446,9 +452,13 @@ struct Carve {               // a workspace cut into 256-byte aligned parts
 // where theirs do not: loads then go straight to LDS.
 bool copied_of(int64_t m, int k, htl_dtype dtype) { return m > kFewRows && k % (dtype == HTL_F32 ? 4 : 8); }
 
-// Items whose copied matrix rows are held at a time.
-constexpr int kPackCols = 65536;
-int pack_cols(int vocab) { return vocab < kPackCols ? vocab : kPackCols; }
+// Items whose copied matrix rows are held at a time (128 MiB), and of a piece at most.
+constexpr int kMostCols = 65536;
+int pack_cols(int vocab, int k, htl_dtype dtype) {
+    int64_t c = (128ll << 20) / (packed_ld(k) * elem(dtype)) / 256 * 256;
+    c = c < 256 ? 256 : c > kMostCols ? kMostCols : c;
+    return (int)(c < vocab ? c : vocab);
+}
 
 struct ForwardSpace {
     bool wide, copied;
@@ -471,7 +481,7 @@ struct ForwardSpace {
         groups = c.take<char>(group_bytes);
         copied = copied_of(m, k, dtype);
         x = c.take<char>(wide || copied ? m * spread_ld(k) * elem(dtype) : 0);
-        w = c.take<char>(wide || copied ? pack_cols(vocab) * packed_ld(k) * elem(dtype) : 0);
+        w = c.take<char>(wide || copied ? pack_cols(vocab, k, dtype) * packed_ld(k) * elem(dtype) : 0);
         bytes = c.at;
     }
 };
@@ -484,7 +494,7 @@ struct ForwardSpace {
 int piece_cols(int64_t m, int vocab, int k, htl_dtype dtype) {
     int64_t c = ((k < 1024 ? 512ll : 256ll) << 20) / (elem(dtype) * (m < 1 ? 1 : m)) / 256 * 256;
     if (c < 256) c = 256;
-    if (c > kPackCols) c = kPackCols;
+    if (c > kMostCols) c = kMostCols;
     return (int)(c < vocab ? c : vocab);
 }
 
@@ -555,7 +565,7 @@ htl_status forward_scores(const Rows2& r, float scale, const ForwardSpace& s, co
         if (st != HTL_OK) return st;
         const bool as_is = packed_as_is(r.x, r.ldx, r.k) && r.m * r.ldx * 2 <= kBufferBytes;
         if (!as_is) st = pack_rows(r.x, r.ldx, r.dtype, s.order, r.m, r.m, r.k, s.x, spread_ld(r.k), stream);
-        const int most = packed_as_is(r.w, r.ldw, r.k) && kPackCols * r.ldw * 2 <= kBufferBytes ? most_cols(r) : kPackCols;
+        const int most = packed_as_is(r.w, r.ldw, r.k) && 256 * r.ldw * 2 <= kBufferBytes ? most_cols(r) : pack_cols(r.vocab, r.k, r.dtype);
         for (int v0 = 0; v0 < r.vocab && st == HTL_OK;) {
             const int cols = r.vocab - v0 < most ? r.vocab - v0 : most;
             const void* w;
@@ -578,7 +588,7 @@ htl_status forward_scores(const Rows2& r, float scale, const ForwardSpace& s, co
         t.ldx = spread_ld(r.k);
         t.k = (int)packed_ld(r.k);
     }
-    const int step = s.copied ? pack_cols(r.vocab) : most_cols(r);
+    const int step = s.copied ? pack_cols(r.vocab, r.k, r.dtype) : most_cols(r);
     for (int v0 = 0; v0 < r.vocab && st == HTL_OK;) {
         const int cols = r.vocab - v0 < step ? r.vocab - v0 : step;
         if (s.copied) st = piece_of(r, v0, cols, s.w, t.w, t.ldw, stream);
@@ -676,7 +686,7 @@ using namespace htl;
     HTL_REQUIRE(k >= 1 && k <= HTL_MAX_PRODUCT_DIM, name ": k out of range");                                \
     HTL_REQUIRE(known(dtype), name ": dtype must be HTL_F32 or HTL_BF16");                                   \
     HTL_REQUIRE(ldx >= k && ldw >= k, name ": row stride below k");                                          \
-    HTL_REQUIRE(temperature > 0.0f && temperature <= 3.0e38f, name ": temperature must be positive and finite"); \
+    HTL_REQUIRE(temperature >= 1.0e-30f && temperature <= 1.0e30f, name ": temperature out of range");       \
     HTL_REQUIRE(index_bits == 32 || index_bits == 64, name ": indices have 32 or 64 bits")
 #define SCORE_POINTERS(name, index)                                                                          \
     HTL_REQUIRE(w && (m == 0 || (x && index)), name ": null pointer");                                       \
@@ -709,7 +719,7 @@ extern "C" htl_status softmax_loss(const void* x, int64_t ldx, const void* w, in
     if (m < 2048)
         hipLaunchKernelGGL(k_softmax_finish, dim3((unsigned)m), dim3(256), 0, stream, s.partial, blocks, m, t, s.target_score, loss, lse);
     else
-        hipLaunchKernelGGL(k_softmax_finish16, dim3((unsigned)ceil_div(m, 16)), dim3(256), 0, stream, s.partial, blocks, m, t,
+        hipLaunchKernelGGL(k_softmax_finish16, dim3(grid_for(m, 16)), dim3(256), 0, stream, s.partial, blocks, m, t,
                            s.target_score, loss, lse);
     return check_launch("softmax_loss");
 }
@@ -762,11 +772,11 @@ extern "C" htl_status distill_loss(const void* x, int64_t ldx, const void* w, in
     const Teacher t = {{items, index_bits == 64, vocab}, logits, ld_logits, logits_dtype == HTL_F32, top, scale};
     const ForwardSpace s(ws, m, vocab, k, dtype);
     int blocks;
-    if (s.wide) hipLaunchKernelGGL(k_taught, dim3((unsigned)ceil_div(m, 4)), dim3(256), 0, stream, m, t, s.ids);
+    if (s.wide) hipLaunchKernelGGL(k_taught, dim3(grid_for(m, 4)), dim3(256), 0, stream, m, t, s.ids);
     const htl_status st = forward_scores(r, scale, s, Items{nullptr, false, vocab}, blocks, stream);
     if (st != HTL_OK) return st;
     const RowsIn xr = {x, nullptr, ldx, 0}, wr = {w, nullptr, ldw, 0};
-    const dim3 grid((unsigned)m);
+    const dim3 grid(grid_for(m, 1));
     if (dtype == HTL_F32)
         hipLaunchKernelGGL(k_distill_finish<kSrcF32>, grid, dim3(256), 0, stream, xr, wr, k, s.partial, blocks, m, t, scores, loss, lse);
     else
@@ -797,6 +807,6 @@ extern "C" htl_status distill_loss_backward(const float* dloss, const void* x, i
     const Teacher t = {{items, index_bits == 64, vocab}, logits, ld_logits, logits_dtype == HTL_F32, top, scale};
     const BackwardSpace s(ws, m, vocab, k, top, dtype);
     if (m > 0)
-        hipLaunchKernelGGL(k_teach, dim3((unsigned)ceil_div(m, 4)), dim3(256), 0, stream, m, t, scores, lse, dloss, s.ids, s.entries);
+        hipLaunchKernelGGL(k_teach, dim3(grid_for(m, 4)), dim3(256), 0, stream, m, t, scores, lse, dloss, s.ids, s.entries);
     return backward_pieces(r, scale, s, Items{nullptr, false, vocab}, t.items, top, lse, dloss, dx, dx_dtype, dw, stream);
 }

@@ -255,6 +255,9 @@ template <int MODE, class End> __device__ __forceinline__ void wide_tiles(const 
             asm volatile("" ::: "memory");
 #pragma unroll
             for (int q = 0; q < 16; ++q) read(row0, col0, q, 0, f0);
+            // (a product's source stands two instructions after a vector instruction has written it: the zeros above)
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_nop 3");
             for (int s = 0; s < stages; s += 2) {        // an odd number is filled up with zeros
                 stage(row0, col0, row1, col1, s);
                 stage(row1, col1, row0, col0, s + 1);

@@ -9,7 +9,6 @@ has loss and gradients of zero, whatever it holds.
 """
 from __future__ import annotations
 
-import math
 from typing import Tuple
 
 import torch
@@ -49,8 +48,8 @@ def _floats(t: torch.Tensor, shape, name: str) -> torch.Tensor:
 
 def _heat(temperature: float) -> float:
     temperature = float(temperature)
-    if not 0.0 < temperature < math.inf:
-        raise ValueError(f"temperature must be positive and finite, got {temperature}")
+    if not 1e-30 <= temperature <= 1e30:
+        raise ValueError(f"temperature must be in [1e-30, 1e30], got {temperature}")
     return temperature
 
 

@@ -722,15 +722,17 @@ htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const void* x, int64
 /* ------------------------------------------- losses over a vocabulary --
  * The head of a model over an embedding lookup scores a row against every row
  * of a vocabulary (the items that can follow): s[i][v] = x[i] . w[v] / T.  The
- * calls below never hold the scores of all rows with all items: memory beside
- * the operands is bounded by pieces of the vocabulary (about 512 MiB), and the
- * backward pass computes the scores again.
+ * calls below never hold the scores of all rows with all items.  The forward
+ * pass keeps 8 bytes a row for every 32 to 128 items; the backward pass computes
+ * the scores again, a piece of the vocabulary at a time, and holds their
+ * gradients for one piece (at most 512 MiB, or 256 items) and dx in fp32 parts
+ * (at most 256 MiB, or one).
  *
  * Shared by both losses:
  *   x          dtype[m][k], w dtype[vocab][k] with row strides ldx, ldw >= k;
  *              1 <= vocab <= HTL_MAX_VOCAB, 1 <= k <= HTL_MAX_PRODUCT_DIM.
  *   indices    of index_bits 32 or 64; one outside [0, vocab) is none.
- *   temperature  T, positive and finite.
+ *   temperature  T, 1e-30 to 1e30.
  *   loss, lse  float[m] out: the loss, and log sum_v exp(s[i][v]), which the
  *              backward pass takes; both 0 for a row without a target.
  *   dloss      float[m]: the gradient of each row's loss.

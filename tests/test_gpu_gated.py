@@ -249,3 +249,63 @@ def test_many_rows_of_small_blocks(htl, m, n, k, g):
     dx, dw = htl.gated_mm_backward(dy.cuda(), x.cuda(), w.cuda(), kept, groups, act="sigmoid")
     want = Want(x[some], w, dy[some], ids[some.numpy()], "sigmoid", True)
     _close(dx[some], want.dx, want.tdx, "dx")
+
+
+def test_wide_graph_and_repeats(htl):
+    """Calls in the largest tiles: repeated, captured and replayed, the same to the bit."""
+    m, n, k, g = 2100, 1040, 300, 3
+    ids = _ids(np.random.default_rng(4), m, g, "dropped")
+    x, w, dy = (t.cuda() for t in _data(m, n, k, g, torch.bfloat16))
+    groups = htl.group_rows(torch.from_numpy(ids).cuda(), g)
+
+    def step():
+        y, kept = htl.gated_mm(x, w, groups, keep=True)
+        return (y, kept, *htl.gated_mm_backward(dy, x, w, kept, groups), *htl.gated_mm_backward(dy, x, w, None, groups))
+    first = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for seed in range(3):
+        for a, b in zip((x, w, dy), _data(m, n, k, g, torch.bfloat16, seed)):
+            a.copy_(b)
+        graph.replay()
+        eager = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, eager))
+        if seed == 0:
+            assert all(torch.equal(a, b) for a, b in zip(first, eager))
+
+
+@pytest.mark.parametrize("m,n,k", [(40, 16, 24), (2048, 1024, 304)])
+@pytest.mark.parametrize("keep", [False, True])
+def test_broken_plans(htl, m, n, k, keep):
+    """A plan whose order names rows that are not there reads and writes nothing outside, and the others are right."""
+    x, w, dy = _data(m, n, k, 1, torch.bfloat16)
+    order = torch.arange(m, dtype=torch.int32)
+    gone = torch.arange(m) % 7 == 3
+    bad = order.clone()
+    bad[gone] = torch.where(torch.arange(int(gone.sum())) % 2 == 0, -5, m + 9).to(torch.int32)
+    plan = htl.RowGroups(torch.zeros(m, dtype=torch.int32).cuda(), bad.cuda(), torch.tensor([0, m], dtype=torch.int32).cuda(), 1)
+    ids = np.where(gone.numpy(), -1, 0).astype(np.int32)
+    want = Want(x, w, dy, ids, "silu", keep)
+    xc, wc, dc = x.cuda(), w.cuda(), dy.cuda()
+    y, kept = htl.gated_mm(xc, wc, plan, keep=keep)
+    _close(y[~gone], want.y[~gone], want.ty[~gone], "y")
+    dx, dw = htl.gated_mm_backward(dc, xc, wc, kept, plan)
+    _close(dx[~gone], want.dx[~gone], want.tdx[~gone], "dx")
+    _close(dw, want.dw, want.tdw, "dw")
+
+
+@pytest.mark.parametrize("m,n,k", [(40, 24, 32), (300, 40, 48), (2100, 1024, 304)])
+def test_matrix_at_any_alignment(htl, m, n, k):
+    x, w, dy = _data(m, n, k, 1, torch.bfloat16)
+    flat = torch.zeros(w.numel() + 1, dtype=torch.bfloat16)
+    flat[1:] = w.view(-1)
+    loose = flat.cuda()[1:].view(1, 2 * n, k)
+    want = Want(x, w, dy, np.zeros(m, dtype=np.int32), "silu", False)
+    y, _ = htl.gated_mm(x.cuda(), loose)
+    _close(y, want.y, want.ty, "y")
+    dx, dw = htl.gated_mm_backward(dy.cuda(), x.cuda(), loose)
+    _close(dx, want.dx, want.tdx, "dx")
+    _close(dw, want.dw, want.tdw, "dw")

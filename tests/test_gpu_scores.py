@@ -345,3 +345,108 @@ def test_block_and_head(htl):
     for got, p in zip((dx, dwg, dwo, dw), a):
         got = got.cpu().double().reshape(p.grad.shape)
         assert float((got - p.grad).norm()) <= 8 * 2.0 ** -8 * float(p.grad.norm())
+
+
+def test_wide_graph_and_repeats(htl):
+    """Both losses in the largest tiles, dx in parts: repeated, captured and replayed, the same to the bit."""
+    m, v, k, t = 1030, 16400, 520, 9
+    x, w, targets, dloss = (a.cuda() for a in _data(m, v, k, torch.bfloat16))
+    gen = torch.Generator().manual_seed(1)
+    items, logits = torch.randint(0, v, (m, t), generator=gen).cuda(), torch.randn(m, t, generator=gen).cuda()
+
+    def step():
+        loss, lse = htl.softmax_loss(x, w, targets)
+        l2, kept = htl.distill_loss(x, w, items, logits)
+        return (loss, lse, *htl.softmax_loss_backward(dloss, x, w, targets, lse), l2,
+                *htl.distill_loss_backward(dloss, x, w, items, logits, kept))
+    first = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for seed in range(3):
+        for a, b in zip((x, w, targets, dloss), _data(m, v, k, torch.bfloat16, seed)):
+            a.copy_(b)
+        graph.replay()
+        eager = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, eager))
+        if seed == 0:
+            assert all(torch.equal(a, b) for a, b in zip(first, eager))
+
+
+def test_two_streams_at_once(htl):
+    """The same calls on two streams, which overlap: each has a workspace of its own."""
+    data = [[a.cuda() for a in _data(500, 4000, 136, torch.bfloat16, s)] for s in range(2)]
+
+    def step(x, w, targets, dloss):
+        loss, lse = htl.softmax_loss(x, w, targets)
+        return (loss, *htl.softmax_loss_backward(dloss, x, w, targets, lse))
+    want = [step(*d) for d in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in data]
+    got = []
+    for _ in range(4):
+        got = []
+        for s, d in zip(streams, data):
+            with torch.cuda.stream(s):
+                got.append(step(*d))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("m", [5, 60, 300])
+def test_vocabulary_past_4_gib(htl, m):
+    """Matrices of more than 4 GiB: offsets past 32 bits, in each kind of tile; every thousandth item's gradient too."""
+    v, k = 1_100_003, 2048
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    x = torch.randn(m, k, device="cuda", generator=gen).bfloat16()
+    w = torch.empty(v, k, device="cuda", dtype=torch.bfloat16)
+    for a in range(0, v, 100_000):
+        w[a:a + 100_000] = (torch.randn(min(100_000, v - a), k, device="cuda", generator=gen) * 0.03).bfloat16()
+    targets = torch.randint(0, v, (m,), device="cuda", generator=gen)
+    targets[0] = v - 1
+    dloss = torch.full((m,), 1.0 / m, device="cuda")
+    loss, lse = htl.softmax_loss(x, w, targets)
+    dx, dw = htl.softmax_loss_backward(dloss, x, w, targets, lse)
+    x8 = x.double()
+    s = torch.cat([torch.mm(x8, w[a:a + 50_000].double().t().contiguous()) for a in range(0, v, 50_000)], 1)
+    want = torch.logsumexp(s, 1)
+    # (terms and bounds as at the top: |x| |w| sums to less than 40 a score, scores are below 12)
+    r = (k + 6) * U * 40 + (8 * 12 + v + 64 + 2 * 20) * U
+    assert float((lse.double() - want).abs().max()) <= r
+    assert float((loss.double() - (want - s.gather(1, targets[:, None])[:, 0])).abs().max()) <= 2 * r
+    d = torch.exp(s - want[:, None])
+    d[torch.arange(m, device="cuda"), targets] -= 1.0
+    d /= m
+    some = torch.cat([torch.arange(0, v, 1000, device="cuda"), targets])
+    dw8 = torch.mm(d[:, some].t().contiguous(), x8)
+    ed = d.abs() * (2 * r + 2.0 ** -8 * 1.1)
+    tol = torch.mm(ed[:, some].t().contiguous(), x8.abs()) * 1.01 + 2.0 ** -8 * 1.01 * dw8.abs()
+    assert bool(((dw[some].double() - dw8).abs() <= tol).all())
+    # dx by norm: every term of it is off by its share of 2^-8, of either sign, and the result by a rounding
+    dx8 = sum(torch.mm(d[:, a:a + 50_000].contiguous(), w[a:a + 50_000].double()) for a in range(0, v, 50_000))
+    assert float((dx.double() - dx8).norm()) <= 2 * 2.0 ** -8 * float(dx8.norm())
+
+
+@pytest.mark.parametrize("pad,first", [(9, 1), (8, 8), (8, 1)])
+def test_wide_strides(htl, pad, first):
+    """Rows of larger matrices, at any alignment, in the largest tiles."""
+    m, v, k = 1100, 14500, 512
+    x, w, targets, dloss = _data(m, v, k, torch.bfloat16)
+    targets[targets >= v] = -1
+    wide, wide_w = torch.full((m, k + pad + 1), float("nan")).bfloat16(), torch.full((v, k + pad), float("nan")).bfloat16()
+    wide[:, first:k + first], wide_w[:, first % pad:k + first % pad] = x, w
+    xs, ws = wide.cuda()[:, first:k + first], wide_w.cuda()[:, first % pad:k + first % pad]
+    loss, lse = htl.softmax_loss(xs, ws, targets.cuda())
+    dx, dw = htl.softmax_loss_backward(dloss.cuda(), xs, ws, targets.cuda(), lse)
+    xc, wc = x.cuda(), w.cuda()
+    want, want_lse = htl.softmax_loss(xc, wc, targets.cuda())
+    assert torch.equal(loss, want) and torch.equal(lse, want_lse)
+    for a, b in zip((dx, dw), htl.softmax_loss_backward(dloss.cuda(), xc, wc, targets.cuda(), lse)):
+        assert torch.equal(a, b)
+    rows = torch.randint(0, m, (40,), generator=torch.Generator().manual_seed(1))
+    some = Want(x[rows], w, targets[rows][:, None], torch.zeros(40, 1).double(), 1.0, dloss[rows])
+    _close(loss[rows], some.loss, some.tloss, "loss")
+    _close(dx[rows], some.dx, some.tdx, "dx")
