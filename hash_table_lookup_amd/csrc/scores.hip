@@ -369,11 +369,16 @@ struct Rows2 {               // x and w as the calls have them
 // The product x w^T of `cols` items (r.w: the first one's row), with an end made
 // by `make` for the tile's shape.  Tiles by size, as the plain products' (product.hip).
 constexpr int64_t kFewRows = 48;
+// Tiles of 32 rows rather than 128: for few rows, and where those of 128 would
+// leave units idle (2,838 fp32 rows of 1,115 against 893: 161 of them).
+bool narrow_of(int64_t m, int vocab, htl_dtype dtype) {
+    return m <= kFewRows || ceil_div(m, 32) * ceil_div(vocab, 128) <= (dtype == HTL_F32 ? 1024 : 512);
+}
 int tile_of(const Rows2& r, int64_t cols, bool& fast) {
     const int es = elem(r.dtype);
     fast = r.ldx * es % 16 == 0 && r.ldw * es % 16 == 0 && (int64_t)r.k * es % 16 == 0 && aligned(r.x, 16) &&
            aligned(r.w, 16) && r.m * r.ldx * es <= kBufferBytes && cols * r.ldw * es <= kBufferBytes;
-    return r.m <= kFewRows ? 32 : 128;
+    return narrow_of(r.m, r.vocab, r.dtype) ? 32 : 128;
 }
 // Whether wide.h's tiles fill the device.
 // Scores of rows shorter than this run as well or better in tiles of 128, of which
@@ -385,7 +390,9 @@ bool wide_of(int64_t m, int vocab, htl_dtype dtype) {
     return dtype == HTL_BF16 && m >= 256 && ceil_div(m, 256) * ceil_div(vocab, 256) >= 224;
 }
 // A wave's columns: those of a block of partial sums.
-int wave_cols(int64_t m, bool wide) { return wide ? Wide::TC * 16 : m <= kFewRows ? Small::TC * 16 : Mid::TC * 16; }
+int wave_cols(int64_t m, int vocab, htl_dtype dtype, bool wide) {
+    return wide ? Wide::TC * 16 : narrow_of(m, vocab, dtype) ? Small::TC * 16 : Mid::TC * 16;
+}
 
 template <class Make>
 void launch_scores(const Rows2& r, int tile, bool fast, int cols, const int32_t* order, const int32_t* offsets, Make make,
@@ -472,7 +479,7 @@ struct ForwardSpace {
     ForwardSpace(void* ws, int64_t m, int vocab, int k, htl_dtype dtype) {
         wide = wide_of(m, vocab, dtype) && k >= kWideK;
         Carve c = {(char*)ws, 0};
-        partial = c.take<Best>(m * ceil_div(vocab, wave_cols(m, wide)));
+        partial = c.take<Best>(m * ceil_div(vocab, wave_cols(m, vocab, dtype, wide)));
         target_score = c.take<float>(m);
         ids = c.take<int32_t>(wide ? m : 0);
         order = c.take<int32_t>(wide ? m : 0);
@@ -558,7 +565,7 @@ htl_status piece_of(const Rows2& r, int v0, int cols, char* room, const void*& w
 // Partial sums of all scores' exponentials; ids (wide tiles only): which rows take part.
 htl_status forward_scores(const Rows2& r, float scale, const ForwardSpace& s, const Items& targets, int& blocks,
                           hipStream_t stream) {
-    const int W = wave_cols(r.m, s.wide);
+    const int W = wave_cols(r.m, r.vocab, r.dtype, s.wide);
     blocks = (int)ceil_div(r.vocab, W);
     if (s.wide) {
         htl_status st = row_groups(s.ids, r.m, 1, s.order, s.offsets, s.groups, s.group_bytes, stream);
