@@ -1,5 +1,5 @@
 // Shared by the dense operators beside the lookup (rows8.hip, norm.hip,
-// gate.hip, product.hip): rows read and written eight elements per lane, the
+// gate.hip, product.hip, gated.hip, scores.hip): rows read and written eight elements per lane, the
 // 8-bit row format, and the map from workgroups to the rows of a group.
 #pragma once
 
