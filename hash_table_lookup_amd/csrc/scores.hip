@@ -235,15 +235,20 @@ struct Teacher {
     bool f32;
     int top;
     float scale;             // 1 / T
-    // logit / T in units of ln 2; -inf for an entry that is not there
+    // -inf for an entry that is not there
     __device__ __forceinline__ float logit(int64_t row, int j) const {
         if (items.at(row * top + j) < 0) return -INFINITY;
-        const float v = f32 ? ((const float*)logits)[row * ld + j] : bf16_lo(((const uint16_t*)logits)[row * ld + j]);
-        return v * scale * kLog2e;
+        return f32 ? ((const float*)logits)[row * ld + j] : bf16_lo(((const uint16_t*)logits)[row * ld + j]);
     }
 };
-// log2 of the sum of the teacher's exponentials of a row, one wave; false where no entry is there.
-__device__ __forceinline__ bool teacher_sum(const Teacher& t, int64_t row, float& sum) {
+// A row's shares: log2 of an entry's is (logit - top) unit - log.  (The largest logit is taken off before
+// anything is multiplied: lists of the type's lowest value keep their equal shares.)
+struct Shares {
+    float top, unit, log;
+    __device__ __forceinline__ float log2_of(float logit) const { return __builtin_fmaf(logit - top, unit, -log); }
+};
+// Found by one wave; false where no entry is there.
+__device__ __forceinline__ bool teacher_sum(const Teacher& t, int64_t row, Shares& all) {
     float top = -INFINITY;
     for (int j = __lane_id(); j < t.top; j += 64) {
         const float v = t.logit(row, j);
@@ -252,11 +257,12 @@ __device__ __forceinline__ bool teacher_sum(const Teacher& t, int64_t row, float
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
     if (top == -INFINITY) return false;
+    const float unit = t.scale * kLog2e;
     float s = 0.0f;
-    for (int j = __lane_id(); j < t.top; j += 64) s += __builtin_amdgcn_exp2f(t.logit(row, j) - top);
+    for (int j = __lane_id(); j < t.top; j += 64) s += __builtin_amdgcn_exp2f((t.logit(row, j) - top) * unit);
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) s += __shfl_xor(s, off);
-    sum = top + __builtin_amdgcn_logf(s);
+    all = {top, unit, __builtin_amdgcn_logf(s)};
     return true;
 }
 
@@ -268,7 +274,7 @@ __global__ __launch_bounds__(256) void k_distill_finish(RowsIn x, RowsIn w, int 
     __shared__ Best s[4];
     __shared__ float s_score[HTL_MAX_TOP];
     for (int64_t row = blockIdx.x; row < m; row += gridDim.x) {
-        float all;
+        Shares all;
         const bool on = teacher_sum(t, row, all);        // (every wave finds the same)
         __syncthreads();                                 // the scores before are read
         for (int j = (threadIdx.x >> 6) * 2; j < t.top; j += 8) {
@@ -293,7 +299,7 @@ __global__ __launch_bounds__(256) void k_distill_finish(RowsIn x, RowsIn w, int 
         if (threadIdx.x >= 64) continue;
         float sum = 0.0f;
         for (int j = threadIdx.x; j < t.top; j += 64) {
-            const float logp = t.logit(row, j) - all;
+            const float logp = all.log2_of(t.logit(row, j));
             if (logp > -INFINITY || logp != logp)        // an entry of share 0 adds nothing
                 sum += __builtin_amdgcn_exp2f(logp) * (logp * kLn2 + (l - s_score[j]));
         }
@@ -314,7 +320,7 @@ __global__ __launch_bounds__(256) void k_teach(int64_t m, Teacher t, const float
                                                const float* __restrict__ lse, const float* __restrict__ dloss,
                                                int32_t* __restrict__ ids, float* __restrict__ d) {
     for (int64_t row = blockIdx.x * 4ll + (threadIdx.x >> 6); row < m; row += gridDim.x * 4ll) {
-        float all;
+        Shares all;
         const bool on = teacher_sum(t, row, all);
         if (__lane_id() == 0) ids[row] = on ? 0 : -1;
         if (!on) continue;
@@ -326,7 +332,7 @@ __global__ __launch_bounds__(256) void k_teach(int64_t m, Teacher t, const float
             for (int i0 = 0; i0 < t.top; i0 += 64) {
                 const int i = i0 + __lane_id();
                 const int other = i < t.top ? t.items.at(row * t.top + i) : -1;
-                const float p = other >= 0 ? __builtin_amdgcn_exp2f(t.logit(row, i) - all) : 0.0f;
+                const float p = other >= 0 ? __builtin_amdgcn_exp2f(all.log2_of(t.logit(row, i))) : 0.0f;
                 const int count = t.top - i0 < 64 ? t.top - i0 : 64;
                 for (int n = 0; n < count; ++n) {
                     const int it = __shfl(other, n);

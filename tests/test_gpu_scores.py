@@ -450,3 +450,29 @@ def test_wide_strides(htl, pad, first):
     some = Want(x[rows], w, targets[rows][:, None], torch.zeros(40, 1).double(), 1.0, dloss[rows])
     _close(loss[rows], some.loss, some.tloss, "loss")
     _close(dx[rows], some.dx, some.tdx, "dx")
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("heat", [1.0, 0.5])
+def test_logits_of_the_lowest_value(htl, kind, heat):
+    # Lists masked with their type's lowest value: all of it, equal shares; some of it, none for those.  A
+    # logit's distance from the row's largest is below twice the ordinary logits' size wherever a share is not 0.
+    m, v, k, t = 60, 700, 40, 6
+    x, w, _, dloss = _data(m, v, k, torch.float32, seed=11)
+    gen = torch.Generator().manual_seed(12)
+    items = torch.stack([torch.randperm(v, generator=gen)[:t] for _ in range(m)])
+    logits = (torch.randn(m, t, generator=gen) * 3.0).to(kind)
+    size = 2.0 * float(logits.float().abs().max()) / heat
+    low = torch.finfo(kind).min
+    logits[:20] = low
+    logits[20:40, ::2] = low
+    items[5, 3:] = -1
+    want = Want(x, w, items, _log_shares(items, logits, v, heat), heat, dloss, size)
+    assert (want.loss[:20] != 0).all()
+    xc, wc, ic, lc = x.cuda(), w.cuda(), items.cuda(), logits.cuda()
+    loss, kept = htl.distill_loss(xc, wc, ic, lc, temperature=heat)
+    _close(kept[0], want.lse, want.tlse, "lse")
+    _close(loss, want.loss, want.tloss, "loss")
+    dx, dw = htl.distill_loss_backward(dloss.cuda(), xc, wc, ic, lc, kept, temperature=heat)
+    _close(dx, want.dx, want.tdx, "dx")
+    _close(dw, want.dw, want.tdw, "dw")
