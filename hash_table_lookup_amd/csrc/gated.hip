@@ -227,11 +227,194 @@ __global__ __launch_bounds__(512, 2) void k_gated_resident(ProdArgs p, GatedEnd<
         }
     }
 }
+// Positions per chunk: so many that no more chunks than workgroups run at once load a matrix,
+// each once.  (426,000 rows of 26 groups, 128 -> 2 x 256: 234 us with 2,048, 246
+// with 1,024, 271 with 512; the backward pass below 285, 313 and 341.)
+uint32_t resident_rows(int64_t m, int n_groups, int at_once) {
+    return (uint32_t)align_up((size_t)(n_groups <= at_once / 4 ? ceil_div(m, at_once - n_groups) : ceil_div(m, 1024)), 256);
+}
 template <int LP> void launch_resident(ProdArgs p, int64_t bytes, const GatedEnd<Resident>& end, hipStream_t s) {
     const int64_t chunks = p.m / p.rows + p.n_groups + 1;
     const dim3 grid(grid_for(align_up((size_t)chunks, kXcds), 1));
     if (bytes <= 81920) hipLaunchKernelGGL((k_gated_resident<LP, 81920>), grid, dim3(512), 0, s, p, end);
     else hipLaunchKernelGGL((k_gated_resident<LP, 163840>), grid, dim3(512), 0, s, p, end);
+}
+
+// Backward of such blocks from what was kept of z and u: a workgroup holds its
+// group's matrix transposed, and its waves take 32 rows at a time from dy, z and u
+// to dz and du in registers, out to d, and through the matrix to dx.  Loads and
+// d are whole 128-byte lines, 64 outputs of eight rows a time, and lanes exchange dz and
+// du to where the matrix instructions have them.  In LDS, for each of 128 columns, the
+// z's rows and then the u's, NP * 32 elements each with zeros behind, 16 bytes apart
+// as above.  Bound: bytes.  WHOLE: n is NP * 32.
+template <int NP, bool WHOLE>
+__global__ __launch_bounds__(512, 2) void k_gated_back_resident(ProdArgs p, RowsIn dy, RowsIn kept, RowsOut d, int act) {
+    constexpr int kLd = NP * 128 + 16;
+    __shared__ __attribute__((aligned(16))) char lds[128 * kLd];
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int piece = (lane & 7) * 8, from_lane = ((lane & 7) * 8 + (lane >> 3 & 1) * 4 + (lane >> 4)) * 4;
+    const RowsIn up = {(const char*)kept.p + p.n * 2ll, nullptr, kept.ld, 0};
+    const RowsOut du = {(char*)d.p + p.n * 2ll, d.ld};
+    for (int64_t b = blockIdx.x;; b += gridDim.x) {
+        TileAt t;
+        const int found = find_tile(p.offsets, p.n_groups, p.m, p.rows, 0, false, 1, b, t);
+        if (found < 0) return;
+        if (!found) continue;
+        const bool grouped = t.g < p.n_groups;
+        auto row_at = [&](int64_t pos) {
+            const int32_t row = pos < t.end ? (p.order ? p.order[pos] : (int32_t)pos) : -1;
+            return row >= 0 && row < p.m ? row : -1;
+        };
+        int64_t pos = t.beg + wv * 32;
+        if (!grouped) {                      // no matrix, and nothing reads their d
+            f32x4 zero[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) zero[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (; pos < t.end; pos += 256)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    for (int c = 0; c < p.k; c += 64)
+                        store_rows<4>(p.out, p.out_f32, row_at(pos + j * 16 + (lane & 15)), p.k, c, p.k, zero);
+            continue;
+        }
+        // eight rows and 64 columns of each: row lane / 8, piece lane % 8
+        struct Raw { Raw8<kSrcBf16> g, z, u; } raw[4];
+        int32_t row[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) row[i] = row_at(pos + i * 8 + (lane >> 3));
+        // a row that is not there: as the first, or zeros
+        auto fetch = [&](int l, int32_t from, Raw& o) __attribute__((always_inline)) {
+            const int64_t r = from < 0 ? 0 : from;
+            const int col = l * 64 + piece;
+            if (WHOLE) {
+                load_at<2>((const uint16_t*)dy.p + r * dy.ld + col, o.g.w);
+                load_at<2>((const uint16_t*)kept.p + r * kept.ld + col, o.z.w);
+                load_at<2>((const uint16_t*)up.p + r * up.ld + col, o.u.w);
+            } else {
+                const int have = from < 0 ? 0 : p.n;
+                load8(dy, r, col, have, o.g);
+                load8(kept, r, col, have, o.z);
+                load8(up, r, col, have, o.u);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fetch(0, row[i], raw[i]);
+        __syncthreads();                     // the matrix before is read
+        const char* w = (const char*)p.b + (int64_t)t.g * 2 * p.n * p.ldw * 2;
+        // two rows of w and eight columns: pairs of neighbours in eight rows of LDS.  A wave has 16 such pairs
+        // of rows beside each other, so that it writes to all banks.
+#pragma unroll 2
+        for (int i = threadIdx.x; i < NP * 32 * 16; i += 512) {
+            const int c = ((i >> 4) & 15) * 8, at_e = ((i >> 8) * 16 + (i & 15)) * 2;   // of both halves
+            const bool half = at_e >= NP * 32;
+            const int e = at_e - (half ? NP * 32 : 0);
+            const char* at = w + (((int64_t)(half ? p.n : 0) + e) * p.ldw + c) * 2;
+            const u32x4 lo = held_piece<2>(at, e < p.n ? p.k - c : 0);
+            const u32x4 hi = held_piece<2>(at + p.ldw * 2, e + 1 < p.n ? p.k - c : 0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t a = lo[j >> 1] >> (16 * (j & 1)) & 0xFFFFu, v = hi[j >> 1] >> (16 * (j & 1));
+                *(uint32_t*)(lds + (c + j) * kLd + at_e * 2) = a | v << 16;
+            }
+        }
+        __syncthreads();
+        for (; pos < t.end; pos += 256) {
+            int32_t next[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) next[i] = row_at(pos + 256 + i * 8 + (lane >> 3));
+            f32x4 acc[2][8];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) acc[j][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+            for (int l = 0; l < NP / 2; ++l) {
+                const bool more = l + 1 < NP / 2;
+                u32x4 w8[2][4];              // dz and du of each eight rows
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float g[8], z[8], u[8];
+                    unpack8(dy, raw[i].g, g);
+                    unpack8(kept, raw[i].z, z);
+                    unpack8(up, raw[i].u, u);
+                    fetch(more ? l + 1 : 0, more ? row[i] : next[i], raw[i]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float slope;
+                        const float a = gate_act(z[e], act, slope);
+                        z[e] = g[e] * u[e] * slope;
+                        u[e] = g[e] * a;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w8[0][i][e] = pack_bf16(z[2 * e], z[2 * e + 1]);
+                        w8[1][i][e] = pack_bf16(u[2 * e], u[2 * e + 1]);
+                    }
+                    if (row[i] >= 0) {
+                        const int col = l * 64 + piece;
+                        if (WHOLE) {
+                            store_at<2>((uint16_t*)d.p + row[i] * d.ld + col, w8[0][i]);
+                            store_at<2>((uint16_t*)du.p + row[i] * du.ld + col, w8[1][i]);
+                        } else {
+                            store8<kSrcBf16>(d, row[i], col, p.n, z);
+                            store8<kSrcBf16>(du, row[i], col, p.n, u);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int s = 0; s < 2; ++s)  // 32 of the columns: pieces s * 4 .. + 4
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        Frag<kSrcBf16> x[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            u32x4 o;
+                            // rows 8 .. 15 to the lanes whose pieces are not of this half, then all to row lane % 16,
+                            // piece lane / 16
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int low = (int)w8[h][j * 2][e], high = (int)w8[h][j * 2 + 1][e];
+                                const int v = s == 0 ? __builtin_amdgcn_update_dpp(low, high, 0x114, 0xF, 0xA, false)
+                                                     : __builtin_amdgcn_update_dpp(high, low, 0x104, 0xF, 0x5, false);
+                                o[e] = (uint32_t)__builtin_amdgcn_ds_bpermute(from_lane, v);
+                            }
+                            __builtin_memcpy(&x[j].v, &o, 16);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            Frag<kSrcBf16> c;
+                            c.v = *(const bf16x8*)(lds + (q * 16 + (lane & 15)) * kLd + (h * NP + l * 2 + s) * 64 + (lane >> 4) * 16);
+                            multiply(c, x[0], 0, acc[0][q]);
+                            multiply(c, x[1], 0, acc[1][q]);
+                        }
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                store_rows<8>(p.out, p.out_f32, row_at(pos + j * 16 + (lane & 15)), p.k, 0, p.k, acc[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) row[i] = next[i];
+        }
+    }
+}
+// Whether a backward pass from z and u goes that way: 426,000 rows of 26 groups, 128 ->
+// 2 x 256: 290 us, where dz and du by themselves and then dx in tiles take 415.  (Lines
+// read and written in two halves, 16 rows a time: 356.)
+bool back_resident(int64_t m, int n_groups, int n, int k, htl_dtype dtype) {
+    return dtype == HTL_BF16 && n <= 256 && k <= 128 && m / n_groups >= 512 && m >= 1 << 16;
+}
+htl_status launch_back_resident(ProdArgs p, const RowsIn& dy, const RowsIn& kept, const RowsOut& d, int act, hipStream_t s) {
+    p.rows = resident_rows(p.m, p.n_groups, 256);
+    const dim3 grid(grid_for(align_up((size_t)(p.m / p.rows + p.n_groups + 1), kXcds), 1));
+    auto go = [&](auto steps) {
+        constexpr int NP = decltype(steps)::value;
+        if (p.n == NP * 32) hipLaunchKernelGGL((k_gated_back_resident<NP, true>), grid, dim3(512), 0, s, p, dy, kept, d, act);
+        else hipLaunchKernelGGL((k_gated_back_resident<NP, false>), grid, dim3(512), 0, s, p, dy, kept, d, act);
+    };
+    if (p.n <= 64) go(std::integral_constant<int, 2>());
+    else if (p.n <= 128) go(std::integral_constant<int, 4>());
+    else go(std::integral_constant<int, 8>());
+    return check_launch("gated_mm_backward");
 }
 
 template <int T, class C, bool ASYNC>
@@ -291,7 +474,7 @@ void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s
     const int lp = p.k <= 32 ? 1 : p.k <= 64 ? 2 : p.k <= 128 ? 4 : 8;
     const int64_t bytes = ceil_div(p.n, 64) * 128 * (lp * 64 + 16);
     if (!c.dy.p && dtype == HTL_BF16 && p.k <= 256 && bytes <= 163840 && each >= 512 && p.m >= 1 << 16) {
-        p.rows = (uint32_t)align_up((size_t)ceil_div(p.m, 1024), 256);
+        p.rows = resident_rows(p.m, p.n_groups, bytes <= 81920 ? 512 : 256);
         const GatedEnd<Resident> end = {p.n, c.act, c.y, c.y_f32, false, c.kept};
         if (lp == 1) launch_resident<1>(p, bytes, end, s);
         else if (lp == 2) launch_resident<2>(p, bytes, end, s);
@@ -475,9 +658,13 @@ extern "C" htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const voi
     const void* xs = as_is ? x : s.x;
     const void* wp = s.copied ? s.w : w;
     const int64_t ldxs = as_is ? ldx : spread_ld(k), ldw = s.copied ? packed_ld(k) : k;
+    const bool fused = m > 0 && kept && dx && !s.wide && back_resident(m, n_groups, n, k, dtype);
     if (m > 0) {
         const RowsIn in = {dy, nullptr, ld_dy, 0};
-        if (kept) {
+        if (fused) {
+            const ProdArgs p = {nullptr, wp, dx, order, offsets, m, 0, k, ldw, n, k, n_groups, 0, nullptr, dx_dtype == HTL_F32, 0};
+            st = launch_back_resident(p, in, {kept, nullptr, 2 * (int64_t)n, 0}, {s.d, s.ld}, (int)act, stream);
+        } else if (kept) {
             const RowsIn from = {kept, nullptr, 2 * (int64_t)n, 0};
             const RowsOut to = {s.d, s.ld};
             const int32_t* by = s.wide ? order : nullptr;
@@ -489,7 +676,7 @@ extern "C" htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const voi
             p.packed = s.wide;
             launch_pairs(p, dtype, {(int)act, nullptr, false, nullptr, in, s.d, s.ld, s.wide}, stream);
         }
-        st = check_launch("gated_mm_backward");
+        if (st == HTL_OK) st = check_launch("gated_mm_backward");
         if (st == HTL_OK && s.ld > 2 * n) st = zero_behind(s.d, dtype, m, 2 * n, s.ld, stream);
         if (st != HTL_OK) return st;
     }
@@ -500,7 +687,7 @@ extern "C" htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const voi
             st = sum_parts(s.parts, s.splits, false, m, k, order, offsets ? offsets + n_groups : nullptr, dx, dx_dtype, stream);
         else if (st == HTL_OK && offsets)
             st = zero_rest(dx, (int64_t)k * elem(dx_dtype), m, order, offsets + n_groups, stream);
-    } else if (dx) {
+    } else if (dx && !fused) {
         st = rows_dx(s.d, s.ld, wp, ldw, dtype, m, 2 * n, k, order, offsets, n_groups, dx, dx_dtype, s.copied, stream);
     }
     if (st != HTL_OK || !dw) return st;

@@ -309,3 +309,41 @@ def test_matrix_at_any_alignment(htl, m, n, k):
     dx, dw = htl.gated_mm_backward(dy.cuda(), x.cuda(), loose)
     _close(dx, want.dx, want.tdx, "dx")
     _close(dw, want.dw, want.tdw, "dw")
+
+
+@pytest.mark.parametrize("m,n,k,g,dx_dtype", [(66000, 256, 128, 3, None), (65536, 33, 50, 1, torch.float32),
+                                              (70000, 100, 72, 26, None), (65551, 32, 7, 2, None), (65600, 64, 128, 4, None),
+                                              (66001, 128, 96, 5, torch.float32), (65536, 250, 128, 1, None)])
+def test_gradients_of_small_blocks(htl, m, n, k, g, dx_dtype):
+    """Backward passes of many rows through blocks that fit in LDS, from z and u: all of dx and dw, with rows of no group."""
+    ids = _ids(np.random.default_rng(m), m, g, "dropped" if g > 1 else "one")
+    x, w, dy = _data(m, n, k, g, torch.bfloat16)
+    want = Want(x, w, dy, ids, "silu", True, dx=dx_dtype)
+    groups = htl.group_rows(torch.from_numpy(ids).cuda(), g) if g > 1 else None
+    none = torch.from_numpy((ids < 0) | (ids >= g))
+    x[none], dy[none] = float("nan"), float("inf")
+    xc, wc, dc = x.cuda(), w.cuda(), dy.cuda()
+    _, kept = htl.gated_mm(xc, wc, groups, keep=True)
+    dx, dw = htl.gated_mm_backward(dc, xc, wc, kept, groups, dx_dtype=dx_dtype)
+    assert dx.dtype == (dx_dtype or torch.bfloat16)
+    _close(dx, want.dx, want.tdx, "dx")
+    _close(dw, want.dw, want.tdw, "dw")
+    only, none_ = htl.gated_mm_backward(dc, xc, wc, kept, groups, dx_dtype=dx_dtype, need_dw=False)
+    assert none_ is None and torch.equal(only, dx)
+    _, only = htl.gated_mm_backward(dc, xc, wc, kept, groups, need_dx=False)
+    _close(only, want.dw, want.tdw, "dw alone")
+
+
+def test_broken_plan_of_small_blocks(htl):
+    m, n, k = 65600, 96, 40
+    x, w, dy = _data(m, n, k, 1, torch.bfloat16)
+    bad = torch.arange(m, dtype=torch.int32)
+    gone = torch.arange(m) % 7 == 3
+    bad[gone] = torch.where(torch.arange(int(gone.sum())) % 2 == 0, -5, m + 9).to(torch.int32)
+    plan = htl.RowGroups(torch.zeros(m, dtype=torch.int32).cuda(), bad.cuda(), torch.tensor([0, m], dtype=torch.int32).cuda(), 1)
+    want = Want(x, w, dy, np.where(gone.numpy(), -1, 0).astype(np.int32), "silu", True)
+    y, kept = htl.gated_mm(x.cuda(), w.cuda(), plan, keep=True)
+    _close(y[~gone], want.y[~gone], want.ty[~gone], "y")
+    dx, dw = htl.gated_mm_backward(dy.cuda(), x.cuda(), w.cuda(), kept, plan)
+    _close(dx[~gone], want.dx[~gone], want.tdx[~gone], "dx")
+    _close(dw, want.dw, want.tdw, "dw")
