@@ -12,8 +12,8 @@
 // Bound: products, and bytes where matrices are small or rows few.  Measured:
 // 16,384 bf16 rows over 16 ragged groups, 2,048 -> 2 x 4,096: forward 598 us
 // (577-654; 919 TFLOP/s), dz and du with z and u again 719 (695-803), dx 639, dw 683.
-// 426,000 rows of 26 groups, 128 -> 2 x 256: forward with z and u kept 279 us (763 MB:
-// 2.7 TB/s), dz and du from them 222 (1.09 GB: 4.9 TB/s).  One row, 2,048 -> 2 x
+// 426,000 rows of 26 groups, 128 -> 2 x 256: forward with z and u kept 234 us (763 MB:
+// 3.3 TB/s), dz, du and dx from them 290 (1.2 GB: 4.1 TB/s).  One row, 2,048 -> 2 x
 // 4,096: 9.7 us (33.6 MB: 3.5 TB/s); 64 rows in 16 groups: 74 us (7.2 TB/s, in part
 // from the last-level cache).  5,001 fp32 rows, 513 -> 2 x 777: 110 us (72 TFLOP/s).
 #include "few.h"
