@@ -564,7 +564,7 @@ struct BackSpace {
             return p;
         };
         d = take((size_t)m * ld * elem(dtype));
-        sums = take(wide ? wide_dw_bytes(m, n_groups, 2 * n, k) : sums_dw_bytes(m, n_groups, 2 * n, k));
+        sums = take(wide ? wide_dw_bytes(m, n_groups, 2 * n, k, ld, spread_ld(k)) : sums_dw_bytes(m, n_groups, 2 * n, k));
         x = take(wide || copied ? x_copy_bytes(m, k, dtype) : 0);
         w = take(copied ? w_copy_bytes(n_groups, n, k, dtype) : 0);
         parts = (float*)take(splits > 1 ? (size_t)splits * m * k * 4 : 0);
@@ -650,8 +650,8 @@ extern "C" htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const voi
     htl_status st = HTL_OK;
     const int64_t rows = (int64_t)n_groups * 2 * n;
     if (s.copied) st = pack_rows(w, k, dtype, nullptr, rows, rows, k, s.w, packed_ld(k), stream);
-    // wide.h takes x by position in the plan
-    const bool as_is = s.wide ? !order && packed_as_is(x, ldx, k) : !s.copied;
+    // wide.h takes x by position in the plan, and sums over as many rows as lie in 4 GiB
+    const bool as_is = s.wide ? !order && packed_as_is(x, ldx, k) && m * ldx * 2 <= kBufferBytes : !s.copied;
     if (st == HTL_OK && !as_is)
         st = pack_rows(x, ldx, dtype, s.wide ? order : nullptr, m, m, k, s.x, spread_ld(k), stream);
     if (st != HTL_OK) return st;

@@ -542,8 +542,10 @@ struct BackwardSpace {
         parts = c.take<float>(step < vocab || splits > 1 ? splits * m * k : 0);
         d = c.take<char>(m * spread_ld(step) * elem(dtype));
         const int last = vocab % step ? vocab % step : step;
-        const size_t a = wide ? wide_dw_bytes(m, 1, step, k) : sums_dw_bytes(m, 1, step, k);
-        const size_t b = wide ? wide_dw_bytes(m, 1, last, k) : sums_dw_bytes(m, 1, last, k);
+        auto sums_of = [&](int cols) {
+            return wide ? wide_dw_bytes(m, 1, cols, k, spread_ld(step), spread_ld(k)) : sums_dw_bytes(m, 1, cols, k);
+        };
+        const size_t a = sums_of(step), b = sums_of(last);
         sums = c.take<char>(a > b ? a : b);
         copied = copied_of(m, k, dtype);
         x = c.take<char>(wide || copied ? m * spread_ld(k) * elem(dtype) : 0);

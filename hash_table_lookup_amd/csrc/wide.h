@@ -335,8 +335,9 @@ htl_status sum_parts(const float* parts, int splits, bool by_row, int64_t m, int
 // Zeros for rows order[pos] of `bytes` each, from position *count on.
 htl_status zero_rest(void* out, int64_t bytes, int64_t m, const int32_t* order, const int32_t* count, hipStream_t stream);
 
-// dw_g = sum of d[pos] x[pos]^T over the group's positions.
-size_t wide_dw_bytes(int64_t m, int n_groups, int n, int k);
+// dw_g = sum of d[pos] x[pos]^T over the group's positions.  The workspace goes by the row strides; x's
+// may be larger in the call where all of x is less than 4 GiB.
+size_t wide_dw_bytes(int64_t m, int n_groups, int n, int k, int64_t ldd, int64_t ldx);
 htl_status wide_dw(const void* d, int64_t ldd, const void* x, int64_t ldx, int64_t m, int n, int k, const int32_t* offsets,
                    int n_groups, void* dw, htl_dtype dw_dtype, void* ws, hipStream_t stream);
 

@@ -120,12 +120,15 @@ __global__ __launch_bounds__(256) void k_zero_rest(char* __restrict__ out, int64
 }
 
 // Positions per chunk of dw's sums: as long as fills the device once with
-// tiles, and less than 4 GiB of an operand.
-uint32_t wide_dw_rows(int64_t m, int n, int k) {
+// tiles, and less than 4 GiB of an operand that is longer in all (offsets have 32
+// bits; groups round a chunk up to 64 positions).
+uint32_t wide_dw_rows(int64_t m, int n, int k, int64_t ldd, int64_t ldx) {
     int64_t r = ceil_div(m * ceil_div(n, 256) * ceil_div(k, 256), 256);
     if (r < 512) r = 512;
-    const int64_t most = kBufferBytes / 2 / (packed_ld(n) > packed_ld(k) ? packed_ld(n) : packed_ld(k));
-    if (r > most) r = most / 64 * 64;
+    for (const int64_t ld : {ldd, ldx}) {
+        const int64_t most = kBufferBytes / 2 / ld / 64 * 64;
+        if (m * ld * 2 > kBufferBytes && r > most) r = most;
+    }
     if (r > m) r = m < 1 ? 1 : m;
     return (uint32_t)r;
 }
@@ -188,15 +191,15 @@ htl_status zero_rest(void* out, int64_t bytes, int64_t m, const int32_t* order, 
     return check_launch("rows of no group");
 }
 
-size_t wide_dw_bytes(int64_t m, int n_groups, int n, int k) {
-    const uint32_t r = wide_dw_rows(m, n, k);
+size_t wide_dw_bytes(int64_t m, int n_groups, int n, int k, int64_t ldd, int64_t ldx) {
+    const uint32_t r = wide_dw_rows(m, n, k, ldd, ldx);
     if (m <= (int64_t)r) return 256;
     return align_up((size_t)split_chunks(m, n_groups, r) * n * k * 4, 256);
 }
 
 htl_status wide_dw(const void* d, int64_t ldd, const void* x, int64_t ldx, int64_t m, int n, int k, const int32_t* offsets,
                    int n_groups, void* dw, htl_dtype dw_dtype, void* ws, hipStream_t stream) {
-    const uint32_t r = wide_dw_rows(m, n, k);
+    const uint32_t r = wide_dw_rows(m, n, k, ldd, ldx);
     const ProdArgs p = {d, x, nullptr, nullptr, offsets, m, ldd, ldx, 0, n, k, n_groups, r, nullptr, 0, split_chunks(m, n_groups, r), true};
     const DwEnd end = {dw, dw_dtype == HTL_F32, (float*)ws, n, k};
     const int64_t tiles = (m / r + n_groups + 1) * ceil_div(n, 256) * ceil_div(k, 256);

@@ -347,3 +347,35 @@ def test_broken_plan_of_small_blocks(htl):
     dx, dw = htl.gated_mm_backward(dy.cuda(), x.cuda(), w.cuda(), kept, plan)
     _close(dx[~gone], want.dx[~gone], want.tdx[~gone], "dx")
     _close(dw, want.dw, want.tdw, "dw")
+
+
+def _backward_of_some(htl, x, w, dy, some, **kw):
+    """dw of one group against the formulas, at `some` of its n outputs (all of x's rows count)."""
+    n = w.shape[0] // 2
+    rows = torch.cat([some, n + some])
+    dx, dw = htl.gated_mm_backward(dy, x, w, **kw)
+    want = Want(x.cpu(), w[rows].cpu()[None], dy[:, some].cpu(), np.zeros(x.shape[0], dtype=np.int32), "silu", False)
+    _close(dw[0][rows], want.dw[0], want.tdw[0], "dw")
+    return dx, dw
+
+
+def test_rows_of_a_larger_matrix_past_4_gib(htl):
+    """x's rows so far apart that they span more than 4 GiB: the same as of rows that lie together."""
+    m, n, k = 65_600, 128, 256
+    x, w, dy = (t.cuda() for t in _data(m, n, k, 1, torch.bfloat16))
+    apart = torch.full((m, 32_768), float("nan"), dtype=torch.bfloat16, device="cuda")
+    apart[:, 512:512 + k] = x
+    dx, dw = _backward_of_some(htl, x, w[0], dy, torch.arange(n, device="cuda"))
+    for got, want in zip(htl.gated_mm_backward(dy, apart[:, 512:512 + k], w[0]), (dx, dw)):
+        assert torch.equal(got, want)
+
+
+def test_slopes_past_4_gib(htl):
+    """dz and du that take 4.3 GB together, in one chunk of sums if it went by the matrices alone."""
+    m, n, k = 32_760, 32_768, 256
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(m, k, device="cuda", generator=gen).bfloat16()
+    w = (torch.randn(2 * n, k, device="cuda", generator=gen) / 8.0).bfloat16()
+    dy = torch.randn(m, n, device="cuda", generator=gen).bfloat16()
+    some = torch.cat([torch.arange(0, n, 257, device="cuda"), torch.tensor([n - 1], device="cuda")])
+    _backward_of_some(htl, x, w, dy, some, need_dx=False)

@@ -69,6 +69,16 @@ def test_gated_refuses(L):
     assert L.gated_mm_workspace_bytes(1000, 1, 64, 65, 1) > L.gated_mm_workspace_bytes(1000, 1, 64, 64, 1) == 256
 
 
+@pytest.mark.parametrize("m,n,k", [(260_200, 4096, 2048), (261_000, 4096, 2048), (262_080, 4096, 2048), (520_000, 2048, 4096),
+                                   (32_760, 32768, 256)])
+def test_sums_of_operands_past_4_gib(L, m, n, k):
+    """dz and du of so many rows, 64 elements more than 2 n apart, take over 4 GiB, which the sums of dw reach in no less
+    than two chunks: room for both chunks' sums beside those rows and a copy of x (as far apart)."""
+    assert 2 * n % 512 == 0 and m * (2 * n + 64) * 2 > 1 << 32
+    ld_x = k + (0 if k % 512 else 64)
+    assert L.gated_mm_backward_workspace_bytes(m, 1, n, k, 1) >= m * (2 * n + 64 + ld_x) * 2 + 2 * 2 * n * k * 4
+
+
 def test_softmax_refuses(L):
     for kw in (dict(m=-1), dict(m=1 << 31), dict(v=0), dict(v=(1 << 30) + 1), dict(k=0, ldx=0), dict(k=65537, ldx=65537),
                dict(ldx=7), dict(ldw=7), dict(dtype=2), dict(bits=16), dict(heat=0.0), dict(heat=-1.0),
