@@ -511,11 +511,13 @@ struct ForwardSpace {
 // rows make little work of a piece, and longer pieces leave fewer partial sums:
 // 16,384 fp32 rows of 128 against 65,536, step: 12.4, 10.9, 10.3 and 10.0 ms with
 // 128, 256, 512 and 1,024 MiB; 4,096 rows of 2,048 against 131,072, step: 7.4, 7.5,
-// 7.9 and 7.8 ms.
+// 7.9 and 7.8 ms.  The matrix rows of a piece span less than 4 GiB (offsets have 32 bits).
 int piece_cols(int64_t m, int vocab, int k, htl_dtype dtype) {
     int64_t c = ((k < 1024 ? 512ll : 256ll) << 20) / (elem(dtype) * (m < 1 ? 1 : m)) / 256 * 256;
+    const int64_t most = kBufferBytes / (packed_ld(k) * elem(dtype)) / 256 * 256;
     if (c < 256) c = 256;
     if (c > kMostCols) c = kMostCols;
+    if (c > most) c = most;
     return (int)(c < vocab ? c : vocab);
 }
 

@@ -476,3 +476,54 @@ def test_logits_of_the_lowest_value(htl, kind, heat):
     dx, dw = htl.distill_loss_backward(dloss.cuda(), xc, wc, ic, lc, kept, temperature=heat)
     _close(dx, want.dx, want.tdx, "dx")
     _close(dw, want.dw, want.tdw, "dw")
+
+
+@pytest.mark.parametrize("m,v,k", [(1024, 65_600, 32_768), (300, 33_000, 65_536)])
+def test_rows_past_4_gib_a_piece(htl, m, v, k):
+    """Rows so long that a piece of the vocabulary would span 4 GiB: cross entropy, and a teacher's lists with items of
+    each piece.  Entries are -1, 0 and 1, and as many 128ths: scores are exact."""
+    gen = torch.Generator(device="cuda").manual_seed(k)
+    f8 = dict(dtype=torch.float64, device="cuda")
+    x = torch.randint(-1, 2, (m, k), device="cuda", generator=gen).bfloat16()
+    w = torch.empty(v, k, device="cuda", dtype=torch.bfloat16)
+    pieces = [slice(a, min(a + 8192, v)) for a in range(0, v, 8192)]
+    for p in pieces:
+        w[p] = (torch.randint(-1, 2, (p.stop - p.start, k), device="cuda", generator=gen) / 128.0).bfloat16()
+    targets = torch.randint(0, v, (m,), device="cuda", generator=gen)
+    targets[:3] = torch.tensor([v - 1, 0, -1], device="cuda")
+    dloss = torch.rand(m, device="cuda", generator=gen) / m
+    items = torch.stack([targets, (targets * 7 + 11) % v], 1)
+    items[2] = -1
+    x8 = x.double()
+    s = torch.cat([torch.mm(x8, w[p].double().t().contiguous()) for p in pieces], 1)
+    on = targets >= 0
+    lse = torch.logsumexp(s, 1)
+    r = (8 * s.abs().amax(1) + v + 64 + 2 * lse.abs()) * U          # (as at the top, of scores that are exact)
+    at = targets.clamp(min=0)[:, None]
+    for teach in (False, True):
+        share = torch.zeros(m, v, **f8)
+        if teach:
+            loss, kept = htl.distill_loss(x, w, items, torch.zeros(m, 2, device="cuda"))
+            share.scatter_add_(1, items.clamp(min=0), torch.full((m, 2), 0.5, **f8))
+            want = lse - 0.5 * (s.gather(1, at)[:, 0] + s.gather(1, items[:, 1:].clamp(min=0))[:, 0]) - math.log(2.0)
+            dx, dw = htl.distill_loss_backward(dloss, x, w, items, torch.zeros(m, 2, device="cuda"), kept)
+        else:
+            loss, kept = htl.softmax_loss(x, w, targets)
+            share.scatter_(1, at, 1.0)
+            want = lse - s.gather(1, at)[:, 0]
+            dx, dw = htl.softmax_loss_backward(dloss, x, w, targets, kept)
+        assert bool(((loss.double() - torch.where(on, want, 0.0)).abs() <= 2 * r + 64 * U).all())
+        g = torch.where(on, dloss.double(), 0.0)[:, None]
+        q = torch.exp(s - lse[:, None])
+        d = (q - share) * g
+        ed = g * (2 * r[:, None] * q + 16 * U * share) + 2 * U * d.abs()
+        ed = ed + HALF[x.dtype] * (d.abs() + ed)
+        dx8, tol = torch.zeros(m, k, **f8), torch.zeros(m, k, **f8)
+        for p in pieces:
+            wp = w[p].double()
+            dx8 += torch.mm(d[:, p].contiguous(), wp)
+            tol += torch.mm((ed[:, p] + (v + 2) * U * (d[:, p].abs() + ed[:, p])).contiguous(), wp.abs())
+            dw8 = torch.mm(d[:, p].t().contiguous(), x8)
+            t = torch.mm((ed[:, p] + (m + 2) * U * (d[:, p].abs() + ed[:, p])).t().contiguous(), x8.abs())
+            assert bool(((dw[p].double() - dw8).abs() <= t + HALF[x.dtype] * (dw8.abs() + t)).all()), (teach, p)
+        assert bool(((dx.double() - dx8).abs() <= tol + HALF[x.dtype] * (dx8.abs() + tol)).all()), teach

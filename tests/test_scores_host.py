@@ -97,6 +97,15 @@ def test_softmax_refuses(L):
     assert L.softmax_loss_backward_workspace_bytes(8192, 131072, 2048, 1) < 1 << 30
 
 
+@pytest.mark.parametrize("k", [36_000, 40_960, 65_536])
+def test_pieces_of_long_rows(L, k):
+    """Backward passes hold a piece of the vocabulary, less than 4 GiB of its rows (and here less than 1 GiB beside them)."""
+    for top in (0, 7):
+        nb = (L.distill_loss_backward_workspace_bytes(256, 131_072, k, top, 1) if top else
+              L.softmax_loss_backward_workspace_bytes(256, 131_072, k, 1))
+        assert 1 << 31 < nb < (1 << 32) + (1 << 28)
+
+
 def test_distill_refuses(L):
     for kw in (dict(m=-1), dict(v=0), dict(top=0), dict(top=1025, ldl=1025), dict(ldl=2), dict(ld=2), dict(bits=31),
                dict(heat=0.0), dict(items=None), dict(items=ODD), dict(logits=None), dict(logits=ODD), dict(loss=None),
