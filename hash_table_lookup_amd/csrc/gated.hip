@@ -466,7 +466,7 @@ template <int T> void launch_few(const ProdArgs& p, const GatedCall& c, hipStrea
 // The kernel by size, as the plain products' (product.hip) at twice the columns.
 // Few fp32 rows a tile leave the device's last round almost empty: 5,001 rows,
 // 513 -> 777 pairs, 137 us in tiles of 128 rows, 127 in tiles of 32.
-void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s) {
+htl_status launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s) {
     const int es = elem(dtype);
     const bool fast = p.lda * es % 16 == 0 && aligned(p.a, 16) && p.ldw * es % 16 == 0 && (int64_t)p.k * es % 16 == 0 &&
                       aligned(p.b, 16) && p.m * p.lda * es <= kBufferBytes && 2 * (int64_t)p.n * p.ldw * es <= kBufferBytes;
@@ -480,7 +480,7 @@ void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s
         else if (lp == 2) launch_resident<2>(p, bytes, end, s);
         else if (lp == 4) launch_resident<4>(p, bytes, end, s);
         else launch_resident<8>(p, bytes, end, s);
-        return;
+        return check_launch("gated projections");
     }
     if (p.packed || (p.k >= 256 && dtype == HTL_BF16 && fast && many(p.m, p.n_groups, ceil_div(p.m, 256) * ceil_div(p.n, 128)))) {
         p.rows = 256;
@@ -492,17 +492,17 @@ void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s
         } else {
             const GatedEnd<Wide> end = {p.n, c.act, c.y, c.y_f32, false, c.kept};
             hipLaunchKernelGGL(k_gated_wide, grid, dim3(Wide::kThreads), 0, s, p, end);
-            if (p.offsets) {
-                zero_rest(c.y, (int64_t)p.n * (c.y_f32 ? 4 : 2), p.m, p.order, p.offsets + p.n_groups, s);
-                if (c.kept) zero_rest(c.kept, (int64_t)p.n * 4, p.m, p.order, p.offsets + p.n_groups, s);
-            }
         }
-        return;
+        htl_status st = check_launch("gated projections");
+        if (c.dy.p || !p.offsets) return st;
+        if (st == HTL_OK) st = zero_rest(c.y, (int64_t)p.n * (c.y_f32 ? 4 : 2), p.m, p.order, p.offsets + p.n_groups, s);
+        if (st == HTL_OK && c.kept) st = zero_rest(c.kept, (int64_t)p.n * 4, p.m, p.order, p.offsets + p.n_groups, s);
+        return st;
     }
     if (few(p.m, p.n_groups)) {
         if (dtype == HTL_F32) launch_few<kSrcF32>(p, c, s);
         else launch_few<kSrcBf16>(p, c, s);
-        return;
+        return check_launch("gated projections");
     }
     const int64_t small = (ceil_div(p.m, 32) + p.n_groups) * ceil_div(p.n, 64);
     const int tile = each <= 48 || small <= (dtype == HTL_F32 ? 4096 : 512) ? 32 : 128;
@@ -530,6 +530,7 @@ void launch_pairs(ProdArgs p, htl_dtype dtype, const GatedCall& c, hipStream_t s
         else if (fast) go(F32(), Small(), Yes());
         else go(F32(), Small(), No());
     }
+    return check_launch("gated projections");
 }
 
 // Copies of x and w whose rows whole 16-byte pieces make up, for rows that they
@@ -617,8 +618,7 @@ extern "C" htl_status gated_mm(const void* x, int64_t ldx, const void* w, htl_dt
         if (st != HTL_OK) return st;
         p = {xc, wc, nullptr, order, offsets, m, spread_ld(k), k, packed_ld(k), n, (int)packed_ld(k), n_groups, 0, nullptr, 0, 0};
     }
-    launch_pairs(p, dtype, {(int)act, y, y_dtype == HTL_F32, kept, {}, nullptr, 0, false}, stream);
-    return check_launch("gated_mm");
+    return launch_pairs(p, dtype, {(int)act, y, y_dtype == HTL_F32, kept, {}, nullptr, 0, false}, stream);
 }
 
 extern "C" size_t gated_mm_backward_workspace_bytes(int64_t m, int n_groups, int n, int k, htl_dtype dtype) {
@@ -674,7 +674,7 @@ extern "C" htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const voi
         } else {
             ProdArgs p = {xs, wp, nullptr, order, offsets, m, ldxs, k, ldw, n, s.copied ? (int)ldw : k, n_groups, 0, nullptr, 0, 0};
             p.packed = s.wide;
-            launch_pairs(p, dtype, {(int)act, nullptr, false, nullptr, in, s.d, s.ld, s.wide}, stream);
+            st = launch_pairs(p, dtype, {(int)act, nullptr, false, nullptr, in, s.d, s.ld, s.wide}, stream);
         }
         if (st == HTL_OK) st = check_launch("gated_mm_backward");
         if (st == HTL_OK && s.ld > 2 * n) st = zero_behind(s.d, dtype, m, 2 * n, s.ld, stream);
