@@ -379,3 +379,56 @@ def test_slopes_past_4_gib(htl):
     dy = torch.randn(m, n, device="cuda", generator=gen).bfloat16()
     some = torch.cat([torch.arange(0, n, 257, device="cuda"), torch.tensor([n - 1], device="cuda")])
     _backward_of_some(htl, x, w, dy, some, need_dx=False)
+
+
+# Sizes of the tiles of 256 x 256 (tests/test_launches.py looks at the kernels that these calls take).
+WIDE = [(4096, 2048, 264, 3), (3700, 2056, 300, 2), (4096, 2048, 304, 1), (8192, 1024, 256, 20), (7300, 1000, 2050, 5)]
+
+
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("m,n,k,g", WIDE)
+def test_wide_tiles(htl, m, n, k, g, keep):
+    """The largest tiles over several groups, some of few rows or none, with rows of no group that hold anything."""
+    rng = np.random.default_rng(m + k)
+    ids = _ids(rng, m, g, "dropped" if g > 1 else "one")
+    if g > 3:
+        ids[ids == 1] = 2                     # a group of no rows
+    x, w, dy = _data(m, n, k, g, torch.bfloat16)
+    want = Want(x, w, dy, ids, "silu", keep)
+    groups = htl.group_rows(torch.from_numpy(ids).cuda(), g) if g > 1 else None
+    none = torch.from_numpy((ids < 0) | (ids >= g))
+    x[none], dy[none] = float("nan"), float("inf")
+    xc, wc, dc = x.cuda(), w.cuda(), dy.cuda()
+    y, kept = htl.gated_mm(xc, wc, groups, keep=keep)
+    _close(y, want.y, want.ty, "y")
+    if keep:
+        _close(kept, want.kept, want.tkept, "kept")
+    dx, dw = htl.gated_mm_backward(dc, xc, wc, kept, groups)
+    _close(dx, want.dx, want.tdx, "dx")
+    _close(dw, want.dw, want.tdw, "dw")
+    # rows of larger matrices, and results one at a time, are the same to the bit
+    apart = torch.full((m, k + 13), float("nan"), dtype=torch.bfloat16, device="cuda")
+    apart[:, 5:5 + k] = xc
+    d_apart = torch.full((m, n + 3), float("nan"), dtype=torch.bfloat16, device="cuda")
+    d_apart[:, 1:1 + n] = dc
+    a, _ = htl.gated_mm_backward(d_apart[:, 1:1 + n], apart[:, 5:5 + k], wc, kept, groups, need_dw=False)
+    _, b = htl.gated_mm_backward(d_apart[:, 1:1 + n], apart[:, 5:5 + k], wc, kept, groups, need_dx=False)
+    assert torch.equal(a, dx) and torch.equal(b, dw)
+
+
+@pytest.mark.parametrize("keep", [False, True])
+def test_broken_plan_of_wide_tiles(htl, keep):
+    m, n, k, _ = WIDE[2]
+    x, w, dy = _data(m, n, k, 1, torch.bfloat16)
+    bad = torch.arange(m, dtype=torch.int32).flip(0).contiguous()
+    gone = torch.arange(m) % 7 == 3
+    there = torch.ones(m, dtype=torch.bool)
+    there[bad[gone].long()] = False
+    bad[gone] = torch.where(torch.arange(int(gone.sum())) % 2 == 0, -5, m + 9).to(torch.int32)
+    plan = htl.RowGroups(torch.zeros(m, dtype=torch.int32).cuda(), bad.cuda(), torch.tensor([0, m], dtype=torch.int32).cuda(), 1)
+    want = Want(x, w, dy, np.where(there.numpy(), 0, -1).astype(np.int32), "silu", keep)
+    y, kept = htl.gated_mm(x.cuda(), w.cuda(), plan, keep=keep)
+    _close(y[there.cuda()], want.y[there], want.ty[there], "y")
+    dx, dw = htl.gated_mm_backward(dy.cuda(), x.cuda(), w.cuda(), kept, plan)
+    _close(dx[there.cuda()], want.dx[there], want.tdx[there], "dx")
+    _close(dw, want.dw, want.tdw, "dw")

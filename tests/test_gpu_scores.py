@@ -527,3 +527,47 @@ def test_rows_past_4_gib_a_piece(htl, m, v, k):
             t = torch.mm((ed[:, p] + (m + 2) * U * (d[:, p].abs() + ed[:, p])).t().contiguous(), x8.abs())
             assert bool(((dw[p].double() - dw8).abs() <= t + HALF[x.dtype] * (dw8.abs() + t)).all()), (teach, p)
         assert bool(((dx.double() - dx8).abs() <= tol + HALF[x.dtype] * (dx8.abs() + tol)).all()), teach
+
+
+# Sizes of the tiles of 256 x 256 (tests/test_launches.py looks at the kernels that these calls take): scores in them
+# too from rows of 384 elements on, and several pieces of the vocabulary.
+WIDE = [(1100, 14500, 512, 9), (1100, 14500, 130, 65), (1100, 66000, 392, 9), (4500, 60000, 264, 12)]
+
+
+def pieces(m, v, k):
+    """Pieces of the vocabulary in a backward pass of bf16 rows below 1,024 elements: 512 MiB of gradients, 65,536 items."""
+    each = min((512 << 20) // (2 * m) // 256 * 256, 65536)
+    return -(-v // each)
+
+
+@pytest.mark.parametrize("m,v,k,t", WIDE)
+def test_wide_tiles(htl, m, v, k, t):
+    """Both losses in the largest tiles: rows without entries, items listed twice, and items at the ends of pieces."""
+    x, w, targets, dloss = _data(m, v, k, torch.bfloat16)
+    gen = torch.Generator().manual_seed(t)
+    items, logits = torch.randint(0, v, (m, t), generator=gen), torch.randn(m, t, generator=gen) * 3.0
+    each = -(-v // pieces(m, v, k)) if pieces(m, v, k) == 1 else min((512 << 20) // (2 * m) // 256 * 256, 65536)
+    ends = torch.tensor([0, min(each, v) - 1, min(each, v - 1), v - 1])
+    items[:, 0] = ends[torch.arange(m) % 4]
+    items[:, 1] = items[:, 0]
+    items[torch.rand(m, t, generator=gen) < 0.1] = -1
+    logits[torch.rand(m, t, generator=gen) < 0.05] = -math.inf
+    items[::50] = -1                            # no entry
+    logits[7::50] = -math.inf                   # entries of no share
+    targets[:4] = ends
+    xc, wc, dc = x.cuda(), w.cuda(), dloss.cuda()
+    for heat, ic, lc in ((1.0, targets[:, None], torch.zeros(m, 1)), (2.0, items, logits)):
+        size = float(lc[lc > -math.inf].abs().max()) / heat
+        # (in 64 bits on the GPU: a reference of this size)
+        want = Want(xc, wc, ic.cuda(), _log_shares(ic, lc, v, heat).cuda(), heat, dc, size)
+        off = ~((ic >= 0) & (ic < v) & (lc > -math.inf)).any(1).cuda()
+        xn, dn = xc.masked_fill(off[:, None], float("nan")), dc.masked_fill(off, float("inf"))
+        if ic is items:
+            loss, kept = htl.distill_loss(xn, wc, ic.cuda(), lc.cuda(), temperature=heat)
+            lse = kept[0]
+            dx, dw = htl.distill_loss_backward(dn, xn, wc, ic.cuda(), lc.cuda(), kept, temperature=heat)
+        else:
+            loss, lse = htl.softmax_loss(xn, wc, targets.cuda(), temperature=heat)
+            dx, dw = htl.softmax_loss_backward(dn, xn, wc, targets.cuda(), lse, temperature=heat)
+        for got, name in ((lse, "lse"), (loss, "loss"), (dx, "dx"), (dw, "dw")):
+            _close(got, getattr(want, name).cpu(), getattr(want, "t" + name).cpu(), (heat, name))
