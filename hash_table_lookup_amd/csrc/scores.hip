@@ -41,12 +41,21 @@ struct Items {
     }
 };
 
-struct Best {                // of some scores, in units of ln 2: the largest, and the sum of 2^(score - largest)
+// Of some products x w: the largest, and the sum of 2^((product - largest) unit), unit = log2(e) / T.  The
+// largest is taken off before anything is multiplied: an item far above the rest has a sum of exactly 1, and its
+// score rounds once on its way to lse, as the target's does, so that no loss is below 0.
+struct Best {
     float top, sum;
 };
-__device__ __forceinline__ Best join(const Best& a, const Best& b) {
+__device__ __forceinline__ Best join(const Best& a, const Best& b, float unit) {
     const float top = fmaxf(a.top, b.top), at = top == -INFINITY ? 0.0f : top;
-    return {top, a.sum * __builtin_amdgcn_exp2f(a.top - at) + b.sum * __builtin_amdgcn_exp2f(b.top - at)};
+    return {top, a.sum * __builtin_amdgcn_exp2f((a.top - at) * unit) + b.sum * __builtin_amdgcn_exp2f((b.top - at) * unit)};
+}
+// log2 of a score's share, s - lse with s rounded as lse has it (kept in one rounding, an item far above the
+// rest would be off its share of 1 by the rounding of its score).
+__device__ __forceinline__ float log2_share(float product, float scale, float lse) {
+#pragma clang fp contract(off)
+    return (product * scale - lse) * kLog2e;
 }
 
 // Forward end: partial[block][row] of each wave's columns, and the target's score.
@@ -77,16 +86,16 @@ template <class C> struct ScoreEnd {
             for (int e = 0; e < 4; ++e) top = fmaxf(top, v[i][e]);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float high = top * unit, at = top == -INFINITY ? 0.0f : high;
+        const float at = top == -INFINITY ? 0.0f : top;
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < C::TC; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(v[i][e], unit, -at));
+            for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f((v[i][e] - at) * unit);
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
         if (row < 0) return;
-        if (q == 0) partial[(int64_t)(block0 + col / W) * m + row] = {high, sum};
+        if (q == 0) partial[(int64_t)(block0 + col / W) * m + row] = {top, sum};
         if (targets.p) {
             const int t = targets.at(row) - v0 - col;
             if ((uint32_t)t < (uint32_t)W) {
@@ -117,12 +126,11 @@ template <class C> struct SlopeEnd {
         if (!grouped) return;
         constexpr int W = C::TC * 16;
         const int q = __lane_id() >> 4;
-        const float unit = scale * kLog2e;
-        const float at = row < 0 ? 0.0f : lse[row] * kLog2e, g = row < 0 ? 0.0f : dloss[row] * scale;
+        const float l = row < 0 ? 0.0f : lse[row], g = row < 0 ? 0.0f : dloss[row] * scale;
 #pragma unroll
         for (int i = 0; i < C::TC; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[i][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[i][e], unit, -at));
+            for (int e = 0; e < 4; ++e) v[i][e] = __builtin_amdgcn_exp2f(log2_share(v[i][e], scale, l));
         if (targets.p && row >= 0) {
             const int at_target = targets.at(row) - v0 - col;
             if ((uint32_t)at_target < (uint32_t)W) {
@@ -153,34 +161,38 @@ __global__ __launch_bounds__(256, 1) void k_scores_wide(ProdArgs p, End end) {
 }
 
 // A row's partial sums joined by the workgroup, the same in every thread.
-__device__ __forceinline__ Best row_best(const Best* partial, int blocks, int64_t m, int64_t row, Best* s) {
+__device__ __forceinline__ Best row_best(const Best* partial, int blocks, int64_t m, int64_t row, float unit, Best* s) {
     Best b = {-INFINITY, 0.0f};
 #pragma unroll 4
-    for (int i = threadIdx.x; i < blocks; i += 256) b = join(b, partial[(int64_t)i * m + row]);
+    for (int i = threadIdx.x; i < blocks; i += 256) b = join(b, partial[(int64_t)i * m + row], unit);
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) b = join(b, {__shfl_xor(b.top, off), __shfl_xor(b.sum, off)});
+    for (int off = 1; off < 64; off <<= 1) b = join(b, {__shfl_xor(b.top, off), __shfl_xor(b.sum, off)}, unit);
     __syncthreads();                                     // (the row before is read)
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = b;
     __syncthreads();
-    return join(join(s[0], s[1]), join(s[2], s[3]));
+    return join(join(s[0], s[1], unit), join(s[2], s[3], unit), unit);
 }
-__device__ __forceinline__ float lse_of(const Best& b) { return (b.top + __builtin_amdgcn_logf(b.sum)) * kLn2; }
+__device__ __forceinline__ float lse_of(const Best& b, float scale) {
+    return __builtin_fmaf(b.top, scale, __builtin_amdgcn_logf(b.sum) * kLn2);
+}
 
 // lse of rows from their partial sums, and the losses: a row a workgroup, or
 // (many rows: whole lines of partial sums are read) 16.
 __global__ __launch_bounds__(256) void k_softmax_finish(const Best* __restrict__ partial, int blocks, int64_t m,
-                                                        Items targets, const float* __restrict__ target_score,
+                                                        float scale, Items targets,
+                                                        const float* __restrict__ target_score,
                                                         float* __restrict__ loss, float* __restrict__ lse) {
     __shared__ Best s[4];
     const int64_t row = blockIdx.x;
     const bool on = targets.at(row) >= 0;                // (the same for the workgroup)
-    const float l = on ? lse_of(row_best(partial, blocks, m, row, s)) : 0.0f;
+    const float l = on ? lse_of(row_best(partial, blocks, m, row, scale * kLog2e, s), scale) : 0.0f;
     if (threadIdx.x) return;
     lse[row] = l;
     loss[row] = on ? l - target_score[row] : 0.0f;
 }
 __global__ __launch_bounds__(256) void k_softmax_finish16(const Best* __restrict__ partial, int blocks, int64_t m,
-                                                          Items targets, const float* __restrict__ target_score,
+                                                          float scale, Items targets,
+                                                          const float* __restrict__ target_score,
                                                           float* __restrict__ loss, float* __restrict__ lse) {
     __shared__ Best s[16][16];
     const int r = threadIdx.x & 15, part = threadIdx.x >> 4;
@@ -190,14 +202,14 @@ __global__ __launch_bounds__(256) void k_softmax_finish16(const Best* __restrict
         Best b = {-INFINITY, 0.0f};
         if (on) {
 #pragma unroll 4
-            for (int i = part; i < blocks; i += 16) b = join(b, partial[(int64_t)i * m + row]);
+            for (int i = part; i < blocks; i += 16) b = join(b, partial[(int64_t)i * m + row], scale * kLog2e);
         }
         __syncthreads();                                 // the rows before are read
         s[part][r] = b;
         __syncthreads();
         if (part || row >= m) continue;
-        for (int i = 1; i < 16; ++i) b = join(b, s[i][r]);
-        const float l = on ? lse_of(b) : 0.0f;
+        for (int i = 1; i < 16; ++i) b = join(b, s[i][r], scale * kLog2e);
+        const float l = on ? lse_of(b, scale) : 0.0f;
         lse[row] = l;
         loss[row] = on ? l - target_score[row] : 0.0f;
     }
@@ -295,7 +307,7 @@ __global__ __launch_bounds__(256) void k_distill_finish(RowsIn x, RowsIn w, int 
             if (threadIdx.x == 0) loss[row] = lse[row] = 0.0f;
             continue;
         }
-        const float l = lse_of(row_best(partial, blocks, m, row, s));
+        const float l = lse_of(row_best(partial, blocks, m, row, t.scale * kLog2e, s), t.scale);
         if (threadIdx.x >= 64) continue;
         float sum = 0.0f;
         for (int j = threadIdx.x; j < t.top; j += 64) {
@@ -734,17 +746,19 @@ extern "C" htl_status softmax_loss(const void* x, int64_t ldx, const void* w, in
     SCORE_SPACE("softmax_loss", softmax_loss_workspace_bytes(m, vocab, k, dtype));
     if (m == 0) return HTL_OK;
     const Rows2 r = {x, w, ldx, ldw, m, vocab, k, dtype};
+    const float scale = 1.0f / temperature;
     const Items t = {targets, index_bits == 64, vocab};
     const ForwardSpace s(ws, m, vocab, k, dtype);
     int blocks;
     if (s.wide) hipLaunchKernelGGL(k_active, dim3(grid_for(m, 256, 1 << 12)), dim3(256), 0, stream, m, t, s.ids);
-    const htl_status st = forward_scores(r, 1.0f / temperature, s, t, blocks, stream);
+    const htl_status st = forward_scores(r, scale, s, t, blocks, stream);
     if (st != HTL_OK) return st;
     // 8 rows of 2,048 blocks: 34 us at 16 rows a workgroup
     if (m < 2048)
-        hipLaunchKernelGGL(k_softmax_finish, dim3((unsigned)m), dim3(256), 0, stream, s.partial, blocks, m, t, s.target_score, loss, lse);
+        hipLaunchKernelGGL(k_softmax_finish, dim3((unsigned)m), dim3(256), 0, stream, s.partial, blocks, m, scale, t, s.target_score,
+                           loss, lse);
     else
-        hipLaunchKernelGGL(k_softmax_finish16, dim3(grid_for(m, 16)), dim3(256), 0, stream, s.partial, blocks, m, t,
+        hipLaunchKernelGGL(k_softmax_finish16, dim3(grid_for(m, 16)), dim3(256), 0, stream, s.partial, blocks, m, scale, t,
                            s.target_score, loss, lse);
     return check_launch("softmax_loss");
 }

@@ -571,3 +571,77 @@ def test_wide_tiles(htl, m, v, k, t):
             dx, dw = htl.softmax_loss_backward(dn, xn, wc, targets.cuda(), lse, temperature=heat)
         for got, name in ((lse, "lse"), (loss, "loss"), (dx, "dx"), (dw, "dw")):
             _close(got, getattr(want, name).cpu(), getattr(want, "t" + name).cpu(), (heat, name))
+
+
+EXACT = [(1, 40, 16), (20, 700, 32), (40, 500, 16), (300, 1500, 32), (1100, 14500, 512)]
+
+
+def _whole(m, v, k, dtype):
+    """Rows and items of whole numbers and 16ths, so few of them not zero that scores are exact in fp32 in any order."""
+    gen = torch.Generator().manual_seed(m + v)
+    x = torch.randint(-8, 9, (m, k), generator=gen).float()
+    w = torch.randint(-8, 9, (v, k), generator=gen).float() / 16.0
+    x[:, 16:], w[:, :2] = 0.0, 0.0
+    return x.to(dtype), w.to(dtype), torch.randint(0, v, (m,), generator=gen), (torch.rand(m, generator=gen) - 0.3) / m
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("heat", [1.0, 0.3, 0.07])
+@pytest.mark.parametrize("m,v,k", EXACT)
+def test_an_item_far_above_the_rest(htl, m, v, k, heat, dtype):
+    """Its share is 1 and the others' are 0, in fp32 and in 64 bits: the loss is 0, neither above nor below, and so are all
+    gradients, whatever the score.  (The others' scores are below 64, this one's over 400 and not a whole number.)"""
+    x, w, _, dloss = _whole(m, v, k, dtype)
+    best = v // 3
+    w[best] = 0.0
+    w[best, :2] = 1.0
+    x[:, 0] = 512.0 + 4.0 * (torch.arange(m) % 100)
+    x[:, 1] = (torch.arange(m) % 200).float() / 128.0 + 0.0078125
+    targets = torch.full((m,), best)
+    xc, wc, tc = x.cuda(), w.cuda(), targets.cuda()
+    loss, lse = htl.softmax_loss(xc, wc, tc, temperature=heat)
+    assert not loss.any(), (float(loss.min()), float(loss.max()))
+    for t in htl.softmax_loss_backward(dloss.cuda(), xc, wc, tc, lse, temperature=heat):
+        assert not t.any(), float(t.abs().max())
+    # a target that is another item: never below 0 either, but the distance
+    loss, _ = htl.softmax_loss(xc, wc, (tc + 1) % v, temperature=heat)
+    assert v == 1 or float(loss.min()) > 400.0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("heat", [1.0, 0.3, 0.01])
+@pytest.mark.parametrize("m,v,k", EXACT)
+def test_gradients_of_large_scores(htl, m, v, k, heat, dtype):
+    """Scores up to some thousands, which are exact before they are divided by the temperature (e at the top is 0): losses
+    and gradients of both kinds.  Shares and products below fp32's least normal number, 2^-126, may be taken as 0: at most
+    14,500 terms, each of a |g| below 128 and an |x| or |w| of at most 8, are off by 2^-126 * 2^14 * 2^7 * 2^3 < 2^-100."""
+    x, w, targets, dloss = _whole(m, v, k, dtype)
+    items, logits = torch.stack([targets, (targets + 7) % v], 1), torch.zeros(m, 2)
+    xc, wc, dc = x.cuda(), w.cuda(), dloss.cuda()
+    x8, w8 = xc.double(), wc.double()
+    s = torch.mm(x8, w8.t().contiguous()) / heat
+    lse = torch.logsumexp(s, 1)
+    r = (8 * s.abs().amax(1) + v + 64 + 2 * lse.abs()) * U
+    q = torch.exp(s - lse[:, None])
+    half, g = HALF[dtype], dc.double()[:, None] / heat
+    for ic in (targets[:, None].cuda(), items.cuda()):
+        t = ic.shape[1]
+        share = torch.zeros_like(q).scatter_add_(1, ic, torch.full(ic.shape, 1.0 / t, dtype=torch.float64, device="cuda"))
+        want = lse - s.gather(1, ic).mean(1) - math.log(t)
+        if t == 1:
+            loss, kept = htl.softmax_loss(xc, wc, ic[:, 0], temperature=heat)
+            dx, dw = htl.softmax_loss_backward(dc, xc, wc, ic[:, 0], kept, temperature=heat)
+            assert bool((loss >= 0.0).all())
+        else:
+            loss, kept = htl.distill_loss(xc, wc, ic, logits.cuda(), temperature=heat)
+            dx, dw = htl.distill_loss_backward(dc, xc, wc, ic, logits.cuda(), kept, temperature=heat)
+        assert bool(((loss.double() - want).abs() <= 3 * r + 64 * U).all()), t
+        d = (q - share) * g
+        ed = g.abs() * (2 * r[:, None] * q + 16 * U * share) + 2 * U * d.abs()
+        ed = ed + half * (d.abs() + ed)
+        e = torch.mm(ed + (v + 2) * U * (d.abs() + ed), w8.abs())
+        want = torch.mm(d, w8)
+        assert bool(((dx.double() - want).abs() <= e + half * (want.abs() + e) + 2.0 ** -100).all()), (t, "dx")
+        e = torch.mm((ed + (m + 2) * U * (d.abs() + ed)).t().contiguous(), x8.abs())
+        want = torch.mm(d.t().contiguous(), x8)
+        assert bool(((dw.double() - want).abs() <= e + half * (want.abs() + e) + 2.0 ** -100).all()), (t, "dw")
