@@ -432,3 +432,35 @@ def test_broken_plan_of_wide_tiles(htl, keep):
     dx, dw = htl.gated_mm_backward(dy.cuda(), x.cuda(), w.cuda(), kept, plan)
     _close(dx[there.cuda()], want.dx[there], want.tdx[there], "dx")
     _close(dw, want.dw, want.tdw, "dw")
+
+
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("m,n,k,g", [(68000, 72, 200, 5), (66000, 300, 64, 3), (65536, 520, 24, 1)])
+def test_all_of_many_rows(htl, m, n, k, g, keep):
+    """Many rows through small blocks whose backward pass does not fit in LDS, or whose z and u are not kept: all results."""
+    ids = _ids(np.random.default_rng(m + n), m, g, "dropped" if g > 1 else "one")
+    x, w, dy = _data(m, n, k, g, torch.bfloat16)
+    want = Want(x, w, dy, ids, "sigmoid", keep)
+    groups = htl.group_rows(torch.from_numpy(ids).cuda(), g) if g > 1 else None
+    y, kept = htl.gated_mm(x.cuda(), w.cuda(), groups, act="sigmoid", keep=keep)
+    _close(y, want.y, want.ty, "y")
+    dx, dw = htl.gated_mm_backward(dy.cuda(), x.cuda(), w.cuda(), kept, groups, act="sigmoid")
+    _close(dx, want.dx, want.tdx, "dx")
+    _close(dw, want.dw, want.tdw, "dw")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_one_group_has_most_rows(htl, dtype):
+    """Eight rows a group on average, 300 of them in one group and none in some."""
+    m, n, k, g = 512, 72, 136, 64
+    ids = (np.arange(m) * 7 % g).astype(np.int32)
+    ids[100:400] = 5
+    ids[ids % 9 == 8] = 3
+    x, w, dy = _data(m, n, k, g, dtype)
+    want = Want(x, w, dy, ids, "silu", False)
+    groups = htl.group_rows(torch.from_numpy(ids).cuda(), g)
+    y, _ = htl.gated_mm(x.cuda(), w.cuda(), groups)
+    _close(y, want.y, want.ty, "y")
+    dx, dw = htl.gated_mm_backward(dy.cuda(), x.cuda(), w.cuda(), None, groups)
+    _close(dx, want.dx, want.tdx, "dx")
+    _close(dw, want.dw, want.tdw, "dw")
