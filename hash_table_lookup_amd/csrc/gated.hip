@@ -13,7 +13,7 @@
 // 16,384 bf16 rows over 16 ragged groups, 2,048 -> 2 x 4,096: forward 598 us
 // (577-654; 919 TFLOP/s), dz and du with z and u again 719 (695-803), dx 639, dw 683.
 // 426,000 rows of 26 groups, 128 -> 2 x 256: forward with z and u kept 234 us (763 MB:
-// 3.3 TB/s), dz, du and dx from them 290 (1.2 GB: 4.1 TB/s).  One row, 2,048 -> 2 x
+// 3.3 TB/s), dz, du and dx from them 294 (1.2 GB: 4.1 TB/s).  One row, 2,048 -> 2 x
 // 4,096: 9.7 us (33.6 MB: 3.5 TB/s); 64 rows in 16 groups: 74 us (7.2 TB/s, in part
 // from the last-level cache).  5,001 fp32 rows, 513 -> 2 x 777: 110 us (72 TFLOP/s).
 #include "few.h"
@@ -228,8 +228,8 @@ __global__ __launch_bounds__(512, 2) void k_gated_resident(ProdArgs p, GatedEnd<
     }
 }
 // Positions per chunk: so many that no more chunks than workgroups run at once load a matrix,
-// each once.  (426,000 rows of 26 groups, 128 -> 2 x 256: 234 us with 2,048, 246
-// with 1,024, 271 with 512; the backward pass below 285, 313 and 341.)
+// each once.  (426,000 rows of 26 groups, 128 -> 2 x 256, one sweep: 234 us with 2,048, 246
+// with 1,024, 271 with 512; the backward pass below 285, 313 and 341; its median elsewhere 294.)
 uint32_t resident_rows(int64_t m, int n_groups, int at_once) {
     return (uint32_t)align_up((size_t)(n_groups <= at_once / 4 ? ceil_div(m, at_once - n_groups) : ceil_div(m, 1024)), 256);
 }
@@ -398,7 +398,7 @@ __global__ __launch_bounds__(512, 2) void k_gated_back_resident(ProdArgs p, Rows
     }
 }
 // Whether a backward pass from z and u goes that way: 426,000 rows of 26 groups, 128 ->
-// 2 x 256: 290 us, where dz and du by themselves and then dx in tiles take 415.  (Lines
+// 2 x 256: 294 us, where dz and du by themselves and then dx in tiles take 415.  (Lines
 // read and written in two halves, 16 rows a time: 356.)
 bool back_resident(int64_t m, int n_groups, int n, int k, htl_dtype dtype) {
     return dtype == HTL_BF16 && n <= 256 && k <= 128 && m / n_groups >= 512 && m >= 1 << 16;

@@ -17,11 +17,11 @@
 // step, 2^-8), then dx += d w and dw = d^T x.
 //
 // Bound: products.  Measured: 8,192 bf16 rows of 2,048 (one in twenty without a
-// target) against 131,072 items: forward 3.55 ms (1,200 TFLOP/s with its end, where the
-// library's product of such sizes alone reaches 1,198), a piece of 16,384 items 539
-// us for d, 417 for dx and 399 for dw (1,277 and 1,309 TFLOP/s).  16,384 fp32 rows of 128
-// against 65,536: forward 2.56 ms (108 TFLOP/s of 154), a piece of 8,192 items 376, 293
-// and 285 us.  16 rows of 1,024 against 65,536: 26 us (134 MB: 5.2 TB/s).
+// target) against 131,072 items: forward 3.60 ms (1,180 TFLOP/s with its end, where the
+// library's product of such sizes alone reaches 1,198), a piece of 16,384 items 541
+// us for d, 426 for dx and 409 for dw (1,251 and 1,278 TFLOP/s).  16,384 fp32 rows of 128
+// against 65,536: forward 2.60 ms (106 TFLOP/s of 154), a piece of 8,192 items 376, 294
+// and 287 us.  16 rows of 1,024 against 65,536: 26 us (134 MB: 5.1 TB/s).
 #include "few.h"
 #include "wide.h"
 
@@ -324,7 +324,10 @@ __global__ __launch_bounds__(256) void k_distill_finish(RowsIn x, RowsIn w, int 
 }
 
 // Which rows take part (0, or -1: none), and, of a teacher's entries, d: an
-// item listed twice has the shares of both in each.  A wave a row.
+// item listed twice has the shares of both in each.  A wave a row, which compares all
+// pairs of its list: little for lists of 64, not for long ones (4,096 bf16 rows of 512
+// against 65,536 items, step: 1.55 ms with 64 or 128 entries, 1.76, 2.29 and 4.01 with
+// 256, 512 and 1,024, whose scores are part of that too).
 __global__ __launch_bounds__(256) void k_active(int64_t m, Items targets, int32_t* __restrict__ ids) {
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < m; i += gridDim.x * 256ll) ids[i] = targets.at(i) >= 0 ? 0 : -1;
 }
@@ -406,12 +409,12 @@ int tile_of(const Rows2& r, int64_t cols, bool& fast) {
            aligned(r.w, 16) && r.m * r.ldx * es <= kBufferBytes && cols * r.ldw * es <= kBufferBytes;
     return narrow_of(r.m, r.vocab, r.dtype) ? 32 : 128;
 }
-// Whether wide.h's tiles fill the device.
 // Scores of rows shorter than this run as well or better in tiles of 128, of which
 // two fill a unit and one's end passes under the other's products (4,096 rows
 // against 65,536, step: 801 and 830 us of 128 elements, 953 and 967 of 256, but 1,639
 // and 1,448 of 504).
 constexpr int kWideK = 384;
+// Whether wide.h's tiles fill the device.
 bool wide_of(int64_t m, int vocab, htl_dtype dtype) {
     return dtype == HTL_BF16 && m >= 256 && ceil_div(m, 256) * ceil_div(vocab, 256) >= 224;
 }

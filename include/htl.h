@@ -744,7 +744,8 @@ htl_status gated_mm_backward(const void* dy, int64_t ld_dy, const void* x, int64
 #define HTL_MAX_VOCAB (1 << 30)
 #define HTL_MAX_TOP 1024
 
-/* softmax_loss, softmax_loss_backward -- loss[i] = lse[i] - s[i][targets[i]].
+/* softmax_loss, softmax_loss_backward -- loss[i] = lse[i] - s[i][targets[i]], never
+ * below 0 (both terms are rounded alike).
  *   ws         at least softmax_loss_workspace_bytes(m, vocab, k, dtype), or
  *              softmax_loss_backward_workspace_bytes of them, bytes,
  *              256-byte aligned (0 for arguments out of range). */
