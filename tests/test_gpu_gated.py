@@ -435,7 +435,7 @@ def test_broken_plan_of_wide_tiles(htl, keep):
 
 
 @pytest.mark.parametrize("keep", [False, True])
-@pytest.mark.parametrize("m,n,k,g", [(68000, 72, 200, 5), (66000, 300, 64, 3), (65536, 520, 24, 1)])
+@pytest.mark.parametrize("m,n,k,g", [(68000, 72, 200, 5), (66000, 300, 64, 3), (65536, 520, 24, 1), (60000, 100, 264, 2)])
 def test_all_of_many_rows(htl, m, n, k, g, keep):
     """Many rows through small blocks whose backward pass does not fit in LDS, or whose z and u are not kept: all results."""
     ids = _ids(np.random.default_rng(m + n), m, g, "dropped" if g > 1 else "one")
